@@ -404,6 +404,182 @@ int hs_swap_in_noalloc(hs_state* st, const int32_t* req_pool_indices_dev,
                        int32_t* stats_dev, int64_t* miss_src_dev, int64_t* miss_dst_dev,
                        int32_t* miss_count_dev, void* stream);
 
+/* ==== 8-bit key/value rows: quantise, attend, evict ========================
+ *
+ * The swap-in moves rows of W opaque bytes.  The calls below give the rows a
+ * content, the keys and values of one token in 8 bits, and do what a decode
+ * step does with them: write them (hs_quantize_kv, hs_append_kv), attend over
+ * the ones a swap-in located (hs_attend), and bound a sequence by dropping the
+ * tokens that have drawn the least attention (hs_accumulate, hs_evict,
+ * hs_compact_kv).  The pages leave the attention to the kernels that consume
+ * device_locs ("SGLang HiSparse", sections 1.2 and 2.1) and give no
+ * counterpart to the rest.
+ *
+ * Row of token t of request q (W = item_size_bytes):
+ *   bytes [0, Hkv * D)            K codes, [Hkv][D]
+ *   bytes [Hkv * D, 2 * Hkv * D)  V codes, [Hkv][D]
+ *   the rest                      never read or written
+ * Scales: float [R, NB, 2, Hkv] with NB = ceil(L / T); K (c = 0) or V (c = 1)
+ * of head h is code * scales[q, t / T, c, h].  A scale is finite and >= 0.
+ *   HS_KV_E4M3: codes are e4m3 (largest 448).  The scales these calls write
+ *     are powers of two, the smallest that bring the largest magnitude of the
+ *     block to 448 or less, so that rounding the codes of a block again under
+ *     a larger scale changes nothing but e4m3's subnormals.
+ *   HS_KV_INT8: codes are two's complement, -127..127; scale = largest
+ *     magnitude / 127.
+ *   A code is the rounding (to nearest, ties to even) of x * (1 / scale), both
+ *   operations in 32 bits.  Magnitudes below 2^-100 count as 2^-100; a block
+ *   of zeros has scale 0.  Infinities and NaN do not count as magnitudes:
+ *   infinities get the largest code of their sign, NaN the e4m3 NaN (0 in
+ *   int8).  hs_attend takes any scales, not only those. */
+#define HS_KV_E4M3 0
+#define HS_KV_INT8 1
+#define HS_DTYPE_BF16 0
+#define HS_DTYPE_FP16 1
+#define HS_DTYPE_FP32 2
+
+#define HS_MAX_KV_BLOCK 4096   /* block_tokens upper bound */
+#define HS_MAX_KV_HEADS 128    /* num_kv_heads and query heads upper bound */
+
+typedef struct hs_kv_format {
+    int32_t num_kv_heads;    /* Hkv: 1..HS_MAX_KV_HEADS                       */
+    int32_t head_dim;        /* D: 32, 64, 96, 128, 192 or 256                */
+    int32_t block_tokens;    /* T: tokens that share a scale                  */
+    int32_t code;            /* HS_KV_E4M3 or HS_KV_INT8                      */
+    int32_t item_size_bytes; /* W: a multiple of 16, 2 * Hkv * D or more      */
+} hs_kv_format;
+
+/* New keys and values: element (b, i, h, d) of K is at k_dev + b * k_stride[0]
+ * + i * k_stride[1] + h * k_stride[2] + d elements, V likewise.  Any strides
+ * (0 broadcasts) and any element-aligned address; 16-byte loads are used where
+ * base and strides allow. */
+typedef struct hs_kv_input {
+    const void* k_dev;
+    const void* v_dev;
+    int32_t dtype; /* HS_DTYPE_* of both */
+    int64_t k_stride[3], v_stride[3];
+} hs_kv_input;
+
+/* HS_OK if the format is valid and supported.  Host only. */
+int hs_kv_format_check(const hs_kv_format* fmt);
+
+/* Quantises new tokens into a store of rows, one warp group per scale group.
+ * Entry b writes the tokens [start[b], start[b] + count[b]) of request req[b]:
+ *   rows_dev   uint8 [num_requests, max_seq_len, W], 16-byte aligned
+ *   scales_dev float [num_requests, NB, 2, Hkv]
+ *   req_dev, start_dev, count_dev int32 [batch]; 0 <= count <= max_count
+ * A block that the new tokens fill from its first token on gets the scale of
+ * the new tokens alone.  A block that begins before start[b] keeps the larger
+ * of its scale and the new tokens'; if it grows, the codes of the block's
+ * tokens before start[b] are rounded again under it.  Blocks without new
+ * tokens, tokens after the new ones and entries whose request or range lies
+ * outside the store are left alone.  The requests of one call must be
+ * distinct.  Asynchronous on `stream`. */
+int hs_quantize_kv(const hs_kv_format* fmt, const hs_kv_input* in, const int32_t* req_dev,
+                   const int32_t* start_dev, const int32_t* count_dev, int32_t batch,
+                   int32_t max_count, void* rows_dev, float* scales_dev, int32_t num_requests,
+                   int32_t max_seq_len, void* stream);
+
+/* hs_quantize_kv into layer `layer_id` of a swap-in handle: like
+ * hs_append_rows, it writes every copy of a token, the host pool row, the
+ * extra-page row (the new length being start + count) and the hot row of a
+ * resident token, here for the new tokens and for those of a block whose
+ * scale grew.  The format's W is the handle's.  An entry out of range is
+ * skipped and sets HS_STATUS_BAD_APPEND.  Order it as hs_append_rows. */
+int hs_append_kv(hs_state* st, int32_t layer_id, const hs_kv_format* fmt, const hs_kv_input* in,
+                 const int32_t* req_dev, const int32_t* start_dev, const int32_t* count_dev,
+                 int32_t batch, int32_t max_count, float* scales_dev, void* stream);
+
+/* Arguments of hs_attend. */
+typedef struct hs_attend_args {
+    const void* q_dev;       /* [batch, steps, heads, D], strides below (elements), the last
+                                dimension dense; element-aligned                            */
+    void* out_dev;           /* the same shape and type, its own strides                    */
+    int32_t dtype;           /* HS_DTYPE_BF16 or HS_DTYPE_FP16, of q and out                */
+    int32_t batch, steps, top_k;
+    int32_t num_heads;       /* query heads, a multiple of Hkv; head i reads K/V head
+                                i / (num_heads / Hkv)                                       */
+    int32_t num_requests;    /* R of the scales                                             */
+    int32_t max_seq_len;     /* L of the scales                                             */
+    float sm_scale;          /* factor of q . k                                             */
+    int64_t q_stride[3];     /* batch, step, head                                           */
+    int64_t out_stride[3];
+    const void* rows_dev;    /* uint8 [num_rows, W], 16-byte aligned: a layer's device KV
+                                buffer, or any store of rows                                */
+    int64_t num_rows;
+    const int32_t* locs_dev; /* [batch, steps, top_k] row of each selected token            */
+    const int32_t* topk_dev; /* [batch, steps, top_k] its position (selects the scale)      */
+    const int32_t* req_dev;  /* [batch] its request (selects the scale)                     */
+    const float* scales_dev; /* [R, NB, 2, Hkv]                                             */
+    float* lse_dev;          /* [batch, steps, heads] natural log of the sum of exp, or NULL */
+    float* weights_dev;      /* [batch, steps, top_k] or NULL: each entry's attention weight
+                                summed over the query heads                                 */
+    float* acc_dev;          /* [R, L] or NULL: acc[req, token] += weights, as hs_accumulate
+                                with every step counted; needs weights_dev if steps > 1     */
+    void* workspace_dev;     /* hs_attend_workspace_bytes, 16-byte aligned, or NULL if 0    */
+    size_t workspace_bytes;
+} hs_attend_args;
+
+/* Device bytes of workspace that an hs_attend call of these sizes needs (0 for
+ * most: the logits of a call stay in shared memory; (size_t)-1 if the sizes are not
+ * accepted).  Uses the batch, steps, top_k and num_heads of `args`, no pointer.  Host only. */
+size_t hs_attend_workspace_bytes(const hs_kv_format* fmt, const hs_attend_args* args);
+
+/* Attention of batch x steps queries, each over its own top_k rows:
+ *   s_j = sm_scale * q . k_j,  p_j = exp(s_j - lse),  lse = ln sum_j exp(s_j),
+ *   out = sum_j p_j v_j,  weights_j = sum over the query heads of p_j
+ * over the entries with 0 <= loc < num_rows and 0 <= token < max_seq_len; the
+ * others (a swap-in's -1 among them) are masked.  A query whose entries are
+ * all masked gets out 0, lse -inf and weights 0; one whose request lies
+ * outside [0, num_requests) likewise.  An entry given twice counts twice.
+ * Products of codes and queries are exact and summed in 32 bits; the softmax
+ * statistics are 32 bits; p_j is rounded to 11 bits for the product with V.
+ * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_KV_HEADS query heads.
+ * Asynchronous on `stream`. */
+int hs_attend(const hs_kv_format* fmt, const hs_attend_args* args, void* stream);
+
+/* acc[req[b], topk[b, s, j]] += weights[b, s, j] for s < counts[b] (all steps
+ * if counts_dev is NULL), the steps one after the other, so that the sums do
+ * not depend on timing (the entries of one step being distinct).  Entries
+ * outside [0, max_seq_len), steps past num_steps and requests outside
+ * [0, num_requests) are skipped.  For speculative decoding, call it once the
+ * accepted steps are known, and hs_attend without acc_dev. */
+int hs_accumulate(const float* weights_dev, const int32_t* topk_dev, const int32_t* req_dev,
+                  const int32_t* counts_dev, int32_t batch, int32_t num_steps, int32_t top_k,
+                  float* acc_dev, int32_t num_requests, int32_t max_seq_len, void* stream);
+
+/* Chooses the tokens that a sequence keeps, by accumulated attention weight.
+ * With n = min(seq_lens[b], max_seq_len): all n if n <= budget; else the last
+ * `recent` tokens and, of those before, the budget - recent with the largest
+ * acc[req[b], t] (ties: the lowest positions; NaN below every number).
+ *   acc_dev      float [num_requests, max_seq_len]
+ *   keep_dev     int32 [batch, budget] out: kept positions, ascending, then -1
+ *   kept_dev     int32 [batch] out: how many
+ *   kept_acc_dev float [batch, budget] out or NULL: their weights, then 0
+ * 0 <= recent <= budget, budget >= 1.  A request outside [0, num_requests) or
+ * a negative length keeps nothing.  Asynchronous on `stream`. */
+int hs_evict(const float* acc_dev, const int32_t* req_dev, const int32_t* seq_lens_dev,
+             int32_t batch, int32_t recent, int32_t budget, int32_t num_requests,
+             int32_t max_seq_len, int32_t* keep_dev, int32_t* kept_dev, float* kept_acc_dev,
+             void* stream);
+
+/* Moves kept tokens together: token j < kept[b] of request dst_req[b] of the
+ * destination becomes token keep[b, j] of request src_req[b] of the source.
+ * The blocks of the destination hold other tokens than the source's, so each
+ * gets the scale of its own tokens (all of them; blocks begin at token 0) and
+ * their values (code * scale) are rounded under it.  Rows and scales past
+ * kept[b] are left alone; kept[b] is clamped to [0, budget] and to the
+ * destination's length.  A keep entry outside the source makes its row zeros;
+ * an entry with a request out of range is skipped.
+ *   src/dst_rows_dev uint8 [R, L, W], src/dst_scales_dev float [R, NB, 2, Hkv]
+ * Source and destination must not overlap; the destination requests of one
+ * call must be distinct.  Asynchronous on `stream`. */
+int hs_compact_kv(const hs_kv_format* fmt, const void* src_rows_dev, const float* src_scales_dev,
+                  int32_t src_requests, int32_t src_seq_len, const int32_t* src_req_dev,
+                  const int32_t* keep_dev, const int32_t* kept_dev, int32_t batch, int32_t budget,
+                  void* dst_rows_dev, float* dst_scales_dev, int32_t dst_requests,
+                  int32_t dst_seq_len, const int32_t* dst_req_dev, void* stream);
+
 /* Static string for a return code (no counterpart on the pages). */
 const char* hs_status_string(int code);
 

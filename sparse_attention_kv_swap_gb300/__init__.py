@@ -11,7 +11,10 @@ from .binding import (HsConfig, HsError, make_config, load_library,  # noqa: F40
                       hs_swap_in, hs_page_table, hs_reset_requests, hs_get_status,
                       hs_export_request_state, hs_status_string, hs_version,
                       hs_set_timeline, hs_set_copy_ctas, hs_set_defer_copy,
-                      hs_copy_planned, hs_append_rows, hs_get_stats)
+                      hs_copy_planned, hs_append_rows, hs_get_stats,
+                      HS_KV_E4M3, HS_KV_INT8, HsKvFormat, make_kv_format, hs_quantize_kv,
+                      hs_append_kv, hs_attend, hs_attend_workspace_bytes, hs_accumulate,
+                      hs_evict, hs_compact_kv)
 
 
 def __getattr__(name):

@@ -45,6 +45,14 @@ HS_MAX_ITEM_BYTES = 65536
 HS_NOALLOC_SCRATCH_BYTES = 16 << 20
 TIMELINE_WORDS_PER_ROW = 8 * 16  # hs_set_timeline: [batch][8 ranks][16 words]
 
+HS_KV_E4M3 = 0
+HS_KV_INT8 = 1
+HS_DTYPE_BF16 = 0
+HS_DTYPE_FP16 = 1
+HS_DTYPE_FP32 = 2
+HS_MAX_KV_BLOCK = 4096
+HS_MAX_KV_HEADS = 128
+
 HEADER = os.path.join(_build.INCLUDE, "hisparse_swap.h")
 
 
@@ -76,11 +84,56 @@ def make_config(num_requests: int, max_seq_len: int, item_size_bytes: int,
                     index_kind, extra_page_size)
 
 
+class HsKvFormat(ctypes.Structure):
+    """Content of a KV row: 8-bit keys and values, a scale per block of tokens and head."""
+    _fields_ = [("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_tokens", ctypes.c_int32), ("code", ctypes.c_int32),
+                ("item_size_bytes", ctypes.c_int32)]
+
+    def num_blocks(self, max_seq_len: int) -> int:
+        """Scale blocks of a sequence of max_seq_len tokens."""
+        return -(-max_seq_len // self.block_tokens)
+
+    def scales_shape(self, num_requests: int, max_seq_len: int):
+        return (num_requests, self.num_blocks(max_seq_len), 2, self.num_kv_heads)
+
+
+def make_kv_format(num_kv_heads: int, head_dim: int, block_tokens: int, code: int = HS_KV_E4M3,
+                   item_size_bytes: Optional[int] = None) -> HsKvFormat:
+    """code: HS_KV_E4M3 or HS_KV_INT8; item_size_bytes: the row's width, by default just
+    its keys and values.  Raises HsError if the library does not take the format."""
+    width = 2 * num_kv_heads * head_dim if item_size_bytes is None else item_size_bytes
+    fmt = HsKvFormat(num_kv_heads, head_dim, block_tokens, code, width)
+    _check(load_library().hs_kv_format_check(ctypes.byref(fmt)), "hs_kv_format_check")
+    return fmt
+
+
+class _HsKvInput(ctypes.Structure):
+    _fields_ = [("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3)]
+
+
+class _HsAttendArgs(ctypes.Structure):
+    _fields_ = [("q_dev", ctypes.c_void_p), ("out_dev", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("num_requests", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
+                ("sm_scale", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3),
+                ("out_stride", ctypes.c_int64 * 3), ("rows_dev", ctypes.c_void_p),
+                ("num_rows", ctypes.c_int64), ("locs_dev", ctypes.c_void_p),
+                ("topk_dev", ctypes.c_void_p), ("req_dev", ctypes.c_void_p),
+                ("scales_dev", ctypes.c_void_p), ("lse_dev", ctypes.c_void_p),
+                ("weights_dev", ctypes.c_void_p), ("acc_dev", ctypes.c_void_p),
+                ("workspace_dev", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 _lock = threading.Lock()
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _cfgp = ctypes.POINTER(HsConfig)
+_fmtp = ctypes.POINTER(HsKvFormat)
 
 
 def _declare(lib) -> None:
@@ -110,6 +163,19 @@ def _declare(lib) -> None:
         "hs_set_defer_copy": (ctypes.c_int, [_vp, _i32]),
         "hs_copy_planned": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _i32, _vp]),
         "hs_set_copy_ctas": (ctypes.c_int, [_vp, _i32]),
+        "hs_kv_format_check": (ctypes.c_int, [_fmtp]),
+        "hs_quantize_kv": (ctypes.c_int, [_fmtp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32,
+                                          _i32, _vp]),
+        "hs_append_kv": (ctypes.c_int, [_vp, _i32, _fmtp, _vp, _vp, _vp, _vp, _i32, _i32, _vp,
+                                        _vp]),
+        "hs_attend_workspace_bytes": (ctypes.c_size_t, [_fmtp, _vp]),
+        "hs_attend": (ctypes.c_int, [_fmtp, _vp, _vp]),
+        "hs_accumulate": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _i32,
+                                         _vp]),
+        "hs_evict": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                    _vp]),
+        "hs_compact_kv": (ctypes.c_int, [_fmtp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32,
+                                         _vp, _vp, _i32, _i32, _vp, _vp]),
         "hs_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "hs_version": (_i32, []),
     }
@@ -505,3 +571,209 @@ def hs_swap_in_noalloc(handle: StateHandle, req_pool_indices, seq_lens, topk, la
             _dptr(miss_dst, torch.int64, "miss_dst"),
             _dptr(miss_count, torch.int32, "miss_count"), _stream_ptr(stream))
         _check(rc, "hs_swap_in_noalloc")
+
+
+# ---- 8-bit key/value rows ------------------------------------------------------
+
+def _dtype_code(t, name, allow_fp32: bool) -> int:
+    import torch
+    codes = {torch.bfloat16: HS_DTYPE_BF16, torch.float16: HS_DTYPE_FP16}
+    if allow_fp32:
+        codes[torch.float32] = HS_DTYPE_FP32
+    if t.dtype not in codes:
+        raise ValueError("%s must have dtype %s" % (name, " or ".join(str(d) for d in codes)))
+    return codes[t.dtype]
+
+
+def _sptr(t, name) -> int:
+    """Address of a device tensor that the kernels read by strides; its last
+    dimension must be dense."""
+    if not t.is_cuda:
+        raise ValueError("%s must be in device memory" % name)
+    want = getattr(_call_device, "index", None)
+    if want is not None and t.device.index != want:
+        raise ValueError("%s is on cuda:%d, the call runs on cuda:%d" % (name, t.device.index,
+                                                                        want))
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension of %s must be dense" % name)
+    return t.data_ptr()
+
+
+def _kv_input(fmt, k, v, req, start, count):
+    if k.dim() != 4 or tuple(k.shape[2:]) != (fmt.num_kv_heads, fmt.head_dim):
+        raise ValueError("k must be [batch, tokens, %d, %d], got %s"
+                         % (fmt.num_kv_heads, fmt.head_dim, tuple(k.shape)))
+    _shape(v, k.shape, "v")
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have one dtype")
+    B = k.shape[0]
+    _shape(req, (B,), "req")
+    _shape(start, (B,), "start")
+    _shape(count, (B,), "count")
+    i64x3 = ctypes.c_int64 * 3
+    return _HsKvInput(_sptr(k, "k"), _sptr(v, "v"), _dtype_code(k, "k", True),
+                      i64x3(*k.stride()[:3]), i64x3(*v.stride()[:3]))
+
+
+def _store(fmt, rows, scales, name):
+    """(requests, tokens) of a store of rows [requests, tokens, W] and its scales."""
+    if rows.dim() != 3 or rows.shape[2] != fmt.item_size_bytes:
+        raise ValueError("%srows must be [requests, tokens, %d], got %s"
+                         % (name, fmt.item_size_bytes, tuple(rows.shape)))
+    R, L = rows.shape[0], rows.shape[1]
+    _shape(scales, fmt.scales_shape(R, L), name + "scales")
+    return R, L
+
+
+def hs_quantize_kv(fmt: HsKvFormat, k, v, req, start, count, rows, scales, stream=None) -> None:
+    """Quantises tokens [start[b], start[b] + count[b]) of request req[b] into a
+    store of rows.  k, v: [batch, tokens, Hkv, D] (bf16, fp16 or fp32, any strides
+    but a dense last dimension); rows uint8 [R, L, W] (device or pinned memory);
+    scales fp32 [R, NB, 2, Hkv], updated."""
+    import torch
+    R, L = _store(fmt, rows, scales, "")
+    with _on_device(k.device.index if k.is_cuda else None):
+        inp = _kv_input(fmt, k, v, req, start, count)
+        rc = load_library().hs_quantize_kv(
+            ctypes.byref(fmt), ctypes.byref(inp), _dptr(req, torch.int32, "req"),
+            _dptr(start, torch.int32, "start"), _dptr(count, torch.int32, "count"), k.shape[0],
+            k.shape[1], _dptr(rows, torch.uint8, "rows"), _dptr(scales, torch.float32, "scales"),
+            R, L, _stream_ptr(stream))
+        _check(rc, "hs_quantize_kv")
+
+
+def hs_append_kv(handle: StateHandle, layer_id: int, fmt: HsKvFormat, k, v, req, start, count,
+                 scales, stream=None) -> None:
+    """hs_quantize_kv into every copy that a swap-in handle keeps of the rows (host
+    pool, extra page, hot rows); scales fp32 [R, NB, 2, Hkv] of the layer, updated."""
+    import torch
+    cfg = handle.cfg
+    _shape(scales, fmt.scales_shape(cfg.num_requests, cfg.max_seq_len), "scales")
+    with _on_device(handle.device):
+        inp = _kv_input(fmt, k, v, req, start, count)
+        rc = load_library().hs_append_kv(
+            handle.ptr, layer_id, ctypes.byref(fmt), ctypes.byref(inp),
+            _dptr(req, torch.int32, "req"), _dptr(start, torch.int32, "start"),
+            _dptr(count, torch.int32, "count"), k.shape[0], k.shape[1],
+            _dptr(scales, torch.float32, "scales"), _stream_ptr(stream))
+        _check(rc, "hs_append_kv")
+
+
+def hs_attend_workspace_bytes(fmt: HsKvFormat, batch: int, steps: int, top_k: int,
+                              num_heads: int) -> int:
+    """Device bytes of workspace that hs_attend needs for these sizes (mostly 0)."""
+    args = _HsAttendArgs(batch=batch, steps=steps, top_k=top_k, num_heads=num_heads)
+    n = load_library().hs_attend_workspace_bytes(ctypes.byref(fmt), ctypes.byref(args))
+    if n == ctypes.c_size_t(-1).value:
+        raise HsError(HS_ERR_INVALID_ARG, "hs_attend_workspace_bytes")
+    return n
+
+
+def hs_attend(fmt: HsKvFormat, q, rows, locs, topk, req, scales, max_seq_len: int, out, lse=None,
+              weights=None, acc=None, sm_scale: Optional[float] = None, workspace=None,
+              stream=None) -> None:
+    """Attention of q [batch, steps, heads, D] (bf16 or fp16) over the rows at
+    locs [batch, steps, top_k] of rows uint8 [N, W].  topk: the rows' positions, req
+    [batch]: their requests, which select the scales [R, NB, 2, Hkv].  Outputs: out
+    as q, lse fp32 [batch, steps, heads], weights fp32 [batch, steps, top_k], acc fp32
+    [R, max_seq_len] added to.  sm_scale: 1 / sqrt(D) by default."""
+    import torch
+    if q.dim() != 4 or q.shape[3] != fmt.head_dim:
+        raise ValueError("q must be [batch, steps, heads, %d], got %s"
+                         % (fmt.head_dim, tuple(q.shape)))
+    B, S, H, D = q.shape
+    if topk.dim() != 3 or topk.shape[0] != B or topk.shape[1] != S:
+        raise ValueError("topk must be [%d, %d, top_k], got %s" % (B, S, tuple(topk.shape)))
+    K = topk.shape[2]
+    if out.dtype != q.dtype:
+        raise ValueError("out must have q's dtype")
+    _shape(out, q.shape, "out")
+    _shape(locs, topk.shape, "locs")
+    _shape(req, (B,), "req")
+    if scales.dim() != 4:
+        raise ValueError("scales must be [requests, blocks, 2, heads]")
+    R = scales.shape[0]
+    _shape(scales, fmt.scales_shape(R, max_seq_len), "scales")
+    _shape(lse, (B, S, H), "lse")
+    _shape(weights, (B, S, K), "weights")
+    _shape(acc, (R, max_seq_len), "acc")
+    if rows.shape[-1] != fmt.item_size_bytes:
+        raise ValueError("rows must be %d bytes wide" % fmt.item_size_bytes)
+    i64x3 = ctypes.c_int64 * 3
+    with _on_device(q.device.index if q.is_cuda else None):
+        args = _HsAttendArgs(
+            _sptr(q, "q"), _sptr(out, "out"), _dtype_code(q, "q", False), B, S, K, H, R,
+            max_seq_len, D ** -0.5 if sm_scale is None else sm_scale, i64x3(*q.stride()[:3]),
+            i64x3(*out.stride()[:3]), _dptr(rows, torch.uint8, "rows"),
+            rows.numel() // fmt.item_size_bytes, _dptr(locs, torch.int32, "locs"),
+            _dptr(topk, torch.int32, "topk"), _dptr(req, torch.int32, "req"),
+            _dptr(scales, torch.float32, "scales"), _dptr(lse, torch.float32, "lse"),
+            _dptr(weights, torch.float32, "weights"), _dptr(acc, torch.float32, "acc"),
+            _dptr(workspace, None, "workspace"),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+        rc = load_library().hs_attend(ctypes.byref(fmt), ctypes.byref(args), _stream_ptr(stream))
+        _check(rc, "hs_attend")
+
+
+def hs_accumulate(weights, topk, req, acc, counts=None, stream=None) -> None:
+    """acc[req[b], topk[b, s, j]] += weights[b, s, j] for the first counts[b] steps
+    (all by default).  weights fp32 and topk int32 [batch, steps, top_k], acc fp32 [R, L]."""
+    import torch
+    if topk.dim() != 3:
+        raise ValueError("topk must be [batch, steps, top_k]")
+    B, S, K = topk.shape
+    _shape(weights, (B, S, K), "weights")
+    _shape(req, (B,), "req")
+    _shape(counts, (B,), "counts")
+    if acc.dim() != 2:
+        raise ValueError("acc must be [requests, tokens]")
+    with _on_device(acc.device.index if acc.is_cuda else None):
+        rc = load_library().hs_accumulate(
+            _dptr(weights, torch.float32, "weights"), _dptr(topk, torch.int32, "topk"),
+            _dptr(req, torch.int32, "req"), _dptr(counts, torch.int32, "counts"), B, S, K,
+            _dptr(acc, torch.float32, "acc"), acc.shape[0], acc.shape[1], _stream_ptr(stream))
+        _check(rc, "hs_accumulate")
+
+
+def hs_evict(acc, req, seq_lens, recent: int, keep, kept, kept_acc=None, stream=None) -> None:
+    """Chooses the tokens that each request keeps: keep int32 [batch, budget] and kept
+    int32 [batch] (out), kept_acc fp32 [batch, budget] (out) from acc fp32 [R, L]."""
+    import torch
+    if acc.dim() != 2 or keep.dim() != 2:
+        raise ValueError("acc must be [requests, tokens] and keep [batch, budget]")
+    B, budget = keep.shape
+    _shape(req, (B,), "req")
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(kept, (B,), "kept")
+    _shape(kept_acc, (B, budget), "kept_acc")
+    with _on_device(acc.device.index if acc.is_cuda else None):
+        rc = load_library().hs_evict(
+            _dptr(acc, torch.float32, "acc"), _dptr(req, torch.int32, "req"),
+            _dptr(seq_lens, torch.int32, "seq_lens"), B, recent, budget, acc.shape[0],
+            acc.shape[1], _dptr(keep, torch.int32, "keep"), _dptr(kept, torch.int32, "kept"),
+            _dptr(kept_acc, torch.float32, "kept_acc"), _stream_ptr(stream))
+        _check(rc, "hs_evict")
+
+
+def hs_compact_kv(fmt: HsKvFormat, src_rows, src_scales, src_req, keep, kept, dst_rows,
+                  dst_scales, dst_req, stream=None) -> None:
+    """Moves the kept tokens (hs_evict's keep and kept) of requests src_req of one
+    store of rows to the first places of requests dst_req of another."""
+    import torch
+    sR, sL = _store(fmt, src_rows, src_scales, "src_")
+    dR, dL = _store(fmt, dst_rows, dst_scales, "dst_")
+    if keep.dim() != 2:
+        raise ValueError("keep must be [batch, budget]")
+    B, budget = keep.shape
+    _shape(kept, (B,), "kept")
+    _shape(src_req, (B,), "src_req")
+    _shape(dst_req, (B,), "dst_req")
+    with _on_device(keep.device.index if keep.is_cuda else None):
+        rc = load_library().hs_compact_kv(
+            ctypes.byref(fmt), _dptr(src_rows, torch.uint8, "src_rows"),
+            _dptr(src_scales, torch.float32, "src_scales"), sR, sL,
+            _dptr(src_req, torch.int32, "src_req"), _dptr(keep, torch.int32, "keep"),
+            _dptr(kept, torch.int32, "kept"), B, budget, _dptr(dst_rows, torch.uint8, "dst_rows"),
+            _dptr(dst_scales, torch.float32, "dst_scales"), dR, dL,
+            _dptr(dst_req, torch.int32, "dst_req"), _stream_ptr(stream))
+        _check(rc, "hs_compact_kv")

@@ -70,6 +70,80 @@ class SwapInCache:
         """Write-back of newly decoded KV rows (host pool, extra page, hot copy)."""
         B.hs_append_rows(self.handle, layer_id, req, tok, seq_lens, rows, stream)
 
+    # ---- 8-bit key/value rows (binding.make_kv_format) --------------------------
+
+    def kv_scales(self, fmt: B.HsKvFormat) -> torch.Tensor:
+        """Scales of one layer's rows: fp32 [R, NB, 2, Hkv]."""
+        return torch.zeros(fmt.scales_shape(self.cfg.num_requests, self.cfg.max_seq_len),
+                           device=self.device)
+
+    def append_kv(self, fmt: B.HsKvFormat, scales: torch.Tensor, k: torch.Tensor,
+                  v: torch.Tensor, req: torch.Tensor, start: torch.Tensor, count: torch.Tensor,
+                  layer_id: int = 0, stream=None) -> None:
+        """Quantises new keys and values [batch, tokens, Hkv, D] and writes them back
+        (host pool, extra page, hot copy)."""
+        B.hs_append_kv(self.handle, layer_id, fmt, k, v, req, start, count, scales, stream)
+
+    def attend(self, fmt: B.HsKvFormat, scales: torch.Tensor, q: torch.Tensor,
+               topk: torch.Tensor, device_locs: torch.Tensor, req_pool_indices: torch.Tensor,
+               layer_id: int = 0, lse: bool = False, weights: bool = False,
+               acc: Optional[torch.Tensor] = None, sm_scale: Optional[float] = None,
+               out: Optional[Dict[str, torch.Tensor]] = None, stream=None):
+        """Attention of q [batch, steps, heads, D] over the rows that a swap-in located."""
+        Bn, S, K = topk.shape
+        o = dict(out or {})
+        if "out" not in o:
+            o["out"] = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        if lse and "lse" not in o:
+            o["lse"] = torch.empty(q.shape[:3], device=self.device)
+        if (weights or (acc is not None and S > 1)) and "weights" not in o:
+            o["weights"] = torch.empty((Bn, S, K), device=self.device)
+        need = B.hs_attend_workspace_bytes(fmt, Bn, S, K, q.shape[2])
+        if need and "workspace" not in o:
+            o["workspace"] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        B.hs_attend(fmt, q, self.device_kv[layer_id], device_locs, topk, req_pool_indices, scales,
+                    self.cfg.max_seq_len, o["out"], o.get("lse"), o.get("weights"), acc, sm_scale,
+                    o.get("workspace"), stream)
+        return o
+
+    def evict(self, fmt: B.HsKvFormat, scales: List[torch.Tensor], acc: List[torch.Tensor],
+              requests: List[int], seq_lens: List[int], budget: int, recent: int,
+              stream=None) -> List[int]:
+        """Cuts the given requests (lengths seq_lens) to `budget` tokens in every layer:
+        the last `recent` and those of the largest accumulated weight acc[layer]
+        [R, max_seq_len].  Kept rows move to the first positions of the host pools;
+        scales[layer] and acc[layer] follow; the requests' cache state is reset and
+        their new lengths are returned.  Needs budget rows of device memory per request."""
+        kept = [min(n, budget) for n in seq_lens]
+        nb = fmt.num_blocks(budget)
+        ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(
+            torch.cuda.current_stream(self.device))
+        with torch.cuda.device(self.device), ctx:
+            i32 = dict(dtype=torch.int32, device=self.device)
+            req, lens = torch.tensor(requests, **i32), torch.tensor(seq_lens, **i32)
+            at = torch.arange(len(requests), **i32)
+            # the entries (request, position) that are written back
+            each = torch.tensor(kept, device=self.device)
+            total = sum(kept)
+            row = torch.repeat_interleave(at.long(), each, output_size=total)
+            pos = torch.arange(total, device=self.device) - (each.cumsum(0) - each)[row]
+            keep = torch.empty((len(requests), budget), **i32)
+            count = torch.empty(len(requests), **i32)
+            sums = torch.empty((len(requests), budget), device=self.device)
+            rows = torch.empty((len(requests), budget, self.cfg.item_size_bytes),
+                               dtype=torch.uint8, device=self.device)
+            self.reset_requests(req)
+            for layer in range(self.cfg.num_layers):
+                B.hs_evict(acc[layer], req, lens, recent, keep, count, sums)
+                new = torch.zeros((len(requests), nb, 2, fmt.num_kv_heads), device=self.device)
+                B.hs_compact_kv(fmt, self.host_pools[layer], scales[layer], req, keep, count,
+                                rows, new, at)
+                self.append_rows(req[row], pos.to(torch.int32), count[row], rows[row, pos], layer)
+                scales[layer][req.long(), :nb] = new[:, :scales[layer].shape[1]]
+                acc[layer][req.long()] = 0
+                acc[layer][req.long(), :budget] = sums[:, :self.cfg.max_seq_len]
+        return kept
+
     def reset_requests(self, req_pool_indices: torch.Tensor, stream=None) -> None:
         B.hs_reset_requests(self.handle, req_pool_indices, stream)
 

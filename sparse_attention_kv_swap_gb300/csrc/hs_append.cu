@@ -33,32 +33,6 @@ struct AppendArgs {
     uint32_t* status;
 };
 
-// Hot slot holding token t of request q, or -1 (bounded probe of the hash
-// bank, or one load of the dense map).
-__device__ int resident_slot(const Dims& d, const LayerView& lv, int q, int t,
-                             uint32_t* status) {
-    if (d.dense) {
-        const int slot = lv.map[(long long)q * d.L + t];
-        return (slot >= 0 && slot < d.H) ? slot : -1;
-    }
-    const long long* bank = lv.bank + (long long)q * d.hash_size;
-    const unsigned mask = (unsigned)d.hash_size - 1u;
-    unsigned p = hash_token(t, d.hash_shift);
-    for (int n = 0; n < d.hash_size; ++n) {
-        const long long x = bank[p];
-        if (x == kEmpty) return -1;
-        if (x >= 0 && (int)(x >> 32) == t) {
-            const int slot = (int)(x & 0xffffffffll);
-            if (slot < d.H) return slot;
-            atomicOr(status, HS_STATUS_PROBE_LIMIT);  // corrupt entry
-            return -1;
-        }
-        p = (p + 1u) & mask;
-    }
-    atomicOr(status, HS_STATUS_PROBE_LIMIT);
-    return -1;
-}
-
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a) {
     const int lane = threadIdx.x & 31;
     const int i = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);

@@ -1,0 +1,367 @@
+// Quantisation of keys and values into 8-bit rows with a scale for each block
+// of tokens and head, and the compaction of a sequence after an eviction
+// (sm_103a).  Layouts and rounding rules: include/hisparse_swap.h.
+//
+// A scale group is the D values of T tokens of one (block, K or V, head).  One
+// CTA owns one group: it holds the group's values in registers, takes their
+// largest magnitude (one block reduction), turns it into the scale and stores
+// the codes, so that the input is read once and the codes are written once.
+// Both kernels are bound by memory traffic: 3 bytes per element to quantise
+// 16-bit values, 2 to compact.
+#include "hs_kv.cuh"
+
+namespace hs {
+namespace {
+
+// Units of 16 elements (16 bytes of codes) that a thread keeps in registers;
+// groups larger than kHeld * blockDim.x units read the rest twice.
+constexpr int kHeld = 4;
+constexpr int kMaxThreads = 512;
+
+int group_threads(int units) {
+    int t = 32;
+    while (t < kMaxThreads && t * kHeld < units) t *= 2;
+    return t;
+}
+
+// 16 consecutive input elements, as loaded.
+template <int DTYPE>
+struct Raw {
+    static constexpr int kVecs = DTYPE == HS_DTYPE_FP32 ? 4 : 2;
+    uint4 v[kVecs];
+
+    __device__ __forceinline__ void load(const void* base, long long at, bool vec) {
+        if (vec) {
+            const uint4* p = reinterpret_cast<const uint4*>(
+                static_cast<const uint8_t*>(base) + at * (DTYPE == HS_DTYPE_FP32 ? 4 : 2));
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) v[i] = ld_stream_v4(p + i);
+        } else {
+            uint32_t w[4 * kVecs];
+#pragma unroll
+            for (int i = 0; i < 4 * kVecs; ++i) {
+                if constexpr (DTYPE == HS_DTYPE_FP32) {
+                    w[i] = static_cast<const uint32_t*>(base)[at + i];
+                } else {
+                    const uint16_t* p = static_cast<const uint16_t*>(base) + at + 2 * i;
+                    w[i] = (uint32_t)p[0] | ((uint32_t)p[1] << 16);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
+
+    // Elements 4 * i .. 4 * i + 3.
+    __device__ __forceinline__ void get(int i, float (&x)[4]) const {
+        if constexpr (DTYPE == HS_DTYPE_FP32) {
+            x[0] = __uint_as_float(v[i].x);
+            x[1] = __uint_as_float(v[i].y);
+            x[2] = __uint_as_float(v[i].z);
+            x[3] = __uint_as_float(v[i].w);
+        } else {
+            const uint32_t lo = i & 1 ? v[i >> 1].z : v[i >> 1].x;
+            const uint32_t hi = i & 1 ? v[i >> 1].w : v[i >> 1].y;
+            if constexpr (DTYPE == HS_DTYPE_BF16) {
+                x[0] = __uint_as_float(lo << 16);
+                x[1] = __uint_as_float(lo & 0xffff0000u);
+                x[2] = __uint_as_float(hi << 16);
+                x[3] = __uint_as_float(hi & 0xffff0000u);
+            } else {
+                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                x[0] = p.x;
+                x[1] = p.y;
+                x[2] = q.x;
+                x[3] = q.y;
+            }
+        }
+    }
+
+    __device__ __forceinline__ float magnitude() const {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x[4];
+            get(i, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a = fmaxf(a, finite_magnitude(x[j]));
+        }
+        return a;
+    }
+
+    template <int CODE>
+    __device__ __forceinline__ uint4 encode(float r) const {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x[4];
+            get(i, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(x[j], r);
+            w[i] = encode4<CODE>(x);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// 16 codes under one scale, as values under another (r = 1 / the new scale).
+template <int CODE>
+__device__ __forceinline__ uint4 recode(const uint4& c, float scale, float r) {
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x[4];
+        decode4<CODE>(in[i], x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], scale), r);
+        w[i] = encode4<CODE>(x);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int CODE>
+__device__ __forceinline__ float magnitude(const uint4& c, float scale) {
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x[4];
+        decode4<CODE>(in[i], x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a = fmaxf(a, finite_magnitude(__fmul_rn(x[j], scale)));
+    }
+    return a;
+}
+
+// Stores 16 bytes of row (q, t) at byte `off`: into the store, and with CACHE
+// into the token's extra-page row (n: the request's length after the call)
+// and its hot row as well.
+template <bool CACHE>
+__device__ __forceinline__ void store_row(const QuantizeArgs& a, int q, int t, int n, int off,
+                                          const uint4& x) {
+    const int W = a.f.item_size_bytes;
+    st_v4(a.rows + ((long long)q * a.L + t) * W + off, x);
+    if constexpr (CACHE) {
+        const Dims& d = a.d;
+        if (d.E > 0 && t >= (n - 1) / d.E * d.E)
+            st_v4(a.lv.device_kv +
+                      ((long long)d.R * (d.H + d.C) + (long long)q * d.E + t % d.E) * W + off,
+                  x);
+        const int slot = resident_slot(d, a.lv, q, t, a.status);
+        if (slot >= 0) {
+            const long long base = (long long)q * (d.H + d.C);
+            st_v4(a.lv.device_kv + (base + a.lv.phys[base + slot]) * W + off, x);
+        }
+    }
+}
+
+template <int CODE, int DTYPE, bool CACHE>
+__global__ void __launch_bounds__(kMaxThreads) quantize_kernel(const QuantizeArgs a) {
+    __shared__ float s_tmp[32];
+    const int heads = a.f.num_kv_heads, D = a.f.head_dim, T = a.f.block_tokens;
+    // CTAs of one block of tokens are neighbours: together they read whole rows
+    const int ch = blockIdx.x % (2 * heads);
+    const int win = blockIdx.x / (2 * heads) % a.windows;
+    const int b = blockIdx.x / (2 * heads) / a.windows;
+    const int q = __ldg(a.req + b), start = __ldg(a.start + b), count = __ldg(a.count + b);
+    if (q < 0 || q >= a.R || start < 0 || count < 0 || count > a.max_count ||
+        start > a.L - count) {
+        if constexpr (CACHE)
+            if (threadIdx.x == 0) atomicOr(a.status, HS_STATUS_BAD_APPEND);
+        return;
+    }
+    const int blk = start / T + win;
+    const long long first = (long long)blk * T;
+    if (first >= start + count || count == 0) return;
+    const int end = start + count;
+    const int lo = first > start ? (int)first : start;
+    const int hi = first + T < end ? (int)first + T : end;
+    const int parts = D >> 4;
+    const int units = (hi - lo) * parts;
+    const int c = ch >= heads, h = c ? ch - heads : ch;
+    const void* base = c ? a.in.v_dev : a.in.k_dev;
+    const int64_t* stride = c ? a.in.v_stride : a.in.k_stride;
+    const long long at0 = b * stride[0] + (lo - start) * stride[1] + h * stride[2];
+
+    float* scale_at = a.scales + (((long long)q * a.NB + blk) * 2 + c) * heads + h;
+    const bool begun = first < lo;  // the block has tokens from before this call
+    const float was = begun ? *scale_at : 0.f;
+    Raw<DTYPE> held[kHeld];
+    float peak = 0.f;
+    const int nt = blockDim.x;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int u = threadIdx.x + i * nt;
+        if (u < units)
+            held[i].load(base, at0 + (long long)(u / parts) * stride[1] + (u % parts) * 16,
+                         a.vec_in);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if ((int)threadIdx.x + i * nt < units) peak = fmaxf(peak, held[i].magnitude());
+    for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
+        Raw<DTYPE> x;
+        x.load(base, at0 + (long long)(u / parts) * stride[1] + (u % parts) * 16, a.vec_in);
+        peak = fmaxf(peak, x.magnitude());
+    }
+    const float now = fmaxf(was, scale_of<CODE>(block_max(peak, s_tmp)));
+    const float r = reciprocal_or_zero(now);
+    if (threadIdx.x == 0) *scale_at = now;
+    const int off = c * heads * D + h * D;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int u = threadIdx.x + i * nt;
+        if (u < units)
+            store_row<CACHE>(a, q, lo + u / parts, end, off + (u % parts) * 16,
+                             held[i].template encode<CODE>(r));
+    }
+    for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
+        Raw<DTYPE> x;
+        x.load(base, at0 + (long long)(u / parts) * stride[1] + (u % parts) * 16, a.vec_in);
+        store_row<CACHE>(a, q, lo + u / parts, end, off + (u % parts) * 16,
+                         x.template encode<CODE>(r));
+    }
+    if (!begun || !(now > was)) return;
+    // The scale grew: the block's older codes are rounded again under it.
+    const int old_units = (int)(lo - first) * parts;
+    for (int u = threadIdx.x; u < old_units; u += nt) {
+        const int t = (int)first + u / parts, o = off + (u % parts) * 16;
+        const uint4 x = *reinterpret_cast<const uint4*>(
+            a.rows + ((long long)q * a.L + t) * a.f.item_size_bytes + o);
+        store_row<CACHE>(a, q, t, end, o, recode<CODE>(x, was, r));
+    }
+}
+
+template <int CODE>
+__global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs a) {
+    __shared__ float s_tmp[32];
+    const int heads = a.f.num_kv_heads, D = a.f.head_dim, T = a.f.block_tokens;
+    const int W = a.f.item_size_bytes;
+    const int ch = blockIdx.x % (2 * heads);
+    const int win = blockIdx.x / (2 * heads) % a.windows;
+    const int b = blockIdx.x / (2 * heads) / a.windows;
+    const int sq = __ldg(a.src_req + b), dq = __ldg(a.dst_req + b);
+    int kept = __ldg(a.kept + b);
+    if (sq < 0 || sq >= a.src_R || dq < 0 || dq >= a.dst_R) return;
+    kept = min(kept, min(a.budget, a.dst_L));
+    const int first = win * T;
+    const int tokens = min(T, kept - first);
+    if (tokens <= 0) return;
+    const int parts = D >> 4;
+    const int units = tokens * parts;
+    const int off = ch * D;
+    const uint8_t* src = a.src + (long long)sq * a.src_L * W + off;
+    uint8_t* dst = a.dst + ((long long)dq * a.dst_L + first) * W + off;
+    const int32_t* keep = a.keep + (long long)b * a.budget + first;
+    const float* scales = a.src_scales + (long long)sq * a.src_NB * 2 * heads + ch;
+
+    uint4 held[kHeld];
+    float scale[kHeld];
+    float peak = 0.f;
+    const int nt = blockDim.x;
+    auto load = [&](int u, uint4& x, float& s) {
+        const int t = __ldg(keep + u / parts);
+        x = make_uint4(0, 0, 0, 0);
+        s = 0.f;
+        if (t >= 0 && t < a.src_L) {
+            x = ld_stream_v4(src + (long long)t * W + (u % parts) * 16);
+            s = __ldg(scales + (long long)(t / T) * 2 * heads);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int u = threadIdx.x + i * nt;
+        if (u < units) load(u, held[i], scale[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if ((int)threadIdx.x + i * nt < units)
+            peak = fmaxf(peak, magnitude<CODE>(held[i], scale[i]));
+    for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
+        uint4 x;
+        float s;
+        load(u, x, s);
+        peak = fmaxf(peak, magnitude<CODE>(x, s));
+    }
+    const float now = scale_of<CODE>(block_max(peak, s_tmp));
+    const float r = reciprocal_or_zero(now);
+    if (threadIdx.x == 0)
+        a.dst_scales[((long long)dq * a.dst_NB + win) * 2 * heads + ch] = now;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int u = threadIdx.x + i * nt;
+        if (u < units)
+            st_v4(dst + (long long)(u / parts) * W + (u % parts) * 16,
+                  recode<CODE>(held[i], scale[i], r));
+    }
+    for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
+        uint4 x;
+        float s;
+        load(u, x, s);
+        st_v4(dst + (long long)(u / parts) * W + (u % parts) * 16, recode<CODE>(x, s, r));
+    }
+}
+
+template <int CODE, bool CACHE>
+void quantize_dtype(const QuantizeArgs& a, int grid, int threads, cudaStream_t s) {
+    if (a.in.dtype == HS_DTYPE_BF16)
+        quantize_kernel<CODE, HS_DTYPE_BF16, CACHE><<<grid, threads, 0, s>>>(a);
+    else if (a.in.dtype == HS_DTYPE_FP16)
+        quantize_kernel<CODE, HS_DTYPE_FP16, CACHE><<<grid, threads, 0, s>>>(a);
+    else
+        quantize_kernel<CODE, HS_DTYPE_FP32, CACHE><<<grid, threads, 0, s>>>(a);
+}
+
+bool grid_of(long long ctas, int* grid) {
+    if (ctas > 0x7fffffffLL) return false;
+    *grid = (int)ctas;
+    return true;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(QuantizeArgs a, bool cache, cudaStream_t s) {
+    const int T = a.f.block_tokens;
+    a.windows = (int)(((long long)a.max_count + T - 2) / T + 1);
+    const int esz = a.in.dtype == HS_DTYPE_FP32 ? 4 : 2;
+    bool vec = ((uintptr_t)a.in.k_dev | (uintptr_t)a.in.v_dev) % 16 == 0;
+    for (int i = 0; i < 3; ++i)
+        vec = vec && (a.in.k_stride[i] * esz) % 16 == 0 && (a.in.v_stride[i] * esz) % 16 == 0;
+    a.vec_in = vec;
+    int grid;
+    if (!grid_of((long long)a.batch * a.windows * 2 * a.f.num_kv_heads, &grid))
+        return cudaErrorInvalidConfiguration;
+    const int threads = group_threads((a.max_count < T ? a.max_count : T) * (a.f.head_dim / 16));
+    if (a.f.code == HS_KV_E4M3) {
+        if (cache)
+            quantize_dtype<HS_KV_E4M3, true>(a, grid, threads, s);
+        else
+            quantize_dtype<HS_KV_E4M3, false>(a, grid, threads, s);
+    } else {
+        if (cache)
+            quantize_dtype<HS_KV_INT8, true>(a, grid, threads, s);
+        else
+            quantize_dtype<HS_KV_INT8, false>(a, grid, threads, s);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_compact(CompactArgs a, cudaStream_t s) {
+    const int T = a.f.block_tokens;
+    const int most = a.budget < a.dst_L ? a.budget : a.dst_L;
+    a.windows = (most + T - 1) / T;
+    int grid;
+    if (!grid_of((long long)a.batch * a.windows * 2 * a.f.num_kv_heads, &grid))
+        return cudaErrorInvalidConfiguration;
+    const int threads = group_threads((most < T ? most : T) * (a.f.head_dim / 16));
+    if (a.f.code == HS_KV_E4M3)
+        compact_kernel<HS_KV_E4M3><<<grid, threads, 0, s>>>(a);
+    else
+        compact_kernel<HS_KV_INT8><<<grid, threads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace hs
