@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 from typing import Dict, List, Optional, Sequence
 
@@ -111,7 +112,7 @@ def make_kv_format(num_kv_heads: int, head_dim: int, block_tokens: int, code: in
 class _HsKvInput(ctypes.Structure):
     _fields_ = [("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
                 ("dtype", ctypes.c_int32), ("k_stride", ctypes.c_int64 * 3),
-                ("v_stride", ctypes.c_int64 * 3)]
+                ("v_stride", ctypes.c_int64 * 3)]  # hs_kv_input
 
 
 class _HsAttendArgs(ctypes.Structure):
@@ -295,7 +296,7 @@ def _hptr(t, name="tensor") -> int:
 
 def _shape(t, shape, name) -> None:
     """The kernels trust the sizes: check them before any launch."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
@@ -574,45 +575,97 @@ def hs_swap_in_noalloc(handle: StateHandle, req_pool_indices, seq_lens, topk, la
 
 
 # ---- 8-bit key/value rows ------------------------------------------------------
+#
+# These calls run once per layer and decode step, some for a few microseconds of GPU time:
+# the checks below take the short way for what is right and leave the wording of errors to
+# the helpers above.
 
-def _dtype_code(t, name, allow_fp32: bool) -> int:
-    import torch
-    codes = {torch.bfloat16: HS_DTYPE_BF16, torch.float16: HS_DTYPE_FP16}
-    if allow_fp32:
-        codes[torch.float32] = HS_DTYPE_FP32
-    if t.dtype not in codes:
-        raise ValueError("%s must have dtype %s" % (name, " or ".join(str(d) for d in codes)))
-    return codes[t.dtype]
+_ATTEND_ARGS = struct.Struct("@PP7if3q3qPq8PN")  # hs_attend_args
+_KV_INPUT = struct.Struct("@PPi3q3q")  # hs_kv_input
 
 
-def _sptr(t, name) -> int:
+def _ptr(t, dtype, name, device) -> int:
+    """_dptr for a call on `device`; None is a null pointer."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    outer = getattr(_call_device, "index", None)
+    _call_device.index = device
+    try:
+        return _dptr(t, dtype, name)
+    finally:
+        _call_device.index = outer
+
+
+def _sptr(t, name, device) -> int:
     """Address of a device tensor that the kernels read by strides; its last
     dimension must be dense."""
-    if not t.is_cuda:
+    d = t.get_device()
+    if d < 0:
         raise ValueError("%s must be in device memory" % name)
-    want = getattr(_call_device, "index", None)
-    if want is not None and t.device.index != want:
-        raise ValueError("%s is on cuda:%d, the call runs on cuda:%d" % (name, t.device.index,
-                                                                        want))
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if d != device:
+        raise ValueError("%s is on cuda:%d, the call runs on cuda:%d" % (name, d, device))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError("the last dimension of %s must be dense" % name)
     return t.data_ptr()
 
 
-def _kv_input(fmt, k, v, req, start, count):
-    if k.dim() != 4 or tuple(k.shape[2:]) != (fmt.num_kv_heads, fmt.head_dim):
+def _device_of(t, name) -> int:
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("%s must be in device memory" % name)
+    return d
+
+
+def _raw_stream(stream, device) -> int:
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError("the stream is on cuda:%d, the call runs on cuda:%d"
+                         % (stream.device.index, device))
+    return stream.cuda_stream
+
+
+def _call(fn, where, device, *args) -> None:
+    """Calls the library with `device` current and raises on an error code."""
+    import torch
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != HS_OK:
+        raise HsError(rc, where)
+
+
+def _dtype_code(t, name, allow_fp32: bool) -> int:
+    import torch
+    d = t.dtype
+    if d is torch.bfloat16:
+        return HS_DTYPE_BF16
+    if d is torch.float16:
+        return HS_DTYPE_FP16
+    if d is torch.float32 and allow_fp32:
+        return HS_DTYPE_FP32
+    raise ValueError("%s must have dtype bfloat16%s float16%s"
+                     % ((name,) + ((",", " or float32") if allow_fp32 else (" or", ""))))
+
+
+def _kv_input(fmt, k, v, req, start, count, device):
+    if k.dim() != 4 or k.shape[2] != fmt.num_kv_heads or k.shape[3] != fmt.head_dim:
         raise ValueError("k must be [batch, tokens, %d, %d], got %s"
                          % (fmt.num_kv_heads, fmt.head_dim, tuple(k.shape)))
     _shape(v, k.shape, "v")
-    if v.dtype != k.dtype:
+    if v.dtype is not k.dtype:
         raise ValueError("k and v must have one dtype")
-    B = k.shape[0]
-    _shape(req, (B,), "req")
-    _shape(start, (B,), "start")
-    _shape(count, (B,), "count")
-    i64x3 = ctypes.c_int64 * 3
-    return _HsKvInput(_sptr(k, "k"), _sptr(v, "v"), _dtype_code(k, "k", True),
-                      i64x3(*k.stride()[:3]), i64x3(*v.stride()[:3]))
+    B = k.shape[:1]
+    _shape(req, B, "req")
+    _shape(start, B, "start")
+    _shape(count, B, "count")
+    return _KV_INPUT.pack(_sptr(k, "k", device), _sptr(v, "v", device),
+                          _dtype_code(k, "k", True), *k.stride()[:3], *v.stride()[:3])
 
 
 def _store(fmt, rows, scales, name):
@@ -620,7 +673,7 @@ def _store(fmt, rows, scales, name):
     if rows.dim() != 3 or rows.shape[2] != fmt.item_size_bytes:
         raise ValueError("%srows must be [requests, tokens, %d], got %s"
                          % (name, fmt.item_size_bytes, tuple(rows.shape)))
-    R, L = rows.shape[0], rows.shape[1]
+    R, L, _ = rows.shape
     _shape(scales, fmt.scales_shape(R, L), name + "scales")
     return R, L
 
@@ -632,14 +685,13 @@ def hs_quantize_kv(fmt: HsKvFormat, k, v, req, start, count, rows, scales, strea
     scales fp32 [R, NB, 2, Hkv], updated."""
     import torch
     R, L = _store(fmt, rows, scales, "")
-    with _on_device(k.device.index if k.is_cuda else None):
-        inp = _kv_input(fmt, k, v, req, start, count)
-        rc = load_library().hs_quantize_kv(
-            ctypes.byref(fmt), ctypes.byref(inp), _dptr(req, torch.int32, "req"),
-            _dptr(start, torch.int32, "start"), _dptr(count, torch.int32, "count"), k.shape[0],
-            k.shape[1], _dptr(rows, torch.uint8, "rows"), _dptr(scales, torch.float32, "scales"),
-            R, L, _stream_ptr(stream))
-        _check(rc, "hs_quantize_kv")
+    i32, dev = torch.int32, k.get_device()
+    inp = _kv_input(fmt, k, v, req, start, count, dev)
+    _call((_lib or load_library()).hs_quantize_kv, "hs_quantize_kv", dev, fmt, inp,
+          _ptr(req, i32, "req", dev), _ptr(start, i32, "start", dev),
+          _ptr(count, i32, "count", dev), k.shape[0], k.shape[1],
+          _ptr(rows, torch.uint8, "rows", dev), _ptr(scales, torch.float32, "scales", dev), R, L,
+          _raw_stream(stream, dev))
 
 
 def hs_append_kv(handle: StateHandle, layer_id: int, fmt: HsKvFormat, k, v, req, start, count,
@@ -649,21 +701,19 @@ def hs_append_kv(handle: StateHandle, layer_id: int, fmt: HsKvFormat, k, v, req,
     import torch
     cfg = handle.cfg
     _shape(scales, fmt.scales_shape(cfg.num_requests, cfg.max_seq_len), "scales")
-    with _on_device(handle.device):
-        inp = _kv_input(fmt, k, v, req, start, count)
-        rc = load_library().hs_append_kv(
-            handle.ptr, layer_id, ctypes.byref(fmt), ctypes.byref(inp),
-            _dptr(req, torch.int32, "req"), _dptr(start, torch.int32, "start"),
-            _dptr(count, torch.int32, "count"), k.shape[0], k.shape[1],
-            _dptr(scales, torch.float32, "scales"), _stream_ptr(stream))
-        _check(rc, "hs_append_kv")
+    i32, dev = torch.int32, handle.device
+    inp = _kv_input(fmt, k, v, req, start, count, dev)
+    _call((_lib or load_library()).hs_append_kv, "hs_append_kv", dev, handle.ptr, layer_id, fmt,
+          inp, _ptr(req, i32, "req", dev), _ptr(start, i32, "start", dev),
+          _ptr(count, i32, "count", dev), k.shape[0], k.shape[1],
+          _ptr(scales, torch.float32, "scales", dev), _raw_stream(stream, dev))
 
 
 def hs_attend_workspace_bytes(fmt: HsKvFormat, batch: int, steps: int, top_k: int,
                               num_heads: int) -> int:
     """Device bytes of workspace that hs_attend needs for these sizes (mostly 0)."""
     args = _HsAttendArgs(batch=batch, steps=steps, top_k=top_k, num_heads=num_heads)
-    n = load_library().hs_attend_workspace_bytes(ctypes.byref(fmt), ctypes.byref(args))
+    n = load_library().hs_attend_workspace_bytes(fmt, ctypes.byref(args))
     if n == ctypes.c_size_t(-1).value:
         raise HsError(HS_ERR_INVALID_ARG, "hs_attend_workspace_bytes")
     return n
@@ -673,19 +723,20 @@ def hs_attend(fmt: HsKvFormat, q, rows, locs, topk, req, scales, max_seq_len: in
               weights=None, acc=None, sm_scale: Optional[float] = None, workspace=None,
               stream=None) -> None:
     """Attention of q [batch, steps, heads, D] (bf16 or fp16) over the rows at
-    locs [batch, steps, top_k] of rows uint8 [N, W].  topk: the rows' positions, req
+    locs [batch, steps, top_k] of rows uint8 [..., W].  topk: the rows' positions, req
     [batch]: their requests, which select the scales [R, NB, 2, Hkv].  Outputs: out
     as q, lse fp32 [batch, steps, heads], weights fp32 [batch, steps, top_k], acc fp32
     [R, max_seq_len] added to.  sm_scale: 1 / sqrt(D) by default."""
     import torch
+    W = fmt.item_size_bytes
     if q.dim() != 4 or q.shape[3] != fmt.head_dim:
         raise ValueError("q must be [batch, steps, heads, %d], got %s"
                          % (fmt.head_dim, tuple(q.shape)))
     B, S, H, D = q.shape
-    if topk.dim() != 3 or topk.shape[0] != B or topk.shape[1] != S:
+    if topk.dim() != 3 or topk.shape[:2] != (B, S):
         raise ValueError("topk must be [%d, %d, top_k], got %s" % (B, S, tuple(topk.shape)))
     K = topk.shape[2]
-    if out.dtype != q.dtype:
+    if out.dtype is not q.dtype:
         raise ValueError("out must have q's dtype")
     _shape(out, q.shape, "out")
     _shape(locs, topk.shape, "locs")
@@ -695,24 +746,22 @@ def hs_attend(fmt: HsKvFormat, q, rows, locs, topk, req, scales, max_seq_len: in
     R = scales.shape[0]
     _shape(scales, fmt.scales_shape(R, max_seq_len), "scales")
     _shape(lse, (B, S, H), "lse")
-    _shape(weights, (B, S, K), "weights")
+    _shape(weights, topk.shape, "weights")
     _shape(acc, (R, max_seq_len), "acc")
-    if rows.shape[-1] != fmt.item_size_bytes:
-        raise ValueError("rows must be %d bytes wide" % fmt.item_size_bytes)
-    i64x3 = ctypes.c_int64 * 3
-    with _on_device(q.device.index if q.is_cuda else None):
-        args = _HsAttendArgs(
-            _sptr(q, "q"), _sptr(out, "out"), _dtype_code(q, "q", False), B, S, K, H, R,
-            max_seq_len, D ** -0.5 if sm_scale is None else sm_scale, i64x3(*q.stride()[:3]),
-            i64x3(*out.stride()[:3]), _dptr(rows, torch.uint8, "rows"),
-            rows.numel() // fmt.item_size_bytes, _dptr(locs, torch.int32, "locs"),
-            _dptr(topk, torch.int32, "topk"), _dptr(req, torch.int32, "req"),
-            _dptr(scales, torch.float32, "scales"), _dptr(lse, torch.float32, "lse"),
-            _dptr(weights, torch.float32, "weights"), _dptr(acc, torch.float32, "acc"),
-            _dptr(workspace, None, "workspace"),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
-        rc = load_library().hs_attend(ctypes.byref(fmt), ctypes.byref(args), _stream_ptr(stream))
-        _check(rc, "hs_attend")
+    if rows.shape[-1] != W:
+        raise ValueError("rows must be %d bytes wide" % W)
+    i32, f32, dev = torch.int32, torch.float32, q.get_device()
+    args = _ATTEND_ARGS.pack(
+        _sptr(q, "q", dev), _sptr(out, "out", dev), _dtype_code(q, "q", False), B, S, K, H, R,
+        max_seq_len, D ** -0.5 if sm_scale is None else sm_scale, *q.stride()[:3],
+        *out.stride()[:3], _ptr(rows, torch.uint8, "rows", dev), rows.numel() // W,
+        _ptr(locs, i32, "locs", dev), _ptr(topk, i32, "topk", dev), _ptr(req, i32, "req", dev),
+        _ptr(scales, f32, "scales", dev), _ptr(lse, f32, "lse", dev),
+        _ptr(weights, f32, "weights", dev), _ptr(acc, f32, "acc", dev),
+        0 if workspace is None else _ptr(workspace, workspace.dtype, "workspace", dev),
+        0 if workspace is None else workspace.numel() * workspace.element_size())
+    _call((_lib or load_library()).hs_attend, "hs_attend", dev, fmt, args,
+          _raw_stream(stream, dev))
 
 
 def hs_accumulate(weights, topk, req, acc, counts=None, stream=None) -> None:
@@ -727,12 +776,11 @@ def hs_accumulate(weights, topk, req, acc, counts=None, stream=None) -> None:
     _shape(counts, (B,), "counts")
     if acc.dim() != 2:
         raise ValueError("acc must be [requests, tokens]")
-    with _on_device(acc.device.index if acc.is_cuda else None):
-        rc = load_library().hs_accumulate(
-            _dptr(weights, torch.float32, "weights"), _dptr(topk, torch.int32, "topk"),
-            _dptr(req, torch.int32, "req"), _dptr(counts, torch.int32, "counts"), B, S, K,
-            _dptr(acc, torch.float32, "acc"), acc.shape[0], acc.shape[1], _stream_ptr(stream))
-        _check(rc, "hs_accumulate")
+    i32, f32, dev = torch.int32, torch.float32, _device_of(acc, "acc")
+    _call((_lib or load_library()).hs_accumulate, "hs_accumulate", dev,
+          _ptr(weights, f32, "weights", dev), _ptr(topk, i32, "topk", dev),
+          _ptr(req, i32, "req", dev), _ptr(counts, i32, "counts", dev), B, S, K,
+          _ptr(acc, f32, "acc", dev), acc.shape[0], acc.shape[1], _raw_stream(stream, dev))
 
 
 def hs_evict(acc, req, seq_lens, recent: int, keep, kept, kept_acc=None, stream=None) -> None:
@@ -746,13 +794,11 @@ def hs_evict(acc, req, seq_lens, recent: int, keep, kept, kept_acc=None, stream=
     _shape(seq_lens, (B,), "seq_lens")
     _shape(kept, (B,), "kept")
     _shape(kept_acc, (B, budget), "kept_acc")
-    with _on_device(acc.device.index if acc.is_cuda else None):
-        rc = load_library().hs_evict(
-            _dptr(acc, torch.float32, "acc"), _dptr(req, torch.int32, "req"),
-            _dptr(seq_lens, torch.int32, "seq_lens"), B, recent, budget, acc.shape[0],
-            acc.shape[1], _dptr(keep, torch.int32, "keep"), _dptr(kept, torch.int32, "kept"),
-            _dptr(kept_acc, torch.float32, "kept_acc"), _stream_ptr(stream))
-        _check(rc, "hs_evict")
+    i32, f32, dev = torch.int32, torch.float32, _device_of(acc, "acc")
+    _call((_lib or load_library()).hs_evict, "hs_evict", dev, _ptr(acc, f32, "acc", dev),
+          _ptr(req, i32, "req", dev), _ptr(seq_lens, i32, "seq_lens", dev), B, recent, budget,
+          acc.shape[0], acc.shape[1], _ptr(keep, i32, "keep", dev), _ptr(kept, i32, "kept", dev),
+          _ptr(kept_acc, f32, "kept_acc", dev), _raw_stream(stream, dev))
 
 
 def hs_compact_kv(fmt: HsKvFormat, src_rows, src_scales, src_req, keep, kept, dst_rows,
@@ -768,12 +814,10 @@ def hs_compact_kv(fmt: HsKvFormat, src_rows, src_scales, src_req, keep, kept, ds
     _shape(kept, (B,), "kept")
     _shape(src_req, (B,), "src_req")
     _shape(dst_req, (B,), "dst_req")
-    with _on_device(keep.device.index if keep.is_cuda else None):
-        rc = load_library().hs_compact_kv(
-            ctypes.byref(fmt), _dptr(src_rows, torch.uint8, "src_rows"),
-            _dptr(src_scales, torch.float32, "src_scales"), sR, sL,
-            _dptr(src_req, torch.int32, "src_req"), _dptr(keep, torch.int32, "keep"),
-            _dptr(kept, torch.int32, "kept"), B, budget, _dptr(dst_rows, torch.uint8, "dst_rows"),
-            _dptr(dst_scales, torch.float32, "dst_scales"), dR, dL,
-            _dptr(dst_req, torch.int32, "dst_req"), _stream_ptr(stream))
-        _check(rc, "hs_compact_kv")
+    i32, f32, u8, dev = torch.int32, torch.float32, torch.uint8, _device_of(keep, "keep")
+    _call((_lib or load_library()).hs_compact_kv, "hs_compact_kv", dev, fmt,
+          _ptr(src_rows, u8, "src_rows", dev), _ptr(src_scales, f32, "src_scales", dev), sR, sL,
+          _ptr(src_req, i32, "src_req", dev), _ptr(keep, i32, "keep", dev),
+          _ptr(kept, i32, "kept", dev), B, budget, _ptr(dst_rows, u8, "dst_rows", dev),
+          _ptr(dst_scales, f32, "dst_scales", dev), dR, dL, _ptr(dst_req, i32, "dst_req", dev),
+          _raw_stream(stream, dev))

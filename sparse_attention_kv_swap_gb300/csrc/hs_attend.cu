@@ -9,13 +9,15 @@ namespace {
 
 constexpr int kSms = 152;
 constexpr int kMaxCluster = 16;
-constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kMaxSmem = 226 * 1024;   // of 227 KB, less the static arrays
+constexpr size_t kHalfSmem = 112 * 1024;  // two CTAs an SM
 
-// Shared-memory layout of a CTA: bytes without the per-token arrays, and theirs.
-void sizes(const hs_kv_format& f, const hs_attend_args& a, int P, AttendShape* sh, size_t* fixed,
-           size_t* token) {
+// Shared memory of a CTA for a cluster of P, and the shape that follows from P.
+void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, AttendShape* sh) {
     AttendKernelArgs& k = sh->a;
-    k.TS = (int)((((long long)a.top_k + P - 1) / P + 15) / 16 * 16);
+    sh->P = P;
+    const long long chunks = ((long long)a.top_k + 15) / 16;
+    k.TS = (int)(16 * ((chunks + P - 1) / P));
     if (k.TS == 0) k.TS = 16;
     // Score rows 4 floats past a multiple of 32 and scale rows 4 past their length: the rows
     // that a warp's lanes touch together fall into different banks.
@@ -24,25 +26,32 @@ void sizes(const hs_kv_format& f, const hs_attend_args& a, int P, AttendShape* s
     const int D = f.head_dim, G = a.num_heads / f.num_kv_heads;
     k.ngroups = (G + 8 * sh->nt - 1) / (8 * sh->nt);
     const int groups = f.num_kv_heads * k.ngroups;
-    // Warps: one task each where they fit; with few heads, a slice is split into parts so
-    // that a CTA has 8 warps or a few more; with many, a warp takes several in turn.
-    const int most = attend_max_warps(D, sh->nt);
+    // Warps: one task each where they fit; with few heads, a CTA's tokens are split into parts
+    // so that it has 8 warps or a few more; with many, a warp takes several in turn.
+    const int most = attend_warps(sh->spill);
     int nsub = groups >= 8 ? 1 : (8 + groups - 1) / groups;
-    if (groups * nsub > most) nsub = most / groups > 0 ? most / groups : 1;
+    if (nsub > 1 && groups * nsub > most) nsub = most / groups;
     if (nsub > k.TS / 16) nsub = k.TS / 16;
     k.nsub = nsub;
     const int rounds = (groups * nsub + most - 1) / most;
     sh->threads = 32 * ((groups * nsub + rounds - 1) / rounds);
+    k.alias = !sh->spill && rounds == 1 && attend_value_passes(D, sh->nt) == 1;
     const size_t HP = (size_t)groups * 8 * sh->nt;
-    *fixed = 4 * ((size_t)a.num_heads * D + 2 * nsub * HP +
-                  (((size_t)P * a.num_heads + 3) & ~(size_t)3) + ((a.num_heads + 3) & ~3));
-    *token = 4 * ((size_t)2 * k.TS + (size_t)2 * f.num_kv_heads * k.TC +
-                  (size_t)a.num_heads * k.TL);
+    const size_t fixed = 2 * nsub * HP + (((size_t)P * a.num_heads + 3) & ~(size_t)3) +
+                         ((a.num_heads + 3) & ~3);
+    const size_t out = (size_t)a.num_heads * D, scale = (size_t)2 * f.num_kv_heads * k.TC;
+    const size_t token = (size_t)3 * k.TS + (size_t)a.num_heads * k.TL;
+    if (sh->spill) {
+        sh->smem = 4 * (fixed + out);
+        k.token_bytes = (int32_t)((4 * (token + scale) + 15) & ~(size_t)15);
+    } else {
+        sh->smem = 4 * (fixed + token + (k.alias ? (out > scale ? out : scale) : out + scale));
+    }
 }
 
-// P: enough CTAs that every SM has two, in slices of 64 tokens or more, and
-// slices of at most 256 tokens while a portable cluster allows; twice the
-// cluster where the scores do not fit; the workspace where that is not enough.
+// P: enough CTAs that every SM has two, of 64 tokens or more, and at most 256
+// tokens each while a portable cluster allows; twice the cluster where two
+// CTAs do not fit an SM; the workspace where not even one does.
 AttendShape shape_of(const hs_kv_format& f, const hs_attend_args& a) {
     AttendShape sh;
     std::memset(&sh, 0, sizeof(sh));
@@ -51,21 +60,16 @@ AttendShape shape_of(const hs_kv_format& f, const hs_attend_args& a) {
     const long long queries = (long long)a.batch * a.steps;
     int P = 1;
     while (P < 8 && (a.top_k > 256 * P || (a.top_k > 64 * P && queries * P < 2 * kSms))) P *= 2;
-    size_t fixed, token;
-    sizes(f, a, P, &sh, &fixed, &token);
-    while (fixed + token > kMaxSmem && P < kMaxCluster) {
+    set_cluster(f, a, P, &sh);
+    while (sh.smem > kHalfSmem && P < kMaxCluster && a.top_k > 64 * P) {
         P *= 2;
-        sizes(f, a, P, &sh, &fixed, &token);
+        set_cluster(f, a, P, &sh);
     }
-    if (fixed + token > kMaxSmem) {
+    if (sh.smem > kMaxSmem) {
         sh.nt = 1;
         sh.spill = true;
-        sizes(f, a, P, &sh, &fixed, &token);
+        set_cluster(f, a, P, &sh);
     }
-    token = (token + 15) & ~(size_t)15;
-    sh.P = P;
-    sh.smem = fixed + (sh.spill ? 0 : token);
-    sh.a.token_bytes = (int32_t)token;
     return sh;
 }
 
@@ -94,12 +98,12 @@ cudaError_t launch_attend(const hs_kv_format& f, const hs_attend_args& a, cudaSt
     k.NB = (a.max_seq_len - 1) / f.block_tokens + 1;
     k.W = f.item_size_bytes;
     k.scale_log2 = a.sm_scale * 1.4426950408889634f;
-    k.vec_q = (uintptr_t)a.q_dev % 16 == 0;
+    k.vec_q = (uintptr_t)a.q_dev % 8 == 0;
     k.vec_out = (uintptr_t)a.out_dev % 8 == 0;
     for (int i = 0; i < 3; ++i) {
         k.q_stride[i] = a.q_stride[i];
         k.out_stride[i] = a.out_stride[i];
-        k.vec_q = k.vec_q && a.q_stride[i] % 8 == 0;
+        k.vec_q = k.vec_q && a.q_stride[i] % 4 == 0;
         k.vec_out = k.vec_out && a.out_stride[i] % 4 == 0;
     }
     k.rows = static_cast<const uint8_t*>(a.rows_dev);

@@ -1,29 +1,29 @@
 // Attention of decode queries over 8-bit rows at device locations (sm_103a);
 // the contract is hs_attend's in include/hisparse_swap.h.
 //
-// A thread-block cluster of P CTAs serves one query position (b, s); CTA r
-// owns the r-th slice of its selected rows, for all heads.  A warp's task is
-// one K/V head (and up to 16 of the query heads that share it) over the tiles
-// of 16 tokens of a slice:
+// A thread-block cluster of P CTAs serves one query position (b, s); the CTAs
+// take its selected rows in turns of 16, for all heads, and drop the masked
+// ones.  A warp's task is one K/V head (and up to 16 of the query heads that
+// share it) over tiles of 16 tokens:
 //   1. scores: S^T[token, head] = K[token, d] Q^T[d, head] with f16
 //      m16n8k16 products summed in 32 bits.  A selected row is read by exactly
 //      one warp per K/V head, so K goes from global memory straight into the
-//      operand registers: lane (g, c) loads a contiguous quarter c of the rows
+//      operand registers: lane (g, c) loads 16 bytes out of each 64 of the rows
 //      g and g + 8, and because a product may visit d in any order, the four
-//      bytes of a word are the four d of one step.  Codes are exact in f16;
+//      bytes of a word are four d of one step.  Codes are exact in f16;
 //      the query is scaled by a power of two per head into f16's range, which
 //      keeps bf16's and f16's significands whole.  Scores go to shared memory
 //      in 32 bits.
 //   2. softmax over the task's own tokens: all scores are known, so there is
 //      no running rescale.
-//   3. O^T[d, head] = V^T[d, token] P^T[token, head]: lane (g, c) loads an
-//      eighth g of the rows of tokens 4 c .. 4 c + 3, a byte permute pairs
-//      neighbouring tokens.  P is exp(s - max) times the token's V scale over
-//      the largest V scale of the task, so it lies in [0, 1] and is rounded
-//      to f16 (11 bits): its rounding error, at most 2^-12 of each term, is
-//      far below the output's own 8 or 11 bits.
+//   3. O^T[d, head] = V^T[d, token] P^T[token, head]: lane (g, c) loads its
+//      16 bytes out of each 128 of the rows of tokens 4 c .. 4 c + 3, a byte
+//      permute pairs neighbouring tokens.  P is exp(s - max) times the token's
+//      V scale over the largest V scale of the task, so it lies in [0, 1] and
+//      is rounded to f16 (11 bits): its rounding error, at most 2^-12 of each
+//      term, is far below the output's own 8 or 11 bits.
 // Then the CTAs of the cluster exchange maxima and sums over distributed
-// shared memory, each adds up a share of the output over the slices in rank
+// shared memory, each adds up a share of the output over the CTAs in rank
 // order, and each turns its own scores into weights with the query's final
 // sums.  Nothing goes through global memory but inputs and outputs, and no
 // result depends on timing.
@@ -59,9 +59,10 @@ struct AttendKernelArgs {
     uint8_t* spill;  // per-token arrays of every CTA if shared memory cannot hold them
     // launch shape
     int32_t vec_q, vec_out;
-    int32_t TS, TC, TL;      // tokens of a slice; strides of the scale and score rows
-    int32_t ngroups, nsub;   // query-head groups of a K/V head; parts of a slice
-    int32_t token_bytes;     // bytes of the per-token arrays
+    int32_t TS, TC, TL;      // tokens of a CTA at most; strides of the scale and score rows
+    int32_t ngroups, nsub;   // query-head groups of a K/V head; parts of a CTA's tokens
+    int32_t alias;           // 1: the output partials reuse the scales' memory
+    int32_t token_bytes;     // bytes of the per-token arrays in the workspace
 };
 
 struct AttendShape {
@@ -75,8 +76,14 @@ struct AttendShape {
 cudaError_t attend_run_e4m3(const AttendShape& sh, int D, cudaStream_t s);
 cudaError_t attend_run_int8(const AttendShape& sh, int D, cudaStream_t s);
 
-// Warps of a CTA at most: the wider tasks need more than 128 registers a thread.
-constexpr int attend_max_warps(int D, int nt) { return D * nt <= 128 ? 16 : 8; }
+// Warps of a CTA at most: 128 registers a thread, more where the arrays are in the workspace
+// (64-bit addresses).
+constexpr int attend_warps(bool spill) { return spill ? 8 : 16; }
+
+// Passes of the V phase, each for a piece of d.
+constexpr int attend_value_passes(int D, int nt) {
+    return D * nt <= 128 ? 1 : (D == 96 ? 3 : 2);
+}
 
 #ifdef __CUDACC__
 
@@ -125,40 +132,62 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// BYTES contiguous bytes (a multiple of 4, so aligned) into registers, or zeros.
-template <int BYTES>
-__device__ __forceinline__ void load_bytes(uint32_t (&r)[BYTES / 4], const uint8_t* p, bool on) {
-    constexpr int V = BYTES % 16 == 0 ? 4 : (BYTES % 8 == 0 ? 2 : 1);
+// A lane's share of a row piece that LANES lanes read together: WORDS words in
+// loads of V words, load i at V * (i * LANES + lane), so that each load of the
+// lanes covers contiguous bytes.
+template <int WORDS>
+constexpr int load_words() {
+    return WORDS % 4 == 0 ? 4 : (WORDS % 2 == 0 ? 2 : 1);
+}
+
+// Byte (element) offset of word w of lane l's share.
+template <int WORDS, int LANES>
+__device__ __forceinline__ int word_at(int w, int l) {
+    constexpr int V = load_words<WORDS>();
+    return 4 * (V * ((w / V) * LANES + l) + w % V);
+}
+
+// `p` is the address of the lane's first load; zeros where off.
+template <int WORDS, int LANES>
+__device__ __forceinline__ void load_share(uint32_t (&r)[WORDS], const uint8_t* p, bool on) {
+    constexpr int V = load_words<WORDS>();
 #pragma unroll
-    for (int i = 0; i < BYTES / 4; i += V) {
+    for (int i = 0; i < WORDS; i += V) {
+        const uint8_t* at = p + 4 * LANES * i;
         if constexpr (V == 4) {
             uint4 x = make_uint4(0, 0, 0, 0);
-            if (on) x = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+            if (on) x = __ldg(reinterpret_cast<const uint4*>(at));
             r[i] = x.x;
             r[i + 1] = x.y;
             r[i + 2] = x.z;
             r[i + 3] = x.w;
         } else if constexpr (V == 2) {
             uint2 x = make_uint2(0, 0);
-            if (on) x = __ldg(reinterpret_cast<const uint2*>(p) + i / 2);
+            if (on) x = __ldg(reinterpret_cast<const uint2*>(at));
             r[i] = x.x;
             r[i + 1] = x.y;
         } else {
-            r[i] = on ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : 0u;
+            r[i] = on ? __ldg(reinterpret_cast<const uint32_t*>(at)) : 0u;
         }
     }
 }
 
-// N pairs of 16-bit elements (N a multiple of 4), or zeros.
-template <int N>
-__device__ __forceinline__ void load_pairs(uint32_t (&r)[N], const uint16_t* p, bool on,
-                                           bool vec) {
-    if (vec) {
-        load_bytes<4 * N>(r, reinterpret_cast<const uint8_t*>(p), on);
-    } else {
+// The 16-bit elements that belong to a lane's words of a K row, as pairs.
+template <int WORDS>
+__device__ __forceinline__ void load_query(uint32_t (&r)[2 * WORDS], const uint16_t* p, int c,
+                                           bool on, bool vec) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            r[i] = on ? (uint32_t)__ldg(p + 2 * i) | ((uint32_t)__ldg(p + 2 * i + 1) << 16) : 0u;
+    for (int w = 0; w < WORDS; ++w) {
+        const uint16_t* at = p + word_at<WORDS, 4>(w, c);
+        if (vec) {
+            uint2 x = make_uint2(0, 0);
+            if (on) x = __ldg(reinterpret_cast<const uint2*>(at));
+            r[2 * w] = x.x;
+            r[2 * w + 1] = x.y;
+        } else {
+            r[2 * w] = on ? (uint32_t)__ldg(at) | ((uint32_t)__ldg(at + 1) << 16) : 0u;
+            r[2 * w + 1] = on ? (uint32_t)__ldg(at + 2) | ((uint32_t)__ldg(at + 3) << 16) : 0u;
+        }
     }
 }
 
@@ -176,11 +205,18 @@ __device__ __forceinline__ float max_over_g(float x) {
 }
 
 template <int CODE, int D, int NT, bool SPILL>
-__global__ void __launch_bounds__(32 * attend_max_warps(D, NT), 1)
+__global__ void __launch_bounds__(32 * attend_warps(SPILL), 1)
     attend_kernel(const AttendKernelArgs a) {
-    constexpr int KW = D / 16;            // words of a lane's quarter of a K row = steps
-    constexpr int VW = D / 32;            // words of a lane's eighth of a V row
-    constexpr int RING = D <= 128 && !SPILL ? 3 : 2;  // tiles in flight in registers
+    // A K row is taken in KP pieces and the V phase in VP passes over the tokens, each for a
+    // piece of d, so that the tiles in flight and the accumulators fit 128 registers.
+    constexpr int KP = D > 128 ? 2 : 1;
+    constexpr int KW = D / 16 / KP;       // words of a lane's share of a K piece = steps
+    constexpr int VP = attend_value_passes(D, NT);
+    constexpr int VD = D / VP;
+    constexpr int VW = VD / 32;           // words of a lane's share of a V piece
+    // tiles (K: pieces of tiles) in flight in registers
+    constexpr int KRING = KP > 1 || (NT == 2 && D > 64) ? 2 : 3;
+    constexpr int VRING = D > 128 || (NT == 2 && D > 64) ? 2 : 3;
     extern __shared__ __align__(16) uint8_t smem[];
     cg::cluster_group cluster = cg::this_cluster();
     const int P = (int)cluster.num_blocks();
@@ -193,48 +229,66 @@ __global__ void __launch_bounds__(32 * attend_max_warps(D, NT), 1)
     const int GP = a.ngroups * 8 * NT;    // padded query heads of a K/V head
     const int HP = a.Hkv * GP;
 
-    // Shared memory: output partials [Hq][D], maxima and sums [nsub][HP], factors [P][Hq],
-    // the query's log2-sum-exp [Hq]; then (or in the workspace) the per-token arrays.
-    float* s_out = reinterpret_cast<float*>(smem);
-    float* s_max = s_out + a.Hq * D;
+    // Shared memory: maxima and sums [nsub][HP], factors [P][Hq], the query's log2-sum-exp
+    // [Hq], output partials [Hq][D]; then (or in the workspace) the per-token arrays.
+    __shared__ int s_scan[33];
+    float* s_max = reinterpret_cast<float*>(smem);
     float* s_sum = s_max + a.nsub * HP;
     float* s_factor = s_sum + a.nsub * HP;
     float* s_lse = s_factor + ((P * a.Hq + 3) & ~3);
+    float* s_out = s_lse + ((a.Hq + 3) & ~3);
+    const int out_floats = a.alias ? max(a.Hq * D, 2 * a.Hkv * a.TC) : a.Hq * D;
     uint8_t* token = SPILL ? a.spill + (size_t)blockIdx.x * a.token_bytes
-                           : reinterpret_cast<uint8_t*>(s_lse + ((a.Hq + 3) & ~3));
-    int* t_loc = reinterpret_cast<int*>(token);               // [TS] row, -1 masked
-    int* t_pos = t_loc + a.TS;                                // [TS] position in the sequence
-    float* t_scale = reinterpret_cast<float*>(t_pos + a.TS);  // [2 Hkv][TC]
-    float* t_score = t_scale + 2 * a.Hkv * a.TC;              // [Hq][TL], base-2 logits
+                           : reinterpret_cast<uint8_t*>(s_out + out_floats);
+    int* t_loc = reinterpret_cast<int*>(token);  // [TS] row, -1 past the last
+    int* t_pos = t_loc + a.TS;                   // [TS] position in the sequence
+    int* t_src = t_pos + a.TS;                   // [TS] entry of the selection
+    float* t_score = reinterpret_cast<float*>(t_src + a.TS);           // [Hq][TL], base-2 logits
+    float* t_scale = !SPILL && a.alias ? s_out : t_score + a.Hq * a.TL;  // [2 Hkv][TC]
 
-    const int first = rank * a.TS;
-    const int mine = max(0, min(a.K - first, a.TS));  // tokens of this slice
-    const long long entry0 = (long long)bs * a.K + first;
+    const long long entry0 = (long long)bs * a.K;
     const int req = __ldg(a.req + b);
     const bool known = req >= 0 && req < a.R;
-    for (int i = tid; i < a.TS; i += nthreads) {
+    // The CTA's entries, masked ones dropped.
+    int live = 0;
+    for (int i0 = 0; i0 < a.TS; i0 += nthreads) {
+        const int i = i0 + tid;
+        const int j = ((i >> 4) * P + rank) * 16 + (i & 15);
         int loc = -1, t = 0;
-        if (i < mine && known) {
-            loc = __ldg(a.locs + entry0 + i);
-            t = __ldg(a.topk + entry0 + i);
-            if (loc < 0 || loc >= a.num_rows || t < 0 || t >= a.L) loc = -1, t = 0;
+        if (i < a.TS && j < a.K) {
+            loc = __ldg(a.locs + entry0 + j);
+            t = __ldg(a.topk + entry0 + j);
+            if (!known || loc < 0 || loc >= a.num_rows || t < 0 || t >= a.L) {
+                loc = -1;
+                if (a.weights) a.weights[entry0 + j] = 0.f;
+            }
         }
-        t_loc[i] = loc;
-        t_pos[i] = t;
+        int n = __syncthreads_count(loc >= 0);
+        int at = live + tid;  // a full turn, or one that only lacks its end, stays in place
+        if (__syncthreads_or(loc >= 0 && tid >= n)) {
+            at = live + block_exclusive_scan(loc >= 0, s_scan, &n);
+        }
+        if (loc >= 0) {
+            t_loc[at] = loc;
+            t_pos[at] = t;
+            t_src[at] = j;
+        }
+        live += n;
     }
+    const int tiles = (live + 15) >> 4;
+    for (int i = live + tid; i < tiles * 16; i += nthreads) t_loc[i] = -1;
     __syncthreads();
     {
         const int per = 2 * a.Hkv;
         const float* base = a.scales + (long long)(known ? req : 0) * a.NB * per;
-        for (int i = tid; i < a.TS * per; i += nthreads) {
+        for (int i = tid; i < tiles * 16 * per; i += nthreads) {
             const int tok = i / per, ch = i - tok * per;
             t_scale[ch * a.TC + tok] =
-                t_loc[tok] >= 0 ? __ldg(base + (long long)(t_pos[tok] / a.T) * per + ch) : 0.f;
+                tok < live ? __ldg(base + (long long)(t_pos[tok] / a.T) * per + ch) : 0.f;
         }
     }
     __syncthreads();
 
-    const int tiles = a.TS >> 4;
     const int groups = a.Hkv * a.ngroups;
     for (int task = warp; task < groups * a.nsub; task += nwarps) {
         const int sub = task / groups, hg = task - sub * groups;
@@ -244,62 +298,94 @@ __global__ void __launch_bounds__(32 * attend_max_warps(D, NT), 1)
         const float* sv = t_scale + (a.Hkv + h) * a.TC;
         float* score = t_score + (h * a.G + j0) * a.TL;
 
-        // Queries as the B operand: lane (g, c) holds head g's quarter c.
-        uint32_t qf[NT][KW][2];
-        float factor[NT][2];  // of the scores of heads 2 c and 2 c + 1
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int j = j0 + nt * 8 + g;
-            const bool on = j < a.G;
-            const long long at = b * a.q_stride[0] + st * a.q_stride[1] +
-                                 (long long)(h * a.G + j) * a.q_stride[2] + c * (D / 4);
-            uint32_t raw[D / 8];
-            load_pairs<D / 8>(raw, static_cast<const uint16_t*>(a.q) + at, on, a.vec_q);
-            float peak = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const float2 x = pair(raw[i], a.fp16);
-                peak = fmaxf(peak, fmaxf(fabsf(x.x), fabsf(x.y)));
-            }
-            peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
-            peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
-            // the head's largest element goes to [2^14, 2^15), f16's top
-            int e = (int)(__float_as_uint(peak) >> 23) - 127;
-            e = e < -100 ? -100 : e;
-            const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-#pragma unroll
-            for (int w = 0; w < KW; ++w) {
-                const float2 x = pair(raw[2 * w], a.fp16), y = pair(raw[2 * w + 1], a.fp16);
-                qf[nt][w][0] = pack_half2(x.x * up, x.y * up);
-                qf[nt][w][1] = pack_half2(y.x * up, y.y * up);
-            }
-            const float down =
-                __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
-            factor[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
-            factor[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
-        }
-
         // ---- scores --------------------------------------------------------------
         float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
         {
-            const uint8_t* kbase = a.rows + h * D + c * (D / 4);
-            uint32_t kr[RING][2][KW];
-            auto load_k = [&](uint32_t (&r)[2][KW], int tile) {
+            const uint8_t* kbase = a.rows + h * D + word_at<KW, 4>(0, c);
+            uint32_t kr[KRING][2][KW];
+            // piece u: part u % KP of tile u / KP
+            auto load_k = [&](uint32_t (&r)[2][KW], int u) {
+                const int tile = tile0 + u / KP;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int loc = tile < tile1 ? t_loc[tile * 16 + g + 8 * i] : -1;
-                    load_bytes<4 * KW>(r[i], kbase + (long long)loc * a.W, loc >= 0);
+                    load_share<KW, 4>(r[i], kbase + (u % KP) * (D / KP) + (long long)loc * a.W,
+                                      loc >= 0);
                 }
             };
+            if constexpr (KP == 1) {
 #pragma unroll
-            for (int i = 0; i < RING; ++i) load_k(kr[i], tile0 + i);
-            for (int tile = tile0; tile < tile1; tile += RING) {
+                for (int i = 0; i < KRING; ++i) load_k(kr[i], i);
+            }
+
+            // Queries as the B operand: lane (g, c) holds head g's elements of its words.
+            uint32_t qf[NT][KP][KW][2];
+            float factor[NT][2];  // of the scores of heads 2 c and 2 c + 1
 #pragma unroll
-                for (int i = 0; i < RING; ++i) {
-                    if (tile + i >= tile1) break;
-                    float s[NT][2][4] = {};
+            for (int nt = 0; nt < NT; ++nt) {
+                const int j = j0 + nt * 8 + g;
+                const long long at = b * a.q_stride[0] + st * a.q_stride[1] +
+                                     (long long)(h * a.G + j) * a.q_stride[2];
+                float peak = 0.f;
+#pragma unroll
+                for (int p = 0; p < KP; ++p) {
+                    uint32_t raw[2 * KW];
+                    load_query<KW>(raw, static_cast<const uint16_t*>(a.q) + at + p * (D / KP), c,
+                                   j < a.G, a.vec_q);
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) {
+                        qf[nt][p][w][0] = raw[2 * w];
+                        qf[nt][p][w][1] = raw[2 * w + 1];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 x = pair(raw[2 * w + i], a.fp16);
+                            peak = fmaxf(peak, fmaxf(fabsf(x.x), fabsf(x.y)));
+                        }
+                    }
+                }
+                peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+                peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
+                // the head's largest element goes to [2^14, 2^15), f16's top
+                int e = (int)(__float_as_uint(peak) >> 23) - 127;
+                e = e < -100 ? -100 : e;
+                const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+#pragma unroll
+                for (int p = 0; p < KP; ++p) {
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 x = pair(qf[nt][p][w][i], a.fp16);
+                            qf[nt][p][w][i] = pack_half2(x.x * up, x.y * up);
+                        }
+                    }
+                }
+                const float down =
+                    __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
+                factor[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+                factor[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+            }
+
+            if constexpr (KP > 1) {  // no registers for them before
+#pragma unroll
+                for (int i = 0; i < KRING; ++i) load_k(kr[i], i);
+            }
+
+            const int pieces = (tile1 - tile0) * KP;
+            float s[NT][2][4];
+            for (int u = 0; u < pieces; u += KRING) {
+#pragma unroll
+                for (int i = 0; i < KRING; ++i) {
+                    if (u + i >= pieces) break;
+                    const int part = i % KP;
+                    if (part == 0) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) s[nt][0][k] = s[nt][1][k] = 0.f;
+                    }
 #pragma unroll
                     for (int w = 0; w < KW; ++w) {
                         uint32_t a0, a1, a2, a3;
@@ -307,11 +393,13 @@ __global__ void __launch_bounds__(32 * attend_max_warps(D, NT), 1)
                         halves<CODE>(kr[i][1][w], a1, a3);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma(s[nt][w & 1], a0, a1, a2, a3, qf[nt][w][0], qf[nt][w][1]);
+                            mma(s[nt][w & 1], a0, a1, a2, a3, qf[nt][part][w][0],
+                                qf[nt][part][w][1]);
                     }
-                    load_k(kr[i], tile + i + RING);
-                    const int t0 = (tile + i) * 16 + g;
-                    const bool on0 = t_loc[t0] >= 0, on1 = t_loc[t0 + 8] >= 0;
+                    load_k(kr[i], u + i + KRING);
+                    if (part != KP - 1) continue;
+                    const int t0 = (tile0 + (u + i) / KP) * 16 + g;
+                    const bool on0 = t0 < live, on1 = t0 + 8 < live;
                     const float k0 = sk[t0], k1 = sk[t0 + 8];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -335,18 +423,19 @@ __global__ void __launch_bounds__(32 * attend_max_warps(D, NT), 1)
         }
 
         // ---- values --------------------------------------------------------------
-        const uint8_t* vbase = a.rows + (a.Hkv + h) * D + g * (D / 8);
-        uint32_t vr[RING][4][VW];
-        auto load_v = [&](uint32_t (&r)[4][VW], int tile) {
+        const uint8_t* vbase = a.rows + (a.Hkv + h) * D + word_at<VW, 8>(0, g);
+        uint32_t vr[VRING][4][VW];
+        auto load_v = [&](uint32_t (&r)[4][VW], int tile, int part) {
             int4 loc = make_int4(-1, -1, -1, -1);
             if (tile < tile1) loc = *reinterpret_cast<const int4*>(t_loc + tile * 16 + 4 * c);
-            load_bytes<4 * VW>(r[0], vbase + (long long)loc.x * a.W, loc.x >= 0);
-            load_bytes<4 * VW>(r[1], vbase + (long long)loc.y * a.W, loc.y >= 0);
-            load_bytes<4 * VW>(r[2], vbase + (long long)loc.z * a.W, loc.z >= 0);
-            load_bytes<4 * VW>(r[3], vbase + (long long)loc.w * a.W, loc.w >= 0);
+            const uint8_t* p = vbase + part * VD;
+            load_share<VW, 8>(r[0], p + (long long)loc.x * a.W, loc.x >= 0);
+            load_share<VW, 8>(r[1], p + (long long)loc.y * a.W, loc.y >= 0);
+            load_share<VW, 8>(r[2], p + (long long)loc.z * a.W, loc.z >= 0);
+            load_share<VW, 8>(r[3], p + (long long)loc.w * a.W, loc.w >= 0);
         };
 #pragma unroll
-        for (int i = 0; i < RING; ++i) load_v(vr[i], tile0 + i);
+        for (int i = 0; i < VRING; ++i) load_v(vr[i], tile0 + i, 0);
 
         float head_max[NT], head_sum[NT];  // of head g of each 8-head tile
 #pragma unroll
@@ -356,7 +445,6 @@ __global__ void __launch_bounds__(32 * attend_max_warps(D, NT), 1)
             const float from0 = __shfl_sync(0xffffffffu, m0, g >> 1);
             const float from1 = __shfl_sync(0xffffffffu, m1, g >> 1);
             head_max[nt] = g & 1 ? from1 : from0;
-            head_sum[nt] = 0.f;
         }
         float ref = 0.f;  // largest V scale of the task's tokens
         for (int i = tile0 * 16 + lane; i < tile1 * 16; i += 32) ref = fmaxf(ref, sv[i]);
@@ -366,102 +454,119 @@ __global__ void __launch_bounds__(32 * attend_max_warps(D, NT), 1)
         const float inv = ref > 0.f ? 1.f / ref : 0.f;
         __syncwarp();  // the warp's scores are in shared memory
 
-        float o[2 * VW][NT][4] = {};
-        for (int tile = tile0; tile < tile1; tile += RING) {
+        float fold[NT][2];  // of the partial outputs of heads 2 c and 2 c + 1
 #pragma unroll
-            for (int i = 0; i < RING; ++i) {
-                if (tile + i >= tile1) break;
-                const int t0 = (tile + i) * 16 + 4 * c;
-                const float4 scale = *reinterpret_cast<const float4*>(sv + t0);
-                uint32_t pf[NT][2];
+        for (int part = 0; part < VP; ++part) {
+            float o[2 * VW][NT][4] = {};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) head_sum[nt] = 0.f;
+            for (int tile = tile0; tile < tile1; tile += VRING) {
+#pragma unroll
+                for (int i = 0; i < VRING; ++i) {
+                    if (tile + i >= tile1) break;
+                    const int t0 = (tile + i) * 16 + 4 * c;
+                    const float4 scale = *reinterpret_cast<const float4*>(sv + t0);
+                    uint32_t pf[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (j0 + nt * 8 + g < a.G)
+                            z = *reinterpret_cast<const float4*>(score + (nt * 8 + g) * a.TL + t0);
+                        const float m = head_max[nt] == -INFINITY ? 0.f : head_max[nt];
+                        const float p0 = exp2_fast(z.x - m), p1 = exp2_fast(z.y - m);
+                        const float p2 = exp2_fast(z.z - m), p3 = exp2_fast(z.w - m);
+                        head_sum[nt] += (p0 + p1) + (p2 + p3);
+                        pf[nt][0] = pack_half2(p0 * (scale.x * inv), p1 * (scale.y * inv));
+                        pf[nt][1] = pack_half2(p2 * (scale.z * inv), p3 * (scale.w * inv));
+                    }
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        // bytes of neighbouring tokens side by side: d, d + 1 | d + 2, d + 3
+                        const uint32_t x0 = __byte_perm(vr[i][0][w], vr[i][1][w], 0x5140);
+                        const uint32_t y0 = __byte_perm(vr[i][0][w], vr[i][1][w], 0x7362);
+                        const uint32_t x1 = __byte_perm(vr[i][2][w], vr[i][3][w], 0x5140);
+                        const uint32_t y1 = __byte_perm(vr[i][2][w], vr[i][3][w], 0x7362);
+                        uint32_t a0, a1, a2, a3;
+                        halves<CODE>(x0, a0, a1);
+                        halves<CODE>(x1, a2, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma(o[2 * w][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        halves<CODE>(y0, a0, a1);
+                        halves<CODE>(y1, a2, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma(o[2 * w + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                    }
+                    load_v(vr[i], tile + i + VRING, part);
+                }
+            }
+            if (part + 1 < VP) {
+#pragma unroll
+                for (int i = 0; i < VRING; ++i) load_v(vr[i], tile0 + i, part + 1);
+            }
+            if (part == 0) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (j0 + nt * 8 + g < a.G)
-                        z = *reinterpret_cast<const float4*>(score + (nt * 8 + g) * a.TL + t0);
-                    const float m = head_max[nt] == -INFINITY ? 0.f : head_max[nt];
-                    const float p0 = exp2_fast(z.x - m), p1 = exp2_fast(z.y - m);
-                    const float p2 = exp2_fast(z.z - m), p3 = exp2_fast(z.w - m);
-                    head_sum[nt] += (p0 + p1) + (p2 + p3);
-                    pf[nt][0] = pack_half2(p0 * (scale.x * inv), p1 * (scale.y * inv));
-                    pf[nt][1] = pack_half2(p2 * (scale.z * inv), p3 * (scale.w * inv));
-                }
-#pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                    // bytes of neighbouring tokens side by side: d, d + 1 | d + 2, d + 3
-                    const uint32_t x0 = __byte_perm(vr[i][0][w], vr[i][1][w], 0x5140);
-                    const uint32_t y0 = __byte_perm(vr[i][0][w], vr[i][1][w], 0x7362);
-                    const uint32_t x1 = __byte_perm(vr[i][2][w], vr[i][3][w], 0x5140);
-                    const uint32_t y1 = __byte_perm(vr[i][2][w], vr[i][3][w], 0x7362);
-                    uint32_t a0, a1, a2, a3;
-                    halves<CODE>(x0, a0, a1);
-                    halves<CODE>(x1, a2, a3);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma(o[2 * w][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                    halves<CODE>(y0, a0, a1);
-                    halves<CODE>(y1, a2, a3);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma(o[2 * w + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                }
-                load_v(vr[i], tile + i + RING);
-            }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x = head_sum[nt];
-            x += __shfl_xor_sync(0xffffffffu, x, 1);
-            x += __shfl_xor_sync(0xffffffffu, x, 2);
-            if (c == 0) {
-                const int at = sub * HP + h * GP + j0 + nt * 8 + g;
-                s_max[at] = head_max[nt];
-                s_sum[at] = x;
-            }
-        }
-        // The partial output relative to the slice's maximum: with several parts to a slice
-        // (one task a warp then), the parts are added in order.
-        if (a.nsub > 1) __syncthreads();
-        float fold[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int at = h * GP + j0 + nt * 8 + 2 * c + k;
-                fold[nt][k] = ref;
-                if (a.nsub > 1) {
-                    float m = -INFINITY;
-                    for (int u = 0; u < a.nsub; ++u) m = fmaxf(m, s_max[u * HP + at]);
-                    fold[nt][k] *= exp2_fast(s_max[sub * HP + at] - (m == -INFINITY ? 0.f : m));
+                    float x = head_sum[nt];
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    if (c == 0) {
+                        const int at = sub * HP + h * GP + j0 + nt * 8 + g;
+                        s_max[at] = head_max[nt];
+                        s_sum[at] = x;
+                    }
                 }
             }
-        }
-        for (int u = 0; u < a.nsub; ++u) {
-            if (u == sub) {
+            // The output may take the scales' place: then every warp has one task and VP is 1,
+            // and all are done with the scales here.  Several parts of a slice have one task a
+            // warp too; their outputs are added in order, relative to their common maximum.
+            if (a.alias || a.nsub > 1) __syncthreads();
+            if (part == 0) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int j = j0 + nt * 8 + 2 * c + k;
-                        if (j >= a.G) continue;
-                        float4* dst = reinterpret_cast<float4*>(s_out + (h * a.G + j) * D +
-                                                                g * (D / 8));
-#pragma unroll
-                        for (int w = 0; w < VW; ++w) {
-                            const float f = fold[nt][k];
-                            float4 x = make_float4(o[2 * w][nt][k] * f, o[2 * w][nt][k + 2] * f,
-                                                   o[2 * w + 1][nt][k] * f,
-                                                   o[2 * w + 1][nt][k + 2] * f);
-                            if (u > 0) {
-                                const float4 y = dst[w];
-                                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-                            }
-                            dst[w] = x;
+                        fold[nt][k] = ref;
+                        if (a.nsub > 1) {
+                            const int at = h * GP + j0 + nt * 8 + 2 * c + k;
+                            float m = -INFINITY;
+                            for (int u = 0; u < a.nsub; ++u) m = fmaxf(m, s_max[u * HP + at]);
+                            fold[nt][k] *=
+                                exp2_fast(s_max[sub * HP + at] - (m == -INFINITY ? 0.f : m));
                         }
                     }
                 }
             }
-            if (a.nsub > 1) __syncthreads();
+            for (int u = 0; u < a.nsub; ++u) {
+                if (u == sub) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = j0 + nt * 8 + 2 * c + k;
+                            if (j >= a.G) continue;
+                            const float f = fold[nt][k];
+                            float* row = s_out + (h * a.G + j) * D + part * VD;
+#pragma unroll
+                            for (int w = 0; w < VW; ++w) {
+                                float4* dst =
+                                    reinterpret_cast<float4*>(row + word_at<VW, 8>(w, g));
+                                float4 x =
+                                    make_float4(o[2 * w][nt][k] * f, o[2 * w][nt][k + 2] * f,
+                                                o[2 * w + 1][nt][k] * f,
+                                                o[2 * w + 1][nt][k + 2] * f);
+                                if (u > 0) {
+                                    const float4 y = *dst;
+                                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                                }
+                                *dst = x;
+                            }
+                        }
+                    }
+                }
+                if (a.nsub > 1) __syncthreads();
+            }
         }
     }
     if (a.nsub > 1) {  // one maximum and sum per head of the slice
@@ -532,14 +637,12 @@ __global__ void __launch_bounds__(32 * attend_max_warps(D, NT), 1)
         }
     }
     if (a.weights || a.acc) {
-        for (int i = tid; i < mine; i += nthreads) {
+        for (int i = tid; i < live; i += nthreads) {
             float w = 0.f;
-            if (t_loc[i] >= 0) {
-                for (int j = 0; j < a.Hq; ++j)
-                    w += exp2_fast(t_score[j * a.TL + i] - s_lse[j]);
-                if (a.acc) atomicAdd(a.acc + (long long)req * a.L + t_pos[i], w);
-            }
-            if (a.weights) a.weights[entry0 + i] = w;
+#pragma unroll 4
+            for (int j = 0; j < a.Hq; ++j) w += exp2_fast(t_score[j * a.TL + i] - s_lse[j]);
+            if (a.acc) atomicAdd(a.acc + (long long)req * a.L + t_pos[i], w);
+            if (a.weights) a.weights[entry0 + t_src[i]] = w;
         }
     }
     cluster.sync();  // no CTA leaves while another reads its shared memory

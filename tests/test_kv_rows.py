@@ -48,6 +48,18 @@ def test_header_constants_and_structs(lib):
                 first = decl.split(",")
                 names += [re.findall(r"(\w+)(?:\[\d+\])?$", part.strip())[0] for part in first]
         assert names == [n for n, _ in cls._fields_], struct
+    # the packed forms that the binding passes have the same layout
+    for cls, pack in ((B._HsAttendArgs, B._ATTEND_ARGS), (B._HsKvInput, B._KV_INPUT)):
+        fields = []
+        for _, kind in cls._fields_:
+            n = getattr(kind, "_length_", 1)
+            fields += range(100 + len(fields), 100 + len(fields) + n)
+        a = cls.from_buffer_copy(pack.pack(*fields))
+        flat = []
+        for name, _ in cls._fields_:
+            x = getattr(a, name)
+            flat += list(x) if isinstance(x, ctypes.Array) else [int(x)]
+        assert flat == fields and pack.size == ctypes.sizeof(cls)
 
 
 def test_format_check(lib):
