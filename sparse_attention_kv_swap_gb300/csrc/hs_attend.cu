@@ -8,50 +8,68 @@ namespace hs {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMaxCluster = 16;
-constexpr size_t kMaxSmem = 226 * 1024;   // of 227 KB, less the static arrays
-constexpr size_t kHalfSmem = 112 * 1024;  // two CTAs an SM
+constexpr size_t kSmSmem = 228 * 1024;             // of an SM; a CTA takes 1 KB more than it asks
+constexpr int kSmCols = 512;                       // tensor-memory columns of an SM
+constexpr size_t kStatic = 512;                    // static arrays of the kernel, rounded up
+constexpr size_t kMaxSmem = kSmSmem - 1024 - kStatic;
+constexpr size_t kHalfSmem = kSmSmem / 2 - 1024 - kStatic;  // two CTAs an SM
 
-// Shared memory of a CTA for a cluster of P, and the shape that follows from P.
+// Memory of a CTA for a cluster of P, and the shape that follows from P.
 void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, AttendShape* sh) {
     AttendKernelArgs& k = sh->a;
     sh->P = P;
     const long long chunks = ((long long)a.top_k + 15) / 16;
     k.TS = (int)(16 * ((chunks + P - 1) / P));
     if (k.TS == 0) k.TS = 16;
-    // Score rows 4 floats past a multiple of 32 and scale rows 4 past their length: the rows
-    // that a warp's lanes touch together fall into different banks.
-    k.TL = (k.TS + 31) / 32 * 32 + 4;
-    k.TC = k.TS + 4;
+    k.TC = k.TS + 4;  // scale rows in different banks
     const int D = f.head_dim, G = a.num_heads / f.num_kv_heads;
     k.ngroups = (G + 8 * sh->nt - 1) / (8 * sh->nt);
     const int groups = f.num_kv_heads * k.ngroups;
     // Warps: one task each where they fit; with few heads, a CTA's tokens are split into parts
     // so that it has 8 warps or a few more; with many, a warp takes several in turn.
-    const int most = attend_warps(sh->spill);
+    const int most = attend_warps(D, sh->spill);
     int nsub = groups >= 8 ? 1 : (8 + groups - 1) / groups;
     if (nsub > 1 && groups * nsub > most) nsub = most / groups;
     if (nsub > k.TS / 16) nsub = k.TS / 16;
     k.nsub = nsub;
     const int rounds = (groups * nsub + most - 1) / most;
-    sh->threads = 32 * ((groups * nsub + rounds - 1) / rounds);
-    k.alias = !sh->spill && rounds == 1 && attend_value_passes(D, sh->nt) == 1;
+    const int warps = (groups * nsub + rounds - 1) / rounds;
+    sh->threads = 32 * warps;
+    k.alias = rounds == 1;
+    const int task_tiles = (k.TS / 16 + nsub - 1) / nsub;
+    k.task_cols = 4 * sh->nt * task_tiles;
+    const long long need = (long long)rounds * ((warps + 3) / 4) * k.task_cols;
+    int cols = 32;
+    while (cols < need && cols < 2 * kSmCols) cols *= 2;
+    k.cols = cols;
     const size_t HP = (size_t)groups * 8 * sh->nt;
-    const size_t fixed = 2 * nsub * HP + (((size_t)P * a.num_heads + 3) & ~(size_t)3) +
-                         ((a.num_heads + 3) & ~3);
-    const size_t out = (size_t)a.num_heads * D, scale = (size_t)2 * f.num_kv_heads * k.TC;
-    const size_t token = (size_t)3 * k.TS + (size_t)a.num_heads * k.TL;
+    const size_t fixed = 4 * ((2 * nsub + 1) * HP + (((size_t)P * a.num_heads + 3) & ~(size_t)3));
+    const size_t scale = (size_t)2 * f.num_kv_heads * k.TC, weight = (size_t)groups * k.TS;
+    const size_t token = 4 * ((size_t)3 * k.TS + (scale > weight ? scale : weight));
+    const size_t out = 4 * (size_t)a.num_heads * (D + 4);
+    const size_t queue = (size_t)warps * attend_stages(D) * 16 * D;
+    const size_t rest = k.alias ? (out > queue ? out : queue) : out + queue;
     if (sh->spill) {
-        sh->smem = 4 * (fixed + out);
-        k.token_bytes = (int32_t)((4 * (token + scale) + 15) & ~(size_t)15);
+        sh->smem = fixed + rest;
+        const size_t score = (size_t)rounds * warps * k.task_cols * 128;
+        k.token_bytes = (int32_t)((token + score + 15) & ~(size_t)15);
+        k.cols = 0;
     } else {
-        sh->smem = 4 * (fixed + token + (k.alias ? (out > scale ? out : scale) : out + scale));
+        sh->smem = fixed + token + rest;
+        // Tensor memory is handed out to CTAs as they ask and a cluster must not wait for it while
+        // another cluster's CTA waits elsewhere: a CTA takes shared memory in proportion to
+        // its columns, so that an SM never holds CTAs of these kernels with more columns than it has.
+        const size_t share = kSmSmem / kSmCols * (size_t)cols - 1024 - kStatic;
+        if (sh->smem < share) sh->smem = share;
     }
 }
 
-// P: enough CTAs that every SM has two, of 64 tokens or more, and at most 256
-// tokens each while a portable cluster allows; twice the cluster where two
-// CTAs do not fit an SM; the workspace where not even one does.
+bool fits(const AttendShape& sh, size_t smem) {
+    return sh.smem <= smem && sh.a.cols <= kSmCols;
+}
+
+// P: the fewest CTAs of which two fit an SM, and enough of them, of 64 tokens
+// or more, that every SM has two; the workspace where not even one of 16 fits.
 AttendShape shape_of(const hs_kv_format& f, const hs_attend_args& a) {
     AttendShape sh;
     std::memset(&sh, 0, sizeof(sh));
@@ -59,13 +77,17 @@ AttendShape shape_of(const hs_kv_format& f, const hs_attend_args& a) {
     sh.nt = G > 8 && f.head_dim <= 128 ? 2 : 1;
     const long long queries = (long long)a.batch * a.steps;
     int P = 1;
-    while (P < 8 && (a.top_k > 256 * P || (a.top_k > 64 * P && queries * P < 2 * kSms))) P *= 2;
+    while (P < 8 && a.top_k > 64 * P && queries * P * 2 <= 2 * kSms) P *= 2;
     set_cluster(f, a, P, &sh);
-    while (sh.smem > kHalfSmem && P < kMaxCluster && a.top_k > 64 * P) {
+    while (!fits(sh, kHalfSmem) && P < kMaxCluster && a.top_k > 64 * P) {
         P *= 2;
         set_cluster(f, a, P, &sh);
     }
-    if (sh.smem > kMaxSmem) {
+    while (!fits(sh, kMaxSmem) && P < kMaxCluster && a.top_k > 16 * P) {
+        P *= 2;
+        set_cluster(f, a, P, &sh);
+    }
+    if (!fits(sh, kMaxSmem)) {
         sh.nt = 1;
         sh.spill = true;
         set_cluster(f, a, P, &sh);
@@ -100,6 +122,7 @@ cudaError_t launch_attend(const hs_kv_format& f, const hs_attend_args& a, cudaSt
     k.scale_log2 = a.sm_scale * 1.4426950408889634f;
     k.vec_q = (uintptr_t)a.q_dev % 8 == 0;
     k.vec_out = (uintptr_t)a.out_dev % 8 == 0;
+    k.vec_scale = (uintptr_t)a.scales_dev % 16 == 0 && f.num_kv_heads % 2 == 0;
     for (int i = 0; i < 3; ++i) {
         k.q_stride[i] = a.q_stride[i];
         k.out_stride[i] = a.out_stride[i];

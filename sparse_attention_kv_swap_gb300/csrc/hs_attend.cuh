@@ -7,21 +7,27 @@
 // share it) over tiles of 16 tokens:
 //   1. scores: S^T[token, head] = K[token, d] Q^T[d, head] with f16
 //      m16n8k16 products summed in 32 bits.  A selected row is read by exactly
-//      one warp per K/V head, so K goes from global memory straight into the
-//      operand registers: lane (g, c) loads 16 bytes out of each 64 of the rows
-//      g and g + 8, and because a product may visit d in any order, the four
-//      bytes of a word are four d of one step.  Codes are exact in f16;
+//      one warp per K/V head, so the warps share nothing: each copies the
+//      pieces of its head (cp.async, whole 128-byte lines where D allows:
+//      gathering in 64-byte pieces costs a fifth of the bandwidth) into a queue
+//      of its own in shared memory, several tiles ahead, and reads them back
+//      as operands (ldmatrix).  A product may visit d in any order, so the
+//      four bytes of a word are four d of one step.  Codes are exact in f16;
 //      the query is scaled by a power of two per head into f16's range, which
-//      keeps bf16's and f16's significands whole.  Scores go to shared memory
-//      in 32 bits.
+//      keeps bf16's and f16's significands whole.  Scores stay in 32 bits, in
+//      the fragment's own layout, in tensor memory: 512 columns of an SM that
+//      nothing else here needs, where shared memory would hold a quarter as
+//      many tokens beside the queues.
 //   2. softmax over the task's own tokens: all scores are known, so there is
 //      no running rescale.
-//   3. O^T[d, head] = V^T[d, token] P^T[token, head]: lane (g, c) loads its
-//      16 bytes out of each 128 of the rows of tokens 4 c .. 4 c + 3, a byte
-//      permute pairs neighbouring tokens.  P is exp(s - max) times the token's
-//      V scale over the largest V scale of the task, so it lies in [0, 1] and
-//      is rounded to f16 (11 bits): its rounding error, at most 2^-12 of each
-//      term, is far below the output's own 8 or 11 bits.
+//   3. O^T[d, head] = V^T[d, token] P^T[token, head]: the byte form of
+//      ldmatrix transposes V, so that a word holds four tokens of one d.  The
+//      rows of a K tile are taken in the order 0, 1, 4, 5, .. | 2, 3, 6, 7, ..
+//      so that the transposed P (movmatrix) pairs the same tokens.  P is
+//      exp(s - max) times the token's V scale over the largest V scale of the
+//      task, so it lies in [0, 1] and is rounded to f16 (11 bits): its rounding
+//      error, at most 2^-12 of each term, is far below the output's own 8 or
+//      11 bits.
 // Then the CTAs of the cluster exchange maxima and sums over distributed
 // shared memory, each adds up a share of the output over the CTAs in rank
 // order, and each turns its own scores into weights with the query's final
@@ -30,9 +36,9 @@
 //
 // What bounds it: every row is read once per step, 2 * Hkv * D bytes, for
 // 4 * Hq * D operations, i.e. 2 * (Hq / Hkv) operations a byte: memory, with
-// the products far below the tensor rate even on mma.sync; tcgen05 would want
-// 128 rows of one operand in shared memory, which here would mean writing
-// every code back to shared memory as f16 first.
+// the products far below the tensor rate even on mma.sync; tcgen05.mma would
+// want 128 rows of one operand in shared memory as f16, which here would mean
+// writing every code back after its conversion.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -56,13 +62,15 @@ struct AttendKernelArgs {
     float* lse;
     float* weights;
     float* acc;
-    uint8_t* spill;  // per-token arrays of every CTA if shared memory cannot hold them
+    uint8_t* spill;  // scores and per-token arrays of every CTA if the SM cannot hold them
     // launch shape
-    int32_t vec_q, vec_out;
-    int32_t TS, TC, TL;      // tokens of a CTA at most; strides of the scale and score rows
+    int32_t vec_q, vec_out, vec_scale;  // vector loads and stores are aligned
+    int32_t TS, TC;          // tokens of a CTA at most; stride of a scale row
     int32_t ngroups, nsub;   // query-head groups of a K/V head; parts of a CTA's tokens
-    int32_t alias;           // 1: the output partials reuse the scales' memory
-    int32_t token_bytes;     // bytes of the per-token arrays in the workspace
+    int32_t alias;           // 1: the output partials reuse the queues' memory
+    int32_t task_cols;       // tensor-memory columns of a task's scores
+    int32_t cols;            // of the CTA (0: scores in the workspace)
+    int32_t token_bytes;     // workspace bytes of a CTA
 };
 
 struct AttendShape {
@@ -76,13 +84,15 @@ struct AttendShape {
 cudaError_t attend_run_e4m3(const AttendShape& sh, int D, cudaStream_t s);
 cudaError_t attend_run_int8(const AttendShape& sh, int D, cudaStream_t s);
 
-// Warps of a CTA at most: 128 registers a thread, more where the arrays are in the workspace
-// (64-bit addresses).
-constexpr int attend_warps(bool spill) { return spill ? 8 : 16; }
+constexpr int kMaxCluster = 16;
+// Warps of a CTA at most: 128 registers a thread, twice that for the widest tasks with 64-bit
+// addresses throughout.
+constexpr int attend_warps(int D, bool spill) { return D > 192 && spill ? 8 : 16; }
 
-// Passes of the V phase, each for a piece of d.
-constexpr int attend_value_passes(int D, int nt) {
-    return D * nt <= 128 ? 1 : (D == 96 ? 3 : 2);
+// Tiles in a warp's queue (16 * D bytes each): all but one are on their way
+// while one is used.
+constexpr int attend_stages(int D) {
+    return D <= 64 ? 8 : (D <= 96 ? 5 : (D <= 128 ? 4 : 3));
 }
 
 #ifdef __CUDACC__
@@ -132,53 +142,65 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// A lane's share of a row piece that LANES lanes read together: WORDS words in
-// loads of V words, load i at V * (i * LANES + lane), so that each load of the
-// lanes covers contiguous bytes.
-template <int WORDS>
-constexpr int load_words() {
-    return WORDS % 4 == 0 ? 4 : (WORDS % 2 == 0 ? 2 : 1);
+// Transposes an 8 x 8 matrix of 16-bit elements that the warp holds as pairs.
+__device__ __forceinline__ uint32_t transpose(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
-// Byte (element) offset of word w of lane l's share.
-template <int WORDS, int LANES>
-__device__ __forceinline__ int word_at(int w, int l) {
-    constexpr int V = load_words<WORDS>();
-    return 4 * (V * ((w / V) * LANES + l) + w % V);
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-// `p` is the address of the lane's first load; zeros where off.
-template <int WORDS, int LANES>
-__device__ __forceinline__ void load_share(uint32_t (&r)[WORDS], const uint8_t* p, bool on) {
-    constexpr int V = load_words<WORDS>();
-#pragma unroll
-    for (int i = 0; i < WORDS; i += V) {
-        const uint8_t* at = p + 4 * LANES * i;
-        if constexpr (V == 4) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (on) x = __ldg(reinterpret_cast<const uint4*>(at));
-            r[i] = x.x;
-            r[i + 1] = x.y;
-            r[i + 2] = x.z;
-            r[i + 3] = x.w;
-        } else if constexpr (V == 2) {
-            uint2 x = make_uint2(0, 0);
-            if (on) x = __ldg(reinterpret_cast<const uint2*>(at));
-            r[i] = x.x;
-            r[i + 1] = x.y;
-        } else {
-            r[i] = on ? __ldg(reinterpret_cast<const uint32_t*>(at)) : 0u;
-        }
-    }
+// A tile in the queue is 16 rows of D bytes, their 16-byte chunks permuted by
+// row so that the 8 chunks of one ldmatrix matrix fall into different banks:
+// of rows 0-7 or 8-15 (V), of rows 0, 1, 4, 5, 8, 9, 12, 13 or those two
+// further (K).
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
+    int x = 0;
+    if constexpr (D % 128 == 0)
+        x = (row & 1) | (row >> 1 & 2) | ((row >> 1 ^ row >> 3) & 1) << 2;
+    else if constexpr (D % 64 == 0)  // two rows to 128 bytes
+        x = (row >> 2 & 1) | ((row >> 1 ^ row >> 3) & 1) << 1;
+    else if constexpr (D == 32)
+        x = (row >> 2 ^ row >> 3) & 1;
+    return (uint32_t)(row * D + (chunk ^ x) * 16);
 }
 
-// The 16-bit elements that belong to a lane's words of a K row, as pairs.
-template <int WORDS>
-__device__ __forceinline__ void load_query(uint32_t (&r)[2 * WORDS], const uint16_t* p, int c,
+__device__ __forceinline__ void commit_copies() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits for all but the last N committed groups of copies of this thread.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements, lane l giving the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void read_matrices(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+// Two 16 x 16 matrices of bytes, transposed, lane l giving the address of row l % 16 of matrix
+// l / 16: word i of lane (g, c) holds rows 4 c .. 4 c + 3 of column g + 8 * (i % 2) of matrix i / 2.
+__device__ __forceinline__ void read_transposed(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+// The 16-bit elements 16 w + 4 c .. + 3 of a query row, as pairs.
+template <int STEPS>
+__device__ __forceinline__ void load_query(uint32_t (&r)[2 * STEPS], const uint16_t* p, int c,
                                            bool on, bool vec) {
 #pragma unroll
-    for (int w = 0; w < WORDS; ++w) {
-        const uint16_t* at = p + word_at<WORDS, 4>(w, c);
+    for (int w = 0; w < STEPS; ++w) {
+        const uint16_t* at = p + 16 * w + 4 * c;
         if (vec) {
             uint2 x = make_uint2(0, 0);
             if (on) x = __ldg(reinterpret_cast<const uint2*>(at));
@@ -197,27 +219,286 @@ __device__ __forceinline__ float2 pair(uint32_t w, int fp16) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Largest over the 8 lanes that share c (lanes differ in g).
+// Loads from the shared memory of another CTA of the cluster: `p` is this CTA's own address of
+// the array.
+__device__ __forceinline__ uint32_t remote(const float* p, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(shared_address(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float load_remote(const float* p, int rank) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(remote(p, rank)));
+    return x;
+}
+__device__ __forceinline__ float4 load_remote4(const float* p, int rank) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(remote(p, rank)));
+    return x;
+}
+
+// Reductions over the 8 lanes that share c (lanes differ in g).
 __device__ __forceinline__ float max_over_g(float x) {
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
 }
+__device__ __forceinline__ float sum_over_g(float x) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The scores of a warp's tasks, one score fragment a lane per tile and 8-head
+// tile: in tensor memory (a warp reaches the 32 lanes of its quarter, and the
+// columns divide among the warps of a quarter), or in the workspace.
+template <int NT, bool SPILL>
+struct Scores {
+    uint32_t col;  // first column of the task, with the warp's lanes in the high half
+    float4* mem;
+
+    // `turn`: which of the warp's tasks.
+    __device__ __forceinline__ Scores(const AttendKernelArgs& a, uint32_t base, float* ws, int warp,
+                                      int nwarps, int turn) {
+        if constexpr (SPILL) {
+            mem = reinterpret_cast<float4*>(ws) +
+                  (long long)(turn * nwarps + warp) * (a.task_cols / 4) * 32 + (threadIdx.x & 31);
+        } else {
+            const int rows = (nwarps + 3) >> 2;  // warps of a quarter at most
+            col = base + ((uint32_t)(warp & 3) << 21) +
+                  (uint32_t)((turn * rows + (warp >> 2)) * a.task_cols);
+        }
+    }
+    // All lanes of the warp store and load together.
+    __device__ __forceinline__ void store(int tile, const float (&s)[NT][4]) const {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (SPILL)
+                mem[(tile * NT + nt) * 32] =
+                    make_float4(s[nt][0], s[nt][1], s[nt][2], s[nt][3]);
+            else
+                asm volatile(
+                    "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                        col + (tile * NT + nt) * 4),
+                    "f"(s[nt][0]), "f"(s[nt][1]), "f"(s[nt][2]), "f"(s[nt][3])
+                    : "memory");
+        }
+    }
+    __device__ __forceinline__ void stored() const {
+        if constexpr (!SPILL) asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    }
+    __device__ __forceinline__ void load(int tile, float (&s)[NT][4]) const {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (SPILL) {
+                const float4 x = mem[(tile * NT + nt) * 32];
+                s[nt][0] = x.x, s[nt][1] = x.y, s[nt][2] = x.z, s[nt][3] = x.w;
+            } else {
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(s[nt][0]), "=f"(s[nt][1]), "=f"(s[nt][2]), "=f"(s[nt][3])
+                             : "r"(col + (tile * NT + nt) * 4)
+                             : "memory");
+            }
+        }
+    }
+    // The loaded scores may be used after this.
+    __device__ __forceinline__ void loaded(float (&s)[NT][4]) const {
+        if constexpr (!SPILL) {
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) asm volatile("" : "+f"(s[nt][k]));
+        }
+    }
+};
+
+// Memory of a CTA: maxima and sums [nsub][HP], the query's log2-sum-exp [HP],
+// factors [P][Hq]; the arrays by token; the warps' queues, whose memory the
+// output partials [Hq][D + 4] take over where every warp has one task.  With SPILL
+// the arrays by token lie in the workspace, and the scores behind them.
+template <bool SPILL>
+struct Layout {
+    float *max, *sum, *lse, *factor;
+    int* loc;      // [TS] row
+    int* pos;      // [TS] position in the sequence
+    int* src;      // [TS] entry of the selection
+    float* scale;  // [2 Hkv][TC], then the heads' weights [groups][TS]
+    float* score;  // SPILL
+    float* out;
+    uint8_t* queue;
+
+    __device__ __forceinline__ Layout(const AttendKernelArgs& a, uint8_t* smem, int P, int HP,
+                                      int D, int nwarps, int block) {
+        max = reinterpret_cast<float*>(smem);
+        sum = max + a.nsub * HP;
+        lse = sum + a.nsub * HP;
+        factor = lse + HP;
+        uint8_t* next = reinterpret_cast<uint8_t*>(factor + ((P * a.Hq + 3) & ~3));
+        uint8_t* token = SPILL ? a.spill + (size_t)block * a.token_bytes : next;
+        loc = reinterpret_cast<int*>(token);
+        pos = loc + a.TS;
+        src = pos + a.TS;
+        scale = reinterpret_cast<float*>(src + a.TS);
+        score = scale + ::max(2 * a.Hkv * a.TC, a.Hkv * a.ngroups * a.TS);
+        queue = SPILL ? next : reinterpret_cast<uint8_t*>(score);
+        out = reinterpret_cast<float*>(
+            a.alias ? queue : queue + (size_t)nwarps * attend_stages(D) * 16 * D);
+    }
+};
+
+// The cluster's output and weights, from every CTA's maxima, sums and partial
+// outputs.  What it needs of the launch is read anew rather than kept in
+// registers through the kernel.
+template <int D, int NT, bool SPILL>
+__device__ __forceinline__ void finish(const AttendKernelArgs& a, uint8_t* smem, int HP, int GP,
+                                       int live, uint32_t tmem) {
+    int P, rank, block;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(P));
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(block));
+    const int tid = threadIdx.x, nthreads = blockDim.x;
+    const Layout<SPILL> at(a, smem, P, HP, D, nthreads >> 5, block);
+    const int bs = block / P, b = bs / a.S, st = bs - b * a.S;
+    // All ranks' values are on their way before the first is used: a remote load takes long.
+    for (int j = tid; j < HP; j += nthreads) {
+        const int h = j / GP, i = h * a.G + (j - h * GP);
+        if (j - h * GP >= a.G) {
+            at.lse[j] = INFINITY;  // a padded head has no weight
+            continue;
+        }
+        float x[kMaxCluster], y[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            x[r] = r < P ? load_remote(at.max + j, r) : -INFINITY;
+            y[r] = r < P ? load_remote(at.sum + j, r) : 0.f;
+        }
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) m = fmaxf(m, x[r]);
+        const float safe = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            x[r] = exp2_fast(x[r] - safe);
+            l += y[r] * x[r];
+        }
+        const float norm = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            if (r < P) at.factor[r * a.Hq + i] = x[r] * norm;
+        const float lse2 = m + log2f(l);
+        at.lse[j] = l == 0.f ? INFINITY : lse2;  // weights of an empty query: 0
+        if (rank == 0 && a.lse)
+            a.lse[(long long)bs * a.Hq + i] = l == 0.f ? -INFINITY : lse2 * 0.69314718056f;
+    }
+    __syncthreads();
+    // A share of the output's quads.  The first one's partial outputs come from the other CTAs
+    // while the weights are computed.
+    const int quads = a.Hq * (D / 4);
+    const int lo = quads * rank / P, hi = quads * (rank + 1) / P;
+    float4 y[kMaxCluster / 2];
+    auto fetch_quad = [&](int i, int r0) {
+#pragma unroll
+        for (int r = 0; r < kMaxCluster / 2; ++r)
+            if (r0 + r < P) y[r] = load_remote4(at.out + 4 * (i + i / (D / 4)), r0 + r);
+    };
+    if (lo + tid < hi) fetch_quad(lo + tid, 0);
+    if (a.weights || a.acc) {
+        // Each task's heads first, then the sum over the tasks in their order.
+        const int groups = a.Hkv * a.ngroups, ntasks = groups * a.nsub;
+        const int tiles = (live + 15) >> 4, nwarps = nthreads >> 5, warp = tid >> 5;
+        const int g = (tid & 31) >> 2, c = tid & 3, t_lo = 4 * (g >> 1) + (g & 1);
+        for (int task = warp, turn = 0; task < ntasks; task += nwarps, ++turn) {
+            const int sub = task / groups, hg = task - sub * groups;
+            const int h = hg / a.ngroups, j0 = (hg - h * a.ngroups) * 8 * NT;
+            const int tile0 = tiles * sub / a.nsub, tile1 = tiles * (sub + 1) / a.nsub;
+            const Scores<NT, SPILL> scores(a, tmem, at.score, warp, nwarps, turn);
+            const float* lse = at.lse + h * GP + j0 + 2 * c;
+            float l[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) l[nt][0] = lse[nt * 8], l[nt][1] = lse[nt * 8 + 1];
+            float* dst = at.scale + hg * a.TS;
+            for (int tile = tile0; tile < tile1; ++tile) {
+                float z[NT][4];
+                scores.load(tile - tile0, z);
+                scores.loaded(z);
+                float w0 = 0.f, w1 = 0.f;  // tokens t_lo and t_lo + 2
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    w0 += exp2_fast(z[nt][0] - l[nt][0]) + exp2_fast(z[nt][1] - l[nt][1]);
+                    w1 += exp2_fast(z[nt][2] - l[nt][0]) + exp2_fast(z[nt][3] - l[nt][1]);
+                }
+                w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
+                w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
+                w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
+                w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
+                if (c == 0) {
+                    dst[tile * 16 + t_lo] = w0;
+                    dst[tile * 16 + t_lo + 2] = w1;
+                }
+            }
+        }
+        __syncthreads();
+        const long long entry0 = (long long)bs * a.K;
+        float* acc = a.acc ? a.acc + (long long)__ldg(a.req + b) * a.L : nullptr;
+        for (int i = tid; i < live; i += nthreads) {
+            float w = 0.f;
+#pragma unroll 8
+            for (int j = 0; j < groups; ++j) w += at.scale[j * a.TS + i];
+            if (acc) atomicAdd(acc + at.pos[i], w);
+            if (a.weights) a.weights[entry0 + at.src[i]] = w;
+        }
+    }
+    for (int i = lo + tid; i < hi; i += nthreads) {
+        const int head = i / (D / 4), d = (i - head * (D / 4)) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r0 = 0; r0 < P; r0 += kMaxCluster / 2) {
+            if (i != lo + tid || r0 > 0) fetch_quad(i, r0);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster / 2; ++r) {
+                if (r0 + r < P) {
+                    const float f = at.factor[(r0 + r) * a.Hq + head];
+                    x = make_float4(x.x + y[r].x * f, x.y + y[r].y * f, x.z + y[r].z * f,
+                                    x.w + y[r].w * f);
+                }
+            }
+        }
+        const long long to = b * a.out_stride[0] + st * a.out_stride[1] + head * a.out_stride[2] + d;
+        uint32_t w0, w1;
+        if (a.fp16) {
+            w0 = pack_half2(x.x, x.y);
+            w1 = pack_half2(x.z, x.w);
+        } else {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x.x, x.y);
+            const __nv_bfloat162 q = __floats2bfloat162_rn(x.z, x.w);
+            w0 = *reinterpret_cast<const uint32_t*>(&p);
+            w1 = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + to;
+        if (a.vec_out) {
+            *reinterpret_cast<uint2*>(dst) = make_uint2(w0, w1);
+        } else {
+            dst[0] = (uint16_t)w0;
+            dst[1] = (uint16_t)(w0 >> 16);
+            dst[2] = (uint16_t)w1;
+            dst[3] = (uint16_t)(w1 >> 16);
+        }
+    }
+}
 
 template <int CODE, int D, int NT, bool SPILL>
-__global__ void __launch_bounds__(32 * attend_warps(SPILL), 1)
+__global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     attend_kernel(const AttendKernelArgs a) {
-    // A K row is taken in KP pieces and the V phase in VP passes over the tokens, each for a
-    // piece of d, so that the tiles in flight and the accumulators fit 128 registers.
-    constexpr int KP = D > 128 ? 2 : 1;
-    constexpr int KW = D / 16 / KP;       // words of a lane's share of a K piece = steps
-    constexpr int VP = attend_value_passes(D, NT);
-    constexpr int VD = D / VP;
-    constexpr int VW = VD / 32;           // words of a lane's share of a V piece
-    // tiles (K: pieces of tiles) in flight in registers
-    constexpr int KRING = KP > 1 || (NT == 2 && D > 64) ? 2 : 3;
-    constexpr int VRING = D > 128 || (NT == 2 && D > 64) ? 2 : 3;
+    constexpr int STEPS = D / 16;     // of a score: 16 d each
+    constexpr int COPIES = D / 32;    // 16-byte chunks of a tile per lane
+    constexpr int kHeldScales = 16;   // K and V scales of 8 heads
+    constexpr int STAGES = attend_stages(D);
+    constexpr uint32_t kTile = 16 * D;
     extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_scan[33];
+    __shared__ uint32_t s_tmem;
     cg::cluster_group cluster = cg::this_cluster();
     const int P = (int)cluster.num_blocks();
     const int rank = (int)cluster.block_rank();
@@ -228,424 +509,384 @@ __global__ void __launch_bounds__(32 * attend_warps(SPILL), 1)
     const int g = lane >> 2, c = lane & 3;
     const int GP = a.ngroups * 8 * NT;    // padded query heads of a K/V head
     const int HP = a.Hkv * GP;
+    const Layout<SPILL> at(a, smem, P, HP, D, nwarps, blockIdx.x);
+    int *const t_loc = at.loc, *const t_pos = at.pos, *const t_src = at.src;
+    float* const t_scale = at.scale;
 
-    // Shared memory: maxima and sums [nsub][HP], factors [P][Hq], the query's log2-sum-exp
-    // [Hq], output partials [Hq][D]; then (or in the workspace) the per-token arrays.
-    __shared__ int s_scan[33];
-    float* s_max = reinterpret_cast<float*>(smem);
-    float* s_sum = s_max + a.nsub * HP;
-    float* s_factor = s_sum + a.nsub * HP;
-    float* s_lse = s_factor + ((P * a.Hq + 3) & ~3);
-    float* s_out = s_lse + ((a.Hq + 3) & ~3);
-    const int out_floats = a.alias ? max(a.Hq * D, 2 * a.Hkv * a.TC) : a.Hq * D;
-    uint8_t* token = SPILL ? a.spill + (size_t)blockIdx.x * a.token_bytes
-                           : reinterpret_cast<uint8_t*>(s_out + out_floats);
-    int* t_loc = reinterpret_cast<int*>(token);  // [TS] row, -1 past the last
-    int* t_pos = t_loc + a.TS;                   // [TS] position in the sequence
-    int* t_src = t_pos + a.TS;                   // [TS] entry of the selection
-    float* t_score = reinterpret_cast<float*>(t_src + a.TS);           // [Hq][TL], base-2 logits
-    float* t_scale = !SPILL && a.alias ? s_out : t_score + a.Hq * a.TL;  // [2 Hkv][TC]
+    if (!SPILL && warp == 0) {
+        // Never waits: the CTA's shared memory is at least its share of the columns, so that the
+        // CTAs of these kernels that an SM holds have columns for all.
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         shared_address(&s_tmem)),
+                     "r"(a.cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+
+    const int groups = a.Hkv * a.ngroups;
+    const int ntasks = groups * a.nsub;
+    // Queries as the B operand: lane (g, c) holds elements 16 w + 4 c .. + 3 of head g.
+    uint32_t qf[NT][STEPS][2];
+    float factor[NT][2];  // of the scores of heads 2 c and 2 c + 1
+    auto load_q = [&](int task) {
+        const int hg = task % groups, h = hg / a.ngroups, j0 = (hg - h * a.ngroups) * 8 * NT;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int j = j0 + nt * 8 + g;
+            const long long from = b * a.q_stride[0] + st * a.q_stride[1] +
+                                   (long long)(h * a.G + j) * a.q_stride[2];
+            uint32_t raw[2 * STEPS];
+            load_query<STEPS>(raw, static_cast<const uint16_t*>(a.q) + from, c, j < a.G, a.vec_q);
+            float peak = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2 * STEPS; ++i) {
+                const float2 x = pair(raw[i], a.fp16);
+                peak = fmaxf(peak, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+            peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+            peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
+            // the head's largest element goes to [2^14, 2^15), f16's top
+            int e = (int)(__float_as_uint(peak) >> 23) - 127;
+            e = e < -100 ? -100 : e;
+            const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < 2 * STEPS; ++i) {
+                const float2 x = pair(raw[i], a.fp16);
+                qf[nt][i >> 1][i & 1] = pack_half2(x.x * up, x.y * up);
+            }
+            const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
+            factor[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+            factor[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+        }
+    };
 
     const long long entry0 = (long long)bs * a.K;
-    const int req = __ldg(a.req + b);
-    const bool known = req >= 0 && req < a.R;
-    // The CTA's entries, masked ones dropped.
-    int live = 0;
-    for (int i0 = 0; i0 < a.TS; i0 += nthreads) {
-        const int i = i0 + tid;
+    // The first turn's entries are under way while the queries come.
+    int loc = -1, t = 0;
+    auto load_entry = [&](int i) {
         const int j = ((i >> 4) * P + rank) * 16 + (i & 15);
-        int loc = -1, t = 0;
-        if (i < a.TS && j < a.K) {
+        loc = -1, t = 0;
+        if (j < a.K) {
             loc = __ldg(a.locs + entry0 + j);
             t = __ldg(a.topk + entry0 + j);
-            if (!known || loc < 0 || loc >= a.num_rows || t < 0 || t >= a.L) {
-                loc = -1;
-                if (a.weights) a.weights[entry0 + j] = 0.f;
+        }
+    };
+    load_entry(tid);
+    const int req = __ldg(a.req + b);
+    if (warp < ntasks) load_q(warp);
+    const bool known = req >= 0 && req < a.R;
+    // The CTA's entries, masked ones dropped.  A thread fetches the scales of its entry as soon
+    // as it has the position, kHeldScales of them into registers.
+    const int chunks = (a.K + 15) >> 4, own = (chunks - rank + P - 1) / P;
+    const int entries = own * 16 - (own > 0 && (chunks - 1) % P == rank ? chunks * 16 - a.K : 0);
+    const int per = 2 * a.Hkv;
+    const float* scales = a.scales + (long long)(known ? req : 0) * a.NB * per;
+    float x[kHeldScales];
+    int live = 0, at_last = -1;
+    auto fetch_scales = [&](int pos, int ch) {
+        const float* src = scales + (long long)(pos / a.T) * per + ch;
+#pragma unroll
+        for (int k = 0; k < kHeldScales; k += 4) {
+            if (ch + k >= per) break;
+            if (a.vec_scale) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(src + k));
+                x[k] = v.x, x[k + 1] = v.y, x[k + 2] = v.z, x[k + 3] = v.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[k + i] = ch + k + i < per ? __ldg(src + k + i) : 0.f;
             }
         }
-        int n = __syncthreads_count(loc >= 0);
-        int at = live + tid;  // a full turn, or one that only lacks its end, stays in place
-        if (__syncthreads_or(loc >= 0 && tid >= n)) {
-            at = live + block_exclusive_scan(loc >= 0, s_scan, &n);
+    };
+    auto put_scales = [&](int to, int ch) {
+#pragma unroll
+        for (int k = 0; k < kHeldScales; ++k)
+            if (ch + k < per) t_scale[(ch + k) * a.TC + to] = x[k];
+    };
+    for (int i0 = 0; i0 < entries; i0 += nthreads) {
+        const int i = i0 + tid;
+        const int j = ((i >> 4) * P + rank) * 16 + (i & 15);
+        if (i0 > 0) load_entry(i);
+        if (i >= entries) {
+            loc = -1;
+        } else if (!known || loc < 0 || loc >= a.num_rows || t < 0 || t >= a.L) {
+            loc = -1;
+            if (a.weights) a.weights[entry0 + j] = 0.f;
         }
+        if (at_last >= 0) put_scales(at_last, 0);
+        if (loc >= 0) fetch_scales(t, 0);
+        int n = __syncthreads_count(loc >= 0);
+        at_last = live + tid;  // in place while no entry is masked
+        if (n != min(nthreads, entries - i0))
+            at_last = live + block_exclusive_scan(loc >= 0, s_scan, &n);
         if (loc >= 0) {
-            t_loc[at] = loc;
-            t_pos[at] = t;
-            t_src[at] = j;
+            t_loc[at_last] = loc;
+            t_pos[at_last] = t;
+            t_src[at_last] = j;
+        } else {
+            at_last = -1;
         }
         live += n;
     }
     const int tiles = (live + 15) >> 4;
-    for (int i = live + tid; i < tiles * 16; i += nthreads) t_loc[i] = -1;
     __syncthreads();
-    {
-        const int per = 2 * a.Hkv;
-        const float* base = a.scales + (long long)(known ? req : 0) * a.NB * per;
-        for (int i = tid; i < tiles * 16 * per; i += nthreads) {
-            const int tok = i / per, ch = i - tok * per;
-            t_scale[ch * a.TC + tok] =
-                tok < live ? __ldg(base + (long long)(t_pos[tok] / a.T) * per + ch) : 0.f;
+    // The places up to a whole tile repeat a live row: their scores are masked and their
+    // weights zero.
+    for (int i = live + tid; i < tiles * 16; i += nthreads) {
+        t_loc[i] = t_loc[live - 1];
+        t_pos[i] = t_pos[live - 1];
+        for (int ch = 0; ch < per; ++ch) t_scale[ch * a.TC + i] = 0.f;
+    }
+    if (!SPILL) asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    __syncthreads();
+    const uint32_t tmem = SPILL ? 0u : s_tmem;
+
+    // The warp's queue: item i of a task is the K rows of its tile i, then the V rows of its
+    // tile i - n.
+    const uint32_t queue = shared_address(at.queue) + warp * STAGES * kTile;
+    auto copy_item = [&](int i, int stage, int h, int tile0, int n) {
+        if (i < 2 * n) {
+            const bool v = i >= n;
+            const uint8_t* p = a.rows + (v ? a.Hkv + h : h) * D;
+            const int* l = t_loc + (tile0 + (v ? i - n : i)) * 16;
+            const uint32_t tile = queue + stage * kTile;
+            int from = lane;
+            if (D * NT > 192) asm volatile("" : "+r"(from));  // offsets computed here, not kept
+#pragma unroll
+            for (int k = 0; k < COPIES; ++k) {
+                const int row = (k * 32 + from) / (D / 16), chunk = (k * 32 + from) % (D / 16);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 tile + chunk_at<D>(row, chunk)),
+                             "l"(p + (long long)l[row] * a.W + chunk * 16)
+                             : "memory");
+            }
+        }
+        commit_copies();  // of nothing past the last item, so that the count stays even
+    };
+    auto first_items = [&](int task) {
+        const int sub = task / groups, h = (task - sub * groups) / a.ngroups;
+        const int tile0 = tiles * sub / a.nsub, n = tiles * (sub + 1) / a.nsub - tile0;
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) copy_item(i, i, h, tile0, n);
+    };
+    if (warp < ntasks) first_items(warp);  // under way while the scales come
+
+    if (at_last >= 0) put_scales(at_last, 0);
+    if (per > kHeldScales) {  // the others of many heads
+        for (int i = tid; i < live; i += nthreads) {
+            for (int ch = kHeldScales; ch < per; ch += kHeldScales) {
+                fetch_scales(t_pos[i], ch);
+                put_scales(i, ch);
+            }
         }
     }
     __syncthreads();
 
-    const int groups = a.Hkv * a.ngroups;
-    for (int task = warp; task < groups * a.nsub; task += nwarps) {
+    for (int task = warp, turn = 0; task < ntasks; task += nwarps, ++turn) {
         const int sub = task / groups, hg = task - sub * groups;
         const int h = hg / a.ngroups, j0 = (hg - h * a.ngroups) * 8 * NT;
-        const int tile0 = tiles * sub / a.nsub, tile1 = tiles * (sub + 1) / a.nsub;
-        const float* sk = t_scale + h * a.TC;
-        const float* sv = t_scale + (a.Hkv + h) * a.TC;
-        float* score = t_score + (h * a.G + j0) * a.TL;
+        const int tile0 = tiles * sub / a.nsub, n = tiles * (sub + 1) / a.nsub - tile0;
+        const float* sk = t_scale + h * a.TC + tile0 * 16;
+        const float* sv = t_scale + (a.Hkv + h) * a.TC + tile0 * 16;
+        const Scores<NT, SPILL> scores(a, tmem, at.score, warp, nwarps, turn);
+        if (turn > 0) {
+            load_q(task);
+            first_items(task);
+        }
+        int stage = 0;  // of the item in use
+        // Item i is in shared memory for the whole warp, and the item before used up: its stage
+        // takes the next copy.
+        auto next_item = [&](int i) {
+            wait_copies<STAGES - 2>();
+            __syncwarp();
+            copy_item(i + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1, h, tile0, n);
+            const uint32_t tile = queue + stage * kTile;
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            return tile;
+        };
+        // Tokens of a tile in this lane's score fragments: t_lo and t_lo + 2.
+        const int t_lo = 4 * (g >> 1) + (g & 1);
+        // This lane's row in the matrices of a K tile (its chunk is lane / 16) and of a V tile.
+        const int k_row = 4 * ((lane & 7) >> 1) + (lane & 1) + 2 * (lane >> 3 & 1);
+        const int v_row = lane & 15;
 
         // ---- scores --------------------------------------------------------------
-        float top[NT][2];
+        float top[NT][2];  // of heads 2 c and 2 c + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
-        {
-            const uint8_t* kbase = a.rows + h * D + word_at<KW, 4>(0, c);
-            uint32_t kr[KRING][2][KW];
-            // piece u: part u % KP of tile u / KP
-            auto load_k = [&](uint32_t (&r)[2][KW], int u) {
-                const int tile = tile0 + u / KP;
+        for (int i = 0; i < n; ++i) {
+            const uint32_t tile = next_item(i);
+            float s[NT][2][4] = {};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int loc = tile < tile1 ? t_loc[tile * 16 + g + 8 * i] : -1;
-                    load_share<KW, 4>(r[i], kbase + (u % KP) * (D / KP) + (long long)loc * a.W,
-                                      loc >= 0);
+            for (int w = 0; w < STEPS; w += 2) {
+                uint32_t r[4];  // rows t_lo, t_lo + 2 of chunk w, then of chunk w + 1
+                read_matrices(r, tile + chunk_at<D>(k_row, w + (lane >> 4)));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t a0, a1, a2, a3;
+                    halves<CODE>(r[2 * k], a0, a2);
+                    halves<CODE>(r[2 * k + 1], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma(s[nt][k], a0, a1, a2, a3, qf[nt][w + k][0], qf[nt][w + k][1]);
                 }
-            };
-            if constexpr (KP == 1) {
-#pragma unroll
-                for (int i = 0; i < KRING; ++i) load_k(kr[i], i);
             }
-
-            // Queries as the B operand: lane (g, c) holds head g's elements of its words.
-            uint32_t qf[NT][KP][KW][2];
-            float factor[NT][2];  // of the scores of heads 2 c and 2 c + 1
+            const int t0 = i * 16 + t_lo;
+            const bool on0 = tile0 * 16 + t0 < live, on1 = tile0 * 16 + t0 + 2 < live;
+            const float k0 = sk[t0], k1 = sk[t0 + 2];
+            float z[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int j = j0 + nt * 8 + g;
-                const long long at = b * a.q_stride[0] + st * a.q_stride[1] +
-                                     (long long)(h * a.G + j) * a.q_stride[2];
-                float peak = 0.f;
 #pragma unroll
-                for (int p = 0; p < KP; ++p) {
-                    uint32_t raw[2 * KW];
-                    load_query<KW>(raw, static_cast<const uint16_t*>(a.q) + at + p * (D / KP), c,
-                                   j < a.G, a.vec_q);
-#pragma unroll
-                    for (int w = 0; w < KW; ++w) {
-                        qf[nt][p][w][0] = raw[2 * w];
-                        qf[nt][p][w][1] = raw[2 * w + 1];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float2 x = pair(raw[2 * w + i], a.fp16);
-                            peak = fmaxf(peak, fmaxf(fabsf(x.x), fabsf(x.y)));
-                        }
-                    }
-                }
-                peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
-                peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
-                // the head's largest element goes to [2^14, 2^15), f16's top
-                int e = (int)(__float_as_uint(peak) >> 23) - 127;
-                e = e < -100 ? -100 : e;
-                const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-#pragma unroll
-                for (int p = 0; p < KP; ++p) {
-#pragma unroll
-                    for (int w = 0; w < KW; ++w) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float2 x = pair(qf[nt][p][w][i], a.fp16);
-                            qf[nt][p][w][i] = pack_half2(x.x * up, x.y * up);
-                        }
-                    }
-                }
-                const float down =
-                    __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
-                factor[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
-                factor[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
-            }
-
-            if constexpr (KP > 1) {  // no registers for them before
-#pragma unroll
-                for (int i = 0; i < KRING; ++i) load_k(kr[i], i);
-            }
-
-            const int pieces = (tile1 - tile0) * KP;
-            float s[NT][2][4];
-            for (int u = 0; u < pieces; u += KRING) {
-#pragma unroll
-                for (int i = 0; i < KRING; ++i) {
-                    if (u + i >= pieces) break;
-                    const int part = i % KP;
-                    if (part == 0) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) s[nt][0][k] = s[nt][1][k] = 0.f;
-                    }
-#pragma unroll
-                    for (int w = 0; w < KW; ++w) {
-                        uint32_t a0, a1, a2, a3;
-                        halves<CODE>(kr[i][0][w], a0, a2);
-                        halves<CODE>(kr[i][1][w], a1, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma(s[nt][w & 1], a0, a1, a2, a3, qf[nt][part][w][0],
-                                qf[nt][part][w][1]);
-                    }
-                    load_k(kr[i], u + i + KRING);
-                    if (part != KP - 1) continue;
-                    const int t0 = (tile0 + (u + i) / KP) * 16 + g;
-                    const bool on0 = t0 < live, on1 = t0 + 8 < live;
-                    const float k0 = sk[t0], k1 = sk[t0 + 8];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float f = factor[nt][k];
-                            const float v0 =
-                                on0 ? (s[nt][0][k] + s[nt][1][k]) * (k0 * f) : -INFINITY;
-                            const float v1 =
-                                on1 ? (s[nt][0][k + 2] + s[nt][1][k + 2]) * (k1 * f) : -INFINITY;
-                            top[nt][k] = fmaxf(top[nt][k], fmaxf(v0, v1));
-                            const int j = nt * 8 + 2 * c + k;
-                            if (j0 + j < a.G) {
-                                score[j * a.TL + t0] = v0;
-                                score[j * a.TL + t0 + 8] = v1;
-                            }
-                        }
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    const float f = factor[nt][k];
+                    z[nt][k] = on0 ? (s[nt][0][k] + s[nt][1][k]) * (k0 * f) : -INFINITY;
+                    z[nt][k + 2] =
+                        on1 ? (s[nt][0][k + 2] + s[nt][1][k + 2]) * (k1 * f) : -INFINITY;
+                    top[nt][k] = fmaxf(top[nt][k], fmaxf(z[nt][k], z[nt][k + 2]));
                 }
             }
+            scores.store(i, z);
         }
 
-        // ---- values --------------------------------------------------------------
-        const uint8_t* vbase = a.rows + (a.Hkv + h) * D + word_at<VW, 8>(0, g);
-        uint32_t vr[VRING][4][VW];
-        auto load_v = [&](uint32_t (&r)[4][VW], int tile, int part) {
-            int4 loc = make_int4(-1, -1, -1, -1);
-            if (tile < tile1) loc = *reinterpret_cast<const int4*>(t_loc + tile * 16 + 4 * c);
-            const uint8_t* p = vbase + part * VD;
-            load_share<VW, 8>(r[0], p + (long long)loc.x * a.W, loc.x >= 0);
-            load_share<VW, 8>(r[1], p + (long long)loc.y * a.W, loc.y >= 0);
-            load_share<VW, 8>(r[2], p + (long long)loc.z * a.W, loc.z >= 0);
-            load_share<VW, 8>(r[3], p + (long long)loc.w * a.W, loc.w >= 0);
-        };
+        // The queries are used up; without this the compiler keeps them for the next turn, which
+        // loads its own.
 #pragma unroll
-        for (int i = 0; i < VRING; ++i) load_v(vr[i], tile0 + i, 0);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int w = 0; w < STEPS; ++w) asm("" : "=r"(qf[nt][w][0]), "=r"(qf[nt][w][1]));
 
-        float head_max[NT], head_sum[NT];  // of head g of each 8-head tile
+        // ---- softmax over the task's tokens ----------------------------------------
+        scores.stored();
+        float safe[NT][2], sum[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float m0 = max_over_g(top[nt][0]), m1 = max_over_g(top[nt][1]);
-            // head g's maximum lies with lanes c = g / 2
-            const float from0 = __shfl_sync(0xffffffffu, m0, g >> 1);
-            const float from1 = __shfl_sync(0xffffffffu, m1, g >> 1);
-            head_max[nt] = g & 1 ? from1 : from0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                top[nt][k] = max_over_g(top[nt][k]);
+                if (g == 0) at.max[sub * HP + h * GP + j0 + nt * 8 + 2 * c + k] = top[nt][k];
+                safe[nt][k] = top[nt][k] == -INFINITY ? 0.f : top[nt][k];
+                sum[nt][k] = 0.f;
+            }
         }
         float ref = 0.f;  // largest V scale of the task's tokens
-        for (int i = tile0 * 16 + lane; i < tile1 * 16; i += 32) ref = fmaxf(ref, sv[i]);
+        for (int i = lane; i < n * 16; i += 32) ref = fmaxf(ref, sv[i]);
         ref = max_over_g(ref);
         ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, 1));
         ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, 2));
         const float inv = ref > 0.f ? 1.f / ref : 0.f;
-        __syncwarp();  // the warp's scores are in shared memory
 
-        float fold[NT][2];  // of the partial outputs of heads 2 c and 2 c + 1
+        // ---- values --------------------------------------------------------------
+        float o[STEPS][NT][4] = {};
+        for (int i = 0; i < n; ++i) {
+            float z[NT][4];
+            scores.load(i, z);
+            const float v0 = sv[i * 16 + t_lo] * inv, v1 = sv[i * 16 + t_lo + 2] * inv;
+            const uint32_t tile = next_item(n + i);
+            scores.loaded(z);
+            uint32_t pf[NT][2];
 #pragma unroll
-        for (int part = 0; part < VP; ++part) {
-            float o[2 * VW][NT][4] = {};
+            for (int nt = 0; nt < NT; ++nt) {
+                const float p0 = exp2_fast(z[nt][0] - safe[nt][0]);
+                const float p1 = exp2_fast(z[nt][1] - safe[nt][1]);
+                const float p2 = exp2_fast(z[nt][2] - safe[nt][0]);
+                const float p3 = exp2_fast(z[nt][3] - safe[nt][1]);
+                sum[nt][0] += p0 + p2;
+                sum[nt][1] += p1 + p3;
+                pf[nt][0] = transpose(pack_half2(p0 * v0, p1 * v0));
+                pf[nt][1] = transpose(pack_half2(p2 * v1, p3 * v1));
+            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) head_sum[nt] = 0.f;
-            for (int tile = tile0; tile < tile1; tile += VRING) {
+            for (int w = 0; w < STEPS; w += 2) {
+                uint32_t r[4];  // d = g, g + 8 of chunk w, then of chunk w + 1; four tokens each
+                read_transposed(r, tile + chunk_at<D>(v_row, w + (lane >> 4)));
 #pragma unroll
-                for (int i = 0; i < VRING; ++i) {
-                    if (tile + i >= tile1) break;
-                    const int t0 = (tile + i) * 16 + 4 * c;
-                    const float4 scale = *reinterpret_cast<const float4*>(sv + t0);
-                    uint32_t pf[NT][2];
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t a0, a1, a2, a3;
+                    halves<CODE>(r[2 * k], a0, a2);
+                    halves<CODE>(r[2 * k + 1], a1, a3);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (j0 + nt * 8 + g < a.G)
-                            z = *reinterpret_cast<const float4*>(score + (nt * 8 + g) * a.TL + t0);
-                        const float m = head_max[nt] == -INFINITY ? 0.f : head_max[nt];
-                        const float p0 = exp2_fast(z.x - m), p1 = exp2_fast(z.y - m);
-                        const float p2 = exp2_fast(z.z - m), p3 = exp2_fast(z.w - m);
-                        head_sum[nt] += (p0 + p1) + (p2 + p3);
-                        pf[nt][0] = pack_half2(p0 * (scale.x * inv), p1 * (scale.y * inv));
-                        pf[nt][1] = pack_half2(p2 * (scale.z * inv), p3 * (scale.w * inv));
-                    }
-#pragma unroll
-                    for (int w = 0; w < VW; ++w) {
-                        // bytes of neighbouring tokens side by side: d, d + 1 | d + 2, d + 3
-                        const uint32_t x0 = __byte_perm(vr[i][0][w], vr[i][1][w], 0x5140);
-                        const uint32_t y0 = __byte_perm(vr[i][0][w], vr[i][1][w], 0x7362);
-                        const uint32_t x1 = __byte_perm(vr[i][2][w], vr[i][3][w], 0x5140);
-                        const uint32_t y1 = __byte_perm(vr[i][2][w], vr[i][3][w], 0x7362);
-                        uint32_t a0, a1, a2, a3;
-                        halves<CODE>(x0, a0, a1);
-                        halves<CODE>(x1, a2, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma(o[2 * w][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                        halves<CODE>(y0, a0, a1);
-                        halves<CODE>(y1, a2, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma(o[2 * w + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                    }
-                    load_v(vr[i], tile + i + VRING, part);
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma(o[w + k][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
                 }
             }
-            if (part + 1 < VP) {
+        }
+        int ranks = P;  // the layout anew, so that it takes no registers through the loops
+        asm("" : "+r"(ranks));
+        const Layout<SPILL> done(a, smem, ranks, HP, D, nwarps, blockIdx.x);
 #pragma unroll
-                for (int i = 0; i < VRING; ++i) load_v(vr[i], tile0 + i, part + 1);
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                sum[nt][k] = sum_over_g(sum[nt][k]);
+                if (g == 0)
+                    done.sum[sub * HP + h * GP + j0 + nt * 8 + 2 * c + k] = sum[nt][k];
             }
-            if (part == 0) {
+        }
+        // The outputs may take the queues' place: then every warp has one task, and all are done
+        // with their queues here.  Several parts of a slice have one task a warp too; their
+        // outputs are added in order, relative to their common maximum.
+        if (a.alias || a.nsub > 1) __syncthreads();
+        float fold[NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float x = head_sum[nt];
-                    x += __shfl_xor_sync(0xffffffffu, x, 1);
-                    x += __shfl_xor_sync(0xffffffffu, x, 2);
-                    if (c == 0) {
-                        const int at = sub * HP + h * GP + j0 + nt * 8 + g;
-                        s_max[at] = head_max[nt];
-                        s_sum[at] = x;
-                    }
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                fold[nt][k] = ref;
+                if (a.nsub > 1) {
+                    const int to = h * GP + j0 + nt * 8 + 2 * c + k;
+                    float m = -INFINITY;
+                    for (int u = 0; u < a.nsub; ++u) m = fmaxf(m, done.max[u * HP + to]);
+                    fold[nt][k] *=
+                        exp2_fast(done.max[sub * HP + to] - (m == -INFINITY ? 0.f : m));
                 }
             }
-            // The output may take the scales' place: then every warp has one task and VP is 1,
-            // and all are done with the scales here.  Several parts of a slice have one task a
-            // warp too; their outputs are added in order, relative to their common maximum.
-            if (a.alias || a.nsub > 1) __syncthreads();
-            if (part == 0) {
+        }
+        for (int u = 0; u < a.nsub; ++u) {
+            if (u == sub) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        fold[nt][k] = ref;
-                        if (a.nsub > 1) {
-                            const int at = h * GP + j0 + nt * 8 + 2 * c + k;
-                            float m = -INFINITY;
-                            for (int u = 0; u < a.nsub; ++u) m = fmaxf(m, s_max[u * HP + at]);
-                            fold[nt][k] *=
-                                exp2_fast(s_max[sub * HP + at] - (m == -INFINITY ? 0.f : m));
+                        const int j = j0 + nt * 8 + 2 * c + k;
+                        if (j >= a.G) continue;
+                        const float f = fold[nt][k];
+                        float* row = done.out + (h * a.G + j) * (D + 4) + g;
+#pragma unroll
+                        for (int w = 0; w < STEPS; ++w) {
+                            const float y0 = o[w][nt][k] * f, y1 = o[w][nt][k + 2] * f;
+                            row[16 * w] = u > 0 ? row[16 * w] + y0 : y0;
+                            row[16 * w + 8] = u > 0 ? row[16 * w + 8] + y1 : y1;
                         }
                     }
                 }
             }
-            for (int u = 0; u < a.nsub; ++u) {
-                if (u == sub) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int j = j0 + nt * 8 + 2 * c + k;
-                            if (j >= a.G) continue;
-                            const float f = fold[nt][k];
-                            float* row = s_out + (h * a.G + j) * D + part * VD;
-#pragma unroll
-                            for (int w = 0; w < VW; ++w) {
-                                float4* dst =
-                                    reinterpret_cast<float4*>(row + word_at<VW, 8>(w, g));
-                                float4 x =
-                                    make_float4(o[2 * w][nt][k] * f, o[2 * w][nt][k + 2] * f,
-                                                o[2 * w + 1][nt][k] * f,
-                                                o[2 * w + 1][nt][k + 2] * f);
-                                if (u > 0) {
-                                    const float4 y = *dst;
-                                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-                                }
-                                *dst = x;
-                            }
-                        }
-                    }
-                }
-                if (a.nsub > 1) __syncthreads();
-            }
+            if (a.nsub > 1) __syncthreads();
         }
     }
     if (a.nsub > 1) {  // one maximum and sum per head of the slice
         for (int i = tid; i < HP; i += nthreads) {
             float m = -INFINITY, l = 0.f;
-            for (int u = 0; u < a.nsub; ++u) m = fmaxf(m, s_max[u * HP + i]);
+            for (int u = 0; u < a.nsub; ++u) m = fmaxf(m, at.max[u * HP + i]);
             const float safe = m == -INFINITY ? 0.f : m;
             for (int u = 0; u < a.nsub; ++u)
-                l += s_sum[u * HP + i] * exp2_fast(s_max[u * HP + i] - safe);
-            s_max[i] = m;
-            s_sum[i] = l;
+                l += at.sum[u * HP + i] * exp2_fast(at.max[u * HP + i] - safe);
+            at.max[i] = m;
+            at.sum[i] = l;
         }
     }
 
     // ---- the cluster's result ----------------------------------------------------
     cluster.sync();
-    for (int i = tid; i < a.Hq; i += nthreads) {
-        const int at = (i / a.G) * GP + i % a.G;
-        float m = -INFINITY, l = 0.f;
-        for (int r = 0; r < P; ++r) m = fmaxf(m, cluster.map_shared_rank(s_max, r)[at]);
-        const float safe = m == -INFINITY ? 0.f : m;
-        for (int r = 0; r < P; ++r) {
-            const float f = exp2_fast(cluster.map_shared_rank(s_max, r)[at] - safe);
-            s_factor[r * a.Hq + i] = f;
-            l += cluster.map_shared_rank(s_sum, r)[at] * f;
-        }
-        const float norm = l == 0.f ? 0.f : 1.f / l;
-        for (int r = 0; r < P; ++r) s_factor[r * a.Hq + i] *= norm;
-        const float lse2 = m + log2f(l);
-        s_lse[i] = l == 0.f ? INFINITY : lse2;  // weights of an empty query: 0
-        if (rank == 0 && a.lse)
-            a.lse[(long long)bs * a.Hq + i] = l == 0.f ? -INFINITY : lse2 * 0.69314718056f;
-    }
-    __syncthreads();
-    {
-        const int quads = a.Hq * (D / 4);
-        const int lo = quads * rank / P, hi = quads * (rank + 1) / P;
-        for (int i = lo + tid; i < hi; i += nthreads) {
-            const int head = i / (D / 4), d = (i - head * (D / 4)) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < P; ++r) {
-                const float4 y =
-                    reinterpret_cast<const float4*>(cluster.map_shared_rank(s_out, r))[i];
-                const float f = s_factor[r * a.Hq + head];
-                x = make_float4(x.x + y.x * f, x.y + y.y * f, x.z + y.z * f, x.w + y.w * f);
-            }
-            const long long at = b * a.out_stride[0] + st * a.out_stride[1] +
-                                 head * a.out_stride[2] + d;
-            uint32_t w0, w1;
-            if (a.fp16) {
-                w0 = pack_half2(x.x, x.y);
-                w1 = pack_half2(x.z, x.w);
-            } else {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(x.x, x.y);
-                const __nv_bfloat162 q = __floats2bfloat162_rn(x.z, x.w);
-                w0 = *reinterpret_cast<const uint32_t*>(&p);
-                w1 = *reinterpret_cast<const uint32_t*>(&q);
-            }
-            uint16_t* dst = static_cast<uint16_t*>(a.out) + at;
-            if (a.vec_out) {
-                *reinterpret_cast<uint2*>(dst) = make_uint2(w0, w1);
-            } else {
-                dst[0] = (uint16_t)w0;
-                dst[1] = (uint16_t)(w0 >> 16);
-                dst[2] = (uint16_t)w1;
-                dst[3] = (uint16_t)(w1 >> 16);
-            }
-        }
-    }
-    if (a.weights || a.acc) {
-        for (int i = tid; i < live; i += nthreads) {
-            float w = 0.f;
-#pragma unroll 4
-            for (int j = 0; j < a.Hq; ++j) w += exp2_fast(t_score[j * a.TL + i] - s_lse[j]);
-            if (a.acc) atomicAdd(a.acc + (long long)req * a.L + t_pos[i], w);
-            if (a.weights) a.weights[entry0 + t_src[i]] = w;
-        }
-    }
+    finish<D, NT, SPILL>(a, smem, HP, GP, live, tmem);
+    if (!SPILL) asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     cluster.sync();  // no CTA leaves while another reads its shared memory
+    if (!SPILL && warp == 0) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(a.cols));
+    }
 }
 
 template <int CODE, int D, int NT, bool SPILL>
