@@ -359,6 +359,8 @@ __device__ __forceinline__ void finish(const AttendKernelArgs& a, uint8_t* smem,
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(P));
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(block));
+    // hs_accumulate's kernel may take the SMs that become free.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, nthreads = blockDim.x;
     const Layout<SPILL> at(a, smem, P, HP, D, nthreads >> 5, block);
     const int bs = block / P, b = bs / a.S, st = bs - b * a.S;

@@ -2,14 +2,14 @@
 // to the sums of each request, and choosing the tokens that a request keeps.
 //
 // Choosing is a selection of the k largest of n weights, not a sort: weights
-// map to unsigned keys that order like them, three passes over the keys (11,
-// 11 and 10 bits, most significant first) find the k-th largest key by
-// counting, and one ordered pass writes the positions above it plus the first
-// ties.  One thread-block cluster serves a request: each CTA counts its
-// segment into its own shared memory, the counts are added over distributed
-// shared memory, and the passes re-read the weights from L2 (4 bytes a token).
-// The kernel is bound by the latency of its passes and barriers, not by the
-// 4 * n bytes it reads.
+// map to unsigned keys that order like them, three counts over the keys (by 11,
+// 11 and 10 bits, most significant first) find the k-th largest key, and one
+// ordered pass writes the positions above it plus the first ties.  A CTA
+// counts into its shared memory; for long sequences a thread-block cluster
+// serves a request and its CTAs read each other's counts over distributed
+// shared memory.  A thread keeps its keys in registers from the first pass
+// on (sequences up to 131072), so the weights are read once.  The kernel is
+// bound by the latency of its passes and barriers, not by the 4 * n bytes.
 #include <cooperative_groups.h>
 
 #include "hs_kv.cuh"
@@ -20,9 +20,13 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kMaxEvictCluster = 8;
+constexpr int kAhead = 4;                        // remote counts read at a time
 constexpr int kBins = 2048;
-constexpr int kPer = 4;  // consecutive positions of a thread in the ordered pass
+constexpr int kOwnBins = kBins / kEvictThreads;  // bins a thread looks through
+constexpr int kChunk = 128;                      // positions a warp takes at a time, 4 a lane
+constexpr int kMaxChunks = 8;                    // a warp holds in registers
 
 // Key of a weight: larger weights have larger keys, NaN the smallest, the two
 // zeros the same.
@@ -42,17 +46,17 @@ struct EvictArgs {
     float* kept_acc;
 };
 
+// CH: chunks of a warp's segment that are held in registers; 0: read anew in every pass.
+template <int CH>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a) {
-    __shared__ int s_hist[kBins];   // this CTA's counts
-    __shared__ int s_sum[kBins];    // the cluster's counts of this CTA's share of the bins
+    __shared__ __align__(16) int s_hist[3][kBins];  // this CTA's counts, pass by pass
     __shared__ int s_tmp[33];
     __shared__ int s_pick[2];       // the chosen bin, and how many are wanted from it
-    __shared__ int s_above, s_equal;
     cg::cluster_group cluster = cg::this_cluster();
     const int P = (int)cluster.num_blocks();
     const int rank = (int)cluster.block_rank();
     const int b = blockIdx.x / P;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int q = __ldg(a.req + b);
     int n = __ldg(a.seq_lens + b);
     n = q < 0 || q >= a.R || n < 0 ? 0 : min(n, a.L);
@@ -75,138 +79,211 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
     }
     const int m = n - a.recent;           // candidates
     const int k = a.budget - a.recent;    // to keep of them, k < m
+    if (k > 0) {
+        // The warp's segment, in chunks of 128 positions, 4 consecutive ones a lane.
+        const int chunks = ((m + kChunk - 1) / kChunk + P * kEvictWarps - 1) / (P * kEvictWarps);
+        const long long lo = (long long)(rank * kEvictWarps + warp) * chunks * kChunk;
+        float x[CH > 0 ? CH : 1][4];
+        auto fetch = [&](int c, float (&v)[4]) {
+            const long long t = lo + c * kChunk + lane * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = t + i < m ? __ldg(acc + t + i) : 0.f;
+        };
+        // Calls f(chunk, its 4 weights) for the warp's chunks in order.
+        auto each = [&](auto f) {
+            if constexpr (CH > 0) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    if (c < chunks) f(c, x[c]);
+            } else {
+                for (int c = 0; c < chunks; ++c) {
+                    fetch(c, x[0]);
+                    f(c, x[0]);
+                }
+            }
+        };
+        if constexpr (CH > 0) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (c < chunks) fetch(c, x[c]);
+        }
+        for (int i = tid; i < 3 * kBins; i += kEvictThreads) (&s_hist[0][0])[i] = 0;
+        __syncthreads();
+
+        // The k-th largest key digit by digit.
+        uint32_t edge = 0;   // the digits found so far; at the end, the key
+        int want = k;        // how many of the keys with those digits are kept
+        int out = 0, ties = 0;  // kept, and equal to the edge, before this CTA's positions
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+            const int bins = pass == 2 ? 1024 : 2048;
+            int* hist = s_hist[pass];
+            each([&](int c, const float (&v)[4]) {
+                const long long t = lo + c * kChunk + lane * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t key = key_of(v[i]);
+                    if (t + i < m && (pass == 0 || key >> (pass == 1 ? 21 : 10) == edge))
+                        atomicAdd(&hist[key >> shift & (bins - 1)], 1);
+                }
+            });
+            cluster.sync();
+            // A thread's bins, counted from the top, over the cluster and before this CTA.
+            const int top = kBins - (tid + 1) * kOwnBins;
+            int mine[kOwnBins], before[kOwnBins];
+#pragma unroll
+            for (int i = 0; i < kOwnBins; ++i) mine[i] = before[i] = 0;
+#pragma unroll 1
+            for (int r0 = 0; r0 < P; r0 += kAhead) {
+                int4 h[kAhead];  // on their way together: a remote load takes long
+#pragma unroll
+                for (int r = 0; r < kAhead; ++r)
+                    if (r0 + r < P)
+                        h[r] = *reinterpret_cast<const int4*>(
+                            cluster.map_shared_rank(hist, r0 + r) + top);
+#pragma unroll
+                for (int r = 0; r < kAhead; ++r) {
+                    if (r0 + r >= P) break;
+                    const int v[kOwnBins] = {h[r].w, h[r].z, h[r].y, h[r].x};
+#pragma unroll
+                    for (int i = 0; i < kOwnBins; ++i) {
+                        mine[i] += v[i];
+                        if (r0 + r < rank) before[i] += v[i];
+                    }
+                }
+            }
+            int all_keys;
+            int above =
+                block_exclusive_scan(mine[0] + mine[1] + mine[2] + mine[3], s_tmp, &all_keys);
+#pragma unroll
+            for (int i = 0; i < kOwnBins; ++i) {
+                if (above < want && want <= above + mine[i]) {
+                    s_pick[0] = top + kOwnBins - 1 - i;
+                    s_pick[1] = want - above;
+                }
+                above += mine[i];
+            }
+            __syncthreads();
+            const int pick = s_pick[0];
+            want = s_pick[1];
+            edge = (edge << (pass == 2 ? 10 : 11)) | (uint32_t)pick;
+            // Kept keys before this CTA: those in bins above the chosen one.  In the last pass the
+            // chosen bin holds the ties.
+            int part = 0, same = 0;
+#pragma unroll
+            for (int i = 0; i < kOwnBins; ++i) {
+                const int bin = top + kOwnBins - 1 - i;
+                if (bin > pick) part += before[i];
+                if (bin == pick) same = before[i];
+            }
+            if (P > 1) {
+                out += block_sum(part, s_tmp);
+                if (pass == 2) ties = block_sum(same, s_tmp);
+            }
+            __syncthreads();
+        }
+        out += min(ties, want);  // the first `want` keys equal to the edge are kept
+
+        // The warps' counts, then the positions in order.
+        int na = 0, ne = 0;
+        each([&](int c, const float (&v)[4]) {
+            const long long t = lo + c * kChunk + lane * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t key = key_of(v[i]);
+                na += t + i < m && key > edge;
+                ne += t + i < m && key == edge;
+            }
+        });
+        na = __reduce_add_sync(0xffffffffu, na);
+        ne = __reduce_add_sync(0xffffffffu, ne);
+        int total;
+        const int wa = block_exclusive_scan(lane == 0 ? na : 0, s_tmp, &total);
+        const int we = block_exclusive_scan(lane == 0 ? ne : 0, s_tmp, &total);
+        int tie = ties + __shfl_sync(0xffffffffu, we, 0);
+        int at = out + __shfl_sync(0xffffffffu, wa, 0) + min(tie, want) - min(ties, want);
+        each([&](int c, const float (&v)[4]) {
+            const long long t = lo + c * kChunk + lane * 4;
+            uint32_t key[4];
+            int both = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                key[i] = key_of(v[i]);
+                both += t + i < m ? (key[i] > edge) + ((key[i] == edge) << 16) : 0;
+            }
+            const int scan = warp_inclusive_scan(both);
+            int e = tie + ((scan - both) >> 16);
+            int w = at + ((scan - both) & 0xffff) + min(e, want) - min(tie, want);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (t + i >= m) break;
+                const bool eq = key[i] == edge;
+                if (key[i] > edge || (eq && e < want)) {
+                    keep[w] = (int)(t + i);
+                    if (kept_acc) kept_acc[w] = v[i];
+                    ++w;
+                }
+                e += eq;
+            }
+            const int last = __shfl_sync(0xffffffffu, scan, 31);
+            const int after = tie + (last >> 16);
+            at += (last & 0xffff) + min(after, want) - min(tie, want);
+            tie = after;
+        });
+    }
     for (int j = gid; j < a.recent; j += all) {
         keep[k + j] = m + j;
         if (kept_acc) kept_acc[k + j] = acc[m + j];
     }
-    if (k == 0) return;
-
-    // This CTA's segment, and the k-th largest key digit by digit.
-    const int seg = (m + P - 1) / P;
-    const int lo = min(m, rank * seg), hi = min(m, lo + seg);
-    uint32_t prefix = 0;  // the digits found so far
-    int want = k;         // how many of the keys with that prefix are kept
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-        const int bins = pass == 2 ? 1024 : 2048;
-        for (int i = tid; i < kBins; i += kEvictThreads) s_hist[i] = 0;
-        __syncthreads();
-        for (int i = lo + tid; i < hi; i += kEvictThreads) {
-            const uint32_t key = key_of(__ldg(acc + i));
-            const bool in = pass == 0 || key >> (pass == 1 ? 21 : 10) == prefix;
-            if (in) atomicAdd(&s_hist[key >> shift & (bins - 1)], 1);
-        }
-        cluster.sync();
-        if (P > 1) {
-            const int share = kBins / P;
-            for (int i = tid; i < share; i += kEvictThreads) {
-                int sum = 0;
-                for (int r = 0; r < P; ++r)
-                    sum += cluster.map_shared_rank(s_hist, r)[rank * share + i];
-                s_sum[i] = sum;
-            }
-            cluster.sync();
-        }
-        // Suffix counts: thread t owns the bins 4 t .. 4 t + 3 counted from the top.
-        int mine[kBins / kEvictThreads], total = 0;
-#pragma unroll
-        for (int i = 0; i < kBins / kEvictThreads; ++i) {
-            const int bin = kBins - 1 - (tid * (kBins / kEvictThreads) + i);
-            mine[i] = P > 1 ? cluster.map_shared_rank(s_sum, bin / (kBins / P))[bin % (kBins / P)]
-                            : s_hist[bin];
-            total += mine[i];
-        }
-        int sum_all;
-        int before = block_exclusive_scan(total, s_tmp, &sum_all);
-#pragma unroll
-        for (int i = 0; i < kBins / kEvictThreads; ++i) {
-            if (before < want && want <= before + mine[i]) {
-                s_pick[0] = kBins - 1 - (tid * (kBins / kEvictThreads) + i);
-                s_pick[1] = want - before;
-            }
-            before += mine[i];
-        }
-        __syncthreads();
-        prefix = (prefix << (pass == 2 ? 10 : 11)) | (uint32_t)s_pick[0];
-        want = s_pick[1];
-        cluster.sync();  // every CTA has read the counts before they are cleared again
-    }
-    // prefix is the k-th largest key; `want` of the keys equal to it are kept, lowest first.
-    const uint32_t edge = prefix;
-    int above = 0, equal = 0;
-    for (int i = lo + tid; i < hi; i += kEvictThreads) {
-        const uint32_t key = key_of(__ldg(acc + i));
-        above += key > edge;
-        equal += key == edge;
-    }
-    above = block_sum(above, s_tmp);
-    equal = block_sum(equal, s_tmp);
-    if (tid == 0) {
-        s_above = above;
-        s_equal = equal;
-    }
-    cluster.sync();
-    int out = 0, ties = 0;  // written and ties seen before this CTA's segment
-    for (int r = 0; r < rank; ++r) {
-        const int e = *cluster.map_shared_rank(&s_equal, r);
-        out += *cluster.map_shared_rank(&s_above, r) + max(0, min(e, want - ties));
-        ties += e;
-    }
-    cluster.sync();  // the other CTAs' shared memory is not read after this
-    for (int base = lo; base < hi; base += kEvictThreads * kPer) {
-        float x[kPer];
-        uint32_t key[kPer];
-        int na = 0, ne = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int t = base + tid * kPer + i;
-            x[i] = t < hi ? __ldg(acc + t) : 0.f;
-            key[i] = key_of(x[i]);
-            na += t < hi && key[i] > edge;
-            ne += t < hi && key[i] == edge;
-        }
-        int both;
-        const int scan = block_exclusive_scan(na | ne << 16, s_tmp, &both);
-        int tie = ties + (scan >> 16);
-        // entries of this chunk before this thread: those above, and the ties still wanted
-        int at = out + (scan & 0xffff) + max(0, min(tie, want) - min(ties, want));
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int t = base + tid * kPer + i;
-            if (t >= hi) break;
-            const bool eq = key[i] == edge;
-            if (key[i] > edge || (eq && tie < want)) {
-                keep[at] = t;
-                if (kept_acc) kept_acc[at] = x[i];
-                ++at;
-            }
-            tie += eq;
-        }
-        const int t1 = ties + (both >> 16);
-        out += (both & 0xffff) + max(0, min(t1, want) - min(ties, want));
-        ties = t1;
-    }
+    if (k > 0) cluster.sync();  // no CTA leaves while another reads its counts
 }
 
-// One CTA per request; the steps follow one another, so that a token selected
-// in several steps is added to in step order.
+// One CTA per request; the steps follow one another (a barrier between them
+// orders the additions), so that a token selected in several steps is added to
+// in step order.  Up to kHeldSteps steps of 2 * 1024 entries are fetched before
+// the first addition; longer calls take the steps one by one.
 constexpr int kAccumulateThreads = 1024;
+constexpr int kHeldSteps = 4, kHeldEntries = 2;
 
 __global__ void __launch_bounds__(kAccumulateThreads)
     accumulate_kernel(const float* weights, const int32_t* topk, const int32_t* req,
                       const int32_t* counts, int32_t S, int32_t K, float* acc, int32_t R,
                       int32_t L) {
-    const int b = blockIdx.x;
+    const int b = blockIdx.x, tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the weights of the kernel before
     const int q = __ldg(req + b);
     if (q < 0 || q >= R) return;
     const int steps = counts ? min(__ldg(counts + b), S) : S;
     float* dst = acc + (long long)q * L;
+    const long long row = (long long)b * S * K;
+    if (K <= kHeldEntries * kAccumulateThreads && steps <= kHeldSteps) {
+        int t[kHeldSteps][kHeldEntries];
+        float w[kHeldSteps][kHeldEntries];
+#pragma unroll
+        for (int s = 0; s < kHeldSteps; ++s) {
+#pragma unroll
+            for (int i = 0; i < kHeldEntries; ++i) {
+                const int j = tid + i * kAccumulateThreads;
+                t[s][i] = s < steps && j < K ? __ldg(topk + row + s * K + j) : -1;
+                w[s][i] = s < steps && j < K ? __ldg(weights + row + s * K + j) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < kHeldSteps; ++s) {
+            if (s >= steps) break;
+#pragma unroll
+            for (int i = 0; i < kHeldEntries; ++i)
+                if (t[s][i] >= 0 && t[s][i] < L) atomicAdd(dst + t[s][i], w[s][i]);
+            __syncthreads();
+        }
+        return;
+    }
     for (int s = 0; s < steps; ++s) {
-        const long long row = ((long long)b * S + s) * K;
-        for (int j = threadIdx.x; j < K; j += kAccumulateThreads) {
-            const int t = __ldg(topk + row + j);
-            if (t >= 0 && t < L) atomicAdd(dst + t, __ldg(weights + row + j));
+#pragma unroll 4
+        for (int j = tid; j < K; j += kAccumulateThreads) {
+            const int t = __ldg(topk + row + (long long)s * K + j);
+            if (t >= 0 && t < L) atomicAdd(dst + t, __ldg(weights + row + (long long)s * K + j));
         }
         __syncthreads();
     }
@@ -217,9 +294,17 @@ __global__ void __launch_bounds__(kAccumulateThreads)
 cudaError_t launch_accumulate(const float* weights, const int32_t* topk, const int32_t* req,
                               const int32_t* counts, int32_t B, int32_t S, int32_t K, float* acc,
                               int32_t R, int32_t L, cudaStream_t s) {
-    accumulate_kernel<<<B, kAccumulateThreads, 0, s>>>(weights, topk, req, counts, S, K, acc, R,
-                                                       L);
-    return cudaGetLastError();
+    // May be launched while the kernel before it (hs_attend's) ends.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(B);
+    cfg.blockDim = dim3(kAccumulateThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, accumulate_kernel, weights, topk, req, counts, S, K, acc, R, L);
 }
 
 cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* seq_lens, int32_t B,
@@ -236,8 +321,12 @@ cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* se
     a.keep = keep;
     a.kept = kept;
     a.kept_acc = kept_acc;
+    // A cluster where one CTA would not hold the sequence's keys in registers.
+    constexpr int kHeld = kMaxChunks * kChunk * kEvictWarps;  // keys of a CTA
     int P = 1;
-    while (P < kMaxEvictCluster && L / P > 8192) P *= 2;
+    while (P < kMaxEvictCluster && L / P > kHeld) P *= 2;
+    const long long chunks = ((long long)L + kChunk - 1) / kChunk;
+    const int per_warp = (int)((chunks + P * kEvictWarps - 1) / (P * kEvictWarps));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(B * P);
     cfg.blockDim = dim3(kEvictThreads);
@@ -249,7 +338,10 @@ cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* se
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, a);
+    if (per_warp <= 1) return cudaLaunchKernelEx(&cfg, evict_kernel<1>, a);
+    if (per_warp <= 3) return cudaLaunchKernelEx(&cfg, evict_kernel<3>, a);
+    if (per_warp <= kMaxChunks) return cudaLaunchKernelEx(&cfg, evict_kernel<kMaxChunks>, a);
+    return cudaLaunchKernelEx(&cfg, evict_kernel<0>, a);
 }
 
 }  // namespace hs

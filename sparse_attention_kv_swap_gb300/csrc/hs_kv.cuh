@@ -61,30 +61,43 @@ cudaError_t launch_attend(const hs_kv_format& f, const hs_attend_args& a, cudaSt
 
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
+// Four codes as two pairs of f16 (e4m3).
+__device__ __forceinline__ void decode_halves(uint32_t w, __half2& lo, __half2& hi) {
+    uint32_t x, y;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+        " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(x), "=r"(y)
+        : "r"(w));
+    lo = *reinterpret_cast<__half2*>(&x);
+    hi = *reinterpret_cast<__half2*>(&y);
+}
+
 // Four codes as 32-bit values.
 template <int CODE>
 __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
     if constexpr (CODE == HS_KV_E4M3) {
-        uint32_t lo, hi;
-        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
-            " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(w));
-        const float2 p = __half22float2(*reinterpret_cast<__half2*>(&lo));
-        const float2 q = __half22float2(*reinterpret_cast<__half2*>(&hi));
+        __half2 lo, hi;
+        decode_halves(w, lo, hi);
+        const float2 p = __half22float2(lo), q = __half22float2(hi);
         x[0] = p.x;
         x[1] = p.y;
         x[2] = q.x;
         x[3] = q.y;
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> (8 * i));
+        // 0x4b000000 | b is the float 2^23 + b of a byte b: with the sign bit flipped, b is the
+        // code + 128.
+        const uint32_t u = w ^ 0x80808080u;
+        x[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540)) - 8388736.f;
+        x[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7541)) - 8388736.f;
+        x[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7542)) - 8388736.f;
+        x[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7543)) - 8388736.f;
     }
 }
 
 // Four codes of y (already divided by the scale): to nearest, ties to even,
-// clamped to the largest code.  NaN becomes the e4m3 NaN, or 0 in int8.
-template <int CODE>
+// clamped to the largest code.  NaN becomes the e4m3 NaN, or 0 in int8.  With
+// INSIDE, every y is known to be finite and to round to a code.
+template <int CODE, bool INSIDE = false>
 __device__ __forceinline__ uint32_t encode4(const float (&y)[4]) {
     uint32_t w;
     if constexpr (CODE == HS_KV_E4M3) {
@@ -93,12 +106,15 @@ __device__ __forceinline__ uint32_t encode4(const float (&y)[4]) {
             : "=r"(w)
             : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
     } else {
-        w = 0;
+        // Adding 1.5 * 2^23 leaves the rounded integer in the low bits.
+        uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int v = __float2int_rn(fminf(fmaxf(y[i], -127.f), 127.f));
-            w |= (uint32_t)((y[i] == y[i] ? v : 0) & 255) << (8 * i);
+            float x = y[i];
+            if (!INSIDE) x = x == x ? fminf(fmaxf(x, -127.f), 127.f) : 0.f;
+            u[i] = __float_as_uint(x + 12582912.f);
         }
+        w = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
     }
     return w;
 }

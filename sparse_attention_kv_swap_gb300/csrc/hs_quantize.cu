@@ -106,34 +106,71 @@ struct Raw {
     }
 };
 
-// 16 codes under one scale, as values under another (r = 1 / the new scale).
-template <int CODE>
+// 16 codes under one scale, as values under another (r = 1 / the new scale).  INSIDE: the new
+// scale covers the values.
+template <int CODE, bool INSIDE>
 __device__ __forceinline__ uint4 recode(const uint4& c, float scale, float r) {
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     uint32_t w[4];
+    if constexpr (CODE == HS_KV_E4M3) {
+        // Powers of two, as the scales written here are: the two factors are one, and exact in
+        // f16 too down to 2^-14 (below it, subnormal codes would lose bits before rounding).
+        const float ratio = scale * r;
+        const bool power = ((__float_as_uint(scale) | __float_as_uint(r)) & 0x7fffffu) == 0;
+        if (power && ratio == 1.f) return c;
+        if (power && ratio >= 6.103515625e-05f && ratio <= 32768.f) {
+            const __half2 f = __float2half2_rn(ratio);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                __half2 lo, hi;
+                decode_halves(in[i], lo, hi);
+                lo = __hmul2(lo, f);
+                hi = __hmul2(hi, f);
+                asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n"
+                    " cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n mov.b32 %0, {a, b};\n}"
+                    : "=r"(w[i])
+                    : "r"(*reinterpret_cast<uint32_t*>(&lo)),
+                      "r"(*reinterpret_cast<uint32_t*>(&hi)));
+            }
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float x[4];
         decode4<CODE>(in[i], x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], scale), r);
-        w[i] = encode4<CODE>(x);
+        w[i] = encode4<CODE, INSIDE>(x);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Largest magnitude of 16 codes under a scale.  Rounding is monotonic, so it is the product of
+// the scale and the largest code; a NaN code does not count.
 template <int CODE>
 __device__ __forceinline__ float magnitude(const uint4& c, float scale) {
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-    float a = 0.f;
+    float a;
+    if constexpr (CODE == HS_KV_E4M3) {
+        __half2 m = __half2half2(__ushort_as_half(0));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float x[4];
-        decode4<CODE>(in[i], x);
+        for (int i = 0; i < 4; ++i) {
+            __half2 lo, hi;
+            decode_halves(in[i], lo, hi);
+            m = __hmax2(m, __hmax2(__habs2(lo), __habs2(hi)));
+        }
+        a = fmaxf(__low2float(m), __high2float(m));
+    } else {
+        a = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a = fmaxf(a, finite_magnitude(__fmul_rn(x[j], scale)));
+        for (int i = 0; i < 4; ++i) {
+            float x[4];
+            decode4<CODE>(in[i], x);
+            a = fmaxf(a, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+        }
     }
-    return a;
+    return finite_magnitude(__fmul_rn(a, scale));
 }
 
 // Stores 16 bytes of row (q, t) at byte `off`: into the store, and with CACHE
@@ -231,7 +268,7 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_kernel(const QuantizeArg
         const int t = (int)first + u / parts, o = off + (u % parts) * 16;
         const uint4 x = *reinterpret_cast<const uint4*>(
             a.rows + ((long long)q * a.L + t) * a.f.item_size_bytes + o);
-        store_row<CACHE>(a, q, t, end, o, recode<CODE>(x, was, r));
+        store_row<CACHE>(a, q, t, end, o, recode<CODE, false>(x, was, r));
     }
 }
 
@@ -295,13 +332,13 @@ __global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs 
         const int u = threadIdx.x + i * nt;
         if (u < units)
             st_v4(dst + (long long)(u / parts) * W + (u % parts) * 16,
-                  recode<CODE>(held[i], scale[i], r));
+                  recode<CODE, true>(held[i], scale[i], r));
     }
     for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
         uint4 x;
         float s;
         load(u, x, s);
-        st_v4(dst + (long long)(u / parts) * W + (u % parts) * 16, recode<CODE>(x, s, r));
+        st_v4(dst + (long long)(u / parts) * W + (u % parts) * 16, recode<CODE, true>(x, s, r));
     }
 }
 
