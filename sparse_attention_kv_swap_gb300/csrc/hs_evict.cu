@@ -19,14 +19,15 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kMaxEvictCluster = 8;
 constexpr int kAhead = 4;                        // remote counts read at a time
 constexpr int kBins = 2048;
-constexpr int kOwnBins = kBins / kEvictThreads;  // bins a thread looks through
+constexpr int kOwnBins = 2;                      // bins a thread looks through
+static_assert(kOwnBins * kEvictThreads == kBins, "every bin has a thread");
 constexpr int kChunk = 128;                      // positions a warp takes at a time, 4 a lane
-constexpr int kMaxChunks = 8;                    // a warp holds in registers
+constexpr int kMaxChunks = 4;                    // a warp holds in registers
 
 // Key of a weight: larger weights have larger keys, NaN the smallest, the two
 // zeros the same.
@@ -34,6 +35,12 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
     if (!(x == x)) return 0u;
     return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// The weight of a key (the NaN of key 0 and a zero come back without their sign bits).
+__device__ __forceinline__ float weight_of(uint32_t key) {
+    if (key == 0u) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
 struct EvictArgs {
@@ -82,14 +89,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
     if (k > 0) {
         // The warp's segment, in chunks of 128 positions, 4 consecutive ones a lane.
         const int chunks = ((m + kChunk - 1) / kChunk + P * kEvictWarps - 1) / (P * kEvictWarps);
-        const long long lo = (long long)(rank * kEvictWarps + warp) * chunks * kChunk;
-        float x[CH > 0 ? CH : 1][4];
-        auto fetch = [&](int c, float (&v)[4]) {
-            const long long t = lo + c * kChunk + lane * 4;
+        const int lo = (rank * kEvictWarps + warp) * chunks * kChunk;
+        uint32_t x[CH > 0 ? CH : 1][4];
+        // Past the last candidate the key is 0, the smallest, and the position behind those of all
+        // candidates: such a key is never among the k kept, so the passes need not tell.
+        auto fetch = [&](int c, uint32_t (&v)[4]) {
+            const int t = lo + c * kChunk + lane * 4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = t + i < m ? __ldg(acc + t + i) : 0.f;
+            for (int i = 0; i < 4; ++i) v[i] = t + i < m ? key_of(__ldg(acc + t + i)) : 0u;
         };
-        // Calls f(chunk, its 4 weights) for the warp's chunks in order.
+        // Calls f(chunk, its 4 keys) for the warp's chunks in order.
         auto each = [&](auto f) {
             if constexpr (CH > 0) {
 #pragma unroll
@@ -119,14 +128,11 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const int bins = pass == 2 ? 1024 : 2048;
             int* hist = s_hist[pass];
-            each([&](int c, const float (&v)[4]) {
-                const long long t = lo + c * kChunk + lane * 4;
+            each([&](int, const uint32_t (&v)[4]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t key = key_of(v[i]);
-                    if (t + i < m && (pass == 0 || key >> (pass == 1 ? 21 : 10) == edge))
-                        atomicAdd(&hist[key >> shift & (bins - 1)], 1);
-                }
+                for (int i = 0; i < 4; ++i)
+                    if (pass == 0 || v[i] >> (pass == 1 ? 21 : 10) == edge)
+                        atomicAdd(&hist[v[i] >> shift & (bins - 1)], 1);
             });
             cluster.sync();
             // A thread's bins, counted from the top, over the cluster and before this CTA.
@@ -136,26 +142,23 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
             for (int i = 0; i < kOwnBins; ++i) mine[i] = before[i] = 0;
 #pragma unroll 1
             for (int r0 = 0; r0 < P; r0 += kAhead) {
-                int4 h[kAhead];  // on their way together: a remote load takes long
+                int2 h[kAhead];  // on their way together: a remote load takes long
 #pragma unroll
                 for (int r = 0; r < kAhead; ++r)
                     if (r0 + r < P)
-                        h[r] = *reinterpret_cast<const int4*>(
+                        h[r] = *reinterpret_cast<const int2*>(
                             cluster.map_shared_rank(hist, r0 + r) + top);
 #pragma unroll
                 for (int r = 0; r < kAhead; ++r) {
                     if (r0 + r >= P) break;
-                    const int v[kOwnBins] = {h[r].w, h[r].z, h[r].y, h[r].x};
-#pragma unroll
-                    for (int i = 0; i < kOwnBins; ++i) {
-                        mine[i] += v[i];
-                        if (r0 + r < rank) before[i] += v[i];
-                    }
+                    mine[0] += h[r].y;
+                    mine[1] += h[r].x;
+                    if (r0 + r < rank) before[0] += h[r].y, before[1] += h[r].x;
                 }
             }
             int all_keys;
             int above =
-                block_exclusive_scan(mine[0] + mine[1] + mine[2] + mine[3], s_tmp, &all_keys);
+                block_exclusive_scan(mine[0] + mine[1], s_tmp, &all_keys);
 #pragma unroll
             for (int i = 0; i < kOwnBins; ++i) {
                 if (above < want && want <= above + mine[i]) {
@@ -187,13 +190,11 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
 
         // The warps' counts, then the positions in order.
         int na = 0, ne = 0;
-        each([&](int c, const float (&v)[4]) {
-            const long long t = lo + c * kChunk + lane * 4;
+        each([&](int, const uint32_t (&v)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t key = key_of(v[i]);
-                na += t + i < m && key > edge;
-                ne += t + i < m && key == edge;
+                na += v[i] > edge;
+                ne += v[i] == edge;
             }
         });
         na = __reduce_add_sync(0xffffffffu, na);
@@ -203,25 +204,20 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
         const int we = block_exclusive_scan(lane == 0 ? ne : 0, s_tmp, &total);
         int tie = ties + __shfl_sync(0xffffffffu, we, 0);
         int at = out + __shfl_sync(0xffffffffu, wa, 0) + min(tie, want) - min(ties, want);
-        each([&](int c, const float (&v)[4]) {
-            const long long t = lo + c * kChunk + lane * 4;
-            uint32_t key[4];
+        each([&](int c, const uint32_t (&v)[4]) {
+            const int t = lo + c * kChunk + lane * 4;
             int both = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                key[i] = key_of(v[i]);
-                both += t + i < m ? (key[i] > edge) + ((key[i] == edge) << 16) : 0;
-            }
+            for (int i = 0; i < 4; ++i) both += (v[i] > edge) + ((v[i] == edge) << 16);
             const int scan = warp_inclusive_scan(both);
             int e = tie + ((scan - both) >> 16);
             int w = at + ((scan - both) & 0xffff) + min(e, want) - min(tie, want);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (t + i >= m) break;
-                const bool eq = key[i] == edge;
-                if (key[i] > edge || (eq && e < want)) {
-                    keep[w] = (int)(t + i);
-                    if (kept_acc) kept_acc[w] = v[i];
+                const bool eq = v[i] == edge;
+                if (v[i] > edge || (eq && e < want)) {
+                    keep[w] = t + i;
+                    if (kept_acc) kept_acc[w] = weight_of(v[i]);
                     ++w;
                 }
                 e += eq;
@@ -339,7 +335,7 @@ cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* se
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (per_warp <= 1) return cudaLaunchKernelEx(&cfg, evict_kernel<1>, a);
-    if (per_warp <= 3) return cudaLaunchKernelEx(&cfg, evict_kernel<3>, a);
+    if (per_warp <= 2) return cudaLaunchKernelEx(&cfg, evict_kernel<2>, a);
     if (per_warp <= kMaxChunks) return cudaLaunchKernelEx(&cfg, evict_kernel<kMaxChunks>, a);
     return cudaLaunchKernelEx(&cfg, evict_kernel<0>, a);
 }

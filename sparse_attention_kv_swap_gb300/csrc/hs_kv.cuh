@@ -30,6 +30,26 @@ struct QuantizeArgs {
 };
 cudaError_t launch_quantize(QuantizeArgs a, bool cache, cudaStream_t s);
 
+// Division of 0 <= t < 2^31 by a constant d: with 2^l >= d, m = ceil(2^(31 + l) / d) is below 2^32
+// and off from the quotient by less than 2^-31, too little to reach the next integer.
+struct Divisor {
+    uint32_t m;
+    int32_t shift;
+    static Divisor by(int32_t d) {
+        int l = 0;
+        while ((1ll << l) < d) ++l;
+        Divisor x;
+        x.m = (uint32_t)(((1ull << (31 + l)) + (uint32_t)d - 1) / (uint32_t)d);
+        x.shift = 31 + l;
+        return x;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int32_t of(int32_t t) const {
+        return (int32_t)(((uint64_t)(uint32_t)t * m) >> shift);
+    }
+#endif
+};
+
 struct CompactArgs {
     hs_kv_format f;
     const uint8_t* src;
@@ -43,6 +63,7 @@ struct CompactArgs {
     int32_t batch, budget;
     int32_t src_R, src_L, src_NB, dst_R, dst_L, dst_NB;
     int32_t windows;
+    Divisor block;  // by block_tokens
 };
 cudaError_t launch_compact(CompactArgs a, cudaStream_t s);
 

@@ -8,20 +8,27 @@
 // the codes, so that the input is read once and the codes are written once.
 // Both kernels are bound by memory traffic: 3 bytes per element to quantise
 // 16-bit values, 2 to compact.
+#include <type_traits>
+
 #include "hs_kv.cuh"
 
 namespace hs {
 namespace {
 
-// Units of 16 elements (16 bytes of codes) that a thread keeps in registers;
-// groups larger than kHeld * blockDim.x units read the rest twice.
+// Thread tid of a group works on part tid % parts of the tokens tid / parts,
+// + step, + 2 * step, ..: a part is 16 elements (16 bytes of codes), and the block
+// has parts * step threads, up to whole warps.  kHeld parts stay in registers; larger groups read
+// the rest twice.
 constexpr int kHeld = 4;
-constexpr int kMaxThreads = 512;
+constexpr int kStep = 16;       // tokens of a turn, or a multiple
+constexpr int kMaxThreads = 448;  // two such blocks an SM leave 72 registers a thread
 
-int group_threads(int units) {
-    int t = 32;
-    while (t < kMaxThreads && t * kHeld < units) t *= 2;
-    return t;
+// Threads of a group of so many tokens, whole warps.
+int group_threads(int tokens, int parts) {
+    int step = kStep;
+    while (step * kHeld < tokens && 2 * step * parts <= kMaxThreads) step *= 2;
+    while (step > tokens && step > 1) step /= 2;
+    return (step * parts + 31) / 32 * 32;
 }
 
 // 16 consecutive input elements, as loaded.
@@ -79,14 +86,37 @@ struct Raw {
         }
     }
 
+    // Largest finite magnitude.
     __device__ __forceinline__ float magnitude() const {
         float a = 0.f;
+        if constexpr (DTYPE == HS_DTYPE_FP32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x[4];
-            get(i, x);
+            for (int i = 0; i < 4; ++i) {
+                float x[4];
+                get(i, x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a = fmaxf(a, finite_magnitude(x[j]));
+                for (int j = 0; j < 4; ++j) a = fmaxf(a, finite_magnitude(x[j]));
+            }
+        } else {
+            using Pair = std::conditional_t<DTYPE == HS_DTYPE_BF16, __nv_bfloat162, __half2>;
+            const uint32_t inf = DTYPE == HS_DTYPE_BF16 ? 0x7f807f80u : 0x7c007c00u;
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // an infinity or a NaN is not below infinity, and becomes 0
+                    uint32_t u = w[j] & 0x7fff7fffu;
+                    u &= __hlt2_mask(*reinterpret_cast<const Pair*>(&u),
+                                     *reinterpret_cast<const Pair*>(&inf));
+                    const Pair p = __hmax2(*reinterpret_cast<const Pair*>(&m),
+                                           *reinterpret_cast<const Pair*>(&u));
+                    m = *reinterpret_cast<const uint32_t*>(&p);
+                }
+            }
+            const Pair p = *reinterpret_cast<const Pair*>(&m);
+            a = fmaxf(__low2float(p), __high2float(p));
         }
         return a;
     }
@@ -196,7 +226,7 @@ __device__ __forceinline__ void store_row(const QuantizeArgs& a, int q, int t, i
 }
 
 template <int CODE, int DTYPE, bool CACHE>
-__global__ void __launch_bounds__(kMaxThreads) quantize_kernel(const QuantizeArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, CACHE ? 1 : 2) quantize_kernel(const QuantizeArgs a) {
     __shared__ float s_tmp[32];
     const int heads = a.f.num_kv_heads, D = a.f.head_dim, T = a.f.block_tokens;
     // CTAs of one block of tokens are neighbours: together they read whole rows
@@ -217,63 +247,61 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_kernel(const QuantizeArg
     const int lo = first > start ? (int)first : start;
     const int hi = first + T < end ? (int)first + T : end;
     const int parts = D >> 4;
-    const int units = (hi - lo) * parts;
+    const int part = threadIdx.x % parts, j0 = threadIdx.x / parts, step = blockDim.x / parts;
+    const int tokens = j0 < step ? hi - lo : 0;  // a part of a warp may be left over
     const int c = ch >= heads, h = c ? ch - heads : ch;
     const void* base = c ? a.in.v_dev : a.in.k_dev;
     const int64_t* stride = c ? a.in.v_stride : a.in.k_stride;
-    const long long at0 = b * stride[0] + (lo - start) * stride[1] + h * stride[2];
+    const long long at0 =
+        b * stride[0] + (lo - start) * stride[1] + h * stride[2] + part * 16;
 
     float* scale_at = a.scales + (((long long)q * a.NB + blk) * 2 + c) * heads + h;
     const bool begun = first < lo;  // the block has tokens from before this call
     const float was = begun ? *scale_at : 0.f;
-    Raw<DTYPE> held[kHeld];
+    constexpr int HELD = DTYPE == HS_DTYPE_FP32 ? kHeld / 2 : kHeld;  // the same registers
+    Raw<DTYPE> held[HELD];
     float peak = 0.f;
-    const int nt = blockDim.x;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int u = threadIdx.x + i * nt;
-        if (u < units)
-            held[i].load(base, at0 + (long long)(u / parts) * stride[1] + (u % parts) * 16,
-                         a.vec_in);
+    for (int i = 0; i < HELD; ++i) {
+        const int j = j0 + i * step;
+        if (j < tokens) held[i].load(base, at0 + j * stride[1], a.vec_in);
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        if ((int)threadIdx.x + i * nt < units) peak = fmaxf(peak, held[i].magnitude());
-    for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
+    for (int i = 0; i < HELD; ++i)
+        if (j0 + i * step < tokens) peak = fmaxf(peak, held[i].magnitude());
+    for (int j = j0 + HELD * step; j < tokens; j += step) {
         Raw<DTYPE> x;
-        x.load(base, at0 + (long long)(u / parts) * stride[1] + (u % parts) * 16, a.vec_in);
+        x.load(base, at0 + j * stride[1], a.vec_in);
         peak = fmaxf(peak, x.magnitude());
     }
     const float now = fmaxf(was, scale_of<CODE>(block_max(peak, s_tmp)));
     const float r = reciprocal_or_zero(now);
     if (threadIdx.x == 0) *scale_at = now;
-    const int off = c * heads * D + h * D;
+    const int off = c * heads * D + h * D + part * 16;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int u = threadIdx.x + i * nt;
-        if (u < units)
-            store_row<CACHE>(a, q, lo + u / parts, end, off + (u % parts) * 16,
-                             held[i].template encode<CODE>(r));
+    for (int i = 0; i < HELD; ++i) {
+        const int j = j0 + i * step;
+        if (j < tokens)
+            store_row<CACHE>(a, q, lo + j, end, off, held[i].template encode<CODE>(r));
     }
-    for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
+    for (int j = j0 + HELD * step; j < tokens; j += step) {
         Raw<DTYPE> x;
-        x.load(base, at0 + (long long)(u / parts) * stride[1] + (u % parts) * 16, a.vec_in);
-        store_row<CACHE>(a, q, lo + u / parts, end, off + (u % parts) * 16,
-                         x.template encode<CODE>(r));
+        x.load(base, at0 + j * stride[1], a.vec_in);
+        store_row<CACHE>(a, q, lo + j, end, off, x.template encode<CODE>(r));
     }
     if (!begun || !(now > was)) return;
     // The scale grew: the block's older codes are rounded again under it.
-    const int old_units = (int)(lo - first) * parts;
-    for (int u = threadIdx.x; u < old_units; u += nt) {
-        const int t = (int)first + u / parts, o = off + (u % parts) * 16;
+    const int old_tokens = j0 < step ? (int)(lo - first) : 0;
+    for (int j = j0; j < old_tokens; j += step) {
+        const int t = (int)first + j;
         const uint4 x = *reinterpret_cast<const uint4*>(
-            a.rows + ((long long)q * a.L + t) * a.f.item_size_bytes + o);
-        store_row<CACHE>(a, q, t, end, o, recode<CODE, false>(x, was, r));
+            a.rows + ((long long)q * a.L + t) * a.f.item_size_bytes + off);
+        store_row<CACHE>(a, q, t, end, off, recode<CODE, false>(x, was, r));
     }
 }
 
 template <int CODE>
-__global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(512, 2) compact_kernel(const CompactArgs a) {
     __shared__ float s_tmp[32];
     const int heads = a.f.num_kv_heads, D = a.f.head_dim, T = a.f.block_tokens;
     const int W = a.f.item_size_bytes;
@@ -285,11 +313,12 @@ __global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs 
     if (sq < 0 || sq >= a.src_R || dq < 0 || dq >= a.dst_R) return;
     kept = min(kept, min(a.budget, a.dst_L));
     const int first = win * T;
-    const int tokens = min(T, kept - first);
+    int tokens = min(T, kept - first);
     if (tokens <= 0) return;
     const int parts = D >> 4;
-    const int units = tokens * parts;
-    const int off = ch * D;
+    const int part = threadIdx.x % parts, j0 = threadIdx.x / parts, step = blockDim.x / parts;
+    if (j0 >= step) tokens = 0;  // a part of a warp may be left over
+    const int off = ch * D + part * 16;
     const uint8_t* src = a.src + (long long)sq * a.src_L * W + off;
     uint8_t* dst = a.dst + ((long long)dq * a.dst_L + first) * W + off;
     const int32_t* keep = a.keep + (long long)b * a.budget + first;
@@ -298,29 +327,32 @@ __global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs 
     uint4 held[kHeld];
     float scale[kHeld];
     float peak = 0.f;
-    const int nt = blockDim.x;
-    auto load = [&](int u, uint4& x, float& s) {
-        const int t = __ldg(keep + u / parts);
+    auto load = [&](int t, uint4& x, float& s) {
         x = make_uint4(0, 0, 0, 0);
         s = 0.f;
         if (t >= 0 && t < a.src_L) {
-            x = ld_stream_v4(src + (long long)t * W + (u % parts) * 16);
-            s = __ldg(scales + (long long)(t / T) * 2 * heads);
+            x = ld_stream_v4(src + (long long)t * W);
+            s = __ldg(scales + (long long)a.block.of(t) * (2 * heads));
         }
     };
+    int t[kHeld];
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-        const int u = threadIdx.x + i * nt;
-        if (u < units) load(u, held[i], scale[i]);
+        const int j = j0 + i * step;
+        t[i] = j < tokens ? __ldg(keep + j) : -1;
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        if ((int)threadIdx.x + i * nt < units)
-            peak = fmaxf(peak, magnitude<CODE>(held[i], scale[i]));
-    for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
+    for (int i = 0; i < kHeld; ++i) load(t[i], held[i], scale[i]);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        peak = fmaxf(peak, magnitude<CODE>(held[i], scale[i]));
+        // the codes are decoded anew below: kept, the values would take four times the registers
+        asm volatile("" : "+r"(held[i].x), "+r"(held[i].y), "+r"(held[i].z), "+r"(held[i].w));
+    }
+    for (int j = j0 + kHeld * step; j < tokens; j += step) {
         uint4 x;
         float s;
-        load(u, x, s);
+        load(__ldg(keep + j), x, s);
         peak = fmaxf(peak, magnitude<CODE>(x, s));
     }
     const float now = scale_of<CODE>(block_max(peak, s_tmp));
@@ -329,16 +361,15 @@ __global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs 
         a.dst_scales[((long long)dq * a.dst_NB + win) * 2 * heads + ch] = now;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-        const int u = threadIdx.x + i * nt;
-        if (u < units)
-            st_v4(dst + (long long)(u / parts) * W + (u % parts) * 16,
-                  recode<CODE, true>(held[i], scale[i], r));
+        const int j = j0 + i * step;
+        if (j < tokens)
+            st_v4(dst + (long long)j * W, recode<CODE, true>(held[i], scale[i], r));
     }
-    for (int u = threadIdx.x + kHeld * nt; u < units; u += nt) {
+    for (int j = j0 + kHeld * step; j < tokens; j += step) {
         uint4 x;
         float s;
-        load(u, x, s);
-        st_v4(dst + (long long)(u / parts) * W + (u % parts) * 16, recode<CODE, true>(x, s, r));
+        load(__ldg(keep + j), x, s);
+        st_v4(dst + (long long)j * W, recode<CODE, true>(x, s, r));
     }
 }
 
@@ -371,7 +402,8 @@ cudaError_t launch_quantize(QuantizeArgs a, bool cache, cudaStream_t s) {
     int grid;
     if (!grid_of((long long)a.batch * a.windows * 2 * a.f.num_kv_heads, &grid))
         return cudaErrorInvalidConfiguration;
-    const int threads = group_threads((a.max_count < T ? a.max_count : T) * (a.f.head_dim / 16));
+    const int parts = a.f.head_dim / 16;
+    const int threads = group_threads(a.max_count < T ? a.max_count : T, parts);
     if (a.f.code == HS_KV_E4M3) {
         if (cache)
             quantize_dtype<HS_KV_E4M3, true>(a, grid, threads, s);
@@ -393,7 +425,9 @@ cudaError_t launch_compact(CompactArgs a, cudaStream_t s) {
     int grid;
     if (!grid_of((long long)a.batch * a.windows * 2 * a.f.num_kv_heads, &grid))
         return cudaErrorInvalidConfiguration;
-    const int threads = group_threads((most < T ? most : T) * (a.f.head_dim / 16));
+    a.block = Divisor::by(T);
+    const int parts = a.f.head_dim / 16;
+    const int threads = group_threads(most < T ? most : T, parts);
     if (a.f.code == HS_KV_E4M3)
         compact_kernel<HS_KV_E4M3><<<grid, threads, 0, s>>>(a);
     else
