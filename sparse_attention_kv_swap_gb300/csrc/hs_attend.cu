@@ -1,4 +1,5 @@
 // Launch shape of hs_attend (the kernel is in hs_attend.cuh).
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -7,7 +8,6 @@
 namespace hs {
 namespace {
 
-constexpr int kSms = 152;
 constexpr size_t kSmSmem = 228 * 1024;             // of an SM; a CTA takes 1 KB more than it asks
 constexpr int kSmCols = 512;                       // tensor-memory columns of an SM
 constexpr size_t kStatic = 512;                    // static arrays of the kernel, rounded up
@@ -23,7 +23,8 @@ void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, AttendSh
     if (k.TS == 0) k.TS = 16;
     k.TC = k.TS + 4;  // scale rows in different banks
     const int D = f.head_dim, G = a.num_heads / f.num_kv_heads;
-    k.ngroups = (G + 8 * sh->nt - 1) / (8 * sh->nt);
+    const int columns = sh->nt == 0 ? 4 : 8 * sh->nt;  // query heads of a task
+    k.ngroups = (G + columns - 1) / columns;
     const int groups = f.num_kv_heads * k.ngroups;
     // Warps: one task each where they fit; with few heads, a CTA's tokens are split into parts
     // so that it has 8 warps or a few more; with many, a warp takes several in turn.
@@ -37,12 +38,12 @@ void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, AttendSh
     sh->threads = 32 * warps;
     k.alias = rounds == 1;
     const int task_tiles = (k.TS / 16 + nsub - 1) / nsub;
-    k.task_cols = 4 * sh->nt * task_tiles;
+    k.task_cols = sh->nt == 0 ? 4 * ((task_tiles + 1) / 2) : 4 * sh->nt * task_tiles;
     const long long need = (long long)rounds * ((warps + 3) / 4) * k.task_cols;
     int cols = 32;
     while (cols < need && cols < 2 * kSmCols) cols *= 2;
     k.cols = cols;
-    const size_t HP = (size_t)groups * 8 * sh->nt;
+    const size_t HP = (size_t)groups * columns;
     const size_t fixed = 4 * ((2 * nsub + 1) * HP + (((size_t)P * a.num_heads + 3) & ~(size_t)3));
     const size_t scale = (size_t)2 * f.num_kv_heads * k.TC, weight = (size_t)groups * k.TS;
     const size_t token = 4 * ((size_t)3 * k.TS + (scale > weight ? scale : weight));
@@ -68,37 +69,86 @@ bool fits(const AttendShape& sh, size_t smem) {
     return sh.smem <= smem && sh.a.cols <= kSmCols;
 }
 
-// P: the fewest CTAs of which two fit an SM, and enough of them, of 64 tokens
-// or more, that every SM has two; the workspace where not even one of 16 fits.
-AttendShape shape_of(const hs_kv_format& f, const hs_attend_args& a) {
+// CTAs in clusters of P that the current device runs at once with one CTA an SM: fewer than
+// SMs where P does not divide a group of SMs (on one GB300, 152 in clusters of 1 or 2, 144 of
+// 4, 120 of 8, 112 of 16).  Asked once per device and cluster size.
+int resident(int P) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][kMaxCluster + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = kDevices;
+    int n = dev < kDevices ? known[dev][P].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        n = attend_resident(P, kMaxSmem);
+        if (n <= 0) n = 112;
+        if (dev < kDevices) known[dev][P].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// The same for a shape: registers leave room for two CTAs of up to 8 warps an SM, and then a
+// cluster of an even P needs P / 2 SMs.
+int slots(const AttendShape& sh) {
+    if (sh.threads > 256 || sh.smem > kHalfSmem) return resident(sh.P);
+    return 2 * resident(sh.P % 2 == 0 ? sh.P / 2 : sh.P);
+}
+
+// Estimated time of a call in us.  The CTAs run in rounds, each with a start and an end (about 10 us
+// and 4 ns a token) besides the rows it gathers, which come at 44 GB/s an SM whether one CTA
+// or two share it.
+double cost(const hs_kv_format& f, const hs_attend_args& a, const AttendShape& sh) {
+    constexpr int kSms = 152;
+    const int n = slots(sh);
+    const double row = 2.0 * f.num_kv_heads * f.head_dim / 44e3;
+    double t = 0;
+    for (long long left = (long long)a.batch * a.steps * sh.P; left > 0; left -= n) {
+        const int per_sm = left > kSms && n > kSms ? 2 : 1;
+        t += 10 + sh.a.TS * (0.004 + per_sm * row);
+    }
+    return t;
+}
+
+// The cluster sizes tried for a call: CTAs of 64 tokens or more, if any of those fit.
+bool worth(const hs_attend_args& a, int P) { return P == 1 || a.top_k >= 64 * P; }
+
+// The first cluster size that fits, among those worth it or else among all; with the scores and
+// the arrays by token in the workspace if none does.  Host only.
+AttendShape first_shape(const hs_kv_format& f, const hs_attend_args& a) {
     AttendShape sh;
     std::memset(&sh, 0, sizeof(sh));
     const int G = a.num_heads / f.num_kv_heads;
-    sh.nt = G > 8 && f.head_dim <= 128 ? 2 : 1;
-    const long long queries = (long long)a.batch * a.steps;
-    int P = 1;
-    while (P < 8 && a.top_k > 64 * P && queries * P * 2 <= 2 * kSms) P *= 2;
-    set_cluster(f, a, P, &sh);
-    while (!fits(sh, kHalfSmem) && P < kMaxCluster && a.top_k > 64 * P) {
-        P *= 2;
-        set_cluster(f, a, P, &sh);
+    sh.nt = G <= 4 && f.head_dim <= 192 ? 0 : G > 8 && f.head_dim <= 128 ? 2 : 1;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int P = 1; P <= kMaxCluster && (pass == 1 || worth(a, P)); ++P) {
+            set_cluster(f, a, P, &sh);
+            if (fits(sh, kMaxSmem)) return sh;
+        }
     }
-    while (!fits(sh, kMaxSmem) && P < kMaxCluster && a.top_k > 16 * P) {
-        P *= 2;
-        set_cluster(f, a, P, &sh);
-    }
-    if (!fits(sh, kMaxSmem)) {
-        sh.nt = 1;
-        sh.spill = true;
-        set_cluster(f, a, P, &sh);
-    }
+    sh.nt = 1;
+    sh.spill = true;
+    set_cluster(f, a, kMaxCluster, &sh);
     return sh;
+}
+
+// Of the cluster sizes that fit and are worth it, the one of the least estimated time.
+AttendShape shape_of(const hs_kv_format& f, const hs_attend_args& a) {
+    AttendShape best = first_shape(f, a);
+    if (best.spill || best.P == kMaxCluster || !worth(a, best.P + 1)) return best;
+    double least = cost(f, a, best);
+    AttendShape sh = best;
+    for (int P = best.P + 1; P <= kMaxCluster && worth(a, P); P += P < 8 ? 1 : 2) {
+        set_cluster(f, a, P, &sh);
+        if (!fits(sh, kMaxSmem)) continue;
+        const double t = cost(f, a, sh);
+        if (t < least) least = t, best = sh;
+    }
+    return best;
 }
 
 }  // namespace
 
 size_t attend_workspace(const hs_kv_format& f, const hs_attend_args& a) {
-    const AttendShape sh = shape_of(f, a);
+    const AttendShape sh = first_shape(f, a);
     return sh.spill ? (size_t)a.batch * a.steps * sh.P * sh.a.token_bytes : 0;
 }
 
@@ -116,7 +166,7 @@ cudaError_t launch_attend(const hs_kv_format& f, const hs_attend_args& a, cudaSt
     k.G = a.num_heads / f.num_kv_heads;
     k.R = a.num_requests;
     k.L = a.max_seq_len;
-    k.T = f.block_tokens;
+    k.block = Divisor::by(f.block_tokens);
     k.NB = (a.max_seq_len - 1) / f.block_tokens + 1;
     k.W = f.item_size_bytes;
     k.scale_log2 = a.sm_scale * 1.4426950408889634f;

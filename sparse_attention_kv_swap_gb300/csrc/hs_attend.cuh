@@ -28,6 +28,10 @@
 //      task, so it lies in [0, 1] and is rounded to f16 (11 bits): its rounding
 //      error, at most 2^-12 of each term, is far below the output's own 8 or
 //      11 bits.
+// With 4 query heads to a K/V head or fewer, one fragment takes two tiles: the
+// 8 columns are the heads of the first tile and again those of the second, the
+// queries lying in columns 0-3 for one product and 4-7 for the other.  Scores,
+// exponentials and tensor memory then halve (NT = 0 below).
 // Then the CTAs of the cluster exchange maxima and sums over distributed
 // shared memory, each adds up a share of the output over the CTAs in rank
 // order, and each turns its own scores into weights with the query's final
@@ -50,7 +54,8 @@ namespace hs {
 struct AttendKernelArgs {
     const void* q;
     void* out;
-    int32_t fp16, B, S, K, Hq, Hkv, G, R, L, NB, T, W;
+    int32_t fp16, B, S, K, Hq, Hkv, G, R, L, NB, W;
+    Divisor block;  // by block_tokens
     float scale_log2;  // sm_scale * log2(e)
     int64_t q_stride[3], out_stride[3];
     const uint8_t* rows;
@@ -83,6 +88,9 @@ struct AttendShape {
 // Defined once per code in hs_attend_e4m3.cu and hs_attend_int8.cu.
 cudaError_t attend_run_e4m3(const AttendShape& sh, int D, cudaStream_t s);
 cudaError_t attend_run_int8(const AttendShape& sh, int D, cudaStream_t s);
+// CTAs in clusters of P that the current device runs at once, with so much shared memory and 8
+// warps a CTA (0 if the query fails).
+int attend_resident(int P, size_t smem);
 
 constexpr int kMaxCluster = 16;
 // Warps of a CTA at most: 128 registers a thread, twice that for the widest tasks with 64-bit
@@ -239,6 +247,12 @@ __device__ __forceinline__ float4 load_remote4(const float* p, int rank) {
     return x;
 }
 
+// Query head, within its group, of column 2 c of a score fragment.
+template <int NT>
+__device__ __forceinline__ int column_head(int c) {
+    return NT == 0 ? (2 * c) & 3 : 2 * c;
+}
+
 // Reductions over the 8 lanes that share c (lanes differ in g).
 __device__ __forceinline__ float max_over_g(float x) {
 #pragma unroll
@@ -303,10 +317,10 @@ struct Scores {
             }
         }
     }
-    // The loaded scores may be used after this.
-    __device__ __forceinline__ void loaded(float (&s)[NT][4]) const {
+    // The loaded scores may be used after this (without a wait: one was waited for already).
+    __device__ __forceinline__ void loaded(float (&s)[NT][4], bool wait = true) const {
         if constexpr (!SPILL) {
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            if (wait) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -412,33 +426,50 @@ __device__ __forceinline__ void finish(const AttendKernelArgs& a, uint8_t* smem,
         const int groups = a.Hkv * a.ngroups, ntasks = groups * a.nsub;
         const int tiles = (live + 15) >> 4, nwarps = nthreads >> 5, warp = tid >> 5;
         const int g = (tid & 31) >> 2, c = tid & 3, t_lo = 4 * (g >> 1) + (g & 1);
+        constexpr int F = NT == 0 ? 2 : 1, N = NT == 0 ? 1 : NT;
         for (int task = warp, turn = 0; task < ntasks; task += nwarps, ++turn) {
             const int sub = task / groups, hg = task - sub * groups;
             const int h = hg / a.ngroups, j0 = (hg - h * a.ngroups) * 8 * NT;
-            const int tile0 = tiles * sub / a.nsub, tile1 = tiles * (sub + 1) / a.nsub;
-            const Scores<NT, SPILL> scores(a, tmem, at.score, warp, nwarps, turn);
-            const float* lse = at.lse + h * GP + j0 + 2 * c;
-            float l[NT][2];
+            const int tile0 = tiles * sub / a.nsub, n = tiles * (sub + 1) / a.nsub - tile0;
+            const Scores<N, SPILL> scores(a, tmem, at.score, warp, nwarps, turn);
+            const float* lse = at.lse + h * GP + j0 + column_head<NT>(c);
+            float l[N][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) l[nt][0] = lse[nt * 8], l[nt][1] = lse[nt * 8 + 1];
-            float* dst = at.scale + hg * a.TS;
-            for (int tile = tile0; tile < tile1; ++tile) {
-                float z[NT][4];
-                scores.load(tile - tile0, z);
-                scores.loaded(z);
-                float w0 = 0.f, w1 = 0.f;  // tokens t_lo and t_lo + 2
+            for (int nt = 0; nt < N; ++nt) l[nt][0] = lse[nt * 8], l[nt][1] = lse[nt * 8 + 1];
+            float* dst = at.scale + hg * a.TS + tile0 * 16;
+            constexpr int AHEAD = N == 1 ? 4 : 2;  // fragments on their way together
+            for (int i0 = 0; i0 < n; i0 += AHEAD * F) {
+                float z[AHEAD][N][4], w0[AHEAD], w1[AHEAD];  // tokens t_lo and t_lo + 2
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    w0 += exp2_fast(z[nt][0] - l[nt][0]) + exp2_fast(z[nt][1] - l[nt][1]);
-                    w1 += exp2_fast(z[nt][2] - l[nt][0]) + exp2_fast(z[nt][3] - l[nt][1]);
+                for (int u = 0; u < AHEAD; ++u) scores.load(min(i0 + u * F, n - 1) / F, z[u]);
+                scores.loaded(z[0]);
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    if (u > 0) scores.loaded(z[u], false);
+                    w0[u] = w1[u] = 0.f;
+#pragma unroll
+                    for (int nt = 0; nt < N; ++nt) {
+                        w0[u] +=
+                            exp2_fast(z[u][nt][0] - l[nt][0]) + exp2_fast(z[u][nt][1] - l[nt][1]);
+                        w1[u] +=
+                            exp2_fast(z[u][nt][2] - l[nt][0]) + exp2_fast(z[u][nt][3] - l[nt][1]);
+                    }
                 }
-                w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
-                w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
-                w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
-                w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-                if (c == 0) {
-                    dst[tile * 16 + t_lo] = w0;
-                    dst[tile * 16 + t_lo + 2] = w1;
+#pragma unroll
+                for (int o = 1; o <= (F == 1 ? 2 : 1); o <<= 1) {
+#pragma unroll
+                    for (int u = 0; u < AHEAD; ++u) {
+                        w0[u] += __shfl_xor_sync(0xffffffffu, w0[u], o);
+                        w1[u] += __shfl_xor_sync(0xffffffffu, w1[u], o);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    const int tile = i0 + u * F + (F == 1 ? 0 : c >> 1);
+                    if (c % (4 / F) == 0 && tile < n) {
+                        dst[tile * 16 + t_lo] = w0[u];
+                        dst[tile * 16 + t_lo + 2] = w1[u];
+                    }
                 }
             }
         }
@@ -493,9 +524,13 @@ __device__ __forceinline__ void finish(const AttendKernelArgs& a, uint8_t* smem,
 template <int CODE, int D, int NT, bool SPILL>
 __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     attend_kernel(const AttendKernelArgs a) {
-    constexpr int STEPS = D / 16;     // of a score: 16 d each
+    constexpr int F = NT == 0 ? 2 : 1;    // tiles of a fragment
+    constexpr int N = NT == 0 ? 1 : NT;   // fragments of a tile
+    constexpr int STEPS = D / 16;         // of a score: 16 d each
     constexpr int COPIES = D / 32;    // 16-byte chunks of a tile per lane
-    constexpr int kHeldScales = 16;   // K and V scales of 8 heads
+    // Entries a thread takes at a time, and their scales held in registers (those of 8 heads);
+    // fewer beside wide queries
+    constexpr int kTurns = D * N > 128 ? 1 : 2, kHeldScales = D * N > 128 ? 4 : 16;
     constexpr int STAGES = attend_stages(D);
     constexpr uint32_t kTile = 16 * D;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -509,7 +544,7 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nthreads = blockDim.x, nwarps = nthreads >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int GP = a.ngroups * 8 * NT;    // padded query heads of a K/V head
+    const int GP = a.ngroups * (NT == 0 ? 4 : 8 * NT);  // padded query heads of a K/V head
     const int HP = a.Hkv * GP;
     const Layout<SPILL> at(a, smem, P, HP, D, nwarps, blockIdx.x);
     int *const t_loc = at.loc, *const t_pos = at.pos, *const t_src = at.src;
@@ -528,14 +563,14 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
 
     const int groups = a.Hkv * a.ngroups;
     const int ntasks = groups * a.nsub;
-    // Queries as the B operand: lane (g, c) holds elements 16 w + 4 c .. + 3 of head g.
-    uint32_t qf[NT][STEPS][2];
-    float factor[NT][2];  // of the scores of heads 2 c and 2 c + 1
+    // Queries as the B operand: lane (g, c) holds elements 16 w + 4 c .. + 3 of head g (g % 4).
+    uint32_t qf[N][STEPS][2];
+    float factor[N][2];  // of the scores of heads 2 c and 2 c + 1
     auto load_q = [&](int task) {
         const int hg = task % groups, h = hg / a.ngroups, j0 = (hg - h * a.ngroups) * 8 * NT;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int j = j0 + nt * 8 + g;
+        for (int nt = 0; nt < N; ++nt) {
+            const int j = j0 + nt * 8 + (NT == 0 ? g & 3 : g);
             const long long from = b * a.q_stride[0] + st * a.q_stride[1] +
                                    (long long)(h * a.G + j) * a.q_stride[2];
             uint32_t raw[2 * STEPS];
@@ -558,36 +593,41 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
                 qf[nt][i >> 1][i & 1] = pack_half2(x.x * up, x.y * up);
             }
             const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
-            factor[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
-            factor[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+            factor[nt][0] = __shfl_sync(0xffffffffu, down, 4 * column_head<NT>(c));
+            factor[nt][1] = __shfl_sync(0xffffffffu, down, 4 * column_head<NT>(c) + 4);
         }
     };
 
+    // The CTA's entries, kTurns * nthreads at a time (all of them, mostly).  The first are under
+    // way while the queries come.
     const long long entry0 = (long long)bs * a.K;
-    // The first turn's entries are under way while the queries come.
-    int loc = -1, t = 0;
-    auto load_entry = [&](int i) {
-        const int j = ((i >> 4) * P + rank) * 16 + (i & 15);
-        loc = -1, t = 0;
-        if (j < a.K) {
-            loc = __ldg(a.locs + entry0 + j);
-            t = __ldg(a.topk + entry0 + j);
+    const int chunks = (a.K + 15) >> 4, own = (chunks - rank + P - 1) / P;
+    const int entries = own * 16 - (own > 0 && (chunks - 1) % P == rank ? chunks * 16 - a.K : 0);
+    auto entry_of = [&](int i) { return ((i >> 4) * P + rank) * 16 + (i & 15); };
+    int loc[kTurns], pos[kTurns];
+    auto load_entries = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            const int i = i0 + u * nthreads + tid;
+            loc[u] = -1, pos[u] = 0;
+            if (i < entries) {
+                loc[u] = __ldg(a.locs + entry0 + entry_of(i));
+                pos[u] = __ldg(a.topk + entry0 + entry_of(i));
+            }
         }
     };
-    load_entry(tid);
+    load_entries(0);
     const int req = __ldg(a.req + b);
     if (warp < ntasks) load_q(warp);
     const bool known = req >= 0 && req < a.R;
-    // The CTA's entries, masked ones dropped.  A thread fetches the scales of its entry as soon
-    // as it has the position, kHeldScales of them into registers.
-    const int chunks = (a.K + 15) >> 4, own = (chunks - rank + P - 1) / P;
-    const int entries = own * 16 - (own > 0 && (chunks - 1) % P == rank ? chunks * 16 - a.K : 0);
+    // Masked entries are dropped.  A thread fetches the scales of its entries as soon as it has
+    // the positions, kHeldScales of each into registers.
     const int per = 2 * a.Hkv;
     const float* scales = a.scales + (long long)(known ? req : 0) * a.NB * per;
-    float x[kHeldScales];
-    int live = 0, at_last = -1;
-    auto fetch_scales = [&](int pos, int ch) {
-        const float* src = scales + (long long)(pos / a.T) * per + ch;
+    float held[kTurns][kHeldScales];
+    int live = 0, at_last[kTurns];
+    auto fetch_scales = [&](float (&x)[kHeldScales], int t, int ch) {
+        const float* src = scales + (long long)a.block.of(t) * per + ch;
 #pragma unroll
         for (int k = 0; k < kHeldScales; k += 4) {
             if (ch + k >= per) break;
@@ -601,35 +641,44 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
             }
         }
     };
-    auto put_scales = [&](int to, int ch) {
+    auto put_scales = [&](const float (&x)[kHeldScales], int to, int ch) {
 #pragma unroll
         for (int k = 0; k < kHeldScales; ++k)
             if (ch + k < per) t_scale[(ch + k) * a.TC + to] = x[k];
     };
-    for (int i0 = 0; i0 < entries; i0 += nthreads) {
-        const int i = i0 + tid;
-        const int j = ((i >> 4) * P + rank) * 16 + (i & 15);
-        if (i0 > 0) load_entry(i);
-        if (i >= entries) {
-            loc = -1;
-        } else if (!known || loc < 0 || loc >= a.num_rows || t < 0 || t >= a.L) {
-            loc = -1;
-            if (a.weights) a.weights[entry0 + j] = 0.f;
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) at_last[u] = -1;
+    for (int i0 = 0; i0 < entries; i0 += kTurns * nthreads) {
+        int row[kTurns], t[kTurns];
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            if (at_last[u] >= 0) put_scales(held[u], at_last[u], 0);  // of the turns before
+            const int i = i0 + u * nthreads + tid;
+            row[u] = known && loc[u] < a.num_rows && pos[u] >= 0 && pos[u] < a.L ? loc[u] : -1;
+            t[u] = pos[u];
+            if (row[u] >= 0)
+                fetch_scales(held[u], t[u], 0);
+            else if (i < entries && a.weights)
+                a.weights[entry0 + entry_of(i)] = 0.f;
         }
-        if (at_last >= 0) put_scales(at_last, 0);
-        if (loc >= 0) fetch_scales(t, 0);
-        int n = __syncthreads_count(loc >= 0);
-        at_last = live + tid;  // in place while no entry is masked
-        if (n != min(nthreads, entries - i0))
-            at_last = live + block_exclusive_scan(loc >= 0, s_scan, &n);
-        if (loc >= 0) {
-            t_loc[at_last] = loc;
-            t_pos[at_last] = t;
-            t_src[at_last] = j;
-        } else {
-            at_last = -1;
+        load_entries(i0 + kTurns * nthreads);  // the next, if any
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            const int left = entries - (i0 + u * nthreads);
+            if (left <= 0) break;
+            int n = __syncthreads_count(row[u] >= 0);
+            int to = live + tid;  // in place while no entry is masked
+            if (n != min(nthreads, left))
+                to = live + block_exclusive_scan(row[u] >= 0, s_scan, &n);
+            at_last[u] = -1;
+            if (row[u] >= 0) {
+                t_loc[to] = row[u];
+                t_pos[to] = t[u];
+                t_src[to] = entry_of(i0 + u * nthreads + tid);
+                at_last[u] = to;
+            }
+            live += n;
         }
-        live += n;
     }
     const int tiles = (live + 15) >> 4;
     __syncthreads();
@@ -654,7 +703,7 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
             const int* l = t_loc + (tile0 + (v ? i - n : i)) * 16;
             const uint32_t tile = queue + stage * kTile;
             int from = lane;
-            if (D * NT > 192) asm volatile("" : "+r"(from));  // offsets computed here, not kept
+            if (D * N > 128) asm volatile("" : "+r"(from));  // offsets computed here, not kept
 #pragma unroll
             for (int k = 0; k < COPIES; ++k) {
                 const int row = (k * 32 + from) / (D / 16), chunk = (k * 32 + from) % (D / 16);
@@ -674,12 +723,14 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     };
     if (warp < ntasks) first_items(warp);  // under way while the scales come
 
-    if (at_last >= 0) put_scales(at_last, 0);
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u)
+        if (at_last[u] >= 0) put_scales(held[u], at_last[u], 0);
     if (per > kHeldScales) {  // the others of many heads
         for (int i = tid; i < live; i += nthreads) {
             for (int ch = kHeldScales; ch < per; ch += kHeldScales) {
-                fetch_scales(t_pos[i], ch);
-                put_scales(i, ch);
+                fetch_scales(held[0], t_pos[i], ch);
+                put_scales(held[0], i, ch);
             }
         }
     }
@@ -691,7 +742,7 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         const int tile0 = tiles * sub / a.nsub, n = tiles * (sub + 1) / a.nsub - tile0;
         const float* sk = t_scale + h * a.TC + tile0 * 16;
         const float* sv = t_scale + (a.Hkv + h) * a.TC + tile0 * 16;
-        const Scores<NT, SPILL> scores(a, tmem, at.score, warp, nwarps, turn);
+        const Scores<N, SPILL> scores(a, tmem, at.score, warp, nwarps, turn);
         if (turn > 0) {
             load_q(task);
             first_items(task);
@@ -714,32 +765,43 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         const int v_row = lane & 15;
 
         // ---- scores --------------------------------------------------------------
-        float top[NT][2];  // of heads 2 c and 2 c + 1
+        float top[N][2];  // of heads 2 c and 2 c + 1
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
-        for (int i = 0; i < n; ++i) {
-            const uint32_t tile = next_item(i);
-            float s[NT][2][4] = {};
+        for (int nt = 0; nt < N; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+        // Columns 0-3 and 4-7 belong to the two tiles of a fragment.
+        const uint32_t own[2] = {F == 1 || g < 4 ? ~0u : 0u, g >= 4 ? ~0u : 0u};
+        for (int i = 0; i < n; i += F) {
+            float s[N][2][4] = {};
 #pragma unroll
-            for (int w = 0; w < STEPS; w += 2) {
-                uint32_t r[4];  // rows t_lo, t_lo + 2 of chunk w, then of chunk w + 1
-                read_matrices(r, tile + chunk_at<D>(k_row, w + (lane >> 4)));
+            for (int f = 0; f < F; ++f) {
+                if (f > 0 && i + f >= n) break;
+                const uint32_t tile = next_item(i + f);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t a0, a1, a2, a3;
-                    halves<CODE>(r[2 * k], a0, a2);
-                    halves<CODE>(r[2 * k + 1], a1, a3);
+                for (int w = 0; w < STEPS; w += 2) {
+                    uint32_t r[4];  // rows t_lo, t_lo + 2 of chunk w, then of chunk w + 1
+                    read_matrices(r, tile + chunk_at<D>(k_row, w + (lane >> 4)));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma(s[nt][k], a0, a1, a2, a3, qf[nt][w + k][0], qf[nt][w + k][1]);
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t a0, a1, a2, a3;
+                        halves<CODE>(r[2 * k], a0, a2);
+                        halves<CODE>(r[2 * k + 1], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < N; ++nt) {
+                            uint32_t b0 = qf[nt][w + k][0], b1 = qf[nt][w + k][1];
+                            if (F == 2) b0 &= own[f], b1 &= own[f];
+                            mma(s[nt][k], a0, a1, a2, a3, b0, b1);
+                        }
+                    }
                 }
             }
-            const int t0 = i * 16 + t_lo;
-            const bool on0 = tile0 * 16 + t0 < live, on1 = tile0 * 16 + t0 + 2 < live;
+            const int mine = F == 1 ? i : i + (c >> 1);  // the tile of this lane's columns
+            const int t0 = (mine < n ? mine : 0) * 16 + t_lo;
+            const bool on0 = mine < n && tile0 * 16 + t0 < live;
+            const bool on1 = mine < n && tile0 * 16 + t0 + 2 < live;
             const float k0 = sk[t0], k1 = sk[t0 + 2];
-            float z[NT][4];
+            float z[N][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float f = factor[nt][k];
@@ -749,25 +811,28 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
                     top[nt][k] = fmaxf(top[nt][k], fmaxf(z[nt][k], z[nt][k + 2]));
                 }
             }
-            scores.store(i, z);
+            scores.store(i / F, z);
         }
 
         // The queries are used up; without this the compiler keeps them for the next turn, which
         // loads its own.
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < N; ++nt)
 #pragma unroll
             for (int w = 0; w < STEPS; ++w) asm("" : "=r"(qf[nt][w][0]), "=r"(qf[nt][w][1]));
 
         // ---- softmax over the task's tokens ----------------------------------------
         scores.stored();
-        float safe[NT][2], sum[NT][2];
+        float safe[N][2], sum[N][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 top[nt][k] = max_over_g(top[nt][k]);
-                if (g == 0) at.max[sub * HP + h * GP + j0 + nt * 8 + 2 * c + k] = top[nt][k];
+                if (F == 2)  // the head's other tiles
+                    top[nt][k] = fmaxf(top[nt][k], __shfl_xor_sync(0xffffffffu, top[nt][k], 2));
+                if (g == 0)
+                    at.max[sub * HP + h * GP + j0 + nt * 8 + column_head<NT>(c) + k] = top[nt][k];
                 safe[nt][k] = top[nt][k] == -INFINITY ? 0.f : top[nt][k];
                 sum[nt][k] = 0.f;
             }
@@ -780,16 +845,17 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         const float inv = ref > 0.f ? 1.f / ref : 0.f;
 
         // ---- values --------------------------------------------------------------
-        float o[STEPS][NT][4] = {};
-        for (int i = 0; i < n; ++i) {
-            float z[NT][4];
-            scores.load(i, z);
-            const float v0 = sv[i * 16 + t_lo] * inv, v1 = sv[i * 16 + t_lo + 2] * inv;
-            const uint32_t tile = next_item(n + i);
+        float o[STEPS][N][4] = {};
+        for (int i = 0; i < n; i += F) {
+            float z[N][4];
+            scores.load(i / F, z);
+            const int mine = F == 1 ? i : i + (c >> 1) < n ? i + (c >> 1) : i;
+            const float v0 = sv[mine * 16 + t_lo] * inv, v1 = sv[mine * 16 + t_lo + 2] * inv;
+            uint32_t tile = next_item(n + i);
             scores.loaded(z);
-            uint32_t pf[NT][2];
+            uint32_t pf[N][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < N; ++nt) {
                 const float p0 = exp2_fast(z[nt][0] - safe[nt][0]);
                 const float p1 = exp2_fast(z[nt][1] - safe[nt][1]);
                 const float p2 = exp2_fast(z[nt][2] - safe[nt][0]);
@@ -800,44 +866,62 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
                 pf[nt][1] = transpose(pack_half2(p2 * v1, p3 * v1));
             }
 #pragma unroll
-            for (int w = 0; w < STEPS; w += 2) {
-                uint32_t r[4];  // d = g, g + 8 of chunk w, then of chunk w + 1; four tokens each
-                read_transposed(r, tile + chunk_at<D>(v_row, w + (lane >> 4)));
+            for (int f = 0; f < F; ++f) {
+                if (f > 0 && i + f >= n) break;
+                if (f > 0) tile = next_item(n + i + f);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t a0, a1, a2, a3;
-                    halves<CODE>(r[2 * k], a0, a2);
-                    halves<CODE>(r[2 * k + 1], a1, a3);
+                for (int w = 0; w < STEPS; w += 2) {
+                    // d = g, g + 8 of chunk w, then of chunk w + 1; four tokens each
+                    uint32_t r[4];
+                    read_transposed(r, tile + chunk_at<D>(v_row, w + (lane >> 4)));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma(o[w + k][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t a0, a1, a2, a3;
+                        halves<CODE>(r[2 * k], a0, a2);
+                        halves<CODE>(r[2 * k + 1], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < N; ++nt) {
+                            uint32_t b0 = pf[nt][0], b1 = pf[nt][1];
+                            if (F == 2) b0 &= own[f], b1 &= own[f];
+                            mma(o[w + k][nt], a0, a1, a2, a3, b0, b1);
+                        }
+                    }
                 }
             }
+        }
+        if constexpr (F == 2) {  // both tiles' columns of a head
+#pragma unroll
+            for (int w = 0; w < STEPS; ++w)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[w][0][k] += __shfl_xor_sync(0xffffffffu, o[w][0][k], 2);
         }
         int ranks = P;  // the layout anew, so that it takes no registers through the loops
         asm("" : "+r"(ranks));
         const Layout<SPILL> done(a, smem, ranks, HP, D, nwarps, blockIdx.x);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 sum[nt][k] = sum_over_g(sum[nt][k]);
+                if (F == 2) sum[nt][k] += __shfl_xor_sync(0xffffffffu, sum[nt][k], 2);
                 if (g == 0)
-                    done.sum[sub * HP + h * GP + j0 + nt * 8 + 2 * c + k] = sum[nt][k];
+                    done.sum[sub * HP + h * GP + j0 + nt * 8 + column_head<NT>(c) + k] =
+                        sum[nt][k];
             }
         }
         // The outputs may take the queues' place: then every warp has one task, and all are done
         // with their queues here.  Several parts of a slice have one task a warp too; their
         // outputs are added in order, relative to their common maximum.
         if (a.alias || a.nsub > 1) __syncthreads();
-        float fold[NT][2];
+        float fold[N][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 fold[nt][k] = ref;
                 if (a.nsub > 1) {
-                    const int to = h * GP + j0 + nt * 8 + 2 * c + k;
+                    const int to = h * GP + j0 + nt * 8 + column_head<NT>(c) + k;
                     float m = -INFINITY;
                     for (int u = 0; u < a.nsub; ++u) m = fmaxf(m, done.max[u * HP + to]);
                     fold[nt][k] *=
@@ -848,11 +932,11 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         for (int u = 0; u < a.nsub; ++u) {
             if (u == sub) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int j = j0 + nt * 8 + 2 * c + k;
-                        if (j >= a.G) continue;
+                        if (j >= a.G || (F == 2 && c > 1)) continue;
                         const float f = fold[nt][k];
                         float* row = done.out + (h * a.G + j) * (D + 4) + g;
 #pragma unroll
@@ -891,34 +975,43 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     }
 }
 
+// Opens the kernel to the shape and fills its launch configuration.
 template <int CODE, int D, int NT, bool SPILL>
-cudaError_t run_one(const AttendShape& sh, cudaStream_t s) {
+cudaError_t configure(int P, int clusters, int threads, size_t smem, cudaStream_t s,
+                      cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr) {
     static SmemOptIn opt;
     auto* kernel = attend_kernel<CODE, D, NT, SPILL>;
-    cudaError_t e = ensure_smem(kernel, sh.smem, &opt);
-    if (e != cudaSuccess) return e;
-    if (sh.P > 8) {
+    cudaError_t e = ensure_smem(kernel, smem, &opt);
+    if (e == cudaSuccess && P > 8)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sh.a.B * sh.a.S * sh.P);
-    cfg.blockDim = dim3(sh.threads);
-    cfg.dynamicSmemBytes = sh.smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cfg->gridDim = dim3(clusters * P);
+    cfg->blockDim = dim3(threads);
+    cfg->dynamicSmemBytes = smem;
+    cfg->stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = sh.P;
+    attr[0].val.clusterDim.x = P;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, sh.a);
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+    return e;
+}
+
+template <int CODE, int D, int NT, bool SPILL>
+cudaError_t run_one(const AttendShape& sh, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    const cudaError_t e = configure<CODE, D, NT, SPILL>(sh.P, sh.a.B * sh.a.S, sh.threads, sh.smem,
+                                                        s, &cfg, attr);
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, attend_kernel<CODE, D, NT, SPILL>, sh.a);
 }
 
 template <int CODE, int D>
 cudaError_t run_dim(const AttendShape& sh, cudaStream_t s) {
     if (sh.spill) return run_one<CODE, D, 1, true>(sh, s);
+    if constexpr (D <= 192)
+        if (sh.nt == 0) return run_one<CODE, D, 0, false>(sh, s);
     if constexpr (D <= 128)
         if (sh.nt == 2) return run_one<CODE, D, 2, false>(sh, s);
     return run_one<CODE, D, 1, false>(sh, s);

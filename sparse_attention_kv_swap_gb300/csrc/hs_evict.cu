@@ -235,53 +235,62 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
     if (k > 0) cluster.sync();  // no CTA leaves while another reads its counts
 }
 
-// One CTA per request; the steps follow one another (a barrier between them
-// orders the additions), so that a token selected in several steps is added to
-// in step order.  Up to kHeldSteps steps of 2 * 1024 entries are fetched before
-// the first addition; longer calls take the steps one by one.
-constexpr int kAccumulateThreads = 1024;
-constexpr int kHeldSteps = 4, kHeldEntries = 2;
+// A cluster of 4 CTAs per request (additions to scattered words leave an SM one at a time, so
+// they are spread); the steps follow one another, a cluster barrier between them ordering the
+// additions, so that a token selected in several steps is added to in step order.  Up to
+// kHeldSteps steps of kHeldEntries entries a thread are fetched before the first addition, the
+// positions even before the kernel that computes the weights has ended.
+constexpr int kAccumulateThreads = 512, kAccumulateCluster = 4;
+constexpr int kHeldSteps = 4, kHeldEntries = 4;
 
 __global__ void __launch_bounds__(kAccumulateThreads)
     accumulate_kernel(const float* weights, const int32_t* topk, const int32_t* req,
                       const int32_t* counts, int32_t S, int32_t K, float* acc, int32_t R,
                       int32_t L) {
-    const int b = blockIdx.x, tid = threadIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the weights of the kernel before
+    constexpr int kAll = kAccumulateThreads * kAccumulateCluster;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int b = blockIdx.x / kAccumulateCluster;
+    const int first = (int)cluster.block_rank() * kAccumulateThreads + threadIdx.x;
     const int q = __ldg(req + b);
-    if (q < 0 || q >= R) return;
-    const int steps = counts ? min(__ldg(counts + b), S) : S;
-    float* dst = acc + (long long)q * L;
+    const int steps = q < 0 || q >= R ? 0 : counts ? min(__ldg(counts + b), S) : S;
+    float* dst = acc + (long long)(steps > 0 ? q : 0) * L;
     const long long row = (long long)b * S * K;
-    if (K <= kHeldEntries * kAccumulateThreads && steps <= kHeldSteps) {
+    if (K <= kHeldEntries * kAll && steps <= kHeldSteps) {
         int t[kHeldSteps][kHeldEntries];
         float w[kHeldSteps][kHeldEntries];
 #pragma unroll
-        for (int s = 0; s < kHeldSteps; ++s) {
+        for (int s = 0; s < kHeldSteps; ++s)
+#pragma unroll
+            for (int i = 0; i < kHeldEntries; ++i)
+                t[s][i] = s < steps && first + i * kAll < K
+                              ? __ldg(topk + row + s * K + first + i * kAll)
+                              : -1;
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // for the weights
+#pragma unroll
+        for (int s = 0; s < kHeldSteps; ++s)
 #pragma unroll
             for (int i = 0; i < kHeldEntries; ++i) {
-                const int j = tid + i * kAccumulateThreads;
-                t[s][i] = s < steps && j < K ? __ldg(topk + row + s * K + j) : -1;
-                w[s][i] = s < steps && j < K ? __ldg(weights + row + s * K + j) : 0.f;
+                if (t[s][i] >= L) t[s][i] = -1;
+                w[s][i] = t[s][i] >= 0 ? __ldg(weights + row + s * K + first + i * kAll) : 0.f;
             }
-        }
 #pragma unroll
         for (int s = 0; s < kHeldSteps; ++s) {
             if (s >= steps) break;
+            if (s > 0) cluster.sync();
 #pragma unroll
             for (int i = 0; i < kHeldEntries; ++i)
-                if (t[s][i] >= 0 && t[s][i] < L) atomicAdd(dst + t[s][i], w[s][i]);
-            __syncthreads();
+                if (t[s][i] >= 0) atomicAdd(dst + t[s][i], w[s][i]);
         }
         return;
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int s = 0; s < steps; ++s) {
+        if (s > 0) cluster.sync();
 #pragma unroll 4
-        for (int j = tid; j < K; j += kAccumulateThreads) {
+        for (int j = first; j < K; j += kAll) {
             const int t = __ldg(topk + row + (long long)s * K + j);
             if (t >= 0 && t < L) atomicAdd(dst + t, __ldg(weights + row + (long long)s * K + j));
         }
-        __syncthreads();
     }
 }
 
@@ -292,14 +301,18 @@ cudaError_t launch_accumulate(const float* weights, const int32_t* topk, const i
                               int32_t R, int32_t L, cudaStream_t s) {
     // May be launched while the kernel before it (hs_attend's) ends.
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(B);
+    cfg.gridDim = dim3(B * kAccumulateCluster);
     cfg.blockDim = dim3(kAccumulateThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kAccumulateCluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, accumulate_kernel, weights, topk, req, counts, S, K, acc, R, L);
 }
 

@@ -158,7 +158,7 @@ int hs_accumulate(const float* weights_dev, const int32_t* topk_dev, const int32
                   float* acc_dev, int32_t num_requests, int32_t max_seq_len, void* stream) {
     if (batch < 0 || num_steps < 1 || top_k < 0 || num_requests < 1 || max_seq_len < 1)
         return HS_ERR_INVALID_ARG;
-    if (top_k > (1 << 22)) return HS_ERR_UNSUPPORTED;
+    if (top_k > (1 << 22) || (long long)batch * 4 > kMaxCtas) return HS_ERR_UNSUPPORTED;
     if (batch == 0 || top_k == 0) return HS_OK;
     if (!weights_dev || !topk_dev || !req_dev || !acc_dev) return HS_ERR_INVALID_ARG;
     if (!aligned(weights_dev, 4) || !aligned(topk_dev, 4) || !aligned(req_dev, 4) ||
