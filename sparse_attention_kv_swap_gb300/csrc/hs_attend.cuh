@@ -30,7 +30,7 @@
 //      11 bits.
 // With 4 query heads to a K/V head or fewer, one fragment takes two tiles: the
 // 8 columns are the heads of the first tile and again those of the second, the
-// queries lying in columns 0-3 for one product and 4-7 for the other.  Scores,
+// queries lying in both halves, and each lane keeping its tile's product.  Scores,
 // exponentials and tensor memory then halve (NT = 0 below).
 // Then the CTAs of the cluster exchange maxima and sums over distributed
 // shared memory, each adds up a share of the output over the CTAs in rank
@@ -100,7 +100,7 @@ constexpr int attend_warps(int D, bool spill) { return D > 192 && spill ? 8 : 16
 // Tiles in a warp's queue (16 * D bytes each): all but one are on their way
 // while one is used.
 constexpr int attend_stages(int D) {
-    return D <= 64 ? 8 : (D <= 96 ? 5 : (D <= 128 ? 4 : 3));
+    return D <= 32 ? 8 : (D <= 64 ? 6 : (D <= 96 ? 5 : (D <= 128 ? 4 : 3)));
 }
 
 #ifdef __CUDACC__
@@ -373,8 +373,7 @@ __device__ __forceinline__ void finish(const AttendKernelArgs& a, uint8_t* smem,
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(P));
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(block));
-    // hs_accumulate's kernel may take the SMs that become free.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    release_next();
     const int tid = threadIdx.x, nthreads = blockDim.x;
     const Layout<SPILL> at(a, smem, P, HP, D, nthreads >> 5, block);
     const int bs = block / P, b = bs / a.S, st = bs - b * a.S;
@@ -561,6 +560,7 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     }
 
+    wait_for_previous();
     const int groups = a.Hkv * a.ngroups;
     const int ntasks = groups * a.nsub;
     // Queries as the B operand: lane (g, c) holds elements 16 w + 4 c .. + 3 of head g (g % 4).
@@ -771,11 +771,12 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         // Columns 0-3 and 4-7 belong to the two tiles of a fragment.
         const uint32_t own[2] = {F == 1 || g < 4 ? ~0u : 0u, g >= 4 ? ~0u : 0u};
         for (int i = 0; i < n; i += F) {
-            float s[N][2][4] = {};
+            float z[N][4];  // the products, then the scores
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 if (f > 0 && i + f >= n) break;
                 const uint32_t tile = next_item(i + f);
+                float s[N][2][4] = {};
 #pragma unroll
                 for (int w = 0; w < STEPS; w += 2) {
                     uint32_t r[4];  // rows t_lo, t_lo + 2 of chunk w, then of chunk w + 1
@@ -786,28 +787,28 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
                         halves<CODE>(r[2 * k], a0, a2);
                         halves<CODE>(r[2 * k + 1], a1, a3);
 #pragma unroll
-                        for (int nt = 0; nt < N; ++nt) {
-                            uint32_t b0 = qf[nt][w + k][0], b1 = qf[nt][w + k][1];
-                            if (F == 2) b0 &= own[f], b1 &= own[f];
-                            mma(s[nt][k], a0, a1, a2, a3, b0, b1);
-                        }
+                        for (int nt = 0; nt < N; ++nt)
+                            mma(s[nt][k], a0, a1, a2, a3, qf[nt][w + k][0], qf[nt][w + k][1]);
                     }
                 }
+#pragma unroll
+                for (int nt = 0; nt < N; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (f == 0 || c >> 1 == f) z[nt][k] = s[nt][0][k] + s[nt][1][k];
             }
             const int mine = F == 1 ? i : i + (c >> 1);  // the tile of this lane's columns
             const int t0 = (mine < n ? mine : 0) * 16 + t_lo;
             const bool on0 = mine < n && tile0 * 16 + t0 < live;
             const bool on1 = mine < n && tile0 * 16 + t0 + 2 < live;
             const float k0 = sk[t0], k1 = sk[t0 + 2];
-            float z[N][4];
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float f = factor[nt][k];
-                    z[nt][k] = on0 ? (s[nt][0][k] + s[nt][1][k]) * (k0 * f) : -INFINITY;
-                    z[nt][k + 2] =
-                        on1 ? (s[nt][0][k + 2] + s[nt][1][k + 2]) * (k1 * f) : -INFINITY;
+                    z[nt][k] = on0 ? z[nt][k] * (k0 * f) : -INFINITY;
+                    z[nt][k + 2] = on1 ? z[nt][k + 2] * (k1 * f) : -INFINITY;
                     top[nt][k] = fmaxf(top[nt][k], fmaxf(z[nt][k], z[nt][k + 2]));
                 }
             }
@@ -975,36 +976,22 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     }
 }
 
-// Opens the kernel to the shape and fills its launch configuration.
+// Opens the kernel to shared memory of this size and to clusters of P.
 template <int CODE, int D, int NT, bool SPILL>
-cudaError_t configure(int P, int clusters, int threads, size_t smem, cudaStream_t s,
-                      cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr) {
+cudaError_t open_kernel(int P, size_t smem) {
     static SmemOptIn opt;
     auto* kernel = attend_kernel<CODE, D, NT, SPILL>;
-    cudaError_t e = ensure_smem(kernel, smem, &opt);
-    if (e == cudaSuccess && P > 8)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    cfg->gridDim = dim3(clusters * P);
-    cfg->blockDim = dim3(threads);
-    cfg->dynamicSmemBytes = smem;
-    cfg->stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = P;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg->attrs = attr;
-    cfg->numAttrs = 1;
-    return e;
+    const cudaError_t e = ensure_smem(kernel, smem, &opt);
+    if (e != cudaSuccess || P <= 8) return e;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 template <int CODE, int D, int NT, bool SPILL>
 cudaError_t run_one(const AttendShape& sh, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    const cudaError_t e = configure<CODE, D, NT, SPILL>(sh.P, sh.a.B * sh.a.S, sh.threads, sh.smem,
-                                                        s, &cfg, attr);
+    const cudaError_t e = open_kernel<CODE, D, NT, SPILL>(sh.P, sh.smem);
     if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&cfg, attend_kernel<CODE, D, NT, SPILL>, sh.a);
+    return launch_chained(attend_kernel<CODE, D, NT, SPILL>, sh.a.B * sh.a.S * sh.P, sh.threads,
+                          sh.smem, sh.P, s, sh.a);
 }
 
 template <int CODE, int D>

@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
     const int rank = (int)cluster.block_rank();
     const int b = blockIdx.x / P;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    wait_for_previous();
+    release_next();
     const int q = __ldg(a.req + b);
     int n = __ldg(a.seq_lens + b);
     n = q < 0 || q >= a.R || n < 0 ? 0 : min(n, a.L);
@@ -251,6 +253,8 @@ __global__ void __launch_bounds__(kAccumulateThreads)
     cg::cluster_group cluster = cg::this_cluster();
     const int b = blockIdx.x / kAccumulateCluster;
     const int first = (int)cluster.block_rank() * kAccumulateThreads + threadIdx.x;
+    // The positions may be read early: the kernel before is hs_attend's, which reads them too, or
+    // one that does not let this one go before it ends.
     const int q = __ldg(req + b);
     const int steps = q < 0 || q >= R ? 0 : counts ? min(__ldg(counts + b), S) : S;
     float* dst = acc + (long long)(steps > 0 ? q : 0) * L;
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(kAccumulateThreads)
                 t[s][i] = s < steps && first + i * kAll < K
                               ? __ldg(topk + row + s * K + first + i * kAll)
                               : -1;
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // for the weights
+        wait_for_previous();  // for the weights
 #pragma unroll
         for (int s = 0; s < kHeldSteps; ++s)
 #pragma unroll
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(kAccumulateThreads)
         }
         return;
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     for (int s = 0; s < steps; ++s) {
         if (s > 0) cluster.sync();
 #pragma unroll 4
@@ -299,21 +303,8 @@ __global__ void __launch_bounds__(kAccumulateThreads)
 cudaError_t launch_accumulate(const float* weights, const int32_t* topk, const int32_t* req,
                               const int32_t* counts, int32_t B, int32_t S, int32_t K, float* acc,
                               int32_t R, int32_t L, cudaStream_t s) {
-    // May be launched while the kernel before it (hs_attend's) ends.
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(B * kAccumulateCluster);
-    cfg.blockDim = dim3(kAccumulateThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kAccumulateCluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, accumulate_kernel, weights, topk, req, counts, S, K, acc, R, L);
+    return launch_chained(accumulate_kernel, B * kAccumulateCluster, kAccumulateThreads, 0,
+                          kAccumulateCluster, s, weights, topk, req, counts, S, K, acc, R, L);
 }
 
 cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* seq_lens, int32_t B,
@@ -336,21 +327,11 @@ cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* se
     while (P < kMaxEvictCluster && L / P > kHeld) P *= 2;
     const long long chunks = ((long long)L + kChunk - 1) / kChunk;
     const int per_warp = (int)((chunks + P * kEvictWarps - 1) / (P * kEvictWarps));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(B * P);
-    cfg.blockDim = dim3(kEvictThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = P;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (per_warp <= 1) return cudaLaunchKernelEx(&cfg, evict_kernel<1>, a);
-    if (per_warp <= 2) return cudaLaunchKernelEx(&cfg, evict_kernel<2>, a);
-    if (per_warp <= kMaxChunks) return cudaLaunchKernelEx(&cfg, evict_kernel<kMaxChunks>, a);
-    return cudaLaunchKernelEx(&cfg, evict_kernel<0>, a);
+    auto* kernel = per_warp <= 1            ? evict_kernel<1>
+                   : per_warp <= 2          ? evict_kernel<2>
+                   : per_warp <= kMaxChunks ? evict_kernel<kMaxChunks>
+                                            : evict_kernel<0>;
+    return launch_chained(kernel, B * P, kEvictThreads, 0, P, s, a);
 }
 
 }  // namespace hs

@@ -80,6 +80,37 @@ cudaError_t launch_attend(const hs_kv_format& f, const hs_attend_args& a, cudaSt
 // ---- device helpers ---------------------------------------------------------
 #ifdef __CUDACC__
 
+// The kernels of these calls run one after the other on a stream, some for a few microseconds:
+// each may be launched while the one before it still runs (launch_chained) and waits for its
+// end, memory included, before it touches any (wait_for_previous).  The next one's launch is
+// let go as soon as all CTAs of this one run (release_next).
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void release_next() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), int grid, int block, size_t smem, int cluster,
+                           cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
 // Four codes as two pairs of f16 (e4m3).

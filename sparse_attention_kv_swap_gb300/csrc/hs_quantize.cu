@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kMaxThreads, CACHE ? 1 : 2) quantize_kernel(co
     const int ch = blockIdx.x % (2 * heads);
     const int win = blockIdx.x / (2 * heads) % a.windows;
     const int b = blockIdx.x / (2 * heads) / a.windows;
+    wait_for_previous();
     const int q = __ldg(a.req + b), start = __ldg(a.start + b), count = __ldg(a.count + b);
     if (q < 0 || q >= a.R || start < 0 || count < 0 || count > a.max_count ||
         start > a.L - count) {
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(512, 2) compact_kernel(const CompactArgs a) {
     const int ch = blockIdx.x % (2 * heads);
     const int win = blockIdx.x / (2 * heads) % a.windows;
     const int b = blockIdx.x / (2 * heads) / a.windows;
+    wait_for_previous();
     const int sq = __ldg(a.src_req + b), dq = __ldg(a.dst_req + b);
     int kept = __ldg(a.kept + b);
     if (sq < 0 || sq >= a.src_R || dq < 0 || dq >= a.dst_R) return;
@@ -374,13 +376,12 @@ __global__ void __launch_bounds__(512, 2) compact_kernel(const CompactArgs a) {
 }
 
 template <int CODE, bool CACHE>
-void quantize_dtype(const QuantizeArgs& a, int grid, int threads, cudaStream_t s) {
+cudaError_t quantize_dtype(const QuantizeArgs& a, int grid, int threads, cudaStream_t s) {
     if (a.in.dtype == HS_DTYPE_BF16)
-        quantize_kernel<CODE, HS_DTYPE_BF16, CACHE><<<grid, threads, 0, s>>>(a);
-    else if (a.in.dtype == HS_DTYPE_FP16)
-        quantize_kernel<CODE, HS_DTYPE_FP16, CACHE><<<grid, threads, 0, s>>>(a);
-    else
-        quantize_kernel<CODE, HS_DTYPE_FP32, CACHE><<<grid, threads, 0, s>>>(a);
+        return launch_chained(quantize_kernel<CODE, HS_DTYPE_BF16, CACHE>, grid, threads, 0, 0, s, a);
+    if (a.in.dtype == HS_DTYPE_FP16)
+        return launch_chained(quantize_kernel<CODE, HS_DTYPE_FP16, CACHE>, grid, threads, 0, 0, s, a);
+    return launch_chained(quantize_kernel<CODE, HS_DTYPE_FP32, CACHE>, grid, threads, 0, 0, s, a);
 }
 
 bool grid_of(long long ctas, int* grid) {
@@ -404,18 +405,11 @@ cudaError_t launch_quantize(QuantizeArgs a, bool cache, cudaStream_t s) {
         return cudaErrorInvalidConfiguration;
     const int parts = a.f.head_dim / 16;
     const int threads = group_threads(a.max_count < T ? a.max_count : T, parts);
-    if (a.f.code == HS_KV_E4M3) {
-        if (cache)
-            quantize_dtype<HS_KV_E4M3, true>(a, grid, threads, s);
-        else
-            quantize_dtype<HS_KV_E4M3, false>(a, grid, threads, s);
-    } else {
-        if (cache)
-            quantize_dtype<HS_KV_INT8, true>(a, grid, threads, s);
-        else
-            quantize_dtype<HS_KV_INT8, false>(a, grid, threads, s);
-    }
-    return cudaGetLastError();
+    if (a.f.code == HS_KV_E4M3)
+        return cache ? quantize_dtype<HS_KV_E4M3, true>(a, grid, threads, s)
+                     : quantize_dtype<HS_KV_E4M3, false>(a, grid, threads, s);
+    return cache ? quantize_dtype<HS_KV_INT8, true>(a, grid, threads, s)
+                 : quantize_dtype<HS_KV_INT8, false>(a, grid, threads, s);
 }
 
 cudaError_t launch_compact(CompactArgs a, cudaStream_t s) {
@@ -428,11 +422,9 @@ cudaError_t launch_compact(CompactArgs a, cudaStream_t s) {
     a.block = Divisor::by(T);
     const int parts = a.f.head_dim / 16;
     const int threads = group_threads(most < T ? most : T, parts);
-    if (a.f.code == HS_KV_E4M3)
-        compact_kernel<HS_KV_E4M3><<<grid, threads, 0, s>>>(a);
-    else
-        compact_kernel<HS_KV_INT8><<<grid, threads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_chained(
+        a.f.code == HS_KV_E4M3 ? compact_kernel<HS_KV_E4M3> : compact_kernel<HS_KV_INT8>, grid,
+        threads, 0, 0, s, a);
 }
 
 }  // namespace hs
