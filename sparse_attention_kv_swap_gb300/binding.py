@@ -628,16 +628,17 @@ def _raw_stream(stream, device) -> int:
     return stream.cuda_stream
 
 
-def _call(fn, where, device, *args) -> None:
+def _run(name, device, *args) -> None:
     """Calls the library with `device` current and raises on an error code."""
     import torch
+    fn = getattr(_lib or load_library(), name)
     if torch._C._cuda_getDevice() == device:
         rc = fn(*args)
     else:
         with torch.cuda.device(device):
             rc = fn(*args)
     if rc != HS_OK:
-        raise HsError(rc, where)
+        raise HsError(rc, name)
 
 
 def _dtype_code(t, name, allow_fp32: bool) -> int:
@@ -654,27 +655,35 @@ def _dtype_code(t, name, allow_fp32: bool) -> int:
 
 
 def _kv_input(fmt, k, v, req, start, count, device):
-    if k.dim() != 4 or k.shape[2] != fmt.num_kv_heads or k.shape[3] != fmt.head_dim:
+    """The packed hs_kv_input, batch and tokens."""
+    shape = k.shape
+    if len(shape) != 4 or shape[2] != fmt.num_kv_heads or shape[3] != fmt.head_dim:
         raise ValueError("k must be [batch, tokens, %d, %d], got %s"
-                         % (fmt.num_kv_heads, fmt.head_dim, tuple(k.shape)))
-    _shape(v, k.shape, "v")
+                         % (fmt.num_kv_heads, fmt.head_dim, tuple(shape)))
+    if v.shape != shape:
+        _shape(v, shape, "v")
     if v.dtype is not k.dtype:
         raise ValueError("k and v must have one dtype")
-    B = k.shape[:1]
-    _shape(req, B, "req")
-    _shape(start, B, "start")
-    _shape(count, B, "count")
-    return _KV_INPUT.pack(_sptr(k, "k", device), _sptr(v, "v", device),
-                          _dtype_code(k, "k", True), *k.stride()[:3], *v.stride()[:3])
+    B = shape[:1]
+    if req.shape != B or start.shape != B or count.shape != B:
+        _shape(req, B, "req")
+        _shape(start, B, "start")
+        _shape(count, B, "count")
+    ka, kb, kc, _ = k.stride()
+    va, vb, vc, _ = v.stride()
+    return _KV_INPUT.pack(_sptr(k, "k", device), _sptr(v, "v", device), _dtype_code(k, "k", True),
+                          ka, kb, kc, va, vb, vc), B[0], shape[1]
 
 
 def _store(fmt, rows, scales, name):
     """(requests, tokens) of a store of rows [requests, tokens, W] and its scales."""
-    if rows.dim() != 3 or rows.shape[2] != fmt.item_size_bytes:
+    shape = rows.shape
+    if len(shape) != 3 or shape[2] != fmt.item_size_bytes:
         raise ValueError("%srows must be [requests, tokens, %d], got %s"
-                         % (name, fmt.item_size_bytes, tuple(rows.shape)))
-    R, L, _ = rows.shape
-    _shape(scales, fmt.scales_shape(R, L), name + "scales")
+                         % (name, fmt.item_size_bytes, tuple(shape)))
+    R, L, _ = shape
+    if scales.shape != (R, -(-L // fmt.block_tokens), 2, fmt.num_kv_heads):
+        _shape(scales, fmt.scales_shape(R, L), name + "scales")
     return R, L
 
 
@@ -686,12 +695,11 @@ def hs_quantize_kv(fmt: HsKvFormat, k, v, req, start, count, rows, scales, strea
     import torch
     R, L = _store(fmt, rows, scales, "")
     i32, dev = torch.int32, k.get_device()
-    inp = _kv_input(fmt, k, v, req, start, count, dev)
-    _call((_lib or load_library()).hs_quantize_kv, "hs_quantize_kv", dev, fmt, inp,
-          _ptr(req, i32, "req", dev), _ptr(start, i32, "start", dev),
-          _ptr(count, i32, "count", dev), k.shape[0], k.shape[1],
-          _ptr(rows, torch.uint8, "rows", dev), _ptr(scales, torch.float32, "scales", dev), R, L,
-          _raw_stream(stream, dev))
+    inp, B, M = _kv_input(fmt, k, v, req, start, count, dev)
+    _run("hs_quantize_kv", dev, fmt, inp, _ptr(req, i32, "req", dev),
+         _ptr(start, i32, "start", dev), _ptr(count, i32, "count", dev), B, M,
+         _ptr(rows, torch.uint8, "rows", dev), _ptr(scales, torch.float32, "scales", dev), R, L,
+         _raw_stream(stream, dev))
 
 
 def hs_append_kv(handle: StateHandle, layer_id: int, fmt: HsKvFormat, k, v, req, start, count,
@@ -702,11 +710,10 @@ def hs_append_kv(handle: StateHandle, layer_id: int, fmt: HsKvFormat, k, v, req,
     cfg = handle.cfg
     _shape(scales, fmt.scales_shape(cfg.num_requests, cfg.max_seq_len), "scales")
     i32, dev = torch.int32, handle.device
-    inp = _kv_input(fmt, k, v, req, start, count, dev)
-    _call((_lib or load_library()).hs_append_kv, "hs_append_kv", dev, handle.ptr, layer_id, fmt,
-          inp, _ptr(req, i32, "req", dev), _ptr(start, i32, "start", dev),
-          _ptr(count, i32, "count", dev), k.shape[0], k.shape[1],
-          _ptr(scales, torch.float32, "scales", dev), _raw_stream(stream, dev))
+    inp, B, M = _kv_input(fmt, k, v, req, start, count, dev)
+    _run("hs_append_kv", dev, handle.ptr, layer_id, fmt, inp, _ptr(req, i32, "req", dev),
+         _ptr(start, i32, "start", dev), _ptr(count, i32, "count", dev), B, M,
+         _ptr(scales, torch.float32, "scales", dev), _raw_stream(stream, dev))
 
 
 def hs_attend_workspace_bytes(fmt: HsKvFormat, batch: int, steps: int, top_k: int,
@@ -728,40 +735,45 @@ def hs_attend(fmt: HsKvFormat, q, rows, locs, topk, req, scales, max_seq_len: in
     as q, lse fp32 [batch, steps, heads], weights fp32 [batch, steps, top_k], acc fp32
     [R, max_seq_len] added to.  sm_scale: 1 / sqrt(D) by default."""
     import torch
-    W = fmt.item_size_bytes
-    if q.dim() != 4 or q.shape[3] != fmt.head_dim:
+    W, shape, sel = fmt.item_size_bytes, q.shape, topk.shape
+    if len(shape) != 4 or shape[3] != fmt.head_dim:
         raise ValueError("q must be [batch, steps, heads, %d], got %s"
-                         % (fmt.head_dim, tuple(q.shape)))
-    B, S, H, D = q.shape
-    if topk.dim() != 3 or topk.shape[:2] != (B, S):
-        raise ValueError("topk must be [%d, %d, top_k], got %s" % (B, S, tuple(topk.shape)))
-    K = topk.shape[2]
+                         % (fmt.head_dim, tuple(shape)))
+    B, S, H, D = shape
+    if len(sel) != 3 or sel[0] != B or sel[1] != S:
+        raise ValueError("topk must be [%d, %d, top_k], got %s" % (B, S, tuple(sel)))
     if out.dtype is not q.dtype:
         raise ValueError("out must have q's dtype")
-    _shape(out, q.shape, "out")
-    _shape(locs, topk.shape, "locs")
-    _shape(req, (B,), "req")
-    if scales.dim() != 4:
-        raise ValueError("scales must be [requests, blocks, 2, heads]")
-    R = scales.shape[0]
-    _shape(scales, fmt.scales_shape(R, max_seq_len), "scales")
-    _shape(lse, (B, S, H), "lse")
-    _shape(weights, topk.shape, "weights")
-    _shape(acc, (R, max_seq_len), "acc")
+    R = scales.shape[0] if scales.dim() else 0
+    if (out.shape != shape or locs.shape != sel or req.shape != shape[:1]
+            or scales.shape != (R, -(-max_seq_len // fmt.block_tokens), 2, fmt.num_kv_heads)):
+        _shape(out, shape, "out")
+        _shape(locs, sel, "locs")
+        _shape(req, (B,), "req")
+        if scales.dim() != 4:
+            raise ValueError("scales must be [requests, blocks, 2, heads]")
+        _shape(scales, fmt.scales_shape(R, max_seq_len), "scales")
+    if lse is not None and lse.shape != shape[:3]:
+        _shape(lse, (B, S, H), "lse")
+    if weights is not None and weights.shape != sel:
+        _shape(weights, sel, "weights")
+    if acc is not None and acc.shape != (R, max_seq_len):
+        _shape(acc, (R, max_seq_len), "acc")
     if rows.shape[-1] != W:
         raise ValueError("rows must be %d bytes wide" % W)
     i32, f32, dev = torch.int32, torch.float32, q.get_device()
+    qa, qb, qc, _ = q.stride()
+    oa, ob, oc, _ = out.stride()
     args = _ATTEND_ARGS.pack(
-        _sptr(q, "q", dev), _sptr(out, "out", dev), _dtype_code(q, "q", False), B, S, K, H, R,
-        max_seq_len, D ** -0.5 if sm_scale is None else sm_scale, *q.stride()[:3],
-        *out.stride()[:3], _ptr(rows, torch.uint8, "rows", dev), rows.numel() // W,
+        _sptr(q, "q", dev), _sptr(out, "out", dev), _dtype_code(q, "q", False), B, S, sel[2], H, R,
+        max_seq_len, D ** -0.5 if sm_scale is None else sm_scale, qa, qb, qc, oa, ob, oc,
+        _ptr(rows, torch.uint8, "rows", dev), rows.numel() // W,
         _ptr(locs, i32, "locs", dev), _ptr(topk, i32, "topk", dev), _ptr(req, i32, "req", dev),
         _ptr(scales, f32, "scales", dev), _ptr(lse, f32, "lse", dev),
         _ptr(weights, f32, "weights", dev), _ptr(acc, f32, "acc", dev),
         0 if workspace is None else _ptr(workspace, workspace.dtype, "workspace", dev),
         0 if workspace is None else workspace.numel() * workspace.element_size())
-    _call((_lib or load_library()).hs_attend, "hs_attend", dev, fmt, args,
-          _raw_stream(stream, dev))
+    _run("hs_attend", dev, fmt, args, _raw_stream(stream, dev))
 
 
 def hs_accumulate(weights, topk, req, acc, counts=None, stream=None) -> None:
@@ -777,10 +789,10 @@ def hs_accumulate(weights, topk, req, acc, counts=None, stream=None) -> None:
     if acc.dim() != 2:
         raise ValueError("acc must be [requests, tokens]")
     i32, f32, dev = torch.int32, torch.float32, _device_of(acc, "acc")
-    _call((_lib or load_library()).hs_accumulate, "hs_accumulate", dev,
-          _ptr(weights, f32, "weights", dev), _ptr(topk, i32, "topk", dev),
-          _ptr(req, i32, "req", dev), _ptr(counts, i32, "counts", dev), B, S, K,
-          _ptr(acc, f32, "acc", dev), acc.shape[0], acc.shape[1], _raw_stream(stream, dev))
+    _run("hs_accumulate", dev,
+         _ptr(weights, f32, "weights", dev), _ptr(topk, i32, "topk", dev),
+         _ptr(req, i32, "req", dev), _ptr(counts, i32, "counts", dev), B, S, K,
+         _ptr(acc, f32, "acc", dev), acc.shape[0], acc.shape[1], _raw_stream(stream, dev))
 
 
 def hs_evict(acc, req, seq_lens, recent: int, keep, kept, kept_acc=None, stream=None) -> None:
@@ -789,16 +801,20 @@ def hs_evict(acc, req, seq_lens, recent: int, keep, kept, kept_acc=None, stream=
     import torch
     if acc.dim() != 2 or keep.dim() != 2:
         raise ValueError("acc must be [requests, tokens] and keep [batch, budget]")
-    B, budget = keep.shape
-    _shape(req, (B,), "req")
-    _shape(seq_lens, (B,), "seq_lens")
-    _shape(kept, (B,), "kept")
-    _shape(kept_acc, (B, budget), "kept_acc")
+    shape = keep.shape
+    (B, budget), one = shape, shape[:1]
+    if req.shape != one or seq_lens.shape != one or kept.shape != one:
+        _shape(req, one, "req")
+        _shape(seq_lens, one, "seq_lens")
+        _shape(kept, one, "kept")
+    if kept_acc is not None and kept_acc.shape != shape:
+        _shape(kept_acc, shape, "kept_acc")
+    R, L = acc.shape
     i32, f32, dev = torch.int32, torch.float32, _device_of(acc, "acc")
-    _call((_lib or load_library()).hs_evict, "hs_evict", dev, _ptr(acc, f32, "acc", dev),
-          _ptr(req, i32, "req", dev), _ptr(seq_lens, i32, "seq_lens", dev), B, recent, budget,
-          acc.shape[0], acc.shape[1], _ptr(keep, i32, "keep", dev), _ptr(kept, i32, "kept", dev),
-          _ptr(kept_acc, f32, "kept_acc", dev), _raw_stream(stream, dev))
+    _run("hs_evict", dev, _ptr(acc, f32, "acc", dev),
+         _ptr(req, i32, "req", dev), _ptr(seq_lens, i32, "seq_lens", dev), B, recent, budget,
+         R, L, _ptr(keep, i32, "keep", dev), _ptr(kept, i32, "kept", dev),
+         _ptr(kept_acc, f32, "kept_acc", dev), _raw_stream(stream, dev))
 
 
 def hs_compact_kv(fmt: HsKvFormat, src_rows, src_scales, src_req, keep, kept, dst_rows,
@@ -810,14 +826,16 @@ def hs_compact_kv(fmt: HsKvFormat, src_rows, src_scales, src_req, keep, kept, ds
     dR, dL = _store(fmt, dst_rows, dst_scales, "dst_")
     if keep.dim() != 2:
         raise ValueError("keep must be [batch, budget]")
-    B, budget = keep.shape
-    _shape(kept, (B,), "kept")
-    _shape(src_req, (B,), "src_req")
-    _shape(dst_req, (B,), "dst_req")
+    shape = keep.shape
+    (B, budget), one = shape, shape[:1]
+    if kept.shape != one or src_req.shape != one or dst_req.shape != one:
+        _shape(kept, one, "kept")
+        _shape(src_req, one, "src_req")
+        _shape(dst_req, one, "dst_req")
     i32, f32, u8, dev = torch.int32, torch.float32, torch.uint8, _device_of(keep, "keep")
-    _call((_lib or load_library()).hs_compact_kv, "hs_compact_kv", dev, fmt,
-          _ptr(src_rows, u8, "src_rows", dev), _ptr(src_scales, f32, "src_scales", dev), sR, sL,
-          _ptr(src_req, i32, "src_req", dev), _ptr(keep, i32, "keep", dev),
-          _ptr(kept, i32, "kept", dev), B, budget, _ptr(dst_rows, u8, "dst_rows", dev),
-          _ptr(dst_scales, f32, "dst_scales", dev), dR, dL, _ptr(dst_req, i32, "dst_req", dev),
-          _raw_stream(stream, dev))
+    _run("hs_compact_kv", dev, fmt,
+         _ptr(src_rows, u8, "src_rows", dev), _ptr(src_scales, f32, "src_scales", dev), sR, sL,
+         _ptr(src_req, i32, "src_req", dev), _ptr(keep, i32, "keep", dev),
+         _ptr(kept, i32, "kept", dev), B, budget, _ptr(dst_rows, u8, "dst_rows", dev),
+         _ptr(dst_scales, f32, "dst_scales", dev), dR, dL, _ptr(dst_req, i32, "dst_req", dev),
+         _raw_stream(stream, dev))
