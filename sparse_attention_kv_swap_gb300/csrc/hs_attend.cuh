@@ -247,6 +247,12 @@ __device__ __forceinline__ float4 load_remote4(const float* p, int rank) {
     return x;
 }
 
+// Place of a token's scale in its row: the two tokens of a lane's score fragment, t and t + 2,
+// lie side by side.
+__device__ __forceinline__ int scale_slot(int t) {
+    return (t & ~3) | (t & 1) << 1 | (t >> 1 & 1);
+}
+
 // Query head, within its group, of column 2 c of a score fragment.
 template <int NT>
 __device__ __forceinline__ int column_head(int c) {
@@ -644,7 +650,7 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     auto put_scales = [&](const float (&x)[kHeldScales], int to, int ch) {
 #pragma unroll
         for (int k = 0; k < kHeldScales; ++k)
-            if (ch + k < per) t_scale[(ch + k) * a.TC + to] = x[k];
+            if (ch + k < per) t_scale[(ch + k) * a.TC + scale_slot(to)] = x[k];
     };
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) at_last[u] = -1;
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     for (int i = live + tid; i < tiles * 16; i += nthreads) {
         t_loc[i] = t_loc[live - 1];
         t_pos[i] = t_pos[live - 1];
-        for (int ch = 0; ch < per; ++ch) t_scale[ch * a.TC + i] = 0.f;
+        for (int ch = 0; ch < per; ++ch) t_scale[ch * a.TC + scale_slot(i)] = 0.f;
     }
     if (!SPILL) asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     __syncthreads();
@@ -704,13 +710,27 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
             const uint32_t tile = queue + stage * kTile;
             int from = lane;
             if (D * N > 128) asm volatile("" : "+r"(from));  // offsets computed here, not kept
+            // A lane's chunks lie in COPIES consecutive rows, or are dealt out in order where a row's
+            // chunks do not divide the lanes.
+            constexpr bool kRows = 32 % (D / 16) == 0;
+            constexpr int kGroup = kRows && COPIES % 4 == 0 ? 4 : 1;
 #pragma unroll
-            for (int k = 0; k < COPIES; ++k) {
-                const int row = (k * 32 + from) / (D / 16), chunk = (k * 32 + from) % (D / 16);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 tile + chunk_at<D>(row, chunk)),
-                             "l"(p + (long long)l[row] * a.W + chunk * 16)
-                             : "memory");
+            for (int k0 = 0; k0 < COPIES; k0 += kGroup) {
+                int loc[kGroup];
+                const int row0 = kRows ? from / (D / 16) * COPIES + k0 : (k0 * 32 + from) / (D / 16);
+                const int chunk = (kRows ? from : k0 * 32 + from) % (D / 16);
+                if constexpr (kGroup == 4) {
+                    const int4 x = *reinterpret_cast<const int4*>(l + row0);
+                    loc[0] = x.x, loc[1] = x.y, loc[2] = x.z, loc[3] = x.w;
+                } else {
+                    loc[0] = l[row0];
+                }
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     tile + chunk_at<D>(row0 + k, chunk)),
+                                 "l"(p + (long long)loc[k] * a.W + chunk * 16)
+                                 : "memory");
             }
         }
         commit_copies();  // of nothing past the last item, so that the count stays even
@@ -801,7 +821,8 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
             const int t0 = (mine < n ? mine : 0) * 16 + t_lo;
             const bool on0 = mine < n && tile0 * 16 + t0 < live;
             const bool on1 = mine < n && tile0 * 16 + t0 + 2 < live;
-            const float k0 = sk[t0], k1 = sk[t0 + 2];
+            const float2 kk = *reinterpret_cast<const float2*>(sk + (mine < n ? mine : 0) * 16 + 2 * g);
+            const float k0 = kk.x, k1 = kk.y;
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
@@ -851,7 +872,8 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
             float z[N][4];
             scores.load(i / F, z);
             const int mine = F == 1 ? i : i + (c >> 1) < n ? i + (c >> 1) : i;
-            const float v0 = sv[mine * 16 + t_lo] * inv, v1 = sv[mine * 16 + t_lo + 2] * inv;
+            const float2 vv = *reinterpret_cast<const float2*>(sv + mine * 16 + 2 * g);
+            const float v0 = vv.x * inv, v1 = vv.y * inv;
             uint32_t tile = next_item(n + i);
             scores.loaded(z);
             uint32_t pf[N][2];
