@@ -23,21 +23,43 @@ void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, AttendSh
     if (k.TS == 0) k.TS = 16;
     k.TC = k.TS + 4;  // scale rows in different banks
     const int D = f.head_dim, G = a.num_heads / f.num_kv_heads;
-    const int columns = sh->nt == 0 ? 4 : 8 * sh->nt;  // query heads of a task
-    k.ngroups = (G + columns - 1) / columns;
-    const int groups = f.num_kv_heads * k.ngroups;
-    // Warps: one task each where they fit; with few heads, a CTA's tokens are split into parts
-    // so that it has 8 warps or a few more; with many, a warp takes several in turn.
     const int most = attend_warps(D, sh->spill);
-    int nsub = groups >= 8 ? 1 : (8 + groups - 1) / groups;
-    if (nsub > 1 && groups * nsub > most) nsub = most / groups;
-    if (nsub > k.TS / 16) nsub = k.TS / 16;
+    int columns, groups, nsub, task_tiles;
+    const auto split = [&](int nt) {
+        sh->nt = nt;
+        columns = nt == 0 ? 4 : 8 * nt;  // query heads of a task
+        k.ngroups = (G + columns - 1) / columns;
+        groups = f.num_kv_heads * k.ngroups;
+        // Warps: one task each where they fit; with few heads, a CTA's tokens are split into parts
+        // so that it has 8 warps or a few more; with many, a warp takes several in turn.
+        nsub = groups >= 8 ? 1 : (8 + groups - 1) / groups;
+        if (nsub > 1 && groups * nsub > most) nsub = most / groups;
+        if (nsub > k.TS / 16) nsub = k.TS / 16;
+        task_tiles = (k.TS / 16 + nsub - 1) / nsub;
+    };
+    // Query heads a warp serves with one reading of keys and values.  Up to 4 heads, a fragment of
+    // 8 columns holds two tiles (nt 0), which halves the scores' tensor memory: slices twice as
+    // long fit, and fit two CTAs an SM (16 requests of 8192 tokens, 8 heads of 64, 4 query heads each:
+    // 48.5 us; 59.4 with one tile and columns left empty).  Above 8 heads, 16 columns (nt 2)
+    // convert every code once instead of twice (128 requests of 2048 tokens, one K/V head of 64, 32
+    // query heads: 29.2 us against 37.1), but leave half the tasks, and with under 4 tiles a task the
+    // warps run short (64 requests of 512 tokens, one K/V head of 128, 16 query heads: 15.1 us
+    // against 12.7).  Wider heads have the registers for one tile and 8 columns only.
+    if (sh->spill) {
+        split(1);
+    } else if (G <= 4 && D <= 192) {
+        split(0);
+    } else if (G > 8 && D <= 128) {
+        split(2);
+        if (task_tiles < 4) split(1);
+    } else {
+        split(1);
+    }
     k.nsub = nsub;
     const int rounds = (groups * nsub + most - 1) / most;
     const int warps = (groups * nsub + rounds - 1) / rounds;
     sh->threads = 32 * warps;
     k.alias = rounds == 1;
-    const int task_tiles = (k.TS / 16 + nsub - 1) / nsub;
     k.task_cols = sh->nt == 0 ? 4 * ((task_tiles + 1) / 2) : 4 * sh->nt * task_tiles;
     const long long need = (long long)rounds * ((warps + 3) / 4) * k.task_cols;
     int cols = 32;
@@ -93,17 +115,23 @@ int slots(const AttendShape& sh) {
     return 2 * resident(sh.P % 2 == 0 ? sh.P / 2 : sh.P);
 }
 
-// Estimated time of a call in us.  The CTAs run in rounds, each with a start and an end (about 10 us
-// and 4 ns a token) besides the rows it gathers, which come at 44 GB/s an SM whether one CTA
-// or two share it.
+// Estimated time of a call in us.  The CTAs run in rounds, with one CTA an SM or, if there are more
+// than that, two.  A round has a start and an end of about 10 us; a token takes 9 ns and 10 ns for
+// every KB gathered (16 with two CTAs an SM, which each get 60% of the speed of one), where the work
+// on a head's codes counts as 0.125 KB and a query head as 2.5 bytes.  The constants are fitted to all
+// cluster sizes of 44 calls with weights, of 1 to 256 queries and 512 to 8192 tokens, whole and
+// with rows left out: the size of the least estimate is 0.5% slower than the fastest one on
+// average, 9% at worst.  64 requests of 2048 tokens and 8 heads of 128, for one, took 62.5 us in
+// clusters of 4, 63.5 of 2, 75.8 of 6 and 67.1 of 8.
 double cost(const hs_kv_format& f, const hs_attend_args& a, const AttendShape& sh) {
-    constexpr int kSms = 152;
-    const int n = slots(sh);
-    const double row = 2.0 * f.num_kv_heads * f.head_dim / 44e3;
+    const int one = resident(sh.P), two = slots(sh);
+    const double kb =
+        f.num_kv_heads * (2e-3 * f.head_dim + 0.125 * sh.a.ngroups) + 2.5e-3 * a.num_heads;
     double t = 0;
-    for (long long left = (long long)a.batch * a.steps * sh.P; left > 0; left -= n) {
-        const int per_sm = left > kSms && n > kSms ? 2 : 1;
-        t += 10 + sh.a.TS * (0.004 + per_sm * row);
+    for (long long left = (long long)a.batch * a.steps * sh.P; left > 0;) {
+        const bool shared = left > one && two > one;
+        t += shared ? 11.5 + sh.a.TS * (0.009 + 0.016 * kb) : 10 + sh.a.TS * (0.009 + 0.010 * kb);
+        left -= shared ? two : one;
     }
     return t;
 }
@@ -116,15 +144,12 @@ bool worth(const hs_attend_args& a, int P) { return P == 1 || a.top_k >= 64 * P;
 AttendShape first_shape(const hs_kv_format& f, const hs_attend_args& a) {
     AttendShape sh;
     std::memset(&sh, 0, sizeof(sh));
-    const int G = a.num_heads / f.num_kv_heads;
-    sh.nt = G <= 4 && f.head_dim <= 192 ? 0 : G > 8 && f.head_dim <= 128 ? 2 : 1;
     for (int pass = 0; pass < 2; ++pass) {
         for (int P = 1; P <= kMaxCluster && (pass == 1 || worth(a, P)); ++P) {
             set_cluster(f, a, P, &sh);
             if (fits(sh, kMaxSmem)) return sh;
         }
     }
-    sh.nt = 1;
     sh.spill = true;
     set_cluster(f, a, kMaxCluster, &sh);
     return sh;
