@@ -219,7 +219,7 @@ cudaError_t launch_attend(const hs_kv_format& f, const hs_attend_args& a, cudaSt
     if (e != cudaSuccess || !a.acc_dev || a.steps == 1) return e;
     // A token may be selected in several steps: its sums follow the steps.
     return launch_accumulate(a.weights_dev, a.topk_dev, a.req_dev, nullptr, a.batch, a.steps,
-                             a.top_k, a.acc_dev, a.num_requests, a.max_seq_len, s);
+                             a.top_k, a.acc_dev, a.num_requests, a.max_seq_len, true, s);
 }
 
 }  // namespace hs

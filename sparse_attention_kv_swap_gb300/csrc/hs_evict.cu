@@ -248,13 +248,14 @@ constexpr int kHeldSteps = 4, kHeldEntries = 4;
 __global__ void __launch_bounds__(kAccumulateThreads)
     accumulate_kernel(const float* weights, const int32_t* topk, const int32_t* req,
                       const int32_t* counts, int32_t S, int32_t K, float* acc, int32_t R,
-                      int32_t L) {
+                      int32_t L, bool after_attend) {
     constexpr int kAll = kAccumulateThreads * kAccumulateCluster;
     cg::cluster_group cluster = cg::this_cluster();
     const int b = blockIdx.x / kAccumulateCluster;
     const int first = (int)cluster.block_rank() * kAccumulateThreads + threadIdx.x;
-    // The positions may be read early: the kernel before is hs_attend's, which reads them too, or
-    // one that does not let this one go before it ends.
+    // Behind hs_attend's own kernel the positions, which that one has read, may be read before its
+    // end; any other kernel before this one may still be writing them.
+    if (!after_attend) wait_for_previous();
     const int q = __ldg(req + b);
     const int steps = q < 0 || q >= R ? 0 : counts ? min(__ldg(counts + b), S) : S;
     float* dst = acc + (long long)(steps > 0 ? q : 0) * L;
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kAccumulateThreads)
                 t[s][i] = s < steps && first + i * kAll < K
                               ? __ldg(topk + row + s * K + first + i * kAll)
                               : -1;
-        wait_for_previous();  // for the weights
+        if (after_attend) wait_for_previous();  // for the weights
 #pragma unroll
         for (int s = 0; s < kHeldSteps; ++s)
 #pragma unroll
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kAccumulateThreads)
         }
         return;
     }
-    wait_for_previous();
+    if (after_attend) wait_for_previous();
     for (int s = 0; s < steps; ++s) {
         if (s > 0) cluster.sync();
 #pragma unroll 4
@@ -302,9 +303,10 @@ __global__ void __launch_bounds__(kAccumulateThreads)
 
 cudaError_t launch_accumulate(const float* weights, const int32_t* topk, const int32_t* req,
                               const int32_t* counts, int32_t B, int32_t S, int32_t K, float* acc,
-                              int32_t R, int32_t L, cudaStream_t s) {
+                              int32_t R, int32_t L, bool after_attend, cudaStream_t s) {
     return launch_chained(accumulate_kernel, B * kAccumulateCluster, kAccumulateThreads, 0,
-                          kAccumulateCluster, s, weights, topk, req, counts, S, K, acc, R, L);
+                          kAccumulateCluster, s, weights, topk, req, counts, S, K, acc, R, L,
+                          after_attend);
 }
 
 cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* seq_lens, int32_t B,

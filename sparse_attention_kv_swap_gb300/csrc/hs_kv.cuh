@@ -69,7 +69,7 @@ cudaError_t launch_compact(CompactArgs a, cudaStream_t s);
 
 cudaError_t launch_accumulate(const float* weights, const int32_t* topk, const int32_t* req,
                               const int32_t* counts, int32_t B, int32_t S, int32_t K, float* acc,
-                              int32_t R, int32_t L, cudaStream_t s);
+                              int32_t R, int32_t L, bool after_attend, cudaStream_t s);
 cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* seq_lens, int32_t B,
                          int32_t recent, int32_t budget, int32_t R, int32_t L, int32_t* keep,
                          int32_t* kept, float* kept_acc, cudaStream_t s);
@@ -82,8 +82,9 @@ cudaError_t launch_attend(const hs_kv_format& f, const hs_attend_args& a, cudaSt
 
 // The kernels of these calls run one after the other on a stream, some for a few microseconds:
 // each may be launched while the one before it still runs (launch_chained) and waits for its
-// end, memory included, before it touches any (wait_for_previous).  The next one's launch is
-// let go as soon as all CTAs of this one run (release_next).
+// end, memory included, before it touches memory that the one before or any earlier one writes
+// (wait_for_previous).  The next launch is let go at the end of this kernel, or where all its CTAs
+// have come to release_next: there the next one's CTAs may take the place that is left.
 __device__ __forceinline__ void wait_for_previous() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -165,7 +165,7 @@ int hs_accumulate(const float* weights_dev, const int32_t* topk_dev, const int32
         !aligned(counts_dev, 4) || !aligned(acc_dev, 4))
         return HS_ERR_INVALID_ARG;
     return result(launch_accumulate(weights_dev, topk_dev, req_dev, counts_dev, batch, num_steps,
-                                    top_k, acc_dev, num_requests, max_seq_len,
+                                    top_k, acc_dev, num_requests, max_seq_len, false,
                                     static_cast<cudaStream_t>(stream)));
 }
 

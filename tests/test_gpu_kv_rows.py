@@ -667,3 +667,160 @@ def test_cache_evict_shrinks_every_layer():
                 assert torch.equal(rows[int(locs[q, 0, j])], want[q, int(topk[q, 0, j])])
     assert cache.status() == (B.HS_OK, 0)
     cache.close()
+
+
+# ---- longer and chained calls ---------------------------------------------------
+
+@pytest.mark.parametrize("L,budget,recent", [(131073, 1000, 10), (300001, 70000, 4096)])
+def test_evict_longer_than_the_registers_hold(L, budget, recent):
+    rng = np.random.default_rng(L)
+    acc = np.exp(2 * rng.standard_normal((2, L))).astype(np.float32)
+    acc[1] = rng.integers(0, 50, L)
+    run_evict(acc, [1, 0], [L, L - 1], recent, budget)
+
+
+@pytest.mark.parametrize("S,K", [(1, 9001), (4, 8193), (5, 600), (7, 8200), (2, 1), (4, 8192)])
+def test_accumulate_steps_and_lengths(S, K):
+    rng = np.random.default_rng(100 * S + K)
+    R, L = 3, K + 33
+    topk = np.stack([[rng.permutation(L)[:K] for _ in range(S)] for _ in range(2)])
+    topk = topk.astype(np.int32)
+    w = rng.random((2, S, K)).astype(np.float32)
+    acc = rng.random((R, L)).astype(np.float32)
+    got = dev(acc)
+    pkg.hs_accumulate(dev(w), dev(topk), dev(np.array([2, 0], np.int32)), got)
+    torch.cuda.synchronize()
+    for b, q in enumerate((2, 0)):
+        for s in range(S):
+            acc[q, topk[b, s]] += w[b, s]
+    assert np.array_equal(got.cpu().numpy(), acc)
+
+
+def test_calls_follow_one_another():
+    """Calls whose inputs the call before them writes, directly and from a graph: positions kept
+    by an eviction are what the next accumulation adds to and the next compaction copies."""
+    rng = np.random.default_rng(21)
+    B_, L, budget, recent, heads, D, T = 48, 3000, 700, 50, 3, 64, 32
+    fmt = pkg.make_kv_format(heads, D, T, B.HS_KV_INT8)
+    k = torch.from_numpy(rng.standard_normal((B_, L, heads, D))).bfloat16()
+    v = torch.from_numpy(rng.standard_normal((B_, L, heads, D))).bfloat16()
+    first = rng.random((B_, L)).astype(np.float32)
+    more = rng.random((B_, 1, budget)).astype(np.float32)
+    req = np.arange(B_, dtype=np.int32)
+    dk, dv, dmore, dreq = dev(k), dev(v), dev(more), dev(req)
+    zero, n = torch.zeros_like(dreq), torch.full_like(dreq, L)
+    rows = torch.zeros((B_, L, 2 * heads * D), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(fmt.scales_shape(B_, L), device="cuda")
+    acc = dev(first)
+    keep = torch.empty((2, B_, 1, budget), dtype=torch.int32, device="cuda")
+    kept = torch.empty((2, B_), dtype=torch.int32, device="cuda")
+    dst = torch.zeros((B_, budget, 2 * heads * D), dtype=torch.uint8, device="cuda")
+    ds = torch.zeros(fmt.scales_shape(B_, budget), device="cuda")
+
+    def calls():
+        acc.copy_(dfirst)
+        pkg.hs_quantize_kv(fmt, dk, dv, dreq, zero, n, rows, scales)
+        pkg.hs_evict(acc, dreq, n, recent, keep[0, :, 0], kept[0])
+        pkg.hs_accumulate(dmore, keep[0], dreq, acc)
+        pkg.hs_evict(acc, dreq, n, recent, keep[1, :, 0], kept[1])
+        pkg.hs_compact_kv(fmt, rows, scales, dreq, keep[1, :, 0], kept[1], dst, ds, dreq)
+
+    dfirst = dev(first)
+    wr, ws = torch.zeros_like(rows, device="cpu"), torch.zeros_like(scales, device="cpu")
+    ref.quantize(k, v, req, [0] * B_, [L] * B_, wr, ws, T, "int8")
+    one, count, _ = ref.evict(first, req, [L] * B_, recent, budget)
+    sums = first.copy()
+    for b in range(B_):
+        sums[b, one[b]] += more[b, 0]
+    two, count, _ = ref.evict(sums, req, [L] * B_, recent, budget)
+    wd, wds = torch.zeros_like(dst, device="cpu"), torch.zeros_like(ds, device="cpu")
+    ref.compact(wr, ws, req, torch.from_numpy(two), torch.from_numpy(count), wd, wds, req, T, heads,
+                D, "int8")
+
+    def check():
+        torch.cuda.synchronize()
+        assert torch.equal(rows.cpu(), wr) and torch.equal(scales.cpu(), ws)
+        assert np.array_equal(keep[0, :, 0].cpu().numpy(), one)
+        assert np.array_equal(acc.cpu().numpy(), sums)
+        assert np.array_equal(keep[1, :, 0].cpu().numpy(), two)
+        assert torch.equal(ds.cpu(), wds) and torch.equal(dst.cpu(), wd)
+
+    for _ in range(3):
+        calls()
+        check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for x in (rows, scales, acc, keep, kept, dst, ds):
+        x.zero_()
+    for _ in range(3):
+        graph.replay()
+    check()
+
+
+@pytest.mark.parametrize("code,dtype,heads,group,D,T", [("e4m3", "bf16", 2, 4, 64, 16),
+                                                        ("int8", "fp16", 3, 2, 96, 24)])
+def test_decode_example(code, dtype, heads, group, D, T):
+    """The example's loop, eviction in between: codes and scales bit for bit, every step's
+    attention within its bounds, over the rows that the host pool should hold."""
+    import importlib.util
+    import pathlib
+    path = pathlib.Path(__file__).resolve().parent.parent / "examples" / "decode_8bit.py"
+    spec = importlib.util.spec_from_file_location("decode_8bit", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    rng = np.random.default_rng(22)
+    R, limit, budget, recent, top_k = 3, 100, 41, 7, 30
+    d = example.Decoder(R, limit, budget, recent, top_k, 2 * top_k, heads, group, D, T, CODES[code],
+                        DTYPES[dtype])
+    pool = d.cache.host_pools[0]
+    pool.zero_()
+    rows, scales = pool.clone(), torch.zeros_like(d.scales, device="cpu")
+    acc = np.zeros((R, limit), np.float32)
+    req = np.arange(R, dtype=np.int32)
+
+    def rand(*shape):
+        return torch.from_numpy(rng.standard_normal(shape)).to(DTYPES[dtype])
+
+    lens = np.array([95, 60, 97])
+    k, v = rand(R, 97, heads, D), rand(R, 97, heads, D)
+    d.prompt(dev(k), dev(v), lens)
+    ref.quantize(k, v, req, [0] * R, lens, rows, scales, T, code)
+    cut = 0
+    for step in range(90):
+        torch.cuda.synchronize()
+        full = [i for i in range(R) if lens[i] == limit]
+        if full:
+            keep, kept, ka = ref.evict(acc, full, lens[full], recent, budget)
+            nb = d.fmt.num_blocks(budget)
+            dst = torch.zeros((len(full), budget, rows.shape[2]), dtype=torch.uint8)
+            ds = torch.zeros((len(full), nb, 2, heads))
+            ref.compact(rows, scales, full, torch.from_numpy(keep), torch.from_numpy(kept), dst, ds,
+                        list(range(len(full))), T, heads, D, code)
+            rows[full, :budget], scales[full, :nb] = dst, ds
+            acc[full], lens[full] = 0, budget
+            acc[full, :budget] = ka
+            cut += len(full)
+        assert d.make_room() == full
+        q, k, v = rand(R, 1, heads * group, D), rand(R, 1, heads, D), rand(R, 1, heads, D)
+        topk = d.select()
+        d.step(dev(q), dev(k), dev(v), topk)
+        torch.cuda.synchronize()
+        ref.quantize(k, v, req, lens, [1] * R, rows, scales, T, code)
+        lens += 1
+        assert torch.equal(pool, rows) and torch.equal(d.scales.cpu(), scales), step
+        topk = topk.cpu().numpy()
+        assert (topk[:, 0, 0] == lens - 1).all()
+        a = Attend.__new__(Attend)
+        a.heads, a.G, a.D, a.T, a.code, a.dtype, a.L = heads, group, D, T, code, dtype, limit
+        a.q, a.topk, a.req, a.scales, a.sm_scale = q, topk, req, scales.numpy(), D ** -0.5
+        a.rows = rows.reshape(R * limit, -1).numpy()
+        a.locs = np.where(topk < 0, -1, topk + limit * req[:, None, None])
+        a.check((d.out["out"], d.out["lse"], d.out["weights"]))
+        w = d.out["weights"].cpu().numpy()
+        for b in range(R):
+            ok = topk[b, 0] >= 0
+            acc[b, topk[b, 0, ok]] += w[b, 0, ok]
+        assert np.array_equal(d.acc.cpu().numpy(), acc)
+    assert cut == 5 and d.cache.status() == (B.HS_OK, 0)
+    d.cache.close()
