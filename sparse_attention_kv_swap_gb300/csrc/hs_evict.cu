@@ -9,7 +9,10 @@
 // serves a request and its CTAs read each other's counts over distributed
 // shared memory.  A thread keeps its keys in registers from the first pass
 // on (sequences up to 131072), so the weights are read once.  The kernel is
-// bound by the latency of its passes and barriers, not by the 4 * n bytes.
+// bound by the latency of its passes and barriers, not by the 4 * n bytes:
+// 7.4 us for one sequence of 1000, 8.5 for 64 of 4096 (1 MB); 17.8 for 8 of
+// 131072 (4 MB) in clusters of 8, of which reading each other's counts is 5
+// (6.6 with 32-bit counts, 64 KB a CTA and pass).
 #include <cooperative_groups.h>
 
 #include "hs_kv.cuh"
@@ -22,7 +25,7 @@ namespace cg = cooperative_groups;
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kMaxEvictCluster = 8;
-constexpr int kAhead = 4;                        // remote counts read at a time
+constexpr int kAhead = 4;                        // CTAs whose counts are read at a time
 constexpr int kBins = 2048;
 constexpr int kOwnBins = 2;                      // bins a thread looks through
 static_assert(kOwnBins * kEvictThreads == kBins, "every bin has a thread");
@@ -56,7 +59,13 @@ struct EvictArgs {
 // CH: chunks of a warp's segment that are held in registers; 0: read anew in every pass.
 template <int CH>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a) {
-    __shared__ __align__(16) int s_hist[3][kBins];  // this CTA's counts, pass by pass
+    __shared__ __align__(16) uint32_t s_hist[3][kBins];  // this CTA's counts, pass by pass
+    // For the cluster: the counts of a thread's bins in one word, where the CTA's keys are few
+    // enough (those in registers are).
+    constexpr bool kPacked = CH > 0;
+    static_assert(kMaxChunks * kChunk * kEvictWarps < 1 << 16, "a CTA's keys fit a count");
+    __shared__ uint32_t s_pair[kPacked ? 3 : 1][kEvictThreads];
+    __shared__ __align__(8) int s_cta[2];  // this CTA's keys above the edge, and equal to it
     __shared__ int s_tmp[33];
     __shared__ int s_pick[2];       // the chosen bin, and how many are wanted from it
     cg::cluster_group cluster = cg::this_cluster();
@@ -124,39 +133,42 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
         // The k-th largest key digit by digit.
         uint32_t edge = 0;   // the digits found so far; at the end, the key
         int want = k;        // how many of the keys with those digits are kept
-        int out = 0, ties = 0;  // kept, and equal to the edge, before this CTA's positions
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const int bins = pass == 2 ? 1024 : 2048;
-            int* hist = s_hist[pass];
+            uint32_t* hist = s_hist[pass];
             each([&](int, const uint32_t (&v)[4]) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (pass == 0 || v[i] >> (pass == 1 ? 21 : 10) == edge)
-                        atomicAdd(&hist[v[i] >> shift & (bins - 1)], 1);
+                        atomicAdd(&hist[v[i] >> shift & (bins - 1)], 1u);
             });
-            cluster.sync();
-            // A thread's bins, counted from the top, over the cluster and before this CTA.
+            // A thread's bins, counted from the top, over the cluster.
             const int top = kBins - (tid + 1) * kOwnBins;
-            int mine[kOwnBins], before[kOwnBins];
-#pragma unroll
-            for (int i = 0; i < kOwnBins; ++i) mine[i] = before[i] = 0;
+            if (kPacked && P > 1) {
+                __syncthreads();
+                s_pair[pass][tid] = hist[top] | hist[top + 1] << 16;
+            }
+            cluster.sync();
+            int mine[kOwnBins] = {};
 #pragma unroll 1
             for (int r0 = 0; r0 < P; r0 += kAhead) {
-                int2 h[kAhead];  // on their way together: a remote load takes long
-#pragma unroll
-                for (int r = 0; r < kAhead; ++r)
-                    if (r0 + r < P)
-                        h[r] = *reinterpret_cast<const int2*>(
-                            cluster.map_shared_rank(hist, r0 + r) + top);
+                uint2 h[kAhead];  // on their way together: a remote load takes long
 #pragma unroll
                 for (int r = 0; r < kAhead; ++r) {
-                    if (r0 + r >= P) break;
-                    mine[0] += h[r].y;
-                    mine[1] += h[r].x;
-                    if (r0 + r < rank) before[0] += h[r].y, before[1] += h[r].x;
+                    h[r] = make_uint2(0, 0);
+                    if (r0 + r >= P) continue;
+                    if (kPacked && P > 1) {
+                        h[r].x = cluster.map_shared_rank(s_pair[pass], r0 + r)[tid];
+                        h[r].y = h[r].x >> 16, h[r].x &= 0xffff;
+                    } else {
+                        h[r] = *reinterpret_cast<const uint2*>(
+                            cluster.map_shared_rank(hist, r0 + r) + top);
+                    }
                 }
+#pragma unroll
+                for (int r = 0; r < kAhead; ++r) mine[0] += h[r].y, mine[1] += h[r].x;
             }
             int all_keys;
             int above =
@@ -173,22 +185,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
             const int pick = s_pick[0];
             want = s_pick[1];
             edge = (edge << (pass == 2 ? 10 : 11)) | (uint32_t)pick;
-            // Kept keys before this CTA: those in bins above the chosen one.  In the last pass the
-            // chosen bin holds the ties.
-            int part = 0, same = 0;
-#pragma unroll
-            for (int i = 0; i < kOwnBins; ++i) {
-                const int bin = top + kOwnBins - 1 - i;
-                if (bin > pick) part += before[i];
-                if (bin == pick) same = before[i];
-            }
-            if (P > 1) {
-                out += block_sum(part, s_tmp);
-                if (pass == 2) ties = block_sum(same, s_tmp);
-            }
-            __syncthreads();
         }
-        out += min(ties, want);  // the first `want` keys equal to the edge are kept
 
         // The warps' counts, then the positions in order.
         int na = 0, ne = 0;
@@ -201,9 +198,27 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
         });
         na = __reduce_add_sync(0xffffffffu, na);
         ne = __reduce_add_sync(0xffffffffu, ne);
-        int total;
-        const int wa = block_exclusive_scan(lane == 0 ? na : 0, s_tmp, &total);
-        const int we = block_exclusive_scan(lane == 0 ? ne : 0, s_tmp, &total);
+        int wa, we, ta, te;  // before this warp in the CTA, and in all of it
+        if constexpr (kPacked) {
+            wa = block_exclusive_scan(lane == 0 ? na | ne << 16 : 0, s_tmp, &ta);
+            we = wa >> 16, wa &= 0xffff;
+            te = ta >> 16, ta &= 0xffff;
+        } else {
+            wa = block_exclusive_scan(lane == 0 ? na : 0, s_tmp, &ta);
+            we = block_exclusive_scan(lane == 0 ? ne : 0, s_tmp, &te);
+        }
+        int out = 0, ties = 0;  // kept, and equal to the edge, before this CTA's positions
+        if (P > 1) {
+            if (tid == 0) s_cta[0] = ta, s_cta[1] = te;
+            cluster.sync();
+            if (lane < rank) {
+                const int2 h = *reinterpret_cast<const int2*>(cluster.map_shared_rank(s_cta, lane));
+                out = h.x, ties = h.y;
+            }
+            out = __reduce_add_sync(0xffffffffu, out);
+            ties = __reduce_add_sync(0xffffffffu, ties);
+            out += min(ties, want);  // the first `want` keys equal to the edge are kept
+        }
         int tie = ties + __shfl_sync(0xffffffffu, we, 0);
         int at = out + __shfl_sync(0xffffffffu, wa, 0) + min(tie, want) - min(ties, want);
         each([&](int c, const uint32_t (&v)[4]) {
