@@ -24,7 +24,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kMaxEvictCluster = 8;
 constexpr int kAhead = 4;                        // CTAs whose counts are read at a time
 constexpr int kBins = 2048;
 constexpr int kOwnBins = 2;                      // bins a thread looks through
@@ -338,10 +337,22 @@ cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* se
     a.keep = keep;
     a.kept = kept;
     a.kept_acc = kept_acc;
-    // A cluster where one CTA would not hold the sequence's keys in registers.
-    constexpr int kHeld = kMaxChunks * kChunk * kEvictWarps;  // keys of a CTA
+    // Cluster size of the least estimate, in us: what a CTA of a cluster of 1, 2, 4 or 8 takes for few
+    // keys, 0.37 for every 1024 of its keys (0.70, and 1.4 to start, if they are read anew in every
+    // pass), times the rounds of a GB300's SMs.  Measured with 1, 2, 4 and 8: one request of 8192, 9.3,
+    // 8.6, 9.8 and 12.8 us; 8 of 16384, 13.2, 10.6, 10.1 and 13.2; 64 of 16384, 13.3, 10.8, 20.3 and
+    // 64; 64 of 131072, keys held by 8, 55 with 2, 70 with 4 and 94 with 8.
+    constexpr int kHeld = kMaxChunks * kChunk * kEvictWarps;  // keys a CTA holds in registers
+    constexpr struct { int size, resident; double start; } kClusters[] = {
+        {1, 152, 7.0}, {2, 152, 8.0}, {4, 144, 9.2}, {8, 120, 12.4}};
     int P = 1;
-    while (P < kMaxEvictCluster && L / P > kHeld) P *= 2;
+    double least = 0;
+    for (const auto& c : kClusters) {
+        const double keys = (double)L / c.size, rounds = (B * (long long)c.size - 1) / c.resident + 1;
+        const double t = rounds * (keys <= kHeld ? c.start + 0.37 / 1024 * keys
+                                                 : c.start + 1.4 + 0.70 / 1024 * keys);
+        if (c.size == 1 || t < least) least = t, P = c.size;
+    }
     const long long chunks = ((long long)L + kChunk - 1) / kChunk;
     const int per_warp = (int)((chunks + P * kEvictWarps - 1) / (P * kEvictWarps));
     auto* kernel = per_warp <= 1            ? evict_kernel<1>

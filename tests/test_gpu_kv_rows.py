@@ -679,6 +679,16 @@ def test_evict_longer_than_the_registers_hold(L, budget, recent):
     run_evict(acc, [1, 0], [L, L - 1], recent, budget)
 
 
+@pytest.mark.parametrize("requests,L", [(1, 9000), (200, 9000), (40, 20000), (3, 40000), (90, 40000),
+                                        (160, 70000)])
+def test_evict_many_requests(requests, L):
+    rng = np.random.default_rng(requests + L)
+    acc = np.exp(2 * rng.standard_normal((5, L))).astype(np.float32)
+    acc[3] = rng.integers(0, 5, L)
+    seq = L - rng.integers(0, L // 2, requests)
+    run_evict(acc, rng.integers(0, 5, requests), seq, 100, L // 3)
+
+
 @pytest.mark.parametrize("S,K", [(1, 9001), (4, 8193), (5, 600), (7, 8200), (2, 1), (4, 8192)])
 def test_accumulate_steps_and_lengths(S, K):
     rng = np.random.default_rng(100 * S + K)
