@@ -210,13 +210,14 @@ __device__ __forceinline__ void load_query(uint32_t (&r)[2 * STEPS], const uint1
     for (int w = 0; w < STEPS; ++w) {
         const uint16_t* at = p + 16 * w + 4 * c;
         if (vec) {
-            uint2 x = make_uint2(0, 0);
-            if (on) x = __ldg(reinterpret_cast<const uint2*>(at));
-            r[2 * w] = x.x;
-            r[2 * w + 1] = x.y;
+            r[2 * w] = r[2 * w + 1] = 0;
+            if (on)
+                asm volatile("ld.global.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(r[2 * w]), "=r"(r[2 * w + 1])
+                             : "l"(at));
         } else {
-            r[2 * w] = on ? (uint32_t)__ldg(at) | ((uint32_t)__ldg(at + 1) << 16) : 0u;
-            r[2 * w + 1] = on ? (uint32_t)__ldg(at + 2) | ((uint32_t)__ldg(at + 3) << 16) : 0u;
+            r[2 * w] = on ? (uint32_t)ld(at) | ((uint32_t)ld(at + 1) << 16) : 0u;
+            r[2 * w + 1] = on ? (uint32_t)ld(at + 2) | ((uint32_t)ld(at + 3) << 16) : 0u;
         }
     }
 }
@@ -480,7 +481,7 @@ __device__ __forceinline__ void finish(const AttendKernelArgs& a, uint8_t* smem,
         }
         __syncthreads();
         const long long entry0 = (long long)bs * a.K;
-        float* acc = a.acc ? a.acc + (long long)__ldg(a.req + b) * a.L : nullptr;
+        float* acc = a.acc ? a.acc + (long long)ld(a.req + b) * a.L : nullptr;
         for (int i = tid; i < live; i += nthreads) {
             float w = 0.f;
 #pragma unroll 8
@@ -617,13 +618,13 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
             const int i = i0 + u * nthreads + tid;
             loc[u] = -1, pos[u] = 0;
             if (i < entries) {
-                loc[u] = __ldg(a.locs + entry0 + entry_of(i));
-                pos[u] = __ldg(a.topk + entry0 + entry_of(i));
+                loc[u] = ld(a.locs + entry0 + entry_of(i));
+                pos[u] = ld(a.topk + entry0 + entry_of(i));
             }
         }
     };
     load_entries(0);
-    const int req = __ldg(a.req + b);
+    const int req = ld(a.req + b);
     if (warp < ntasks) load_q(warp);
     const bool known = req >= 0 && req < a.R;
     // Masked entries are dropped.  A thread fetches the scales of its entries as soon as it has
@@ -638,12 +639,12 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         for (int k = 0; k < kHeldScales; k += 4) {
             if (ch + k >= per) break;
             if (a.vec_scale) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(src + k));
+                const float4 v = ld(reinterpret_cast<const float4*>(src + k));
                 x[k] = v.x, x[k + 1] = v.y, x[k + 2] = v.z, x[k + 3] = v.w;
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    x[k + i] = ch + k + i < per ? __ldg(src + k + i) : 0.f;
+                    x[k + i] = ch + k + i < per ? ld(src + k + i) : 0.f;
             }
         }
     };

@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     wait_for_previous();
     release_next();
-    const int q = __ldg(a.req + b);
-    int n = __ldg(a.seq_lens + b);
+    const int q = ld(a.req + b);
+    int n = ld(a.seq_lens + b);
     n = q < 0 || q >= a.R || n < 0 ? 0 : min(n, a.L);
     const float* acc = a.acc + (long long)(n > 0 ? q : 0) * a.L;
     int32_t* keep = a.keep + (long long)b * a.budget;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
         auto fetch = [&](int c, uint32_t (&v)[4]) {
             const int t = lo + c * kChunk + lane * 4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = t + i < m ? key_of(__ldg(acc + t + i)) : 0u;
+            for (int i = 0; i < 4; ++i) v[i] = t + i < m ? key_of(ld(acc + t + i)) : 0u;
         };
         // Calls f(chunk, its 4 keys) for the warp's chunks in order.
         auto each = [&](auto f) {
@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(kAccumulateThreads)
     // Behind hs_attend's own kernel the positions, which that one has read, may be read before its
     // end; any other kernel before this one may still be writing them.
     if (!after_attend) wait_for_previous();
-    const int q = __ldg(req + b);
-    const int steps = q < 0 || q >= R ? 0 : counts ? min(__ldg(counts + b), S) : S;
+    const int q = ld(req + b);
+    const int steps = q < 0 || q >= R ? 0 : counts ? min(ld(counts + b), S) : S;
     float* dst = acc + (long long)(steps > 0 ? q : 0) * L;
     const long long row = (long long)b * S * K;
     if (K <= kHeldEntries * kAll && steps <= kHeldSteps) {
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kAccumulateThreads)
 #pragma unroll
             for (int i = 0; i < kHeldEntries; ++i)
                 t[s][i] = s < steps && first + i * kAll < K
-                              ? __ldg(topk + row + s * K + first + i * kAll)
+                              ? ld(topk + row + s * K + first + i * kAll)
                               : -1;
         if (after_attend) wait_for_previous();  // for the weights
 #pragma unroll
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kAccumulateThreads)
 #pragma unroll
             for (int i = 0; i < kHeldEntries; ++i) {
                 if (t[s][i] >= L) t[s][i] = -1;
-                w[s][i] = t[s][i] >= 0 ? __ldg(weights + row + s * K + first + i * kAll) : 0.f;
+                w[s][i] = t[s][i] >= 0 ? ld(weights + row + s * K + first + i * kAll) : 0.f;
             }
 #pragma unroll
         for (int s = 0; s < kHeldSteps; ++s) {
@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(kAccumulateThreads)
         if (s > 0) cluster.sync();
 #pragma unroll 4
         for (int j = first; j < K; j += kAll) {
-            const int t = __ldg(topk + row + (long long)s * K + j);
-            if (t >= 0 && t < L) atomicAdd(dst + t, __ldg(weights + row + (long long)s * K + j));
+            const int t = ld(topk + row + (long long)s * K + j);
+            if (t >= 0 && t < L) atomicAdd(dst + t, ld(weights + row + (long long)s * K + j));
         }
     }
 }

@@ -92,6 +92,20 @@ __device__ __forceinline__ void release_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Reads of what an earlier kernel may have written: ordinary loads, because those of read-only data
+// may be moved ahead of the wait and keep what the kernel before has left in an SM's L1.
+template <typename T>
+__device__ __forceinline__ T ld(const T* p) {
+    return *p;
+}
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 template <typename... P, typename... A>
 cudaError_t launch_chained(void (*kernel)(P...), int grid, int block, size_t smem, int cluster,
                            cudaStream_t s, const A&... args) {

@@ -42,7 +42,7 @@ struct Raw {
             const uint4* p = reinterpret_cast<const uint4*>(
                 static_cast<const uint8_t*>(base) + at * (DTYPE == HS_DTYPE_FP32 ? 4 : 2));
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) v[i] = ld_stream_v4(p + i);
+            for (int i = 0; i < kVecs; ++i) v[i] = ld_once_v4(p + i);
         } else {
             uint32_t w[4 * kVecs];
 #pragma unroll
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kMaxThreads, CACHE ? 1 : 2) quantize_kernel(co
     const int win = blockIdx.x / (2 * heads) % a.windows;
     const int b = blockIdx.x / (2 * heads) / a.windows;
     wait_for_previous();
-    const int q = __ldg(a.req + b), start = __ldg(a.start + b), count = __ldg(a.count + b);
+    const int q = ld(a.req + b), start = ld(a.start + b), count = ld(a.count + b);
     if (q < 0 || q >= a.R || start < 0 || count < 0 || count > a.max_count ||
         start > a.L - count) {
         if constexpr (CACHE)
@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(512, 2) compact_kernel(const CompactArgs a) {
     const int win = blockIdx.x / (2 * heads) % a.windows;
     const int b = blockIdx.x / (2 * heads) / a.windows;
     wait_for_previous();
-    const int sq = __ldg(a.src_req + b), dq = __ldg(a.dst_req + b);
-    int kept = __ldg(a.kept + b);
+    const int sq = ld(a.src_req + b), dq = ld(a.dst_req + b);
+    int kept = ld(a.kept + b);
     if (sq < 0 || sq >= a.src_R || dq < 0 || dq >= a.dst_R) return;
     kept = min(kept, min(a.budget, a.dst_L));
     const int first = win * T;
@@ -333,15 +333,15 @@ __global__ void __launch_bounds__(512, 2) compact_kernel(const CompactArgs a) {
         x = make_uint4(0, 0, 0, 0);
         s = 0.f;
         if (t >= 0 && t < a.src_L) {
-            x = ld_stream_v4(src + (long long)t * W);
-            s = __ldg(scales + (long long)a.block.of(t) * (2 * heads));
+            x = ld_once_v4(src + (long long)t * W);
+            s = ld(scales + (long long)a.block.of(t) * (2 * heads));
         }
     };
     int t[kHeld];
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int j = j0 + i * step;
-        t[i] = j < tokens ? __ldg(keep + j) : -1;
+        t[i] = j < tokens ? ld(keep + j) : -1;
     }
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) load(t[i], held[i], scale[i]);
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(512, 2) compact_kernel(const CompactArgs a) {
     for (int j = j0 + kHeld * step; j < tokens; j += step) {
         uint4 x;
         float s;
-        load(__ldg(keep + j), x, s);
+        load(ld(keep + j), x, s);
         peak = fmaxf(peak, magnitude<CODE>(x, s));
     }
     const float now = scale_of<CODE>(block_max(peak, s_tmp));
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(512, 2) compact_kernel(const CompactArgs a) {
     for (int j = j0 + kHeld * step; j < tokens; j += step) {
         uint4 x;
         float s;
-        load(__ldg(keep + j), x, s);
+        load(ld(keep + j), x, s);
         st_v4(dst + (long long)j * W, recode<CODE, true>(x, s, r));
     }
 }
