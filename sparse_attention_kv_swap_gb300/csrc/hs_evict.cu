@@ -251,21 +251,25 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
     if (k > 0) cluster.sync();  // no CTA leaves while another reads its counts
 }
 
-// A cluster of 4 CTAs per request (additions to scattered words leave an SM one at a time, so
-// they are spread); the steps follow one another, a cluster barrier between them ordering the
-// additions, so that a token selected in several steps is added to in step order.  Up to
-// kHeldSteps steps of kHeldEntries entries a thread are fetched before the first addition, the
-// positions even before the kernel that computes the weights has ended.
-constexpr int kAccumulateThreads = 512, kAccumulateCluster = 4;
+// A cluster of up to 4 CTAs per request (additions to scattered words leave an SM one at a time, so
+// they are spread as long as all CTAs are resident); the steps follow one another, a cluster barrier
+// between them ordering the additions, so that a token selected in several steps is added to in step
+// order.  Up to kHeldSteps steps of kHeldEntries entries a thread are fetched before the first
+// addition, the positions even before hs_attend's kernel has ended.  Four steps of 2048 entries with
+// clusters of 1, 2, 4 and 8: 8.5, 6.4, 5.0 and 5.0 us for 8 requests, 9.1, 6.7, 6.8 and 11.7 for 64;
+// of 512 entries for 256 requests 6.6, 10.3, 16.1 and 27.4.  Entries fetched step by step instead:
+// 5.4 us for the 8 requests, 7.6 for the 64.
+constexpr int kAccumulateThreads = 512;
 constexpr int kHeldSteps = 4, kHeldEntries = 4;
 
+template <int P>
 __global__ void __launch_bounds__(kAccumulateThreads)
     accumulate_kernel(const float* weights, const int32_t* topk, const int32_t* req,
                       const int32_t* counts, int32_t S, int32_t K, float* acc, int32_t R,
                       int32_t L, bool after_attend) {
-    constexpr int kAll = kAccumulateThreads * kAccumulateCluster;
     cg::cluster_group cluster = cg::this_cluster();
-    const int b = blockIdx.x / kAccumulateCluster;
+    constexpr int all = kAccumulateThreads * P;
+    const int b = blockIdx.x / P;
     const int first = (int)cluster.block_rank() * kAccumulateThreads + threadIdx.x;
     // Behind hs_attend's own kernel the positions, which that one has read, may be read before its
     // end; any other kernel before this one may still be writing them.
@@ -274,15 +278,15 @@ __global__ void __launch_bounds__(kAccumulateThreads)
     const int steps = q < 0 || q >= R ? 0 : counts ? min(ld(counts + b), S) : S;
     float* dst = acc + (long long)(steps > 0 ? q : 0) * L;
     const long long row = (long long)b * S * K;
-    if (K <= kHeldEntries * kAll && steps <= kHeldSteps) {
+    if (K <= kHeldEntries * all && steps <= kHeldSteps) {
         int t[kHeldSteps][kHeldEntries];
         float w[kHeldSteps][kHeldEntries];
 #pragma unroll
         for (int s = 0; s < kHeldSteps; ++s)
 #pragma unroll
             for (int i = 0; i < kHeldEntries; ++i)
-                t[s][i] = s < steps && first + i * kAll < K
-                              ? ld(topk + row + s * K + first + i * kAll)
+                t[s][i] = s < steps && first + i * all < K
+                              ? ld(topk + row + s * K + first + i * all)
                               : -1;
         if (after_attend) wait_for_previous();  // for the weights
 #pragma unroll
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(kAccumulateThreads)
 #pragma unroll
             for (int i = 0; i < kHeldEntries; ++i) {
                 if (t[s][i] >= L) t[s][i] = -1;
-                w[s][i] = t[s][i] >= 0 ? ld(weights + row + s * K + first + i * kAll) : 0.f;
+                w[s][i] = t[s][i] >= 0 ? ld(weights + row + s * K + first + i * all) : 0.f;
             }
 #pragma unroll
         for (int s = 0; s < kHeldSteps; ++s) {
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kAccumulateThreads)
     for (int s = 0; s < steps; ++s) {
         if (s > 0) cluster.sync();
 #pragma unroll 4
-        for (int j = first; j < K; j += kAll) {
+        for (int j = first; j < K; j += all) {
             const int t = ld(topk + row + (long long)s * K + j);
             if (t >= 0 && t < L) atomicAdd(dst + t, ld(weights + row + (long long)s * K + j));
         }
@@ -318,9 +322,13 @@ __global__ void __launch_bounds__(kAccumulateThreads)
 cudaError_t launch_accumulate(const float* weights, const int32_t* topk, const int32_t* req,
                               const int32_t* counts, int32_t B, int32_t S, int32_t K, float* acc,
                               int32_t R, int32_t L, bool after_attend, cudaStream_t s) {
-    return launch_chained(accumulate_kernel, B * kAccumulateCluster, kAccumulateThreads, 0,
-                          kAccumulateCluster, s, weights, topk, req, counts, S, K, acc, R, L,
-                          after_attend);
+    constexpr int kRound = 2 * 152;  // two CTAs an SM
+    const int P = B <= kRound / 4 ? 4 : (B <= kRound / 2 ? 2 : 1);
+    return launch_chained(P == 4   ? accumulate_kernel<4>
+                          : P == 2 ? accumulate_kernel<2>
+                                   : accumulate_kernel<1>,
+                          B * P, kAccumulateThreads, 0, P, s, weights, topk, req, counts, S, K, acc, R,
+                          L, after_attend);
 }
 
 cudaError_t launch_evict(const float* acc, const int32_t* req, const int32_t* seq_lens, int32_t B,

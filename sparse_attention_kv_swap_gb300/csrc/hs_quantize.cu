@@ -15,20 +15,22 @@
 namespace hs {
 namespace {
 
-// Thread tid of a group works on part tid % parts of the tokens tid / parts,
-// + step, + 2 * step, ..: a part is 16 elements (16 bytes of codes), and the block
-// has parts * step threads, up to whole warps.  kHeld parts stay in registers; larger groups read
-// the rest twice.
+// Thread tid of a group works on part tid % parts of the tokens tid / parts, + step, + 2 * step, ..:
+// a part is 16 elements (16 bytes of codes).  A thread keeps kHeld parts in registers (half as many of
+// 32-bit input); groups too large for that at the most threads read the rest twice.
 constexpr int kHeld = 4;
-constexpr int kStep = 16;       // tokens of a turn, or a multiple
-constexpr int kMaxThreads = 448;  // two such blocks an SM leave 72 registers a thread
+constexpr int kQuantizeThreads = 448;  // two such CTAs an SM leave 72 registers a thread
+constexpr int kCompactThreads = 512;
 
-// Threads of a group of so many tokens, whole warps.
-int group_threads(int tokens, int parts) {
-    int step = kStep;
-    while (step * kHeld < tokens && 2 * step * parts <= kMaxThreads) step *= 2;
-    while (step > tokens && step > 1) step /= 2;
-    return (step * parts + 31) / 32 * 32;
+// Threads of a group of so many tokens, whole warps: the fewest whose registers hold it.  More leave
+// each too few loads on their way, fewer read twice.  4 x 8192 tokens, 8 heads of 128, bf16, with 32,
+// 64, 128 and 256 threads: 53, 42, 32 and 49 us in blocks of 64 tokens, 32, 43, 70 and 143 of 16;
+// 256 and 448 threads in blocks of 256: 49 and 44.  Compaction of 64 x 2048 tokens of that row
+// with 64, 128 and 256: 131, 97 and 149 us in blocks of 64; 256 and 512 in blocks of 256: 137 and 112.
+int group_threads(int tokens, int parts, int held, int most) {
+    const int step = (tokens + held - 1) / held;
+    const long long threads = ((long long)step * parts + 31) / 32 * 32;
+    return threads < most ? (int)threads : most;
 }
 
 // 16 consecutive input elements, as loaded.
@@ -226,7 +228,7 @@ __device__ __forceinline__ void store_row(const QuantizeArgs& a, int q, int t, i
 }
 
 template <int CODE, int DTYPE, bool CACHE>
-__global__ void __launch_bounds__(kMaxThreads, CACHE ? 1 : 2) quantize_kernel(const QuantizeArgs a) {
+__global__ void __launch_bounds__(kQuantizeThreads, CACHE ? 1 : 2) quantize_kernel(const QuantizeArgs a) {
     __shared__ float s_tmp[32];
     const int heads = a.f.num_kv_heads, D = a.f.head_dim, T = a.f.block_tokens;
     // CTAs of one block of tokens are neighbours: together they read whole rows
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kMaxThreads, CACHE ? 1 : 2) quantize_kernel(co
 }
 
 template <int CODE>
-__global__ void __launch_bounds__(512, 2) compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const CompactArgs a) {
     __shared__ float s_tmp[32];
     const int heads = a.f.num_kv_heads, D = a.f.head_dim, T = a.f.block_tokens;
     const int W = a.f.item_size_bytes;
@@ -404,7 +406,9 @@ cudaError_t launch_quantize(QuantizeArgs a, bool cache, cudaStream_t s) {
     if (!grid_of((long long)a.batch * a.windows * 2 * a.f.num_kv_heads, &grid))
         return cudaErrorInvalidConfiguration;
     const int parts = a.f.head_dim / 16;
-    const int threads = group_threads(a.max_count < T ? a.max_count : T, parts);
+    const int threads = group_threads(a.max_count < T ? a.max_count : T, parts,
+                                      a.in.dtype == HS_DTYPE_FP32 ? kHeld / 2 : kHeld,
+                                      kQuantizeThreads);
     if (a.f.code == HS_KV_E4M3)
         return cache ? quantize_dtype<HS_KV_E4M3, true>(a, grid, threads, s)
                      : quantize_dtype<HS_KV_E4M3, false>(a, grid, threads, s);
@@ -421,7 +425,7 @@ cudaError_t launch_compact(CompactArgs a, cudaStream_t s) {
         return cudaErrorInvalidConfiguration;
     a.block = Divisor::by(T);
     const int parts = a.f.head_dim / 16;
-    const int threads = group_threads(most < T ? most : T, parts);
+    const int threads = group_threads(most < T ? most : T, parts, kHeld, kCompactThreads);
     return launch_chained(
         a.f.code == HS_KV_E4M3 ? compact_kernel<HS_KV_E4M3> : compact_kernel<HS_KV_INT8>, grid,
         threads, 0, 0, s, a);
