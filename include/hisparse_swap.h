@@ -431,7 +431,8 @@ int hs_swap_in_noalloc(hs_state* st, const int32_t* req_pool_indices_dev,
  *   operations in 32 bits.  Magnitudes below 2^-100 count as 2^-100; a block
  *   of zeros has scale 0.  Infinities and NaN do not count as magnitudes:
  *   infinities get the largest code of their sign, NaN the e4m3 NaN (0 in
- *   int8).  hs_attend takes any scales, not only those. */
+ *   int8); in a block whose scale is 0 an infinity is coded as NaN is.
+ *   hs_attend takes any scales, not only those. */
 #define HS_KV_E4M3 0
 #define HS_KV_INT8 1
 #define HS_DTYPE_BF16 0
@@ -463,7 +464,7 @@ typedef struct hs_kv_input {
 /* HS_OK if the format is valid and supported.  Host only. */
 int hs_kv_format_check(const hs_kv_format* fmt);
 
-/* Quantises new tokens into a store of rows, one warp group per scale group.
+/* Quantises new tokens into a store of rows.
  * Entry b writes the tokens [start[b], start[b] + count[b]) of request req[b]:
  *   rows_dev   uint8 [num_requests, max_seq_len, W], 16-byte aligned
  *   scales_dev float [num_requests, NB, 2, Hkv]
@@ -521,7 +522,7 @@ typedef struct hs_attend_args {
 } hs_attend_args;
 
 /* Device bytes of workspace that an hs_attend call of these sizes needs (0 for
- * most: the logits of a call stay in shared memory; (size_t)-1 if the sizes are not
+ * most: a query's scores stay on the SMs that work on it; (size_t)-1 if the sizes are not
  * accepted).  Uses the batch, steps, top_k and num_heads of `args`, no pointer.  Host only. */
 size_t hs_attend_workspace_bytes(const hs_kv_format* fmt, const hs_attend_args* args);
 
@@ -534,6 +535,9 @@ size_t hs_attend_workspace_bytes(const hs_kv_format* fmt, const hs_attend_args* 
  * outside [0, num_requests) likewise.  An entry given twice counts twice.
  * Products of codes and queries are exact and summed in 32 bits; the softmax
  * statistics are 32 bits; p_j is rounded to 11 bits for the product with V.
+ * A NaN code in a selected row spoils the outputs of the heads that read it, an
+ * infinity or a NaN in a query those of its head; rows that no valid entry
+ * selects are not read.
  * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_KV_HEADS query heads.
  * Asynchronous on `stream`. */
 int hs_attend(const hs_kv_format* fmt, const hs_attend_args* args, void* stream);
