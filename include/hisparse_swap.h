@@ -544,7 +544,8 @@ int hs_attend(const hs_kv_format* fmt, const hs_attend_args* args, void* stream)
 
 /* acc[req[b], topk[b, s, j]] += weights[b, s, j] for s < counts[b] (all steps
  * if counts_dev is NULL), the steps one after the other, so that the sums do
- * not depend on timing (the entries of one step being distinct).  Entries
+ * not depend on timing (the entries of one step and the requests of one call
+ * being distinct).  Entries
  * outside [0, max_seq_len), steps past num_steps and requests outside
  * [0, num_requests) are skipped.  For speculative decoding, call it once the
  * accepted steps are known, and hs_attend without acc_dev. */

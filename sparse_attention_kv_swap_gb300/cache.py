@@ -114,6 +114,13 @@ class SwapInCache:
         [R, max_seq_len].  Kept rows move to the first positions of the host pools;
         scales[layer] and acc[layer] follow; the requests' cache state is reset and
         their new lengths are returned.  Needs budget rows of device memory per request."""
+        if not 0 <= recent <= budget or budget < 1:
+            raise ValueError("need 0 <= recent <= budget and budget >= 1")
+        if len(requests) != len(seq_lens) or any(not 0 <= n <= self.cfg.max_seq_len
+                                                 for n in seq_lens):
+            raise ValueError("need a length from 0 to %d for every request" % self.cfg.max_seq_len)
+        if not requests:
+            return []
         kept = [min(n, budget) for n in seq_lens]
         nb = fmt.num_blocks(budget)
         ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(

@@ -834,3 +834,23 @@ def test_decode_example(code, dtype, heads, group, D, T):
         assert np.array_equal(d.acc.cpu().numpy(), acc)
     assert cut == 5 and d.cache.status() == (B.HS_OK, 0)
     d.cache.close()
+
+
+def test_cache_evict_refuses_before_it_acts():
+    from sparse_attention_kv_swap_gb300.cache import SwapInCache
+    cfg = pkg.make_config(2, 40, 256, 16, 8, 1)
+    fmt = pkg.make_kv_format(2, 64, 16)
+    cache = SwapInCache(cfg)
+    cache.host_pools[0].random_(0, 120)
+    pool = cache.host_pools[0].clone()
+    scales, acc = [cache.kv_scales(fmt) + 1], [torch.ones((2, 40), device="cuda")]
+    for requests, lens, budget, recent in (([0], [40], 8, 9), ([0], [40], 8, -1), ([0], [40], 0, 0),
+                                           ([0, 1], [40], 8, 2), ([0], [41], 8, 2),
+                                           ([0], [-1], 8, 2)):
+        with pytest.raises(ValueError):
+            cache.evict(fmt, scales, acc, requests, lens, budget, recent)
+    assert cache.evict(fmt, scales, acc, [], [], 8, 2) == []
+    assert cache.evict(fmt, scales, acc, [1], [0], 8, 2) == [0]  # nothing to keep
+    torch.cuda.synchronize()
+    assert torch.equal(cache.host_pools[0], pool)
+    cache.close()
