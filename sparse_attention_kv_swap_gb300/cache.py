@@ -113,12 +113,9 @@ class SwapInCache:
         the last `recent` and those of the largest accumulated weight acc[layer]
         [R, max_seq_len].  Kept rows move to the first positions of the host pools;
         scales[layer] and acc[layer] follow; the requests' cache state is reset and
-        their new lengths are returned.  Needs budget rows of device memory per request."""
-        if not 0 <= recent <= budget or budget < 1:
-            raise ValueError("need 0 <= recent <= budget and budget >= 1")
-        if len(requests) != len(seq_lens) or any(not 0 <= n <= self.cfg.max_seq_len
-                                                 for n in seq_lens):
-            raise ValueError("need a length from 0 to %d for every request" % self.cfg.max_seq_len)
+        their new lengths are returned.  Needs budget rows of device memory per request.
+        Arguments that do not fit the cache raise ValueError before anything changes."""
+        self._check_evict(fmt, scales, acc, requests, seq_lens, budget, recent)
         if not requests:
             return []
         kept = [min(n, budget) for n in seq_lens]
@@ -150,6 +147,30 @@ class SwapInCache:
                 acc[layer][req.long()] = 0
                 acc[layer][req.long(), :budget] = sums[:, :self.cfg.max_seq_len]
         return kept
+
+    def _check_evict(self, fmt, scales, acc, requests, seq_lens, budget, recent) -> None:
+        """The arguments of evict, on the host: layers are cut one after the other, and indexing
+        by a request knows no range, so nothing may be refused once the first kernel runs."""
+        cfg = self.cfg
+        R, L = cfg.num_requests, cfg.max_seq_len
+        if not 0 <= recent <= budget or budget < 1:
+            raise ValueError("need 0 <= recent <= budget and budget >= 1")
+        if len(requests) != len(seq_lens) or any(not 0 <= n <= L for n in seq_lens):
+            raise ValueError("need a length from 0 to %d for every request" % L)
+        if any(not 0 <= q < R for q in requests) or len(set(requests)) != len(requests):
+            raise ValueError("requests must be distinct and from 0 to %d" % (R - 1))
+        rc = B.load_library().hs_kv_format_check(fmt)
+        if rc != B.HS_OK or fmt.item_size_bytes != cfg.item_size_bytes:
+            raise ValueError("the format must be valid and its rows %d bytes wide"
+                             % cfg.item_size_bytes)
+        for name, given, shape in (("scales", scales, fmt.scales_shape(R, L)),
+                                   ("acc", acc, (R, L))):
+            if len(given) != cfg.num_layers or any(
+                    t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous()
+                    or t.device != self.device_kv[0].device for t in given):
+                raise ValueError("%s must hold a contiguous float32 tensor %s for each of the %d "
+                                 "layers, on the cache's device" % (name, tuple(shape),
+                                                                    cfg.num_layers))
 
     def reset_requests(self, req_pool_indices: torch.Tensor, stream=None) -> None:
         B.hs_reset_requests(self.handle, req_pool_indices, stream)

@@ -1,0 +1,57 @@
+"""The 8-bit key/value row calls where they could go wrong, on the CPU."""
+import pytest
+import torch
+
+import sparse_attention_kv_swap_gb300 as pkg
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_attention_kv_swap_gb300 import binding, build
+    build.build()
+    return binding.load_library()
+
+
+def cpu_cache(R=3, L=40, W=256, layers=2):
+    """A cache without a handle, its tensors in host memory: a call that is refused on the
+    host needs no more."""
+    from sparse_attention_kv_swap_gb300.cache import SwapInCache
+    cache = SwapInCache.__new__(SwapInCache)
+    cache.cfg = pkg.make_config(R, L, W, 16, 8, 1, num_layers=layers)
+    cache.device = torch.device("cpu")
+    cache.host_pools = [torch.zeros((R, L, W), dtype=torch.uint8) for _ in range(layers)]
+    cache.device_kv = [torch.zeros((R * 24, W), dtype=torch.uint8) for _ in range(layers)]
+    return cache
+
+
+def evict_refusals(make):
+    """(arguments of evict that a cache of 3 requests of 40 tokens in 2 layers refuses), each from
+    fresh scales and sums of make(shape)."""
+    fmt = pkg.make_kv_format(2, 64, 16)
+    good = dict(requests=[0, 2], seq_lens=[40, 30], budget=8, recent=2)
+
+    def scales(R=3, blocks=3, n=2):
+        return [make((R, blocks, 2, 2)) for _ in range(n)]
+
+    def acc(R=3, L=40, n=2):
+        return [make((R, L)) for _ in range(n)]
+
+    bad = [dict(requests=[0, -1]), dict(requests=[0, 3]), dict(requests=[2, 2]),
+           dict(requests=[1 << 40, 0]), dict(requests=[0]), dict(seq_lens=[40, 41]),
+           dict(seq_lens=[-1, 0]), dict(budget=0, recent=0), dict(recent=9), dict(recent=-1),
+           dict(scales=scales(n=1)), dict(scales=scales(n=3)), dict(scales=scales(blocks=2)),
+           dict(scales=scales(R=2)), dict(scales=[x.half() for x in scales()]),
+           dict(scales=[x.transpose(0, 2).contiguous().transpose(0, 2) for x in scales()]),
+           dict(acc=acc(n=1)), dict(acc=acc(L=39)), dict(acc=acc(R=4)),
+           dict(acc=[x.double() for x in acc()]), dict(acc=[acc(n=1)[0], acc(L=41, n=1)[0]]),
+           dict(fmt=pkg.make_kv_format(1, 64, 16)),  # narrower rows than the cache's
+           dict(fmt=pkg.HsKvFormat(1, 100, 16, pkg.HS_KV_E4M3, 256))]  # no such head size
+    for kw in bad:
+        yield {**dict(fmt=fmt, scales=scales(), acc=acc()), **good, **kw}
+
+
+def test_cache_evict_refuses_on_the_host(lib):
+    cache = cpu_cache()
+    for kw in evict_refusals(torch.ones):
+        with pytest.raises(ValueError):
+            cache.evict(**kw)
