@@ -365,6 +365,11 @@ class StateHandle:
         self.device = device  # the CUDA device the handle and its buffers are on
         self._keep = list(keep)
 
+    def pool_ptr(self, t) -> Optional[int]:
+        """Address of `t` if it is one of the handle's host pools (which may be pageable), or None."""
+        at = t.data_ptr()
+        return at if any(at == x.data_ptr() for x in self._keep[:self.cfg.num_layers]) else None
+
     def close(self) -> None:
         if self.ptr:
             load_library().hs_destroy_state(self.ptr)
@@ -818,9 +823,10 @@ def hs_evict(acc, req, seq_lens, recent: int, keep, kept, kept_acc=None, stream=
 
 
 def hs_compact_kv(fmt: HsKvFormat, src_rows, src_scales, src_req, keep, kept, dst_rows,
-                  dst_scales, dst_req, stream=None) -> None:
+                  dst_scales, dst_req, stream=None, handle: Optional[StateHandle] = None) -> None:
     """Moves the kept tokens (hs_evict's keep and kept) of requests src_req of one
-    store of rows to the first places of requests dst_req of another."""
+    store of rows to the first places of requests dst_req of another.  src_rows that are a
+    host pool of `handle` may be of any memory that the handle has accepted."""
     import torch
     sR, sL = _store(fmt, src_rows, src_scales, "src_")
     dR, dL = _store(fmt, dst_rows, dst_scales, "dst_")
@@ -833,8 +839,10 @@ def hs_compact_kv(fmt: HsKvFormat, src_rows, src_scales, src_req, keep, kept, ds
         _shape(src_req, one, "src_req")
         _shape(dst_req, one, "dst_req")
     i32, f32, u8, dev = torch.int32, torch.float32, torch.uint8, _device_of(keep, "keep")
-    _run("hs_compact_kv", dev, fmt,
-         _ptr(src_rows, u8, "src_rows", dev), _ptr(src_scales, f32, "src_scales", dev), sR, sL,
+    src = handle.pool_ptr(src_rows) if handle is not None else None
+    if src is None:
+        src = _ptr(src_rows, u8, "src_rows", dev)
+    _run("hs_compact_kv", dev, fmt, src, _ptr(src_scales, f32, "src_scales", dev), sR, sL,
          _ptr(src_req, i32, "src_req", dev), _ptr(keep, i32, "keep", dev),
          _ptr(kept, i32, "kept", dev), B, budget, _ptr(dst_rows, u8, "dst_rows", dev),
          _ptr(dst_scales, f32, "dst_scales", dev), dR, dL, _ptr(dst_req, i32, "dst_req", dev),

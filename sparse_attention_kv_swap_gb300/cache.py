@@ -141,7 +141,7 @@ class SwapInCache:
                 B.hs_evict(acc[layer], req, lens, recent, keep, count, sums)
                 new = torch.zeros((len(requests), nb, 2, fmt.num_kv_heads), device=self.device)
                 B.hs_compact_kv(fmt, self.host_pools[layer], scales[layer], req, keep, count,
-                                rows, new, at)
+                                rows, new, at, handle=self.handle)
                 self.append_rows(req[row], pos.to(torch.int32), count[row], rows[row, pos], layer)
                 scales[layer][req.long(), :nb] = new[:, :scales[layer].shape[1]]
                 acc[layer][req.long()] = 0
@@ -163,6 +163,10 @@ class SwapInCache:
         if rc != B.HS_OK or fmt.item_size_bytes != cfg.item_size_bytes:
             raise ValueError("the format must be valid and its rows %d bytes wide"
                              % cfg.item_size_bytes)
+        if any(p.shape != (R, L, cfg.item_size_bytes) or p.dtype != torch.uint8
+               for p in self.host_pools):
+            raise ValueError("the host pools must be uint8 [%d, %d, %d]"
+                             % (R, L, cfg.item_size_bytes))
         for name, given, shape in (("scales", scales, fmt.scales_shape(R, L)),
                                    ("acc", acc, (R, L))):
             if len(given) != cfg.num_layers or any(

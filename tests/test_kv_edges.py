@@ -55,3 +55,13 @@ def test_cache_evict_refuses_on_the_host(lib):
     for kw in evict_refusals(torch.ones):
         with pytest.raises(ValueError):
             cache.evict(**kw)
+
+
+def test_cache_evict_refuses_pools_of_another_shape(lib):
+    kw = next(evict_refusals(torch.ones))
+    kw["requests"] = [0, 2]
+    cache = cpu_cache()
+    for pool in (cache.host_pools[1].view(-1), cache.host_pools[1].view(torch.int8)):
+        cache.host_pools[1] = pool
+        with pytest.raises(ValueError, match="host pools"):
+            cache.evict(**kw)
