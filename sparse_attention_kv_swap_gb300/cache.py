@@ -113,13 +113,17 @@ class SwapInCache:
         the last `recent` and those of the largest accumulated weight acc[layer]
         [R, max_seq_len].  Kept rows move to the first positions of the host pools;
         scales[layer] and acc[layer] follow; the requests' cache state is reset and
-        their new lengths are returned.  Needs budget rows of device memory per request.
+        their new lengths are returned.  Bytes of a row past its keys and values move with it
+        (the call then waits for the stream in every layer).  Needs budget rows of device
+        memory per request.
         Arguments that do not fit the cache raise ValueError before anything changes."""
         self._check_evict(fmt, scales, acc, requests, seq_lens, budget, recent)
         if not requests:
             return []
         kept = [min(n, budget) for n in seq_lens]
         nb = fmt.num_blocks(budget)
+        used = 2 * fmt.num_kv_heads * fmt.head_dim
+        owner = torch.tensor(requests)[:, None]
         ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(
             torch.cuda.current_stream(self.device))
         with torch.cuda.device(self.device), ctx:
@@ -137,11 +141,14 @@ class SwapInCache:
             rows = torch.empty((len(requests), budget, self.cfg.item_size_bytes),
                                dtype=torch.uint8, device=self.device)
             self.reset_requests(req)
-            for layer in range(self.cfg.num_layers):
+            for layer, pool in enumerate(self.host_pools):
                 B.hs_evict(acc[layer], req, lens, recent, keep, count, sums)
                 new = torch.zeros((len(requests), nb, 2, fmt.num_kv_heads), device=self.device)
-                B.hs_compact_kv(fmt, self.host_pools[layer], scales[layer], req, keep, count,
-                                rows, new, at, handle=self.handle)
+                B.hs_compact_kv(fmt, pool, scales[layer], req, keep, count, rows, new, at,
+                                handle=self.handle)
+                if used < self.cfg.item_size_bytes:  # on the host, which has the pool at hand
+                    index = keep.cpu().clamp_(min=0).long()
+                    rows[..., used:] = pool[owner, index, used:].to(self.device)
                 self.append_rows(req[row], pos.to(torch.int32), count[row], rows[row, pos], layer)
                 scales[layer][req.long(), :nb] = new[:, :scales[layer].shape[1]]
                 acc[layer][req.long()] = 0

@@ -98,3 +98,12 @@ def test_cache_evict_from_pageable_pools():
         return
     e.check([2, 0], [90, 37], 40, 7)
     e.cache.close()
+
+
+@pytest.mark.parametrize("W", [272, 400])
+def test_cache_evict_moves_the_whole_row(W):
+    """Rows wider than their keys and values: the other bytes stay with their token."""
+    e = Evicted(np.random.default_rng(W), W=W)
+    e.check([1, 2, 0], [90, 61, 12], 33, 4)
+    e.check([2], [33], 20, 0)
+    e.cache.close()
