@@ -534,7 +534,8 @@ size_t hs_attend_workspace_bytes(const hs_kv_format* fmt, const hs_attend_args* 
  * all masked gets out 0, lse -inf and weights 0; one whose request lies
  * outside [0, num_requests) likewise.  An entry given twice counts twice.
  * Products of codes and queries are exact and summed in 32 bits; the softmax
- * statistics are 32 bits; p_j is rounded to 11 bits for the product with V.
+ * statistics are 32 bits; p_j times the V scale is rounded to 11 bits for the product
+ * with the V codes (or by 2^-39 of the largest such term of the head, if that is more).
  * A NaN code in a selected row spoils the outputs of the heads that read it, an
  * infinity or a NaN in a query those of its head; rows that no valid entry
  * selects are not read.

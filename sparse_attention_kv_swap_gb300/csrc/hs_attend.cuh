@@ -24,10 +24,14 @@
 //      ldmatrix transposes V, so that a word holds four tokens of one d.  The
 //      rows of a K tile are taken in the order 0, 1, 4, 5, .. | 2, 3, 6, 7, ..
 //      so that the transposed P (movmatrix) pairs the same tokens.  P is
-//      exp(s - max) times the token's V scale over the largest V scale of the
-//      task, so it lies in [0, 1] and is rounded to f16 (11 bits): its rounding
-//      error, at most 2^-12 of each term, is far below the output's own 8 or
-//      11 bits.
+//      exp(s - max) times the token's V scale, brought by powers of two to where
+//      the largest one of a head in the task lies near f16's top, and rounded
+//      to f16: by 2^-11 of each at most, or 2^-39 of the largest one where that
+//      is more.  That is an eighth of a bf16 output's own rounding, and as much
+//      as an f16 output's (against 64 bits, f16 outputs of the timed cases are
+//      off by 2.3 to 3.0e-4 of their norm; 2.1e-4 with P in 32 bits).  The scale
+//      belongs to the largest product of P and V scale, not to the largest V scale:
+//      that one may belong to a token of no weight.
 // With 4 query heads to a K/V head or fewer, one fragment takes two tiles: the
 // 8 columns are the heads of the first tile and again those of the second, the
 // queries lying in both halves, and each lane keeping its tile's product.  Scores,
@@ -153,6 +157,12 @@ __device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float log2_fast(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -797,9 +807,11 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         const int v_row = lane & 15;
 
         // ---- scores --------------------------------------------------------------
-        float top[N][2];  // of heads 2 c and 2 c + 1
+        float top[N][2];   // of heads 2 c and 2 c + 1
+        float most[N][2];  // largest of score + log2(V scale)
 #pragma unroll
-        for (int nt = 0; nt < N; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+        for (int nt = 0; nt < N; ++nt)
+            top[nt][0] = top[nt][1] = most[nt][0] = most[nt][1] = -INFINITY;
         // Columns 0-3 and 4-7 belong to the two tiles of a fragment.
         const uint32_t own[2] = {F == 1 || g < 4 ? ~0u : 0u, g >= 4 ? ~0u : 0u};
         for (int i = 0; i < n; i += F) {
@@ -835,6 +847,8 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
             const bool on1 = mine < n && tile0 * 16 + t0 + 2 < live;
             const float2 kk = *reinterpret_cast<const float2*>(sk + (mine < n ? mine : 0) * 16 + 2 * g);
             const float k0 = kk.x, k1 = kk.y;
+            const float2 vv = *reinterpret_cast<const float2*>(sv + (mine < n ? mine : 0) * 16 + 2 * g);
+            const float v0 = log2_fast(vv.x), v1 = log2_fast(vv.y);
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
@@ -843,6 +857,7 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
                     z[nt][k] = on0 ? z[nt][k] * (k0 * f) : -INFINITY;
                     z[nt][k + 2] = on1 ? z[nt][k + 2] * (k1 * f) : -INFINITY;
                     top[nt][k] = fmaxf(top[nt][k], fmaxf(z[nt][k], z[nt][k + 2]));
+                    most[nt][k] = fmaxf(most[nt][k], fmaxf(z[nt][k] + v0, z[nt][k + 2] + v1));
                 }
             }
             scores.store(i / F, z);
@@ -858,25 +873,27 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         // ---- softmax over the task's tokens ----------------------------------------
         scores.stored();
         float safe[N][2], sum[N][2];
+        uint32_t up[N];  // of both heads, the upper half of the float 2^-e
 #pragma unroll
         for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 top[nt][k] = max_over_g(top[nt][k]);
-                if (F == 2)  // the head's other tiles
+                most[nt][k] = max_over_g(most[nt][k]);
+                if (F == 2) {  // the head's other tiles
                     top[nt][k] = fmaxf(top[nt][k], __shfl_xor_sync(0xffffffffu, top[nt][k], 2));
+                    most[nt][k] = fmaxf(most[nt][k], __shfl_xor_sync(0xffffffffu, most[nt][k], 2));
+                }
                 if (g == 0)
                     at.max[sub * HP + h * GP + j0 + nt * 8 + column_head<NT>(c) + k] = top[nt][k];
                 safe[nt][k] = top[nt][k] == -INFINITY ? 0.f : top[nt][k];
+                // The head's largest product of P and V scale goes to 2^14.5 .. 2^15.5.
+                const int e = __float2int_rn(most[nt][k] - safe[nt][k] - 15.f);
+                const uint32_t half = (uint32_t)(127 - min(max(e, -126), 126)) << 7;
+                up[nt] = k == 0 ? half : up[nt] | half << 16;
                 sum[nt][k] = 0.f;
             }
         }
-        float ref = 0.f;  // largest V scale of the task's tokens
-        for (int i = lane; i < n * 16; i += 32) ref = fmaxf(ref, sv[i]);
-        ref = max_over_g(ref);
-        ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, 1));
-        ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, 2));
-        const float inv = ref > 0.f ? 1.f / ref : 0.f;
 
         // ---- values --------------------------------------------------------------
         float o[STEPS][N][4] = {};
@@ -884,10 +901,11 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
             float z[N][4];
             scores.load(i / F, z);
             const int mine = F == 1 ? i : i + (c >> 1) < n ? i + (c >> 1) : i;
-            const float2 vv = *reinterpret_cast<const float2*>(sv + mine * 16 + 2 * g);
-            const float v0 = vv.x * inv, v1 = vv.y * inv;
             uint32_t tile = next_item(n + i);
             scores.loaded(z);
+            // the scales last, for the registers
+            const float2 vv = *reinterpret_cast<const float2*>(sv + mine * 16 + 2 * g);
+            const float v0 = vv.x, v1 = vv.y;
             uint32_t pf[N][2];
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
@@ -897,8 +915,11 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
                 const float p3 = exp2_fast(z[nt][3] - safe[nt][1]);
                 sum[nt][0] += p0 + p2;
                 sum[nt][1] += p1 + p3;
-                pf[nt][0] = transpose(pack_half2(p0 * v0, p1 * v0));
-                pf[nt][1] = transpose(pack_half2(p2 * v1, p3 * v1));
+                // P first: the V scale may be any of 32 bits' where P is 0
+                const float u0 = __uint_as_float(up[nt] << 16);
+                const float u1 = __uint_as_float(up[nt] & 0xffff0000u);
+                pf[nt][0] = transpose(pack_half2(p0 * u0 * v0, p1 * u1 * v0));
+                pf[nt][1] = transpose(pack_half2(p2 * u0 * v1, p3 * u1 * v1));
             }
 #pragma unroll
             for (int f = 0; f < F; ++f) {
@@ -954,7 +975,8 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                fold[nt][k] = ref;
+                const uint32_t u = k == 0 ? up[nt] << 16 : up[nt] & 0xffff0000u;
+                fold[nt][k] = __uint_as_float(0x7f000000u - u);  // 2^e
                 if (a.nsub > 1) {
                     const int to = h * GP + j0 + nt * 8 + column_head<NT>(c) + k;
                     float m = -INFINITY;

@@ -6,7 +6,7 @@ import torch
 import kv_reference as ref
 import sparse_attention_kv_swap_gb300 as pkg
 from sparse_attention_kv_swap_gb300 import binding as B
-from test_gpu_kv_rows import dev
+from test_gpu_kv_rows import Attend, dev
 from test_kv_edges import evict_refusals
 
 pytestmark = pytest.mark.gpu
@@ -107,3 +107,70 @@ def test_cache_evict_moves_the_whole_row(W):
     e.check([1, 2, 0], [90, 61, 12], 33, 4)
     e.check([2], [33], 20, 0)
     e.cache.close()
+
+
+# ---- attention: V scales far apart ----------------------------------------------
+
+@pytest.mark.parametrize("light", [True, False], ids=["quiet", "even"])
+@pytest.mark.parametrize("gap", [12, 16, 20, 24, 30, 60, 90])
+@pytest.mark.parametrize("heads,G,D,K,code", [(2, 4, 128, 300, "e4m3"), (1, 16, 64, 1000, "int8"),
+                                              (2, 6, 256, 90, "int8"), (1, 8, 192, 60, "e4m3")])
+def test_attend_v_scales_far_apart(heads, G, D, K, code, gap, light):
+    """A block in five has V scales 2^gap times the others', on tokens whose weight makes up for
+    the scale, or for e^20 times that.  Bound: as for any scales, with f16's smallest step
+    counted from the largest product of weight and V scale: 2^-25 of 2^14.5 for every entry."""
+    rng = np.random.default_rng(gap + D)
+    a = Attend(rng, 2, 1, K, heads, G, D, 4, code, "bf16")
+    used = np.unique(a.locs[a.locs >= 0])
+    loud = (a.topk // a.T) % 5 == 0
+    a.scales[:, :, 1] *= 2.0 ** -gap
+    a.scales[:, ::5, 1] *= 2.0 ** gap
+    # channel 0 of K alone carries the gap in the scores
+    a.q[..., 0] = 1
+    a.rows[used[:, None], np.arange(heads)[None] * D] = 0
+    one = {"e4m3": 0x70, "int8": 64}[code]  # 128 (e4m3), 64
+    value = {"e4m3": 128.0, "int8": 64.0}[code]
+    for b in range(2):
+        at = a.locs[b, 0][loud[b, 0] & (a.locs[b, 0] >= 0)]
+        a.rows[at[:, None], np.arange(heads)[None] * D] = one
+    a.scales[:, :, 0] = 2.0 ** -7
+    down = -(gap * np.log(2.0) + (20.0 if light else 0.0))
+    a.q[..., 0] = float(np.float32(down / (value * 2.0 ** -7 * a.sm_scale)))
+    want = a.reference()
+    out = a.run()[0].cpu().double().numpy()
+    assert np.isfinite(out).all()
+    x = ref.decode_table(code)[a.rows[..., :2 * heads * D]].reshape(a.N, 2, heads, D)
+    u = torch.finfo(torch.bfloat16).eps / 2
+    dz = (D + 8) * 2.0 ** -23 * want["logit"] + 2.0 ** -20 + K * 2.0 ** -24
+    for b in range(2):
+        ok = a.locs[b, 0] >= 0
+        k = x[a.locs[b, 0, ok], 0] * a.scales[a.req[b], a.topk[b, 0, ok] // 4, 0][..., None]
+        v = a.scales[a.req[b], a.topk[b, 0, ok] // 4, 1].astype(np.float64)
+        for i in range(heads * G):
+            z = (k[:, i // G] @ a.q.double().numpy()[b, 0, i]) * a.sm_scale
+            most = (np.exp(z - want["lse"][b, 0, i]) * v[:, i // G]).max()
+            tol = (u * np.abs(want["out"][b, 0, i])
+                   + want["spread"][b, 0, i] * (2.0 ** -11 + 2 * dz[b, 0, i]) * (1 + u)
+                   + K * 2.0 ** -39 * most * 448 + 1e-37)
+            err = np.abs(out[b, 0, i] - want["out"][b, 0, i])
+            assert (err <= tol).all(), (b, i, (err / tol).max())
+
+
+@pytest.mark.parametrize("exponent", [-140, -126, -110, 100, 120])
+def test_attend_v_scales_of_any_size(exponent):
+    """V scales near either end of 32 bits, the codes so small or large that the output is in
+    range."""
+    rng = np.random.default_rng(200 + exponent)
+    a = Attend(rng, 2, 1, 120, 2, 4, 64, 8, "e4m3", "bf16")
+    a.scales[:, :, 1] = 2.0 ** exponent
+    if exponent > 0:  # V codes 2^-9 .. 2^-6
+        used = np.unique(a.locs[a.locs >= 0])
+        a.rows[used, 128:256] = rng.integers(1, 9, (used.size, 128))
+    want = a.reference()
+    out = a.run()[0].cpu().double().numpy()
+    u = torch.finfo(torch.bfloat16).eps / 2
+    dz = (64 + 8) * 2.0 ** -23 * want["logit"] + 2.0 ** -20 + 120 * 2.0 ** -24
+    tol = (u * np.abs(want["out"]) + want["spread"] * (2.0 ** -11 + 2 * dz[..., None]) * (1 + u)
+           + 120 * 2.0 ** -39 * 2.0 ** exponent * 448 + 2.0 ** -134)
+    err = np.abs(out - want["out"])
+    assert (err <= tol).all(), (err / tol).max()
