@@ -14,8 +14,8 @@ constexpr size_t kStatic = 512;                    // static arrays of the kerne
 constexpr size_t kMaxSmem = kSmSmem - 1024 - kStatic;
 constexpr size_t kHalfSmem = kSmSmem / 2 - 1024 - kStatic;  // two CTAs an SM
 
-// Memory of a CTA for a cluster of P, and the shape that follows from P.
-void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, AttendShape* sh) {
+// Memory of a CTA for a cluster of P with at most `most` warps a CTA, and the shape that follows.
+void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, int most, AttendShape* sh) {
     AttendKernelArgs& k = sh->a;
     sh->P = P;
     const long long chunks = ((long long)a.top_k + 15) / 16;
@@ -23,7 +23,6 @@ void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, AttendSh
     if (k.TS == 0) k.TS = 16;
     k.TC = k.TS + 4;  // scale rows in different banks
     const int D = f.head_dim, G = a.num_heads / f.num_kv_heads;
-    const int most = attend_warps(D, sh->spill);
     int columns, groups, nsub, task_tiles;
     const auto split = [&](int nt) {
         sh->nt = nt;
@@ -35,6 +34,7 @@ void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, AttendSh
         nsub = groups >= 8 ? 1 : (8 + groups - 1) / groups;
         if (nsub > 1 && groups * nsub > most) nsub = most / groups;
         if (nsub > k.TS / 16) nsub = k.TS / 16;
+        if (nsub < 1) nsub = 1;
         task_tiles = (k.TS / 16 + nsub - 1) / nsub;
     };
     // Query heads a warp serves with one reading of keys and values.  Up to 4 heads, a fragment of
@@ -146,12 +146,17 @@ AttendShape first_shape(const hs_kv_format& f, const hs_attend_args& a) {
     std::memset(&sh, 0, sizeof(sh));
     for (int pass = 0; pass < 2; ++pass) {
         for (int P = 1; P <= kMaxCluster && (pass == 1 || worth(a, P)); ++P) {
-            set_cluster(f, a, P, &sh);
+            set_cluster(f, a, P, attend_warps(f.head_dim, false), &sh);
             if (fits(sh, kMaxSmem)) return sh;
         }
     }
+    // Wide outputs of many heads leave no room for the queues of that many warps (128 heads of 256
+    // are 133 KB, the queues of 8 warps 98): as many as fit, and at least one does, take more turns.
     sh.spill = true;
-    set_cluster(f, a, kMaxCluster, &sh);
+    for (int most = attend_warps(f.head_dim, true); most > 0; --most) {
+        set_cluster(f, a, kMaxCluster, most, &sh);
+        if (fits(sh, kMaxSmem)) break;
+    }
     return sh;
 }
 
@@ -162,7 +167,7 @@ AttendShape shape_of(const hs_kv_format& f, const hs_attend_args& a) {
     double least = cost(f, a, best);
     AttendShape sh = best;
     for (int P = best.P + 1; P <= kMaxCluster && worth(a, P); P += P < 8 ? 1 : 2) {
-        set_cluster(f, a, P, &sh);
+        set_cluster(f, a, P, attend_warps(f.head_dim, false), &sh);
         if (!fits(sh, kMaxSmem)) continue;
         const double t = cost(f, a, sh);
         if (t < least) least = t, best = sh;

@@ -174,3 +174,21 @@ def test_attend_v_scales_of_any_size(exponent):
            + 120 * 2.0 ** -39 * 2.0 ** exponent * 448 + 2.0 ** -134)
     err = np.abs(out - want["out"])
     assert (err <= tol).all(), (err / tol).max()
+
+
+# ---- attention: many wide heads ---------------------------------------------------
+
+@pytest.mark.parametrize("heads,G,D,K,code", [(32, 4, 192, 64, "e4m3"), (64, 2, 192, 130, "int8"),
+                                              (96, 1, 192, 40, "e4m3"), (128, 1, 192, 300, "e4m3"),
+                                              (14, 9, 192, 0, "e4m3"), (40, 3, 256, 90, "int8"),
+                                              (128, 1, 256, 64, "e4m3"), (112, 1, 256, 1, "int8"),
+                                              (8, 16, 256, 8192, "e4m3"), (1, 128, 256, 8192, "int8"),
+                                              (16, 8, 256, 5000, "e4m3")])
+def test_attend_many_wide_heads(heads, G, D, K, code):
+    """Head layouts whose outputs leave room for fewer warps than usual."""
+    rng = np.random.default_rng(heads + D + K)
+    a = Attend(rng, 2 if K < 1000 else 1, 2 if K < 100 else 1, K, heads, G, D, 16, code, "bf16")
+    B_, S = a.topk.shape[:2]
+    n = pkg.hs_attend_workspace_bytes(a.fmt, B_, S, K, heads * G)
+    ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") if n else None
+    a.check(a.run(workspace=ws))

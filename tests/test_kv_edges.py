@@ -1,4 +1,7 @@
 """The 8-bit key/value row calls where they could go wrong, on the CPU."""
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -65,3 +68,27 @@ def test_cache_evict_refuses_pools_of_another_shape(lib):
         cache.host_pools[1] = pool
         with pytest.raises(ValueError, match="host pools"):
             cache.evict(**kw)
+
+
+def run_cuda_program(name, tmp_path):
+    """Compiles tests/c/<name>.cu, which needs no GPU, and returns what it prints."""
+    from sparse_attention_kv_swap_gb300 import build
+    try:
+        nvcc = build._nvcc()
+    except Exception:
+        pytest.skip("no nvcc")
+    exe = str(tmp_path / name)
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "c", name + ".cu")
+    cmd = ([nvcc] + build.ARCH_FLAGS + build.NVCC_FLAGS
+           + ["-I", build.INCLUDE, "-I", build.CSRC, src, "-o", exe])
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    res = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout + res.stderr
+    return res.stdout
+
+
+def test_attend_shapes_fit_an_sm(tmp_path):
+    """Every head size, head layout and length that hs_attend accepts gets a launch shape that
+    an SM can run."""
+    assert run_cuda_program("attend_shapes", tmp_path).startswith("ok ")
