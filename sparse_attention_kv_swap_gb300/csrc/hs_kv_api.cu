@@ -10,7 +10,13 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 int32_t blocks_of(const hs_kv_format* f, int32_t L) { return (L - 1) / f->block_tokens + 1; }
 
-int result(cudaError_t e) { return e == cudaSuccess ? HS_OK : HS_ERR_CUDA; }
+// The runtime keeps a failure as its last error, which the next call that asks for it would
+// report as its own.
+int result(cudaError_t e) {
+    if (e == cudaSuccess) return HS_OK;
+    cudaGetLastError();
+    return HS_ERR_CUDA;
+}
 
 constexpr int32_t kMaxCtas = 0x7fffffff;
 

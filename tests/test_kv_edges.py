@@ -92,3 +92,7 @@ def test_attend_shapes_fit_an_sm(tmp_path):
     """Every head size, head layout and length that hs_attend accepts gets a launch shape that
     an SM can run."""
     assert run_cuda_program("attend_shapes", tmp_path).startswith("ok ")
+
+
+def test_a_failed_launch_leaves_no_error_behind(tmp_path):
+    assert run_cuda_program("kv_errors", tmp_path).startswith("ok")
