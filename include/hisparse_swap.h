@@ -578,8 +578,8 @@ int hs_evict(const float* acc_dev, const int32_t* req_dev, const int32_t* seq_le
  * destination's length.  A keep entry outside the source makes its row zeros;
  * an entry with a request out of range is skipped.
  *   src/dst_rows_dev uint8 [R, L, W], src/dst_scales_dev float [R, NB, 2, Hkv]
- * Source and destination must not overlap; the destination requests of one
- * call must be distinct.  Asynchronous on `stream`. */
+ * Source and destination must not overlap, neither rows nor scales; the
+ * destination requests of one call must be distinct.  Asynchronous on `stream`. */
 int hs_compact_kv(const hs_kv_format* fmt, const void* src_rows_dev, const float* src_scales_dev,
                   int32_t src_requests, int32_t src_seq_len, const int32_t* src_req_dev,
                   const int32_t* keep_dev, const int32_t* kept_dev, int32_t batch, int32_t budget,

@@ -8,6 +8,10 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+bool overlap(const void* p, size_t p_bytes, const void* q, size_t q_bytes) {
+    return (uintptr_t)p < (uintptr_t)q + q_bytes && (uintptr_t)q < (uintptr_t)p + p_bytes;
+}
+
 int32_t blocks_of(const hs_kv_format* f, int32_t L) { return (L - 1) / f->block_tokens + 1; }
 
 // The runtime keeps a failure as its last error, which the next call that asks for it would
@@ -214,11 +218,12 @@ int hs_compact_kv(const hs_kv_format* fmt, const void* src_rows_dev, const float
         !aligned(dst_scales_dev, 4) || !aligned(src_req_dev, 4) || !aligned(keep_dev, 4) ||
         !aligned(kept_dev, 4) || !aligned(dst_req_dev, 4))
         return HS_ERR_INVALID_ARG;
-    const size_t W = fmt->item_size_bytes;
-    const uintptr_t src = (uintptr_t)src_rows_dev, dst = (uintptr_t)dst_rows_dev;
-    const size_t src_bytes = (size_t)src_requests * src_seq_len * W;
-    const size_t dst_bytes = (size_t)dst_requests * dst_seq_len * W;
-    if (src < dst + dst_bytes && dst < src + src_bytes) return HS_ERR_INVALID_ARG;
+    const size_t W = fmt->item_size_bytes, block = sizeof(float) * 2 * fmt->num_kv_heads;
+    if (overlap(src_rows_dev, (size_t)src_requests * src_seq_len * W, dst_rows_dev,
+                (size_t)dst_requests * dst_seq_len * W) ||
+        overlap(src_scales_dev, (size_t)src_requests * blocks_of(fmt, src_seq_len) * block,
+                dst_scales_dev, (size_t)dst_requests * blocks_of(fmt, dst_seq_len) * block))
+        return HS_ERR_INVALID_ARG;
     const int32_t most = budget < dst_seq_len ? budget : dst_seq_len;
     if ((long long)batch * blocks_of(fmt, most) * 2 * fmt->num_kv_heads > kMaxCtas)
         return HS_ERR_UNSUPPORTED;

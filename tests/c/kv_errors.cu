@@ -68,6 +68,11 @@ int main() {
     check("hs_evict", hs_evict(x, i, i, 1, 0, 4, 1, 64, i, i, nullptr, nullptr));
     check("hs_compact_kv",
           hs_compact_kv(&f, at, x, 1, 64, i, i, i, 1, 4, far, y, 1, 64, i, nullptr));
+    // scales side by side (one request with 4 blocks of 2 x 2: 64 bytes) are not refused
+    for (char* to : {at + 64, at - 16})
+        check("hs_compact_kv beside its source's scales",
+              hs_compact_kv(&f, at, x, 1, 64, i, i, i, 1, 4, far, reinterpret_cast<float*>(to), 1,
+                            16, i, nullptr));
     if (!bad) std::printf("ok\n");
     return bad;
 }

@@ -1,4 +1,5 @@
 """The 8-bit key/value row calls where they could go wrong, on the CPU."""
+import ctypes
 import os
 import subprocess
 
@@ -6,13 +7,14 @@ import pytest
 import torch
 
 import sparse_attention_kv_swap_gb300 as pkg
+from sparse_attention_kv_swap_gb300 import binding as B
 
 
 @pytest.fixture(scope="module")
 def lib():
-    from sparse_attention_kv_swap_gb300 import binding, build
+    from sparse_attention_kv_swap_gb300 import build
     build.build()
-    return binding.load_library()
+    return B.load_library()
 
 
 def cpu_cache(R=3, L=40, W=256, layers=2):
@@ -96,3 +98,18 @@ def test_attend_shapes_fit_an_sm(tmp_path):
 
 def test_a_failed_launch_leaves_no_error_behind(tmp_path):
     assert run_cuda_program("kv_errors", tmp_path).startswith("ok")
+
+
+def test_compact_refuses_overlapping_scales(lib):
+    """Scales that source and destination share would be read and written in any order."""
+    fmt = pkg.make_kv_format(8, 128, 64)
+    at, src, dst = 0x20000, 0x1000000, 0x2000000
+    scales = 0x400000  # of 2 requests with 3 blocks of 2 x 8 floats: 384 bytes
+
+    def call(dst_scales):
+        return lib.hs_compact_kv(ctypes.byref(fmt), src, scales, 2, 130, at, at, at, 1, 32, dst,
+                                 dst_scales, 2, 70, at, None)
+
+    # the destination's 2 requests with 2 blocks: 256 bytes
+    for to in (scales, scales + 380, scales - 252, scales + 64):
+        assert call(to) == B.HS_ERR_INVALID_ARG, hex(to)
