@@ -3,6 +3,7 @@ PyTorch (pinned host pools, device KV buffers, state, workspace) and forwards
 each call to the library.  Nothing here computes any part of the swap-in."""
 from __future__ import annotations
 
+import contextlib
 from typing import Dict, List, Optional
 
 import torch
@@ -36,19 +37,26 @@ class SwapInCache:
         self.handle = B.hs_create_state(cfg, self.host_pools, self.device_kv, self.state,
                                         self.workspace, stream)
 
+    @staticmethod
+    def _allocate_on(stream):
+        """Outputs that a call allocates belong to the stream it runs on: memory of another
+        stream may still be in use there."""
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
     def swap_in(self, req_pool_indices: torch.Tensor, seq_lens: torch.Tensor,
                 topk: torch.Tensor, layer_id: int = 0, stats: bool = False, plan: bool = False,
                 out: Optional[Dict[str, torch.Tensor]] = None, stream=None):
         Bn, S, K = topk.shape
         o = dict(out or {})
-        if "device_locs" not in o:
-            o["device_locs"] = torch.empty((Bn, S, K), dtype=torch.int32, device=self.device)
-        if stats and "stats" not in o:
-            o["stats"] = torch.empty((Bn, B.HS_NUM_STATS), dtype=torch.int32, device=self.device)
-        if plan and "miss_src" not in o:
-            o["miss_src"] = torch.full((Bn, self.C), -1, dtype=torch.int64, device=self.device)
-            o["miss_dst"] = torch.full((Bn, self.C), -1, dtype=torch.int64, device=self.device)
-            o["miss_count"] = torch.empty(Bn, dtype=torch.int32, device=self.device)
+        with self._allocate_on(stream):
+            if "device_locs" not in o:
+                o["device_locs"] = torch.empty((Bn, S, K), dtype=torch.int32, device=self.device)
+            if stats and "stats" not in o:
+                o["stats"] = torch.empty((Bn, B.HS_NUM_STATS), dtype=torch.int32, device=self.device)
+            if plan and "miss_src" not in o:
+                o["miss_src"] = torch.full((Bn, self.C), -1, dtype=torch.int64, device=self.device)
+                o["miss_dst"] = torch.full((Bn, self.C), -1, dtype=torch.int64, device=self.device)
+                o["miss_count"] = torch.empty(Bn, dtype=torch.int32, device=self.device)
         B.hs_swap_in(self.handle, req_pool_indices, seq_lens, topk, layer_id, o["device_locs"],
                      o.get("stats"), o.get("miss_src"), o.get("miss_dst"), o.get("miss_count"),
                      stream)
@@ -58,9 +66,10 @@ class SwapInCache:
                    out: Optional[Dict[str, torch.Tensor]] = None, stream=None):
         Bn, S, K = topk.shape
         o = dict(out or {})
-        o.setdefault("pages", torch.empty((Bn, S * K), dtype=torch.int32, device=self.device))
-        o.setdefault("num_pages", torch.empty(Bn, dtype=torch.int32, device=self.device))
-        o.setdefault("token_page", torch.empty((Bn, S, K), dtype=torch.int32, device=self.device))
+        with self._allocate_on(stream):
+            o.setdefault("pages", torch.empty((Bn, S * K), dtype=torch.int32, device=self.device))
+            o.setdefault("num_pages", torch.empty(Bn, dtype=torch.int32, device=self.device))
+            o.setdefault("token_page", torch.empty((Bn, S, K), dtype=torch.int32, device=self.device))
         B.hs_page_table(topk, seq_lens, self.cfg.max_seq_len, page_size, o["pages"],
                         o["num_pages"], o["token_page"], stream)
         return o
@@ -92,15 +101,16 @@ class SwapInCache:
         """Attention of q [batch, steps, heads, D] over the rows that a swap-in located."""
         Bn, S, K = topk.shape
         o = dict(out or {})
-        if "out" not in o:
-            o["out"] = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        if lse and "lse" not in o:
-            o["lse"] = torch.empty(q.shape[:3], device=self.device)
-        if (weights or (acc is not None and S > 1)) and "weights" not in o:
-            o["weights"] = torch.empty((Bn, S, K), device=self.device)
-        need = B.hs_attend_workspace_bytes(fmt, Bn, S, K, q.shape[2])
-        if need and "workspace" not in o:
-            o["workspace"] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        with self._allocate_on(stream):
+            if "out" not in o:
+                o["out"] = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+            if lse and "lse" not in o:
+                o["lse"] = torch.empty(q.shape[:3], device=self.device)
+            if (weights or (acc is not None and S > 1)) and "weights" not in o:
+                o["weights"] = torch.empty((Bn, S, K), device=self.device)
+            need = B.hs_attend_workspace_bytes(fmt, Bn, S, K, q.shape[2])
+            if need and "workspace" not in o:
+                o["workspace"] = torch.empty(need, dtype=torch.uint8, device=self.device)
         B.hs_attend(fmt, q, self.device_kv[layer_id], device_locs, topk, req_pool_indices, scales,
                     self.cfg.max_seq_len, o["out"], o.get("lse"), o.get("weights"), acc, sm_scale,
                     o.get("workspace"), stream)

@@ -192,3 +192,45 @@ def test_attend_many_wide_heads(heads, G, D, K, code):
     n = pkg.hs_attend_workspace_bytes(a.fmt, B_, S, K, heads * G)
     ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") if n else None
     a.check(a.run(workspace=ws))
+
+
+# ---- streams ------------------------------------------------------------------------
+
+def test_outputs_belong_to_the_stream_of_the_call():
+    """While the current stream has work pending, calls on another stream allocate their
+    outputs: neither may they take memory that the pending work still reads, nor may
+    the current stream write them."""
+    from sparse_attention_kv_swap_gb300.cache import SwapInCache
+    rng = np.random.default_rng(51)
+    Bn, K, heads, D, L = 64, 64, 32, 128, 200
+    cache = SwapInCache(pkg.make_config(Bn, L, 2 * D, 2 * K, K, 1))
+    cache.host_pools[0].random_(0, 120)
+    fmt = pkg.make_kv_format(1, D, 16)
+    scales = cache.kv_scales(fmt) + 2.0 ** -7
+    req = torch.arange(Bn, dtype=torch.int32, device="cuda")
+    lens = torch.full_like(req, L)
+    topk = dev(np.stack([rng.permutation(L)[:K] for _ in range(Bn)]).astype(np.int32)[:, None])
+    q = dev(torch.from_numpy(rng.standard_normal((Bn, 1, heads, D))).bfloat16())
+    want_plan = cache.swap_in(req, lens, topk, plan=True)
+    want = cache.attend(fmt, scales, q, topk, want_plan["device_locs"], req, lse=True,
+                        weights=True)
+    cache.reset_requests(req)
+    side = torch.cuda.Stream()
+    like = [want[k] for k in ("out", "lse", "weights")] + [
+        want_plan[k] for k in ("device_locs", "miss_src", "miss_dst", "miss_count")]
+    old = [torch.full_like(t, 7) for t in like]
+    new = [torch.empty_like(t) for t in like]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms of the current stream
+    for x, y in zip(old, new):
+        y.copy_(x)
+    del x, y
+    old.clear()  # free for the current stream, behind its copies
+    plan = cache.swap_in(req, lens, topk, plan=True, stream=side)
+    got = cache.attend(fmt, scales, q, topk, plan["device_locs"], req, lse=True, weights=True,
+                       stream=side)
+    torch.cuda.synchronize()
+    assert all((y == 7).all() for y in new)
+    for k, x in list(want.items()) + list(want_plan.items()):
+        assert torch.equal(got[k] if k in got else plan[k], x), k
+    cache.close()
