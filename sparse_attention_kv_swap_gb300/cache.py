@@ -99,6 +99,8 @@ class SwapInCache:
                acc: Optional[torch.Tensor] = None, sm_scale: Optional[float] = None,
                out: Optional[Dict[str, torch.Tensor]] = None, stream=None):
         """Attention of q [batch, steps, heads, D] over the rows that a swap-in located."""
+        if not 0 <= layer_id < self.cfg.num_layers:  # a list would take -1 for its last entry
+            raise B.HsError(B.HS_ERR_INVALID_ARG, "SwapInCache.attend")
         Bn, S, K = topk.shape
         o = dict(out or {})
         with self._allocate_on(stream):

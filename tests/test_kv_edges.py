@@ -113,3 +113,14 @@ def test_compact_refuses_overlapping_scales(lib):
     # the destination's 2 requests with 2 blocks: 256 bytes
     for to in (scales, scales + 380, scales - 252, scales + 64):
         assert call(to) == B.HS_ERR_INVALID_ARG, hex(to)
+
+
+@pytest.mark.parametrize("layer", [-1, -2, 2])
+def test_cache_attend_refuses_layers_out_of_range(lib, layer):
+    """As every other call of the cache does; -1 is not its last layer."""
+    cache, fmt = cpu_cache(), pkg.make_kv_format(2, 64, 16)
+    topk = torch.zeros((1, 1, 8), dtype=torch.int32)
+    with pytest.raises(pkg.HsError) as error:
+        cache.attend(fmt, torch.ones((3, 3, 2, 2)), torch.zeros((1, 1, 4, 64)).bfloat16(), topk, topk,
+                     topk[:, 0, 0], layer_id=layer)
+    assert error.value.code == B.HS_ERR_INVALID_ARG
