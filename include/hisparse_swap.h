@@ -539,6 +539,10 @@ size_t hs_attend_workspace_bytes(const hs_kv_format* fmt, const hs_attend_args* 
  * A NaN code in a selected row spoils the outputs of the heads that read it, an
  * infinity or a NaN in a query those of its head; rows that no valid entry
  * selects are not read.
+ * The kernel keeps scores in tensor memory while its CTAs wait for one another.  A
+ * kernel of another library that does the same, in clusters that hold over half of an
+ * SM's tensor memory with less than half of its shared memory, must not run at the same
+ * time on another stream: each could wait for what the other holds.
  * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_KV_HEADS query heads.
  * Asynchronous on `stream`. */
 int hs_attend(const hs_kv_format* fmt, const hs_attend_args* args, void* stream);

@@ -84,6 +84,14 @@ void set_cluster(const hs_kv_format& f, const hs_attend_args& a, int P, int most
         // its columns, so that an SM never holds CTAs of these kernels with more columns than it has.
         const size_t share = kSmSmem / kSmCols * (size_t)cols - 1024 - kStatic;
         if (sh->smem < share) sh->smem = share;
+        // Kernels of other libraries, on another stream, follow no such rule.  A lone CTA then waits for
+        // its columns until theirs end.  But CTAs of a cluster wait for one another with their columns
+        // held, and two kernels that both do could wait for each other.  So they take half an SM:
+        // beside them fits only what takes the other half at most, and that blocks them only if
+        // its clusters hold over half of the columns.  (In CTAs of under 8 warps more than two
+        // would fit an SM: 1000 requests of 64 rows, one K/V head of 64, 4 query heads, take 19 us, and
+        // 33 us if single CTAs took half an SM too.)
+        if (P > 1 && sh->smem < kHalfSmem) sh->smem = kHalfSmem;
     }
 }
 

@@ -578,8 +578,9 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
     float* const t_scale = at.scale;
 
     if (!SPILL && warp == 0) {
-        // Never waits: the CTA's shared memory is at least its share of the columns, so that the
-        // CTAs of these kernels that an SM holds have columns for all.
+        // Never waits for another CTA of these kernels: a CTA's shared memory is at least its share of
+        // the columns, so that those that an SM holds have columns for all.  It does wait for what
+        // holds columns otherwise, be it the kernel before this one or one on another stream.
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          shared_address(&s_tmem)),
                      "r"(a.cols)

@@ -54,6 +54,8 @@ static const char* wrong(const hs_kv_format& f, const hs_attend_args& a, const A
         if (k.cols < 32 || k.cols > 512 || (k.cols & (k.cols - 1)) != 0 ||
             k.cols < rounds * ((warps + 3) / 4) * k.task_cols)
             return "tensor memory";
+        // CTAs that wait for one another leave others half an SM at most
+        if (sh.P > 1 && 2 * (sh.smem + 1024 + kStatic) < (size_t)228 * 1024) return "half of an SM";
         // as much of the SM's shared memory as of its tensor memory
         if ((sh.smem + 1024 + kStatic) * 512 < (size_t)228 * 1024 * k.cols) return "share of an SM";
     }
