@@ -24,12 +24,12 @@
 //      ldmatrix transposes V, so that a word holds four tokens of one d.  The
 //      rows of a K tile are taken in the order 0, 1, 4, 5, .. | 2, 3, 6, 7, ..
 //      so that the transposed P (movmatrix) pairs the same tokens.  P is
-//      exp(s - max) times the token's V scale, brought by powers of two to where
-//      the largest one of a head in the task lies near f16's top, and rounded
-//      to f16: by 2^-11 of each at most, or 2^-39 of the largest one where that
-//      is more.  That is an eighth of a bf16 output's own rounding, and as much
+//      exp(s - max) times the token's V scale, multiplied by what brings the largest
+//      one of a head in the task to 2^15, and rounded to f16: by 2^-11 of each at
+//      most, or 2^-40 of the largest one where that is more; the largest itself
+//      stays whole.  That is an eighth of a bf16 output's own rounding, and as much
 //      as an f16 output's (against 64 bits, f16 outputs of the timed cases are
-//      off by 2.3 to 3.0e-4 of their norm; 2.1e-4 with P in 32 bits).  The scale
+//      off by 2.1 to 2.3e-4 of their norm; 2.1e-4 with P in 32 bits).  The factor
 //      belongs to the largest product of P and V scale, not to the largest V scale:
 //      that one may belong to a token of no weight.
 // With 4 query heads to a K/V head or fewer, one fragment takes two tiles: the
@@ -168,6 +168,12 @@ __device__ __forceinline__ float log2_fast(float x) {
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float reciprocal_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -874,7 +880,11 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         // ---- softmax over the task's tokens ----------------------------------------
         scores.stored();
         float safe[N][2], sum[N][2];
-        uint32_t up[N];  // of both heads, the upper half of the float 2^-e
+        // What brings the head's largest product of P and V scale to 2^15; where registers are
+        // short, in the place of the head's sum, which comes after.
+        constexpr bool kUpShared = D * N > 192 && N > 1;
+        float up[N][2];
+        float* const up_at = at.sum + sub * HP + h * GP + j0 + column_head<NT>(c);
 #pragma unroll
         for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
@@ -888,10 +898,8 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
                 if (g == 0)
                     at.max[sub * HP + h * GP + j0 + nt * 8 + column_head<NT>(c) + k] = top[nt][k];
                 safe[nt][k] = top[nt][k] == -INFINITY ? 0.f : top[nt][k];
-                // The head's largest product of P and V scale goes to 2^14.5 .. 2^15.5.
-                const int e = __float2int_rn(most[nt][k] - safe[nt][k] - 15.f);
-                const uint32_t half = (uint32_t)(127 - min(max(e, -126), 126)) << 7;
-                up[nt] = k == 0 ? half : up[nt] | half << 16;
+                up[nt][k] = exp2_fast(fminf(fmaxf(15.f - (most[nt][k] - safe[nt][k]), -126.f), 126.f));
+                if (kUpShared && g == 0) up_at[nt * 8 + k] = up[nt][k];
                 sum[nt][k] = 0.f;
             }
         }
@@ -917,10 +925,13 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
                 sum[nt][0] += p0 + p2;
                 sum[nt][1] += p1 + p3;
                 // P first: the V scale may be any of 32 bits' where P is 0
-                const float u0 = __uint_as_float(up[nt] << 16);
-                const float u1 = __uint_as_float(up[nt] & 0xffff0000u);
-                pf[nt][0] = transpose(pack_half2(p0 * u0 * v0, p1 * u1 * v0));
-                pf[nt][1] = transpose(pack_half2(p2 * u0 * v1, p3 * u1 * v1));
+                float2 u;
+                if constexpr (kUpShared)
+                    u = *reinterpret_cast<const float2*>(up_at + nt * 8);
+                else
+                    u = make_float2(up[nt][0], up[nt][1]);
+                pf[nt][0] = transpose(pack_half2(p0 * u.x * v0, p1 * u.y * v0));
+                pf[nt][1] = transpose(pack_half2(p2 * u.x * v1, p3 * u.y * v1));
             }
 #pragma unroll
             for (int f = 0; f < F; ++f) {
@@ -956,6 +967,17 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         int ranks = P;  // the layout anew, so that it takes no registers through the loops
         asm("" : "+r"(ranks));
         const Layout<SPILL> done(a, smem, ranks, HP, D, nwarps, blockIdx.x);
+        float fold[N][2];
+        if (kUpShared) __syncwarp();  // with no tile, nothing came between
+#pragma unroll
+        for (int nt = 0; nt < N; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                fold[nt][k] = reciprocal_fast(
+                    kUpShared ? done.sum[sub * HP + h * GP + j0 + nt * 8 + column_head<NT>(c) + k]
+                              : up[nt][k]);
+        }
+        if (kUpShared) __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
@@ -971,13 +993,10 @@ __global__ void __launch_bounds__(32 * attend_warps(D, SPILL), 1)
         // with their queues here.  Several parts of a slice have one task a warp too; their
         // outputs are added in order, relative to their common maximum.
         if (a.alias || a.nsub > 1) __syncthreads();
-        float fold[N][2];
 #pragma unroll
         for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint32_t u = k == 0 ? up[nt] << 16 : up[nt] & 0xffff0000u;
-                fold[nt][k] = __uint_as_float(0x7f000000u - u);  // 2^e
                 if (a.nsub > 1) {
                     const int to = h * GP + j0 + nt * 8 + column_head<NT>(c) + k;
                     float m = -INFINITY;

@@ -6,7 +6,7 @@ import torch
 import kv_reference as ref
 import sparse_attention_kv_swap_gb300 as pkg
 from sparse_attention_kv_swap_gb300 import binding as B
-from test_gpu_kv_rows import Attend, dev
+from test_gpu_kv_rows import Attend, dev, random_codes
 from test_kv_edges import evict_refusals
 
 pytestmark = pytest.mark.gpu
@@ -234,3 +234,52 @@ def test_outputs_belong_to_the_stream_of_the_call():
     for k, x in list(want.items()) + list(want_plan.items()):
         assert torch.equal(got[k] if k in got else plan[k], x), k
     cache.close()
+
+
+# ---- attention: queries of one large element ------------------------------------------
+
+@pytest.mark.parametrize("gap", [12, 20, 28, 34, 45])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_attend_small_query_elements(gap, code):
+    """One element of the query 2^gap times the others, on a channel whose K codes are zero: the
+    others' products stay exact to 2^-39 of the largest element."""
+    rng = np.random.default_rng(300 + gap)
+    heads, G, D, K = 2, 4, 64, 200
+    a = Attend(rng, 2, 1, K, heads, G, D, 8, code, "bf16")
+    a.sm_scale = 2.0 ** gap * D ** -0.5
+    q = a.q.double() * 2.0 ** -gap
+    q[..., 5] = 1
+    a.q = q.to(torch.bfloat16)
+    used = np.unique(a.locs[a.locs >= 0])
+    a.rows[used[:, None], np.arange(heads)[None] * D + 5] = 0
+    want = a.reference()
+    out, lse, _ = (x.cpu().double().numpy() for x in a.run())
+    # a score's error: 32-bit sums as in Attend.check, and every query element's own
+    size = a.scales[:, :, 0].max() * {"e4m3": 448, "int8": 127}[code]
+    dz = ((D + 8) * 2.0 ** -23 * want["logit"] + 2.0 ** -20 + K * 2.0 ** -24
+          + D * 2.0 ** -39 * size * a.sm_scale)
+    bound = dz + 2.0 ** -22 * np.abs(want["lse"])
+    assert (np.abs(lse - want["lse"]) <= bound).all(), (np.abs(lse - want["lse"]) / bound).max()
+    # exp(2 dz) - 1 is the most that a weight changes by
+    tol = 2.0 ** -8 * np.abs(want["out"]) + want["spread"] * (
+        2.0 ** -11 + np.expm1(np.minimum(2 * dz, 30))[..., None]) * 1.01 + K * 2.0 ** -24
+    assert (np.abs(out - want["out"]) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,G,D,code", [(2, 4, 128, "int8"), (1, 16, 128, "int8"), (2, 1, 256, "e4m3"),
+                                            (3, 9, 64, "e4m3"), (1, 6, 192, "int8")])
+def test_attend_largest_weight_stays_whole(heads, G, D, code, dtype):
+    """One live entry, of any scale: its V row comes out with the output's own rounding alone
+    (and some 32-bit ones: exp2, log2, reciprocals)."""
+    rng = np.random.default_rng(400 + D)
+    for K in (1, 40):
+        a = Attend(rng, 3, 2, K, heads, G, D, 8, code, dtype, holes=0)
+        a.scales[:, :, 1] = rng.random(a.scales[:, :, 1].shape) + 0.1
+        a.locs[:, :, 1:] = -1
+        a.rows[a.locs[:, :, 0], :2 * heads * D] = random_codes(rng, (3, 2, 2 * heads * D), code)
+        want = a.reference()["out"]
+        got = a.run()[0].cpu().double().numpy()
+        u = torch.finfo(a.q.dtype).eps / 2
+        tol = (u + 2.0 ** -20) * np.abs(want) + (2.0 ** -25 if dtype == "fp16" else 0)
+        assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / np.maximum(tol, 1e-30)).max()
