@@ -422,8 +422,8 @@ int hs_swap_in_noalloc(hs_state* st, const int32_t* req_pool_indices_dev,
  * Scales: float [R, NB, 2, Hkv] with NB = ceil(L / T); K (c = 0) or V (c = 1)
  * of head h is code * scales[q, t / T, c, h].  A scale is finite and >= 0.
  *   HS_KV_E4M3: codes are e4m3 (largest 448).  The scales these calls write
- *     are powers of two, the smallest that bring the largest magnitude of the
- *     block to 448 or less, so that rounding the codes of a block again under
+ *     are powers of two, the smallest from 2^-100 on that bring the largest magnitude of
+ *     the block to 448 or less, so that rounding the codes of a block again under
  *     a larger scale changes nothing but e4m3's subnormals.
  *   HS_KV_INT8: codes are two's complement, -127..127; scale = largest
  *     magnitude / 127.
@@ -516,7 +516,9 @@ typedef struct hs_attend_args {
     float* weights_dev;      /* [batch, steps, top_k] or NULL: each entry's attention weight
                                 summed over the query heads                                 */
     float* acc_dev;          /* [R, L] or NULL: acc[req, token] += weights, as hs_accumulate
-                                with every step counted; needs weights_dev if steps > 1     */
+                                with every step counted; needs weights_dev if steps > 1.
+                                The weights of a request given twice, or of a token given in
+                                two rows of one step, are added in any order             */
     void* workspace_dev;     /* hs_attend_workspace_bytes, 16-byte aligned, or NULL if 0    */
     size_t workspace_bytes;
 } hs_attend_args;
@@ -533,9 +535,10 @@ size_t hs_attend_workspace_bytes(const hs_kv_format* fmt, const hs_attend_args* 
  * others (a swap-in's -1 among them) are masked.  A query whose entries are
  * all masked gets out 0, lse -inf and weights 0; one whose request lies
  * outside [0, num_requests) likewise.  An entry given twice counts twice.
- * Products of codes and queries are exact and summed in 32 bits; the softmax
+ * Products of codes and queries are exact (but for query elements under 2^-28 of their head's
+ * largest, which are off by 2^-39 of that at most) and summed in 32 bits; the softmax
  * statistics are 32 bits; p_j times the V scale is rounded to 11 bits for the product
- * with the V codes (or by 2^-39 of the largest such term of the head, if that is more).
+ * with the V codes (or by 2^-40 of the head's largest such term, if that is more).
  * A NaN code in a selected row spoils the outputs of the heads that read it, an
  * infinity or a NaN in a query those of its head; rows that no valid entry
  * selects are not read.

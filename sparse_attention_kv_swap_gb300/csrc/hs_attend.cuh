@@ -7,14 +7,15 @@
 // share it) over tiles of 16 tokens:
 //   1. scores: S^T[token, head] = K[token, d] Q^T[d, head] with f16
 //      m16n8k16 products summed in 32 bits.  A selected row is read by exactly
-//      one warp per K/V head, so the warps share nothing: each copies the
+//      one warp per K/V head and group of query heads, so the warps share nothing: each copies the
 //      pieces of its head (cp.async, whole 128-byte lines where D allows:
 //      gathering in 64-byte pieces costs a fifth of the bandwidth) into a queue
 //      of its own in shared memory, several tiles ahead, and reads them back
 //      as operands (ldmatrix).  A product may visit d in any order, so the
 //      four bytes of a word are four d of one step.  Codes are exact in f16;
 //      the query is scaled by a power of two per head into f16's range, which
-//      keeps bf16's and f16's significands whole.  Scores stay in 32 bits, in
+//      keeps bf16's and f16's significands whole down to 2^-28 of the head's
+//      largest element (smaller ones are off by 2^-39 of it at most).  Scores stay in 32 bits, in
 //      the fragment's own layout, in tensor memory: 512 columns of an SM that
 //      nothing else here needs, where shared memory would hold a quarter as
 //      many tokens beside the queues.
@@ -40,17 +41,20 @@
 // shared memory, each adds up a share of the output over the CTAs in rank
 // order, and each turns its own scores into weights with the query's final
 // sums.  Nothing goes through global memory but inputs and outputs, and no
-// result depends on timing.
+// result depends on timing, but for sums that get several additions in one launch: of a
+// request that the batch holds twice, or of a token that a query holds in two rows.
 //
 // What bounds it: every row is read once per step, 2 * Hkv * D bytes, for
 // 4 * Hq * D operations, i.e. 2 * (Hq / Hkv) operations a byte: memory, with
 // the products far below the tensor rate even on mma.sync.  64 queries of 2048
-// rows, 8 heads of 128 (268 MB), take 62 us, 4.5 TB/s, where gathering the same
-// rows and nothing else takes 55-57 from a cold start.  Where steps share rows
+// rows, 8 heads of 128 (268 MB), take 62-63 us, 4.3 TB/s.  Gathering the same rows and
+// nothing else, launches back to back, takes 44 us in whole rows and 48 through queues
+// like these; the rest is the start and the end of a cluster (positions, scales,
+// exchange), in which nothing is gathered and which all CTAs go through together.  Where steps share rows
 // or heads are many, the work on the codes bounds it: converting 16 x D codes
-// to f16 is most of the 440 instructions that a tile takes for 8 query heads,
+// to f16 is most of the 460 instructions that a tile takes for 8 query heads,
 // and 64 x 4 queries of 2048 rows, 4 heads of 128, 70% of them shared by
-// neighbouring steps, take 90 us (5.9 TB/s out of L2 and memory).  tcgen05.mma would
+// neighbouring steps, take 92 us (5.8 TB/s out of L2 and memory).  tcgen05.mma would
 // want 128 rows of one operand in shared memory as f16, which here would mean
 // writing every code back after its conversion; its e4m3 form takes codes
 // as they are, but queries and weights then in three e4m3 parts each, int8

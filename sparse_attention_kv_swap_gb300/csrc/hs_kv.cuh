@@ -30,8 +30,9 @@ struct QuantizeArgs {
 };
 cudaError_t launch_quantize(QuantizeArgs a, bool cache, cudaStream_t s);
 
-// Division of 0 <= t < 2^31 by a constant d: with 2^l >= d, m = ceil(2^(31 + l) / d) is below 2^32
-// and off from the quotient by less than 2^-31, too little to reach the next integer.
+// Division of 0 <= t < 2^31 by a constant d: with 2^l >= d > 2^(l-1), m = ceil(2^(31 + l) / d) is
+// below 2^32 and m / 2^(31 + l) above 1 / d by less than 2^-(31 + l).  So the product is above t / d by less
+// than 2^-l <= 1 / d, too little to reach the next integer.
 struct Divisor {
     uint32_t m;
     int32_t shift;
