@@ -593,6 +593,191 @@ int hs_compact_kv(const hs_kv_format* fmt, const void* src_rows_dev, const float
                   void* dst_rows_dev, float* dst_scales_dev, int32_t dst_requests,
                   int32_t dst_seq_len, const int32_t* dst_req_dev, void* stream);
 
+/* ==== Around a decode step: norms and rotation, block selection, shared prefix ==
+ *
+ * What a step with selected tokens does before and beside the swap-in:
+ * hs_norm_rope makes the step's queries and keys of a projection's outputs,
+ * hs_bound_keys and hs_select_blocks choose the tokens that hs_swap_in takes
+ * as its top-k indices, and hs_attend_prefix attends over the tokens that requests
+ * have in common.  The pages take the indices from the model's own indexer and
+ * give no counterpart to these calls. */
+
+#define HS_MAX_ROPE_AXES 4        /* num_axes upper bound                            */
+#define HS_MAX_SELECT_BLOCKS 16384 /* blocks of a sequence for hs_select_blocks       */
+#define HS_MAX_SELECT_WIDTH 8192  /* num_kv_heads * head_dim for hs_select_blocks; twice
+                                     that times steps                                 */
+#define HS_MAX_PREFIXES 256       /* num_prefixes upper bound                        */
+
+/* Arguments of hs_norm_rope. */
+typedef struct hs_norm_rope_args {
+    const void* q_dev;         /* [batch, tokens, heads, D], strides below (elements), the last
+                                  dimension dense; element-aligned.  NULL if num_heads is 0  */
+    const void* k_dev;         /* [batch, tokens, kv heads, D] likewise                      */
+    void* q_out_dev;           /* as q, of the same type, its own strides; may be q itself with
+                                  q's strides, and must not overlap q or k otherwise         */
+    void* k_out_dev;           /* as k                                                       */
+    int32_t dtype;             /* HS_DTYPE_* of all four                                     */
+    int32_t batch, tokens;
+    int32_t num_heads, num_kv_heads; /* either may be 0                                      */
+    int32_t head_dim;          /* D: 32, 64, 96, 128, 192 or 256                             */
+    int32_t rot_dim;           /* elements of a head that turn, its first ones: a multiple of
+                                  16 from 0 to D                                             */
+    int32_t adjacent;          /* pair j is (2 j, 2 j + 1) if 1, (j, j + rot_dim / 2) if 0   */
+    int32_t num_axes;          /* 1..HS_MAX_ROPE_AXES                                        */
+    float eps;                 /* > 0 where a weight is given                                */
+    int64_t q_stride[3];       /* batch, token, head                                         */
+    int64_t k_stride[3];
+    int64_t q_out_stride[3];
+    int64_t k_out_stride[3];
+    const float* q_weight_dev; /* [D]; NULL: queries are not normalised                      */
+    const float* k_weight_dev; /* [D]; NULL: keys are not normalised                         */
+    const int32_t* pos_dev;    /* [axes, batch, tokens], any value; NULL if rot_dim is 0     */
+    const int64_t* turns_dev;  /* [rot_dim / 2]: angle of pair j at position 1, in units of
+                                  2^-64 turns (modulo a turn)                                */
+    const int32_t* axis_dev;   /* [rot_dim / 2]: the axis of pair j, clamped to the axes given;
+                                  NULL: axis 0 for all                                       */
+    const int32_t* count_dev;  /* [batch] or NULL: entry b has tokens i < count[b] only; the
+                                  outputs of the others are left alone                       */
+} hs_norm_rope_args;
+
+/* For every head x of every query and key:
+ *   y = x * weight / sqrt(mean of x^2 + eps)      (y = x without a weight)
+ *   out = y with each pair (y0, y1) of its first rot_dim elements turned by
+ *     a_j = 2 pi * 2^-64 * turns[j] * pos[axis[j], b, i]:
+ *     (y0 cos a_j - y1 sin a_j, y0 sin a_j + y1 cos a_j)
+ * in 32 bits, rounded once to the outputs' type.  The product turns * pos is
+ * exact modulo whole turns, so that angles of far positions are as good as those of
+ * near ones; pos may be negative.
+ * Returns HS_ERR_UNSUPPORTED for 2^31 heads or more in all.
+ * Asynchronous on `stream`. */
+int hs_norm_rope(const hs_norm_rope_args* args, void* stream);
+
+/* Bounds of the keys of every block of block_tokens tokens:
+ *   bounds_dev [num_requests, NB, Hkv, 2, D], NB = ceil(max_seq_len / block_tokens):
+ *     the least (0) and the greatest (1) key of the block, channel by channel, in the
+ *     keys' own type (bf16 or fp16)
+ * Entry b brings the keys k[b, i] of the tokens start[b] + i, i < count[b], of request
+ * req[b] (k_stride: batch, token, head, in elements; the last dimension dense).  A
+ * block that they fill from its first token on gets the bounds of the new keys alone; those of
+ * a block that begins before start[b] are widened.  NaN does not count (a channel
+ * with nothing else gets +inf and -inf).  Blocks without new tokens, and entries whose request
+ * or range lies outside the store or whose count is above max_count, are left
+ * alone.  The requests of one call must be distinct.  block_tokens from 1 to
+ * HS_MAX_KV_BLOCK, head_dim as in hs_kv_format.  Keys in place of rows that
+ * hs_compact_kv has moved are brought anew, from token 0.
+ * Asynchronous on `stream`. */
+int hs_bound_keys(const void* k_dev, const int64_t* k_stride, int32_t dtype, int32_t num_kv_heads,
+                  int32_t head_dim, int32_t block_tokens, const int32_t* req_dev,
+                  const int32_t* start_dev, const int32_t* count_dev, int32_t batch,
+                  int32_t max_count, void* bounds_dev, int32_t num_requests, int32_t max_seq_len,
+                  void* stream);
+
+/* Arguments of hs_select_blocks. */
+typedef struct hs_select_args {
+    const void* q_dev;           /* [batch, steps, heads, D], strides below (elements), the last
+                                    dimension dense; element-aligned                         */
+    const void* bounds_dev;      /* [R, NB, Hkv, 2, D], of q's type (hs_bound_keys)          */
+    int32_t dtype;               /* HS_DTYPE_BF16 or HS_DTYPE_FP16                           */
+    int32_t batch, steps;        /* steps: 1..HS_MAX_STEPS                                   */
+    int32_t num_heads;           /* query heads, a multiple of num_kv_heads                  */
+    int32_t num_kv_heads, head_dim;
+    int32_t num_requests;        /* R                                                        */
+    int32_t max_seq_len;
+    int32_t block_tokens;        /* T                                                        */
+    int32_t select;              /* blocks to select, 1 or more                              */
+    int32_t first, last;         /* of these, always the first and the newest ones; together
+                                    at most `select`                                         */
+    int64_t q_stride[3];         /* batch, step, head                                        */
+    const int32_t* req_dev;      /* [batch]                                                  */
+    const int32_t* seq_lens_dev; /* [batch]                                                  */
+    int32_t* blocks_dev;         /* [batch, steps, select] out or NULL: the blocks, ascending,
+                                    then -1                                                  */
+    int32_t* topk_dev;           /* [batch, steps, select * T] out: their tokens in the same
+                                    order, -1 for those past the sequence: hs_swap_in's
+                                    topk_dev for top_k = select * T                          */
+    float* scores_dev;           /* [batch, steps, NB] out: the scores, -inf past the sequence */
+    void* workspace_dev;         /* hs_select_workspace_bytes, 4-byte aligned                */
+    size_t workspace_bytes;
+} hs_select_args;
+
+/* Device bytes of workspace that an hs_select_blocks call needs ((size_t)-1 if the sizes are
+ * not accepted).  Host only. */
+size_t hs_select_workspace_bytes(int32_t batch, int32_t steps, int32_t max_seq_len,
+                                 int32_t block_tokens);
+
+/* Selects, for each of batch x steps queries, blocks of its request's tokens:
+ *   score(n) = sum over query heads h and channels d of
+ *              max(q_hd * lo_nd, q_hd * hi_nd),   lo, hi: block n's bounds of h's K/V head
+ * which is no less than the sum over the query heads of q_h . k_t for any token t of block n.
+ * With n = min(seq_lens[b], max_seq_len) tokens in ceil(n / T) blocks: all blocks if these
+ * are no more than `select`; else the first `first`, the last `last` and, of those between, the
+ * ones of the largest scores, ties to the lower block, a NaN below every number.
+ * Scores are sums in 32 bits.  For finite bounds and queries the selection is that of scores of 46
+ * bits: blocks that are closer than the sums tell apart are scored again.
+ * A request outside [0, num_requests) or a length of 0 or less selects nothing (-1, scores -inf).
+ * Bounds of blocks past the sequence are not read.
+ * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_SELECT_BLOCKS blocks of a sequence, HS_MAX_KV_HEADS query
+ * heads, or where num_kv_heads * head_dim is above HS_MAX_SELECT_WIDTH or that times steps above
+ * twice as much.  Asynchronous on `stream`. */
+int hs_select_blocks(const hs_select_args* args, void* stream);
+
+/* Arguments of hs_attend_prefix. */
+typedef struct hs_prefix_args {
+    const void* q_dev;           /* [batch, steps, heads, D], strides below (elements), the last
+                                    dimension dense; element-aligned                         */
+    void* out_dev;               /* the same shape and type, its own strides                 */
+    int32_t dtype;               /* HS_DTYPE_BF16 or HS_DTYPE_FP16, of q, out and join_out   */
+    int32_t batch, steps;
+    int32_t num_heads;           /* query heads, a multiple of Hkv, as in hs_attend          */
+    int32_t num_requests;        /* R: prefixes that the store holds                         */
+    int32_t max_seq_len;         /* L: rows of each                                          */
+    int32_t num_prefixes;        /* P: prefixes of this call, 0..HS_MAX_PREFIXES             */
+    float sm_scale;              /* factor of q . k                                          */
+    int64_t q_stride[3];         /* batch, step, head                                        */
+    int64_t out_stride[3];
+    int64_t join_stride[3];      /* of join_out                                              */
+    const void* rows_dev;        /* uint8 [R, L, W], 16-byte aligned: a store as hs_quantize_kv
+                                    writes it                                                */
+    const float* scales_dev;     /* [R, NB, 2, Hkv]                                          */
+    const int32_t* prefix_dev;   /* [P]: the store's request that holds prefix p             */
+    const int32_t* lens_dev;     /* [P]: its tokens                                          */
+    const int32_t* starts_dev;   /* [P + 1], ascending: batch rows starts[p] .. starts[p + 1] - 1
+                                    share prefix p                                           */
+    float* lse_dev;              /* [batch, steps, heads] natural log of the sum of exp, or NULL */
+    const void* join_out_dev;    /* [batch, steps, heads, D] or NULL: attention over other tokens
+                                    of the same queries (hs_attend's out), to be joined      */
+    const float* join_lse_dev;   /* [batch, steps, heads]: its lse; given if join_out is     */
+    void* workspace_dev;         /* hs_prefix_workspace_bytes, 16-byte aligned               */
+    size_t workspace_bytes;
+} hs_prefix_args;
+
+/* Device bytes of workspace that an hs_attend_prefix call of these sizes needs on the current
+ * device ((size_t)-1 if they are not accepted).  Uses batch, steps, num_heads and num_prefixes of
+ * `args`, no pointer.  Host only. */
+size_t hs_prefix_workspace_bytes(const hs_kv_format* fmt, const hs_prefix_args* args);
+
+/* Attention of batch x steps queries over prefixes that consecutive batch rows share: every
+ * query of the rows of prefix p attends to the tokens t < min(lens[p], max_seq_len) of
+ * store row prefix[p], all of them.
+ *   s_t = sm_scale * q . k_t,  lse = ln sum_t exp(s_t),  out = sum_t exp(s_t - lse) v_t
+ * and, where join_out is given, the attention over both sets of tokens:
+ *   lse' = ln(exp(lse) + exp(join_lse)),
+ *   out' = out * exp(lse - lse') + join_out * exp(join_lse - lse')
+ * out and lse may be join_out and join_lse themselves (the same strides).  An empty set has lse
+ * -inf and out 0 (a join_out of lse -inf is not read); so do rows of no prefix: those
+ * before starts[0] or from starts[P] on, and those of a prefix whose request lies outside [0, num_requests) or
+ * whose length is 0 or less.  starts is taken as ascending and clamped to [0, batch].
+ * Products of codes and queries are exact (but for query elements under 2^-28 of their head's
+ * largest, which are off by 2^-39 of that at most) and summed in 32 bits; the softmax statistics
+ * are 32 bits; each weight times its V scale is rounded to 11 bits for the product with the V
+ * codes (or by 2^-36 of the largest such term, if that is more).
+ * A NaN code in the prefix spoils the outputs of the heads that read it, an infinity or a NaN in a
+ * query those of its head.  Outputs do not depend on timing.
+ * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_KV_HEADS query heads or HS_MAX_PREFIXES.
+ * Should a wait inside the kernel ever give up, the outputs it would have written are NaN.
+ * Asynchronous on `stream`. */
+int hs_attend_prefix(const hs_kv_format* fmt, const hs_prefix_args* args, void* stream);
+
 /* Static string for a return code (no counterpart on the pages). */
 const char* hs_status_string(int code);
 

@@ -14,7 +14,9 @@ from .binding import (HsConfig, HsError, make_config, load_library,  # noqa: F40
                       hs_copy_planned, hs_append_rows, hs_get_stats,
                       HS_KV_E4M3, HS_KV_INT8, HsKvFormat, make_kv_format, hs_quantize_kv,
                       hs_append_kv, hs_attend, hs_attend_workspace_bytes, hs_accumulate,
-                      hs_evict, hs_compact_kv)
+                      hs_evict, hs_compact_kv, HsRope, make_rope, hs_norm_rope, bounds_shape,
+                      hs_bound_keys, hs_select_blocks, hs_select_workspace_bytes,
+                      hs_attend_prefix, hs_prefix_workspace_bytes)
 
 
 def __getattr__(name):

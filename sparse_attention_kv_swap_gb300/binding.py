@@ -53,6 +53,10 @@ HS_DTYPE_FP16 = 1
 HS_DTYPE_FP32 = 2
 HS_MAX_KV_BLOCK = 4096
 HS_MAX_KV_HEADS = 128
+HS_MAX_ROPE_AXES = 4
+HS_MAX_SELECT_BLOCKS = 16384
+HS_MAX_SELECT_WIDTH = 8192
+HS_MAX_PREFIXES = 256
 
 HEADER = os.path.join(_build.INCLUDE, "hisparse_swap.h")
 
@@ -129,6 +133,48 @@ class _HsAttendArgs(ctypes.Structure):
                 ("workspace_dev", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class _HsNormRopeArgs(ctypes.Structure):
+    _fields_ = [("q_dev", ctypes.c_void_p), ("k_dev", ctypes.c_void_p),
+                ("q_out_dev", ctypes.c_void_p), ("k_out_dev", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("q_out_stride", ctypes.c_int64 * 3),
+                ("k_out_stride", ctypes.c_int64 * 3), ("q_weight_dev", ctypes.c_void_p),
+                ("k_weight_dev", ctypes.c_void_p), ("pos_dev", ctypes.c_void_p),
+                ("turns_dev", ctypes.c_void_p), ("axis_dev", ctypes.c_void_p),
+                ("count_dev", ctypes.c_void_p)]
+
+
+class _HsSelectArgs(ctypes.Structure):
+    _fields_ = [("q_dev", ctypes.c_void_p), ("bounds_dev", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_requests", ctypes.c_int32),
+                ("max_seq_len", ctypes.c_int32), ("block_tokens", ctypes.c_int32),
+                ("select", ctypes.c_int32), ("first", ctypes.c_int32), ("last", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64 * 3), ("req_dev", ctypes.c_void_p),
+                ("seq_lens_dev", ctypes.c_void_p), ("blocks_dev", ctypes.c_void_p),
+                ("topk_dev", ctypes.c_void_p), ("scores_dev", ctypes.c_void_p),
+                ("workspace_dev", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class _HsPrefixArgs(ctypes.Structure):
+    _fields_ = [("q_dev", ctypes.c_void_p), ("out_dev", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("num_requests", ctypes.c_int32),
+                ("max_seq_len", ctypes.c_int32), ("num_prefixes", ctypes.c_int32),
+                ("sm_scale", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3),
+                ("out_stride", ctypes.c_int64 * 3), ("join_stride", ctypes.c_int64 * 3),
+                ("rows_dev", ctypes.c_void_p), ("scales_dev", ctypes.c_void_p),
+                ("prefix_dev", ctypes.c_void_p), ("lens_dev", ctypes.c_void_p),
+                ("starts_dev", ctypes.c_void_p), ("lse_dev", ctypes.c_void_p),
+                ("join_out_dev", ctypes.c_void_p), ("join_lse_dev", ctypes.c_void_p),
+                ("workspace_dev", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 _lock = threading.Lock()
 _vp = ctypes.c_void_p
@@ -177,6 +223,13 @@ def _declare(lib) -> None:
                                     _vp]),
         "hs_compact_kv": (ctypes.c_int, [_fmtp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32,
                                          _vp, _vp, _i32, _i32, _vp, _vp]),
+        "hs_norm_rope": (ctypes.c_int, [_vp, _vp]),
+        "hs_bound_keys": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32,
+                                         _i32, _vp, _i32, _i32, _vp]),
+        "hs_select_workspace_bytes": (ctypes.c_size_t, [_i32, _i32, _i32, _i32]),
+        "hs_select_blocks": (ctypes.c_int, [_vp, _vp]),
+        "hs_prefix_workspace_bytes": (ctypes.c_size_t, [_fmtp, _vp]),
+        "hs_attend_prefix": (ctypes.c_int, [_fmtp, _vp, _vp]),
         "hs_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "hs_version": (_i32, []),
     }
@@ -847,3 +900,252 @@ def hs_compact_kv(fmt: HsKvFormat, src_rows, src_scales, src_req, keep, kept, ds
          _ptr(kept, i32, "kept", dev), B, budget, _ptr(dst_rows, u8, "dst_rows", dev),
          _ptr(dst_scales, f32, "dst_scales", dev), dR, dL, _ptr(dst_req, i32, "dst_req", dev),
          _raw_stream(stream, dev))
+
+
+# ---- around a decode step: norms and rotation, block selection, shared prefix ----
+
+_NORM_ROPE_ARGS = struct.Struct("@4P9if3q3q3q3q6P")  # hs_norm_rope_args
+_STRIDES = struct.Struct("@3q")
+_SELECT_ARGS = struct.Struct("@PP12i3q6PN")  # hs_select_args
+_PREFIX_ARGS = struct.Struct("@PP7if3q3q3q9PN")  # hs_prefix_args
+_NO_SIZES = ctypes.c_size_t(-1).value
+
+
+class HsRope:
+    """Frequencies of a position rotation on one device (make_rope)."""
+
+    def __init__(self, turns, axis, rot_dim: int, num_axes: int, adjacent: bool):
+        self.turns, self.axis = turns, axis  # int64 and int32 [rot_dim / 2]; axis None: all 0
+        self.rot_dim, self.num_axes, self.adjacent = rot_dim, num_axes, adjacent
+
+
+def make_rope(inv_freq, axis=None, adjacent: bool = False, device=None) -> HsRope:
+    """inv_freq: radians per position of each pair (floats or a 64-bit tensor), a multiple of 8
+    of them; axis: the position axis of each pair (all 0 by default); adjacent: pairs are
+    (2 j, 2 j + 1) instead of (j, j + rot_dim / 2)."""
+    import math
+    import torch
+    freq = [float(f) for f in inv_freq]
+    axis = None if axis is None else [int(x) for x in axis]
+    if len(freq) % 8 or not all(math.isfinite(f) for f in freq):
+        raise ValueError("inv_freq must be a multiple of 8 finite numbers")
+    if axis is not None and (len(axis) != len(freq)
+                             or any(not 0 <= x < HS_MAX_ROPE_AXES for x in axis)):
+        raise ValueError("axis must give an axis from 0 to %d for every pair"
+                         % (HS_MAX_ROPE_AXES - 1))
+    # parts of a turn in 64-bit fixed point, whole turns dropped
+    turns = [round(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in freq]
+    turns = [x - 2 ** 64 if x >= 2 ** 63 else x for x in turns]
+    device = torch.device(device or "cuda")
+    num_axes = 1 + max(axis, default=0) if axis else 1
+    if num_axes == 1:
+        axis = None
+    return HsRope(torch.tensor(turns, dtype=torch.int64, device=device),
+                  None if axis is None else torch.tensor(axis, dtype=torch.int32, device=device),
+                  2 * len(freq), num_axes, bool(adjacent))
+
+
+def _heads(t, name, batch_tokens=None, dim=None):
+    """Shape of a tensor [batch, tokens, heads, D] (dense last dimension)."""
+    shape = t.shape
+    if len(shape) != 4 or (dim is not None and shape[3] != dim) or (
+            batch_tokens is not None and shape[:2] != batch_tokens):
+        raise ValueError("%s must be [batch, tokens, heads, head_dim]%s, got %s"
+                         % (name, "" if dim is None else " with %s and head_dim %d"
+                            % (tuple(batch_tokens), dim), tuple(shape)))
+    return shape
+
+
+def hs_norm_rope(q, k, positions, rope: Optional[HsRope], q_out, k_out, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, count=None, stream=None) -> None:
+    """Norms of the heads of q [batch, tokens, heads, D] and k [batch, tokens, kv heads, D] (bf16,
+    fp16 or fp32; either may be None), each if its weight (fp32 [D]) is given, and the rotation
+    by positions int32 [axes, batch, tokens] ([batch, tokens] for one axis; rope None: no
+    rotation) into q_out and k_out, which may be q and k.  count int32 [batch]: tokens
+    of each entry."""
+    import torch
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k must be given")
+    B, M, _, D = _heads(one, "q" if q is not None else "k")
+    dev, i32, f32 = one.get_device(), torch.int32, torch.float32
+    sides, ptrs, strides, heads = ((q, q_out, "q"), (k, k_out, "k")), [], [], []
+    for t, out, name in sides:
+        if (t is None) != (out is None):
+            raise ValueError("%s and %s_out must be given together" % (name, name))
+        if t is None:
+            ptrs.append((0, 0))
+            strides.append(((0, 0, 0), (0, 0, 0)))
+            heads.append(0)
+            continue
+        shape = _heads(t, name, one.shape[:2], D)
+        if out.shape != shape:
+            _shape(out, shape, name + "_out")
+        if t.dtype is not one.dtype or out.dtype is not one.dtype:
+            raise ValueError("q, k and their outputs must have one dtype")
+        ptrs.append((_sptr(t, name, dev), _sptr(out, name + "_out", dev)))
+        strides.append((t.stride()[:3], out.stride()[:3]))
+        heads.append(shape[2])
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.shape != (D,):
+            _shape(w, (D,), name)
+    rot, axes, turns, axis, pos = 0, 1, 0, 0, 0
+    if rope is not None:
+        rot, axes = rope.rot_dim, rope.num_axes
+        if positions is None or (positions.shape != (axes, B, M)
+                                 and (axes > 1 or positions.shape != (B, M))):
+            raise ValueError("positions must be [%d, %d, %d]" % (axes, B, M))
+        turns = _ptr(rope.turns, torch.int64, "the rotation's frequencies", dev)
+        axis = _ptr(rope.axis, i32, "the rotation's axes", dev)
+        pos = _ptr(positions, i32, "positions", dev)
+    if count is not None and count.shape != (B,):
+        _shape(count, (B,), "count")
+    args = _NORM_ROPE_ARGS.pack(
+        ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1], _dtype_code(one, "q and k", True), B, M,
+        heads[0], heads[1], D, rot, 1 if rope is not None and rope.adjacent else 0, axes, eps,
+        *strides[0][0], *strides[1][0], *strides[0][1], *strides[1][1],
+        _ptr(q_weight, f32, "q_weight", dev), _ptr(k_weight, f32, "k_weight", dev), pos, turns,
+        axis, _ptr(count, i32, "count", dev))
+    _run("hs_norm_rope", dev, args, _raw_stream(stream, dev))
+
+
+def bounds_shape(num_requests: int, max_seq_len: int, block_tokens: int, num_kv_heads: int,
+                 head_dim: int):
+    """Shape of the bounds on the keys of a store (hs_bound_keys)."""
+    return (num_requests, -(-max_seq_len // block_tokens), num_kv_heads, 2, head_dim)
+
+
+def _bounds(bounds, block_tokens, max_seq_len, heads, dim) -> int:
+    """Requests of bounds [R, NB, Hkv, 2, D]."""
+    if block_tokens < 1 or max_seq_len < 1:
+        raise ValueError("need block_tokens >= 1 and max_seq_len >= 1")
+    R = bounds.shape[0] if bounds.dim() else 0
+    if bounds.shape != (R, -(-max_seq_len // block_tokens), heads, 2, dim):
+        _shape(bounds, bounds_shape(R, max_seq_len, block_tokens, heads, dim), "bounds")
+    return R
+
+
+def hs_bound_keys(k, req, start, count, block_tokens: int, max_seq_len: int, bounds,
+                  stream=None) -> None:
+    """Least and greatest key of each block of tokens: k [batch, tokens, Hkv, D] (bf16 or fp16,
+    any strides but a dense last dimension) are the tokens [start[b], start[b] + count[b]) of
+    request req[b]; bounds [R, NB, Hkv, 2, D] of k's type, updated."""
+    import torch
+    B, M, H, D = _heads(k, "k")
+    R = _bounds(bounds, block_tokens, max_seq_len, H, D)
+    if bounds.dtype is not k.dtype:
+        raise ValueError("bounds must have k's dtype")
+    one = k.shape[:1]
+    if req.shape != one or start.shape != one or count.shape != one:
+        _shape(req, one, "req")
+        _shape(start, one, "start")
+        _shape(count, one, "count")
+    i32, dev = torch.int32, _device_of(k, "k")
+    _run("hs_bound_keys", dev, _sptr(k, "k", dev), _STRIDES.pack(*k.stride()[:3]),
+         _dtype_code(k, "k", False), H, D, block_tokens, _ptr(req, i32, "req", dev),
+         _ptr(start, i32, "start", dev), _ptr(count, i32, "count", dev), B, M,
+         _ptr(bounds, bounds.dtype, "bounds", dev), R, max_seq_len, _raw_stream(stream, dev))
+
+
+def hs_select_workspace_bytes(batch: int, steps: int, max_seq_len: int, block_tokens: int) -> int:
+    """Device bytes of workspace that hs_select_blocks needs for these sizes."""
+    n = load_library().hs_select_workspace_bytes(batch, steps, max_seq_len, block_tokens)
+    if n == _NO_SIZES:
+        raise HsError(HS_ERR_INVALID_ARG, "hs_select_workspace_bytes")
+    return n
+
+
+def hs_select_blocks(q, bounds, req, seq_lens, block_tokens: int, max_seq_len: int, first: int,
+                     last: int, blocks, topk, scores, workspace, stream=None) -> None:
+    """Selects key blocks for q [batch, steps, heads, D] (bf16 or fp16) by the bounds
+    [R, NB, Hkv, 2, D] of the same type: the first `first`, the last `last` and those of the largest
+    scores.  Outputs: blocks int32 [batch, steps, n] or None, topk int32
+    [batch, steps, n * block_tokens] (their tokens), scores fp32 [batch, steps, NB]."""
+    import torch
+    B, S, H, D = _heads(q, "q")
+    if bounds.dim() != 5:
+        raise ValueError("bounds must be [requests, blocks, heads, 2, head_dim]")
+    R = _bounds(bounds, block_tokens, max_seq_len, bounds.shape[2], D)
+    if bounds.dtype is not q.dtype:
+        raise ValueError("bounds must have q's dtype")
+    if topk.dim() != 3 or topk.shape[2] % block_tokens:
+        raise ValueError("topk must be [batch, steps, blocks * %d], got %s"
+                         % (block_tokens, tuple(topk.shape)))
+    n = topk.shape[2] // block_tokens
+    one = q.shape[:1]
+    if (topk.shape[:2] != q.shape[:2] or scores.shape != (B, S, bounds.shape[1])
+            or req.shape != one or seq_lens.shape != one
+            or (blocks is not None and blocks.shape != (B, S, n))):
+        _shape(topk, (B, S, n * block_tokens), "topk")
+        _shape(scores, (B, S, bounds.shape[1]), "scores")
+        _shape(req, one, "req")
+        _shape(seq_lens, one, "seq_lens")
+        _shape(blocks, (B, S, n), "blocks")
+    i32, dev = torch.int32, _device_of(q, "q")
+    args = _SELECT_ARGS.pack(
+        _sptr(q, "q", dev), _ptr(bounds, bounds.dtype, "bounds", dev), _dtype_code(q, "q", False),
+        B, S, H, bounds.shape[2], D, R, max_seq_len, block_tokens, n, first, last,
+        *q.stride()[:3], _ptr(req, i32, "req", dev), _ptr(seq_lens, i32, "seq_lens", dev),
+        _ptr(blocks, i32, "blocks", dev), _ptr(topk, i32, "topk", dev),
+        _ptr(scores, torch.float32, "scores", dev),
+        _ptr(workspace, workspace.dtype, "workspace", dev),
+        workspace.numel() * workspace.element_size())
+    _run("hs_select_blocks", dev, args, _raw_stream(stream, dev))
+
+
+def hs_prefix_workspace_bytes(fmt: HsKvFormat, batch: int, steps: int, num_heads: int,
+                              num_prefixes: int) -> int:
+    """Device bytes of workspace that hs_attend_prefix needs for these sizes."""
+    args = _HsPrefixArgs(batch=batch, steps=steps, num_heads=num_heads, num_prefixes=num_prefixes)
+    n = load_library().hs_prefix_workspace_bytes(fmt, ctypes.byref(args))
+    if n == _NO_SIZES:
+        raise HsError(HS_ERR_INVALID_ARG, "hs_prefix_workspace_bytes")
+    return n
+
+
+def hs_attend_prefix(fmt: HsKvFormat, q, rows, scales, prefix, lens, starts, out, lse=None,
+                     join_out=None, join_lse=None, sm_scale: Optional[float] = None,
+                     workspace=None, stream=None) -> None:
+    """Attention of q [batch, steps, heads, D] (bf16 or fp16) over prefixes that consecutive batch
+    rows share: rows starts[p] .. starts[p + 1] - 1 (starts int32 [P + 1]) attend to the first
+    lens[p] tokens of request prefix[p] of the store rows uint8 [R, L, W], scales fp32
+    [R, NB, 2, Hkv].  Outputs: out as q, lse fp32 [batch, steps, heads].  join_out and join_lse: the
+    same queries' attention over other tokens, to be joined (they may be out and lse).
+    sm_scale: 1 / sqrt(D) by default."""
+    import torch
+    B, S, H, D = _heads(q, "q")
+    if D != fmt.head_dim:
+        raise ValueError("q must be [batch, steps, heads, %d], got %s"
+                         % (fmt.head_dim, tuple(q.shape)))
+    R, L = _store(fmt, rows, scales, "")
+    P = prefix.shape[0] if prefix.dim() else 0
+    if prefix.shape != (P,) or lens.shape != (P,) or starts.shape != (P + 1,):
+        _shape(prefix, (P,), "prefix")
+        _shape(lens, (P,), "lens")
+        _shape(starts, (P + 1,), "starts")
+    if out.shape != q.shape:
+        _shape(out, q.shape, "out")
+    if out.dtype is not q.dtype:
+        raise ValueError("out must have q's dtype")
+    if lse is not None and lse.shape != (B, S, H):
+        _shape(lse, (B, S, H), "lse")
+    dev, join, strides = _device_of(q, "q"), 0, (0, 0, 0)
+    if (join_out is None) != (join_lse is None):
+        raise ValueError("join_out and join_lse must be given together")
+    if join_out is not None:
+        if join_out.dtype is not q.dtype:
+            raise ValueError("join_out must have q's dtype")
+        _shape(join_out, q.shape, "join_out")
+        _shape(join_lse, (B, S, H), "join_lse")
+        join, strides = _sptr(join_out, "join_out", dev), join_out.stride()[:3]
+    i32, f32 = torch.int32, torch.float32
+    args = _PREFIX_ARGS.pack(
+        _sptr(q, "q", dev), _sptr(out, "out", dev), _dtype_code(q, "q", False), B, S, H, R, L, P,
+        D ** -0.5 if sm_scale is None else sm_scale, *q.stride()[:3], *out.stride()[:3], *strides,
+        _ptr(rows, torch.uint8, "rows", dev), _ptr(scales, f32, "scales", dev),
+        _ptr(prefix, i32, "prefix", dev), _ptr(lens, i32, "lens", dev),
+        _ptr(starts, i32, "starts", dev), _ptr(lse, f32, "lse", dev), join,
+        _ptr(join_lse, f32, "join_lse", dev),
+        0 if workspace is None else _ptr(workspace, workspace.dtype, "workspace", dev),
+        0 if workspace is None else workspace.numel() * workspace.element_size())
+    _run("hs_attend_prefix", dev, fmt, args, _raw_stream(stream, dev))

@@ -1,0 +1,206 @@
+// Launch of hs_attend_prefix (the kernel is in hs_prefix.cuh), and the kernel that puts
+// together the rows whose tokens fell to several CTAs.
+//
+// A CTA takes 32 rows of a K/V head, a lane a row, the warps the quads of its elements; partial
+// outputs lie with consecutive rows side by side.  They come mostly out of L2.
+#include "hs_prefix.cuh"
+
+namespace hs {
+namespace {
+
+using prefix::Joined;
+using prefix::Plan;
+
+constexpr int kWarps = 16;
+
+__global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a, int D,
+                                                              int groups) {
+    __shared__ Plan plan;
+    __shared__ long long s_first[kPrefixCtas + 1];  // first unit of every CTA
+    __shared__ float s_factor[kPrefixCtas][32];     // of a CTA's part of a row
+    __shared__ float s_tmp[kWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tile_tokens = prefix_tokens(D), tile_rows = kPrefixRows * prefix_pipes(D);
+    wait_for_previous();
+    if (warp == 0) prefix::fill_plan(plan, a, tile_rows, tile_tokens);
+    __syncthreads();
+    release_next();
+    const long long units = plan.unit[a.P];
+    const int ctas = prefix::working(units, a.ctas);
+    for (int c = threadIdx.x; c <= ctas; c += 32 * kWarps)
+        s_first[c] = ctas > 0 ? prefix::first_unit(units, c, ctas) : 0;
+    __syncthreads();
+    const int h = blockIdx.x / groups, all = a.B * a.S * a.G;
+    const int i = (blockIdx.x - h * groups) * 32 + lane;  // row of all batch rows
+    const bool on = i < all;
+    const prefix::Row at(a, 0, h, on ? i : 0);
+    const long long out_row = ((long long)at.b * a.S + at.s) * a.Hq + at.head;
+    int p = a.P - 1;  // the row's prefix: the last that begins at its batch row or before, and has rows
+    while (p >= 0 && (plan.lo[p] > at.b || plan.hi[p] <= plan.lo[p])) --p;
+    const bool some = on && p >= 0 && at.b < plan.hi[p] && plan.len[p] > 0;
+    int first = 0, last = -1;  // CTAs with units of the row's tile
+    long long unit0 = 0;
+    int tile_row = 0;
+    if (some) {
+        const int rows = (plan.hi[p] - plan.lo[p]) * a.S * a.G;
+        const int tiles = (plan.len[p] + tile_tokens - 1) / tile_tokens;
+        const int r = i - plan.lo[p] * a.S * a.G, row_tiles = (rows + tile_rows - 1) / tile_rows;
+        tile_row = r % tile_rows;
+        unit0 = plan.unit[p] + (long long)(h * row_tiles + r / tile_rows) * tiles;
+        // The last CTA that begins at unit0 or before, and at the tile's last unit or before.
+        auto owner = [&](long long unit) {
+            int lo = 0, hi = ctas;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (s_first[mid] <= unit)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            return lo;
+        };
+        first = owner(unit0);
+        last = owner(unit0 + tiles - 1);
+    }
+    // Where one CTA has the whole tile, it has written the outputs.
+    const bool mine = on && (!some || last > first);
+    const int parts = some && mine ? last - first + 1 : 0;
+    // A CTA's part lies in the place of its first segment if it begins within the tile.
+    auto place = [&](int c) {
+        return (2 * (long long)c + (s_first[c] >= unit0 ? 0 : 1)) * tile_rows;
+    };
+    // The factors of a row's parts, a warp every 16th of them: sums relative to the largest.
+    float top = -INFINITY;
+    bool nan = false;
+    for (int c = warp; c < parts; c += kWarps) {
+        const float2 x = ld(a.part_sum + place(first + c) + tile_row);
+        const float y = x.x + log2f(x.y);
+        top = fmaxf(top, y);
+        nan = nan || !(y == y);
+    }
+    s_tmp[warp][lane] = nan ? NAN : top;
+    __syncthreads();
+    top = s_tmp[0][lane];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+        const float y = s_tmp[w][lane];
+        top = y == y && top == top ? fmaxf(top, y) : NAN;
+    }
+    __syncthreads();
+    float sum = 0.f;
+    for (int c = warp; c < parts; c += kWarps) {
+        const float2 x = ld(a.part_sum + place(first + c) + tile_row);
+        const float f = exp2f(x.x - top);
+        s_factor[c][lane] = f;
+        sum += x.y * f;
+    }
+    s_tmp[warp][lane] = sum;
+    // before any warp writes lse, which may be the same array
+    const float other = on && a.join ? ld(a.join_lse + out_row) : -INFINITY;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += s_tmp[w][lane];
+    if (!mine) return;
+    const Joined j(some ? top + log2f(sum) : -INFINITY, other);
+    if (warp == 0 && a.lse) a.lse[out_row] = j.lse;
+    const float by = some ? j.mine / sum : 0.f;
+    uint16_t* out = a.out + at.at(a.out_stride);
+    const uint16_t* join = a.join + at.at(a.join_stride);
+    const int quads = D / 4;
+    const float4* part = reinterpret_cast<const float4*>(a.part) + tile_row;
+    for (int d = warp; d < quads; d += kWarps) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int c = 0; c < parts; ++c) {
+            const float f = s_factor[c][lane];
+            const float4 z = ld(part + place(first + c) * quads + (long long)d * tile_rows);
+            y = make_float4(y.x + z.x * f, y.y + z.y * f, y.z + z.z * f, y.w + z.w * f);
+        }
+        y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+        if (j.other > 0.f) {
+            const uint2 z = prefix::load4(join + 4 * d, a.vec_join);
+            const float2 z0 = prefix::pair(z.x, a.fp16), z1 = prefix::pair(z.y, a.fp16);
+            y = make_float4(y.x + z0.x * j.other, y.y + z0.y * j.other, y.z + z1.x * j.other,
+                            y.w + z1.y * j.other);
+        }
+        prefix::store4(out + 4 * d, prefix::unpair(y.x, y.y, a.fp16),
+                       prefix::unpair(y.z, y.w, a.fp16), a.vec_out);
+    }
+}
+
+// CTAs of the kernel: one an SM of the current device.
+int prefix_ctas() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+        cudaGetLastError();
+        sms = 152;
+    }
+    return sms < kPrefixCtas ? sms : kPrefixCtas;
+}
+
+size_t part_bytes(const hs_kv_format& f, int ctas) {
+    return (size_t)ctas * 2 * kPrefixRows * prefix_pipes(f.head_dim) * f.head_dim * sizeof(float);
+}
+
+}  // namespace
+
+size_t prefix_workspace(const hs_kv_format& f) {
+    const int ctas = prefix_ctas();
+    return part_bytes(f, ctas) + (size_t)ctas * 2 * kPrefixRows * prefix_pipes(f.head_dim) *
+                                     sizeof(float2);
+}
+
+cudaError_t launch_prefix(const hs_kv_format& f, const hs_prefix_args& x, cudaStream_t s) {
+    PrefixArgs a = {};
+    a.q = static_cast<const uint16_t*>(x.q_dev);
+    a.out = static_cast<uint16_t*>(x.out_dev);
+    a.fp16 = x.dtype == HS_DTYPE_FP16;
+    a.B = x.batch;
+    a.S = x.steps;
+    a.Hq = x.num_heads;
+    a.Hkv = f.num_kv_heads;
+    a.G = x.num_heads / f.num_kv_heads;
+    a.R = x.num_requests;
+    a.L = x.max_seq_len;
+    a.NB = (x.max_seq_len - 1) / f.block_tokens + 1;
+    a.W = f.item_size_bytes;
+    a.P = x.num_prefixes;
+    a.block = Divisor::by(f.block_tokens);
+    a.scale_log2 = fabsf(x.sm_scale) * 1.4426950408889634f;
+    a.k_sign = x.sm_scale < 0.f ? -1.f : 1.f;
+    a.vec_q = (uintptr_t)x.q_dev % 16 == 0;
+    a.vec_out = (uintptr_t)x.out_dev % 8 == 0;
+    a.vec_join = (uintptr_t)x.join_out_dev % 8 == 0;
+    for (int i = 0; i < 3; ++i) {
+        a.q_stride[i] = x.q_stride[i];
+        a.out_stride[i] = x.out_stride[i];
+        a.join_stride[i] = x.join_stride[i];
+        a.vec_q = a.vec_q && x.q_stride[i] % 8 == 0;
+        a.vec_out = a.vec_out && x.out_stride[i] % 4 == 0;
+        a.vec_join = a.vec_join && x.join_stride[i] % 4 == 0;
+    }
+    a.rows = static_cast<const uint8_t*>(x.rows_dev);
+    a.scales = x.scales_dev;
+    a.prefix = x.prefix_dev;
+    a.lens = x.lens_dev;
+    a.starts = x.starts_dev;
+    a.lse = x.lse_dev;
+    a.join = static_cast<const uint16_t*>(x.join_out_dev);
+    a.join_lse = x.join_lse_dev;
+    a.ctas = prefix_ctas();
+    uint8_t* ws = static_cast<uint8_t*>(x.workspace_dev);
+    a.part = reinterpret_cast<float*>(ws);
+    a.part_sum = reinterpret_cast<float2*>(ws + part_bytes(f, a.ctas));
+    if (a.P > 0) {
+        const cudaError_t e = f.code == HS_KV_E4M3 ? prefix_run_e4m3(a, f.head_dim, s)
+                                                   : prefix_run_int8(a, f.head_dim, s);
+        if (e != cudaSuccess) return e;
+    }
+    const int groups = (int)(((long long)a.B * a.S * a.G + 31) / 32);
+    return launch_chained(combine_kernel, a.Hkv * groups, 32 * kWarps, 0, 0, s, a, f.head_dim,
+                          groups);
+}
+
+}  // namespace hs

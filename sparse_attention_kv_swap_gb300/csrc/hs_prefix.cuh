@@ -1,0 +1,900 @@
+// Attention over prefixes that requests of a batch share (sm_103a); the contract is
+// hs_attend_prefix's in include/hisparse_swap.h.
+//
+// The queries of all requests of a prefix that read one K/V head are the rows of two matrix products
+// with that head's keys and values, and each tile of these is read once for up to 256 rows.  One
+// CTA an SM; the work is a list of units, one unit being a tile of tokens for a tile of rows of a
+// K/V head, and every CTA takes an equal run of consecutive ones, so that few rows over a long
+// prefix and many rows over a short one fill the SMs alike.  Rows whose units fell to several
+// CTAs are put together by a second kernel (combine_kernel, hs_prefix.cu).
+//
+// Warps of a CTA:
+//   converters (4)  read codes, write them as f16 to shared memory in the layout of the matrix
+//                   instructions (128-byte swizzle), one tile ahead in registers, two in shared
+//                   memory; and the tokens' scales.  Codes are exact in f16.
+//   matrix (1)      S = Q K^T (128 rows x TOK tokens) and O += P V by tcgen05.mma, accumulators and P
+//                   in tensor memory
+//   softmax (4 for each of the NPIPE pipelines)   a thread has a row: it reads S, writes P over it
+// Two pipelines (D <= 128) keep the matrix instructions busy while one of them is in its
+// softmax: they hold rows 0-127 and 128-255 of a row tile, or, where it has 128 rows or fewer, the even
+// and the odd tiles of tokens of the same rows.
+//
+// Numbers: a query is scaled by a power of two into f16's range, as in hs_attend.  With z = s log2(e)
+// and v_t the V scale, the row keeps one reference r:
+//   p_t = 2^(z_t - r),  l = sum p_t,  P_t = f16(p_t v_t),  O = sum P_t code_t,  out = O / l
+// r is chosen so that the largest p_t v_t so far lies between 2^11 and 2^16 (r grows only when that
+// is passed, and O and l are scaled then): f16 keeps its 11 bits down to 2^-26 of the largest term and
+// is off by 2^-36 of it below.  Where V scales differ by 2^88 and more, r stays within 100
+// of the largest z, so that l stays in range.
+#pragma once
+
+#include "hs_step.cuh"
+
+namespace hs {
+
+constexpr int kPrefixRows = 128;  // of a pipeline
+constexpr int kPrefixCtas = 256;  // at most
+
+struct PrefixArgs {
+    const uint16_t* q;
+    uint16_t* out;
+    int32_t fp16, B, S, G, Hq, Hkv, R, L, NB, W, P;
+    Divisor block;     // by block_tokens
+    float scale_log2;  // |sm_scale| * log2(e)
+    float k_sign;      // its sign
+    int64_t q_stride[3], out_stride[3], join_stride[3];
+    int32_t vec_q, vec_out, vec_join;
+    const uint8_t* rows;
+    const float* scales;
+    const int32_t* prefix;
+    const int32_t* lens;
+    const int32_t* starts;
+    float* lse;
+    const uint16_t* join;
+    const float* join_lse;
+    int32_t ctas;
+    float* part;       // [ctas][2][D / 4][rows of a tile][4] outputs
+    float2* part_sum;  // [ctas][2][rows of a tile] (r, l)
+};
+
+constexpr int prefix_pipes(int D) { return D <= 128 ? 2 : 1; }
+constexpr int prefix_tokens(int D) { return D <= 128 ? 128 : 64; }
+constexpr int prefix_panels(int D) { return (D + 63) / 64; }
+
+cudaError_t prefix_run_e4m3(const PrefixArgs& a, int D, cudaStream_t s);
+cudaError_t prefix_run_int8(const PrefixArgs& a, int D, cudaStream_t s);
+
+#ifdef __CUDACC__
+
+namespace prefix {
+
+// The prefixes of a call and their units.
+struct Plan {
+    int32_t lo[HS_MAX_PREFIXES], hi[HS_MAX_PREFIXES];  // batch rows
+    int32_t len[HS_MAX_PREFIXES];
+    long long unit[HS_MAX_PREFIXES + 1];  // first unit; units of a prefix: [K/V head][row tile][tile]
+};
+
+// Filled by one warp; everyone else waits at the caller's barrier.
+__device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int rows, int tokens) {
+    const int lane = threadIdx.x & 31;
+    int taken = 0;          // batch rows of the prefixes before
+    long long units = 0;
+    for (int p0 = 0; p0 < a.P; p0 += 32) {
+        const int p = p0 + lane;
+        int first = 0, end = 0, len = 0;
+        if (p < a.P) {
+            first = min(max(ld(a.starts + p), 0), a.B);
+            end = max(min(max(ld(a.starts + p + 1), 0), a.B), first);
+            const int r = ld(a.prefix + p);
+            len = r < 0 || r >= a.R ? 0 : min(max(ld(a.lens + p), 0), a.L);
+        }
+        int most = max(end, taken);  // the largest end up to this prefix
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, most, o);
+            if (lane >= o) most = max(most, x);
+        }
+        int before = __shfl_up_sync(0xffffffffu, most, 1);
+        if (lane == 0) before = taken;
+        const int lo = max(first, before), hi = max(end, lo);
+        const long long n = (long long)(hi - lo) * a.S * a.G;
+        long long mine = 0;
+        if (p < a.P && len > 0)
+            mine = a.Hkv * ((n + rows - 1) / rows) * ((len + tokens - 1) / tokens);
+        long long sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (p < a.P) {
+            plan.lo[p] = lo;
+            plan.hi[p] = hi;
+            plan.len[p] = len;
+            plan.unit[p] = units + sum - mine;
+        }
+        units += __shfl_sync(0xffffffffu, sum, 31);
+        taken = __shfl_sync(0xffffffffu, most, 31);
+    }
+    if (lane == 0) plan.unit[a.P] = units;
+}
+
+// CTAs with work: each has a unit or more.
+__device__ __forceinline__ int working(long long units, int ctas) {
+    return (int)min(units, (long long)ctas);
+}
+// First unit of CTA `cta` of `n` that work.
+__device__ __forceinline__ long long first_unit(long long units, int cta, int n) {
+    return units * cta / n;
+}
+
+// Consecutive units of one tile of rows.
+struct Segment {
+    int p, h, row0, rows;  // prefix, K/V head, first row of the tile, rows of the prefix
+    int tile0, n, tiles;   // tiles of tokens: the first, how many, all of the prefix
+    __device__ __forceinline__ Segment(const Plan& plan, const PrefixArgs& a, long long from,
+                                       long long to, int tile_rows, int tile_tokens) {
+        p = a.P - 1;
+        while (plan.unit[p] > from) --p;  // the last one that begins here or before: not empty
+        rows = (plan.hi[p] - plan.lo[p]) * a.S * a.G;
+        tiles = (plan.len[p] + tile_tokens - 1) / tile_tokens;
+        const long long at = from - plan.unit[p];
+        const int turn = (int)(at / tiles), row_tiles = (rows + tile_rows - 1) / tile_rows;
+        tile0 = (int)(at - (long long)turn * tiles);
+        h = turn / row_tiles;
+        row0 = (turn - h * row_tiles) * tile_rows;
+        n = (int)min((long long)(tiles - tile0), to - from);
+    }
+};
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+// ---- barriers in shared memory --------------------------------------------------
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_n(uint32_t bar, int n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Waits for the phase of this parity, for two seconds at most: then, or once another thread has
+// given up, the CTA goes on without waiting and its outputs become NaN.
+__device__ __forceinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+    unsigned long long begin = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (try_wait(bar, parity) || *gave_up) return;
+        if ((i & 255) == 255) {
+            const unsigned long long now = global_timer();
+            if (begin == 0) begin = now;
+            if (now - begin > 2000000000ull) *gave_up = 1;
+        }
+    }
+}
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+    if (!try_wait(bar, parity)) wait_slow(bar, parity, gave_up);
+}
+
+// ---- tensor memory and matrix instructions -----------------------------------------
+
+__device__ __forceinline__ void load_columns(uint32_t (&x)[32], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+          "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
+          "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), "=r"(x[19]),
+          "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]), "=r"(x[24]), "=r"(x[25]),
+          "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
+        : "r"(at)
+        : "memory");
+}
+// The loaded values may be used after this.
+__device__ __forceinline__ void loaded(uint32_t (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(x[i]));
+}
+__device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31, %32};" ::"r"(at),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]),
+        "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]),
+        "r"(x[15]), "r"(x[16]), "r"(x[17]), "r"(x[18]), "r"(x[19]), "r"(x[20]), "r"(x[21]),
+        "r"(x[22]), "r"(x[23]), "r"(x[24]), "r"(x[25]), "r"(x[26]), "r"(x[27]), "r"(x[28]),
+        "r"(x[29]), "r"(x[30]), "r"(x[31])
+        : "memory");
+}
+__device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(at),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]),
+        "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]),
+        "r"(x[15])
+        : "memory");
+}
+__device__ __forceinline__ void stored() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// What this thread has written to shared memory is seen by the matrix instructions issued after
+// a barrier that it arrives at next.
+__device__ __forceinline__ void fence_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Descriptor of a matrix in shared memory with the 128-byte swizzle: rows of 128 bytes, eight to a
+// group of 1024; `lead` is the distance of panels of 64 elements where the rows run along the
+// product's sum (V), and unused where they run along its result (Q, K).
+__device__ __forceinline__ uint64_t matrix(uint32_t at, uint32_t lead) {
+    return (uint64_t)((at & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 |
+           (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// f16 by f16 into f32, 128 rows and n columns; B by columns of the sum if `rows_of_sum`.
+constexpr uint32_t instruction(int n, bool rows_of_sum) {
+    return 1u << 4 | (rows_of_sum ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t kind,
+                                         bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void multiply_tensor(uint32_t d, uint32_t a, uint64_t b, uint32_t kind,
+                                                bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+        : "memory");
+}
+// The barrier gets an arrival once the matrix instructions that this thread has issued are done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+
+// ---- arithmetic ------------------------------------------------------------------
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 pair(uint32_t w, int fp16) {
+    if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t unpair(float a, float b, int fp16) {
+    if (fp16) return pack_half2(a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight 16-bit elements.
+__device__ __forceinline__ uint4 load8(const uint16_t* p, bool vec) {
+    if (vec) return ld(reinterpret_cast<const uint4*>(p));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)ld(p + 2 * i) | (uint32_t)ld(p + 2 * i + 1) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint2 load4(const uint16_t* p, bool vec) {
+    if (vec) return ld(reinterpret_cast<const uint2*>(p));
+    return make_uint2((uint32_t)ld(p) | (uint32_t)ld(p + 1) << 16,
+                      (uint32_t)ld(p + 2) | (uint32_t)ld(p + 3) << 16);
+}
+__device__ __forceinline__ void store4(uint16_t* p, uint32_t a, uint32_t b, bool vec) {
+    if (vec) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+    } else {
+        p[0] = (uint16_t)a, p[1] = (uint16_t)(a >> 16);
+        p[2] = (uint16_t)b, p[3] = (uint16_t)(b >> 16);
+    }
+}
+
+// The codes in the low and the high half of a word, as two f16 pairs.
+template <int CODE>
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (CODE == HS_KV_E4M3) {
+        __half2 x, y;
+        decode_halves(w, x, y);
+        lo = *reinterpret_cast<const uint32_t*>(&x);
+        hi = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+        // 0x6400 | x is the f16 1024 + x for a byte x: with the code's sign bit
+        // flipped, x = code + 128, and 1152 is taken off exactly.
+        const uint32_t x = w ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));
+        uint32_t p = __byte_perm(x, 0x64646464u, 0x4140), q = __byte_perm(x, 0x64646464u, 0x4342);
+        const __half2 a = __hsub2(*reinterpret_cast<__half2*>(&p), off);
+        const __half2 b = __hsub2(*reinterpret_cast<__half2*>(&q), off);
+        lo = *reinterpret_cast<const uint32_t*>(&a);
+        hi = *reinterpret_cast<const uint32_t*>(&b);
+    }
+}
+
+// Place of 8 elements (16 bytes) in a matrix of rows of 128 bytes, 64 elements to a panel.
+__device__ __forceinline__ uint32_t place(int row, int d, int panel_bytes) {
+    return (uint32_t)(d / 64 * panel_bytes + row * 128 + (((d % 64) / 8 ^ (row & 7)) << 4));
+}
+
+// A query row: batch row, step, head.
+struct Row {
+    int b, s, head;
+    __device__ __forceinline__ Row(const PrefixArgs& a, int first, int h, int r) {
+        const int sg = a.S * a.G, m = r / sg, rest = r - m * sg;
+        b = first + m;
+        s = rest / a.G;
+        head = h * a.G + rest - s * a.G;
+    }
+    __device__ __forceinline__ long long at(const int64_t (&stride)[3]) const {
+        return b * stride[0] + s * stride[1] + head * stride[2];
+    }
+};
+
+// How a row's own attention over the prefix, of log2-sum-exp `lse2` (-inf: none), is joined
+// with the given one: the factors of both outputs and the lse.
+struct Joined {
+    float mine, other, lse;
+    // `o`: the given lse, -inf without one.
+    __device__ __forceinline__ Joined(float lse2, float o) {
+        const float e = lse2 * 0.69314718056f;
+        mine = lse2 == -INFINITY ? 0.f : 1.f;
+        other = 0.f;
+        lse = e;
+        if (o == -INFINITY) return;
+        const float top = fmaxf(e, o);
+        const float x = expf(e - top), y = expf(o - top), sum = x + y;
+        mine = x / sum;
+        other = y / sum;
+        lse = top + logf(sum);
+    }
+};
+
+// ---- the kernel -------------------------------------------------------------------
+
+template <int D>
+struct Shape {
+    static constexpr int kPipes = prefix_pipes(D), kTok = prefix_tokens(D);
+    static constexpr int kPanels = prefix_panels(D);
+    static constexpr int kRows = kPrefixRows * kPipes;          // of a tile
+    static constexpr int kQ = kPanels * kPrefixRows * 128;      // bytes of a pipeline's queries
+    static constexpr int kTile = kPanels * kTok * 128;          // of a tile's keys or values
+    static constexpr int kStages = 2, kScales = 4;              // tiles under way
+    static constexpr int kSoftmax = 4 * kPipes, kConvert = 4;   // warps
+    static constexpr int kThreads = 32 * (kSoftmax + kConvert + 1);
+    static constexpr int kSmem = kPipes * kQ + 2 * kStages * kTile + 1024;  // aligned by the kernel
+    static constexpr int kChunks = kTok * D / 16 / (32 * kConvert);  // of 16 codes a converter
+    static constexpr int kOut = kPipes * kTok;                  // tensor-memory column of O
+};
+
+enum Bar : int {
+    kQFull = 0,                  // [pipe]
+    kSFull = 2, kPFull = 4, kOFull = 6,
+    kKFull = 8, kKEmpty = 10, kVFull = 12, kVEmpty = 14,  // [stage]
+    kScFull = 16, kScEmpty = 20,  // [scale stage]
+    kDone = 24, kBars = 25
+};
+
+template <int CODE, int D>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefix_kernel(const PrefixArgs a) {
+    using X = Shape<D>;
+    constexpr int NP = X::kPipes, TOK = X::kTok;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Plan plan;
+    __shared__ __align__(16) float s_k[X::kScales][TOK], s_v[X::kScales][TOK];
+    __shared__ __align__(16) float s_log[X::kScales][TOK];  // log2 of the V scale
+    __shared__ __align__(16) int s_small[X::kScales][X::kConvert];  // a V scale below 2^-60
+    __shared__ __align__(8) unsigned long long s_bar[kBars];
+    __shared__ float2 s_sum[kPrefixRows];  // of the second pipeline
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_gave_up;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t* const smem = smem_raw + (-(int)shared_address(smem_raw) & 1023);
+    const uint32_t q_at = shared_address(smem), k_at = q_at + NP * X::kQ;
+    const uint32_t v_at = k_at + X::kStages * X::kTile;
+    const uint32_t bars = shared_address(s_bar);
+    auto bar = [&](int i) { return (uint32_t)(bars + 8 * i); };
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(bar(kQFull + i), kPrefixRows);
+            barrier_init(bar(kSFull + i), 1);
+            barrier_init(bar(kPFull + i), kPrefixRows);
+            barrier_init(bar(kOFull + i), 1);
+            barrier_init(bar(kKFull + i), 32 * X::kConvert);
+            barrier_init(bar(kKEmpty + i), 1);
+            barrier_init(bar(kVFull + i), 32 * X::kConvert);
+            barrier_init(bar(kVEmpty + i), 1);
+        }
+        for (int i = 0; i < X::kScales; ++i) {
+            barrier_init(bar(kScFull + i), 32 * X::kConvert);
+            barrier_init(bar(kScEmpty + i), X::kSoftmax);
+        }
+        barrier_init(bar(kDone), 1);
+        s_gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == X::kSoftmax + X::kConvert) {
+        // One CTA an SM; waits for what else holds tensor memory, never the other way round.
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         shared_address(&s_tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        fence_before();
+    }
+    wait_for_previous();
+    if (warp == 0) fill_plan(plan, a, X::kRows, TOK);
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    const long long units = plan.unit[a.P];
+    const int ctas = working(units, a.ctas);
+    const bool works = (int)blockIdx.x < ctas;
+    const long long u0 = works ? first_unit(units, blockIdx.x, ctas) : 0;
+    const long long u1 = works ? first_unit(units, blockIdx.x + 1, ctas) : 0;
+    volatile int* const gave_up = &s_gave_up;
+
+    if (warp >= X::kSoftmax && warp < X::kSoftmax + X::kConvert) {
+        // ---- converters ----------------------------------------------------------
+        const int t = tid - 32 * X::kSoftmax;
+        constexpr int kRowChunks = D / 16;  // 16-byte pieces of a token
+        uint4 k_next[X::kChunks], v_next[X::kChunks];
+        float ks_next = 0.f, vs_next = 0.f;
+        // The unit to be loaded next.
+        long long from = u0;
+        int tile = 0, end = 0, len = 0;
+        const uint8_t* rows = nullptr;    // of the prefix, at the K head
+        const float* scales = nullptr;    // likewise
+        auto move_on = [&]() {
+            if (tile < end || from >= u1) return;
+            const Segment g(plan, a, from, u1, X::kRows, TOK);
+            from += g.n;
+            tile = g.tile0;
+            end = g.tile0 + g.n;
+            len = plan.len[g.p];
+            const int r = ld(a.prefix + g.p);
+            rows = a.rows + (long long)r * a.L * a.W + g.h * D;
+            scales = a.scales + (long long)r * a.NB * 2 * a.Hkv + g.h;
+        };
+        auto load = [&](uint4 (&x)[X::kChunks], const uint8_t* base) {
+#pragma unroll
+            for (int c = 0; c < X::kChunks; ++c) {
+                const int i = c * 32 * X::kConvert + t;
+                const int token = tile * TOK + i / kRowChunks;
+                x[c] = make_uint4(0, 0, 0, 0);
+                if (tile < end && token < len)
+                    x[c] = ld_once_v4(base + (long long)token * a.W + i % kRowChunks * 16);
+            }
+        };
+        auto load_scales = [&]() {
+            const int token = tile * TOK + t;
+            ks_next = vs_next = 0.f;
+            if (tile < end && t < TOK && token < len) {
+                const float* p = scales + (long long)a.block.of(token) * 2 * a.Hkv;
+                ks_next = ld(p) * a.k_sign;
+                vs_next = ld(p + a.Hkv);
+            }
+        };
+        auto put = [&](const uint4 (&x)[X::kChunks], uint32_t at) {
+#pragma unroll
+            for (int c = 0; c < X::kChunks; ++c) {
+                const int i = c * 32 * X::kConvert + t;
+                const int row = i / kRowChunks, d = i % kRowChunks * 16;
+                uint32_t y[8];
+                halves<CODE>(x[c].x, y[0], y[1]);
+                halves<CODE>(x[c].y, y[2], y[3]);
+                halves<CODE>(x[c].z, y[4], y[5]);
+                halves<CODE>(x[c].w, y[6], y[7]);
+                // Lanes of the second panel begin with their second half: the 8 lanes that store
+                // together then use different banks.
+                const bool swap = d / 64 & 1;
+                const uint32_t lo = at + place(row, d, TOK * 128), hi = at + place(row, d + 8, TOK * 128);
+                const uint32_t p0 = swap ? hi : lo, p1 = swap ? lo : hi;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p0),
+                             "r"(swap ? y[4] : y[0]), "r"(swap ? y[5] : y[1]),
+                             "r"(swap ? y[6] : y[2]), "r"(swap ? y[7] : y[3])
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p1),
+                             "r"(swap ? y[0] : y[4]), "r"(swap ? y[1] : y[5]),
+                             "r"(swap ? y[2] : y[6]), "r"(swap ? y[3] : y[7])
+                             : "memory");
+            }
+        };
+        move_on();
+        load(k_next, rows);
+        load(v_next, rows + a.Hkv * D);
+        load_scales();
+        const long long n = u1 - u0;
+        for (long long i = 0; i < n; ++i) {
+            const int stage = (int)(i & 1), sc = (int)(i & 3);
+            const uint32_t phase = (uint32_t)(i >> 1) & 1, sc_phase = (uint32_t)(i >> 2) & 1;
+            wait(bar(kScEmpty + sc), sc_phase ^ 1, gave_up);
+            if (t < TOK) {
+                s_k[sc][t] = ks_next;
+                s_v[sc][t] = vs_next;
+                s_log[sc][t] = log2f(vs_next);
+            }
+            const bool small = __any_sync(0xffffffffu, t < TOK && vs_next < 0x1p-60f);
+            if (lane == 0) s_small[sc][warp - X::kSoftmax] = small;
+            arrive(bar(kScFull + sc));
+            wait(bar(kKEmpty + stage), phase ^ 1, gave_up);
+            put(k_next, k_at + stage * X::kTile);
+            fence_shared();
+            arrive(bar(kKFull + stage));
+            // the next tile's keys are under way while the values are converted
+            ++tile;
+            move_on();
+            load(k_next, rows);
+            load_scales();
+            wait(bar(kVEmpty + stage), phase ^ 1, gave_up);
+            put(v_next, v_at + stage * X::kTile);
+            fence_shared();
+            arrive(bar(kVFull + stage));
+            load(v_next, rows + a.Hkv * D);
+        }
+    }
+    if (warp == X::kSoftmax + X::kConvert && lane == 0) {
+        // ---- matrix instructions ---------------------------------------------------
+        constexpr uint32_t kScores = instruction(TOK, false), kValues = instruction(D, true);
+        uint32_t p_done = 0, q_done = 0;  // phases, a bit a pipeline
+        long long tiles = 0;  // of the segments before
+        for (long long from = u0; from < u1;) {
+            const Segment g(plan, a, from, u1, X::kRows, TOK);
+            const bool both = NP == 2 && g.rows - g.row0 > kPrefixRows;
+            const int items = both ? 2 * g.n : g.n;
+            for (int w = 0; w < items + NP; ++w) {
+                if (w >= NP) {
+                    const int v = w - NP, p = v % NP, i = both ? v / 2 : v;
+                    const long long at = tiles + i;
+                    const int stage = (int)(at & 1);
+                    wait(bar(kVFull + stage), (uint32_t)(at >> 1) & 1, gave_up);
+                    wait(bar(kPFull + p), p_done >> p & 1, gave_up);
+                    p_done ^= 1u << p;
+                    fence_after();
+                    const uint32_t o = tmem + X::kOut + p * D, s = tmem + p * TOK;
+                    const bool first = both ? i == 0 : i < NP;
+                    const uint64_t b = matrix(v_at + stage * X::kTile, TOK * 128);
+#pragma unroll
+                    for (int k = 0; k < TOK / 16; ++k)  // 16 tokens are 16 rows of 128 bytes
+                        multiply_tensor(o, s + 8 * k, b + k * (2048 >> 4), kValues,
+                                        !(first && k == 0));
+                    if (!both || p == 1) commit(bar(kVEmpty + stage));
+                    if (both ? i == g.n - 1 : i + NP >= g.n) commit(bar(kOFull + p));
+                }
+                if (w < items) {
+                    const int p = w % NP, i = both ? w / 2 : w;
+                    const long long at = tiles + i;
+                    const int stage = (int)(at & 1);
+                    if (both ? i == 0 : i < NP) {
+                        wait(bar(kQFull + p), q_done >> p & 1, gave_up);
+                        q_done ^= 1u << p;
+                    }
+                    wait(bar(kKFull + stage), (uint32_t)(at >> 1) & 1, gave_up);
+                    fence_after();
+                    const uint32_t q = q_at + p * X::kQ, key = k_at + stage * X::kTile;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int panel = k / 4, in = k % 4 * 32;
+                        multiply(tmem + p * TOK, matrix(q + panel * kPrefixRows * 128 + in, 16),
+                                 matrix(key + panel * TOK * 128 + in, 16), kScores, k > 0);
+                    }
+                    commit(bar(kSFull + p));
+                    if (!both || p == 1) commit(bar(kKEmpty + stage));
+                }
+            }
+            tiles += g.n;
+            from += g.n;
+        }
+        commit(bar(kDone));
+        wait(bar(kDone), 0, gave_up);
+    }
+    if (warp < X::kSoftmax) {
+        // ---- softmax ---------------------------------------------------------------
+        const int p = warp / 4, row = tid - p * kPrefixRows;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t s_col = lanes + p * TOK, o_col = lanes + X::kOut + p * D;
+        uint32_t s_done = 0, o_done = 0;
+        long long tiles = 0;  // of the segments before
+        for (long long from = u0; from < u1;) {
+            const Segment g(plan, a, from, u1, X::kRows, TOK);
+            const bool both = NP == 2 && g.rows - g.row0 > kPrefixRows;
+            const int mine = NP == 1 || both ? g.n : (g.n + 1 - p) / 2;
+            const int r = g.row0 + (both ? p * kPrefixRows : 0) + row;
+            const bool on = r < g.rows;
+            const Row at(a, plan.lo[g.p], g.h, on ? r : g.row0);
+            const int len = plan.len[g.p];
+            float f = 0.f;  // of the products
+            if (mine > 0) {
+                // The row's largest element goes to [2^14, 2^15), f16's top.
+                const uint16_t* q = a.q + at.at(a.q_stride);
+                float peak = 0.f;
+                if (on) {
+#pragma unroll 4
+                    for (int d = 0; d < D; d += 8) {
+                        const uint4 x = load8(q + d, a.vec_q);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 y = pair(w[i], a.fp16);
+                            peak = fmaxf(peak, fmaxf(fabsf(y.x), fabsf(y.y)));
+                        }
+                    }
+                }
+                int e = (int)(__float_as_uint(peak) >> 23) - 127;
+                e = e < -100 ? -100 : e;
+                const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+                f = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
+                const uint32_t to = q_at + p * X::kQ;
+#pragma unroll 4
+                for (int d = 0; d < D; d += 8) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (on) x = load8(q + d, a.vec_q);
+                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 y = pair(w[i], a.fp16);
+                        w[i] = pack_half2(y.x * up, y.y * up);
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     to + place(row, d, kPrefixRows * 128)),
+                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                }
+                fence_shared();
+                arrive(bar(kQFull + p));
+            }
+            float ref = 0.f, l = 0.f;
+            for (int j = 0; j < mine; ++j) {
+                const int i = NP == 1 || both ? j : 2 * j + p;
+                const long long t = tiles + i;
+                const int sc = (int)(t & 3);
+                const int live = len - (g.tile0 + i) * TOK;  // tokens of the tile, or more
+                wait(bar(kScFull + sc), (uint32_t)(t >> 2) & 1, gave_up);
+                const int4 small = *reinterpret_cast<const int4*>(s_small[sc]);
+                const bool special = live < TOK || (small.x | small.y | small.z | small.w);
+                wait(bar(kSFull + p), s_done++ & 1, gave_up);
+                fence_after();
+                // The largest score, and the largest of score + log2(V scale).
+                float top = -INFINITY, most = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < TOK; c += 32) {
+                    uint32_t x[32];
+                    load_columns(x, s_col + c);
+                    loaded(x);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 ks = *reinterpret_cast<const float4*>(&s_k[sc][c + k]);
+                        const float4 lg = *reinterpret_cast<const float4*>(&s_log[sc][c + k]);
+                        const float kk[4] = {ks.x, ks.y, ks.z, ks.w};
+                        const float ll[4] = {lg.x, lg.y, lg.z, lg.w};
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const float z = __uint_as_float(x[k + m]) * kk[m] * f;
+                            if (!special || c + k + m < live) {
+                                most = fmaxf(most, z + ll[m]);
+                                if (special) top = fmaxf(top, z);
+                            }
+                        }
+                    }
+                }
+                float want = most - 11.5f;
+                if (special) want = fmaxf(want, top - 100.f);
+                if (j == 0) {
+                    ref = want;
+                } else {
+                    const bool grow = want > ref + 4.f;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float by = grow ? exp2_fast(ref - want) : 1.f;
+                        l *= by;
+                        if (grow) ref = want;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t x[32];
+                            load_columns(x, o_col + c);
+                            loaded(x);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                x[k] = __float_as_uint(__uint_as_float(x[k]) * by);
+                            store_columns(o_col + c, x);
+                        }
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; c < TOK; c += 32) {
+                    uint32_t x[32], y[16];
+                    load_columns(x, s_col + c);
+                    loaded(x);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 ks = *reinterpret_cast<const float4*>(&s_k[sc][c + k]);
+                        const float4 vs = *reinterpret_cast<const float4*>(&s_v[sc][c + k]);
+                        const float kk[4] = {ks.x, ks.y, ks.z, ks.w};
+                        const float vv[4] = {vs.x, vs.y, vs.z, vs.w};
+                        float e[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const float z = __uint_as_float(x[k + m]) * kk[m] * f;
+                            e[m] = exp2_fast(z - ref);
+                            if (special && c + k + m >= live) e[m] = 0.f;
+                            l += e[m];
+                            e[m] *= vv[m];
+                        }
+                        y[k / 2] = pack_half2(e[0], e[1]);
+                        y[k / 2 + 1] = pack_half2(e[2], e[3]);
+                    }
+                    store_columns(s_col + c / 2, y);
+                }
+                stored();
+                fence_before();
+                arrive(bar(kPFull + p));
+                __syncwarp();
+                if (lane == 0) arrive_n(bar(kScEmpty + sc), NP == 1 || both ? 1 : 2);
+            }
+
+            // ---- the segment's outputs ---------------------------------------------------
+            if (mine > 0) {
+                wait(bar(kOFull + p), o_done++ & 1, gave_up);
+                fence_after();
+            }
+            if (*gave_up) l = NAN;
+            // Two halves of the tokens: the second pipeline's go through the queries' memory.
+            constexpr int kQuads = D / 4;
+            float4* const second = reinterpret_cast<float4*>(smem) + row * kQuads;
+            float mine_by = 1.f, second_by = 0.f;
+            if (NP == 2 && !both) {
+                asm volatile("bar.sync 1, 256;" ::: "memory");  // both are done with the queries
+                if (p == 1) {
+                    s_sum[row] = make_float2(ref, l);
+                    if (mine > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t x[32];
+                            load_columns(x, o_col + c);
+                            loaded(x);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)  // rotated by the row: different banks
+                                second[(c / 4 + k + row) % kQuads] = make_float4(
+                                    __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]),
+                                    __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+                        }
+                    }
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (p == 0 && g.n > 1) {
+                    const float2 o = s_sum[row];
+                    const float top = fmaxf(ref + log2f(l), o.x + log2f(o.y));
+                    mine_by = exp2_fast(ref - top);
+                    second_by = exp2_fast(o.x - top);
+                    l = l * mine_by + o.y * second_by;
+                    ref = top;
+                }
+            }
+            if (NP == 1 || both || p == 0) {
+                const bool whole = g.n == g.tiles;
+                const long long out_row = ((long long)at.b * a.S + at.s) * a.Hq + at.head;
+                float other = 0.f;
+                if (whole) {
+                    const Joined j(ref + log2f(l), a.join ? ld(a.join_lse + out_row) : -INFINITY);
+                    const float by = j.mine / l;
+                    mine_by *= by;
+                    second_by *= by;
+                    other = j.other;
+                    if (on && a.lse) a.lse[out_row] = j.lse;
+                }
+                const int tile_row = (both ? p * kPrefixRows : 0) + row;
+                const long long slot = 2 * (long long)blockIdx.x + (from == u0 ? 0 : 1);
+                float4* part = reinterpret_cast<float4*>(a.part) + slot * kQuads * X::kRows + tile_row;
+                if (!whole && on)
+                    a.part_sum[slot * X::kRows + tile_row] = make_float2(ref, l);
+                uint16_t* out = a.out + at.at(a.out_stride);
+                const uint16_t* join = a.join + at.at(a.join_stride);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t x[32];
+                    load_columns(x, o_col + c);
+                    loaded(x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float y[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) y[m] = __uint_as_float(x[4 * k + m]) * mine_by;
+                        if (NP == 2 && !both && g.n > 1) {
+                            const float4 z = second[(c / 4 + k + row) % kQuads];
+                            y[0] += z.x * second_by, y[1] += z.y * second_by;
+                            y[2] += z.z * second_by, y[3] += z.w * second_by;
+                        }
+                        if (!on) continue;
+                        const int d = c + 4 * k;
+                        if (!whole) {
+                            part[(long long)(d / 4) * X::kRows] = make_float4(y[0], y[1], y[2], y[3]);
+                            continue;
+                        }
+                        if (other > 0.f) {
+                            const uint2 z = load4(join + d, a.vec_join);
+                            const float2 z0 = pair(z.x, a.fp16), z1 = pair(z.y, a.fp16);
+                            y[0] += z0.x * other, y[1] += z0.y * other;
+                            y[2] += z1.x * other, y[3] += z1.y * other;
+                        }
+                        store4(out + d, unpair(y[0], y[1], a.fp16), unpair(y[2], y[3], a.fp16),
+                               a.vec_out);
+                    }
+                }
+            }
+            if (NP == 2 && !both) asm volatile("bar.sync 1, 256;" ::: "memory");
+            tiles += g.n;
+            from += g.n;
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (warp == X::kSoftmax + X::kConvert) {
+        __syncwarp();
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+template <int CODE, int D>
+cudaError_t run_one(const PrefixArgs& a, cudaStream_t s) {
+    static SmemOptIn opt;
+    const cudaError_t e = ensure_smem(prefix_kernel<CODE, D>, Shape<D>::kSmem, &opt);
+    if (e != cudaSuccess) return e;
+    return launch_chained(prefix_kernel<CODE, D>, a.ctas, Shape<D>::kThreads, Shape<D>::kSmem, 0, s,
+                          a);
+}
+
+template <int CODE>
+cudaError_t run(const PrefixArgs& a, int D, cudaStream_t s) {
+    switch (D) {
+        case 32: return run_one<CODE, 32>(a, s);
+        case 64: return run_one<CODE, 64>(a, s);
+        case 96: return run_one<CODE, 96>(a, s);
+        case 128: return run_one<CODE, 128>(a, s);
+        case 192: return run_one<CODE, 192>(a, s);
+        case 256: return run_one<CODE, 256>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace prefix
+
+#endif  // __CUDACC__
+
+}  // namespace hs

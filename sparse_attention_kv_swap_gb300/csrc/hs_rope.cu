@@ -1,0 +1,297 @@
+// RMS norm of every query and key head and the position rotation, in one pass
+// (sm_103a).
+//
+// D / 16 lanes hold a head, 16 elements each: two pieces of 8 that lie rot / 2
+// apart, so that a lane holds both elements of its pairs whichever way they are
+// paired.  The sum of squares goes over the lanes by shuffles; nothing is read twice.
+//
+// Angles: position * frequency would lose what matters in 32 bits (at position 131072 an angle
+// is off by 2^-8) and take sines of large numbers.  The frequency comes as a part of a turn in
+// 64-bit fixed point, the product is taken modulo 2^64, that is modulo whole turns, and
+// is off by |position| * 2^-65 turns.  What is left of an eighth of a turn goes through sincospif, the
+// quadrant is put back by exchange and sign.  A CTA computes the cosines and sines of its tokens
+// once for all their heads.
+//
+// What bounds it: 2 * size bytes an element, for about 10 operations: memory.
+#include "hs_step.cuh"
+
+namespace hs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 16;  // of a CTA
+
+struct RopeArgs {
+    const void* in[2];  // queries, keys
+    void* out[2];
+    int64_t in_stride[2][3], out_stride[2][3];
+    const float* weight[2];
+    float eps;
+    int32_t rot, adjacent, axes, M, Hq, heads;  // heads: of queries and keys
+    long long tokens;  // batch * M
+    int32_t items, per_cta;  // (token, head) pairs in all, and of a CTA
+    Divisor by_heads, by_M;
+    const int32_t* pos;
+    const int64_t* turns;
+    const int32_t* axis;
+    const int32_t* count;
+    int32_t vec_in[2], vec_out[2], vec_weight[2];
+};
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x) {
+    return (float)x;
+}
+
+// Eight consecutive elements.
+template <typename T>
+__device__ __forceinline__ void load8(float (&x)[8], const T* p, bool vec) {
+    if (vec) {
+        if constexpr (sizeof(T) == 4) {
+            const uint4 a = ld_once_v4(p), b = ld_once_v4(p + 4);
+            x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y);
+            x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
+            x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y);
+            x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
+        } else {
+            const uint4 a = ld_once_v4(p);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 2 && __is_same(T, __half)) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+                } else {
+                    x[2 * i] = __uint_as_float(w[i] << 16);
+                    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_float(ld(p + i));
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8], bool vec) {
+    if (vec) {
+        alignas(16) T y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = from_float<T>(x[i]);
+        const uint4* v = reinterpret_cast<const uint4*>(y);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) st_v4(p + i * (16 / sizeof(T)), v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = from_float<T>(x[i]);
+    }
+}
+
+// (cos, sin) of the angle of a position, whose frequency is `turn` * 2^-64 turns.
+__device__ __forceinline__ float2 rotation(int32_t pos, int64_t turn) {
+    const uint64_t phase = (uint64_t)(int64_t)pos * (uint64_t)turn + 0x80000000ull;
+    const uint32_t t = (uint32_t)(phase >> 32);
+    const uint32_t quadrant = (t + 0x20000000u) >> 30;
+    const int32_t rest = (int32_t)(t - (quadrant << 30));  // within an eighth of a turn
+    float s, c;
+    sincospif((float)rest * 0x1p-31f, &s, &c);
+    if (quadrant & 1) {
+        const float x = c;
+        c = -s;
+        s = x;
+    }
+    return quadrant & 2 ? make_float2(-c, -s) : make_float2(c, s);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const RopeArgs a) {
+    constexpr int kUsed = D / 16;                                        // lanes of a head
+    constexpr int kLanes = kUsed <= 2 ? 2 : kUsed <= 4 ? 4 : kUsed <= 8 ? 8 : 16;  // padded
+    constexpr int kGroups = kThreads / kLanes;
+    constexpr int kAhead = 2;  // heads a lane has under way
+    extern __shared__ __align__(16) float2 s_turn[];  // [token][rot / 2]
+    const int tid = threadIdx.x, lane = tid % kLanes, group = tid / kLanes;
+    const int first = blockIdx.x * a.per_cta;
+    const int end = min(first + a.per_cta, a.items);
+    const int token0 = a.by_heads.of(first), tokens = a.by_heads.of(end - 1) - token0 + 1;
+    const int half = a.rot / 2;
+    wait_for_previous();
+    for (int i = tid; i < tokens * half; i += kThreads) {
+        const int t = i / half, j = i - t * half;
+        int x = a.axis ? ld(a.axis + j) : 0;
+        x = min(max(x, 0), a.axes - 1);
+        s_turn[i] = rotation(ld(a.pos + x * a.tokens + token0 + t), ld(a.turns + j));
+    }
+    // This lane's pieces of 8 elements: a pair of them that turns together, or two that do not turn.
+    const int pairs = a.rot / 16;
+    const bool turns = lane < pairs, used = lane < kUsed;
+    const int p0 = 8 * (turns ? lane : 2 * lane), p1 = turns ? p0 + half : p0 + 8;
+    __syncthreads();
+    release_next();
+    for (int i0 = first + group; i0 < end; i0 += kAhead * kGroups) {
+        float x[kAhead][2][8];
+        int token[kAhead], head[kAhead];
+        bool live[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kGroups;
+            token[u] = a.by_heads.of(i), head[u] = i - token[u] * a.heads;
+            const int b = a.by_M.of(token[u]), m = token[u] - b * a.M;
+            live[u] = used && i < end && (!a.count || m < ld(a.count + b));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[u][0][k] = x[u][1][k] = 0.f;
+            if (live[u]) {
+                const int w = head[u] >= a.Hq, h = head[u] - (w ? a.Hq : 0);
+                const T* p = static_cast<const T*>(a.in[w]) + b * a.in_stride[w][0] +
+                             m * a.in_stride[w][1] + h * a.in_stride[w][2];
+                load8(x[u][0], p + p0, a.vec_in[w]);
+                load8(x[u][1], p + p1, a.vec_in[w]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int w = head[u] >= a.Hq;
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += x[u][0][k] * x[u][0][k] + x[u][1][k] * x[u][1][k];
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (!live[u]) continue;
+            if (a.weight[w]) {
+                const float r = rsqrtf(sum * (1.f / D) + a.eps);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float* wt = a.weight[w] + (c == 0 ? p0 : p1);
+                    float g[8];
+                    if (a.vec_weight[w]) {
+                        const float4 v0 = ld(reinterpret_cast<const float4*>(wt));
+                        const float4 v1 = ld(reinterpret_cast<const float4*>(wt) + 1);
+                        g[0] = v0.x, g[1] = v0.y, g[2] = v0.z, g[3] = v0.w;
+                        g[4] = v1.x, g[5] = v1.y, g[6] = v1.z, g[7] = v1.w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) g[k] = ld(wt + k);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[u][c][k] *= r * g[k];
+                }
+            }
+            if (turns) {
+                const float2* cs = s_turn + (token[u] - token0) * half;
+                if (a.adjacent) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 t = cs[(c == 0 ? p0 : p1) / 2 + k];
+                            const float y0 = x[u][c][2 * k], y1 = x[u][c][2 * k + 1];
+                            x[u][c][2 * k] = y0 * t.x - y1 * t.y;
+                            x[u][c][2 * k + 1] = y0 * t.y + y1 * t.x;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float2 t = cs[p0 + k];
+                        const float y0 = x[u][0][k], y1 = x[u][1][k];
+                        x[u][0][k] = y0 * t.x - y1 * t.y;
+                        x[u][1][k] = y0 * t.y + y1 * t.x;
+                    }
+                }
+            }
+            const int b = a.by_M.of(token[u]), m = token[u] - b * a.M;
+            const int h = head[u] - (w ? a.Hq : 0);
+            T* p = static_cast<T*>(a.out[w]) + b * a.out_stride[w][0] + m * a.out_stride[w][1] +
+                   h * a.out_stride[w][2];
+            store8(p + p0, x[u][0], a.vec_out[w]);
+            store8(p + p1, x[u][1], a.vec_out[w]);
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t run(RopeArgs a, cudaStream_t s) {
+    constexpr int kUsed = D / 16;
+    constexpr int kLanes = kUsed <= 2 ? 2 : kUsed <= 4 ? 4 : kUsed <= 8 ? 8 : 16;
+    constexpr int kGroups = kThreads / kLanes;
+    // Heads of a lane group: one while that fills the SMs, more where the angles of a token serve many
+    // heads.
+    long long each = a.items / ((long long)kGroups * 152 * 4);
+    each = each < 1 ? 1 : each > 8 ? 8 : each;
+    while (each > 1 && each * kGroups / a.heads + 2 > kMaxTokens) --each;
+    a.per_cta = (int)each * kGroups;
+    if (a.per_cta / a.heads + 2 > kMaxTokens) a.per_cta = (kMaxTokens - 2) * a.heads;
+    const size_t smem = (size_t)(a.per_cta / a.heads + 2) * (a.rot / 2) * sizeof(float2);
+    const int grid = (a.items - 1) / a.per_cta + 1;
+    return launch_chained(norm_rope_kernel<T, D>, grid, kThreads, smem, 0, s, a);
+}
+
+template <typename T>
+cudaError_t run_dim(const RopeArgs& a, int D, cudaStream_t s) {
+    switch (D) {
+        case 32: return run<T, 32>(a, s);
+        case 64: return run<T, 64>(a, s);
+        case 96: return run<T, 96>(a, s);
+        case 128: return run<T, 128>(a, s);
+        case 192: return run<T, 192>(a, s);
+        case 256: return run<T, 256>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const hs_norm_rope_args& x, cudaStream_t s) {
+    RopeArgs a = {};
+    const int esz = x.dtype == HS_DTYPE_FP32 ? 4 : 2;
+    const void* in[2] = {x.q_dev, x.k_dev};
+    void* out[2] = {x.q_out_dev, x.k_out_dev};
+    const float* weight[2] = {x.q_weight_dev, x.k_weight_dev};
+    const int64_t* strides[4] = {x.q_stride, x.k_stride, x.q_out_stride, x.k_out_stride};
+    for (int w = 0; w < 2; ++w) {
+        a.in[w] = in[w];
+        a.out[w] = out[w];
+        a.weight[w] = weight[w];
+        a.vec_in[w] = (uintptr_t)in[w] % 16 == 0;
+        a.vec_out[w] = (uintptr_t)out[w] % 16 == 0;
+        a.vec_weight[w] = (uintptr_t)weight[w] % 16 == 0;
+        for (int i = 0; i < 3; ++i) {
+            a.in_stride[w][i] = strides[w][i];
+            a.out_stride[w][i] = strides[2 + w][i];
+            a.vec_in[w] = a.vec_in[w] && strides[w][i] * esz % 16 == 0;
+            a.vec_out[w] = a.vec_out[w] && strides[2 + w][i] * esz % 16 == 0;
+        }
+    }
+    a.eps = x.eps;
+    a.rot = x.rot_dim;
+    a.adjacent = x.adjacent;
+    a.axes = x.num_axes;
+    a.M = x.tokens;
+    a.Hq = x.num_heads;
+    a.heads = x.num_heads + x.num_kv_heads;
+    a.tokens = (long long)x.batch * x.tokens;
+    a.items = (int32_t)(a.tokens * a.heads);
+    a.by_heads = Divisor::by(a.heads);
+    a.by_M = Divisor::by(a.M);
+    a.pos = x.pos_dev;
+    a.turns = x.turns_dev;
+    a.axis = x.axis_dev;
+    a.count = x.count_dev;
+    if (x.dtype == HS_DTYPE_BF16) return run_dim<__nv_bfloat16>(a, x.head_dim, s);
+    if (x.dtype == HS_DTYPE_FP16) return run_dim<__half>(a, x.head_dim, s);
+    return run_dim<float>(a, x.head_dim, s);
+}
+
+}  // namespace hs
