@@ -16,7 +16,7 @@ constexpr int kWarps = 16;
 __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a, int D,
                                                               int groups) {
     __shared__ Plan plan;
-    __shared__ long long s_first[kPrefixCtas + 1];  // first unit of every CTA
+    __shared__ int s_first[kPrefixCtas + 1];  // first unit of every CTA
     __shared__ float s_factor[kPrefixCtas][32];     // of a CTA's part of a row
     __shared__ float s_tmp[kWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a
     if (warp == 0) prefix::fill_plan(plan, a, tile_rows, tile_tokens);
     __syncthreads();
     release_next();
-    const long long units = plan.unit[a.P];
+    const int units = plan.unit[a.P];
     const int ctas = prefix::working(units, a.ctas);
     for (int c = threadIdx.x; c <= ctas; c += 32 * kWarps)
         s_first[c] = ctas > 0 ? prefix::first_unit(units, c, ctas) : 0;
@@ -39,16 +39,16 @@ __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a
     while (p >= 0 && (plan.lo[p] > at.b || plan.hi[p] <= plan.lo[p])) --p;
     const bool some = on && p >= 0 && at.b < plan.hi[p] && plan.len[p] > 0;
     int first = 0, last = -1;  // CTAs with units of the row's tile
-    long long unit0 = 0;
+    int unit0 = 0;
     int tile_row = 0;
     if (some) {
         const int rows = (plan.hi[p] - plan.lo[p]) * a.S * a.G;
         const int tiles = (plan.len[p] + tile_tokens - 1) / tile_tokens;
         const int r = i - plan.lo[p] * a.S * a.G, row_tiles = (rows + tile_rows - 1) / tile_rows;
         tile_row = r % tile_rows;
-        unit0 = plan.unit[p] + (long long)(h * row_tiles + r / tile_rows) * tiles;
+        unit0 = plan.unit[p] + (h * row_tiles + r / tile_rows) * tiles;
         // The last CTA that begins at unit0 or before, and at the tile's last unit or before.
-        auto owner = [&](long long unit) {
+        auto owner = [&](int unit) {
             int lo = 0, hi = ctas;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
@@ -140,6 +140,36 @@ int prefix_ctas() {
     return sms < kPrefixCtas ? sms : kPrefixCtas;
 }
 
+// The tensor map of the store.  The encoder is the driver's; its entry point is looked up once.
+cudaError_t make_map(const hs_kv_format& f, const hs_prefix_args& x, CUtensorMap* map) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<void*> known{nullptr};
+    void* fn = known.load(std::memory_order_acquire);
+    if (!fn) {
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion(
+            "cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (!fn || found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+        known.store(fn, std::memory_order_release);
+    }
+    const int D = f.head_dim, box_bytes = prefix_box(D);
+    const cuuint64_t W = (cuuint64_t)f.item_size_bytes;
+    const cuuint64_t dims[3] = {W, (cuuint64_t)x.max_seq_len, (cuuint64_t)x.num_requests};
+    const cuuint64_t strides[2] = {W, W * (cuuint64_t)x.max_seq_len};
+    const cuuint32_t box[3] = {(cuuint32_t)box_bytes, (cuuint32_t)prefix_tokens(D), 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = reinterpret_cast<Encode>(fn)(
+        map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(x.rows_dev), dims, strides, box,
+        step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 size_t part_bytes(const hs_kv_format& f, int ctas) {
     return (size_t)ctas * 2 * kPrefixRows * prefix_pipes(f.head_dim) * f.head_dim * sizeof(float);
 }
@@ -168,6 +198,7 @@ cudaError_t launch_prefix(const hs_kv_format& f, const hs_prefix_args& x, cudaSt
     a.W = f.item_size_bytes;
     a.P = x.num_prefixes;
     a.block = Divisor::by(f.block_tokens);
+    a.even = f.block_tokens % 16 == 0 && x.sm_scale >= 0.f;
     a.scale_log2 = fabsf(x.sm_scale) * 1.4426950408889634f;
     a.k_sign = x.sm_scale < 0.f ? -1.f : 1.f;
     a.vec_q = (uintptr_t)x.q_dev % 16 == 0;
@@ -194,8 +225,11 @@ cudaError_t launch_prefix(const hs_kv_format& f, const hs_prefix_args& x, cudaSt
     a.part = reinterpret_cast<float*>(ws);
     a.part_sum = reinterpret_cast<float2*>(ws + part_bytes(f, a.ctas));
     if (a.P > 0) {
-        const cudaError_t e = f.code == HS_KV_E4M3 ? prefix_run_e4m3(a, f.head_dim, s)
-                                                   : prefix_run_int8(a, f.head_dim, s);
+        CUtensorMap map;
+        cudaError_t e = make_map(f, x, &map);
+        if (e != cudaSuccess) return e;
+        e = f.code == HS_KV_E4M3 ? prefix_run_e4m3(a, map, f.head_dim, s)
+                                 : prefix_run_int8(a, map, f.head_dim, s);
         if (e != cudaSuccess) return e;
     }
     const int groups = (int)(((long long)a.B * a.S * a.G + 31) / 32);

@@ -9,12 +9,13 @@
 // CTAs are put together by a second kernel (combine_kernel, hs_prefix.cu).
 //
 // Warps of a CTA:
-//   converters (4)  read codes, write them as f16 to shared memory in the layout of the matrix
-//                   instructions (128-byte swizzle), one tile ahead in registers, two in shared
-//                   memory; and the tokens' scales.  Codes are exact in f16.
-//   matrix (1)      S = Q K^T (128 rows x TOK tokens) and O += P V by tcgen05.mma, accumulators and P
-//                   in tensor memory
-//   softmax (4 for each of the NPIPE pipelines)   a thread has a row: it reads S, writes P over it
+//   converters (4)  have tiles of codes copied to a ring in shared memory (TMA), and write them
+//                   as f16 in the layout of the matrix instructions (128-byte swizzle), with
+//                   the tokens' scales.  Codes are exact in f16.
+//   softmax (4 for each of the NPIPE pipelines)   a thread has a row: it reads S, writes P over it.
+//                   The first of the four issues the pipeline's matrix instructions (tcgen05.mma: S = Q K^T,
+//                   128 rows x TOK tokens, and O += P V; accumulators and P in tensor memory): it
+//                   has nothing else to do until they are done.
 // Two pipelines (D <= 128) keep the matrix instructions busy while one of them is in its
 // softmax: they hold rows 0-127 and 128-255 of a row tile, or, where it has 128 rows or fewer, the even
 // and the odd tiles of tokens of the same rows.
@@ -22,11 +23,13 @@
 // Numbers: a query is scaled by a power of two into f16's range, as in hs_attend.  With z = s log2(e)
 // and v_t the V scale, the row keeps one reference r:
 //   p_t = 2^(z_t - r),  l = sum p_t,  P_t = f16(p_t v_t),  O = sum P_t code_t,  out = O / l
-// r is chosen so that the largest p_t v_t so far lies between 2^11 and 2^16 (r grows only when that
-// is passed, and O and l are scaled then): f16 keeps its 11 bits down to 2^-26 of the largest term and
-// is off by 2^-36 of it below.  Where V scales differ by 2^88 and more, r stays within 100
+// r is chosen so that the largest p_t v_t so far lies between 2^9 and 2^16 (r grows only when that
+// is passed, and O and l are scaled then): f16 keeps its 11 bits down to 2^-23 of the largest term and
+// is off by 2^-34 of it below.  Where V scales differ by 2^88 and more, r stays within 100
 // of the largest z, so that l stays in range.
 #pragma once
+
+#include <cuda.h>
 
 #include "hs_step.cuh"
 
@@ -40,6 +43,7 @@ struct PrefixArgs {
     uint16_t* out;
     int32_t fp16, B, S, G, Hq, Hkv, R, L, NB, W, P;
     Divisor block;     // by block_tokens
+    int32_t even;      // block_tokens is a multiple of 16 and sm_scale >= 0
     float scale_log2;  // |sm_scale| * log2(e)
     float k_sign;      // its sign
     int64_t q_stride[3], out_stride[3], join_stride[3];
@@ -61,8 +65,11 @@ constexpr int prefix_pipes(int D) { return D <= 128 ? 2 : 1; }
 constexpr int prefix_tokens(int D) { return D <= 128 ? 128 : 64; }
 constexpr int prefix_panels(int D) { return (D + 63) / 64; }
 
-cudaError_t prefix_run_e4m3(const PrefixArgs& a, int D, cudaStream_t s);
-cudaError_t prefix_run_int8(const PrefixArgs& a, int D, cudaStream_t s);
+// The store as the copies see it: [R][L][W] bytes, in boxes of so many tokens and bytes of a head.
+constexpr int prefix_box(int D) { return D % 64 == 0 ? 64 : 32; }
+
+cudaError_t prefix_run_e4m3(const PrefixArgs& a, const CUtensorMap& map, int D, cudaStream_t s);
+cudaError_t prefix_run_int8(const PrefixArgs& a, const CUtensorMap& map, int D, cudaStream_t s);
 
 #ifdef __CUDACC__
 
@@ -72,14 +79,14 @@ namespace prefix {
 struct Plan {
     int32_t lo[HS_MAX_PREFIXES], hi[HS_MAX_PREFIXES];  // batch rows
     int32_t len[HS_MAX_PREFIXES];
-    long long unit[HS_MAX_PREFIXES + 1];  // first unit; units of a prefix: [K/V head][row tile][tile]
+    int32_t unit[HS_MAX_PREFIXES + 1];  // first unit; units of a prefix: [K/V head][row tile][tile]
 };
 
 // Filled by one warp; everyone else waits at the caller's barrier.
 __device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int rows, int tokens) {
     const int lane = threadIdx.x & 31;
     int taken = 0;          // batch rows of the prefixes before
-    long long units = 0;
+    int units = 0;
     for (int p0 = 0; p0 < a.P; p0 += 32) {
         const int p = p0 + lane;
         int first = 0, end = 0, len = 0;
@@ -98,14 +105,14 @@ __device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int r
         int before = __shfl_up_sync(0xffffffffu, most, 1);
         if (lane == 0) before = taken;
         const int lo = max(first, before), hi = max(end, lo);
-        const long long n = (long long)(hi - lo) * a.S * a.G;
-        long long mine = 0;
+        int mine = 0;  // the launcher has made sure that all fit 31 bits
         if (p < a.P && len > 0)
-            mine = a.Hkv * ((n + rows - 1) / rows) * ((len + tokens - 1) / tokens);
-        long long sum = mine;
+            mine = a.Hkv * (((hi - lo) * a.S * a.G + rows - 1) / rows) *
+                   ((len + tokens - 1) / tokens);
+        int sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += x;
         }
         if (p < a.P) {
@@ -121,30 +128,28 @@ __device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int r
 }
 
 // CTAs with work: each has a unit or more.
-__device__ __forceinline__ int working(long long units, int ctas) {
-    return (int)min(units, (long long)ctas);
-}
+__device__ __forceinline__ int working(int units, int ctas) { return min(units, ctas); }
 // First unit of CTA `cta` of `n` that work.
-__device__ __forceinline__ long long first_unit(long long units, int cta, int n) {
-    return units * cta / n;
+__device__ __forceinline__ int first_unit(int units, int cta, int n) {
+    return units / n * cta + min(cta, units % n);
 }
 
 // Consecutive units of one tile of rows.
 struct Segment {
     int p, h, row0, rows;  // prefix, K/V head, first row of the tile, rows of the prefix
     int tile0, n, tiles;   // tiles of tokens: the first, how many, all of the prefix
-    __device__ __forceinline__ Segment(const Plan& plan, const PrefixArgs& a, long long from,
-                                       long long to, int tile_rows, int tile_tokens) {
+    __device__ __forceinline__ Segment(const Plan& plan, const PrefixArgs& a, int from, int to,
+                                       int tile_rows, int tile_tokens) {
         p = a.P - 1;
         while (plan.unit[p] > from) --p;  // the last one that begins here or before: not empty
         rows = (plan.hi[p] - plan.lo[p]) * a.S * a.G;
         tiles = (plan.len[p] + tile_tokens - 1) / tile_tokens;
-        const long long at = from - plan.unit[p];
-        const int turn = (int)(at / tiles), row_tiles = (rows + tile_rows - 1) / tile_rows;
-        tile0 = (int)(at - (long long)turn * tiles);
+        const int at = from - plan.unit[p];
+        const int turn = at / tiles, row_tiles = (rows + tile_rows - 1) / tile_rows;
+        tile0 = at - turn * tiles;
         h = turn / row_tiles;
         row0 = (turn - h * row_tiles) * tile_rows;
-        n = (int)min((long long)(tiles - tile0), to - from);
+        n = min(tiles - tile0, to - from);
     }
 };
 
@@ -157,12 +162,6 @@ __device__ __forceinline__ uint32_t shared_address(const void* p) {
 __device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void arrive_n(uint32_t bar, int n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
-}
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -174,17 +173,19 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-// Waits for the phase of this parity, for two seconds at most: then, or once another thread has
-// given up, the CTA goes on without waiting and its outputs become NaN.
+// Waits for the phase of this parity, with a limit that no wait comes near (a tenth of a second
+// at the least): then, or once another thread has given up, the CTA goes on without waiting and
+// its outputs become NaN.
 __device__ __forceinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-    unsigned long long begin = 0;
-    for (uint32_t i = 0;; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < 1 << 22; ++i)
         if (try_wait(bar, parity) || *gave_up) return;
-        if ((i & 255) == 255) {
-            const unsigned long long now = global_timer();
-            if (begin == 0) begin = now;
-            if (now - begin > 2000000000ull) *gave_up = 1;
-        }
+    *gave_up = 1;
+}
+// The same where a thread must not go on, whoever has given up.
+__device__ __forceinline__ void wait_still(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 1 << 22 && !try_wait(bar, parity); ++i) {
     }
 }
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
@@ -242,10 +243,20 @@ __device__ __forceinline__ void fence_before() {
 __device__ __forceinline__ void fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// What this thread has written to shared memory is seen by the matrix instructions issued after
-// a barrier that it arrives at next.
+// What this thread has written to shared memory, or seen written by others, is seen by the matrix
+// instructions that follow: this thread's, or those of threads that it lets go after.  It waits for
+// this thread's loads: the converters, which always have some under way, leave it to the warp
+// that issues (with theirs, a tile took 5000 cycles instead of XXXX).
 __device__ __forceinline__ void fence_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// One lane of a whole warp.
+__device__ __forceinline__ bool elected() {
+    uint32_t x;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(x));
+    return x != 0;
 }
 
 // Descriptor of a matrix in shared memory with the 128-byte swizzle: rows of 128 bytes, eight to a
@@ -386,6 +397,183 @@ struct Joined {
     }
 };
 
+// The largest p_t v_t gets 2^kTop when the reference is set, and may grow by 2^kRoom from there.
+constexpr float kTop = 9.5f, kRoom = 6.f;
+
+// The reference moves to `want`: O and l with it.  The whole warp calls it.
+template <int D>
+__device__ __forceinline__ void move_reference(uint32_t o_col, float want, bool first, float& ref,
+                                               float& l) {
+    if (first) {
+        ref = want;
+        return;
+    }
+    const bool grow = want > ref + kRoom;
+    if (!__any_sync(0xffffffffu, grow)) return;
+    const float by = grow ? exp2_fast(ref - want) : 1.f;
+    l *= by;
+    if (grow) ref = want;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t x[32];
+        load_columns(x, o_col + c);
+        loaded(x);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * by);
+        store_columns(o_col + c, x);
+    }
+}
+
+// One tile of a row: S is replaced by P.  Any scales and any number of live tokens.
+template <int TOK, int D>
+__device__ __forceinline__ void softmax_any(uint32_t s_col, uint32_t o_col, float f,
+                                            const float* s_k, const float* s_v, const float* s_log,
+                                            int live, bool first, float& ref, float& l) {
+    // The largest score, and the largest of score + log2(V scale).
+    float top = -INFINITY, most = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < TOK; c += 32) {
+        uint32_t x[32];
+        load_columns(x, s_col + c);
+        loaded(x);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            const float4 ks = *reinterpret_cast<const float4*>(s_k + c + k);
+            const float4 lg = *reinterpret_cast<const float4*>(s_log + c + k);
+            const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, ll[4] = {lg.x, lg.y, lg.z, lg.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float z = __uint_as_float(x[k + m]) * kk[m] * f;
+                if (c + k + m < live) {
+                    most = fmaxf(most, z + ll[m]);
+                    top = fmaxf(top, z);
+                }
+            }
+        }
+    }
+    move_reference<D>(o_col, fmaxf(most - kTop, top - 100.f), first, ref, l);
+#pragma unroll 1
+    for (int c = 0; c < TOK; c += 32) {
+        uint32_t x[32], y[16];
+        load_columns(x, s_col + c);
+        loaded(x);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            const float4 ks = *reinterpret_cast<const float4*>(s_k + c + k);
+            const float4 vs = *reinterpret_cast<const float4*>(s_v + c + k);
+            const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, vv[4] = {vs.x, vs.y, vs.z, vs.w};
+            float e[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                e[m] = exp2_fast(__uint_as_float(x[k + m]) * kk[m] * f - ref);
+                if (c + k + m >= live) e[m] = 0.f;
+                l += e[m];
+                e[m] *= vv[m];
+            }
+            y[k / 2] = pack_half2(e[0], e[1]);
+            y[k / 2 + 1] = pack_half2(e[2], e[3]);
+        }
+        store_columns(s_col + c / 2, y);
+    }
+}
+
+// a * b + c for two pairs at once.
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ void load_columns(uint32_t (&x)[16], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+          "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
+          "=r"(x[14]), "=r"(x[15])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void loaded(uint32_t (&x)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
+}
+__device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+        : "memory");
+}
+
+// The same for whole tiles whose scales are equal in each 16 tokens, V scales of 2^-60 or more
+// and K scales >= 0: the scales leave the loops.  p_t v_t comes out of the exponential at
+// once, 2^(z_t + log2 v - r), and l takes the sum of 16 by 1 / v.
+template <int TOK, int D>
+__device__ __forceinline__ void softmax_even(uint32_t s_col, uint32_t o_col, float f,
+                                             const float* s_k, const float2* s_even, bool first,
+                                             float& ref, float& l) {
+    // Tensor memory answers after some 250 cycles: all of S is asked for at once.
+    constexpr int kSteps = TOK / 32;
+    uint32_t x[kSteps][32];
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) load_columns(x[c], s_col + c * 32);
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) loaded(x[c]);
+    float most = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t* z = &x[c][16 * h];
+            float m[4];  // four chains
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                m[k] = fmaxf(fmaxf(__uint_as_float(z[k]), __uint_as_float(z[k + 4])),
+                             fmaxf(__uint_as_float(z[k + 8]), __uint_as_float(z[k + 12])));
+            m[0] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            most = fmaxf(most, fmaf(m[0], s_k[c * 32 + h * 16] * f, s_even[c * 2 + h].x));
+        }
+    }
+    move_reference<D>(o_col, most - kTop, first, ref, l);
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = c * 32 + 16 * h;
+            const float k0 = s_k[at] * f;
+            const float2 v = s_even[at / 16];
+            const float2 kk = make_float2(k0, k0), off = make_float2(v.x - ref, v.x - ref);
+            float2 sum[2] = {};
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                float2 e = make_float2(__uint_as_float(x[c][16 * h + k]),
+                                       __uint_as_float(x[c][16 * h + k + 1]));
+                e = fma_pair(e, kk, off);
+                e.x = exp2_fast(e.x);
+                e.y = exp2_fast(e.y);
+                sum[k / 2 & 1] = add_pair(sum[k / 2 & 1], e);
+                w[8 * h + k / 2] = pack_half2(e.x, e.y);
+            }
+            sum[0] = add_pair(sum[0], sum[1]);
+            l = fmaf(sum[0].x + sum[0].y, v.y, l);
+        }
+        store_columns(s_col + c * 16, w);
+    }
+}
+
 // ---- the kernel -------------------------------------------------------------------
 
 template <int D>
@@ -395,30 +583,157 @@ struct Shape {
     static constexpr int kRows = kPrefixRows * kPipes;          // of a tile
     static constexpr int kQ = kPanels * kPrefixRows * 128;      // bytes of a pipeline's queries
     static constexpr int kTile = kPanels * kTok * 128;          // of a tile's keys or values
-    static constexpr int kStages = 2, kScales = 4;              // tiles under way
+    static constexpr int kKeys = 1, kValues = 2;                // tiles of f16 in place
+    static constexpr int kScales = 4;                           // scales of tiles in place
     static constexpr int kSoftmax = 4 * kPipes, kConvert = 4;   // warps
-    static constexpr int kThreads = 32 * (kSoftmax + kConvert + 1);
-    static constexpr int kSmem = kPipes * kQ + 2 * kStages * kTile + 1024;  // aligned by the kernel
+    static constexpr int kThreads = 32 * (kSoftmax + kConvert);
+    static constexpr int kBox = prefix_box(D);
+    static constexpr int kRaw = kTok * D;                       // bytes of a tile's codes, K or V
+    static constexpr int kF16 = kPipes * kQ + (kKeys + kValues) * kTile;
+    static constexpr int kFit = (213 * 1024 - kF16) / kRaw;
+    static constexpr int kRing = kFit < 8 ? kFit : 8;           // of them in the ring
+    static_assert(kRing >= 3, "a tile and a half on their way");
+    static constexpr int kSmem = kF16 + kRing * kRaw + 1024;    // aligned by the kernel
     static constexpr int kChunks = kTok * D / 16 / (32 * kConvert);  // of 16 codes a converter
+    // Registers of a thread: what the block is launched with, then each role's share (with two
+    // pipelines).  A quarter of an SM holds one converter and a warp of each pipeline.
+    static constexpr int kLaunchRegs = 168, kSoftmaxRegs = D <= 64 ? 208 : 200;
+    static constexpr int kConvertRegs = D <= 64 ? 88 : 104;
+    static_assert(2 * kSoftmaxRegs + kConvertRegs <= 3 * kLaunchRegs,
+                  "a share beyond what was launched would wait for ever");
     static constexpr int kOut = kPipes * kTok;                  // tensor-memory column of O
 };
 
+// The outputs of a segment, and the partial ones of a segment that is not a whole tile: called by
+// all softmax warps together.  `done`: the barrier of this pipeline's product (0: it had no tile).
+template <int D>
+__device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, uint8_t* smem,
+                                       float2* s_sum, uint32_t o_col, int from, int u0, int u1,
+                                       int row, int p, float ref, float l, uint32_t done,
+                                       uint32_t parity, volatile int* gave_up) {
+    using X = Shape<D>;
+    constexpr int NP = X::kPipes, kQuads = D / 4;
+    const Segment g(plan, a, from, u1, X::kRows, X::kTok);
+    const bool both = NP == 2 && g.rows - g.row0 > kPrefixRows;
+    const int tile_row = (both ? p * kPrefixRows : 0) + row, r = g.row0 + tile_row;
+    const bool on = r < g.rows;
+    const Row at(a, plan.lo[g.p], g.h, on ? r : g.row0);
+    if (done) {
+        wait(done, parity, gave_up);
+        fence_after();
+    }
+    if (*gave_up) l = NAN;
+    // Two halves of the tokens: the second pipeline's go through the queries' memory.
+    float4* const second = reinterpret_cast<float4*>(smem) + row * kQuads;
+    float mine_by = 1.f, second_by = 0.f;
+    if (NP == 2 && !both) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // both are done with the queries
+        if (p == 1) {
+            s_sum[row] = make_float2(ref, l);
+            if (done) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t x[32];
+                    load_columns(x, o_col + c);
+                    loaded(x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // rotated by the row: different banks
+                        second[(c / 4 + k + row) % kQuads] = make_float4(
+                            __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]),
+                            __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+                }
+            }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (p == 0 && g.n > 1) {
+            const float2 o = s_sum[row];
+            const float top = fmaxf(ref + log2f(l), o.x + log2f(o.y));
+            mine_by = exp2_fast(ref - top);
+            second_by = exp2_fast(o.x - top);
+            l = l * mine_by + o.y * second_by;
+            ref = top;
+        }
+    }
+    if (NP == 1 || both || p == 0) {
+        const bool whole = g.n == g.tiles;
+        const long long out_row = ((long long)at.b * a.S + at.s) * a.Hq + at.head;
+        float other = 0.f;
+        if (whole) {
+            const Joined j(ref + log2f(l), a.join ? ld(a.join_lse + out_row) : -INFINITY);
+            const float by = j.mine / l;
+            mine_by *= by;
+            second_by *= by;
+            other = j.other;
+            if (on && a.lse) a.lse[out_row] = j.lse;
+        }
+        const long long slot = 2 * (long long)blockIdx.x + (from == u0 ? 0 : 1);
+        float4* part = reinterpret_cast<float4*>(a.part) + slot * kQuads * X::kRows + tile_row;
+        if (!whole && on) a.part_sum[slot * X::kRows + tile_row] = make_float2(ref, l);
+        uint16_t* out = a.out + at.at(a.out_stride);
+        const uint16_t* join = a.join + at.at(a.join_stride);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t x[32];
+            load_columns(x, o_col + c);
+            loaded(x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float y[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) y[m] = __uint_as_float(x[4 * k + m]) * mine_by;
+                if (NP == 2 && !both && g.n > 1) {
+                    const float4 z = second[(c / 4 + k + row) % kQuads];
+                    y[0] += z.x * second_by, y[1] += z.y * second_by;
+                    y[2] += z.z * second_by, y[3] += z.w * second_by;
+                }
+                if (!on) continue;
+                const int d = c + 4 * k;
+                if (!whole) {
+                    part[(long long)(d / 4) * X::kRows] = make_float4(y[0], y[1], y[2], y[3]);
+                    continue;
+                }
+                if (other > 0.f) {
+                    const uint2 z = load4(join + d, a.vec_join);
+                    const float2 z0 = pair(z.x, a.fp16), z1 = pair(z.y, a.fp16);
+                    y[0] += z0.x * other, y[1] += z0.y * other;
+                    y[2] += z1.x * other, y[3] += z1.y * other;
+                }
+                store4(out + d, unpair(y[0], y[1], a.fp16), unpair(y[2], y[3], a.fp16), a.vec_out);
+            }
+        }
+    }
+    if (NP == 2 && !both) asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// Barriers in shared memory: what the matrix instructions and the copies signal.
 enum Bar : int {
-    kQFull = 0,                  // [pipe]
-    kSFull = 2, kPFull = 4, kOFull = 6,
-    kKFull = 8, kKEmpty = 10, kVFull = 12, kVEmpty = 14,  // [stage]
-    kScFull = 16, kScEmpty = 20,  // [scale stage]
-    kDone = 24, kBars = 25
+    kSFull = 0, kOFull = 2,   // [pipe]
+    kKEmpty = 4, kVEmpty = 5, // [kKeys], [kValues]
+    kDone = 7,
+    kRawFull = 8,             // [kRing], by the copies
+    kBars = 16
 };
 
+// Barriers of the SM between the four converters and a pipeline's four warps: a tile's keys (and
+// scales) are written; its values are written, and P.  They let a warp go on with loads under
+// way, where an arrival at a barrier in shared memory waits for these.
+__device__ __forceinline__ int keys_barrier(int stage, int p) { return 2 + 2 * stage + p; }
+__device__ __forceinline__ int values_barrier(int stage, int p) { return 6 + 2 * stage + p; }
+__device__ __forceinline__ void meet(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void meet_later(int id) {
+    asm volatile("bar.arrive %0, 256;" ::"r"(id) : "memory");
+}
+
 template <int CODE, int D>
-__global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefix_kernel(const PrefixArgs a) {
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+    prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map) {
     using X = Shape<D>;
     constexpr int NP = X::kPipes, TOK = X::kTok;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Plan plan;
     __shared__ __align__(16) float s_k[X::kScales][TOK], s_v[X::kScales][TOK];
     __shared__ __align__(16) float s_log[X::kScales][TOK];  // log2 of the V scale
+    __shared__ __align__(8) float2 s_even[X::kScales][TOK / 16];  // of 16 tokens: log2, 1 / V scale
     __shared__ __align__(16) int s_small[X::kScales][X::kConvert];  // a V scale below 2^-60
     __shared__ __align__(8) unsigned long long s_bar[kBars];
     __shared__ float2 s_sum[kPrefixRows];  // of the second pipeline
@@ -427,30 +742,23 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefix_kernel(const Pre
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* const smem = smem_raw + (-(int)shared_address(smem_raw) & 1023);
     const uint32_t q_at = shared_address(smem), k_at = q_at + NP * X::kQ;
-    const uint32_t v_at = k_at + X::kStages * X::kTile;
+    const uint32_t v_at = k_at + X::kKeys * X::kTile, raw_at = v_at + X::kValues * X::kTile;
     const uint32_t bars = shared_address(s_bar);
     auto bar = [&](int i) { return (uint32_t)(bars + 8 * i); };
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            barrier_init(bar(kQFull + i), kPrefixRows);
             barrier_init(bar(kSFull + i), 1);
-            barrier_init(bar(kPFull + i), kPrefixRows);
             barrier_init(bar(kOFull + i), 1);
-            barrier_init(bar(kKFull + i), 32 * X::kConvert);
-            barrier_init(bar(kKEmpty + i), 1);
-            barrier_init(bar(kVFull + i), 32 * X::kConvert);
-            barrier_init(bar(kVEmpty + i), 1);
         }
-        for (int i = 0; i < X::kScales; ++i) {
-            barrier_init(bar(kScFull + i), 32 * X::kConvert);
-            barrier_init(bar(kScEmpty + i), X::kSoftmax);
-        }
-        barrier_init(bar(kDone), 1);
+        for (int i = 0; i < X::kKeys; ++i) barrier_init(bar(kKEmpty + i), NP);
+        for (int i = 0; i < X::kValues; ++i) barrier_init(bar(kVEmpty + i), NP);
+        for (int i = 0; i < X::kRing; ++i) barrier_init(bar(kRawFull + i), 1);
+        barrier_init(bar(kDone), NP);
         s_gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == X::kSoftmax + X::kConvert) {
+    if (warp == 0) {
         // One CTA an SM; waits for what else holds tensor memory, never the other way round.
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          shared_address(&s_tmem))
@@ -459,187 +767,199 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefix_kernel(const Pre
         fence_before();
     }
     wait_for_previous();
-    if (warp == 0) fill_plan(plan, a, X::kRows, TOK);
+    if (warp == 1) fill_plan(plan, a, X::kRows, TOK);
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
-    const long long units = plan.unit[a.P];
+    const int units = plan.unit[a.P];
     const int ctas = working(units, a.ctas);
     const bool works = (int)blockIdx.x < ctas;
-    const long long u0 = works ? first_unit(units, blockIdx.x, ctas) : 0;
-    const long long u1 = works ? first_unit(units, blockIdx.x + 1, ctas) : 0;
+    const int u0 = works ? first_unit(units, blockIdx.x, ctas) : 0;
+    const int u1 = works ? first_unit(units, blockIdx.x + 1, ctas) : 0;
     volatile int* const gave_up = &s_gave_up;
 
-    if (warp >= X::kSoftmax && warp < X::kSoftmax + X::kConvert) {
+    if (warp >= X::kSoftmax) {
+        if constexpr (NP == 2)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kConvertRegs));
         // ---- converters ----------------------------------------------------------
         const int t = tid - 32 * X::kSoftmax;
         constexpr int kRowChunks = D / 16;  // 16-byte pieces of a token
-        uint4 k_next[X::kChunks], v_next[X::kChunks];
-        float ks_next = 0.f, vs_next = 0.f;
-        // The unit to be loaded next.
-        long long from = u0;
-        int tile = 0, end = 0, len = 0;
-        const uint8_t* rows = nullptr;    // of the prefix, at the K head
-        const float* scales = nullptr;    // likewise
-        auto move_on = [&]() {
-            if (tile < end || from >= u1) return;
-            const Segment g(plan, a, from, u1, X::kRows, TOK);
-            from += g.n;
-            tile = g.tile0;
-            end = g.tile0 + g.n;
-            len = plan.len[g.p];
-            const int r = ld(a.prefix + g.p);
-            rows = a.rows + (long long)r * a.L * a.W + g.h * D;
-            scales = a.scales + (long long)r * a.NB * 2 * a.Hkv + g.h;
+        // Units in order: one walk for the copies (thread 0), one for what is converted.
+        struct Walk {
+            int from, tile, end, first, len, h, r;
+            bool both;
         };
-        auto load = [&](uint4 (&x)[X::kChunks], const uint8_t* base) {
+        auto next = [&](Walk& w) {  // false past the last
+            if (++w.tile < w.end) return true;
+            if (w.from >= u1) return false;
+            const Segment g(plan, a, w.from, u1, X::kRows, TOK);
+            w.from += g.n;
+            w.tile = w.first = g.tile0;
+            w.end = g.tile0 + g.n;
+            w.len = plan.len[g.p];
+            w.both = NP == 2 && g.rows - g.row0 > kPrefixRows;
+            w.h = g.h;
+            w.r = ld(a.prefix + g.p);
+            return true;
+        };
+        Walk copy = {u0, 0, 0, 0, 0, 0, 0, false};
+        int copies = 0;  // of K and V tiles so far
+        auto start_copy = [&]() {  // thread 0
+            if (copies % 2 == 0 && !next(copy)) return;
+            const int slot = copies % X::kRing;
+            const uint32_t full = bar(kRawFull + slot);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
+                         "n"(X::kRaw)
+                         : "memory");
+            const int x = (copy.h + (copies % 2 == 0 ? 0 : a.Hkv)) * D;
+#pragma unroll
+            for (int i = 0; i < D / X::kBox; ++i)
+                asm volatile(
+                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::"
+                    "bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(raw_at + slot * X::kRaw +
+                                                                  i * TOK * X::kBox),
+                    "l"(&map), "r"(full), "r"(x + i * X::kBox), "r"(copy.tile * TOK), "r"(copy.r)
+                    : "memory");
+            ++copies;
+        };
+        if (t == 0) {
+            for (int i = 0; i < X::kRing; ++i)
+                if (copies == i) start_copy();  // while there are units
+        }
+        Walk walk = {u0, 0, 0, 0, 0, 0, 0, false};
+        float k_scale = 0.f, v_scale = 0.f;
+        auto load_scales = [&]() {  // of the unit that the walk is at
+            const int token = walk.tile * TOK + t;
+            k_scale = v_scale = 0.f;
+            if (t < TOK && token < walk.len) {
+                const float* p = a.scales +
+                                 ((long long)walk.r * a.NB + a.block.of(token)) * 2 * a.Hkv + walk.h;
+                k_scale = ld(p);
+                v_scale = ld(p + a.Hkv);
+            }
+        };
+        // Codes of the ring's tile `which` as f16; those of tokens from `live` on as zeros.  Eight lanes
+        // take one piece of eight rows: what they read and store together lies in
+        // different banks.
+        auto convert = [&](int which, uint32_t to, int live) {
+            const int slot = which % X::kRing;
+            const uint32_t raw = raw_at + slot * X::kRaw;
+            wait(bar(kRawFull + slot), which / X::kRing & 1, gave_up);
+            uint4 x[X::kChunks];
 #pragma unroll
             for (int c = 0; c < X::kChunks; ++c) {
                 const int i = c * 32 * X::kConvert + t;
-                const int token = tile * TOK + i / kRowChunks;
-                x[c] = make_uint4(0, 0, 0, 0);
-                if (tile < end && token < len)
-                    x[c] = ld_once_v4(base + (long long)token * a.W + i % kRowChunks * 16);
+                const int row = i / (8 * kRowChunks) * 8 + i % 8, piece = i / 8 % kRowChunks;
+                constexpr int kIn = X::kBox / 16;  // pieces of a box's row
+                const int swizzle = X::kBox == 64 ? row >> 1 & 3 : row >> 2 & 1;
+                const uint32_t at = raw + piece / kIn * (TOK * X::kBox) + row * X::kBox +
+                                    ((piece % kIn ^ swizzle) << 4);
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[c].x), "=r"(x[c].y), "=r"(x[c].z), "=r"(x[c].w)
+                             : "r"(at)
+                             : "memory");
             }
-        };
-        auto load_scales = [&]() {
-            const int token = tile * TOK + t;
-            ks_next = vs_next = 0.f;
-            if (tile < end && t < TOK && token < len) {
-                const float* p = scales + (long long)a.block.of(token) * 2 * a.Hkv;
-                ks_next = ld(p) * a.k_sign;
-                vs_next = ld(p + a.Hkv);
-            }
-        };
-        auto put = [&](const uint4 (&x)[X::kChunks], uint32_t at) {
+            asm volatile("bar.sync 12, 128;" ::: "memory");  // all have read it
+            if (t == 0) start_copy();
 #pragma unroll
             for (int c = 0; c < X::kChunks; ++c) {
                 const int i = c * 32 * X::kConvert + t;
-                const int row = i / kRowChunks, d = i % kRowChunks * 16;
+                const int row = i / (8 * kRowChunks) * 8 + i % 8, piece = i / 8 % kRowChunks;
+                if (row >= live) x[c] = make_uint4(0, 0, 0, 0);
                 uint32_t y[8];
                 halves<CODE>(x[c].x, y[0], y[1]);
                 halves<CODE>(x[c].y, y[2], y[3]);
                 halves<CODE>(x[c].z, y[4], y[5]);
                 halves<CODE>(x[c].w, y[6], y[7]);
-                // Lanes of the second panel begin with their second half: the 8 lanes that store
-                // together then use different banks.
-                const bool swap = d / 64 & 1;
-                const uint32_t lo = at + place(row, d, TOK * 128), hi = at + place(row, d + 8, TOK * 128);
-                const uint32_t p0 = swap ? hi : lo, p1 = swap ? lo : hi;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p0),
-                             "r"(swap ? y[4] : y[0]), "r"(swap ? y[5] : y[1]),
-                             "r"(swap ? y[6] : y[2]), "r"(swap ? y[7] : y[3])
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 to + place(row, piece * 16, TOK * 128)),
+                             "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                              : "memory");
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p1),
-                             "r"(swap ? y[0] : y[4]), "r"(swap ? y[1] : y[5]),
-                             "r"(swap ? y[2] : y[6]), "r"(swap ? y[3] : y[7])
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 to + place(row, piece * 16 + 8, TOK * 128)),
+                             "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
                              : "memory");
             }
         };
-        move_on();
-        load(k_next, rows);
-        load(v_next, rows + a.Hkv * D);
-        load_scales();
-        const long long n = u1 - u0;
-        for (long long i = 0; i < n; ++i) {
-            const int stage = (int)(i & 1), sc = (int)(i & 3);
-            const uint32_t phase = (uint32_t)(i >> 1) & 1, sc_phase = (uint32_t)(i >> 2) & 1;
-            wait(bar(kScEmpty + sc), sc_phase ^ 1, gave_up);
+        if (next(walk)) load_scales();
+        const int n = u1 - u0;
+        for (int i = 0; i < n; ++i) {
+            const int ks = i % X::kKeys, vs = i % X::kValues, sc = i & 3;
+            const int live = walk.len - walk.tile * TOK;
+            // The pipelines that read this tile.
+            const bool reads[2] = {NP == 1 || walk.both || (walk.tile - walk.first) % 2 == 0,
+                                   NP == 2 && (walk.both || (walk.tile - walk.first) % 2 == 1)};
+            // The scales' place is free with the keys': the scores of a tile come behind the softmax
+            // of the tile before (both pipelines) or of two before (each its own), and
+            // scales are kept for four.
+            wait(bar(kKEmpty + ks), (i / X::kKeys & 1) ^ 1, gave_up);
+            const float lg = log2f(v_scale);
             if (t < TOK) {
-                s_k[sc][t] = ks_next;
-                s_v[sc][t] = vs_next;
-                s_log[sc][t] = log2f(vs_next);
+                s_k[sc][t] = k_scale * a.k_sign;
+                s_v[sc][t] = v_scale;
+                s_log[sc][t] = lg;
+                if (t % 16 == 0) s_even[sc][t / 16] = make_float2(lg, __frcp_rn(v_scale));
             }
-            const bool small = __any_sync(0xffffffffu, t < TOK && vs_next < 0x1p-60f);
+            const bool small = __any_sync(0xffffffffu, t < TOK && v_scale < 0x1p-60f);
             if (lane == 0) s_small[sc][warp - X::kSoftmax] = small;
-            arrive(bar(kScFull + sc));
-            wait(bar(kKEmpty + stage), phase ^ 1, gave_up);
-            put(k_next, k_at + stage * X::kTile);
-            fence_shared();
-            arrive(bar(kKFull + stage));
-            // the next tile's keys are under way while the values are converted
-            ++tile;
-            move_on();
-            load(k_next, rows);
-            load_scales();
-            wait(bar(kVEmpty + stage), phase ^ 1, gave_up);
-            put(v_next, v_at + stage * X::kTile);
-            fence_shared();
-            arrive(bar(kVFull + stage));
-            load(v_next, rows + a.Hkv * D);
-        }
-    }
-    if (warp == X::kSoftmax + X::kConvert && lane == 0) {
-        // ---- matrix instructions ---------------------------------------------------
-        constexpr uint32_t kScores = instruction(TOK, false), kValues = instruction(D, true);
-        uint32_t p_done = 0, q_done = 0;  // phases, a bit a pipeline
-        long long tiles = 0;  // of the segments before
-        for (long long from = u0; from < u1;) {
-            const Segment g(plan, a, from, u1, X::kRows, TOK);
-            const bool both = NP == 2 && g.rows - g.row0 > kPrefixRows;
-            const int items = both ? 2 * g.n : g.n;
-            for (int w = 0; w < items + NP; ++w) {
-                if (w >= NP) {
-                    const int v = w - NP, p = v % NP, i = both ? v / 2 : v;
-                    const long long at = tiles + i;
-                    const int stage = (int)(at & 1);
-                    wait(bar(kVFull + stage), (uint32_t)(at >> 1) & 1, gave_up);
-                    wait(bar(kPFull + p), p_done >> p & 1, gave_up);
-                    p_done ^= 1u << p;
-                    fence_after();
-                    const uint32_t o = tmem + X::kOut + p * D, s = tmem + p * TOK;
-                    const bool first = both ? i == 0 : i < NP;
-                    const uint64_t b = matrix(v_at + stage * X::kTile, TOK * 128);
+            convert(2 * i, k_at + ks * X::kTile, live);
 #pragma unroll
-                    for (int k = 0; k < TOK / 16; ++k)  // 16 tokens are 16 rows of 128 bytes
-                        multiply_tensor(o, s + 8 * k, b + k * (2048 >> 4), kValues,
-                                        !(first && k == 0));
-                    if (!both || p == 1) commit(bar(kVEmpty + stage));
-                    if (both ? i == g.n - 1 : i + NP >= g.n) commit(bar(kOFull + p));
-                }
-                if (w < items) {
-                    const int p = w % NP, i = both ? w / 2 : w;
-                    const long long at = tiles + i;
-                    const int stage = (int)(at & 1);
-                    if (both ? i == 0 : i < NP) {
-                        wait(bar(kQFull + p), q_done >> p & 1, gave_up);
-                        q_done ^= 1u << p;
-                    }
-                    wait(bar(kKFull + stage), (uint32_t)(at >> 1) & 1, gave_up);
-                    fence_after();
-                    const uint32_t q = q_at + p * X::kQ, key = k_at + stage * X::kTile;
+            for (int p = 0; p < NP; ++p)
+                if (reads[p]) meet_later(keys_barrier(0, p));
+            if (next(walk)) load_scales();  // of the next tile
+            wait(bar(kVEmpty + vs), (i / X::kValues & 1) ^ 1, gave_up);
+            convert(2 * i + 1, v_at + vs * X::kTile, live);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const int panel = k / 4, in = k % 4 * 32;
-                        multiply(tmem + p * TOK, matrix(q + panel * kPrefixRows * 128 + in, 16),
-                                 matrix(key + panel * TOK * 128 + in, 16), kScores, k > 0);
-                    }
-                    commit(bar(kSFull + p));
-                    if (!both || p == 1) commit(bar(kKEmpty + stage));
-                }
-            }
-            tiles += g.n;
-            from += g.n;
+            for (int p = 0; p < NP; ++p)
+                if (reads[p]) meet_later(values_barrier(vs, p));
         }
-        commit(bar(kDone));
-        wait(bar(kDone), 0, gave_up);
-    }
-    if (warp < X::kSoftmax) {
+        // No copy is under way when the CTA ends, even if a wait was given up.
+        if (t == 0)
+            for (int i = max(0, copies - X::kRing); i < copies; ++i)
+                wait_still(bar(kRawFull + i % X::kRing), i / X::kRing & 1);
+    } else {
+        if constexpr (NP == 2)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kSoftmaxRegs));
         // ---- softmax ---------------------------------------------------------------
         const int p = warp / 4, row = tid - p * kPrefixRows;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t s_col = lanes + p * TOK, o_col = lanes + X::kOut + p * D;
         uint32_t s_done = 0, o_done = 0;
-        long long tiles = 0;  // of the segments before
-        for (long long from = u0; from < u1;) {
+        constexpr uint32_t kScores = instruction(TOK, false), kValues = instruction(D, true);
+        const bool issuer = (warp & 3) == 0, leader = issuer && elected();
+        // S = Q K^T of the CTA's tile t.
+        auto scores = [&](int t, int users) {
+            const int stage = t % X::kKeys;
+            meet(keys_barrier(0, p));
+            if (!issuer) return;
+            fence_shared();
+            fence_after();
+            const uint64_t q = matrix(q_at + p * X::kQ, 16);
+            const uint64_t key = matrix(k_at + stage * X::kTile, 16);
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int panel = k / 4, in = k % 4 * 32;
+                    multiply(tmem + p * TOK, q + ((panel * kPrefixRows * 128 + in) >> 4),
+                             key + ((panel * TOK * 128 + in) >> 4), kScores, k > 0);
+                }
+                commit(bar(kSFull + p));
+                for (int i = users; i <= NP; ++i) commit(bar(kKEmpty + stage));
+            }
+            __syncwarp();
+        };
+        for (int from = u0; from < u1;) {
             const Segment g(plan, a, from, u1, X::kRows, TOK);
             const bool both = NP == 2 && g.rows - g.row0 > kPrefixRows;
             const int mine = NP == 1 || both ? g.n : (g.n + 1 - p) / 2;
             const int r = g.row0 + (both ? p * kPrefixRows : 0) + row;
             const bool on = r < g.rows;
             const Row at(a, plan.lo[g.p], g.h, on ? r : g.row0);
-            const int len = plan.len[g.p];
-            float f = 0.f;  // of the products
+            const int rest = plan.len[g.p] - g.tile0 * TOK;
+            // Warps without rows leave theirs as they are: a row's products are its own.
+            const bool alive = r - lane < g.rows;
+            const int users = both ? 2 : 1;  // pipelines that read a tile
+            float f = 0.f;                   // of the products
             if (mine > 0) {
                 // The row's largest element goes to [2^14, 2^15), f16's top.
                 const uint16_t* q = a.q + at.at(a.q_stride);
@@ -662,7 +982,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefix_kernel(const Pre
                 f = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
                 const uint32_t to = q_at + p * X::kQ;
 #pragma unroll 4
-                for (int d = 0; d < D; d += 8) {
+                for (int d = 0; alive && d < D; d += 8) {
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (on) x = load8(q + d, a.vec_q);
                     uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -677,194 +997,64 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefix_kernel(const Pre
                                  : "memory");
                 }
                 fence_shared();
-                arrive(bar(kQFull + p));
+                scores(from - u0 + (both || NP == 1 ? 0 : p), users);
             }
             float ref = 0.f, l = 0.f;
             for (int j = 0; j < mine; ++j) {
                 const int i = NP == 1 || both ? j : 2 * j + p;
-                const long long t = tiles + i;
-                const int sc = (int)(t & 3);
-                const int live = len - (g.tile0 + i) * TOK;  // tokens of the tile, or more
-                wait(bar(kScFull + sc), (uint32_t)(t >> 2) & 1, gave_up);
-                const int4 small = *reinterpret_cast<const int4*>(s_small[sc]);
-                const bool special = live < TOK || (small.x | small.y | small.z | small.w);
+                const int t = from - u0 + i, sc = t & 3;
+                const int live = rest - i * TOK;  // tokens of the tile, or more
                 wait(bar(kSFull + p), s_done++ & 1, gave_up);
                 fence_after();
-                // The largest score, and the largest of score + log2(V scale).
-                float top = -INFINITY, most = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < TOK; c += 32) {
-                    uint32_t x[32];
-                    load_columns(x, s_col + c);
-                    loaded(x);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 ks = *reinterpret_cast<const float4*>(&s_k[sc][c + k]);
-                        const float4 lg = *reinterpret_cast<const float4*>(&s_log[sc][c + k]);
-                        const float kk[4] = {ks.x, ks.y, ks.z, ks.w};
-                        const float ll[4] = {lg.x, lg.y, lg.z, lg.w};
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const float z = __uint_as_float(x[k + m]) * kk[m] * f;
-                            if (!special || c + k + m < live) {
-                                most = fmaxf(most, z + ll[m]);
-                                if (special) top = fmaxf(top, z);
-                            }
-                        }
-                    }
-                }
-                float want = most - 11.5f;
-                if (special) want = fmaxf(want, top - 100.f);
-                if (j == 0) {
-                    ref = want;
-                } else {
-                    const bool grow = want > ref + 4.f;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float by = grow ? exp2_fast(ref - want) : 1.f;
-                        l *= by;
-                        if (grow) ref = want;
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t x[32];
-                            load_columns(x, o_col + c);
-                            loaded(x);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                x[k] = __float_as_uint(__uint_as_float(x[k]) * by);
-                            store_columns(o_col + c, x);
-                        }
-                    }
-                }
-#pragma unroll 1
-                for (int c = 0; c < TOK; c += 32) {
-                    uint32_t x[32], y[16];
-                    load_columns(x, s_col + c);
-                    loaded(x);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 ks = *reinterpret_cast<const float4*>(&s_k[sc][c + k]);
-                        const float4 vs = *reinterpret_cast<const float4*>(&s_v[sc][c + k]);
-                        const float kk[4] = {ks.x, ks.y, ks.z, ks.w};
-                        const float vv[4] = {vs.x, vs.y, vs.z, vs.w};
-                        float e[4];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const float z = __uint_as_float(x[k + m]) * kk[m] * f;
-                            e[m] = exp2_fast(z - ref);
-                            if (special && c + k + m >= live) e[m] = 0.f;
-                            l += e[m];
-                            e[m] *= vv[m];
-                        }
-                        y[k / 2] = pack_half2(e[0], e[1]);
-                        y[k / 2 + 1] = pack_half2(e[2], e[3]);
-                    }
-                    store_columns(s_col + c / 2, y);
+                if (alive) {
+                    const int4 small = *reinterpret_cast<const int4*>(s_small[sc]);
+                    const bool special = live < TOK || (small.x | small.y | small.z | small.w);
+                    if (a.even && !special)
+                        softmax_even<TOK, D>(s_col, o_col, f, s_k[sc], s_even[sc], j == 0, ref, l);
+                    else
+                        softmax_any<TOK, D>(s_col, o_col, f, s_k[sc], s_v[sc], s_log[sc], live,
+                                            j == 0, ref, l);
                 }
                 stored();
                 fence_before();
-                arrive(bar(kPFull + p));
-                __syncwarp();
-                if (lane == 0) arrive_n(bar(kScEmpty + sc), NP == 1 || both ? 1 : 2);
+                const int stage = t % X::kValues;
+                if (issuer) {  // O += P V
+                    meet(values_barrier(stage, p));
+                    fence_shared();
+                    fence_after();
+                    const uint64_t b = matrix(v_at + stage * X::kTile, TOK * 128);
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < TOK / 16; ++k)  // 16 tokens are 16 rows of 128 bytes
+                            multiply_tensor(tmem + X::kOut + p * D, tmem + p * TOK + 8 * k,
+                                            b + k * (2048 >> 4), kValues, k > 0 || j > 0);
+                        for (int u = users; u <= NP; ++u) commit(bar(kVEmpty + stage));
+                        if (j + 1 == mine) commit(bar(kOFull + p));
+                    }
+                    __syncwarp();
+                } else {
+                    meet_later(values_barrier(stage, p));
+                }
+                // The next scores take P's place, behind the product with V.
+                if (j + 1 < mine) scores(t + (both || NP == 1 ? 1 : 2), users);
             }
 
             // ---- the segment's outputs ---------------------------------------------------
-            if (mine > 0) {
-                wait(bar(kOFull + p), o_done++ & 1, gave_up);
-                fence_after();
-            }
-            if (*gave_up) l = NAN;
-            // Two halves of the tokens: the second pipeline's go through the queries' memory.
-            constexpr int kQuads = D / 4;
-            float4* const second = reinterpret_cast<float4*>(smem) + row * kQuads;
-            float mine_by = 1.f, second_by = 0.f;
-            if (NP == 2 && !both) {
-                asm volatile("bar.sync 1, 256;" ::: "memory");  // both are done with the queries
-                if (p == 1) {
-                    s_sum[row] = make_float2(ref, l);
-                    if (mine > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t x[32];
-                            load_columns(x, o_col + c);
-                            loaded(x);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)  // rotated by the row: different banks
-                                second[(c / 4 + k + row) % kQuads] = make_float4(
-                                    __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]),
-                                    __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
-                        }
-                    }
-                }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (p == 0 && g.n > 1) {
-                    const float2 o = s_sum[row];
-                    const float top = fmaxf(ref + log2f(l), o.x + log2f(o.y));
-                    mine_by = exp2_fast(ref - top);
-                    second_by = exp2_fast(o.x - top);
-                    l = l * mine_by + o.y * second_by;
-                    ref = top;
-                }
-            }
-            if (NP == 1 || both || p == 0) {
-                const bool whole = g.n == g.tiles;
-                const long long out_row = ((long long)at.b * a.S + at.s) * a.Hq + at.head;
-                float other = 0.f;
-                if (whole) {
-                    const Joined j(ref + log2f(l), a.join ? ld(a.join_lse + out_row) : -INFINITY);
-                    const float by = j.mine / l;
-                    mine_by *= by;
-                    second_by *= by;
-                    other = j.other;
-                    if (on && a.lse) a.lse[out_row] = j.lse;
-                }
-                const int tile_row = (both ? p * kPrefixRows : 0) + row;
-                const long long slot = 2 * (long long)blockIdx.x + (from == u0 ? 0 : 1);
-                float4* part = reinterpret_cast<float4*>(a.part) + slot * kQuads * X::kRows + tile_row;
-                if (!whole && on)
-                    a.part_sum[slot * X::kRows + tile_row] = make_float2(ref, l);
-                uint16_t* out = a.out + at.at(a.out_stride);
-                const uint16_t* join = a.join + at.at(a.join_stride);
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t x[32];
-                    load_columns(x, o_col + c);
-                    loaded(x);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float y[4];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) y[m] = __uint_as_float(x[4 * k + m]) * mine_by;
-                        if (NP == 2 && !both && g.n > 1) {
-                            const float4 z = second[(c / 4 + k + row) % kQuads];
-                            y[0] += z.x * second_by, y[1] += z.y * second_by;
-                            y[2] += z.z * second_by, y[3] += z.w * second_by;
-                        }
-                        if (!on) continue;
-                        const int d = c + 4 * k;
-                        if (!whole) {
-                            part[(long long)(d / 4) * X::kRows] = make_float4(y[0], y[1], y[2], y[3]);
-                            continue;
-                        }
-                        if (other > 0.f) {
-                            const uint2 z = load4(join + d, a.vec_join);
-                            const float2 z0 = pair(z.x, a.fp16), z1 = pair(z.y, a.fp16);
-                            y[0] += z0.x * other, y[1] += z0.y * other;
-                            y[2] += z1.x * other, y[3] += z1.y * other;
-                        }
-                        store4(out + d, unpair(y[0], y[1], a.fp16), unpair(y[2], y[3], a.fp16),
-                               a.vec_out);
-                    }
-                }
-            }
-            if (NP == 2 && !both) asm volatile("bar.sync 1, 256;" ::: "memory");
-            tiles += g.n;
+            // What they need of the segment is read anew, so that it takes no registers in the loop.
+            int anew = from, row_anew = row;
+            asm volatile("" : "+r"(anew), "+r"(row_anew));
+            finish<D>(a, plan, smem, s_sum, o_col, anew, u0, u1, row_anew, p, ref, l,
+                      mine > 0 ? bar(kOFull + p) : 0u, o_done & 1, gave_up);
+            o_done += mine > 0;
             from += g.n;
         }
+        if (leader) commit(bar(kDone));
+        if (issuer) wait_still(bar(kDone), 0);
     }
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (warp == X::kSoftmax + X::kConvert) {
+    if (warp == 0) {
         __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -872,23 +1062,36 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefix_kernel(const Pre
 }
 
 template <int CODE, int D>
-cudaError_t run_one(const PrefixArgs& a, cudaStream_t s) {
+cudaError_t run_one(const PrefixArgs& a, const CUtensorMap& map, cudaStream_t s) {
     static SmemOptIn opt;
-    const cudaError_t e = ensure_smem(prefix_kernel<CODE, D>, Shape<D>::kSmem, &opt);
+    cudaError_t e = ensure_smem(prefix_kernel<CODE, D>, Shape<D>::kSmem, &opt);
     if (e != cudaSuccess) return e;
+    if (Shape<D>::kPipes == 2) {
+        // The roles' shares are there only if the compiler has used the whole launch bound.
+        static std::atomic<int> regs{0};
+        int n = regs.load(std::memory_order_relaxed);
+        if (n == 0) {
+            cudaFuncAttributes attr;
+            e = cudaFuncGetAttributes(&attr, prefix_kernel<CODE, D>);
+            if (e != cudaSuccess) return e;
+            n = attr.numRegs;
+            regs.store(n, std::memory_order_relaxed);
+        }
+        if (n != Shape<D>::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
     return launch_chained(prefix_kernel<CODE, D>, a.ctas, Shape<D>::kThreads, Shape<D>::kSmem, 0, s,
-                          a);
+                          a, map);
 }
 
 template <int CODE>
-cudaError_t run(const PrefixArgs& a, int D, cudaStream_t s) {
+cudaError_t run(const PrefixArgs& a, const CUtensorMap& map, int D, cudaStream_t s) {
     switch (D) {
-        case 32: return run_one<CODE, 32>(a, s);
-        case 64: return run_one<CODE, 64>(a, s);
-        case 96: return run_one<CODE, 96>(a, s);
-        case 128: return run_one<CODE, 128>(a, s);
-        case 192: return run_one<CODE, 192>(a, s);
-        case 256: return run_one<CODE, 256>(a, s);
+        case 32: return run_one<CODE, 32>(a, map, s);
+        case 64: return run_one<CODE, 64>(a, map, s);
+        case 96: return run_one<CODE, 96>(a, map, s);
+        case 128: return run_one<CODE, 128>(a, map, s);
+        case 192: return run_one<CODE, 192>(a, map, s);
+        case 256: return run_one<CODE, 256>(a, map, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -3,8 +3,8 @@
 
 namespace hs {
 
-cudaError_t prefix_run_e4m3(const PrefixArgs& a, int D, cudaStream_t s) {
-    return prefix::run<HS_KV_E4M3>(a, D, s);
+cudaError_t prefix_run_e4m3(const PrefixArgs& a, const CUtensorMap& map, int D, cudaStream_t s) {
+    return prefix::run<HS_KV_E4M3>(a, map, D, s);
 }
 
 }  // namespace hs
