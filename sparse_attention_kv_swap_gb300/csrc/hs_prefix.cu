@@ -1,8 +1,8 @@
 // Launch of hs_attend_prefix (the kernel is in hs_prefix.cuh), and the kernel that puts
 // together the rows whose tokens fell to several CTAs.
 //
-// A CTA takes 32 rows of a K/V head, a lane a row, the warps the quads of its elements; partial
-// outputs lie with consecutive rows side by side.  They come mostly out of L2.
+// A CTA takes 32 rows of a K/V head, a lane a row, and 16 quads of their elements, a warp a quad;
+// partial outputs lie with consecutive rows side by side.  They come mostly out of L2.
 #include "hs_prefix.cuh"
 
 namespace hs {
@@ -12,26 +12,23 @@ using prefix::Joined;
 using prefix::Plan;
 
 constexpr int kWarps = 16;
+constexpr int kParts = 2 * kPrefixCtas;  // of a row at most
 
 __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a, int D,
                                                               int groups) {
     __shared__ Plan plan;
-    __shared__ int s_first[kPrefixCtas + 1];  // first unit of every CTA
-    __shared__ float s_factor[kPrefixCtas][32];     // of a CTA's part of a row
+    __shared__ float s_factor[kParts][32];  // of a part of a row
     __shared__ float s_tmp[kWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tile_tokens = prefix_tokens(D), tile_rows = kPrefixRows * prefix_pipes(D);
+    const int pipes = prefix_pipes(D), tile_rows = kPrefixRows * pipes;
     wait_for_previous();
-    if (warp == 0) prefix::fill_plan(plan, a, tile_rows, tile_tokens);
+    if (warp == 0) prefix::fill_plan(plan, a, tile_rows, kPrefixTokens);
     __syncthreads();
     release_next();
-    const int units = plan.unit[a.P];
-    const int ctas = prefix::working(units, a.ctas);
-    for (int c = threadIdx.x; c <= ctas; c += 32 * kWarps)
-        s_first[c] = ctas > 0 ? prefix::first_unit(units, c, ctas) : 0;
-    __syncthreads();
-    const int h = blockIdx.x / groups, all = a.B * a.S * a.G;
-    const int i = (blockIdx.x - h * groups) * 32 + lane;  // row of all batch rows
+    const int units = plan.unit[a.P], ctas = prefix::working(units, a.ctas);
+    const int slice = blockIdx.x / (a.Hkv * groups), hg = blockIdx.x - slice * a.Hkv * groups;
+    const int h = hg / groups, all = a.B * a.S * a.G;
+    const int i = (hg - h * groups) * 32 + lane;  // row of all batch rows
     const bool on = i < all;
     const prefix::Row at(a, 0, h, on ? i : 0);
     const long long out_row = ((long long)at.b * a.S + at.s) * a.Hq + at.head;
@@ -39,42 +36,40 @@ __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a
     while (p >= 0 && (plan.lo[p] > at.b || plan.hi[p] <= plan.lo[p])) --p;
     const bool some = on && p >= 0 && at.b < plan.hi[p] && plan.len[p] > 0;
     int first = 0, last = -1;  // CTAs with units of the row's tile
-    int unit0 = 0;
-    int tile_row = 0;
+    int unit0 = 0, tile_row = 0, halves = 1;
     if (some) {
         const int rows = (plan.hi[p] - plan.lo[p]) * a.S * a.G;
-        const int tiles = (plan.len[p] + tile_tokens - 1) / tile_tokens;
+        const int tiles = (plan.len[p] + kPrefixTokens - 1) / kPrefixTokens;
         const int r = i - plan.lo[p] * a.S * a.G, row_tiles = (rows + tile_rows - 1) / tile_rows;
         tile_row = r % tile_rows;
+        // Two pipelines that share the tile's rows leave a part each.
+        if (pipes == 2 && rows - (r - tile_row) <= kPrefixRows) halves = 2;
         unit0 = plan.unit[p] + (h * row_tiles + r / tile_rows) * tiles;
-        // The last CTA that begins at unit0 or before, and at the tile's last unit or before.
+        const int each = units / ctas, more = units % ctas;  // the first `more` CTAs have one more
         auto owner = [&](int unit) {
-            int lo = 0, hi = ctas;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (s_first[mid] <= unit)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            return lo;
+            const int edge = more * (each + 1);
+            return unit < edge ? unit / (each + 1) : more + (unit - edge) / each;
         };
         first = owner(unit0);
         last = owner(unit0 + tiles - 1);
     }
     // Where one CTA has the whole tile, it has written the outputs.
     const bool mine = on && (!some || last > first);
-    const int parts = some && mine ? last - first + 1 : 0;
-    // A CTA's part lies in the place of its first segment if it begins within the tile.
-    auto place = [&](int c) {
-        return (2 * (long long)c + (s_first[c] >= unit0 ? 0 : 1)) * tile_rows;
+    const int parts = some && mine ? (last - first + 1) * halves : 0;
+    // A CTA's part lies in the place of its first segment if it begins within the tile; the second
+    // pipeline's, 128 rows on.
+    auto slot = [&](int c) {
+        const int cta = first + (halves == 2 ? c >> 1 : c);
+        return 2 * cta + (prefix::first_unit(units, cta, ctas) >= unit0 ? 0 : 1);
     };
+    auto row_of = [&](int c) { return tile_row + (halves == 2 && (c & 1) ? kPrefixRows : 0); };
     // The factors of a row's parts, a warp every 16th of them: sums relative to the largest.
     float top = -INFINITY;
     bool nan = false;
     for (int c = warp; c < parts; c += kWarps) {
-        const float2 x = ld(a.part_sum + place(first + c) + tile_row);
-        const float y = x.x + log2f(x.y);
+        const float2 x = ld(a.part_sum + slot(c) * tile_rows + row_of(c));
+        const float y = x.x + log2f(x.y);  // -inf for a part without tokens
+        s_factor[c][lane] = x.x;
         top = fmaxf(top, y);
         nan = nan || !(y == y);
     }
@@ -89,10 +84,9 @@ __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a
     __syncthreads();
     float sum = 0.f;
     for (int c = warp; c < parts; c += kWarps) {
-        const float2 x = ld(a.part_sum + place(first + c) + tile_row);
-        const float f = exp2f(x.x - top);
+        const float f = exp2f(s_factor[c][lane] - top);
         s_factor[c][lane] = f;
-        sum += x.y * f;
+        sum += ld(a.part_sum + slot(c) * tile_rows + row_of(c)).y * f;
     }
     s_tmp[warp][lane] = sum;
     // before any warp writes lse, which may be the same array
@@ -103,30 +97,37 @@ __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a
     for (int w = 0; w < kWarps; ++w) sum += s_tmp[w][lane];
     if (!mine) return;
     const Joined j(some ? top + log2f(sum) : -INFINITY, other);
-    if (warp == 0 && a.lse) a.lse[out_row] = j.lse;
+    if (warp == 0 && slice == 0 && a.lse) a.lse[out_row] = j.lse;
     const float by = some ? j.mine / sum : 0.f;
-    uint16_t* out = a.out + at.at(a.out_stride);
-    const uint16_t* join = a.join + at.at(a.join_stride);
-    const int quads = D / 4;
-    const float4* part = reinterpret_cast<const float4*>(a.part) + tile_row;
-    for (int d = warp; d < quads; d += kWarps) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int c = 0; c < parts; ++c) {
-            const float f = s_factor[c][lane];
-            const float4 z = ld(part + place(first + c) * quads + (long long)d * tile_rows);
-            y = make_float4(y.x + z.x * f, y.y + z.y * f, y.z + z.z * f, y.w + z.w * f);
+    const int quads = D / 4, d = slice * kWarps + warp;
+    if (d >= quads) return;
+    const float4* part = reinterpret_cast<const float4*>(a.part) + (long long)d * tile_rows;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAhead = 6;
+    for (int c0 = 0; c0 < parts; c0 += kAhead) {
+        float4 z[kAhead];
+        float f[kAhead];
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c) {
+            f[c] = c0 + c < parts ? s_factor[c0 + c][lane] : 0.f;
+            z[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (f[c] != 0.f)  // a part without tokens is not written
+                z[c] = ld(part + (long long)slot(c0 + c) * quads * tile_rows + row_of(c0 + c));
         }
-        y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
-        if (j.other > 0.f) {
-            const uint2 z = prefix::load4(join + 4 * d, a.vec_join);
-            const float2 z0 = prefix::pair(z.x, a.fp16), z1 = prefix::pair(z.y, a.fp16);
-            y = make_float4(y.x + z0.x * j.other, y.y + z0.y * j.other, y.z + z1.x * j.other,
-                            y.w + z1.y * j.other);
-        }
-        prefix::store4(out + 4 * d, prefix::unpair(y.x, y.y, a.fp16),
-                       prefix::unpair(y.z, y.w, a.fp16), a.vec_out);
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c)
+            y = make_float4(y.x + z[c].x * f[c], y.y + z[c].y * f[c], y.z + z[c].z * f[c],
+                            y.w + z[c].w * f[c]);
     }
+    y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+    if (j.other > 0.f) {
+        const uint2 z = prefix::load4(a.join + at.at(a.join_stride) + 4 * d, a.vec_join);
+        const float2 z0 = prefix::pair(z.x, a.fp16), z1 = prefix::pair(z.y, a.fp16);
+        y = make_float4(y.x + z0.x * j.other, y.y + z0.y * j.other, y.z + z1.x * j.other,
+                        y.w + z1.y * j.other);
+    }
+    prefix::store4(a.out + at.at(a.out_stride) + 4 * d, prefix::unpair(y.x, y.y, a.fp16),
+                   prefix::unpair(y.z, y.w, a.fp16), a.vec_out);
 }
 
 // CTAs of the kernel: one an SM of the current device.
@@ -160,12 +161,14 @@ cudaError_t make_map(const hs_kv_format& f, const hs_prefix_args& x, CUtensorMap
     const cuuint64_t W = (cuuint64_t)f.item_size_bytes;
     const cuuint64_t dims[3] = {W, (cuuint64_t)x.max_seq_len, (cuuint64_t)x.num_requests};
     const cuuint64_t strides[2] = {W, W * (cuuint64_t)x.max_seq_len};
-    const cuuint32_t box[3] = {(cuuint32_t)box_bytes, (cuuint32_t)prefix_tokens(D), 1};
+    const cuuint32_t box[3] = {(cuuint32_t)box_bytes, (cuuint32_t)kPrefixTokens, 1};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r = reinterpret_cast<Encode>(fn)(
         map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(x.rows_dev), dims, strides, box,
         step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+        box_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+        : box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                          : CU_TENSOR_MAP_SWIZZLE_32B,
         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -233,8 +236,9 @@ cudaError_t launch_prefix(const hs_kv_format& f, const hs_prefix_args& x, cudaSt
         if (e != cudaSuccess) return e;
     }
     const int groups = (int)(((long long)a.B * a.S * a.G + 31) / 32);
-    return launch_chained(combine_kernel, a.Hkv * groups, 32 * kWarps, 0, 0, s, a, f.head_dim,
-                          groups);
+    const int slices = (f.head_dim / 4 + kWarps - 1) / kWarps;
+    return launch_chained(combine_kernel, a.Hkv * groups * slices, 32 * kWarps, 0, 0, s, a,
+                          f.head_dim, groups);
 }
 
 }  // namespace hs

@@ -8,17 +8,18 @@
 // prefix and many rows over a short one fill the SMs alike.  Rows whose units fell to several
 // CTAs are put together by a second kernel (combine_kernel, hs_prefix.cu).
 //
-// Warps of a CTA:
-//   converters (4)  have tiles of codes copied to a ring in shared memory (TMA), and write them
-//                   as f16 in the layout of the matrix instructions (128-byte swizzle), with
-//                   the tokens' scales.  Codes are exact in f16.
-//   softmax (4 for each of the NPIPE pipelines)   a thread has a row: it reads S, writes P over it.
-//                   The first of the four issues the pipeline's matrix instructions (tcgen05.mma: S = Q K^T,
-//                   128 rows x TOK tokens, and O += P V; accumulators and P in tensor memory): it
-//                   has nothing else to do until they are done.
-// Two pipelines (D <= 128) keep the matrix instructions busy while one of them is in its
-// softmax: they hold rows 0-127 and 128-255 of a row tile, or, where it has 128 rows or fewer, the even
-// and the odd tiles of tokens of the same rows.
+// Warps of a CTA, which hand tiles of 64 tokens to one another by barriers in shared memory:
+//   copies (1)      the codes of a K/V head, to rings in shared memory (TMA)
+//   scales (1)      the tokens' scales
+//   converters (4 for keys, 4 for values)   write codes as f16 in the layout of the matrix instructions
+//                   (128-byte swizzle).  Codes are exact in f16.
+//   matrix (1 for each of the NPIPE pipelines)   S = Q K^T (128 rows x 64 tokens) and O += P V by
+//                   tcgen05.mma, accumulators and P in tensor memory
+//   softmax (4 for each pipeline)   a thread has a row: it reads S, writes P over it
+// Two pipelines (D <= 128) hold rows 0-127 and 128-255 of a row tile, or, where it has 128 rows or fewer,
+// the even and the odd tiles of tokens of the same rows.  Each has two places for S: the scores of
+// the next tile are there when the softmax of one is done, and its product with V runs beside
+// the softmax of the next.
 //
 // Numbers: a query is scaled by a power of two into f16's range, as in hs_attend.  With z = s log2(e)
 // and v_t the V scale, the row keeps one reference r:
@@ -62,11 +63,11 @@ struct PrefixArgs {
 };
 
 constexpr int prefix_pipes(int D) { return D <= 128 ? 2 : 1; }
-constexpr int prefix_tokens(int D) { return D <= 128 ? 128 : 64; }
+constexpr int kPrefixTokens = 64;  // of a tile
 constexpr int prefix_panels(int D) { return (D + 63) / 64; }
 
 // The store as the copies see it: [R][L][W] bytes, in boxes of so many tokens and bytes of a head.
-constexpr int prefix_box(int D) { return D % 64 == 0 ? 64 : 32; }
+constexpr int prefix_box(int D) { return D % 128 == 0 ? 128 : D % 64 == 0 ? 64 : 32; }
 
 cudaError_t prefix_run_e4m3(const PrefixArgs& a, const CUtensorMap& map, int D, cudaStream_t s);
 cudaError_t prefix_run_int8(const PrefixArgs& a, const CUtensorMap& map, int D, cudaStream_t s);
@@ -78,7 +79,7 @@ namespace prefix {
 // The prefixes of a call and their units.
 struct Plan {
     int32_t lo[HS_MAX_PREFIXES], hi[HS_MAX_PREFIXES];  // batch rows
-    int32_t len[HS_MAX_PREFIXES];
+    int32_t len[HS_MAX_PREFIXES], req[HS_MAX_PREFIXES];  // tokens, and the store's request
     int32_t unit[HS_MAX_PREFIXES + 1];  // first unit; units of a prefix: [K/V head][row tile][tile]
 };
 
@@ -89,11 +90,11 @@ __device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int r
     int units = 0;
     for (int p0 = 0; p0 < a.P; p0 += 32) {
         const int p = p0 + lane;
-        int first = 0, end = 0, len = 0;
+        int first = 0, end = 0, len = 0, r = 0;
         if (p < a.P) {
             first = min(max(ld(a.starts + p), 0), a.B);
             end = max(min(max(ld(a.starts + p + 1), 0), a.B), first);
-            const int r = ld(a.prefix + p);
+            r = ld(a.prefix + p);
             len = r < 0 || r >= a.R ? 0 : min(max(ld(a.lens + p), 0), a.L);
         }
         int most = max(end, taken);  // the largest end up to this prefix
@@ -119,6 +120,7 @@ __device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int r
             plan.lo[p] = lo;
             plan.hi[p] = hi;
             plan.len[p] = len;
+            plan.req[p] = r;
             plan.unit[p] = units + sum - mine;
         }
         units += __shfl_sync(0xffffffffu, sum, 31);
@@ -162,30 +164,40 @@ __device__ __forceinline__ uint32_t shared_address(const void* p) {
 __device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_n(uint32_t bar, int n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+// True once the phase of this parity is over; the thread sleeps for up to 20 us before it says no.
+// (Without the time it comes back at once, and the waiting warps' loops take half of the others' issue
+// slots.)
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(done)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(20000)
         : "memory");
     return done != 0;
 }
 
-// Waits for the phase of this parity, with a limit that no wait comes near (a tenth of a second
-// at the least): then, or once another thread has given up, the CTA goes on without waiting and
-// its outputs become NaN.
+// Waits for the phase of this parity, with a limit that no wait comes near (about a second): then,
+// or once another thread has given up, the CTA goes on without waiting and its outputs become
+// NaN.
+constexpr int kTries = 1 << 16;
 __device__ __forceinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
 #pragma unroll 1
-    for (int i = 0; i < 1 << 22; ++i)
+    for (int i = 0; i < kTries; ++i)
         if (try_wait(bar, parity) || *gave_up) return;
     *gave_up = 1;
 }
 // The same where a thread must not go on, whoever has given up.
 __device__ __forceinline__ void wait_still(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
-    for (int i = 0; i < 1 << 22 && !try_wait(bar, parity); ++i) {
+    for (int i = 0; i < kTries && !try_wait(bar, parity); ++i) {
     }
 }
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
@@ -400,11 +412,18 @@ struct Joined {
 // The largest p_t v_t gets 2^kTop when the reference is set, and may grow by 2^kRoom from there.
 constexpr float kTop = 9.5f, kRoom = 6.f;
 
+// The product with V that a pipeline issued last; none in the first tile of a segment.
+struct Product {
+    uint32_t done, parity;
+    bool none;
+    volatile int* gave_up;
+};
+
 // The reference moves to `want`: O and l with it.  The whole warp calls it.
 template <int D>
-__device__ __forceinline__ void move_reference(uint32_t o_col, float want, bool first, float& ref,
-                                               float& l) {
-    if (first) {
+__device__ __forceinline__ void move_reference(uint32_t o_col, float want, const Product& before,
+                                               float& ref, float& l) {
+    if (before.none) {
         ref = want;
         return;
     }
@@ -413,6 +432,8 @@ __device__ __forceinline__ void move_reference(uint32_t o_col, float want, bool 
     const float by = grow ? exp2_fast(ref - want) : 1.f;
     l *= by;
     if (grow) ref = want;
+    wait(before.done, before.parity, before.gave_up);
+    fence_after();
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         uint32_t x[32];
@@ -428,7 +449,7 @@ __device__ __forceinline__ void move_reference(uint32_t o_col, float want, bool 
 template <int TOK, int D>
 __device__ __forceinline__ void softmax_any(uint32_t s_col, uint32_t o_col, float f,
                                             const float* s_k, const float* s_v, const float* s_log,
-                                            int live, bool first, float& ref, float& l) {
+                                            int live, const Product& before, float& ref, float& l) {
     // The largest score, and the largest of score + log2(V scale).
     float top = -INFINITY, most = -INFINITY;
 #pragma unroll 1
@@ -451,7 +472,7 @@ __device__ __forceinline__ void softmax_any(uint32_t s_col, uint32_t o_col, floa
             }
         }
     }
-    move_reference<D>(o_col, fmaxf(most - kTop, top - 100.f), first, ref, l);
+    move_reference<D>(o_col, fmaxf(most - kTop, top - 100.f), before, ref, l);
 #pragma unroll 1
     for (int c = 0; c < TOK; c += 32) {
         uint32_t x[32], y[16];
@@ -495,36 +516,23 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
     return d;
 }
 
-__device__ __forceinline__ void load_columns(uint32_t (&x)[16], uint32_t at) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15}, [%16];"
-        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
-          "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
-          "=r"(x[14]), "=r"(x[15])
-        : "r"(at)
-        : "memory");
-}
-__device__ __forceinline__ void loaded(uint32_t (&x)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
-}
-__device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[8]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at),
-        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-        : "memory");
-}
-
 // The same for whole tiles whose scales are equal in each 16 tokens, V scales of 2^-60 or more
 // and K scales >= 0: the scales leave the loops.  p_t v_t comes out of the exponential at
 // once, 2^(z_t + log2 v - r), and l takes the sum of 16 by 1 / v.
+template <int TOK>
+struct Even {  // of 16 tokens each: factor of the products, log2 of the V scale, its reciprocal
+    float k[TOK / 16], log[TOK / 16], inverse[TOK / 16];
+    __device__ __forceinline__ Even(const float4* s_even, float f) {
+#pragma unroll
+        for (int i = 0; i < TOK / 16; ++i) {
+            const float4 x = s_even[i];
+            k[i] = x.x * f, log[i] = x.y, inverse[i] = x.z;
+        }
+    }
+};
 template <int TOK, int D>
-__device__ __forceinline__ void softmax_even(uint32_t s_col, uint32_t o_col, float f,
-                                             const float* s_k, const float2* s_even, bool first,
-                                             float& ref, float& l) {
-    // Tensor memory answers after some 250 cycles: all of S is asked for at once.
+__device__ __forceinline__ void softmax_even(uint32_t s_col, uint32_t o_col, const Even<TOK>& scale,
+                                             const Product& before, float& ref, float& l) {
     constexpr int kSteps = TOK / 32;
     uint32_t x[kSteps][32];
 #pragma unroll
@@ -533,29 +541,24 @@ __device__ __forceinline__ void softmax_even(uint32_t s_col, uint32_t o_col, flo
     for (int c = 0; c < kSteps; ++c) loaded(x[c]);
     float most = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < kSteps; ++c) {
+    for (int c = 0; c < TOK / 16; ++c) {
+        const uint32_t* z = &x[c / 2][c % 2 * 16];
+        float m[4];  // four chains
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t* z = &x[c][16 * h];
-            float m[4];  // four chains
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                m[k] = fmaxf(fmaxf(__uint_as_float(z[k]), __uint_as_float(z[k + 4])),
-                             fmaxf(__uint_as_float(z[k + 8]), __uint_as_float(z[k + 12])));
-            m[0] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-            most = fmaxf(most, fmaf(m[0], s_k[c * 32 + h * 16] * f, s_even[c * 2 + h].x));
-        }
+        for (int k = 0; k < 4; ++k)
+            m[k] = fmaxf(fmaxf(__uint_as_float(z[k]), __uint_as_float(z[k + 4])),
+                         fmaxf(__uint_as_float(z[k + 8]), __uint_as_float(z[k + 12])));
+        m[0] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        most = fmaxf(most, fmaf(m[0], scale.k[c], scale.log[c]));
     }
-    move_reference<D>(o_col, most - kTop, first, ref, l);
+    move_reference<D>(o_col, most - kTop, before, ref, l);
 #pragma unroll
     for (int c = 0; c < kSteps; ++c) {
         uint32_t w[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int at = c * 32 + 16 * h;
-            const float k0 = s_k[at] * f;
-            const float2 v = s_even[at / 16];
-            const float2 kk = make_float2(k0, k0), off = make_float2(v.x - ref, v.x - ref);
+            const float k0 = scale.k[2 * c + h], o0 = scale.log[2 * c + h] - ref;
+            const float2 kk = make_float2(k0, k0), off = make_float2(o0, o0);
             float2 sum[2] = {};
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
@@ -568,7 +571,7 @@ __device__ __forceinline__ void softmax_even(uint32_t s_col, uint32_t o_col, flo
                 w[8 * h + k / 2] = pack_half2(e.x, e.y);
             }
             sum[0] = add_pair(sum[0], sum[1]);
-            l = fmaf(sum[0].x + sum[0].y, v.y, l);
+            l = fmaf(sum[0].x + sum[0].y, scale.inverse[2 * c + h], l);
         }
         store_columns(s_col + c * 16, w);
     }
@@ -576,32 +579,39 @@ __device__ __forceinline__ void softmax_even(uint32_t s_col, uint32_t o_col, flo
 
 // ---- the kernel -------------------------------------------------------------------
 
+// Tiles of f16 in place, for keys and for values each: as many as leave room for rings of three.
+constexpr int prefix_pool(int D) { return D == 256 ? 1 : D == 192 ? 2 : D > 64 ? 3 : 4; }
+
 template <int D>
 struct Shape {
-    static constexpr int kPipes = prefix_pipes(D), kTok = prefix_tokens(D);
+    static constexpr int kPipes = prefix_pipes(D), kTok = kPrefixTokens;
     static constexpr int kPanels = prefix_panels(D);
     static constexpr int kRows = kPrefixRows * kPipes;          // of a tile
     static constexpr int kQ = kPanels * kPrefixRows * 128;      // bytes of a pipeline's queries
     static constexpr int kTile = kPanels * kTok * 128;          // of a tile's keys or values
-    static constexpr int kKeys = 1, kValues = 2;                // tiles of f16 in place
     static constexpr int kScales = 4;                           // scales of tiles in place
-    static constexpr int kSoftmax = 4 * kPipes, kConvert = 4;   // warps
-    static constexpr int kThreads = 32 * (kSoftmax + kConvert);
+    static constexpr int kSoftmax = 4 * kPipes, kConvert = 4;   // warps; kConvert of keys, and of values
+    static constexpr int kControl = kSoftmax + 2 * kConvert;    // first of 4: matrix (2), copies, scales
+    static constexpr int kThreads = 32 * (kControl + 4);
     static constexpr int kBox = prefix_box(D);
     static constexpr int kRaw = kTok * D;                       // bytes of a tile's codes, K or V
-    static constexpr int kF16 = kPipes * kQ + (kKeys + kValues) * kTile;
-    static constexpr int kFit = (213 * 1024 - kF16) / kRaw;
-    static constexpr int kRing = kFit < 8 ? kFit : 8;           // of them in the ring
-    static_assert(kRing >= 3, "a tile and a half on their way");
-    static constexpr int kSmem = kF16 + kRing * kRaw + 1024;    // aligned by the kernel
+    static constexpr int kPool = prefix_pool(D);
+    static constexpr int kF16 = kPipes * kQ + 2 * kPool * kTile;
+    static constexpr int kFit = (213 * 1024 - kF16) / (2 * kRaw);
+    static constexpr int kRing = kFit < 8 ? kFit : 8;           // tiles in the rings
+    static_assert(kRing >= 2, "one is used, one on its way");
+    static constexpr int kSmem = kF16 + 2 * kRing * kRaw + 1024;  // aligned by the kernel
     static constexpr int kChunks = kTok * D / 16 / (32 * kConvert);  // of 16 codes a converter
-    // Registers of a thread: what the block is launched with, then each role's share (with two
-    // pipelines).  A quarter of an SM holds one converter and a warp of each pipeline.
-    static constexpr int kLaunchRegs = 168, kSoftmaxRegs = D <= 64 ? 208 : 200;
-    static constexpr int kConvertRegs = D <= 64 ? 88 : 104;
-    static_assert(2 * kSoftmaxRegs + kConvertRegs <= 3 * kLaunchRegs,
+    // Registers of a thread: what the block is launched with, then each role's share.  A quarter of an SM
+    // holds a warp of each pipeline, two converters and one of the others.
+    static constexpr int kLaunchRegs = kPipes == 2 ? 96 : 128;
+    static constexpr int kSoftmaxRegs = kPipes == 2 ? 128 : 208;
+    static constexpr int kConvertRegs = kPipes == 2 ? 72 : 104, kControlRegs = kPipes == 2 ? 80 : 96;
+    static_assert(kPipes * kSoftmaxRegs + 2 * kConvertRegs + kControlRegs <=
+                      (kPipes + 3) * kLaunchRegs,
                   "a share beyond what was launched would wait for ever");
-    static constexpr int kOut = kPipes * kTok;                  // tensor-memory column of O
+    static constexpr int kOut = 2 * kPipes * kTok;              // tensor-memory column of O
+    static_assert(kOut + kPipes * D <= 512, "tensor memory");
 };
 
 // The outputs of a segment, and the partial ones of a segment that is not a whole tile: called by
@@ -615,7 +625,8 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
     constexpr int NP = X::kPipes, kQuads = D / 4;
     const Segment g(plan, a, from, u1, X::kRows, X::kTok);
     const bool both = NP == 2 && g.rows - g.row0 > kPrefixRows;
-    const int tile_row = (both ? p * kPrefixRows : 0) + row, r = g.row0 + tile_row;
+    const bool whole = g.n == g.tiles;
+    const int r = g.row0 + (both ? p * kPrefixRows : 0) + row;
     const bool on = r < g.rows;
     const Row at(a, plan.lo[g.p], g.h, on ? r : g.row0);
     if (done) {
@@ -623,14 +634,17 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
         fence_after();
     }
     if (*gave_up) l = NAN;
-    // Two halves of the tokens: the second pipeline's go through the queries' memory.
+    const bool alive = r - (row & 31) < g.rows;  // the warp has rows
+    // Two halves of the tokens: of a whole tile, the second pipeline's go through the queries' memory;
+    // else each is a part of its own.
     float4* const second = reinterpret_cast<float4*>(smem) + row * kQuads;
     float mine_by = 1.f, second_by = 0.f;
-    if (NP == 2 && !both) {
+    const bool join = NP == 2 && !both && whole;
+    if (join) {
         asm volatile("bar.sync 1, 256;" ::: "memory");  // both are done with the queries
         if (p == 1) {
             s_sum[row] = make_float2(ref, l);
-            if (done) {
+            if (done && alive) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t x[32];
@@ -654,8 +668,7 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
             ref = top;
         }
     }
-    if (NP == 1 || both || p == 0) {
-        const bool whole = g.n == g.tiles;
+    if (alive && (!join || p == 0)) {
         const long long out_row = ((long long)at.b * a.S + at.s) * a.Hq + at.head;
         float other = 0.f;
         if (whole) {
@@ -667,10 +680,13 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
             if (on && a.lse) a.lse[out_row] = j.lse;
         }
         const long long slot = 2 * (long long)blockIdx.x + (from == u0 ? 0 : 1);
+        const int tile_row = p * kPrefixRows + row;
         float4* part = reinterpret_cast<float4*>(a.part) + slot * kQuads * X::kRows + tile_row;
-        if (!whole && on) a.part_sum[slot * X::kRows + tile_row] = make_float2(ref, l);
+        // without a tile: nothing, whatever the reference
+        if (!whole && on) a.part_sum[slot * X::kRows + tile_row] = make_float2(done ? ref : -INFINITY, l);
+        if (!whole && !done) return;
         uint16_t* out = a.out + at.at(a.out_stride);
-        const uint16_t* join = a.join + at.at(a.join_stride);
+        const uint16_t* others = a.join + at.at(a.join_stride);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t x[32];
@@ -681,7 +697,7 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
                 float y[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) y[m] = __uint_as_float(x[4 * k + m]) * mine_by;
-                if (NP == 2 && !both && g.n > 1) {
+                if (join && g.n > 1) {
                     const float4 z = second[(c / 4 + k + row) % kQuads];
                     y[0] += z.x * second_by, y[1] += z.y * second_by;
                     y[2] += z.z * second_by, y[3] += z.w * second_by;
@@ -693,7 +709,7 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
                     continue;
                 }
                 if (other > 0.f) {
-                    const uint2 z = load4(join + d, a.vec_join);
+                    const uint2 z = load4(others + d, a.vec_join);
                     const float2 z0 = pair(z.x, a.fp16), z1 = pair(z.y, a.fp16);
                     y[0] += z0.x * other, y[1] += z0.y * other;
                     y[2] += z1.x * other, y[3] += z1.y * other;
@@ -702,27 +718,20 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
             }
         }
     }
-    if (NP == 2 && !both) asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (join) asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-// Barriers in shared memory: what the matrix instructions and the copies signal.
+// Barriers in shared memory.
 enum Bar : int {
-    kSFull = 0, kOFull = 2,   // [pipe]
-    kKEmpty = 4, kVEmpty = 5, // [kKeys], [kValues]
-    kDone = 7,
-    kRawFull = 8,             // [kRing], by the copies
-    kBars = 16
+    kQFull = 0,      // [pipe] the queries of a segment
+    kSFull = 2,      // [pipe][place] scores, by the matrix instructions
+    kPFull = 6,      // [pipe][place]
+    kPvDone = 10,    // [pipe] a product with V
+    kKFull = 12, kVFull = 16, kKEmpty = 20, kVEmpty = 24,   // [kPool] f16 tiles
+    kRawFull = 28, kRawEmpty = 44,                          // [keys, values][8] codes
+    kScFull = 60, kScEmpty = 64,                            // [kScales]
+    kDone = 68, kBars = 69
 };
-
-// Barriers of the SM between the four converters and a pipeline's four warps: a tile's keys (and
-// scales) are written; its values are written, and P.  They let a warp go on with loads under
-// way, where an arrival at a barrier in shared memory waits for these.
-__device__ __forceinline__ int keys_barrier(int stage, int p) { return 2 + 2 * stage + p; }
-__device__ __forceinline__ int values_barrier(int stage, int p) { return 6 + 2 * stage + p; }
-__device__ __forceinline__ void meet(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void meet_later(int id) {
-    asm volatile("bar.arrive %0, 256;" ::"r"(id) : "memory");
-}
 
 template <int CODE, int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
@@ -733,8 +742,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     __shared__ Plan plan;
     __shared__ __align__(16) float s_k[X::kScales][TOK], s_v[X::kScales][TOK];
     __shared__ __align__(16) float s_log[X::kScales][TOK];  // log2 of the V scale
-    __shared__ __align__(8) float2 s_even[X::kScales][TOK / 16];  // of 16 tokens: log2, 1 / V scale
-    __shared__ __align__(16) int s_small[X::kScales][X::kConvert];  // a V scale below 2^-60
+    __shared__ __align__(16) float4 s_even[X::kScales][TOK / 16];  // of 16 tokens: K, log2 V, 1 / V
+    __shared__ int s_small[X::kScales];                     // a V scale is below 2^-60
     __shared__ __align__(8) unsigned long long s_bar[kBars];
     __shared__ float2 s_sum[kPrefixRows];  // of the second pipeline
     __shared__ uint32_t s_tmem;
@@ -742,23 +751,34 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* const smem = smem_raw + (-(int)shared_address(smem_raw) & 1023);
     const uint32_t q_at = shared_address(smem), k_at = q_at + NP * X::kQ;
-    const uint32_t v_at = k_at + X::kKeys * X::kTile, raw_at = v_at + X::kValues * X::kTile;
+    const uint32_t v_at = k_at + X::kPool * X::kTile, raw_at = v_at + X::kPool * X::kTile;
     const uint32_t bars = shared_address(s_bar);
     auto bar = [&](int i) { return (uint32_t)(bars + 8 * i); };
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            barrier_init(bar(kSFull + i), 1);
-            barrier_init(bar(kOFull + i), 1);
+            barrier_init(bar(kQFull + i), 4);
+            barrier_init(bar(kPvDone + i), 1);
         }
-        for (int i = 0; i < X::kKeys; ++i) barrier_init(bar(kKEmpty + i), NP);
-        for (int i = 0; i < X::kValues; ++i) barrier_init(bar(kVEmpty + i), NP);
-        for (int i = 0; i < X::kRing; ++i) barrier_init(bar(kRawFull + i), 1);
+        for (int i = 0; i < 4; ++i) {
+            barrier_init(bar(kSFull + i), 1);
+            barrier_init(bar(kPFull + i), 4);
+            barrier_init(bar(kKFull + i), X::kConvert);
+            barrier_init(bar(kVFull + i), X::kConvert);
+            barrier_init(bar(kKEmpty + i), NP);
+            barrier_init(bar(kVEmpty + i), NP);
+            barrier_init(bar(kScFull + i), 1);
+            barrier_init(bar(kScEmpty + i), X::kSoftmax);
+        }
+        for (int i = 0; i < 16; ++i) {
+            barrier_init(bar(kRawFull + i), 1);
+            barrier_init(bar(kRawEmpty + i), X::kConvert);
+        }
         barrier_init(bar(kDone), NP);
         s_gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
+    if (warp == X::kControl) {
         // One CTA an SM; waits for what else holds tensor memory, never the other way round.
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          shared_address(&s_tmem))
@@ -767,7 +787,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         fence_before();
     }
     wait_for_previous();
-    if (warp == 1) fill_plan(plan, a, X::kRows, TOK);
+    if (warp == X::kControl + 1) fill_plan(plan, a, X::kRows, TOK);
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
@@ -776,267 +796,336 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const bool works = (int)blockIdx.x < ctas;
     const int u0 = works ? first_unit(units, blockIdx.x, ctas) : 0;
     const int u1 = works ? first_unit(units, blockIdx.x + 1, ctas) : 0;
+    const int count = u1 - u0;  // tiles of this CTA, numbered from 0
     volatile int* const gave_up = &s_gave_up;
 
-    if (warp >= X::kSoftmax) {
-        if constexpr (NP == 2)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kConvertRegs));
-        // ---- converters ----------------------------------------------------------
-        const int t = tid - 32 * X::kSoftmax;
-        constexpr int kRowChunks = D / 16;  // 16-byte pieces of a token
-        // Units in order: one walk for the copies (thread 0), one for what is converted.
-        struct Walk {
-            int from, tile, end, first, len, h, r;
-            bool both;
-        };
-        auto next = [&](Walk& w) {  // false past the last
-            if (++w.tile < w.end) return true;
-            if (w.from >= u1) return false;
-            const Segment g(plan, a, w.from, u1, X::kRows, TOK);
-            w.from += g.n;
-            w.tile = w.first = g.tile0;
-            w.end = g.tile0 + g.n;
-            w.len = plan.len[g.p];
-            w.both = NP == 2 && g.rows - g.row0 > kPrefixRows;
-            w.h = g.h;
-            w.r = ld(a.prefix + g.p);
-            return true;
-        };
-        Walk copy = {u0, 0, 0, 0, 0, 0, 0, false};
-        int copies = 0;  // of K and V tiles so far
-        auto start_copy = [&]() {  // thread 0
-            if (copies % 2 == 0 && !next(copy)) return;
-            const int slot = copies % X::kRing;
-            const uint32_t full = bar(kRawFull + slot);
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
-                         "n"(X::kRaw)
-                         : "memory");
-            const int x = (copy.h + (copies % 2 == 0 ? 0 : a.Hkv)) * D;
+    if (warp >= X::kControl) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kControlRegs));
+        const int role = warp - X::kControl;
+        if (role < NP) {
+            // ---- matrix instructions: the whole warp goes along, one lane issues ---------------
+            constexpr uint32_t kScores = instruction(TOK, false), kValues = instruction(D, true);
+            const int p = role;
+            const bool leader = elected();
+            const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+            uint32_t done = 0, segments = 0;  // items and segments before
+            for (int from = u0; from < u1;) {
+                const Segment g(plan, a, from, u1, X::kRows, TOK);
+                const int n = __shfl_sync(0xffffffffu, g.n, 0);
+                const bool both =
+                    __shfl_sync(0xffffffffu, (int)(NP == 2 && g.rows - g.row0 > kPrefixRows), 0);
+                const bool shared = NP == 2 && !both;  // the pipelines take turns
+                const int items = shared ? (n + 1 - p) / 2 : n, first = from - u0 + (shared ? p : 0);
+                const int users = both ? 2 : 1;
+                if (items > 0) wait(bar(kQFull + p), segments++ & 1, gave_up);
+                for (int k = 0; k < items + 2; ++k) {
+                    if (k >= 2) {  // O += P V of two items before
+                        const uint32_t it = done + k - 2;
+                        const int t = first + (shared ? 2 : 1) * (k - 2);
+                        const int place = t % X::kPool;
+                        wait(bar(kVFull) + 8 * place, t / X::kPool & 1, gave_up);
+                        wait(bar(kPFull + 2 * p) + 8 * (it & 1), it >> 1 & 1, gave_up);
+                        fence_shared();
+                        fence_after();
+                        const uint64_t b = matrix(v_at + place * X::kTile, TOK * 128);
+                        const uint32_t s = base + (2 * p + (it & 1)) * TOK;
+                        if (leader) {
 #pragma unroll
-            for (int i = 0; i < D / X::kBox; ++i)
-                asm volatile(
-                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::"
-                    "bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(raw_at + slot * X::kRaw +
-                                                                  i * TOK * X::kBox),
-                    "l"(&map), "r"(full), "r"(x + i * X::kBox), "r"(copy.tile * TOK), "r"(copy.r)
-                    : "memory");
-            ++copies;
-        };
-        if (t == 0) {
-            for (int i = 0; i < X::kRing; ++i)
-                if (copies == i) start_copy();  // while there are units
-        }
-        Walk walk = {u0, 0, 0, 0, 0, 0, 0, false};
-        float k_scale = 0.f, v_scale = 0.f;
-        auto load_scales = [&]() {  // of the unit that the walk is at
-            const int token = walk.tile * TOK + t;
-            k_scale = v_scale = 0.f;
-            if (t < TOK && token < walk.len) {
-                const float* p = a.scales +
-                                 ((long long)walk.r * a.NB + a.block.of(token)) * 2 * a.Hkv + walk.h;
-                k_scale = ld(p);
-                v_scale = ld(p + a.Hkv);
-            }
-        };
-        // Codes of the ring's tile `which` as f16; those of tokens from `live` on as zeros.  Eight lanes
-        // take one piece of eight rows: what they read and store together lies in
-        // different banks.
-        auto convert = [&](int which, uint32_t to, int live) {
-            const int slot = which % X::kRing;
-            const uint32_t raw = raw_at + slot * X::kRaw;
-            wait(bar(kRawFull + slot), which / X::kRing & 1, gave_up);
-            uint4 x[X::kChunks];
+                            for (int i = 0; i < TOK / 16; ++i)  // 16 tokens are 16 rows of 128 bytes
+                                multiply_tensor(base + X::kOut + p * D, s + 8 * i,
+                                                b + i * (2048 >> 4), kValues, i > 0 || k > 2);
+                            for (int u = users; u <= NP; ++u) commit(bar(kVEmpty) + 8 * place);
+                            commit(bar(kPvDone + p));
+                        }
+                        __syncwarp();
+                    }
+                    if (k < items) {  // S = Q K^T, where P of two items before has been
+                        const uint32_t it = done + k;
+                        const int t = first + (shared ? 2 : 1) * k;
+                        const int place = t % X::kPool;
+                        wait(bar(kKFull) + 8 * place, t / X::kPool & 1, gave_up);
+                        fence_shared();
+                        fence_after();
+                        const uint64_t q = matrix(q_at + p * X::kQ, 16);
+                        const uint64_t key = matrix(k_at + place * X::kTile, 16);
+                        const uint32_t s = base + (2 * p + (it & 1)) * TOK;
+                        if (leader) {
 #pragma unroll
-            for (int c = 0; c < X::kChunks; ++c) {
-                const int i = c * 32 * X::kConvert + t;
-                const int row = i / (8 * kRowChunks) * 8 + i % 8, piece = i / 8 % kRowChunks;
-                constexpr int kIn = X::kBox / 16;  // pieces of a box's row
-                const int swizzle = X::kBox == 64 ? row >> 1 & 3 : row >> 2 & 1;
-                const uint32_t at = raw + piece / kIn * (TOK * X::kBox) + row * X::kBox +
-                                    ((piece % kIn ^ swizzle) << 4);
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(x[c].x), "=r"(x[c].y), "=r"(x[c].z), "=r"(x[c].w)
-                             : "r"(at)
-                             : "memory");
-            }
-            asm volatile("bar.sync 12, 128;" ::: "memory");  // all have read it
-            if (t == 0) start_copy();
-#pragma unroll
-            for (int c = 0; c < X::kChunks; ++c) {
-                const int i = c * 32 * X::kConvert + t;
-                const int row = i / (8 * kRowChunks) * 8 + i % 8, piece = i / 8 % kRowChunks;
-                if (row >= live) x[c] = make_uint4(0, 0, 0, 0);
-                uint32_t y[8];
-                halves<CODE>(x[c].x, y[0], y[1]);
-                halves<CODE>(x[c].y, y[2], y[3]);
-                halves<CODE>(x[c].z, y[4], y[5]);
-                halves<CODE>(x[c].w, y[6], y[7]);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 to + place(row, piece * 16, TOK * 128)),
-                             "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                             : "memory");
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 to + place(row, piece * 16 + 8, TOK * 128)),
-                             "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
-                             : "memory");
-            }
-        };
-        if (next(walk)) load_scales();
-        const int n = u1 - u0;
-        for (int i = 0; i < n; ++i) {
-            const int ks = i % X::kKeys, vs = i % X::kValues, sc = i & 3;
-            const int live = walk.len - walk.tile * TOK;
-            // The pipelines that read this tile.
-            const bool reads[2] = {NP == 1 || walk.both || (walk.tile - walk.first) % 2 == 0,
-                                   NP == 2 && (walk.both || (walk.tile - walk.first) % 2 == 1)};
-            // The scales' place is free with the keys': the scores of a tile come behind the softmax
-            // of the tile before (both pipelines) or of two before (each its own), and
-            // scales are kept for four.
-            wait(bar(kKEmpty + ks), (i / X::kKeys & 1) ^ 1, gave_up);
-            const float lg = log2f(v_scale);
-            if (t < TOK) {
-                s_k[sc][t] = k_scale * a.k_sign;
-                s_v[sc][t] = v_scale;
-                s_log[sc][t] = lg;
-                if (t % 16 == 0) s_even[sc][t / 16] = make_float2(lg, __frcp_rn(v_scale));
-            }
-            const bool small = __any_sync(0xffffffffu, t < TOK && v_scale < 0x1p-60f);
-            if (lane == 0) s_small[sc][warp - X::kSoftmax] = small;
-            convert(2 * i, k_at + ks * X::kTile, live);
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-                if (reads[p]) meet_later(keys_barrier(0, p));
-            if (next(walk)) load_scales();  // of the next tile
-            wait(bar(kVEmpty + vs), (i / X::kValues & 1) ^ 1, gave_up);
-            convert(2 * i + 1, v_at + vs * X::kTile, live);
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-                if (reads[p]) meet_later(values_barrier(vs, p));
-        }
-        // No copy is under way when the CTA ends, even if a wait was given up.
-        if (t == 0)
-            for (int i = max(0, copies - X::kRing); i < copies; ++i)
-                wait_still(bar(kRawFull + i % X::kRing), i / X::kRing & 1);
-    } else {
-        if constexpr (NP == 2)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kSoftmaxRegs));
-        // ---- softmax ---------------------------------------------------------------
-        const int p = warp / 4, row = tid - p * kPrefixRows;
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-        const uint32_t s_col = lanes + p * TOK, o_col = lanes + X::kOut + p * D;
-        uint32_t s_done = 0, o_done = 0;
-        constexpr uint32_t kScores = instruction(TOK, false), kValues = instruction(D, true);
-        const bool issuer = (warp & 3) == 0, leader = issuer && elected();
-        // S = Q K^T of the CTA's tile t.
-        auto scores = [&](int t, int users) {
-            const int stage = t % X::kKeys;
-            meet(keys_barrier(0, p));
-            if (!issuer) return;
-            fence_shared();
-            fence_after();
-            const uint64_t q = matrix(q_at + p * X::kQ, 16);
-            const uint64_t key = matrix(k_at + stage * X::kTile, 16);
-            if (leader) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int panel = k / 4, in = k % 4 * 32;
-                    multiply(tmem + p * TOK, q + ((panel * kPrefixRows * 128 + in) >> 4),
-                             key + ((panel * TOK * 128 + in) >> 4), kScores, k > 0);
+                            for (int i = 0; i < D / 16; ++i) {
+                                const int panel = i / 4, in = i % 4 * 32;
+                                multiply(s, q + ((panel * kPrefixRows * 128 + in) >> 4),
+                                         key + ((panel * TOK * 128 + in) >> 4), kScores, i > 0);
+                            }
+                            commit(bar(kSFull + 2 * p) + 8 * (it & 1));
+                            for (int u = users; u <= NP; ++u) commit(bar(kKEmpty) + 8 * place);
+                        }
+                        __syncwarp();
+                    }
                 }
-                commit(bar(kSFull + p));
-                for (int i = users; i <= NP; ++i) commit(bar(kKEmpty + stage));
+                done += items;
+                from += n;
+            }
+            if (leader) commit(bar(kDone));
+            __syncwarp();
+            wait_still(bar(kDone), 0);
+        } else if (role == 2) {
+            // ---- copies ------------------------------------------------------------------
+            const bool leader = elected();
+            int tile = 0, end = 0, x = 0, r = 0, slot = 0;
+            uint32_t free = 1;  // phase of the ring's places
+            for (int i = 0; i < count; ++i) {
+                if (++tile >= end) {
+                    const Segment g(plan, a, u0 + i, u1, X::kRows, TOK);
+                    tile = g.tile0;
+                    end = g.tile0 + g.n;
+                    x = g.h * D;
+                    r = plan.req[g.p];
+                }
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {  // keys, values
+                    wait(bar(kRawEmpty + 8 * side) + 8 * slot, free, gave_up);
+                    const uint32_t full = bar(kRawFull + 8 * side) + 8 * slot;
+                    if (leader) {
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                                         full),
+                                     "n"(X::kRaw)
+                                     : "memory");
+#pragma unroll
+                        for (int k = 0; k < D / X::kBox; ++k)
+                            asm volatile(
+                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::"
+                                "complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+                                    raw_at + (side * X::kRing + slot) * X::kRaw +
+                                    k * TOK * X::kBox),
+                                "l"(&map), "r"(full), "r"(x + side * a.Hkv * D + k * X::kBox),
+                                "r"(tile * TOK), "r"(r)
+                                : "memory");
+                    }
+                    __syncwarp();
+                }
+                if (++slot == X::kRing) slot = 0, free ^= 1;
+            }
+            // No copy is under way when the CTA ends, even if a wait was given up.
+            for (int i = max(0, count - X::kRing); i < count; ++i)
+                for (int side = 0; side < 2; ++side)
+                    wait_still(bar(kRawFull + 8 * side) + 8 * (i % X::kRing), i / X::kRing & 1);
+        } else if (role == 3) {
+            // ---- scales --------------------------------------------------------------------
+            // A lane has two tokens, of two tiles ahead.
+            int tile = 0, end = 0, len = 0;
+            const float* scales = nullptr;
+            float k[2][2], v[2][2];  // [tile][token]
+            auto load = [&](int i, float (&k)[2], float (&v)[2]) {
+                if (i >= count) return;
+                if (++tile >= end) {
+                    const Segment g(plan, a, u0 + i, u1, X::kRows, TOK);
+                    tile = g.tile0;
+                    end = g.tile0 + g.n;
+                    len = plan.len[g.p];
+                    scales = a.scales + (long long)plan.req[g.p] * a.NB * 2 * a.Hkv + g.h;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int token = tile * TOK + 32 * h + lane;
+                    k[h] = v[h] = 0.f;
+                    if (token < len) {
+                        const float* at = scales + (long long)a.block.of(token) * 2 * a.Hkv;
+                        k[h] = ld(at);
+                        v[h] = ld(at + a.Hkv);
+                    }
+                }
+            };
+            auto put = [&](int i, const float (&k)[2], const float (&v)[2]) {
+                const int sc = i % X::kScales;
+                wait(bar(kScEmpty) + 8 * sc, (i / X::kScales & 1) ^ 1, gave_up);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = 32 * h + lane;
+                    const float lg = log2f(v[h]);
+                    s_k[sc][t] = k[h] * a.k_sign;
+                    s_v[sc][t] = v[h];
+                    s_log[sc][t] = lg;
+                    if (t % 16 == 0)
+                        s_even[sc][t / 16] = make_float4(k[h] * a.k_sign, lg, __frcp_rn(v[h]), 0.f);
+                }
+                const bool small = __any_sync(0xffffffffu, fminf(v[0], v[1]) < 0x1p-60f);
+                __syncwarp();
+                if (lane == 0) {
+                    s_small[sc] = small;
+                    arrive(bar(kScFull) + 8 * sc);
+                }
+            };
+            load(0, k[0], v[0]);
+            load(1, k[1], v[1]);
+            for (int i = 0; i < count; i += 2) {
+                put(i, k[0], v[0]);
+                load(i + 2, k[0], v[0]);
+                if (i + 1 == count) break;
+                put(i + 1, k[1], v[1]);
+                load(i + 3, k[1], v[1]);
+            }
+        }
+    } else if (warp >= X::kSoftmax) {
+        // ---- converters ------------------------------------------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kConvertRegs));
+        const int side = warp >= X::kSoftmax + X::kConvert;  // 0: keys, 1: values
+        const int t = tid % (32 * X::kConvert);
+        constexpr int kRowChunks = D / 16;  // 16-byte pieces of a token
+        const uint32_t raws = raw_at + side * X::kRing * X::kRaw;
+        const uint32_t tiles = side ? v_at : k_at;
+        int tile = 0, end = 0, len = 0, slot = 0, place_of = 0;
+        uint32_t full = 0, free = 1;  // phases of the ring's and of the f16 tiles' places
+        for (int i = 0; i < count; ++i) {
+            if (++tile >= end) {
+                const Segment g(plan, a, u0 + i, u1, X::kRows, TOK);
+                tile = g.tile0;
+                end = g.tile0 + g.n;
+                len = plan.len[g.p];
+            }
+            const int live = len - tile * TOK;  // codes of tokens from here on count as zeros
+            const uint32_t raw = raws + slot * X::kRaw, to = tiles + place_of * X::kTile;
+            wait(bar(kRawFull + 8 * side) + 8 * slot, full, gave_up);
+            wait(bar(side ? kVEmpty : kKEmpty) + 8 * place_of, free, gave_up);
+            // Eight lanes take one piece of eight rows: what they read and store together lies in
+            // different banks.
+            constexpr int kGroup = X::kChunks % 4 == 0 ? 4 : X::kChunks % 3 == 0 ? 3 : X::kChunks;
+#pragma unroll
+            for (int c0 = 0; c0 < X::kChunks; c0 += kGroup) {
+                uint4 x[kGroup];
+#pragma unroll
+                for (int c = 0; c < kGroup; ++c) {
+                    const int j = (c0 + c) * 32 * X::kConvert + t;
+                    const int row = j / (8 * kRowChunks) * 8 + j % 8, piece = j / 8 % kRowChunks;
+                    constexpr int kIn = X::kBox / 16;  // pieces of a box's row
+                    const int swizzle =
+                        X::kBox == 128 ? row & 7 : X::kBox == 64 ? row >> 1 & 3 : row >> 2 & 1;
+                    const uint32_t at = raw + piece / kIn * (TOK * X::kBox) + row * X::kBox +
+                                        ((piece % kIn ^ swizzle) << 4);
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x[c].x), "=r"(x[c].y), "=r"(x[c].z), "=r"(x[c].w)
+                                 : "r"(at)
+                                 : "memory");
+                }
+#pragma unroll
+                for (int c = 0; c < kGroup; ++c) {
+                    const int j = (c0 + c) * 32 * X::kConvert + t;
+                    const int row = j / (8 * kRowChunks) * 8 + j % 8, piece = j / 8 % kRowChunks;
+                    if (live < TOK && row >= live) x[c] = make_uint4(0, 0, 0, 0);
+                    uint32_t y[8];
+                    halves<CODE>(x[c].x, y[0], y[1]);
+                    halves<CODE>(x[c].y, y[2], y[3]);
+                    halves<CODE>(x[c].z, y[4], y[5]);
+                    halves<CODE>(x[c].w, y[6], y[7]);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     to + place(row, piece * 16, TOK * 128)),
+                                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     to + place(row, piece * 16 + 8, TOK * 128)),
+                                 "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                                 : "memory");
+                }
             }
             __syncwarp();
-        };
+            if (lane == 0) {
+                arrive(bar(side ? kVFull : kKFull) + 8 * place_of);
+                arrive(bar(kRawEmpty + 8 * side) + 8 * slot);
+            }
+            if (++slot == X::kRing) slot = 0, full ^= 1;
+            if (++place_of == X::kPool) place_of = 0, free ^= 1;
+        }
+    } else {
+        // ---- softmax ---------------------------------------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kSoftmaxRegs));
+        const int p = warp / 4, row = tid - p * kPrefixRows;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t o_col = lanes + X::kOut + p * D;
+        uint32_t done = 0;  // items before
         for (int from = u0; from < u1;) {
             const Segment g(plan, a, from, u1, X::kRows, TOK);
             const bool both = NP == 2 && g.rows - g.row0 > kPrefixRows;
-            const int mine = NP == 1 || both ? g.n : (g.n + 1 - p) / 2;
+            const bool shared = NP == 2 && !both;  // the pipelines take turns
+            const int first = from - u0 + (shared ? p : 0), stop = from - u0 + g.n;
+            const int step = shared ? 2 : 1;
             const int r = g.row0 + (both ? p * kPrefixRows : 0) + row;
             const bool on = r < g.rows;
-            const Row at(a, plan.lo[g.p], g.h, on ? r : g.row0);
-            const int rest = plan.len[g.p] - g.tile0 * TOK;
             // Warps without rows leave theirs as they are: a row's products are its own.
             const bool alive = r - lane < g.rows;
-            const int users = both ? 2 : 1;  // pipelines that read a tile
-            float f = 0.f;                   // of the products
-            if (mine > 0) {
+            const int rest = plan.len[g.p] + (from - u0 - g.tile0) * TOK;  // less TOK a tile of the CTA
+            float f = 0.f;  // of the products
+            if (first < stop) {
                 // The row's largest element goes to [2^14, 2^15), f16's top.
+                const Row at(a, plan.lo[g.p], g.h, on ? r : g.row0);
                 const uint16_t* q = a.q + at.at(a.q_stride);
-                float peak = 0.f;
-                if (on) {
-#pragma unroll 4
-                    for (int d = 0; d < D; d += 8) {
-                        const uint4 x = load8(q + d, a.vec_q);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint4 x[D / 8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 y = pair(w[i], a.fp16);
-                            peak = fmaxf(peak, fmaxf(fabsf(y.x), fabsf(y.y)));
-                        }
+                for (int i = 0; i < D / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
+                if (on && a.vec_q) {  // all on their way together
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) x[i] = load8(q + 8 * i, true);
+                } else if (on) {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) x[i] = load8(q + 8 * i, false);
+                }
+                float peak = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 y = pair(w[k], a.fp16);
+                        peak = fmaxf(peak, fmaxf(fabsf(y.x), fabsf(y.y)));
                     }
                 }
                 int e = (int)(__float_as_uint(peak) >> 23) - 127;
                 e = e < -100 ? -100 : e;
                 const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
                 f = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
-                const uint32_t to = q_at + p * X::kQ;
-#pragma unroll 4
-                for (int d = 0; alive && d < D; d += 8) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (on) x = load8(q + d, a.vec_q);
-                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                if (alive) {
+                    const uint32_t to = q_at + p * X::kQ;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 y = pair(w[i], a.fp16);
-                        w[i] = pack_half2(y.x * up, y.y * up);
+                    for (int i = 0; i < D / 8; ++i) {
+                        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 y = pair(w[k], a.fp16);
+                            w[k] = pack_half2(y.x * up, y.y * up);
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         to + place(row, 8 * i, kPrefixRows * 128)),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
                     }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     to + place(row, d, kPrefixRows * 128)),
-                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                 : "memory");
                 }
                 fence_shared();
-                scores(from - u0 + (both || NP == 1 ? 0 : p), users);
+                __syncwarp();
+                if (lane == 0) arrive(bar(kQFull + p));
             }
             float ref = 0.f, l = 0.f;
-            for (int j = 0; j < mine; ++j) {
-                const int i = NP == 1 || both ? j : 2 * j + p;
-                const int t = from - u0 + i, sc = t & 3;
-                const int live = rest - i * TOK;  // tokens of the tile, or more
-                wait(bar(kSFull + p), s_done++ & 1, gave_up);
+            for (int t = first; t < stop; t += step, ++done) {
+                const int sc = t % X::kScales;
+                wait(bar(kScFull) + 8 * sc, t / X::kScales & 1, gave_up);
+                const Even<TOK> even(s_even[sc], f);  // while the scores come
+                wait(bar(kSFull + 2 * p) + 8 * (done & 1), done >> 1 & 1, gave_up);
                 fence_after();
                 if (alive) {
-                    const int4 small = *reinterpret_cast<const int4*>(s_small[sc]);
-                    const bool special = live < TOK || (small.x | small.y | small.z | small.w);
-                    if (a.even && !special)
-                        softmax_even<TOK, D>(s_col, o_col, f, s_k[sc], s_even[sc], j == 0, ref, l);
+                    const uint32_t s_col = lanes + (2 * p + (done & 1)) * TOK;
+                    // The product before, which may still be adding to O.
+                    const Product before = {bar(kPvDone + p), (done + 1) & 1, t == first, gave_up};
+                    const int live = rest - t * TOK;  // tokens of the tile, or more
+                    if (a.even && live >= TOK && !s_small[sc])
+                        softmax_even<TOK, D>(s_col, o_col, even, before, ref, l);
                     else
                         softmax_any<TOK, D>(s_col, o_col, f, s_k[sc], s_v[sc], s_log[sc], live,
-                                            j == 0, ref, l);
+                                            before, ref, l);
                 }
                 stored();
                 fence_before();
-                const int stage = t % X::kValues;
-                if (issuer) {  // O += P V
-                    meet(values_barrier(stage, p));
-                    fence_shared();
-                    fence_after();
-                    const uint64_t b = matrix(v_at + stage * X::kTile, TOK * 128);
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < TOK / 16; ++k)  // 16 tokens are 16 rows of 128 bytes
-                            multiply_tensor(tmem + X::kOut + p * D, tmem + p * TOK + 8 * k,
-                                            b + k * (2048 >> 4), kValues, k > 0 || j > 0);
-                        for (int u = users; u <= NP; ++u) commit(bar(kVEmpty + stage));
-                        if (j + 1 == mine) commit(bar(kOFull + p));
-                    }
-                    __syncwarp();
-                } else {
-                    meet_later(values_barrier(stage, p));
+                __syncwarp();
+                if (lane == 0) {
+                    arrive(bar(kPFull + 2 * p) + 8 * (done & 1));
+                    arrive_n(bar(kScEmpty) + 8 * sc, shared ? 2 : 1);
                 }
-                // The next scores take P's place, behind the product with V.
-                if (j + 1 < mine) scores(t + (both || NP == 1 ? 1 : 2), users);
             }
 
             // ---- the segment's outputs ---------------------------------------------------
@@ -1044,17 +1133,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             int anew = from, row_anew = row;
             asm volatile("" : "+r"(anew), "+r"(row_anew));
             finish<D>(a, plan, smem, s_sum, o_col, anew, u0, u1, row_anew, p, ref, l,
-                      mine > 0 ? bar(kOFull + p) : 0u, o_done & 1, gave_up);
-            o_done += mine > 0;
+                      first < stop ? bar(kPvDone + p) : 0u, (done + 1) & 1, gave_up);
             from += g.n;
         }
-        if (leader) commit(bar(kDone));
-        if (issuer) wait_still(bar(kDone), 0);
     }
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == X::kControl) {
         __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -1066,19 +1152,17 @@ cudaError_t run_one(const PrefixArgs& a, const CUtensorMap& map, cudaStream_t s)
     static SmemOptIn opt;
     cudaError_t e = ensure_smem(prefix_kernel<CODE, D>, Shape<D>::kSmem, &opt);
     if (e != cudaSuccess) return e;
-    if (Shape<D>::kPipes == 2) {
-        // The roles' shares are there only if the compiler has used the whole launch bound.
-        static std::atomic<int> regs{0};
-        int n = regs.load(std::memory_order_relaxed);
-        if (n == 0) {
-            cudaFuncAttributes attr;
-            e = cudaFuncGetAttributes(&attr, prefix_kernel<CODE, D>);
-            if (e != cudaSuccess) return e;
-            n = attr.numRegs;
-            regs.store(n, std::memory_order_relaxed);
-        }
-        if (n != Shape<D>::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    // The roles' shares are there only if the compiler has used the whole launch bound.
+    static std::atomic<int> regs{0};
+    int n = regs.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, prefix_kernel<CODE, D>);
+        if (e != cudaSuccess) return e;
+        n = attr.numRegs;
+        regs.store(n, std::memory_order_relaxed);
     }
+    if (n != Shape<D>::kLaunchRegs) return cudaErrorInvalidConfiguration;
     return launch_chained(prefix_kernel<CODE, D>, a.ctas, Shape<D>::kThreads, Shape<D>::kSmem, 0, s,
                           a, map);
 }
