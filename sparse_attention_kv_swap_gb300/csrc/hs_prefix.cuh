@@ -167,9 +167,6 @@ __device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void arrive_n(uint32_t bar, int n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
-}
 // True once the phase of this parity is over; the thread sleeps for up to 20 us before it says no.
 // (Without the time it comes back at once, and the waiting warps' loops take half of the others' issue
 // slots.)
@@ -729,8 +726,10 @@ enum Bar : int {
     kPvDone = 10,    // [pipe] a product with V
     kKFull = 12, kVFull = 16, kKEmpty = 20, kVEmpty = 24,   // [kPool] f16 tiles
     kRawFull = 28, kRawEmpty = 44,                          // [keys, values][8] codes
-    kScFull = 60, kScEmpty = 64,                            // [kScales]
-    kDone = 68, kBars = 69
+    kScFull = 60, kScEmpty = 68,                            // [pipe][kScales]
+    kOFull = 76,     // [pipe] the products of a segment: kPvDone alone could not tell the last from the
+                     // one before the last but one
+    kDone = 78, kBars = 79
 };
 
 template <int CODE, int D>
@@ -740,10 +739,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     constexpr int NP = X::kPipes, TOK = X::kTok;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Plan plan;
-    __shared__ __align__(16) float s_k[X::kScales][TOK], s_v[X::kScales][TOK];
-    __shared__ __align__(16) float s_log[X::kScales][TOK];  // log2 of the V scale
-    __shared__ __align__(16) float4 s_even[X::kScales][TOK / 16];  // of 16 tokens: K, log2 V, 1 / V
-    __shared__ int s_small[X::kScales];                     // a V scale is below 2^-60
+    // Scales of the tiles of each pipeline.
+    struct Scales {
+        float k[TOK], v[TOK], log[TOK];  // log2 of the V scale
+        float4 even[TOK / 16];           // of 16 tokens: K, log2 V, 1 / V
+        int small;                       // a V scale is below 2^-60
+    };
+    __shared__ __align__(16) Scales s_scales[NP][X::kScales];
     __shared__ __align__(8) unsigned long long s_bar[kBars];
     __shared__ float2 s_sum[kPrefixRows];  // of the second pipeline
     __shared__ uint32_t s_tmem;
@@ -759,6 +761,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             barrier_init(bar(kQFull + i), 4);
             barrier_init(bar(kPvDone + i), 1);
+            barrier_init(bar(kOFull + i), 1);
         }
         for (int i = 0; i < 4; ++i) {
             barrier_init(bar(kSFull + i), 1);
@@ -767,8 +770,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             barrier_init(bar(kVFull + i), X::kConvert);
             barrier_init(bar(kKEmpty + i), NP);
             barrier_init(bar(kVEmpty + i), NP);
-            barrier_init(bar(kScFull + i), 1);
-            barrier_init(bar(kScEmpty + i), X::kSoftmax);
+            for (int p = 0; p < 2; ++p) {
+                barrier_init(bar(kScFull + 4 * p + i), 1);
+                barrier_init(bar(kScEmpty + 4 * p + i), 4);
+            }
         }
         for (int i = 0; i < 16; ++i) {
             barrier_init(bar(kRawFull + i), 1);
@@ -809,6 +814,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             const bool leader = elected();
             const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
             uint32_t done = 0, segments = 0;  // items and segments before
+            // Each pipeline releases every tile, one of the other's as soon as it is there: the barriers'
+            // phases then tell tiles apart, for nobody is two behind or ahead.
+            int k_next = 0, v_next = 0;
+            auto pass = [&](int full, int empty, int& next, int to) {
+                for (; NP == 2 && next < to; ++next) {
+                    const int place = next % X::kPool;
+                    wait(bar(full) + 8 * place, next / X::kPool & 1, gave_up);
+                    if (leader) arrive(bar(empty) + 8 * place);
+                    __syncwarp();
+                }
+            };
             for (int from = u0; from < u1;) {
                 const Segment g(plan, a, from, u1, X::kRows, TOK);
                 const int n = __shfl_sync(0xffffffffu, g.n, 0);
@@ -816,13 +832,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     __shfl_sync(0xffffffffu, (int)(NP == 2 && g.rows - g.row0 > kPrefixRows), 0);
                 const bool shared = NP == 2 && !both;  // the pipelines take turns
                 const int items = shared ? (n + 1 - p) / 2 : n, first = from - u0 + (shared ? p : 0);
-                const int users = both ? 2 : 1;
                 if (items > 0) wait(bar(kQFull + p), segments++ & 1, gave_up);
                 for (int k = 0; k < items + 2; ++k) {
                     if (k >= 2) {  // O += P V of two items before
                         const uint32_t it = done + k - 2;
                         const int t = first + (shared ? 2 : 1) * (k - 2);
                         const int place = t % X::kPool;
+                        pass(kVFull, kVEmpty, v_next, t);
+                        v_next = t + 1;
                         wait(bar(kVFull) + 8 * place, t / X::kPool & 1, gave_up);
                         wait(bar(kPFull + 2 * p) + 8 * (it & 1), it >> 1 & 1, gave_up);
                         fence_shared();
@@ -834,8 +851,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                             for (int i = 0; i < TOK / 16; ++i)  // 16 tokens are 16 rows of 128 bytes
                                 multiply_tensor(base + X::kOut + p * D, s + 8 * i,
                                                 b + i * (2048 >> 4), kValues, i > 0 || k > 2);
-                            for (int u = users; u <= NP; ++u) commit(bar(kVEmpty) + 8 * place);
+                            commit(bar(kVEmpty) + 8 * place);
                             commit(bar(kPvDone + p));
+                            if (k == items + 1) commit(bar(kOFull + p));
                         }
                         __syncwarp();
                     }
@@ -843,6 +861,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                         const uint32_t it = done + k;
                         const int t = first + (shared ? 2 : 1) * k;
                         const int place = t % X::kPool;
+                        pass(kKFull, kKEmpty, k_next, t);
+                        k_next = t + 1;
                         wait(bar(kKFull) + 8 * place, t / X::kPool & 1, gave_up);
                         fence_shared();
                         fence_after();
@@ -857,11 +877,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                                          key + ((panel * TOK * 128 + in) >> 4), kScores, i > 0);
                             }
                             commit(bar(kSFull + 2 * p) + 8 * (it & 1));
-                            for (int u = users; u <= NP; ++u) commit(bar(kKEmpty) + 8 * place);
+                            commit(bar(kKEmpty) + 8 * place);
                         }
                         __syncwarp();
                     }
                 }
+                pass(kKFull, kKEmpty, k_next, from - u0 + n);
+                pass(kVFull, kVEmpty, v_next, from - u0 + n);
                 done += items;
                 from += n;
             }
@@ -912,18 +934,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         } else if (role == 3) {
             // ---- scales --------------------------------------------------------------------
             // A lane has two tokens, of two tiles ahead.
-            int tile = 0, end = 0, len = 0;
+            int tile = 0, end = 0, len = 0, readers = 0;
             const float* scales = nullptr;
             float k[2][2], v[2][2];  // [tile][token]
-            auto load = [&](int i, float (&k)[2], float (&v)[2]) {
+            int to[2];               // pipelines that read the tile, a bit each
+            auto load = [&](int i, float (&k)[2], float (&v)[2], int& to) {
                 if (i >= count) return;
+                if (NP == 2 && readers != 3) readers ^= 3;
                 if (++tile >= end) {
                     const Segment g(plan, a, u0 + i, u1, X::kRows, TOK);
                     tile = g.tile0;
                     end = g.tile0 + g.n;
                     len = plan.len[g.p];
+                    readers = NP == 2 && g.rows - g.row0 > kPrefixRows ? 3 : 1;
                     scales = a.scales + (long long)plan.req[g.p] * a.NB * 2 * a.Hkv + g.h;
                 }
+                to = readers;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int token = tile * TOK + 32 * h + lane;
@@ -935,34 +961,39 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     }
                 }
             };
-            auto put = [&](int i, const float (&k)[2], const float (&v)[2]) {
-                const int sc = i % X::kScales;
-                wait(bar(kScEmpty) + 8 * sc, (i / X::kScales & 1) ^ 1, gave_up);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int t = 32 * h + lane;
-                    const float lg = log2f(v[h]);
-                    s_k[sc][t] = k[h] * a.k_sign;
-                    s_v[sc][t] = v[h];
-                    s_log[sc][t] = lg;
-                    if (t % 16 == 0)
-                        s_even[sc][t / 16] = make_float4(k[h] * a.k_sign, lg, __frcp_rn(v[h]), 0.f);
-                }
+            int items[2] = {0, 0};  // of each pipeline
+            auto put = [&](const float (&k)[2], const float (&v)[2], int to) {
                 const bool small = __any_sync(0xffffffffu, fminf(v[0], v[1]) < 0x1p-60f);
-                __syncwarp();
-                if (lane == 0) {
-                    s_small[sc] = small;
-                    arrive(bar(kScFull) + 8 * sc);
+                const float lg[2] = {log2f(v[0]), log2f(v[1])};
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    if (!(to >> p & 1)) continue;
+                    const int sc = items[p] % X::kScales;
+                    wait(bar(kScEmpty + 4 * p) + 8 * sc, (items[p] / X::kScales & 1) ^ 1, gave_up);
+                    Scales& s = s_scales[p][sc];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = 32 * h + lane;
+                        s.k[t] = k[h] * a.k_sign;
+                        s.v[t] = v[h];
+                        s.log[t] = lg[h];
+                        if (t % 16 == 0)
+                            s.even[t / 16] = make_float4(k[h] * a.k_sign, lg[h], __frcp_rn(v[h]), 0.f);
+                    }
+                    if (lane == 0) s.small = small;
+                    __syncwarp();
+                    if (lane == 0) arrive(bar(kScFull + 4 * p) + 8 * sc);
+                    ++items[p];
                 }
             };
-            load(0, k[0], v[0]);
-            load(1, k[1], v[1]);
+            load(0, k[0], v[0], to[0]);
+            load(1, k[1], v[1], to[1]);
             for (int i = 0; i < count; i += 2) {
-                put(i, k[0], v[0]);
-                load(i + 2, k[0], v[0]);
+                put(k[0], v[0], to[0]);
+                load(i + 2, k[0], v[0], to[0]);
                 if (i + 1 == count) break;
-                put(i + 1, k[1], v[1]);
-                load(i + 3, k[1], v[1]);
+                put(k[1], v[1], to[1]);
+                load(i + 3, k[1], v[1], to[1]);
             }
         }
     } else if (warp >= X::kSoftmax) {
@@ -984,8 +1015,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
             const int live = len - tile * TOK;  // codes of tokens from here on count as zeros
             const uint32_t raw = raws + slot * X::kRaw, to = tiles + place_of * X::kTile;
-            wait(bar(kRawFull + 8 * side) + 8 * slot, full, gave_up);
-            wait(bar(side ? kVEmpty : kKEmpty) + 8 * place_of, free, gave_up);
+            const uint32_t raw_full = bar(kRawFull + 8 * side) + 8 * slot;
+            const uint32_t empty = bar(side ? kVEmpty : kKEmpty) + 8 * place_of;
+            // both are asked at once: an answer takes some 100 cycles
+            const bool have = try_wait(raw_full, full), may = try_wait(empty, free);
+            if (!have) wait_slow(raw_full, full, gave_up);
+            if (!may) wait_slow(empty, free, gave_up);
             // Eight lanes take one piece of eight rows: what they read and store together lies in
             // different banks.
             constexpr int kGroup = X::kChunks % 4 == 0 ? 4 : X::kChunks % 3 == 0 ? 3 : X::kChunks;
@@ -1040,7 +1075,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         const int p = warp / 4, row = tid - p * kPrefixRows;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t o_col = lanes + X::kOut + p * D;
-        uint32_t done = 0;  // items before
+        uint32_t done = 0, segments = 0;  // items and segments (with items) before
         for (int from = u0; from < u1;) {
             const Segment g(plan, a, from, u1, X::kRows, TOK);
             const bool both = NP == 2 && g.rows - g.row0 > kPrefixRows;
@@ -1103,20 +1138,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
             float ref = 0.f, l = 0.f;
             for (int t = first; t < stop; t += step, ++done) {
-                const int sc = t % X::kScales;
-                wait(bar(kScFull) + 8 * sc, t / X::kScales & 1, gave_up);
-                const Even<TOK> even(s_even[sc], f);  // while the scores come
+                const int sc = done % X::kScales;
+                wait(bar(kScFull + 4 * p) + 8 * sc, done / X::kScales & 1, gave_up);
+                const Scales& scales = s_scales[p][sc];
+                const Even<TOK> even(scales.even, f);  // while the scores come
                 wait(bar(kSFull + 2 * p) + 8 * (done & 1), done >> 1 & 1, gave_up);
                 fence_after();
                 if (alive) {
                     const uint32_t s_col = lanes + (2 * p + (done & 1)) * TOK;
-                    // The product before, which may still be adding to O.
+                    // The product before, which may still be adding to O; the one before that is done, for
+                    // these scores were issued behind it.
                     const Product before = {bar(kPvDone + p), (done + 1) & 1, t == first, gave_up};
                     const int live = rest - t * TOK;  // tokens of the tile, or more
-                    if (a.even && live >= TOK && !s_small[sc])
+                    if (a.even && live >= TOK && !scales.small)
                         softmax_even<TOK, D>(s_col, o_col, even, before, ref, l);
                     else
-                        softmax_any<TOK, D>(s_col, o_col, f, s_k[sc], s_v[sc], s_log[sc], live,
+                        softmax_any<TOK, D>(s_col, o_col, f, scales.k, scales.v, scales.log, live,
                                             before, ref, l);
                 }
                 stored();
@@ -1124,7 +1161,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     arrive(bar(kPFull + 2 * p) + 8 * (done & 1));
-                    arrive_n(bar(kScEmpty) + 8 * sc, shared ? 2 : 1);
+                    arrive(bar(kScEmpty + 4 * p) + 8 * sc);
                 }
             }
 
@@ -1133,7 +1170,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             int anew = from, row_anew = row;
             asm volatile("" : "+r"(anew), "+r"(row_anew));
             finish<D>(a, plan, smem, s_sum, o_col, anew, u0, u1, row_anew, p, ref, l,
-                      first < stop ? bar(kPvDone + p) : 0u, (done + 1) & 1, gave_up);
+                      first < stop ? bar(kOFull + p) : 0u, segments & 1, gave_up);
+            segments += first < stop;
             from += g.n;
         }
     }
