@@ -7,9 +7,11 @@
 // two multiply-adds for each pair of bounds, whatever the number of query heads: the bounds
 // are read once and nothing else counts (4 bytes for 2 * steps operations: memory).
 //
-// The first kernel scores: a warp takes 256 elements (512 bytes) of up to 32 / steps blocks, each lane
-// 8 of them, holds the sums of all in registers and adds them up over its lanes by halving exchanges (31
-// shuffles for 32 sums).
+// The first kernel scores: a warp takes 256 elements (512 bytes) of 4 or 8 blocks, each lane 8 of
+// them, and holds the sums of all in registers, of even and odd channels apart (one instruction
+// multiplies and adds both); over its lanes they add up by halving exchanges.  A lane copies its own 16
+// bytes of the next blocks to shared memory ahead of itself (cp.async; no other lane reads
+// them, so nothing is synchronised), and begins that before it computes Q.
 //
 // The second selects, one CTA a query.  Sums in 32 bits depend on their order and would swap blocks whose
 // scores are close.  So the first kernel also bounds the error of its sums (a few 2^-24 of
@@ -25,11 +27,26 @@ namespace {
 constexpr int kScoreWarps = 8;
 constexpr int kSlice = 256;            // elements of a block that a warp takes at a time
 constexpr int kMostSums = 1024;        // scores of a CTA: its blocks times the steps
-constexpr int kSelectThreads = 512;
+constexpr int kList = 64;              // close blocks that are ranked pair by pair
+constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 1024;
 
-// Blocks of a warp's registers: 32 sums.
-constexpr int batch_blocks(int S) { return S == 1 ? 32 : S == 2 ? 16 : S == 3 ? 10 : 8; }
+// Blocks of a warp's registers (8 to 16 sums), those it copies together, and copies of these: a ring of
+// 64 KB a CTA.
+constexpr int batch_blocks(int S) { return S == 1 ? 8 : 4; }
+constexpr int kGroup = 4;
+constexpr int kStages = 4;
+constexpr size_t kRingBytes = (size_t)kScoreWarps * kStages * kGroup * kSlice * 2;
+// CTAs of an SM, by registers and shared memory.
+constexpr int score_ctas(int S) { return S <= 2 ? 3 : 2; }
+// Warps that share a block: as many as leave each two slices of it or more (it adds up over its
+// lanes once for them).
+constexpr int warps_per_row(int row) {
+    const int slices = (row + kSlice - 1) / kSlice;
+    int w = 1;
+    while (w < kScoreWarps && slices >= 4 * w) w *= 2;
+    return w;
+}
 
 struct ScoreArgs {
     const uint16_t* q;
@@ -42,7 +59,7 @@ struct ScoreArgs {
     int32_t B, S, Hkv, G, D, R, L, T, NB, row;  // row: elements of a block's bounds
     int32_t chunks, blocks;  // CTAs of a batch entry, blocks of each
     int32_t wpr;             // warps that share a block
-    int32_t vec_bounds;
+    int32_t vec_bounds, vec_q;
     float gamma;
     // the selection's
     int32_t select, first, last;
@@ -63,18 +80,25 @@ __device__ __forceinline__ float2 values(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Larger of the magnitudes, two elements at a time (a NaN does not count).
+// Larger of the magnitudes, two elements at a time (a NaN does not count).  The sign bits of the result
+// mean nothing.
 template <bool FP16>
 __device__ __forceinline__ uint32_t greater_magnitude(uint32_t m, uint32_t w) {
-    w &= 0x7fff7fffu;
-    if constexpr (FP16) {
-        const __half2 x = __hmax2(*reinterpret_cast<__half2*>(&m), *reinterpret_cast<__half2*>(&w));
-        return *reinterpret_cast<const uint32_t*>(&x);
-    } else {
-        const __nv_bfloat162 x = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m),
-                                         *reinterpret_cast<__nv_bfloat162*>(&w));
-        return *reinterpret_cast<const uint32_t*>(&x);
-    }
+    uint32_t x;
+    if constexpr (FP16)
+        asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(x) : "r"(m), "r"(w));
+    else
+        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(m), "r"(w));
+    return x;
+}
+
+// z += q v, both halves.
+__device__ __forceinline__ void fma_pair(float2& z, float2 q, float2 v) {
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%0, %1};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "+f"(z.x), "+f"(z.y)
+        : "f"(q.x), "f"(q.y), "f"(v.x), "f"(v.y));
 }
 
 // A number of about 48 bits, the sum of two floats.
@@ -93,44 +117,62 @@ struct Two {
     }
 };
 
-// Q+ and Q- of column `col` (K/V head, channel) of one query, in twice 32 bits.
-template <bool FP16>
-__device__ __forceinline__ void query_sums(const ScoreArgs& a, const uint16_t* q, int col, Two& up,
-                                           Two& down) {
-    const int h = col / a.D, d = col - h * a.D;
-    const uint16_t* p = q + (long long)h * a.G * a.q_stride[2] + d;
-    up = down = Two{0.f, 0.f};
-#pragma unroll 4
-    for (int g = 0; g < a.G; ++g) {
-        const float x = value<FP16>(ld(p + g * a.q_stride[2]));
-        if (x < 0.f)
-            down.add(x);
-        else
-            up.add(x);  // a NaN spoils the query's scores
-    }
-    up.normalise();
-    down.normalise();
+// Four consecutive 16-bit elements.
+__device__ __forceinline__ uint2 load4(const uint16_t* p, bool vec) {
+    if (vec) return ld(reinterpret_cast<const uint2*>(p));
+    return make_uint2((uint32_t)ld(p) | (uint32_t)ld(p + 1) << 16,
+                      (uint32_t)ld(p + 2) | (uint32_t)ld(p + 3) << 16);
 }
 
-// The 256 elements of a block that a warp takes: 8 a lane.
-__device__ __forceinline__ uint4 load_bounds(const uint16_t* p, bool vec, bool on) {
-    if (!on) return make_uint4(0, 0, 0, 0);
-    if (vec) return ld_once_v4(p);
-    uint32_t w[4];
+// Q+ and Q- of channels d .. d + 3 of K/V head h of one query, in twice 32 bits.
+template <bool FP16>
+__device__ __forceinline__ void query_sums(const ScoreArgs& a, const uint16_t* q, int h, int d,
+                                           Two (&up)[4], Two (&down)[4]) {
+    const uint16_t* p = q + (long long)h * a.G * a.q_stride[2] + d;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)ld(p + 2 * i) | (uint32_t)ld(p + 2 * i + 1) << 16;
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int k = 0; k < 4; ++k) up[k] = down[k] = Two{0.f, 0.f};
+#pragma unroll 4
+    for (int g = 0; g < a.G; ++g) {
+        const uint2 w = load4(p + g * a.q_stride[2], a.vec_q);
+        const float2 y[2] = {values<FP16>(w.x), values<FP16>(w.y)};
+        const float x[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            down[k].add(x[k] < 0.f ? x[k] : 0.f);
+            up[k].add(x[k] < 0.f ? 0.f : x[k]);  // a NaN spoils the query's scores
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        up[k].normalise();
+        down[k].normalise();
+    }
+}
+
+// Copies this lane's 8 elements of a block to shared memory, or zeros.
+__device__ __forceinline__ void copy_bounds(uint32_t to, const uint16_t* p, bool vec, bool on) {
+    if (vec) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p),
+                     "r"(on ? 16 : 0)
+                     : "memory");
+    } else {
+        uint2 x = make_uint2(0, 0), y = x;
+        if (on) x = load4(p, false), y = load4(p + 4, false);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(x.x), "r"(x.y),
+                     "r"(y.x), "r"(y.y)
+                     : "memory");
+    }
 }
 
 template <bool FP16, int S>
-__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScoreArgs a) {
-    constexpr int NB = batch_blocks(S);
-    constexpr int kGroup = NB % 8 == 0 ? 8 : 5;  // blocks under way together
-    extern __shared__ __align__(16) float s_q[];  // [S][row], then the warps' sums
+__global__ void __launch_bounds__(32 * kScoreWarps, score_ctas(S)) score_kernel(const ScoreArgs a) {
+    constexpr int NB = batch_blocks(S), kSums = S * NB > 8 ? 16 : 8;
+    extern __shared__ __align__(16) uint8_t s_ring[];  // [warp][stage][block][256], then Q and sums
     __shared__ float s_error[kScoreWarps][S];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunk = blockIdx.x % a.chunks, b = blockIdx.x / a.chunks;
-    float* const s_sum = s_q + S * a.row;  // [wpr][blocks * S]
+    float* const s_q = reinterpret_cast<float*>(s_ring + kRingBytes);  // [S][row]
+    float* const s_sum = s_q + S * a.row;                                 // [wpr][blocks * S]
     wait_for_previous();
     const int r = ld(a.req + b);
     int n = ld(a.seq_lens + b);
@@ -138,95 +180,128 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScoreArgs
     const int nb = (n + a.T - 1) / a.T;
     const int n0 = chunk * a.blocks, n1 = min(n0 + a.blocks, a.NB);
     const int live = max(0, min(n1, nb) - n0);  // blocks to score
+    const uint16_t* const base = a.bounds + ((long long)max(r, 0) * a.NB + n0) * a.row;
+    const int part = warp % a.wpr, turns = kScoreWarps / a.wpr;
+    const int e_first = part * kSlice, e_step = a.wpr * kSlice;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring) +
+                          warp * (kStages * kGroup * kSlice * 2) + lane * 16;
+    // The copies run ahead of the sums in the same order: blocks, slices, groups of the slice's blocks.
+    int c_j = warp / a.wpr * NB, c_e = e_first, c_g = 0, c_stage = 0;
+    const auto copy_next = [&] {
+        if (c_j < live && c_e < a.row) {
+            // blocks past the last are that one again: their sums are not kept
+            const bool on = c_e + lane * 8 < a.row;
+            const uint16_t* from = base + (on ? c_e + lane * 8 : 0);
+            const uint32_t to = ring + c_stage * (kGroup * kSlice * 2);
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g)
+                copy_bounds(to + g * (kSlice * 2), from + min(c_j + c_g + g, live - 1) * a.row,
+                            a.vec_bounds, on);
+            c_g += kGroup;
+            if (c_g >= NB || c_j + c_g >= live) {
+                c_g = 0;
+                c_e += e_step;
+                if (c_e >= a.row) {
+                    c_e = e_first;
+                    c_j += turns * NB;
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        c_stage = (c_stage + 1) % kStages;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) copy_next();
     if (live > 0) {
         // Q- and Q+ of all columns, in the order of the bounds.
-        const int columns = a.Hkv * a.D;
-        for (int i = tid; i < S * columns; i += 32 * kScoreWarps) {
-            const int s = i / columns, col = i - s * columns;
-            const uint16_t* q = a.q + b * a.q_stride[0] + s * a.q_stride[1];
-            Two up, down;
-            query_sums<FP16>(a, q, col, up, down);
-            const int h = col / a.D;
-            float* to = s_q + s * a.row + col + h * a.D;
-            to[0] = down.hi;
-            to[a.D] = up.hi;
+        const int quads = a.D / 4, all = a.Hkv * quads;
+        for (int i = tid; i < S * all; i += 32 * kScoreWarps) {
+            const int s = i / all, u = i - s * all, h = u / quads, d = 4 * (u - h * quads);
+            Two up[4], down[4];
+            query_sums<FP16>(a, a.q + b * a.q_stride[0] + s * a.q_stride[1], h, d, up, down);
+            float* to = s_q + s * a.row + 2 * h * a.D + d;
+            *reinterpret_cast<float4*>(to) =
+                make_float4(down[0].hi, down[1].hi, down[2].hi, down[3].hi);
+            *reinterpret_cast<float4*>(to + a.D) =
+                make_float4(up[0].hi, up[1].hi, up[2].hi, up[3].hi);
         }
     }
     __syncthreads();
     float worst[S] = {};
-    if (live > 0) {
-        const uint16_t* base = a.bounds + ((long long)r * a.NB + n0) * a.row;
-        const int part = warp % a.wpr, turns = kScoreWarps / a.wpr;
-        for (int j0 = warp / a.wpr * NB; j0 < live; j0 += turns * NB) {
-            float acc[32];
+    int stage = 0;
+    for (int j0 = warp / a.wpr * NB; j0 < live; j0 += turns * NB) {
+        float2 both[kSums];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-            float error[S] = {};
-            for (int e0 = part * kSlice; e0 < a.row; e0 += a.wpr * kSlice) {
-                const int e = e0 + lane * 8;
-                const bool on = e < a.row;
-                float q[S][8];
+        for (int i = 0; i < kSums; ++i) both[i] = make_float2(0.f, 0.f);
+        float error[S] = {};
+        for (int e0 = e_first; e0 < a.row; e0 += e_step) {
+            const int e = e0 + lane * 8;
+            float2 q[S][4];
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                    if (on) {
-                        x = *reinterpret_cast<const float4*>(s_q + s * a.row + e);
-                        y = *reinterpret_cast<const float4*>(s_q + s * a.row + e + 4);
-                    }
-                    q[s][0] = x.x, q[s][1] = x.y, q[s][2] = x.z, q[s][3] = x.w;
-                    q[s][4] = y.x, q[s][5] = y.y, q[s][6] = y.z, q[s][7] = y.w;
+            for (int s = 0; s < S; ++s) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                if (e < a.row) {
+                    x = *reinterpret_cast<const float4*>(s_q + s * a.row + e);
+                    y = *reinterpret_cast<const float4*>(s_q + s * a.row + e + 4);
                 }
-                uint32_t most[4] = {};
+                q[s][0] = make_float2(x.x, x.y), q[s][1] = make_float2(x.z, x.w);
+                q[s][2] = make_float2(y.x, y.y), q[s][3] = make_float2(y.z, y.w);
+            }
+            uint32_t most[4] = {};
 #pragma unroll
-                for (int g0 = 0; g0 < NB; g0 += kGroup) {
-                    if (j0 + g0 >= live) break;
-                    uint4 x[kGroup];
+            for (int g0 = 0; g0 < NB; g0 += kGroup) {
+                if (j0 + g0 >= live) break;
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                copy_next();  // to the stage of the group before this one, whose sums are taken
+                const uint32_t at = ring + stage * (kGroup * kSlice * 2);
 #pragma unroll
-                    for (int g = 0; g < kGroup; ++g)
-                        x[g] = load_bounds(base + (long long)(j0 + g0 + g) * a.row + e, a.vec_bounds,
-                                           on && j0 + g0 + g < live);
+                for (int g = 0; g < kGroup; ++g) {
+                    uint32_t w[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(at + g * (kSlice * 2))
+                                 : "memory");
 #pragma unroll
-                    for (int g = 0; g < kGroup; ++g) {
-                        const uint32_t w[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+                    for (int i = 0; i < 4; ++i) {
+                        most[i] = greater_magnitude<FP16>(most[i], w[i]);
+                        const float2 v = values<FP16>(w[i]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            most[i] = greater_magnitude<FP16>(most[i], w[i]);
-                            const float2 v = values<FP16>(w[i]);
-#pragma unroll
-                            for (int s = 0; s < S; ++s) {
-                                float& z = acc[s * NB + g0 + g];
-                                z = fmaf(q[s][2 * i], v.x, z);
-                                z = fmaf(q[s][2 * i + 1], v.y, z);
-                            }
-                        }
+                        for (int s = 0; s < S; ++s) fma_pair(both[s * NB + g0 + g], q[s][i], v);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 m = values<FP16>(most[i]);
-#pragma unroll
-                    for (int s = 0; s < S; ++s)
-                        error[s] += fabsf(q[s][2 * i]) * m.x + fabsf(q[s][2 * i + 1]) * m.y;
-                }
+                stage = (stage + 1) % kStages;
             }
 #pragma unroll
-            for (int s = 0; s < S; ++s)  // no bound where there is an infinity
-                worst[s] = fmaxf(worst[s], error[s] == error[s] ? error[s] : INFINITY);
-            // Lane l gets the sum over the lanes of number l.
+            for (int i = 0; i < 4; ++i) {
+                const float2 m = values<FP16>(most[i]);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const bool up = lane & o;
-#pragma unroll
-                for (int i = 0; i < o; ++i) {
-                    const float give = up ? acc[i] : acc[i + o];
-                    const float keep = up ? acc[i + o] : acc[i];
-                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                }
+                for (int s = 0; s < S; ++s)
+                    error[s] += fabsf(q[s][i].x) * fabsf(m.x) + fabsf(q[s][i].y) * fabsf(m.y);
             }
-            const int s = lane / NB, j = j0 + lane - s * NB;
-            if (s < S && j < live) s_sum[part * a.blocks * S + s * a.blocks + j] = acc[0];
         }
+#pragma unroll
+        for (int s = 0; s < S; ++s)  // no bound where there is an infinity
+            worst[s] = fmaxf(worst[s], error[s] == error[s] ? error[s] : INFINITY);
+        // Lane l gets the sum over the lanes of number l modulo their count.
+        float acc[kSums];
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) acc[i] = both[i].x + both[i].y;
+#pragma unroll
+        for (int o = kSums / 2; o > 0; o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < o; ++i) {
+                const float give = up ? acc[i] : acc[i + o];
+                const float keep = up ? acc[i + o] : acc[i];
+                acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+        }
+#pragma unroll
+        for (int o = kSums; o < 32; o <<= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+        const int s = lane / NB, j = j0 + lane - s * NB;
+        if (s < S && j < live) s_sum[part * a.blocks * S + s * a.blocks + j] = acc[0];
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         float x = worst[s];
@@ -271,9 +346,12 @@ struct Edge {
     int want;      // keys equal to it that are among the k
 };
 
-// The k-th largest of keys[lo, hi), 1 <= k <= hi - lo.  All threads call it.
+// The k-th largest of keys[lo, hi), 1 <= k <= hi - lo.  All threads call it.  Counts the keys of each
+// of 1024 ranges and goes on within the one that holds the k-th, until that is a few keys, which are
+// compared one by one.
 __device__ __forceinline__ Edge kth_largest(const uint32_t* keys, int lo, int hi, int k,
-                                            uint32_t* hist, int* tmp, uint32_t* range, int* pick) {
+                                            uint32_t* hist, int* tmp, uint32_t* range, int* pick,
+                                            uint32_t* list) {
     const int tid = threadIdx.x;
     // The keys' range first: scores share their top bits, and counting by these would bring all into
     // a few bins.
@@ -314,6 +392,8 @@ __device__ __forceinline__ Edge kth_largest(const uint32_t* keys, int lo, int hi
             if (above < want && want <= above + mine[i]) {
                 pick[0] = top + kOwn - 1 - i;
                 pick[1] = want - above;
+                pick[2] = mine[i];
+                pick[3] = 0;
             }
             above += mine[i];
         }
@@ -323,6 +403,27 @@ __device__ __forceinline__ Edge kth_largest(const uint32_t* keys, int lo, int hi
         want = pick[1];
         if (shift == 0) break;
         width = (1u << shift) - 1;
+        const int count = pick[2];
+        if (count <= kList) {
+            for (int i = lo + tid; i < hi; i += kSelectThreads)
+                if (keys[i] >= base && keys[i] - base <= width) list[atomicAdd(&pick[3], 1)] = keys[i];
+            __syncthreads();
+            if (tid < count) {
+                int above = 0, equal = 0;
+                for (int i = 0; i < count; ++i) {
+                    above += list[i] > list[tid];
+                    equal += list[i] == list[tid];
+                }
+                if (above < want && want <= above + equal) {  // equal keys write the same
+                    range[0] = list[tid];
+                    pick[1] = want - above;
+                }
+            }
+            __syncthreads();
+            base = range[0];
+            want = pick[1];
+            break;
+        }
         shift = max(0, shift - 10);
         __syncthreads();  // the picks have been read
     }
@@ -330,22 +431,32 @@ __device__ __forceinline__ Edge kth_largest(const uint32_t* keys, int lo, int hi
     return Edge{base, want};
 }
 
-// Score of block n in twice 32 bits; the whole warp calls it and every lane gets the result.
+// Sum in twice 32 bits over the quads of channels [u0, u1) of block n's score; the whole warp calls it
+// and every lane gets the result.  The table holds, for each quad, Q+ (upper and lower halves), Q-.
 template <bool FP16>
-__device__ __forceinline__ Two score_again(const ScoreArgs& a, const float4* table, int r, int n) {
-    const int lane = threadIdx.x & 31, columns = a.Hkv * a.D;
+__device__ __forceinline__ Two score_again(const ScoreArgs& a, const float4* table, int r, int n,
+                                           int u0, int u1) {
+    const int lane = threadIdx.x & 31, quads = a.D / 4;
     const uint16_t* base = a.bounds + ((long long)r * a.NB + n) * a.row;
     Two z = {0.f, 0.f};
-    for (int col = lane; col < columns; col += 32) {
-        const int h = col / a.D;
-        const uint16_t* p = base + col + h * a.D;
-        const float low = value<FP16>(ld(p)), high = value<FP16>(ld(p + a.D));
-        const float4 t = table[col];  // Q+, Q-
-        const float x = __fmul_rn(t.x, high), y = __fmul_rn(t.z, low);
-        z.add(x);
-        z.add(y);
-        const float ex = __fmaf_rn(t.x, high, -x), ey = __fmaf_rn(t.z, low, -y);
-        z.lo = __fadd_rn(z.lo, __fadd_rn(__fmaf_rn(t.y, high, ex), __fmaf_rn(t.w, low, ey)));
+    for (int u = u0 + lane; u < u1; u += 32) {
+        const int h = u / quads, d = 4 * (u - h * quads);
+        const uint16_t* p = base + 2 * h * a.D + d;
+        const uint2 wl = load4(p, a.vec_bounds), wh = load4(p + a.D, a.vec_bounds);
+        const float2 l[2] = {values<FP16>(wl.x), values<FP16>(wl.y)};
+        const float2 g[2] = {values<FP16>(wh.x), values<FP16>(wh.y)};
+        const float low[4] = {l[0].x, l[0].y, l[1].x, l[1].y};
+        const float high[4] = {g[0].x, g[0].y, g[1].x, g[1].y};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 t = table[4 * u + k];
+            const float x = __fmul_rn(t.x, high[k]), y = __fmul_rn(t.z, low[k]);
+            z.add(x);
+            z.add(y);
+            const float ex = __fmaf_rn(t.x, high[k], -x), ey = __fmaf_rn(t.z, low[k], -y);
+            z.lo = __fadd_rn(z.lo,
+                             __fadd_rn(__fmaf_rn(t.y, high[k], ex), __fmaf_rn(t.w, low[k], ey)));
+        }
     }
     // Both lanes of a pair compute the same sum: the larger lane's number comes second in both.
 #pragma unroll
@@ -366,8 +477,11 @@ template <bool FP16>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const ScoreArgs a) {
     extern __shared__ __align__(16) uint32_t s_keys[];  // [NB], then the table or the blocks
     __shared__ uint32_t s_hist[kBins];
-    __shared__ int s_tmp[33], s_pick[2];
-    __shared__ uint32_t s_range[2];
+    __shared__ int s_tmp[33], s_pick[4];
+    __shared__ uint32_t s_range[2], s_some[kList];
+    __shared__ int s_list[kList], s_found;
+    __shared__ float2 s_part[kList];
+    __shared__ uint64_t s_rank[kList];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int bs = blockIdx.x, b = bs / a.S, s = bs - b * a.S;
     float4* const table = reinterpret_cast<float4*>(s_keys + ((a.NB + 3) & ~3));
@@ -384,63 +498,106 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const ScoreArgs 
     if (!all && k > 0) {
         const float* scores = a.scores + (long long)bs * a.NB;
         for (int i = tid; i < nb; i += kSelectThreads) s_keys[i] = key_of(ld(scores + i));
+        if (tid == 0) s_found = 0;
         float error = 0.f;
         for (int c = lane; c < a.chunks; c += 32)
             error = fmaxf(error, ld(a.error + ((long long)b * a.chunks + c) * a.S + s));
         // bit patterns of floats >= 0 order like the floats
         error = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(error)));
         __syncthreads();
-        edge = kth_largest(s_keys, lo, hi, k, s_hist, s_tmp, s_range, s_pick);
+        edge = kth_largest(s_keys, lo, hi, k, s_hist, s_tmp, s_range, s_pick,
+                           s_some);
         // The true scores of the k-th largest and of every block lie within `error` of the sums.
         const float at = score_of(edge.key);
         const float below = __fadd_rd(at, -2.f * error), above = __fadd_ru(at, 2.f * error);
         if (below > -INFINITY && above < INFINITY) {
             uint32_t low = key_of(below), high = key_of(above);
-            int sure = 0, near = 0;
+            int both = 0;  // blocks above the band, and (upper half) within it
             for (int i = lo + tid; i < hi; i += kSelectThreads) {
-                sure += s_keys[i] > high;
-                near += s_keys[i] >= low && s_keys[i] <= high;
+                both += s_keys[i] > high ? 1 : s_keys[i] >= low ? 1 << 16 : 0;
+                if (s_keys[i] <= high && s_keys[i] >= low) {
+                    const int at = atomicAdd(&s_found, 1);
+                    if (at < kList) s_list[at] = i;  // in any order: ranked below
+                }
             }
-            sure = block_sum(sure, s_tmp);
-            near = block_sum(near, s_tmp);
-            if (near == k - sure) {
-                edge = Edge{low, near};  // all of them
-                for (int i = lo + tid; i < hi; i += kSelectThreads)
-                    if (s_keys[i] >= low && s_keys[i] <= high) s_keys[i] = low;
-                __syncthreads();
+            both = block_sum(both, s_tmp);
+            const int near = both >> 16, open = k - (both & 0xffff);
+            if (near == open) {
+                edge = Edge{low - 1, 0};  // all of them
             } else {
                 const uint16_t* q = a.q + b * a.q_stride[0] + s * a.q_stride[1];
-                for (int col = tid; col < a.Hkv * a.D; col += kSelectThreads) {
-                    Two up, down;
-                    query_sums<FP16>(a, q, col, up, down);
-                    table[col] = make_float4(up.hi, up.lo, down.hi, down.lo);
+                const int quads = a.D / 4, units = a.Hkv * quads;
+                for (int u = tid; u < units; u += kSelectThreads) {
+                    const int h = u / quads, d = 4 * (u - h * quads);
+                    Two up[4], down[4];
+                    query_sums<FP16>(a, q, h, d, up, down);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        table[4 * u + i] =
+                            make_float4(up[i].hi, up[i].lo, down[i].hi, down[i].lo);
                 }
                 __syncthreads();
-                // Twice: by the upper half of the new scores, then the blocks equal in it by the lower.
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    for (int i0 = lo + warp * 32; i0 < hi; i0 += kSelectThreads) {
-                        const int i = i0 + lane;
-                        const uint32_t key = i < hi ? s_keys[i] : 0u;
-                        const bool open = i < hi && key >= low && key <= high;
-                        if (i < hi && !open) s_keys[i] = key > high ? 0xffffffffu : 0u;
-                        unsigned todo = __ballot_sync(0xffffffffu, open);
-                        while (todo) {
-                            const int j = __ffs(todo) - 1;
-                            todo &= todo - 1;
-                            const Two z = score_again<FP16>(a, table, r, i0 + j);
-                            const uint32_t x = key_of(half == 0 ? z.hi : z.lo);
-                            if (lane == 0) s_keys[i0 + j] = min(max(x, 1u), 0xfffffffeu);
-                        }
+                if (near <= kList) {
+                    // A few: a block's sum in equal parts over the warps, then a rank for each.
+                    const int parts = near >= kSelectWarps ? 1 : kSelectWarps / near;
+                    const int each = (units + parts - 1) / parts;
+                    for (int w = warp; w < near * parts; w += kSelectWarps) {
+                        const int i = w / parts, u0 = (w - i * parts) * each;
+                        const Two z = score_again<FP16>(a, table, r, s_list[i], u0,
+                                                        min(u0 + each, units));
+                        if (lane == 0) s_part[w] = make_float2(z.hi, z.lo);
                     }
                     __syncthreads();
-                    edge = kth_largest(s_keys, lo, hi, k, s_hist, s_tmp, s_range, s_pick);
-                    int equal = 0;
-                    for (int i = lo + tid; i < hi; i += kSelectThreads)
-                        equal += s_keys[i] == edge.key;
-                    equal = block_sum(equal, s_tmp);
-                    if (equal == edge.want) break;
-                    low = high = edge.key;
+                    if (tid < near) {
+                        Two z = {0.f, 0.f};
+                        for (int i = 0; i < parts; ++i) {
+                            const float2 x = s_part[tid * parts + i];
+                            z.add(x.x);
+                            z.lo = __fadd_rn(z.lo, x.y);
+                        }
+                        z.normalise();
+                        s_rank[tid] = (uint64_t)key_of(z.hi) << 32 | key_of(z.lo);
+                    }
+                    __syncthreads();
+                    if (tid < near) {
+                        const uint64_t mine = s_rank[tid];
+                        const int me = s_list[tid];
+                        int before = 0;
+                        for (int i = 0; i < near; ++i)
+                            before += s_rank[i] > mine || (s_rank[i] == mine && s_list[i] < me);
+                        s_keys[me] = before < open ? 0xffffffffu : 0u;
+                    }
+                    edge = Edge{high, 0};
+                    __syncthreads();
+                } else {
+                    // Many (mostly equal ones): by the upper half of the new scores, then the blocks
+                    // equal in it by the lower.
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        for (int i0 = lo + warp * 32; i0 < hi; i0 += kSelectThreads) {
+                            const int i = i0 + lane;
+                            const uint32_t key = i < hi ? s_keys[i] : 0u;
+                            const bool in = i < hi && key >= low && key <= high;
+                            if (i < hi && !in) s_keys[i] = key > high ? 0xffffffffu : 0u;
+                            unsigned todo = __ballot_sync(0xffffffffu, in);
+                            while (todo) {
+                                const int j = __ffs(todo) - 1;
+                                todo &= todo - 1;
+                                const Two z = score_again<FP16>(a, table, r, i0 + j, 0, units);
+                                const uint32_t x = key_of(half == 0 ? z.hi : z.lo);
+                                if (lane == 0) s_keys[i0 + j] = min(max(x, 1u), 0xfffffffeu);
+                            }
+                        }
+                        __syncthreads();
+                        edge = kth_largest(s_keys, lo, hi, k, s_hist, s_tmp, s_range, s_pick,
+                                           s_some);
+                        int equal = 0;
+                        for (int i = lo + tid; i < hi; i += kSelectThreads)
+                            equal += s_keys[i] == edge.key;
+                        equal = block_sum(equal, s_tmp);
+                        if (equal == edge.want) break;
+                        low = high = edge.key;
+                    }
                 }
             }
         }
@@ -494,7 +651,8 @@ cudaError_t score(const ScoreArgs& a, size_t smem, cudaStream_t s) {
 
 template <bool FP16>
 cudaError_t run(const ScoreArgs& a, cudaStream_t s) {
-    const size_t smem = 4 * ((size_t)a.S * a.row + (size_t)a.wpr * a.blocks * a.S);
+    const size_t smem =
+        kRingBytes + 4 * ((size_t)a.S * a.row + (size_t)a.wpr * a.blocks * a.S);
     cudaError_t e;
     switch (a.S) {
         case 1: e = score<FP16, 1>(a, smem, s); break;
@@ -515,11 +673,14 @@ cudaError_t run(const ScoreArgs& a, cudaStream_t s) {
 }  // namespace
 
 SelectShape select_shape(int32_t batch, int32_t steps, int32_t row, int32_t NB) {
-    // Chunks of whole turns of a CTA's warps, about three CTAs an SM in all.
-    const int wpr = row > 4 * kSlice ? 8 : row > 2 * kSlice ? 4 : row > kSlice ? 2 : 1;
-    const int turn = batch_blocks(steps) * (kScoreWarps / wpr);
+    // Chunks of whole turns of a CTA's warps, as many CTAs as the SMs hold: all read from the start on,
+    // and a second wave of a few would take as long as the first.
+    const int wpr = warps_per_row(row);
+    int turn = batch_blocks(steps) * (kScoreWarps / wpr);
+    if (turn < kSelectChunk) turn = kSelectChunk;  // a multiple of either
     const int most = kMostSums / steps / turn * turn;
-    const long long want = 3 * 152 / batch > 0 ? 3 * 152 / batch : 1;
+    const long long held = score_ctas(steps) * 152;
+    const long long want = batch < held ? held / batch : 1;
     long long blocks = (NB + want - 1) / want;
     blocks = (blocks + turn - 1) / turn * turn;
     if (blocks > most) blocks = most;
@@ -547,17 +708,22 @@ cudaError_t launch_select(const hs_select_args& x, cudaStream_t s) {
     a.T = x.block_tokens;
     a.NB = (x.max_seq_len - 1) / x.block_tokens + 1;
     a.row = 2 * a.Hkv * a.D;
-    a.wpr = a.row > 4 * kSlice ? 8 : a.row > 2 * kSlice ? 4 : a.row > kSlice ? 2 : 1;
+    a.wpr = warps_per_row(a.row);
     const SelectShape sh = select_shape(a.B, a.S, a.row, a.NB);
     a.chunks = sh.chunks;
     a.blocks = sh.blocks;
     a.vec_bounds = (uintptr_t)x.bounds_dev % 16 == 0;
-    for (int i = 0; i < 3; ++i) a.q_stride[i] = x.q_stride[i];
-    // A sum's terms go through one rounding of Q, one of each fused product and sum of a lane's 8
-    // elements a slice, 5 additions over the lanes and one for each warp: half a step of 2^-23 of the
-    // sum of magnitudes each; the bound itself is a sum of as many, rounded likewise.
+    a.vec_q = (uintptr_t)x.q_dev % 8 == 0;
+    for (int i = 0; i < 3; ++i) {
+        a.q_stride[i] = x.q_stride[i];
+        a.vec_q = a.vec_q && x.q_stride[i] % 4 == 0;
+    }
+    // A sum's terms go through one rounding of Q, one of each fused product and sum of a lane's 4
+    // channels of either parity a slice, one of the parities' sum, 5 additions over the lanes and one for
+    // each warp: half a step of 2^-23 of the sum of magnitudes each; the bound itself is a sum of as many
+    // positive terms (up to 8 a slice), rounded likewise.
     const int slices = (a.row + kSlice * a.wpr - 1) / (kSlice * a.wpr);
-    a.gamma = (float)(1 + 8 * slices + 5 + a.wpr) * 0x1p-24f * 1.01f;
+    a.gamma = (float)(1 + 4 * slices + 1 + 5 + a.wpr) * 0x1p-24f * 1.01f;
     a.select = x.select;
     a.first = x.first;
     a.last = x.last;

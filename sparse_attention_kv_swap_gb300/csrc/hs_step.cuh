@@ -24,7 +24,9 @@ struct BoundArgs {
 };
 cudaError_t launch_bound(BoundArgs a, cudaStream_t s);
 
-// CTAs that score one batch entry's blocks, and the blocks of each.
+// CTAs that score one batch entry's blocks, and the blocks of each: kSelectChunk or more, which bounds the
+// workspace.
+constexpr int kSelectChunk = 8;
 struct SelectShape {
     int chunks, blocks;
 };

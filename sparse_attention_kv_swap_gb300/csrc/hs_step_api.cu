@@ -26,15 +26,15 @@ int check_select_sizes(int32_t batch, int32_t steps, int32_t max_seq_len, int32_
     if (steps > HS_MAX_STEPS || block_tokens > HS_MAX_KV_BLOCK ||
         (max_seq_len - 1) / block_tokens + 1 > HS_MAX_SELECT_BLOCKS)
         return HS_ERR_UNSUPPORTED;
-    // a chunk of a batch entry holds 32 blocks or more: its CTAs are counted in 32 bits
-    if ((long long)batch * (HS_MAX_SELECT_BLOCKS / 8) > kMaxCtas) return HS_ERR_UNSUPPORTED;
+    // CTAs are counted in 32 bits
+    if ((long long)batch * (HS_MAX_SELECT_BLOCKS / kSelectChunk) > kMaxCtas) return HS_ERR_UNSUPPORTED;
     return HS_OK;
 }
 
-// Bytes of error bounds: one for every step of a CTA that scores, at most one CTA for 8 blocks.
+// Bytes of error bounds: one for every step of a CTA that scores.
 size_t select_bytes(int32_t batch, int32_t steps, int32_t max_seq_len, int32_t block_tokens) {
     const size_t blocks = (size_t)(max_seq_len - 1) / block_tokens + 1;
-    return 4 * (size_t)batch * steps * ((blocks + 7) / 8);
+    return 4 * (size_t)batch * steps * ((blocks + kSelectChunk - 1) / kSelectChunk);
 }
 
 int check_prefix(const hs_kv_format* f, const hs_prefix_args* a) {

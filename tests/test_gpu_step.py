@@ -320,6 +320,23 @@ def test_select_largest(S, H, D, L, T):
     s.check(s.run())
 
 
+@pytest.mark.parametrize("S,H,D,L,T", [(1, 1, 32, 700, 4), (1, 64, 128, 9000, 8), (2, 16, 128, 20000, 128),
+                                       (4, 16, 256, 2500, 16), (3, 20, 128, 70, 1), (2, 1, 64, 5, 16)])
+def test_select_stays_in_workspace(S, H, D, L, T):
+    rng = np.random.default_rng(L + S)
+    B_ = 2
+    s = Select(rng, B_, S, H, 1, D, T, L, 9)
+    size = pkg.hs_select_workspace_bytes(B_, S, L, T)
+    ws = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+    topk = torch.full((B_, S, 9 * T), -7, dtype=torch.int32, device="cuda")
+    out = torch.full((B_, S, 9), -7, dtype=torch.int32, device="cuda")
+    scores = torch.full((B_, S, -(-L // T)), float("nan"), device="cuda")
+    pkg.hs_select_blocks(dev(s.q), dev(s.bounds), i32(s.req), i32(s.lens), T, L, 1, 1, out, topk,
+                         scores, ws[:size])
+    s.check((out, topk, scores))
+    assert (ws[size:] == 255).all()
+
+
 @pytest.mark.parametrize("first,last,n", [(0, 0, 1), (0, 0, 12), (5, 0, 5), (0, 5, 5), (2, 3, 5),
                                           (1, 2, 30), (0, 1, 31), (0, 0, 32), (3, 3, 33), (1, 1, 100)])
 def test_select_first_and_last(first, last, n):
