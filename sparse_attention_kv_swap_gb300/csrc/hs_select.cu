@@ -346,22 +346,17 @@ struct Edge {
     int want;      // keys equal to it that are among the k
 };
 
-// The k-th largest of keys[lo, hi), 1 <= k <= hi - lo.  All threads call it.  Counts the keys of each
-// of 1024 ranges and goes on within the one that holds the k-th, until that is a few keys, which are
-// compared one by one.
+// The k-th largest of keys[lo, hi), 1 <= k <= hi - lo.  All threads call it, each with the least and the
+// greatest of its keys: scores share their top bits, and counting by these would bring all into a few
+// bins.  Counts the keys of each of 1024 ranges and goes on within the one that holds the k-th, until
+// that is a few keys, which are compared one by one.
 __device__ __forceinline__ Edge kth_largest(const uint32_t* keys, int lo, int hi, int k,
-                                            uint32_t* hist, int* tmp, uint32_t* range, int* pick,
-                                            uint32_t* list) {
+                                            uint32_t least, uint32_t most, uint32_t* hist, int* tmp,
+                                            uint32_t* range, int* pick, uint32_t* list) {
     const int tid = threadIdx.x;
-    // The keys' range first: scores share their top bits, and counting by these would bring all into
-    // a few bins.
-    uint32_t least = 0xffffffffu, most = 0u;
-    for (int i = lo + tid; i < hi; i += kSelectThreads) {
-        least = min(least, keys[i]);
-        most = max(most, keys[i]);
-    }
     if (tid == 0) range[0] = 0xffffffffu, range[1] = 0u;
-    for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kBins; i += kSelectThreads) hist[i + tid] = 0;
     __syncthreads();
     least = __reduce_min_sync(0xffffffffu, least);
     most = __reduce_max_sync(0xffffffffu, most);
@@ -376,6 +371,7 @@ __device__ __forceinline__ Edge kth_largest(const uint32_t* keys, int lo, int hi
     uint32_t width = span;  // keys base .. base + width are counted
     int want = k;
     while (true) {
+#pragma unroll 1
         for (int i = lo + tid; i < hi; i += kSelectThreads) {
             const uint32_t x = keys[i] - base;
             if (keys[i] >= base && x <= width) atomicAdd(&hist[x >> shift], 1u);
@@ -397,6 +393,7 @@ __device__ __forceinline__ Edge kth_largest(const uint32_t* keys, int lo, int hi
             }
             above += mine[i];
         }
+#pragma unroll
         for (int i = 0; i < kOwn; ++i) hist[top + i] = 0;
         __syncthreads();
         base += (uint32_t)pick[0] << shift;
@@ -405,11 +402,13 @@ __device__ __forceinline__ Edge kth_largest(const uint32_t* keys, int lo, int hi
         width = (1u << shift) - 1;
         const int count = pick[2];
         if (count <= kList) {
+#pragma unroll 1
             for (int i = lo + tid; i < hi; i += kSelectThreads)
                 if (keys[i] >= base && keys[i] - base <= width) list[atomicAdd(&pick[3], 1)] = keys[i];
             __syncthreads();
             if (tid < count) {
                 int above = 0, equal = 0;
+#pragma unroll 1
                 for (int i = 0; i < count; ++i) {
                     above += list[i] > list[tid];
                     equal += list[i] == list[tid];
@@ -479,7 +478,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const ScoreArgs 
     __shared__ uint32_t s_hist[kBins];
     __shared__ int s_tmp[33], s_pick[4];
     __shared__ uint32_t s_range[2], s_some[kList];
-    __shared__ int s_list[kList], s_found;
+    __shared__ int s_list[kList], s_found, s_both, s_taken[kSelectWarps];
     __shared__ float2 s_part[kList];
     __shared__ uint64_t s_rank[kList];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -487,40 +486,68 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const ScoreArgs 
     float4* const table = reinterpret_cast<float4*>(s_keys + ((a.NB + 3) & ~3));
     int* const chosen = reinterpret_cast<int*>(table);
     wait_for_previous();
+    // All loads under way at once; scores past the sequence are -inf.
     const int r = ld(a.req + b);
     int n = ld(a.seq_lens + b);
-    n = r < 0 || r >= a.R || n < 0 ? 0 : min(n, a.L);
-    const int nb = (n + a.T - 1) / a.T;
-    const int lo = min(a.first, nb), hi = max(lo, nb - a.last);  // the candidates
-    const int k = a.select - a.first - a.last;                    // wanted of them
+    float error = 0.f;
+#pragma unroll 1
+    for (int c = lane; c < a.chunks; c += 32)
+        error = fmaxf(error, ld(a.error + ((long long)b * a.chunks + c) * a.S + s));
+    // bit patterns of floats >= 0 order like the floats
+    error = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(error)));
+    constexpr int kLoads = 8;
+    const float* const scores = a.scores + (long long)bs * a.NB;
+    uint32_t least = 0xffffffffu, most = 0u;
+    int nb = 0, lo = 0, hi = 0;
+#pragma unroll 1
+    for (int i0 = tid; i0 < a.NB + tid; i0 += kLoads * kSelectThreads) {
+        float x[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int i = i0 + u * kSelectThreads;
+            x[u] = i < a.NB ? ld(scores + i) : 0.f;
+        }
+        if (i0 == tid) {
+            n = r < 0 || r >= a.R || n < 0 ? 0 : min(n, a.L);
+            nb = (n + a.T - 1) / a.T;
+            lo = min(a.first, nb), hi = max(lo, nb - a.last);  // the candidates
+        }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int i = i0 + u * kSelectThreads;
+            const uint32_t key = key_of(x[u]);
+            if (i < a.NB) s_keys[i] = key;
+            if (i >= lo && i < hi) {
+                least = min(least, key);
+                most = max(most, key);
+            }
+        }
+    }
+    const int k = a.select - a.first - a.last;  // wanted of the candidates
     const bool all = nb <= a.select;
-    Edge edge = {0u, 0};
+    Edge edge = {0xffffffffu, 0};
     if (!all && k > 0) {
-        const float* scores = a.scores + (long long)bs * a.NB;
-        for (int i = tid; i < nb; i += kSelectThreads) s_keys[i] = key_of(ld(scores + i));
-        if (tid == 0) s_found = 0;
-        float error = 0.f;
-        for (int c = lane; c < a.chunks; c += 32)
-            error = fmaxf(error, ld(a.error + ((long long)b * a.chunks + c) * a.S + s));
-        // bit patterns of floats >= 0 order like the floats
-        error = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(error)));
-        __syncthreads();
-        edge = kth_largest(s_keys, lo, hi, k, s_hist, s_tmp, s_range, s_pick,
-                           s_some);
+        if (tid == 0) s_found = s_both = 0;
+        edge = kth_largest(s_keys, lo, hi, k, least, most, s_hist, s_tmp, s_range, s_pick, s_some);
         // The true scores of the k-th largest and of every block lie within `error` of the sums.
         const float at = score_of(edge.key);
         const float below = __fadd_rd(at, -2.f * error), above = __fadd_ru(at, 2.f * error);
         if (below > -INFINITY && above < INFINITY) {
             uint32_t low = key_of(below), high = key_of(above);
             int both = 0;  // blocks above the band, and (upper half) within it
+#pragma unroll 1
             for (int i = lo + tid; i < hi; i += kSelectThreads) {
-                both += s_keys[i] > high ? 1 : s_keys[i] >= low ? 1 << 16 : 0;
-                if (s_keys[i] <= high && s_keys[i] >= low) {
+                const uint32_t key = s_keys[i];
+                both += key > high ? 1 : key >= low ? 1 << 16 : 0;
+                if (key <= high && key >= low) {
                     const int at = atomicAdd(&s_found, 1);
                     if (at < kList) s_list[at] = i;  // in any order: ranked below
                 }
             }
-            both = block_sum(both, s_tmp);
+            both = __reduce_add_sync(0xffffffffu, both);
+            if (lane == 0 && both) atomicAdd(&s_both, both);
+            __syncthreads();
+            both = s_both;
             const int near = both >> 16, open = k - (both & 0xffff);
             if (near == open) {
                 edge = Edge{low - 1, 0};  // all of them
@@ -589,8 +616,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const ScoreArgs 
                             }
                         }
                         __syncthreads();
-                        edge = kth_largest(s_keys, lo, hi, k, s_hist, s_tmp, s_range, s_pick,
-                                           s_some);
+                        least = 0xffffffffu, most = 0u;
+                        for (int i = lo + tid; i < hi; i += kSelectThreads) {
+                            least = min(least, s_keys[i]);
+                            most = max(most, s_keys[i]);
+                        }
+                        edge = kth_largest(s_keys, lo, hi, k, least, most, s_hist, s_tmp, s_range,
+                                           s_pick, s_some);
                         int equal = 0;
                         for (int i = lo + tid; i < hi; i += kSelectThreads)
                             equal += s_keys[i] == edge.key;
@@ -603,37 +635,47 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const ScoreArgs 
         }
     }
     release_next();
-    // The chosen blocks in order; a thread takes consecutive ones.
-    const int per = (nb + kSelectThreads - 1) / kSelectThreads;
-    const int i0 = min(tid * per, nb), i1 = min(i0 + per, nb);
-    int both = 0;  // blocks above the edge or always taken, and (upper half) equal to it
-    if (!all) {
-        for (int i = i0; i < i1; ++i) {
-            const bool open = i >= lo && i < hi;
-            both += !open || (k > 0 && s_keys[i] > edge.key);
-            both += open && k > 0 && s_keys[i] == edge.key ? 1 << 16 : 0;
-        }
-    }
-    int total;
-    const int before = block_exclusive_scan(both, s_tmp, &total);
-    int ties = before >> 16, to = (before & 0xffff) + min(ties, edge.want);
-    if (all) to = i0;
-    for (int i = i0; i < i1; ++i) {
-        bool in = all || i < lo || i >= hi;
-        if (!in && k > 0) {
-            in = s_keys[i] > edge.key;
-            if (s_keys[i] == edge.key) in = ties++ < edge.want;
-        }
-        if (in) chosen[to++] = i;
+    // The chosen blocks in order.  A warp has consecutive ones: it counts those above the edge (or
+    // always taken) and, in the upper half of the number, those equal to it.
+    const int per = (nb + kSelectThreads - 1) / kSelectThreads * 32;
+    const int i0 = warp * per, i1 = min(i0 + per, nb);
+    const auto kind = [&](int i) {
+        if (i >= i1) return 0;
+        if (all || i < lo || i >= hi) return 1;
+        const uint32_t key = s_keys[i];
+        return key > edge.key ? 1 : key == edge.key ? 1 << 16 : 0;
+    };
+    int taken = 0;
+#pragma unroll 1
+    for (int i = i0; i < i1; i += 32) taken += kind(i + lane);
+    taken = __reduce_add_sync(0xffffffffu, taken);
+    if (lane == 0) s_taken[warp] = taken;
+    __syncthreads();
+    taken = __reduce_add_sync(0xffffffffu, lane < warp ? s_taken[lane] : 0);
+    int above = taken & 0xffff, equal = taken >> 16;
+    const unsigned below_lane = (1u << lane) - 1;
+#pragma unroll 1
+    for (int i = i0; i < i1; i += 32) {
+        const int x = kind(i + lane);
+        const unsigned ups = __ballot_sync(0xffffffffu, x == 1);
+        const unsigned ties = __ballot_sync(0xffffffffu, x > 1);
+        const int at = equal + __popc(ties & below_lane);
+        if (x == 1 || (x > 1 && at < edge.want))
+            chosen[above + __popc(ups & below_lane) + min(at, edge.want)] = i + lane;
+        above += __popc(ups);
+        equal += __popc(ties);
     }
     const int kept = min(nb, a.select);
+#pragma unroll 1
     for (int i = kept + tid; i < a.select; i += kSelectThreads) chosen[i] = -1;
     __syncthreads();
     if (a.out_blocks) {
         int32_t* out = a.out_blocks + (long long)bs * a.select;
+#pragma unroll 1
         for (int i = tid; i < a.select; i += kSelectThreads) out[i] = chosen[i];
     }
     int32_t* topk = a.topk + (long long)bs * a.select * a.T;
+#pragma unroll 1
     for (int i = tid; i < a.select * a.T; i += kSelectThreads) {
         const int j = a.by_T.of(i), block = chosen[j];
         const int t = block * a.T + (i - j * a.T);
