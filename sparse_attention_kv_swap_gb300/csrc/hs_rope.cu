@@ -38,38 +38,47 @@ struct RopeArgs {
     int32_t vec_in[2], vec_out[2], vec_weight[2];
 };
 
+// Eight consecutive elements as they lie in memory.
 template <typename T>
-__device__ __forceinline__ float to_float(T x) {
-    return (float)x;
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(Raw<T>& x, const T* p, bool vec) {
+    constexpr int kEach = 16 / sizeof(T);
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) x.v[i] = ld_once_v4(p + i * kEach);
+    } else {
+        alignas(16) T y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = ld(p + i);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) x.v[i] = reinterpret_cast<const uint4*>(y)[i];
+    }
 }
 
-// Eight consecutive elements.
 template <typename T>
-__device__ __forceinline__ void load8(float (&x)[8], const T* p, bool vec) {
-    if (vec) {
-        if constexpr (sizeof(T) == 4) {
-            const uint4 a = ld_once_v4(p), b = ld_once_v4(p + 4);
-            x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y);
-            x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
-            x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y);
-            x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
-        } else {
-            const uint4 a = ld_once_v4(p);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void decode8(float (&x)[8], const Raw<T>& raw) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(T) == 2 && __is_same(T, __half)) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                    x[2 * i] = f.x, x[2 * i + 1] = f.y;
-                } else {
-                    x[2 * i] = __uint_as_float(w[i] << 16);
-                    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-                }
-            }
+        for (int i = 0; i < 2; ++i) {
+            x[4 * i] = __uint_as_float(raw.v[i].x), x[4 * i + 1] = __uint_as_float(raw.v[i].y);
+            x[4 * i + 2] = __uint_as_float(raw.v[i].z), x[4 * i + 3] = __uint_as_float(raw.v[i].w);
         }
     } else {
+        const uint32_t w[4] = {raw.v[0].x, raw.v[0].y, raw.v[0].z, raw.v[0].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_float(ld(p + i));
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (__is_same(T, __half)) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
     }
 }
 
@@ -115,109 +124,124 @@ __device__ __forceinline__ float2 rotation(int32_t pos, int64_t turn) {
     return quadrant & 2 ? make_float2(-c, -s) : make_float2(c, s);
 }
 
+__device__ __forceinline__ void turn(float& y0, float& y1, float c, float s) {
+    const float z = y0;
+    y0 = z * c - y1 * s;
+    y1 = z * s + y1 * c;
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(const RopeArgs a) {
     constexpr int kUsed = D / 16;                                        // lanes of a head
     constexpr int kLanes = kUsed <= 2 ? 2 : kUsed <= 4 ? 4 : kUsed <= 8 ? 8 : 16;  // padded
     constexpr int kGroups = kThreads / kLanes;
-    constexpr int kAhead = 2;  // heads a lane has under way
-    extern __shared__ __align__(16) float2 s_turn[];  // [token][rot / 2]
+    // Cosines and sines, [token][4][rot / 16 lanes][2]: the 8 pairs of a lane two at a time, so that
+    // lanes side by side read side by side.
+    extern __shared__ __align__(16) float2 s_turn[];
     const int tid = threadIdx.x, lane = tid % kLanes, group = tid / kLanes;
     const int first = blockIdx.x * a.per_cta;
-    const int end = min(first + a.per_cta, a.items);
-    const int token0 = a.by_heads.of(first), tokens = a.by_heads.of(end - 1) - token0 + 1;
-    const int half = a.rot / 2;
+    const int items = min(a.per_cta, a.items - first);
+    const int token0 = a.by_heads.of(first), tokens = a.by_heads.of(first + items - 1) - token0 + 1;
+    const int half = a.rot / 2, pairs = a.rot / 16;
+    // This lane's pieces of 8 elements: a pair of them that turns together, or two that do not turn.
+    const bool turns = lane < pairs, used = lane < kUsed;
+    const int p0 = 8 * (turns ? lane : 2 * lane), p1 = turns ? p0 + half : p0 + 8;
     wait_for_previous();
+    struct Item {
+        Raw<T> x[2];
+        bool live;
+    };
+    const auto fetch = [&](Item& it, int rel) {
+        const int i = first + min(rel, items - 1);
+        const int token = a.by_heads.of(i), head = i - token * a.heads;
+        const int b = a.by_M.of(token), m = token - b * a.M;
+        it.live = used && rel < items && (!a.count || m < ld(a.count + b));
+        if (it.live) {
+            const int w = head >= a.Hq, h = head - (w ? a.Hq : 0);
+            const T* p = static_cast<const T*>(a.in[w]) + b * a.in_stride[w][0] +
+                         m * a.in_stride[w][1] + h * a.in_stride[w][2];
+            load8(it.x[0], p + p0, a.vec_in[w]);
+            load8(it.x[1], p + p1, a.vec_in[w]);
+        }
+    };
+    const auto turn_and_store = [&](const Item& it, int rel) {
+        const int i = first + min(rel, items - 1);
+        const int token = a.by_heads.of(i), head = i - token * a.heads;
+        const int w = head >= a.Hq;
+        float x[2][8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) decode8<T>(x[c], it.x[c]);
+        float r = 1.f;
+        if (a.weight[0] || a.weight[1]) {
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += x[0][k] * x[0][k] + x[1][k] * x[1][k];
+            if (!it.live) sum = 0.f;
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            r = rsqrtf(sum * (1.f / D) + a.eps);
+        }
+        if (!it.live) return;
+        if (a.weight[w]) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float* wt = a.weight[w] + (c == 0 ? p0 : p1);
+                float g[8];
+                if (a.vec_weight[w]) {
+                    const float4 v0 = ld(reinterpret_cast<const float4*>(wt));
+                    const float4 v1 = ld(reinterpret_cast<const float4*>(wt) + 1);
+                    g[0] = v0.x, g[1] = v0.y, g[2] = v0.z, g[3] = v0.w;
+                    g[4] = v1.x, g[5] = v1.y, g[6] = v1.z, g[7] = v1.w;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) g[k] = ld(wt + k);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[c][k] *= r * g[k];
+            }
+        }
+        if (turns) {
+            const float4* cs = reinterpret_cast<const float4*>(s_turn + (token - token0) * half) + lane;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 t = cs[k * pairs];
+                if (a.adjacent) {
+                    turn(x[k / 2][4 * (k % 2)], x[k / 2][4 * (k % 2) + 1], t.x, t.y);
+                    turn(x[k / 2][4 * (k % 2) + 2], x[k / 2][4 * (k % 2) + 3], t.z, t.w);
+                } else {
+                    turn(x[0][2 * k], x[1][2 * k], t.x, t.y);
+                    turn(x[0][2 * k + 1], x[1][2 * k + 1], t.z, t.w);
+                }
+            }
+        }
+        const int b = a.by_M.of(token), m = token - b * a.M;
+        const int h = head - (w ? a.Hq : 0);
+        T* p = static_cast<T*>(a.out[w]) + b * a.out_stride[w][0] + m * a.out_stride[w][1] +
+               h * a.out_stride[w][2];
+        store8(p + p0, x[0], a.vec_out[w]);
+        store8(p + p1, x[1], a.vec_out[w]);
+    };
+    // The next head of a lane group is fetched while this one is worked on; the first ones while the
+    // angles are.
+    Item here, ahead;
+    fetch(here, group);
     for (int i = tid; i < tokens * half; i += kThreads) {
         const int t = i / half, j = i - t * half;
         int x = a.axis ? ld(a.axis + j) : 0;
         x = min(max(x, 0), a.axes - 1);
-        s_turn[i] = rotation(ld(a.pos + x * a.tokens + token0 + t), ld(a.turns + j));
+        // pair j is number u of lane l
+        const int quarter = j / 4, l = a.adjacent ? quarter % pairs : j / 8;
+        const int u = a.adjacent ? quarter / pairs * 4 + j % 4 : j % 8;
+        s_turn[t * half + (u / 2 * pairs + l) * 2 + u % 2] =
+            rotation(ld(a.pos + x * a.tokens + token0 + t), ld(a.turns + j));
     }
-    // This lane's pieces of 8 elements: a pair of them that turns together, or two that do not turn.
-    const int pairs = a.rot / 16;
-    const bool turns = lane < pairs, used = lane < kUsed;
-    const int p0 = 8 * (turns ? lane : 2 * lane), p1 = turns ? p0 + half : p0 + 8;
     __syncthreads();
     release_next();
-    for (int i0 = first + group; i0 < end; i0 += kAhead * kGroups) {
-        float x[kAhead][2][8];
-        int token[kAhead], head[kAhead];
-        bool live[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u * kGroups;
-            token[u] = a.by_heads.of(i), head[u] = i - token[u] * a.heads;
-            const int b = a.by_M.of(token[u]), m = token[u] - b * a.M;
-            live[u] = used && i < end && (!a.count || m < ld(a.count + b));
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[u][0][k] = x[u][1][k] = 0.f;
-            if (live[u]) {
-                const int w = head[u] >= a.Hq, h = head[u] - (w ? a.Hq : 0);
-                const T* p = static_cast<const T*>(a.in[w]) + b * a.in_stride[w][0] +
-                             m * a.in_stride[w][1] + h * a.in_stride[w][2];
-                load8(x[u][0], p + p0, a.vec_in[w]);
-                load8(x[u][1], p + p1, a.vec_in[w]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int w = head[u] >= a.Hq;
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += x[u][0][k] * x[u][0][k] + x[u][1][k] * x[u][1][k];
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (!live[u]) continue;
-            if (a.weight[w]) {
-                const float r = rsqrtf(sum * (1.f / D) + a.eps);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float* wt = a.weight[w] + (c == 0 ? p0 : p1);
-                    float g[8];
-                    if (a.vec_weight[w]) {
-                        const float4 v0 = ld(reinterpret_cast<const float4*>(wt));
-                        const float4 v1 = ld(reinterpret_cast<const float4*>(wt) + 1);
-                        g[0] = v0.x, g[1] = v0.y, g[2] = v0.z, g[3] = v0.w;
-                        g[4] = v1.x, g[5] = v1.y, g[6] = v1.z, g[7] = v1.w;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) g[k] = ld(wt + k);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[u][c][k] *= r * g[k];
-                }
-            }
-            if (turns) {
-                const float2* cs = s_turn + (token[u] - token0) * half;
-                if (a.adjacent) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 t = cs[(c == 0 ? p0 : p1) / 2 + k];
-                            const float y0 = x[u][c][2 * k], y1 = x[u][c][2 * k + 1];
-                            x[u][c][2 * k] = y0 * t.x - y1 * t.y;
-                            x[u][c][2 * k + 1] = y0 * t.y + y1 * t.x;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float2 t = cs[p0 + k];
-                        const float y0 = x[u][0][k], y1 = x[u][1][k];
-                        x[u][0][k] = y0 * t.x - y1 * t.y;
-                        x[u][1][k] = y0 * t.y + y1 * t.x;
-                    }
-                }
-            }
-            const int b = a.by_M.of(token[u]), m = token[u] - b * a.M;
-            const int h = head[u] - (w ? a.Hq : 0);
-            T* p = static_cast<T*>(a.out[w]) + b * a.out_stride[w][0] + m * a.out_stride[w][1] +
-                   h * a.out_stride[w][2];
-            store8(p + p0, x[u][0], a.vec_out[w]);
-            store8(p + p1, x[u][1], a.vec_out[w]);
-        }
+    for (int i = 0; i < items; i += 2 * kGroups) {  // the same for all lanes of a warp
+        fetch(ahead, i + kGroups + group);
+        turn_and_store(here, i + group);
+        fetch(here, i + 2 * kGroups + group);
+        turn_and_store(ahead, i + kGroups + group);
     }
 }
 
