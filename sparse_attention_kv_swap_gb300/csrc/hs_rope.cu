@@ -19,7 +19,8 @@ namespace hs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;  // of a CTA
+constexpr int kTableBytes = 32 << 10;  // angles of a CTA's tokens, at most
+constexpr int kMaxTokens = 256, kMaxRun = 16;
 
 struct RopeArgs {
     const void* in[2];  // queries, keys
@@ -29,13 +30,13 @@ struct RopeArgs {
     float eps;
     int32_t rot, adjacent, axes, M, Hq, heads;  // heads: of queries and keys
     long long tokens;  // batch * M
-    int32_t items, per_cta;  // (token, head) pairs in all, and of a CTA
-    Divisor by_heads, by_M;
+    int32_t tile, run;  // tokens of a CTA, and of a lane group at a time
+    Divisor by_heads;
     const int32_t* pos;
     const int64_t* turns;
     const int32_t* axis;
     const int32_t* count;
-    int32_t vec_in[2], vec_out[2], vec_weight[2];
+    int32_t vec_in, vec_out;
 };
 
 // Eight consecutive elements as they lie in memory.
@@ -131,100 +132,123 @@ __device__ __forceinline__ void turn(float& y0, float& y1, float c, float s) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) norm_rope_kernel(const RopeArgs a) {
     constexpr int kUsed = D / 16;                                        // lanes of a head
     constexpr int kLanes = kUsed <= 2 ? 2 : kUsed <= 4 ? 4 : kUsed <= 8 ? 8 : 16;  // padded
     constexpr int kGroups = kThreads / kLanes;
     // Cosines and sines, [token][4][rot / 16 lanes][2]: the 8 pairs of a lane two at a time, so that
     // lanes side by side read side by side.
     extern __shared__ __align__(16) float2 s_turn[];
+    __shared__ __align__(16) float s_weight[2 * D];  // [queries, keys][4][lanes][4] likewise
     const int tid = threadIdx.x, lane = tid % kLanes, group = tid / kLanes;
-    const int first = blockIdx.x * a.per_cta;
-    const int items = min(a.per_cta, a.items - first);
-    const int token0 = a.by_heads.of(first), tokens = a.by_heads.of(first + items - 1) - token0 + 1;
+    const int tiles = (a.M + a.tile - 1) / a.tile, b = blockIdx.x / tiles;
+    const int m0 = (blockIdx.x - b * tiles) * a.tile;
     const int half = a.rot / 2, pairs = a.rot / 16;
     // This lane's pieces of 8 elements: a pair of them that turns together, or two that do not turn.
     const bool turns = lane < pairs, used = lane < kUsed;
-    const int p0 = 8 * (turns ? lane : 2 * lane), p1 = turns ? p0 + half : p0 + 8;
+    const int p0 = 8 * (turns ? lane : 2 * lane), p1 = turns ? half : 8;
     wait_for_previous();
+    const int tokens = min(a.tile, (a.count ? min(a.M, ld(a.count + b)) : a.M) - m0);
+    if (tokens <= 0) return;
+    // Heads are taken in runs of the same head of consecutive tokens, run after run of all heads.
+    const int units = (tokens + a.run - 1) / a.run * a.heads;
+    struct Cursor {
+        int unit, token, left;  // the token's number in the tile, tokens left of the run
+    };
+    const auto head_of = [&](Cursor& c) {  // starts a run
+        const int unit = min(c.unit, units - 1), sub = a.by_heads.of(unit);
+        c.token = sub * a.run;
+        c.left = a.run;
+        return unit - sub * a.heads;
+    };
+    Cursor in = {group, 0, 0}, out = in;
+    const T* from = nullptr;
+    T* to = nullptr;
+    long long from_step = 0, to_step = 0;
+    const float* weight = s_weight;
+    bool norm = false;
+    const auto enter_in = [&] {
+        const int head = head_of(in), w = head >= a.Hq, h = head - (w ? a.Hq : 0);
+        from = static_cast<const T*>(a.in[w]) + b * a.in_stride[w][0] +
+               (m0 + in.token) * a.in_stride[w][1] + h * a.in_stride[w][2] + p0;
+        from_step = a.in_stride[w][1];
+    };
+    const auto enter_out = [&] {
+        const int head = head_of(out), w = head >= a.Hq, h = head - (w ? a.Hq : 0);
+        to = static_cast<T*>(a.out[w]) + b * a.out_stride[w][0] +
+             (m0 + out.token) * a.out_stride[w][1] + h * a.out_stride[w][2] + p0;
+        to_step = a.out_stride[w][1];
+        norm = a.weight[w];
+        weight = s_weight + w * D;
+    };
     struct Item {
         Raw<T> x[2];
-        bool live;
     };
-    const auto fetch = [&](Item& it, int rel) {
-        const int i = first + min(rel, items - 1);
-        const int token = a.by_heads.of(i), head = i - token * a.heads;
-        const int b = a.by_M.of(token), m = token - b * a.M;
-        it.live = used && rel < items && (!a.count || m < ld(a.count + b));
-        if (it.live) {
-            const int w = head >= a.Hq, h = head - (w ? a.Hq : 0);
-            const T* p = static_cast<const T*>(a.in[w]) + b * a.in_stride[w][0] +
-                         m * a.in_stride[w][1] + h * a.in_stride[w][2];
-            load8(it.x[0], p + p0, a.vec_in[w]);
-            load8(it.x[1], p + p1, a.vec_in[w]);
+    const auto fetch = [&](Item& it) {
+        if (in.left == 0) enter_in();
+        if (used && in.unit < units && in.token < tokens) {
+            load8(it.x[0], from, a.vec_in);
+            load8(it.x[1], from + p1, a.vec_in);
         }
+        from += from_step;
+        ++in.token;
+        if (--in.left == 0) in.unit += kGroups;
     };
-    const auto turn_and_store = [&](const Item& it, int rel) {
-        const int i = first + min(rel, items - 1);
-        const int token = a.by_heads.of(i), head = i - token * a.heads;
-        const int w = head >= a.Hq;
+    const auto step = [&](Item& it) {
+        if (out.left == 0) enter_out();
+        const bool live = used && out.unit < units && out.token < tokens;
         float x[2][8];
 #pragma unroll
         for (int c = 0; c < 2; ++c) decode8<T>(x[c], it.x[c]);
-        float r = 1.f;
-        if (a.weight[0] || a.weight[1]) {
-            float sum = 0.f;
+        fetch(it);
+        float sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += x[0][k] * x[0][k] + x[1][k] * x[1][k];
-            if (!it.live) sum = 0.f;
+        for (int k = 0; k < 8; ++k) sum += x[0][k] * x[0][k] + x[1][k] * x[1][k];
+        if (!live) sum = 0.f;
 #pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            r = rsqrtf(sum * (1.f / D) + a.eps);
-        }
-        if (!it.live) return;
-        if (a.weight[w]) {
+        for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (live) {
+            if (norm) {
+                const float r = rsqrtf(sum * (1.f / D) + a.eps);
+                const float4* wt = reinterpret_cast<const float4*>(weight) + lane;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float* wt = a.weight[w] + (c == 0 ? p0 : p1);
-                float g[8];
-                if (a.vec_weight[w]) {
-                    const float4 v0 = ld(reinterpret_cast<const float4*>(wt));
-                    const float4 v1 = ld(reinterpret_cast<const float4*>(wt) + 1);
-                    g[0] = v0.x, g[1] = v0.y, g[2] = v0.z, g[3] = v0.w;
-                    g[4] = v1.x, g[5] = v1.y, g[6] = v1.z, g[7] = v1.w;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) g[k] = ld(wt + k);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[c][k] *= r * g[k];
-            }
-        }
-        if (turns) {
-            const float4* cs = reinterpret_cast<const float4*>(s_turn + (token - token0) * half) + lane;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 t = cs[k * pairs];
-                if (a.adjacent) {
-                    turn(x[k / 2][4 * (k % 2)], x[k / 2][4 * (k % 2) + 1], t.x, t.y);
-                    turn(x[k / 2][4 * (k % 2) + 2], x[k / 2][4 * (k % 2) + 3], t.z, t.w);
-                } else {
-                    turn(x[0][2 * k], x[1][2 * k], t.x, t.y);
-                    turn(x[0][2 * k + 1], x[1][2 * k + 1], t.z, t.w);
+                for (int k = 0; k < 4; ++k) {
+                    const float4 v = wt[k * kUsed];
+                    float* y = x[k / 2] + k % 2 * 4;
+                    y[0] *= r * v.x, y[1] *= r * v.y, y[2] *= r * v.z, y[3] *= r * v.w;
                 }
             }
+            if (turns) {
+                const float4* cs = reinterpret_cast<const float4*>(s_turn + out.token * half) + lane;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 t = cs[k * pairs];
+                    if (a.adjacent) {
+                        turn(x[k / 2][4 * (k % 2)], x[k / 2][4 * (k % 2) + 1], t.x, t.y);
+                        turn(x[k / 2][4 * (k % 2) + 2], x[k / 2][4 * (k % 2) + 3], t.z, t.w);
+                    } else {
+                        turn(x[0][2 * k], x[1][2 * k], t.x, t.y);
+                        turn(x[0][2 * k + 1], x[1][2 * k + 1], t.z, t.w);
+                    }
+                }
+            }
+            store8(to, x[0], a.vec_out);
+            store8(to + p1, x[1], a.vec_out);
         }
-        const int b = a.by_M.of(token), m = token - b * a.M;
-        const int h = head - (w ? a.Hq : 0);
-        T* p = static_cast<T*>(a.out[w]) + b * a.out_stride[w][0] + m * a.out_stride[w][1] +
-               h * a.out_stride[w][2];
-        store8(p + p0, x[0], a.vec_out[w]);
-        store8(p + p1, x[1], a.vec_out[w]);
+        to += to_step;
+        ++out.token;
+        if (--out.left == 0) out.unit += kGroups;
     };
-    // The next head of a lane group is fetched while this one is worked on; the first ones while the
-    // angles are.
-    Item here, ahead;
-    fetch(here, group);
+    // Two heads are under way ahead of the one that is worked on, the first ones while the angles are.
+    Item even, odd;
+    fetch(even);
+    fetch(odd);
+    for (int i = tid; i < 2 * D; i += kThreads) {
+        const int w = i / D, d = i - w * D, l = d / 4 % kUsed, k = d / 4 / kUsed;
+        // number 4 k + d % 4 of lane l
+        const int at = (l < pairs ? 8 * l + k / 2 * half : 16 * l + k / 2 * 8) + k % 2 * 4 + d % 4;
+        if (a.weight[w]) s_weight[i] = ld(a.weight[w] + at);
+    }
     for (int i = tid; i < tokens * half; i += kThreads) {
         const int t = i / half, j = i - t * half;
         int x = a.axis ? ld(a.axis + j) : 0;
@@ -233,15 +257,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_ke
         const int quarter = j / 4, l = a.adjacent ? quarter % pairs : j / 8;
         const int u = a.adjacent ? quarter / pairs * 4 + j % 4 : j % 8;
         s_turn[t * half + (u / 2 * pairs + l) * 2 + u % 2] =
-            rotation(ld(a.pos + x * a.tokens + token0 + t), ld(a.turns + j));
+            rotation(ld(a.pos + x * a.tokens + (long long)b * a.M + m0 + t), ld(a.turns + j));
     }
     __syncthreads();
     release_next();
-    for (int i = 0; i < items; i += 2 * kGroups) {  // the same for all lanes of a warp
-        fetch(ahead, i + kGroups + group);
-        turn_and_store(here, i + group);
-        fetch(here, i + 2 * kGroups + group);
-        turn_and_store(ahead, i + kGroups + group);
+    const int steps = (units + kGroups - 1) / kGroups * a.run;  // the same for all lanes
+    for (int i = 0; i < steps; i += 2) {
+        step(even);
+        if (i + 1 < steps) step(odd);
     }
 }
 
@@ -250,15 +273,21 @@ cudaError_t run(RopeArgs a, cudaStream_t s) {
     constexpr int kUsed = D / 16;
     constexpr int kLanes = kUsed <= 2 ? 2 : kUsed <= 4 ? 4 : kUsed <= 8 ? 8 : 16;
     constexpr int kGroups = kThreads / kLanes;
-    // Heads of a lane group: one while that fills the SMs, more where the angles of a token serve many
-    // heads.
-    long long each = a.items / ((long long)kGroups * 152 * 4);
-    each = each < 1 ? 1 : each > 8 ? 8 : each;
-    while (each > 1 && each * kGroups / a.heads + 2 > kMaxTokens) --each;
-    a.per_cta = (int)each * kGroups;
-    if (a.per_cta / a.heads + 2 > kMaxTokens) a.per_cta = (kMaxTokens - 2) * a.heads;
-    const size_t smem = (size_t)(a.per_cta / a.heads + 2) * (a.rot / 2) * sizeof(float2);
-    const int grid = (a.items - 1) / a.per_cta + 1;
+    // A CTA takes all heads of a tile of tokens, as large as fills the SMs and the table holds: no
+    // angle is computed twice.  A run reads a weight once and steps through memory; four
+    // rounds of runs spread the heads over the lane groups evenly enough.
+    const int half = a.rot / 2;
+    const auto largest = [](long long x, long long most) {  // power of two up to x and most
+        int p = 1;
+        while (2 * p <= x && 2 * p <= most) p *= 2;
+        return p;
+    };
+    const long long held = half ? kTableBytes / (half * (int)sizeof(float2)) : kMaxTokens;
+    a.tile = largest(a.tokens / (152 * 4), held < kMaxTokens ? held : kMaxTokens);
+    while (a.tile >= 2 * a.M) a.tile /= 2;
+    a.run = largest((long long)a.tile * a.heads / (4 * kGroups), a.tile < kMaxRun ? a.tile : kMaxRun);
+    const size_t smem = (size_t)a.tile * half * sizeof(float2);
+    const int grid = (int)(a.tokens / a.M * ((a.M + a.tile - 1) / a.tile));
     return launch_chained(norm_rope_kernel<T, D>, grid, kThreads, smem, 0, s, a);
 }
 
@@ -284,18 +313,19 @@ cudaError_t launch_norm_rope(const hs_norm_rope_args& x, cudaStream_t s) {
     void* out[2] = {x.q_out_dev, x.k_out_dev};
     const float* weight[2] = {x.q_weight_dev, x.k_weight_dev};
     const int64_t* strides[4] = {x.q_stride, x.k_stride, x.q_out_stride, x.k_out_stride};
+    a.vec_in = a.vec_out = 1;
     for (int w = 0; w < 2; ++w) {
         a.in[w] = in[w];
         a.out[w] = out[w];
         a.weight[w] = weight[w];
-        a.vec_in[w] = (uintptr_t)in[w] % 16 == 0;
-        a.vec_out[w] = (uintptr_t)out[w] % 16 == 0;
-        a.vec_weight[w] = (uintptr_t)weight[w] % 16 == 0;
+        a.vec_in &= (uintptr_t)in[w] % 16 == 0;
+        a.vec_out &= (uintptr_t)out[w] % 16 == 0;
+        if (!(w ? x.num_kv_heads : x.num_heads)) continue;
         for (int i = 0; i < 3; ++i) {
             a.in_stride[w][i] = strides[w][i];
             a.out_stride[w][i] = strides[2 + w][i];
-            a.vec_in[w] = a.vec_in[w] && strides[w][i] * esz % 16 == 0;
-            a.vec_out[w] = a.vec_out[w] && strides[2 + w][i] * esz % 16 == 0;
+            a.vec_in &= strides[w][i] * esz % 16 == 0;
+            a.vec_out &= strides[2 + w][i] * esz % 16 == 0;
         }
     }
     a.eps = x.eps;
@@ -306,9 +336,7 @@ cudaError_t launch_norm_rope(const hs_norm_rope_args& x, cudaStream_t s) {
     a.Hq = x.num_heads;
     a.heads = x.num_heads + x.num_kv_heads;
     a.tokens = (long long)x.batch * x.tokens;
-    a.items = (int32_t)(a.tokens * a.heads);
     a.by_heads = Divisor::by(a.heads);
-    a.by_M = Divisor::by(a.M);
     a.pos = x.pos_dev;
     a.turns = x.turns_dev;
     a.axis = x.axis_dev;
