@@ -737,7 +737,7 @@ typedef struct hs_prefix_args {
     int64_t out_stride[3];
     int64_t join_stride[3];      /* of join_out                                              */
     const void* rows_dev;        /* uint8 [R, L, W], 16-byte aligned: a store as hs_quantize_kv
-                                    writes it                                                */
+                                    writes it, in device memory                              */
     const float* scales_dev;     /* [R, NB, 2, Hkv]                                          */
     const int32_t* prefix_dev;   /* [P]: the store's request that holds prefix p             */
     const int32_t* lens_dev;     /* [P]: its tokens                                          */
@@ -770,10 +770,13 @@ size_t hs_prefix_workspace_bytes(const hs_kv_format* fmt, const hs_prefix_args* 
  * Products of codes and queries are exact (but for query elements under 2^-28 of their head's
  * largest, which are off by 2^-39 of that at most) and summed in 32 bits; the softmax statistics
  * are 32 bits; each weight times its V scale is rounded to 11 bits for the product with the V
- * codes (or by 2^-36 of the largest such term, if that is more).
+ * codes (or by 2^-34 of the largest such term, if that is more; V scales up to about 2^100).
  * A NaN code in the prefix spoils the outputs of the heads that read it, an infinity or a NaN in a
  * query those of its head.  Outputs do not depend on timing.
- * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_KV_HEADS query heads or HS_MAX_PREFIXES.
+ * The kernel holds the tensor memory of the SMs it runs on until it ends; it waits for nothing but
+ * its own copies and products.
+ * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_KV_HEADS query heads or HS_MAX_PREFIXES, for 2^31 tiles of
+ * queries and tokens or more, or for a store of 2^40 bytes a request or more.
  * Should a wait inside the kernel ever give up, the outputs it would have written are NaN.
  * Asynchronous on `stream`. */
 int hs_attend_prefix(const hs_kv_format* fmt, const hs_prefix_args* args, void* stream);

@@ -118,6 +118,71 @@ class SwapInCache:
                     o.get("workspace"), stream)
         return o
 
+    # ---- selection by bounds on the keys, shared prefixes -----------------------
+
+    def key_bounds(self, fmt: B.HsKvFormat, dtype: torch.dtype, block_tokens: int) -> torch.Tensor:
+        """Bounds on one layer's keys, which are of `dtype`: [R, NB, Hkv, 2, D]."""
+        return torch.zeros(B.bounds_shape(self.cfg.num_requests, self.cfg.max_seq_len, block_tokens,
+                                          fmt.num_kv_heads, fmt.head_dim), dtype=dtype,
+                           device=self.device)
+
+    def bound_keys(self, bounds: torch.Tensor, block_tokens: int, k: torch.Tensor,
+                   req: torch.Tensor, start: torch.Tensor, count: torch.Tensor,
+                   stream=None) -> None:
+        """Brings new keys [batch, tokens, Hkv, D], those of append_kv, into their blocks' bounds.
+        (evict moves keys to other blocks: those of a sequence that it cut are brought anew, all of
+        them from token 0.)"""
+        B.hs_bound_keys(k, req, start, count, block_tokens, self.cfg.max_seq_len, bounds, stream)
+
+    def select_blocks(self, bounds: torch.Tensor, block_tokens: int, q: torch.Tensor,
+                      req_pool_indices: torch.Tensor, seq_lens: torch.Tensor, first: int = 1,
+                      last: int = 1, out: Optional[Dict[str, torch.Tensor]] = None, stream=None):
+        """The top-k tokens for swap_in, as whole blocks, for q [batch, steps, heads, D]: the first
+        `first` blocks, the last `last` and those of the largest bounds on their scores."""
+        if block_tokens < 1 or self.cfg.top_k % block_tokens:
+            raise ValueError("the cache's top_k (%d) must be a multiple of block_tokens (%d)"
+                             % (self.cfg.top_k, block_tokens))
+        Bn, S = q.shape[:2]
+        o = dict(out or {})
+        with self._allocate_on(stream):
+            if "topk" not in o:
+                o["topk"] = torch.empty((Bn, S, self.cfg.top_k), dtype=torch.int32,
+                                        device=self.device)
+            if "scores" not in o:
+                o["scores"] = torch.empty((Bn, S, bounds.shape[1]), device=self.device)
+            if "select_workspace" not in o:
+                o["select_workspace"] = torch.empty(
+                    B.hs_select_workspace_bytes(Bn, S, self.cfg.max_seq_len, block_tokens),
+                    dtype=torch.uint8, device=self.device)
+        B.hs_select_blocks(q, bounds, req_pool_indices, seq_lens, block_tokens,
+                           self.cfg.max_seq_len, first, last, o.get("blocks"), o["topk"],
+                           o["scores"], o["select_workspace"], stream)
+        return o
+
+    def attend_prefix(self, fmt: B.HsKvFormat, rows: torch.Tensor, scales: torch.Tensor,
+                      q: torch.Tensor, prefix: torch.Tensor, lens: torch.Tensor,
+                      starts: torch.Tensor, join: Optional[Dict[str, torch.Tensor]] = None,
+                      sm_scale: Optional[float] = None,
+                      out: Optional[Dict[str, torch.Tensor]] = None, stream=None):
+        """Attention of q over prefixes that consecutive batch rows share, kept in device memory
+        (rows [P, tokens, W] and their scales, as hs_quantize_kv writes them); join: what attend
+        returned for the same q with lse=True, which is joined in."""
+        Bn, S, heads = q.shape[:3]
+        o = dict(out or {})
+        with self._allocate_on(stream):
+            if "out" not in o:
+                o["out"] = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+            if "lse" not in o:
+                o["lse"] = torch.empty(q.shape[:3], device=self.device)
+            if "workspace" not in o:
+                o["workspace"] = torch.empty(
+                    B.hs_prefix_workspace_bytes(fmt, Bn, S, heads, prefix.shape[0]),
+                    dtype=torch.uint8, device=self.device)
+        B.hs_attend_prefix(fmt, q, rows, scales, prefix, lens, starts, o["out"], o["lse"],
+                           None if join is None else join["out"],
+                           None if join is None else join["lse"], sm_scale, o["workspace"], stream)
+        return o
+
     def evict(self, fmt: B.HsKvFormat, scales: List[torch.Tensor], acc: List[torch.Tensor],
               requests: List[int], seq_lens: List[int], budget: int, recent: int,
               stream=None) -> List[int]:

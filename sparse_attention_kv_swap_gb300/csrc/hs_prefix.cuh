@@ -36,7 +36,6 @@
 
 namespace hs {
 
-constexpr int kPrefixRows = 128;  // of a pipeline
 constexpr int kPrefixCtas = 256;  // at most
 
 struct PrefixArgs {
@@ -63,7 +62,6 @@ struct PrefixArgs {
 };
 
 constexpr int prefix_pipes(int D) { return D <= 128 ? 2 : 1; }
-constexpr int kPrefixTokens = 64;  // of a tile
 constexpr int prefix_panels(int D) { return (D + 63) / 64; }
 
 // The store as the copies see it: [R][L][W] bytes, in boxes of so many tokens and bytes of a head.
@@ -255,7 +253,7 @@ __device__ __forceinline__ void fence_after() {
 // What this thread has written to shared memory, or seen written by others, is seen by the matrix
 // instructions that follow: this thread's, or those of threads that it lets go after.  It waits for
 // this thread's loads: the converters, which always have some under way, leave it to the warp
-// that issues (with theirs, a tile took 5000 cycles instead of XXXX).
+// that issues (with theirs, a tile took 5000 cycles).
 __device__ __forceinline__ void fence_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

@@ -33,6 +33,9 @@ struct SelectShape {
 SelectShape select_shape(int32_t batch, int32_t steps, int32_t row, int32_t NB);
 cudaError_t launch_select(const hs_select_args& a, cudaStream_t s);
 
+// Rows of queries that a pipeline of the prefix kernel takes at a time, and tokens of a tile.
+constexpr int kPrefixRows = 128;
+constexpr int kPrefixTokens = 64;
 size_t prefix_workspace(const hs_kv_format& f);
 cudaError_t launch_prefix(const hs_kv_format& f, const hs_prefix_args& a, cudaStream_t s);
 

@@ -170,6 +170,13 @@ int hs_attend_prefix(const hs_kv_format* fmt, const hs_prefix_args* a, void* str
     if (a->dtype != HS_DTYPE_BF16 && a->dtype != HS_DTYPE_FP16) return HS_ERR_INVALID_ARG;
     if (a->num_requests < 1 || a->max_seq_len < 1 || !a->join_out_dev != !a->join_lse_dev)
         return HS_ERR_INVALID_ARG;
+    // tiles of rows and tokens are counted in 32 bits; a copy's strides have 40
+    const long long rows = (long long)a->batch * a->steps * (a->num_heads / fmt->num_kv_heads);
+    const long long tiles = (a->max_seq_len - 1) / kPrefixTokens + 1;
+    const long long row_tiles = (rows + kPrefixRows - 1) / kPrefixRows + a->num_prefixes;
+    if (row_tiles * fmt->num_kv_heads > INT32_MAX / tiles ||
+        (long long)fmt->item_size_bytes > ((1ll << 40) - 1) / a->max_seq_len)
+        return HS_ERR_UNSUPPORTED;
     if (a->batch == 0) return HS_OK;
     if (!a->q_dev || !a->out_dev) return HS_ERR_INVALID_ARG;
     if (a->num_prefixes > 0 && (!a->rows_dev || !a->scales_dev || !a->prefix_dev || !a->lens_dev ||

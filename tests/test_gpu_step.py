@@ -781,3 +781,86 @@ def test_step_repeats_streams_and_graphs():
     for other in [again] + held:
         for x, y in zip(first[:8], other[:8]):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("code,dtype,heads,group,D,T", [("e4m3", "bf16", 2, 4, 64, 16),
+                                                        ("int8", "fp16", 3, 2, 96, 16)])
+def test_decode_example(code, dtype, heads, group, D, T):
+    """The example's loop, each call by the tensors it was given: rotated heads within their bounds,
+    codes, scales, key bounds and selection exactly, the attention over the selected rows and the
+    one joined with the shared prompt's within their bounds."""
+    import importlib.util
+    import pathlib
+    import kv_reference as kvref
+    path = pathlib.Path(__file__).resolve().parent.parent / "examples" / "decode_selected.py"
+    spec = importlib.util.spec_from_file_location("decode_selected", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    rng = np.random.default_rng(25)
+    R, limit, shared, blocks = 3, 150, 77, 4
+    d = example.SelectingDecoder(R, limit, shared, blocks, heads, group, D, T, CODES[code],
+                                 DTYPES[dtype])
+    d.weight = [dev(1 + 0.3 * rng.standard_normal(D).astype(np.float32)) for _ in range(2)]
+    pool = d.cache.host_pools[0]
+    pool.zero_()
+    rows, scales = pool.clone(), torch.zeros_like(d.scales, device="cpu")
+    bounds = d.bounds.cpu().double().numpy()
+    req = np.arange(R, dtype=np.int32)
+
+    def turned(x, w, first, got):
+        r = Rotate.__new__(Rotate)
+        r.freq, r.axis, r.adjacent = ref.frequencies(D), [0] * (D // 2), False
+        r.dtype, r.D, r.eps, r.w = dtype, D, 1e-6, [w, w]
+        r.pos = (np.asarray(first)[:, None] + np.arange(x.shape[1])).astype(np.int32)[None]
+        r.q = r.k = x
+        r.check((got, got))
+
+    def append(k, v, start, count):
+        kvref.quantize(k, v, req, start, count, rows, scales, T, code)
+        ref.bound(k.double().numpy(), req, start, count, T, limit, bounds)
+        assert torch.equal(pool, rows) and torch.equal(d.scales.cpu(), scales)
+        assert np.array_equal(d.bounds.cpu().double().numpy(), bounds)
+
+    w = [x.cpu().numpy() for x in d.weight]
+    k, v = randn(rng, (1, shared, heads, D), dtype), randn(rng, (1, shared, heads, D), dtype)
+    ks = d.share(dev(k), dev(v))
+    turned(k, w[1], [0], ks)
+    srows, sscales = torch.zeros_like(d.rows, device="cpu"), torch.zeros_like(d.shared_scales,
+                                                                             device="cpu")
+    kvref.quantize(ks.cpu(), v, [0], [0], [shared], srows, sscales, T, code)
+    assert torch.equal(d.rows.cpu(), srows) and torch.equal(d.shared_scales.cpu(), sscales)
+    lens = np.array([140, 9, 97], dtype=np.int32)
+    k, v = randn(rng, (R, 140, heads, D), dtype), randn(rng, (R, 140, heads, D), dtype)
+    ks = d.prompt(dev(k), dev(v), i32(lens))
+    torch.cuda.synchronize()
+    turned(k, w[1], [shared] * R, ks)
+    append(ks.cpu(), v, [0] * R, lens)
+    for step in range(10):
+        q = randn(rng, (R, 1, heads * group, D), dtype)
+        k, v = randn(rng, (R, 1, heads, D), dtype), randn(rng, (R, 1, heads, D), dtype)
+        d.step(dev(q), dev(k), dev(v))
+        torch.cuda.synchronize()
+        turned(q, w[0], shared + lens, d.q)
+        turned(k, w[1], shared + lens, d.k)
+        append(d.k.cpu(), v, lens, [1] * R)
+        lens += 1
+        dq = d.q.cpu().double().numpy()
+        score, _ = ref.scores(dq, bounds, req, lens, T, limit)
+        topk = ref.select(score, lens, req, R, T, limit, blocks, 1, 1)[1]
+        assert np.array_equal(d.selected["topk"].cpu().numpy(), topk)
+        # over the selected rows, as one prefix for each request
+        a = Prefix.__new__(Prefix)
+        a.H, a.G, a.D, a.T, a.code, a.dtype = heads, group, D, T, code, dtype
+        a.lens = np.array([(topk[b] >= 0).sum() for b in range(R)])
+        part = [ref.attend(dq[b:b + 1], rows[b:b + 1].numpy()[:, topk[b, 0, :a.lens[b]]],
+                           np.ascontiguousarray(scales[b:b + 1].numpy()[:, topk[b, 0, :a.lens[b]] // T]),
+                           [0], [a.lens[b]], [0, 1], 1, heads, code, D ** -0.5) for b in range(R)]
+        want = {x: np.concatenate([y[x] for y in part]) for x in part[0]}
+        a.check((d.own["out"], d.own["lse"]), want)
+        a.lens = np.array([shared])
+        want = ref.attend(dq, srows.numpy(), sscales.numpy(), [0], [shared], [0, R], T, heads, code,
+                          D ** -0.5, (d.own["out"].cpu().double().numpy(),
+                                      d.own["lse"].cpu().double().numpy()))
+        a.check((d.out["out"], d.out["lse"]), want)
+    assert d.cache.status() == (B.HS_OK, 0)
+    d.cache.close()

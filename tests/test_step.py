@@ -171,6 +171,12 @@ def test_attend_prefix_refuses(lib):
         assert call(**kw) == bad, kw
     for kw in (dict(num_heads=130), dict(num_prefixes=257), dict(batch=1 << 30)):
         assert call(**kw) == unsupported, kw
+    # tiles: 2 heads, (batch * 8 rows of a head / 128 + 2) by (max_seq_len / 64)
+    for kw in (dict(batch=1 << 17, steps=2, max_seq_len=2 ** 31 - 1),
+               dict(batch=1 << 24, steps=2, max_seq_len=1 << 16)):
+        assert call(**kw) == unsupported, kw
+    wide = pkg.make_kv_format(2, 64, 16, item_size_bytes=1024)
+    assert call(f=wide, max_seq_len=1 << 30) == unsupported
     assert call(batch=0, q_dev=None) == B.HS_OK
     assert pkg.hs_prefix_workspace_bytes(fmt, 0, 1, 8, 1) == 0
     assert pkg.hs_prefix_workspace_bytes(fmt, 4, 1, 8, 1) > 0
@@ -256,6 +262,23 @@ def test_binding_refuses_shapes(lib):
                dict(join_out=q[:, :, :4], join_lse=lse), dict(join_out=q, join_lse=lse[:1]), dict()):
         with pytest.raises(ValueError):
             prefix(**kw)
+
+
+def test_cache_refuses():
+    from sparse_attention_kv_swap_gb300.cache import SwapInCache
+    cache = SwapInCache.__new__(SwapInCache)  # the sizes alone are looked at
+    cache.cfg, cache.device = pkg.make_config(4, 70, 256, 48, 48, 1), torch.device("cpu")
+    fmt = pkg.make_kv_format(2, 64, 16)
+    bounds = cache.key_bounds(fmt, torch.bfloat16, 16)
+    assert bounds.shape == (4, 5, 2, 2, 64) and bounds.dtype is torch.bfloat16
+    q, one = torch.zeros((2, 3, 8, 64), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for T in (0, -1, 32, 96):
+        with pytest.raises(ValueError):
+            cache.select_blocks(bounds, T, q, one, one)
+    with pytest.raises(ValueError):
+        cache.select_blocks(bounds[:, 1:], 16, q, one, one)
+    with pytest.raises(ValueError):
+        cache.bound_keys(bounds, 16, q, one, one, one)
 
 
 # ---- the plain implementation itself ---------------------------------------------------
