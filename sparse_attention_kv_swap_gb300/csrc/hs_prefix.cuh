@@ -214,23 +214,22 @@ __device__ __forceinline__ void load_columns(uint32_t (&x)[32], uint32_t at) {
         : "r"(at)
         : "memory");
 }
+__device__ __forceinline__ void load_columns(uint32_t (&x)[16], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+          "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
+          "=r"(x[14]), "=r"(x[15])
+        : "r"(at)
+        : "memory");
+}
 // The loaded values may be used after this.
-__device__ __forceinline__ void loaded(uint32_t (&x)[32]) {
+template <int N>
+__device__ __forceinline__ void loaded(uint32_t (&x)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(x[i]));
-}
-__device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-        "%28, %29, %30, %31, %32};" ::"r"(at),
-        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]),
-        "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]),
-        "r"(x[15]), "r"(x[16]), "r"(x[17]), "r"(x[18]), "r"(x[19]), "r"(x[20]), "r"(x[21]),
-        "r"(x[22]), "r"(x[23]), "r"(x[24]), "r"(x[25]), "r"(x[26]), "r"(x[27]), "r"(x[28]),
-        "r"(x[29]), "r"(x[30]), "r"(x[31])
-        : "memory");
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i]));
 }
 __device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[16]) {
     asm volatile(
@@ -414,83 +413,105 @@ struct Product {
     volatile int* gave_up;
 };
 
-// The reference moves to `want`: O and l with it.  The whole warp calls it.
+// The two warps that share rows, a half of a tile's tokens (and of O's columns) each.
+struct Twins {
+    int id;                // named barrier
+    float* mine;           // this row's places in shared memory
+    const float* other;
+    __device__ __forceinline__ void sync() const {
+        asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+    }
+    // Whether x holds for a row of either warp.
+    __device__ __forceinline__ bool any(bool x) const {
+        uint32_t y;
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n"
+            " selp.u32 %0, 1, 0, q;\n}"
+            : "=r"(y)
+            : "r"((uint32_t)x), "r"(id)
+            : "memory");
+        return y != 0;
+    }
+    // The larger of both halves'.  A barrier must come before the next call.
+    __device__ __forceinline__ float larger(float x) const {
+        *mine = x;
+        sync();
+        return fmaxf(x, *other);
+    }
+};
+
+// The reference moves to what the halves want, if one of them has outgrown it: O and l with it.  Both
+// warps call it, once a tile, with their S in registers: P may be written over S after it.
 template <int D>
 __device__ __forceinline__ void move_reference(uint32_t o_col, float want, const Product& before,
-                                               float& ref, float& l) {
+                                               const Twins& twins, float& ref, float& l) {
+    if (!twins.any(before.none || want > ref + kRoom)) return;
+    want = twins.larger(want);
     if (before.none) {
         ref = want;
         return;
     }
     const bool grow = want > ref + kRoom;
-    if (!__any_sync(0xffffffffu, grow)) return;
     const float by = grow ? exp2_fast(ref - want) : 1.f;
     l *= by;
     if (grow) ref = want;
     wait(before.done, before.parity, before.gave_up);
     fence_after();
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-        uint32_t x[32];
+    for (int c = 0; c < D / 2; c += 16) {
+        uint32_t x[16];
         load_columns(x, o_col + c);
         loaded(x);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * by);
+        for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * by);
         store_columns(o_col + c, x);
     }
 }
 
-// One tile of a row: S is replaced by P.  Any scales and any number of live tokens.
-template <int TOK, int D>
-__device__ __forceinline__ void softmax_any(uint32_t s_col, uint32_t o_col, float f,
+// Half a tile of a row: S is replaced by P.  Any scales and any number of live tokens.
+template <int D>
+__device__ __forceinline__ void softmax_any(uint32_t s_col, uint32_t p_col, uint32_t o_col, float f,
                                             const float* s_k, const float* s_v, const float* s_log,
-                                            int live, const Product& before, float& ref, float& l) {
+                                            int live, const Product& before, const Twins& twins,
+                                            float& ref, float& l) {
+    uint32_t x[32];
+    load_columns(x, s_col);
+    loaded(x);
     // The largest score, and the largest of score + log2(V scale).
     float top = -INFINITY, most = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < TOK; c += 32) {
-        uint32_t x[32];
-        load_columns(x, s_col + c);
-        loaded(x);
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(s_k + c + k);
-            const float4 lg = *reinterpret_cast<const float4*>(s_log + c + k);
-            const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, ll[4] = {lg.x, lg.y, lg.z, lg.w};
+    for (int k = 0; k < 32; k += 4) {
+        const float4 ks = *reinterpret_cast<const float4*>(s_k + k);
+        const float4 lg = *reinterpret_cast<const float4*>(s_log + k);
+        const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, ll[4] = {lg.x, lg.y, lg.z, lg.w};
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float z = __uint_as_float(x[k + m]) * kk[m] * f;
-                if (c + k + m < live) {
-                    most = fmaxf(most, z + ll[m]);
-                    top = fmaxf(top, z);
-                }
+        for (int m = 0; m < 4; ++m) {
+            const float z = __uint_as_float(x[k + m]) * kk[m] * f;
+            x[k + m] = __float_as_uint(z);
+            if (k + m < live) {
+                most = fmaxf(most, z + ll[m]);
+                top = fmaxf(top, z);
             }
         }
     }
-    move_reference<D>(o_col, fmaxf(most - kTop, top - 100.f), before, ref, l);
-#pragma unroll 1
-    for (int c = 0; c < TOK; c += 32) {
-        uint32_t x[32], y[16];
-        load_columns(x, s_col + c);
-        loaded(x);
+    move_reference<D>(o_col, fmaxf(most - kTop, top - 100.f), before, twins, ref, l);
+    uint32_t y[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(s_k + c + k);
-            const float4 vs = *reinterpret_cast<const float4*>(s_v + c + k);
-            const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, vv[4] = {vs.x, vs.y, vs.z, vs.w};
-            float e[4];
+    for (int k = 0; k < 32; k += 4) {
+        const float4 vs = *reinterpret_cast<const float4*>(s_v + k);
+        const float vv[4] = {vs.x, vs.y, vs.z, vs.w};
+        float e[4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                e[m] = exp2_fast(__uint_as_float(x[k + m]) * kk[m] * f - ref);
-                if (c + k + m >= live) e[m] = 0.f;
-                l += e[m];
-                e[m] *= vv[m];
-            }
-            y[k / 2] = pack_half2(e[0], e[1]);
-            y[k / 2 + 1] = pack_half2(e[2], e[3]);
+        for (int m = 0; m < 4; ++m) {
+            e[m] = exp2_fast(__uint_as_float(x[k + m]) - ref);
+            if (k + m >= live) e[m] = 0.f;
+            l += e[m];
+            e[m] *= vv[m];
         }
-        store_columns(s_col + c / 2, y);
+        y[k / 2] = pack_half2(e[0], e[1]);
+        y[k / 2 + 1] = pack_half2(e[2], e[3]);
     }
+    store_columns(p_col, y);
 }
 
 // a * b + c for two pairs at once.
@@ -514,62 +535,56 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
 // The same for whole tiles whose scales are equal in each 16 tokens, V scales of 2^-60 or more
 // and K scales >= 0: the scales leave the loops.  p_t v_t comes out of the exponential at
 // once, 2^(z_t + log2 v - r), and l takes the sum of 16 by 1 / v.
-template <int TOK>
 struct Even {  // of 16 tokens each: factor of the products, log2 of the V scale, its reciprocal
-    float k[TOK / 16], log[TOK / 16], inverse[TOK / 16];
+    float k[2], log[2], inverse[2];
     __device__ __forceinline__ Even(const float4* s_even, float f) {
 #pragma unroll
-        for (int i = 0; i < TOK / 16; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const float4 x = s_even[i];
             k[i] = x.x * f, log[i] = x.y, inverse[i] = x.z;
         }
     }
 };
-template <int TOK, int D>
-__device__ __forceinline__ void softmax_even(uint32_t s_col, uint32_t o_col, const Even<TOK>& scale,
-                                             const Product& before, float& ref, float& l) {
-    constexpr int kSteps = TOK / 32;
-    uint32_t x[kSteps][32];
-#pragma unroll
-    for (int c = 0; c < kSteps; ++c) load_columns(x[c], s_col + c * 32);
-#pragma unroll
-    for (int c = 0; c < kSteps; ++c) loaded(x[c]);
+template <int D>
+__device__ __forceinline__ void softmax_even(uint32_t s_col, uint32_t p_col, uint32_t o_col,
+                                             const Even& scale, const Product& before,
+                                             const Twins& twins, float& ref, float& l) {
+    uint32_t x[32];
+    load_columns(x, s_col);
+    loaded(x);
     float most = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < TOK / 16; ++c) {
-        const uint32_t* z = &x[c / 2][c % 2 * 16];
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t* z = x + 16 * h;
         float m[4];  // four chains
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             m[k] = fmaxf(fmaxf(__uint_as_float(z[k]), __uint_as_float(z[k + 4])),
                          fmaxf(__uint_as_float(z[k + 8]), __uint_as_float(z[k + 12])));
         m[0] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-        most = fmaxf(most, fmaf(m[0], scale.k[c], scale.log[c]));
+        most = fmaxf(most, fmaf(m[0], scale.k[h], scale.log[h]));
     }
-    move_reference<D>(o_col, most - kTop, before, ref, l);
+    move_reference<D>(o_col, most - kTop, before, twins, ref, l);
+    uint32_t w[16];
 #pragma unroll
-    for (int c = 0; c < kSteps; ++c) {
-        uint32_t w[16];
+    for (int h = 0; h < 2; ++h) {
+        const float k0 = scale.k[h], o0 = scale.log[h] - ref;
+        const float2 kk = make_float2(k0, k0), off = make_float2(o0, o0);
+        float2 sum[2] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float k0 = scale.k[2 * c + h], o0 = scale.log[2 * c + h] - ref;
-            const float2 kk = make_float2(k0, k0), off = make_float2(o0, o0);
-            float2 sum[2] = {};
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-                float2 e = make_float2(__uint_as_float(x[c][16 * h + k]),
-                                       __uint_as_float(x[c][16 * h + k + 1]));
-                e = fma_pair(e, kk, off);
-                e.x = exp2_fast(e.x);
-                e.y = exp2_fast(e.y);
-                sum[k / 2 & 1] = add_pair(sum[k / 2 & 1], e);
-                w[8 * h + k / 2] = pack_half2(e.x, e.y);
-            }
-            sum[0] = add_pair(sum[0], sum[1]);
-            l = fmaf(sum[0].x + sum[0].y, scale.inverse[2 * c + h], l);
+        for (int k = 0; k < 16; k += 2) {
+            float2 e = make_float2(__uint_as_float(x[16 * h + k]),
+                                   __uint_as_float(x[16 * h + k + 1]));
+            e = fma_pair(e, kk, off);
+            e.x = exp2_fast(e.x);
+            e.y = exp2_fast(e.y);
+            sum[k / 2 & 1] = add_pair(sum[k / 2 & 1], e);
+            w[8 * h + k / 2] = pack_half2(e.x, e.y);
         }
-        store_columns(s_col + c * 16, w);
+        sum[0] = add_pair(sum[0], sum[1]);
+        l = fmaf(sum[0].x + sum[0].y, scale.inverse[h], l);
     }
+    store_columns(p_col, w);
 }
 
 // ---- the kernel -------------------------------------------------------------------
@@ -585,25 +600,25 @@ struct Shape {
     static constexpr int kQ = kPanels * kPrefixRows * 128;      // bytes of a pipeline's queries
     static constexpr int kTile = kPanels * kTok * 128;          // of a tile's keys or values
     static constexpr int kScales = 4;                           // scales of tiles in place
-    static constexpr int kSoftmax = 4 * kPipes, kConvert = 4;   // warps; kConvert of keys, and of values
+    static constexpr int kSoftmax = 8 * kPipes, kConvert = 4;   // warps; kConvert of keys, and of values
     static constexpr int kControl = kSoftmax + 2 * kConvert;    // first of 4: matrix (2), copies, scales
     static constexpr int kThreads = 32 * (kControl + 4);
     static constexpr int kBox = prefix_box(D);
     static constexpr int kRaw = kTok * D;                       // bytes of a tile's codes, K or V
     static constexpr int kPool = prefix_pool(D);
     static constexpr int kF16 = kPipes * kQ + 2 * kPool * kTile;
-    static constexpr int kFit = (213 * 1024 - kF16) / (2 * kRaw);
+    static constexpr int kFit = (209 * 1024 - kF16) / (2 * kRaw);
     static constexpr int kRing = kFit < 8 ? kFit : 8;           // tiles in the rings
     static_assert(kRing >= 2, "one is used, one on its way");
     static constexpr int kSmem = kF16 + 2 * kRing * kRaw + 1024;  // aligned by the kernel
     static constexpr int kChunks = kTok * D / 16 / (32 * kConvert);  // of 16 codes a converter
     // Registers of a thread: what the block is launched with, then each role's share.  A quarter of an SM
-    // holds a warp of each pipeline, two converters and one of the others.
-    static constexpr int kLaunchRegs = kPipes == 2 ? 96 : 128;
-    static constexpr int kSoftmaxRegs = kPipes == 2 ? 128 : 208;
-    static constexpr int kConvertRegs = kPipes == 2 ? 72 : 104, kControlRegs = kPipes == 2 ? 80 : 96;
-    static_assert(kPipes * kSoftmaxRegs + 2 * kConvertRegs + kControlRegs <=
-                      (kPipes + 3) * kLaunchRegs,
+    // holds two warps of each pipeline, two converters and one of the others.
+    static constexpr int kLaunchRegs = kPipes == 2 ? 72 : 96;
+    static constexpr int kSoftmaxRegs = kPipes == 2 ? 88 : 104;
+    static constexpr int kConvertRegs = kPipes == 2 ? 48 : 88, kControlRegs = kPipes == 2 ? 56 : 88;
+    static_assert(2 * kPipes * kSoftmaxRegs + 2 * kConvertRegs + kControlRegs <=
+                      (2 * kPipes + 3) * kLaunchRegs,
                   "a share beyond what was launched would wait for ever");
     static constexpr int kOut = 2 * kPipes * kTok;              // tensor-memory column of O
     static_assert(kOut + kPipes * D <= 512, "tensor memory");
@@ -614,8 +629,9 @@ struct Shape {
 template <int D>
 __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, uint8_t* smem,
                                        float2* s_sum, uint32_t o_col, int from, int u0, int u1,
-                                       int row, int p, float ref, float l, uint32_t done,
-                                       uint32_t parity, volatile int* gave_up) {
+                                       int row, int p, int half, const Twins& sums, float ref,
+                                       float l, uint32_t done, uint32_t parity,
+                                       volatile int* gave_up) {
     using X = Shape<D>;
     constexpr int NP = X::kPipes, kQuads = D / 4;
     const Segment g(plan, a, from, u1, X::kRows, X::kTok);
@@ -629,6 +645,13 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
         fence_after();
     }
     if (*gave_up) l = NAN;
+    // the halves' sums, added in the same order by both
+    *sums.mine = l;
+    sums.sync();
+    l = half ? *sums.other + l : l + *sums.other;
+    sums.sync();
+    o_col += half * (D / 2);
+    const int d0 = half * (D / 2);  // this half's columns
     const bool alive = r - (row & 31) < g.rows;  // the warp has rows
     // Two halves of the tokens: of a whole tile, the second pipeline's go through the queries' memory;
     // else each is a part of its own.
@@ -636,24 +659,24 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
     float mine_by = 1.f, second_by = 0.f;
     const bool join = NP == 2 && !both && whole;
     if (join) {
-        asm volatile("bar.sync 1, 256;" ::: "memory");  // both are done with the queries
+        asm volatile("bar.sync 9, 512;" ::: "memory");  // both are done with the queries
         if (p == 1) {
-            s_sum[row] = make_float2(ref, l);
+            if (half == 0) s_sum[row] = make_float2(ref, l);
             if (done && alive) {
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t x[32];
+                for (int c = 0; c < D / 2; c += 16) {
+                    uint32_t x[16];
                     load_columns(x, o_col + c);
                     loaded(x);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)  // rotated by the row: different banks
-                        second[(c / 4 + k + row) % kQuads] = make_float4(
+                    for (int k = 0; k < 4; ++k)  // rotated by the row: different banks
+                        second[((d0 + c) / 4 + k + row) % kQuads] = make_float4(
                             __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]),
                             __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
                 }
             }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 9, 512;" ::: "memory");
         if (p == 0 && g.n > 1) {
             const float2 o = s_sum[row];
             const float top = fmaxf(ref + log2f(l), o.x + log2f(o.y));
@@ -672,33 +695,35 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
             mine_by *= by;
             second_by *= by;
             other = j.other;
-            if (on && a.lse) a.lse[out_row] = j.lse;
+            // both halves have read the given one, which may lie in the same place
+            sums.sync();
+            if (on && a.lse && half == 0) a.lse[out_row] = j.lse;
         }
         const long long slot = 2 * (long long)blockIdx.x + (from == u0 ? 0 : 1);
         const int tile_row = p * kPrefixRows + row;
         float4* part = reinterpret_cast<float4*>(a.part) + slot * kQuads * X::kRows + tile_row;
         // without a tile: nothing, whatever the reference
-        if (!whole && on) a.part_sum[slot * X::kRows + tile_row] = make_float2(done ? ref : -INFINITY, l);
+        if (!whole && on && half == 0) a.part_sum[slot * X::kRows + tile_row] = make_float2(done ? ref : -INFINITY, l);
         if (!whole && !done) return;
         uint16_t* out = a.out + at.at(a.out_stride);
         const uint16_t* others = a.join + at.at(a.join_stride);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-            uint32_t x[32];
+        for (int c = 0; c < D / 2; c += 16) {
+            uint32_t x[16];
             load_columns(x, o_col + c);
             loaded(x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 float y[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) y[m] = __uint_as_float(x[4 * k + m]) * mine_by;
                 if (join && g.n > 1) {
-                    const float4 z = second[(c / 4 + k + row) % kQuads];
+                    const float4 z = second[((d0 + c) / 4 + k + row) % kQuads];
                     y[0] += z.x * second_by, y[1] += z.y * second_by;
                     y[2] += z.z * second_by, y[3] += z.w * second_by;
                 }
                 if (!on) continue;
-                const int d = c + 4 * k;
+                const int d = d0 + c + 4 * k;
                 if (!whole) {
                     part[(long long)(d / 4) * X::kRows] = make_float4(y[0], y[1], y[2], y[3]);
                     continue;
@@ -713,7 +738,7 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
             }
         }
     }
-    if (join) asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (join) asm volatile("bar.sync 9, 512;" ::: "memory");
 }
 
 // Barriers in shared memory.
@@ -746,6 +771,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     __shared__ __align__(16) Scales s_scales[NP][X::kScales];
     __shared__ __align__(8) unsigned long long s_bar[kBars];
     __shared__ float2 s_sum[kPrefixRows];  // of the second pipeline
+    __shared__ float s_half[2][NP][2][kPrefixRows];  // what halves of rows tell one another; their sums
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -757,20 +783,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            barrier_init(bar(kQFull + i), 4);
+            barrier_init(bar(kQFull + i), 8);
             barrier_init(bar(kPvDone + i), 1);
             barrier_init(bar(kOFull + i), 1);
         }
         for (int i = 0; i < 4; ++i) {
             barrier_init(bar(kSFull + i), 1);
-            barrier_init(bar(kPFull + i), 4);
+            barrier_init(bar(kPFull + i), 8);
             barrier_init(bar(kKFull + i), X::kConvert);
             barrier_init(bar(kVFull + i), X::kConvert);
             barrier_init(bar(kKEmpty + i), NP);
             barrier_init(bar(kVEmpty + i), NP);
             for (int p = 0; p < 2; ++p) {
                 barrier_init(bar(kScFull + 4 * p + i), 1);
-                barrier_init(bar(kScEmpty + 4 * p + i), 4);
+                barrier_init(bar(kScEmpty + 4 * p + i), 8);
             }
         }
         for (int i = 0; i < 16; ++i) {
@@ -1070,9 +1096,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     } else {
         // ---- softmax ---------------------------------------------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kSoftmaxRegs));
-        const int p = warp / 4, row = tid - p * kPrefixRows;
+        const int p = warp / 8, half = warp / 4 & 1, row = tid % kPrefixRows;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t o_col = lanes + X::kOut + p * D;
+        const Twins twins = {1 + 4 * p + (warp & 3), &s_half[0][p][half][row],
+                           &s_half[0][p][half ^ 1][row]};
         uint32_t done = 0, segments = 0;  // items and segments (with items) before
         for (int from = u0; from < u1;) {
             const Segment g(plan, a, from, u1, X::kRows, TOK);
@@ -1089,20 +1117,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (first < stop) {
                 // The row's largest element goes to [2^14, 2^15), f16's top.
                 const Row at(a, plan.lo[g.p], g.h, on ? r : g.row0);
-                const uint16_t* q = a.q + at.at(a.q_stride);
-                uint4 x[D / 8];
+                const uint16_t* q = a.q + at.at(a.q_stride) + half * (D / 2);
+                uint4 x[D / 16];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < D / 16; ++i) x[i] = make_uint4(0, 0, 0, 0);
                 if (on && a.vec_q) {  // all on their way together
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) x[i] = load8(q + 8 * i, true);
+                    for (int i = 0; i < D / 16; ++i) x[i] = load8(q + 8 * i, true);
                 } else if (on) {
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) x[i] = load8(q + 8 * i, false);
+                    for (int i = 0; i < D / 16; ++i) x[i] = load8(q + 8 * i, false);
                 }
                 float peak = 0.f;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
+                for (int i = 0; i < D / 16; ++i) {
                     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -1110,6 +1138,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                         peak = fmaxf(peak, fmaxf(fabsf(y.x), fabsf(y.y)));
                     }
                 }
+                peak = twins.larger(peak);
                 int e = (int)(__float_as_uint(peak) >> 23) - 127;
                 e = e < -100 ? -100 : e;
                 const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
@@ -1117,7 +1146,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 if (alive) {
                     const uint32_t to = q_at + p * X::kQ;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
+                    for (int i = 0; i < D / 16; ++i) {
                         uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -1125,7 +1154,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                             w[k] = pack_half2(y.x * up, y.y * up);
                         }
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         to + place(row, 8 * i, kPrefixRows * 128)),
+                                         to + place(row, half * (D / 2) + 8 * i, kPrefixRows * 128)),
                                      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                                      : "memory");
                     }
@@ -1137,22 +1166,29 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             float ref = 0.f, l = 0.f;
             for (int t = first; t < stop; t += step, ++done) {
                 const int sc = done % X::kScales;
-                wait(bar(kScFull + 4 * p) + 8 * sc, done / X::kScales & 1, gave_up);
+                const uint32_t sc_full = bar(kScFull + 4 * p) + 8 * sc;
+                const uint32_t s_full = bar(kSFull + 2 * p) + 8 * (done & 1);
+                // both are asked at once: an answer takes some 100 cycles
+                const bool have = try_wait(sc_full, done / X::kScales & 1);
+                const bool there = try_wait(s_full, done >> 1 & 1);
+                if (!have) wait_slow(sc_full, done / X::kScales & 1, gave_up);
+                if (!there) wait_slow(s_full, done >> 1 & 1, gave_up);
                 const Scales& scales = s_scales[p][sc];
-                const Even<TOK> even(scales.even, f);  // while the scores come
-                wait(bar(kSFull + 2 * p) + 8 * (done & 1), done >> 1 & 1, gave_up);
                 fence_after();
                 if (alive) {
                     const uint32_t s_col = lanes + (2 * p + (done & 1)) * TOK;
+                    const uint32_t mine = s_col + half * 32, to = s_col + half * 16;
                     // The product before, which may still be adding to O; the one before that is done, for
                     // these scores were issued behind it.
                     const Product before = {bar(kPvDone + p), (done + 1) & 1, t == first, gave_up};
                     const int live = rest - t * TOK;  // tokens of the tile, or more
                     if (a.even && live >= TOK && !scales.small)
-                        softmax_even<TOK, D>(s_col, o_col, even, before, ref, l);
+                        softmax_even<D>(mine, to, o_col + half * (D / 2),
+                                        Even(scales.even + 2 * half, f), before, twins, ref, l);
                     else
-                        softmax_any<TOK, D>(s_col, o_col, f, scales.k, scales.v, scales.log, live,
-                                            before, ref, l);
+                        softmax_any<D>(mine, to, o_col + half * (D / 2), f, scales.k + 32 * half,
+                                       scales.v + 32 * half, scales.log + 32 * half,
+                                       live - 32 * half, before, twins, ref, l);
                 }
                 stored();
                 fence_before();
@@ -1166,8 +1202,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             // ---- the segment's outputs ---------------------------------------------------
             // What they need of the segment is read anew, so that it takes no registers in the loop.
             int anew = from, row_anew = row;
+            const Twins sums = {twins.id, &s_half[1][p][half][row], &s_half[1][p][half ^ 1][row]};
             asm volatile("" : "+r"(anew), "+r"(row_anew));
-            finish<D>(a, plan, smem, s_sum, o_col, anew, u0, u1, row_anew, p, ref, l,
+            finish<D>(a, plan, smem, s_sum, o_col, anew, u0, u1, row_anew, p, half,
+                      sums, ref, l,
                       first < stop ? bar(kOFull + p) : 0u, segments & 1, gave_up);
             segments += first < stop;
             from += g.n;
