@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     struct Scales {
         float k[TOK], v[TOK], log[TOK];  // log2 of the V scale
         float4 even[TOK / 16];           // of 16 tokens: K, log2 V, 1 / V
-        int small;                       // a V scale is below 2^-60
+        int each;                        // the tokens' own are to be used
     };
     __shared__ __align__(16) Scales s_scales[NP][X::kScales];
     __shared__ __align__(8) unsigned long long s_bar[kBars];
@@ -957,67 +957,63 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     wait_still(bar(kRawFull + 8 * side) + 8 * (i % X::kRing), i / X::kRing & 1);
         } else if (role == 3) {
             // ---- scales --------------------------------------------------------------------
-            // A lane has two tokens, of two tiles ahead.
-            int tile = 0, end = 0, len = 0, readers = 0;
-            const float* scales = nullptr;
-            float k[2][2], v[2][2];  // [tile][token]
-            int to[2];               // pipelines that read the tile, a bit each
-            auto load = [&](int i, float (&k)[2], float (&v)[2], int& to) {
-                if (i >= count) return;
-                if (NP == 2 && readers != 3) readers ^= 3;
-                if (++tile >= end) {
-                    const Segment g(plan, a, u0 + i, u1, X::kRows, TOK);
-                    tile = g.tile0;
-                    end = g.tile0 + g.n;
-                    len = plan.len[g.p];
-                    readers = NP == 2 && g.rows - g.row0 > kPrefixRows ? 3 : 1;
-                    scales = a.scales + (long long)plan.req[g.p] * a.NB * 2 * a.Hkv + g.h;
-                }
-                to = readers;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int token = tile * TOK + 32 * h + lane;
-                    k[h] = v[h] = 0.f;
+            // The lanes take 8 tiles at once, 4 groups of 16 tokens each; the next 8 are on their way
+            // meanwhile.  Letting a tile go waits for the loads that are under way: with a load
+            // for each tile, and every token's scales written, this warp alone took 1500 cycles a tile.
+            // Tiles whose scales differ within a group, or are not all there, get every token's.
+            int items[2] = {0, 0};  // of each pipeline
+            for (int from = u0; from < u1;) {
+                const Segment g(plan, a, from, u1, X::kRows, TOK);
+                const int len = plan.len[g.p], first = g.tile0, n = g.n;
+                const bool both = NP == 1 || g.rows - g.row0 > kPrefixRows;
+                const float* const scales =
+                    a.scales + (long long)plan.req[g.p] * a.NB * 2 * a.Hkv + g.h;
+                auto load = [&](int token, float& k, float& v) {
+                    k = v = 0.f;
                     if (token < len) {
                         const float* at = scales + (long long)a.block.of(token) * 2 * a.Hkv;
-                        k[h] = ld(at);
-                        v[h] = ld(at + a.Hkv);
+                        k = ld(at);
+                        v = ld(at + a.Hkv);
+                    }
+                };
+                float k, v, next_k, next_v;
+                load(first * TOK + lane * 16, next_k, next_v);
+                for (int c = 0; c < n; c += 8) {
+                    k = next_k, v = next_v;
+                    load((first + c + 8) * TOK + lane * 16, next_k, next_v);
+                    const unsigned small = __ballot_sync(0xffffffffu, v < 0x1p-60f);
+                    const float4 even = make_float4(k * a.k_sign, log2f(v), __frcp_rn(v), 0.f);
+                    const int stop = min(8, n - c);
+#pragma unroll 1
+                    for (int j = 0; j < stop; ++j) {
+                        const int tile = first + c + j;
+                        const bool each = !a.even || small >> (4 * j) & 15 || (tile + 1) * TOK > len;
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) {
+                            if (!both && ((c + j) & 1) != p) continue;
+                            const int sc = items[p] % X::kScales;
+                            wait(bar(kScEmpty + 4 * p) + 8 * sc, (items[p] / X::kScales & 1) ^ 1,
+                                 gave_up);
+                            Scales& s = s_scales[p][sc];
+                            if (lane >> 2 == j) s.even[lane & 3] = even;
+                            if (lane == 0) s.each = each;
+                            if (each) {
+#pragma unroll
+                                for (int h = 0; h < TOK; h += 32) {
+                                    float one_k, one_v;
+                                    load(tile * TOK + h + lane, one_k, one_v);
+                                    s.k[h + lane] = one_k * a.k_sign;
+                                    s.v[h + lane] = one_v;
+                                    s.log[h + lane] = log2f(one_v);
+                                }
+                            }
+                            __syncwarp();
+                            if (lane == 0) arrive(bar(kScFull + 4 * p) + 8 * sc);
+                            ++items[p];
+                        }
                     }
                 }
-            };
-            int items[2] = {0, 0};  // of each pipeline
-            auto put = [&](const float (&k)[2], const float (&v)[2], int to) {
-                const bool small = __any_sync(0xffffffffu, fminf(v[0], v[1]) < 0x1p-60f);
-                const float lg[2] = {log2f(v[0]), log2f(v[1])};
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    if (!(to >> p & 1)) continue;
-                    const int sc = items[p] % X::kScales;
-                    wait(bar(kScEmpty + 4 * p) + 8 * sc, (items[p] / X::kScales & 1) ^ 1, gave_up);
-                    Scales& s = s_scales[p][sc];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int t = 32 * h + lane;
-                        s.k[t] = k[h] * a.k_sign;
-                        s.v[t] = v[h];
-                        s.log[t] = lg[h];
-                        if (t % 16 == 0)
-                            s.even[t / 16] = make_float4(k[h] * a.k_sign, lg[h], __frcp_rn(v[h]), 0.f);
-                    }
-                    if (lane == 0) s.small = small;
-                    __syncwarp();
-                    if (lane == 0) arrive(bar(kScFull + 4 * p) + 8 * sc);
-                    ++items[p];
-                }
-            };
-            load(0, k[0], v[0], to[0]);
-            load(1, k[1], v[1], to[1]);
-            for (int i = 0; i < count; i += 2) {
-                put(k[0], v[0], to[0]);
-                load(i + 2, k[0], v[0], to[0]);
-                if (i + 1 == count) break;
-                put(k[1], v[1], to[1]);
-                load(i + 3, k[1], v[1], to[1]);
+                from += n;
             }
         }
     } else if (warp >= X::kSoftmax) {
@@ -1182,7 +1178,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     // these scores were issued behind it.
                     const Product before = {bar(kPvDone + p), (done + 1) & 1, t == first, gave_up};
                     const int live = rest - t * TOK;  // tokens of the tile, or more
-                    if (a.even && live >= TOK && !scales.small)
+                    if (!scales.each)
                         softmax_even<D>(mine, to, o_col + half * (D / 2),
                                         Even(scales.even + 2 * half, f), before, twins, ref, l);
                     else
