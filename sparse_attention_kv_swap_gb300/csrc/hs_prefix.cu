@@ -1,8 +1,10 @@
 // Launch of hs_attend_prefix (the kernel is in hs_prefix.cuh), and the kernel that puts
 // together the rows whose tokens fell to several CTAs.
 //
-// A CTA takes 32 rows of a K/V head, a lane a row, and 16 quads of their elements, a warp a quad;
-// partial outputs lie with consecutive rows side by side.  They come mostly out of L2.
+// A CTA takes 32 rows of a K/V head, a lane a row, and 16 quads of their elements, a warp a quad, or 4
+// quads, four warps a quad; partial outputs lie with consecutive rows side by side.  They come
+// mostly out of L2; latencies bound it, so its launch and its plan overlap the end of
+// prefix_kernel and the first parts are loaded while their factors are worked out.
 #include "hs_prefix.cuh"
 
 namespace hs {
@@ -14,17 +16,18 @@ using prefix::Plan;
 constexpr int kWarps = 16;
 constexpr int kParts = 2 * kPrefixCtas;  // of a row at most
 
-__global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a, int D,
-                                                              int groups) {
+__global__ void __launch_bounds__(32 * kWarps, 2) combine_kernel(const PrefixArgs a, int D,
+                                                              int groups, int split) {
     __shared__ Plan plan;
     __shared__ float s_factor[kParts][32];  // of a part of a row
     __shared__ float s_tmp[kWarps][32];
+    __shared__ float4 s_y[kWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int pipes = prefix_pipes(D), tile_rows = kPrefixRows * pipes;
-    wait_for_previous();
+    // The plan's inputs come from before prefix_kernel, which lets this one start only after it has
+    // itself waited for them (without prefixes there is no plan, and nothing is read).
     if (warp == 0) prefix::fill_plan(plan, a, tile_rows, kPrefixTokens);
     __syncthreads();
-    release_next();
     const int units = plan.unit[a.P], ctas = prefix::working(units, a.ctas);
     const int slice = blockIdx.x / (a.Hkv * groups), hg = blockIdx.x - slice * a.Hkv * groups;
     const int h = hg / groups, all = a.B * a.S * a.G;
@@ -63,11 +66,29 @@ __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a
         return 2 * cta + (prefix::first_unit(units, cta, ctas) >= unit0 ? 0 : 1);
     };
     auto row_of = [&](int c) { return tile_row + (halves == 2 && (c & 1) ? kPrefixRows : 0); };
+    wait_for_previous();
+    release_next();
+    // The first parts' outputs, on their way while the factors are worked out.
+    const int quads = D / 4, d = (slice * kWarps + warp) / split, sub = warp % split;
+    const float4* part = reinterpret_cast<const float4*>(a.part) + (long long)d * tile_rows;
+    constexpr int kAhead = 6;
+    float4 z[kAhead];
+    const auto fetch = [&](int c0) {
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c) {
+            z[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int at = sub + (c0 + c) * split;
+            if (at < parts && d < quads)
+                z[c] = ld(part + (long long)slot(at) * quads * tile_rows + row_of(at));
+        }
+    };
+    fetch(0);
     // The factors of a row's parts, a warp every 16th of them: sums relative to the largest.
-    float top = -INFINITY;
+    float top = -INFINITY, first_sum = 0.f;
     bool nan = false;
     for (int c = warp; c < parts; c += kWarps) {
         const float2 x = ld(a.part_sum + slot(c) * tile_rows + row_of(c));
+        if (c == warp) first_sum = x.y;
         const float y = x.x + log2f(x.y);  // -inf for a part without tokens
         s_factor[c][lane] = x.x;
         top = fmaxf(top, y);
@@ -86,7 +107,7 @@ __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a
     for (int c = warp; c < parts; c += kWarps) {
         const float f = exp2f(s_factor[c][lane] - top);
         s_factor[c][lane] = f;
-        sum += ld(a.part_sum + slot(c) * tile_rows + row_of(c)).y * f;
+        sum += (c == warp ? first_sum : ld(a.part_sum + slot(c) * tile_rows + row_of(c)).y) * f;
     }
     s_tmp[warp][lane] = sum;
     // before any warp writes lse, which may be the same array
@@ -95,30 +116,30 @@ __global__ void __launch_bounds__(32 * kWarps) combine_kernel(const PrefixArgs a
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += s_tmp[w][lane];
-    if (!mine) return;
     const Joined j(some ? top + log2f(sum) : -INFINITY, other);
-    if (warp == 0 && slice == 0 && a.lse) a.lse[out_row] = j.lse;
+    if (mine && warp == 0 && slice == 0 && a.lse) a.lse[out_row] = j.lse;
     const float by = some ? j.mine / sum : 0.f;
-    const int quads = D / 4, d = slice * kWarps + warp;
-    if (d >= quads) return;
-    const float4* part = reinterpret_cast<const float4*>(a.part) + (long long)d * tile_rows;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kAhead = 6;
-    for (int c0 = 0; c0 < parts; c0 += kAhead) {
-        float4 z[kAhead];
-        float f[kAhead];
+    for (int c0 = 0; sub + c0 * split < parts; c0 += kAhead) {
+        if (c0 > 0) fetch(c0);
 #pragma unroll
         for (int c = 0; c < kAhead; ++c) {
-            f[c] = c0 + c < parts ? s_factor[c0 + c][lane] : 0.f;
-            z[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (f[c] != 0.f)  // a part without tokens is not written
-                z[c] = ld(part + (long long)slot(c0 + c) * quads * tile_rows + row_of(c0 + c));
+            const int at = sub + (c0 + c) * split;
+            const float f = at < parts ? s_factor[at][lane] : 0.f;
+            if (f == 0.f) continue;  // a part without tokens is not written
+            y = make_float4(y.x + z[c].x * f, y.y + z[c].y * f, y.z + z[c].z * f, y.w + z[c].w * f);
         }
-#pragma unroll
-        for (int c = 0; c < kAhead; ++c)
-            y = make_float4(y.x + z[c].x * f[c], y.y + z[c].y * f[c], y.z + z[c].z * f[c],
-                            y.w + z[c].w * f[c]);
     }
+    if (split > 1) {
+        s_y[warp][lane] = y;
+        __syncthreads();
+        if (sub > 0) return;
+        for (int i = 1; i < split; ++i) {
+            const float4 x = s_y[warp + i][lane];
+            y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+        }
+    }
+    if (!mine || d >= quads) return;
     y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
     if (j.other > 0.f) {
         const uint2 z = prefix::load4(a.join + at.at(a.join_stride) + 4 * d, a.vec_join);
@@ -236,9 +257,12 @@ cudaError_t launch_prefix(const hs_kv_format& f, const hs_prefix_args& x, cudaSt
         if (e != cudaSuccess) return e;
     }
     const int groups = (int)(((long long)a.B * a.S * a.G + 31) / 32);
-    const int slices = (f.head_dim / 4 + kWarps - 1) / kWarps;
+    // Where that leaves SMs idle, four warps share a quad's parts.
+    const int quads = f.head_dim / 4;
+    const int split = (long long)a.Hkv * groups * ((quads + kWarps - 1) / kWarps) * 4 <= a.ctas ? 4 : 1;
+    const int slices = (quads * split + kWarps - 1) / kWarps;
     return launch_chained(combine_kernel, a.Hkv * groups * slices, 32 * kWarps, 0, 0, s, a,
-                          f.head_dim, groups);
+                          f.head_dim, groups, split);
 }
 
 }  // namespace hs

@@ -1200,6 +1200,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             int anew = from, row_anew = row;
             const Twins sums = {twins.id, &s_half[1][p][half][row], &s_half[1][p][half ^ 1][row]};
             asm volatile("" : "+r"(anew), "+r"(row_anew));
+            if (from + g.n >= u1) release_next();
             finish<D>(a, plan, smem, s_sum, o_col, anew, u0, u1, row_anew, p, half,
                       sums, ref, l,
                       first < stop ? bar(kOFull + p) : 0u, segments & 1, gave_up);
@@ -1207,6 +1208,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             from += g.n;
         }
     }
+    if (warp >= X::kSoftmax) release_next();
     __syncwarp();
     fence_before();
     __syncthreads();
