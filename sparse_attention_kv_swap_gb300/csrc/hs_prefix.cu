@@ -59,11 +59,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) combine_kernel(const PrefixArg
     // Where one CTA has the whole tile, it has written the outputs.
     const bool mine = on && (!some || last > first);
     const int parts = some && mine ? (last - first + 1) * halves : 0;
-    // A CTA's part lies in the place of its first segment if it begins within the tile; the second
-    // pipeline's, 128 rows on.
+    // A CTA's part lies in the place of its first segment if it begins within the tile, as all but the
+    // tile's first CTA do; the second pipeline's, 128 rows on.
+    const int later = some && prefix::first_unit(units, first, ctas) < unit0 ? 1 : 0;
     auto slot = [&](int c) {
-        const int cta = first + (halves == 2 ? c >> 1 : c);
-        return 2 * cta + (prefix::first_unit(units, cta, ctas) >= unit0 ? 0 : 1);
+        const int n = halves == 2 ? c >> 1 : c;
+        return 2 * (first + n) + (n == 0 ? later : 0);
     };
     auto row_of = [&](int c) { return tile_row + (halves == 2 && (c & 1) ? kPrefixRows : 0); };
     wait_for_previous();

@@ -15,7 +15,7 @@
 //                   (128-byte swizzle).  Codes are exact in f16.
 //   matrix (1 for each of the NPIPE pipelines)   S = Q K^T (128 rows x 64 tokens) and O += P V by
 //                   tcgen05.mma, accumulators and P in tensor memory
-//   softmax (4 for each pipeline)   a thread has a row: it reads S, writes P over it
+//   softmax (8 for each pipeline)   a thread has half a row (32 tokens): it reads S, writes P over it
 // Two pipelines (D <= 128) hold rows 0-127 and 128-255 of a row tile, or, where it has 128 rows or fewer,
 // the even and the odd tiles of tokens of the same rows.  Each has two places for S: the scores of
 // the next tile are there when the softmax of one is done, and its product with V runs beside
@@ -28,6 +28,14 @@
 // is passed, and O and l are scaled then): f16 keeps its 11 bits down to 2^-23 of the largest term and
 // is off by 2^-34 of it below.  Where V scales differ by 2^88 and more, r stays within 100
 // of the largest z, so that l stays in range.
+//
+// What bounds it (e4m3, D = 128, 8 K/V heads, both kernels): 64 requests of 8 query heads a K/V head
+// over 32768 shared tokens take 83 us, 0.83 PFLOP/s; 2 requests of 4 over 131072 take 87 us, 3.1 TB/s.  With
+// 256 rows a tile costs 1.0 us, of which the matrix instructions alone need 0.96 (they read the queries
+// from shared memory anew for each 64 tokens: tensor memory is full of S and O) and the
+// softmax's chain alone 0.90; taking out the conversions saves 3%.  Launch, the first
+// tile's way through the roles, partial outputs and their joining cost some 25 us a call, whatever its
+// length.
 #pragma once
 
 #include <cuda.h>
@@ -81,7 +89,8 @@ struct Plan {
     int32_t unit[HS_MAX_PREFIXES + 1];  // first unit; units of a prefix: [K/V head][row tile][tile]
 };
 
-// Filled by one warp; everyone else waits at the caller's barrier.
+// Filled by one warp; everyone else waits at the caller's barrier.  From L2: combine_kernel comes here
+// before it waits.
 __device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int rows, int tokens) {
     const int lane = threadIdx.x & 31;
     int taken = 0;          // batch rows of the prefixes before
@@ -90,10 +99,10 @@ __device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int r
         const int p = p0 + lane;
         int first = 0, end = 0, len = 0, r = 0;
         if (p < a.P) {
-            first = min(max(ld(a.starts + p), 0), a.B);
-            end = max(min(max(ld(a.starts + p + 1), 0), a.B), first);
-            r = ld(a.prefix + p);
-            len = r < 0 || r >= a.R ? 0 : min(max(ld(a.lens + p), 0), a.L);
+            first = min(max(__ldcg(a.starts + p), 0), a.B);
+            end = max(min(max(__ldcg(a.starts + p + 1), 0), a.B), first);
+            r = __ldcg(a.prefix + p);
+            len = r < 0 || r >= a.R ? 0 : min(max(__ldcg(a.lens + p), 0), a.L);
         }
         int most = max(end, taken);  // the largest end up to this prefix
 #pragma unroll
@@ -1043,7 +1052,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (!may) wait_slow(empty, free, gave_up);
             // Eight lanes take one piece of eight rows: what they read and store together lies in
             // different banks.
-            constexpr int kGroup = X::kChunks % 4 == 0 ? 4 : X::kChunks % 3 == 0 ? 3 : X::kChunks;
+            constexpr int kGroup = X::kChunks % 4 == 0 ? 4 : X::kChunks % 2 == 0 ? 2 : 1;
 #pragma unroll
             for (int c0 = 0; c0 < X::kChunks; c0 += kGroup) {
                 uint4 x[kGroup];
