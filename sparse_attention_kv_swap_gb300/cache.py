@@ -166,7 +166,7 @@ class SwapInCache:
                       out: Optional[Dict[str, torch.Tensor]] = None, stream=None):
         """Attention of q over prefixes that consecutive batch rows share, kept in device memory
         (rows [P, tokens, W] and their scales, as hs_quantize_kv writes them); join: what attend
-        returned for the same q with lse=True, which is joined in."""
+        returned for the same q with lse=True, which is joined in (and may be `out` too)."""
         Bn, S, heads = q.shape[:3]
         o = dict(out or {})
         with self._allocate_on(stream):
@@ -174,13 +174,14 @@ class SwapInCache:
                 o["out"] = torch.empty(q.shape, dtype=q.dtype, device=self.device)
             if "lse" not in o:
                 o["lse"] = torch.empty(q.shape[:3], device=self.device)
-            if "workspace" not in o:
-                o["workspace"] = torch.empty(
+            if "prefix_workspace" not in o:
+                o["prefix_workspace"] = torch.empty(
                     B.hs_prefix_workspace_bytes(fmt, Bn, S, heads, prefix.shape[0]),
                     dtype=torch.uint8, device=self.device)
         B.hs_attend_prefix(fmt, q, rows, scales, prefix, lens, starts, o["out"], o["lse"],
                            None if join is None else join["out"],
-                           None if join is None else join["lse"], sm_scale, o["workspace"], stream)
+                           None if join is None else join["lse"], sm_scale,
+                           o["prefix_workspace"], stream)
         return o
 
     def evict(self, fmt: B.HsKvFormat, scales: List[torch.Tensor], acc: List[torch.Tensor],

@@ -93,6 +93,23 @@ def test_rotate_axes(axes):
     r.check(r.run())
 
 
+@pytest.mark.parametrize("B_,M,Hq,Hkv,D,dtype", [(3, 5001, 3, 1, 64, "fp16"), (1, 12000, 1, 1, 32, "fp32"),
+                                                 (700, 3, 2, 2, 128, "bf16"), (2, 37, 128, 120, 96, "bf16"),
+                                                 (5000, 1, 2, 1, 192, "fp16"), (2, 911, 7, 5, 256, "fp32")])
+def test_rotate_tiles(B_, M, Hq, Hkv, D, dtype):
+    """Tiles and runs that do not divide the tokens, in one wave of CTAs and in several."""
+    rng = np.random.default_rng(M)
+    a = Rotate(rng, B_, M, Hq, Hkv, D, D // 2, dtype)
+    count = rng.integers(0, M + 1, B_)
+    count[0], count[1:2] = M, 0
+    got = a.run(count=i32(count))
+    want = a.run()
+    a.check(want)
+    on = torch.arange(M, device="cuda") < i32(count)[:, None]
+    for x, y in zip(got, want):
+        assert torch.equal(x[on], y[on]) and torch.isnan(x[~on]).all()
+
+
 def test_rotate_without_norm_and_one_side():
     rng = np.random.default_rng(1)
     r = Rotate(rng, 2, 9, 4, 2, 64, 32, "fp16", norm=False)
@@ -535,6 +552,15 @@ def test_prefix_head_sizes(code, D, H, G, dtype, B_):
     a.check(a.run())
 
 
+@pytest.mark.parametrize("T", [1, 7, 24, 40, 64])
+@pytest.mark.parametrize("B_,code", [(2, "e4m3"), (50, "int8")])
+def test_prefix_block_sizes(T, B_, code):
+    """Scales by 16 tokens and by token, rows of one tile and of two."""
+    rng = np.random.default_rng(T)
+    a = Prefix(rng, B_, 1, 2, 4, 64, [4000 - T], T=T, code=code)
+    a.check(a.run())
+
+
 @pytest.mark.parametrize("H,G", [(1, 1), (1, 128), (5, 3), (12, 4), (32, 1), (128, 1), (2, 17)])
 def test_prefix_head_layouts(H, G):
     rng = np.random.default_rng(H * 200 + G)
@@ -862,5 +888,11 @@ def test_decode_example(code, dtype, heads, group, D, T):
                           D ** -0.5, (d.own["out"].cpu().double().numpy(),
                                       d.own["lse"].cpu().double().numpy()))
         a.check((d.out["out"], d.out["lse"]), want)
+    # joined in place, over the attention of the requests' own tokens
+    got = d.cache.attend_prefix(d.fmt, d.rows, d.shared_scales, d.q, d.prefix, d.prefix_len, d.starts,
+                                join=d.own, out=d.own)
+    torch.cuda.synchronize()
+    assert got["out"] is d.own["out"] and torch.equal(got["out"], d.out["out"])
+    assert torch.equal(got["lse"], d.out["lse"])
     assert d.cache.status() == (B.HS_OK, 0)
     d.cache.close()
