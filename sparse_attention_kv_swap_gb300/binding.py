@@ -1108,7 +1108,7 @@ def hs_attend_prefix(fmt: HsKvFormat, q, rows, scales, prefix, lens, starts, out
                      workspace=None, stream=None) -> None:
     """Attention of q [batch, steps, heads, D] (bf16 or fp16) over prefixes that consecutive batch
     rows share: rows starts[p] .. starts[p + 1] - 1 (starts int32 [P + 1]) attend to the first
-    lens[p] tokens of request prefix[p] of the store rows uint8 [R, L, W], scales fp32
+    lens[p] tokens of request prefix[p] of the store rows uint8 [R, L, W] (device memory), scales fp32
     [R, NB, 2, Hkv].  Outputs: out as q, lse fp32 [batch, steps, heads].  join_out and join_lse: the
     same queries' attention over other tokens, to be joined (they may be out and lse).
     sm_scale: 1 / sqrt(D) by default."""
@@ -1138,6 +1138,7 @@ def hs_attend_prefix(fmt: HsKvFormat, q, rows, scales, prefix, lens, starts, out
         _shape(join_out, q.shape, "join_out")
         _shape(join_lse, (B, S, H), "join_lse")
         join, strides = _sptr(join_out, "join_out", dev), join_out.stride()[:3]
+    _device_of(rows, "rows")  # they are copied in tiles, which takes device memory
     i32, f32 = torch.int32, torch.float32
     args = _PREFIX_ARGS.pack(
         _sptr(q, "q", dev), _sptr(out, "out", dev), _dtype_code(q, "q", False), B, S, H, R, L, P,

@@ -615,6 +615,15 @@ def test_prefix_without_prefixes_is_the_join():
     assert (out == 0).all() and torch.isneginf(lse).all()
 
 
+def test_prefix_refuses_rows_in_host_memory():
+    a = Prefix(np.random.default_rng(3), 2, 1, 1, 2, 64, [40])
+    out = torch.full(a.q.shape, 7.0, dtype=a.q.dtype, device="cuda")
+    for rows in (torch.from_numpy(a.rows), torch.from_numpy(a.rows).pin_memory()):
+        with pytest.raises(ValueError):
+            a.run(out=out, rows=rows)
+    assert (out == 7).all()
+
+
 def test_prefix_joined_in_place_and_strides():
     rng = np.random.default_rng(16)
     for lens, B_ in (([500], 3), ([90], 90), ([3000, 10], 5)):
