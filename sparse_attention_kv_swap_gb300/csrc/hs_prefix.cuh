@@ -33,7 +33,8 @@
 // over 32768 shared tokens take 83 us, 0.83 PFLOP/s; 2 requests of 4 over 131072 take 87 us, 3.1 TB/s.  With
 // 256 rows a tile costs 1.0 us, of which the matrix instructions alone need 0.96 (they read the queries
 // from shared memory anew for each 64 tokens: tensor memory is full of S and O) and the
-// softmax's chain alone 0.90; taking out the conversions saves 3%.  Launch, the first
+// softmax's chain alone 0.90; taking out the conversions saves 3%.  (A warp for all 64 tokens of its rows, with
+// half as many softmax warps, made the second call 4% slower, the first 1.5% faster.)  Launch, the first
 // tile's way through the roles, partial outputs and their joining cost some 25 us a call, whatever its
 // length.
 #pragma once
@@ -712,7 +713,8 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
         const int tile_row = p * kPrefixRows + row;
         float4* part = reinterpret_cast<float4*>(a.part) + slot * kQuads * X::kRows + tile_row;
         // without a tile: nothing, whatever the reference
-        if (!whole && on && half == 0) a.part_sum[slot * X::kRows + tile_row] = make_float2(done ? ref : -INFINITY, l);
+        if (!whole && on && half == 0)
+            a.part_sum[slot * X::kRows + tile_row] = make_float2(done ? ref : -INFINITY, l);
         if (!whole && !done) return;
         uint16_t* out = a.out + at.at(a.out_stride);
         const uint16_t* others = a.join + at.at(a.join_stride);
