@@ -111,14 +111,19 @@ __global__ void __launch_bounds__(32 * kWarps, 2) combine_kernel(const PrefixArg
         sum += (c == warp ? first_sum : ld(a.part_sum + slot(c) * tile_rows + row_of(c)).y) * f;
     }
     s_tmp[warp][lane] = sum;
-    // before any warp writes lse, which may be the same array
-    const float other = on && a.join ? ld(a.join_lse + out_row) : -INFINITY;
+    // lse may be the given one itself, and a row's slices are CTAs of their own, which nothing orders:
+    // the slice that writes a row's lse must not be where the others read.  They read the parts' copy; a
+    // row without parts keeps the given lse.
+    float other = -INFINITY;
+    if (mine && a.join)
+        other = parts > 0 ? ld(a.part_join + slot(0) * tile_rows + row_of(0)) : ld(a.join_lse + out_row);
     __syncthreads();
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += s_tmp[w][lane];
     const Joined j(some ? top + log2f(sum) : -INFINITY, other);
-    if (mine && warp == 0 && slice == 0 && a.lse) a.lse[out_row] = j.lse;
+    if (mine && warp == 0 && slice == 0 && a.lse && (parts > 0 || a.lse != a.join_lse))
+        a.lse[out_row] = j.lse;
     const float by = some ? j.mine / sum : 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c0 = 0; sub + c0 * split < parts; c0 += kAhead) {
@@ -204,7 +209,7 @@ size_t part_bytes(const hs_kv_format& f, int ctas) {
 size_t prefix_workspace(const hs_kv_format& f) {
     const int ctas = prefix_ctas();
     return part_bytes(f, ctas) + (size_t)ctas * 2 * kPrefixRows * prefix_pipes(f.head_dim) *
-                                     sizeof(float2);
+                                     (sizeof(float2) + sizeof(float));
 }
 
 cudaError_t launch_prefix(const hs_kv_format& f, const hs_prefix_args& x, cudaStream_t s) {
@@ -249,6 +254,8 @@ cudaError_t launch_prefix(const hs_kv_format& f, const hs_prefix_args& x, cudaSt
     uint8_t* ws = static_cast<uint8_t*>(x.workspace_dev);
     a.part = reinterpret_cast<float*>(ws);
     a.part_sum = reinterpret_cast<float2*>(ws + part_bytes(f, a.ctas));
+    a.part_join = reinterpret_cast<float*>(a.part_sum + (size_t)a.ctas * 2 * kPrefixRows *
+                                                            prefix_pipes(f.head_dim));
     if (a.P > 0) {
         CUtensorMap map;
         cudaError_t e = make_map(f, x, &map);

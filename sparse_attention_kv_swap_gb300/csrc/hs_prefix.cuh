@@ -68,6 +68,7 @@ struct PrefixArgs {
     int32_t ctas;
     float* part;       // [ctas][2][D / 4][rows of a tile][4] outputs
     float2* part_sum;  // [ctas][2][rows of a tile] (r, l)
+    float* part_join;  // [ctas][2][rows of a tile] the row's given lse
 };
 
 constexpr int prefix_pipes(int D) { return D <= 128 ? 2 : 1; }
@@ -713,8 +714,11 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
         const int tile_row = p * kPrefixRows + row;
         float4* part = reinterpret_cast<float4*>(a.part) + slot * kQuads * X::kRows + tile_row;
         // without a tile: nothing, whatever the reference
-        if (!whole && on && half == 0)
-            a.part_sum[slot * X::kRows + tile_row] = make_float2(done ? ref : -INFINITY, l);
+        if (!whole && on && half == 0) {
+            const long long place = slot * X::kRows + tile_row;
+            a.part_sum[place] = make_float2(done ? ref : -INFINITY, l);
+            if (a.join) a.part_join[place] = ld(a.join_lse + out_row);
+        }
         if (!whole && !done) return;
         uint16_t* out = a.out + at.at(a.out_stride);
         const uint16_t* others = a.join + at.at(a.join_stride);

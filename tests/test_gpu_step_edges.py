@@ -1,0 +1,53 @@
+"""Calls around a decode step at the edges of what they accept."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_step import Prefix, dev
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- shared prefixes, joined in place ---------------------------------------------------------
+
+@pytest.mark.parametrize("B_,S,H,G,D,lens", [
+    (64, 4, 8, 8, 128, [4096]),    # 1024 CTAs put rows together, 2 for each row: several waves
+    (64, 4, 8, 8, 192, [2048]),    # 3
+    (64, 4, 8, 8, 256, [2048]),    # 4
+    (40, 4, 8, 8, 96, [3000, 1]),  # rows of one part beside rows of many
+    (200, 2, 4, 4, 64, [900, 70, 0]),
+    (4, 1, 2, 4, 256, [6000]),     # 16 for each row
+    (2, 1, 1, 1, 128, [6000]),
+])
+def test_prefix_joined_in_place(B_, S, H, G, D, lens):
+    """The same bits whether the outputs are the given ones, both or one of them, or lie apart; the
+    CTAs that put a row together are not ordered.  Nothing past the workspace is written."""
+    rng = np.random.default_rng(D + B_)
+    a = Prefix(rng, B_, S, H, G, D, lens, 16, join=True)
+    rows, scales = dev(a.rows), dev(a.scales)
+    size = a.workspace().numel()
+    ws = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+    want = a.run(rows=rows, workspace=ws[:size])
+    for out_too, lse_too in ((True, True), (False, True), (True, False)):
+        for _ in range(3):
+            join = (dev(a.join[0]), dev(a.join[1]))
+            got = a.run(rows=rows, join=join, out=join[0] if out_too else None,
+                        lse=join[1] if lse_too else None, workspace=ws[:size])
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (ws[size:] == 255).all()
+    if B_ * S * H * G * lens[0] < 1 << 17:
+        a.check(want)
+
+
+def test_prefix_joined_in_place_without_prefixes():
+    """Rows of no prefix keep what they are given, and an empty set is still zeros."""
+    rng = np.random.default_rng(30)
+    a = Prefix(rng, 300, 4, 8, 8, 128, [40], starts=[100, 101], join=True)
+    want = a.run()
+    out, lse = dev(a.join[0]), dev(a.join[1])
+    got = a.run(join=(out, lse), out=out, lse=lse)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    none = torch.from_numpy(np.isneginf(a.join[1]))[101:]
+    assert torch.equal(got[1].cpu()[101:], torch.from_numpy(a.join[1])[101:])
+    assert (got[0].cpu()[101:][none] == 0).all()
+    assert torch.equal(got[0].cpu()[101:][~none], a.join[0][101:][~none])
