@@ -463,8 +463,11 @@ __device__ __forceinline__ void move_reference(uint32_t o_col, float want, const
         return;
     }
     const bool grow = want > ref + kRoom;
-    const float by = grow ? exp2_fast(ref - want) : 1.f;
-    l *= by;
+    const float step = grow ? ref - want : 0.f;
+    const float by = exp2_fast(step);  // 0 under 2^-126: so little of O does not show beside the new term
+    // l, of terms up to 2^106, may still count then: by two factors that are not 0
+    const float root = exp2_fast(0.5f * step);
+    l = step < -125.f ? l * root * root : l * by;
     if (grow) ref = want;
     wait(before.done, before.parity, before.gave_up);
     fence_after();

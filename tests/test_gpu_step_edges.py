@@ -51,3 +51,32 @@ def test_prefix_joined_in_place_without_prefixes():
     assert torch.equal(got[1].cpu()[101:], torch.from_numpy(a.join[1])[101:])
     assert (got[0].cpu()[101:][none] == 0).all()
     assert torch.equal(got[0].cpu()[101:][~none], a.join[0][101:][~none])
+
+
+# ---- V scales that are far apart --------------------------------------------------------------
+
+def prefix_with_scales(rng, B_, D, n, T, steps):
+    """A call whose blocks' V scales have the logarithms `steps` (None: 0), over and over; equal
+    logits, then ones that fall where V's scale rises."""
+    a = Prefix(rng, B_, 1, 1, 4, D, [n], T)
+    a.rows[0, :, :D] = 0x38  # 1.0 in every channel of K
+    a.q = torch.zeros_like(a.q)
+    a.q[..., 0] = 1.0
+    at = [steps[i % len(steps)] for i in range(a.scales.shape[1])]
+    log = np.array([x or 0.0 for x in at])
+    a.scales[0, :, 1, 0] = np.where([x is not None for x in at], np.exp2(log), 0.0)
+    for tilt in (0.0, -1.0):
+        z = 8 + tilt * (log - log.min()) * np.log(2) / 40
+        a.scales[0, :, 0, 0] = z * D ** 0.5
+        yield a
+
+
+@pytest.mark.parametrize("D,B_", [(64, 2), (128, 50), (192, 2)])
+@pytest.mark.parametrize("steps", [40 * (-50,) + 300 * (87,), 300 * (-100,) + 40 * (100,),
+                                   200 * (None,) + 200 * (50,) + 200 * (100,)])
+def test_prefix_reference_jumps(D, B_, steps):
+    """A token's weight in the sum stays when a later V scale, 2^137 and more times its own, moves the
+    reference.  Blocks of 7 tokens, several tiles a CTA; the bounds are those of Prefix.check."""
+    rng = np.random.default_rng(D)
+    for a in prefix_with_scales(rng, B_, D, 7 * 9000, 7, steps):
+        a.check(a.run())
