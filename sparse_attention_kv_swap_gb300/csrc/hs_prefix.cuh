@@ -546,9 +546,11 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
     return d;
 }
 
-// The same for whole tiles whose scales are equal in each 16 tokens, V scales of 2^-60 or more
-// and K scales >= 0: the scales leave the loops.  p_t v_t comes out of the exponential at
-// once, 2^(z_t + log2 v - r), and l takes the sum of 16 by 1 / v.
+// The same for whole tiles whose scales are equal in each 16 tokens, V scales of 2^-60 to 2^50,
+// with none above in the segment so far, and K scales >= 0: the scales leave the loops.  p_t v_t comes
+// out of the exponential at once, 2^(z_t + log2 v - r), and l takes the sum of 16 by 1 / v.  r is
+// at most the largest z plus 50 - kTop then, so that a token whose weight counts in l, z_t no less than
+// the largest by 25, has an exponent above -126: no weight is flushed to 0 before it is divided by v.
 struct Even {  // of 16 tokens each: factor of the products, log2 of the V scale, its reciprocal
     float k[2], log[2], inverse[2];
     __device__ __forceinline__ Even(const float4* s_even, float f) {
@@ -981,6 +983,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             // Tiles whose scales differ within a group, or are not all there, get every token's.
             int items[2] = {0, 0};  // of each pipeline
             for (int from = u0; from < u1;) {
+                bool even = a.even;  // no V scale of the segment has been beyond softmax_even so far
                 const Segment g(plan, a, from, u1, X::kRows, TOK);
                 const int len = plan.len[g.p], first = g.tile0, n = g.n;
                 const bool both = NP == 1 || g.rows - g.row0 > kPrefixRows;
@@ -1000,12 +1003,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     k = next_k, v = next_v;
                     load((first + c + 8) * TOK + lane * 16, next_k, next_v);
                     const unsigned small = __ballot_sync(0xffffffffu, v < 0x1p-60f);
-                    const float4 even = make_float4(k * a.k_sign, log2f(v), __frcp_rn(v), 0.f);
+                    even = even && !__any_sync(0xffffffffu, v > 0x1p50f);
+                    const float4 group = make_float4(k * a.k_sign, log2f(v), __frcp_rn(v), 0.f);
                     const int stop = min(8, n - c);
 #pragma unroll 1
                     for (int j = 0; j < stop; ++j) {
                         const int tile = first + c + j;
-                        const bool each = !a.even || small >> (4 * j) & 15 || (tile + 1) * TOK > len;
+                        const bool each = !even || small >> (4 * j) & 15 || (tile + 1) * TOK > len;
 #pragma unroll
                         for (int p = 0; p < NP; ++p) {
                             if (!both && ((c + j) & 1) != p) continue;
@@ -1013,7 +1017,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                             wait(bar(kScEmpty + 4 * p) + 8 * sc, (items[p] / X::kScales & 1) ^ 1,
                                  gave_up);
                             Scales& s = s_scales[p][sc];
-                            if (lane >> 2 == j) s.even[lane & 3] = even;
+                            if (lane >> 2 == j) s.even[lane & 3] = group;
                             if (lane == 0) s.each = each;
                             if (each) {
 #pragma unroll

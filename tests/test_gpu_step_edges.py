@@ -80,3 +80,21 @@ def test_prefix_reference_jumps(D, B_, steps):
     rng = np.random.default_rng(D)
     for a in prefix_with_scales(rng, B_, D, 7 * 9000, 7, steps):
         a.check(a.run())
+
+
+# log2 of the V scales of consecutive blocks, repeated along the prefix.
+STEPS = [(80, -59), (-59, 80), (-50, 87), (87, -50), (100, -100), (-100, 100), (49, -60),
+         (51, -60), (-60, -61), (-61, 100, -60, 49), (100,) + 30 * (-59,), 30 * (-59,) + (100,),
+         (None, 90, -90), (0, None, -59, 51)]
+
+
+@pytest.mark.parametrize("T,n", [(16, 597), (16, 20005), (64, 40011)])
+@pytest.mark.parametrize("D,B_", [(64, 2), (128, 34), (192, 2)])
+def test_prefix_v_scales_in_steps(T, n, D, B_):
+    """Blocks of 16 tokens and more, whose scales leave the softmax's loops: a token of a small V scale
+    has its full weight whatever came before it, beside it in its tile or after it.  One tile a
+    CTA, or several; the bounds are those of Prefix.check."""
+    rng = np.random.default_rng(T + D)
+    for steps in STEPS:
+        for a in prefix_with_scales(rng, B_, D, n, T, steps):
+            a.check(a.run())
