@@ -83,21 +83,21 @@ __global__ void __launch_bounds__(32 * kWarps) bound_kernel(const BoundArgs a) {
     if (r < 0 || r >= a.R || start < 0 || count <= 0 || count > a.max_count ||
         start > a.L - count)
         return;
+    if (window > (start + count - 1) / a.T - start / a.T) return;
     const int block = start / a.T + window;
     const long long t0 = (long long)block * a.T;
-    if (t0 >= start + count) return;
-    const int lo = t0 > start ? (int)(t0 - start) : 0;  // the block's new tokens
-    const int hi = (int)min((long long)count, t0 + a.T - start);
+    const int lo = t0 > start ? (int)(t0 - start) : 0;  // the block's first new token
+    const int n = (int)min((long long)count, t0 + a.T - start) - lo;
     uint32_t low[4], high[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) low[i] = E::kHigh, high[i] = E::kLow;
     if (used) {
-        const uint8_t* p = a.k + 2 * (b * a.stride[0] + h * a.stride[2] + d);
-        for (int i0 = lo + warp; i0 < hi; i0 += kWarps * kAhead) {
+        const uint8_t* p = a.k + 2 * (b * a.stride[0] + lo * a.stride[1] + h * a.stride[2] + d);
+        for (int i0 = warp; i0 < n; i0 += kWarps * kAhead) {
             uint4 x[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)  // past the last one, the first again
-                x[u] = load16x8(p + 2 * (i0 + u * kWarps < hi ? i0 + u * kWarps : i0) * a.stride[1],
+                x[u] = load16x8(p + 2 * (i0 + u * kWarps < n ? i0 + u * kWarps : i0) * a.stride[1],
                                 a.vec_k);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) join<E>(low, high, x[u], x[u]);

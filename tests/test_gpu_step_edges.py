@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_step import Prefix, dev
+import sparse_attention_kv_swap_gb300 as pkg
+from test_gpu_step import Prefix, dev, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +99,30 @@ def test_prefix_v_scales_in_steps(T, n, D, B_):
     for steps in STEPS:
         for a in prefix_with_scales(rng, B_, D, n, T, steps):
             a.check(a.run())
+
+
+# ---- the longest sequences ---------------------------------------------------------------------
+
+def test_bounds_of_the_longest_sequence():
+    """2^31 - 1 tokens, each of 32 elements that begin one element after the token before's."""
+    M, T, D = 2 ** 31 - 1, 4096, 32
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(40)
+    flat = torch.empty(M + D - 1, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    k = flat.as_strided((1, M, 1, D), (0, 1, 0, 1))
+    got = torch.zeros(pkg.bounds_shape(1, M, T, 1, D), dtype=torch.bfloat16, device="cuda")
+    pkg.hs_bound_keys(k, i32([0]), i32([0]), i32([M]), T, M, got)
+    whole = M // T
+    for d in range(D):
+        x = flat[d:d + whole * T].view(whole, T)
+        assert torch.equal(got[0, :whole, 0, 0, d], x.amin(1))
+        assert torch.equal(got[0, :whole, 0, 1, d], x.amax(1))
+        x = flat[d + whole * T:d + M]
+        assert got[0, whole, 0, 0, d] == x.min() and got[0, whole, 0, 1, d] == x.max()
+    # the last tokens alone, into the blocks as they are
+    again = got.clone()
+    n = 5000
+    pkg.hs_bound_keys(k[:, M - n:], i32([0]), i32([M - n]), i32([n]), T, M, again)
+    assert torch.equal(again, got)
+    del flat, k, got, again, x
+    torch.cuda.empty_cache()
