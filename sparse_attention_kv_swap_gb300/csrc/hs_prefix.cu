@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) combine_kernel(const PrefixArg
     int unit0 = 0, tile_row = 0, halves = 1;
     if (some) {
         const int rows = (plan.hi[p] - plan.lo[p]) * a.S * a.G;
-        const int tiles = (plan.len[p] + kPrefixTokens - 1) / kPrefixTokens;
+        const int tiles = prefix::tiles_of(plan.len[p], kPrefixTokens);
         const int r = i - plan.lo[p] * a.S * a.G, row_tiles = (rows + tile_rows - 1) / tile_rows;
         tile_row = r % tile_rows;
         // Two pipelines that share the tile's rows leave a part each.

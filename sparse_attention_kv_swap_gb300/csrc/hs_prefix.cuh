@@ -84,6 +84,11 @@ cudaError_t prefix_run_int8(const PrefixArgs& a, const CUtensorMap& map, int D, 
 
 namespace prefix {
 
+// Tiles of `each` tokens for n: n may be 2^31 - 1.
+__device__ __forceinline__ int tiles_of(int n, int each) {
+    return (int)(((uint32_t)n + each - 1) / each);
+}
+
 // The prefixes of a call and their units.
 struct Plan {
     int32_t lo[HS_MAX_PREFIXES], hi[HS_MAX_PREFIXES];  // batch rows
@@ -117,8 +122,7 @@ __device__ __forceinline__ void fill_plan(Plan& plan, const PrefixArgs& a, int r
         const int lo = max(first, before), hi = max(end, lo);
         int mine = 0;  // the launcher has made sure that all fit 31 bits
         if (p < a.P && len > 0)
-            mine = a.Hkv * (((hi - lo) * a.S * a.G + rows - 1) / rows) *
-                   ((len + tokens - 1) / tokens);
+            mine = a.Hkv * (((hi - lo) * a.S * a.G + rows - 1) / rows) * tiles_of(len, tokens);
         int sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -154,7 +158,7 @@ struct Segment {
         p = a.P - 1;
         while (plan.unit[p] > from) --p;  // the last one that begins here or before: not empty
         rows = (plan.hi[p] - plan.lo[p]) * a.S * a.G;
-        tiles = (plan.len[p] + tile_tokens - 1) / tile_tokens;
+        tiles = tiles_of(plan.len[p], tile_tokens);
         const int at = from - plan.unit[p];
         const int turn = at / tiles, row_tiles = (rows + tile_rows - 1) / tile_rows;
         tile0 = at - turn * tiles;
@@ -989,19 +993,19 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 const bool both = NP == 1 || g.rows - g.row0 > kPrefixRows;
                 const float* const scales =
                     a.scales + (long long)plan.req[g.p] * a.NB * 2 * a.Hkv + g.h;
-                auto load = [&](int token, float& k, float& v) {
+                auto load = [&](uint32_t token, float& k, float& v) {  // those ahead pass 2^31
                     k = v = 0.f;
-                    if (token < len) {
-                        const float* at = scales + (long long)a.block.of(token) * 2 * a.Hkv;
+                    if (token < (uint32_t)len) {
+                        const float* at = scales + (long long)a.block.of((int)token) * 2 * a.Hkv;
                         k = ld(at);
                         v = ld(at + a.Hkv);
                     }
                 };
                 float k, v, next_k, next_v;
-                load(first * TOK + lane * 16, next_k, next_v);
+                load((uint32_t)first * TOK + lane * 16, next_k, next_v);
                 for (int c = 0; c < n; c += 8) {
                     k = next_k, v = next_v;
-                    load((first + c + 8) * TOK + lane * 16, next_k, next_v);
+                    load((uint32_t)(first + c + 8) * TOK + lane * 16, next_k, next_v);
                     const unsigned small = __ballot_sync(0xffffffffu, v < 0x1p-60f);
                     even = even && !__any_sync(0xffffffffu, v > 0x1p50f);
                     const float4 group = make_float4(k * a.k_sign, log2f(v), __frcp_rn(v), 0.f);
@@ -1009,7 +1013,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll 1
                     for (int j = 0; j < stop; ++j) {
                         const int tile = first + c + j;
-                        const bool each = !even || small >> (4 * j) & 15 || (tile + 1) * TOK > len;
+                        const bool each = !even || small >> (4 * j) & 15 || len - tile * TOK < TOK;
 #pragma unroll
                         for (int p = 0; p < NP; ++p) {
                             if (!both && ((c + j) & 1) != p) continue;
@@ -1023,7 +1027,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll
                                 for (int h = 0; h < TOK; h += 32) {
                                     float one_k, one_v;
-                                    load(tile * TOK + h + lane, one_k, one_v);
+                                    load((uint32_t)tile * TOK + h + lane, one_k, one_v);
                                     s.k[h + lane] = one_k * a.k_sign;
                                     s.v[h + lane] = one_v;
                                     s.log[h + lane] = log2f(one_v);
@@ -1130,7 +1134,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             const bool on = r < g.rows;
             // Warps without rows leave theirs as they are: a row's products are its own.
             const bool alive = r - lane < g.rows;
-            const int rest = plan.len[g.p] + (from - u0 - g.tile0) * TOK;  // less TOK a tile of the CTA
+            // less TOK a tile of the CTA; may pass 2^31
+            const uint32_t rest = plan.len[g.p] + (uint32_t)(from - u0 - g.tile0) * TOK;
             float f = 0.f;  // of the products
             if (first < stop) {
                 // The row's largest element goes to [2^14, 2^15), f16's top.
@@ -1199,7 +1204,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     // The product before, which may still be adding to O; the one before that is done, for
                     // these scores were issued behind it.
                     const Product before = {bar(kPvDone + p), (done + 1) & 1, t == first, gave_up};
-                    const int live = rest - t * TOK;  // tokens of the tile, or more
+                    const int live = (int)(rest - (uint32_t)t * TOK);  // tokens of the tile, or more
                     if (!scales.each)
                         softmax_even<D>(mine, to, o_col + half * (D / 2),
                                         Even(scales.even + 2 * half, f), before, twins, ref, l);

@@ -45,8 +45,9 @@ int check_prefix(const hs_kv_format* f, const hs_prefix_args* a) {
         return HS_ERR_INVALID_ARG;
     if (a->num_heads > HS_MAX_KV_HEADS || a->num_prefixes > HS_MAX_PREFIXES)
         return HS_ERR_UNSUPPORTED;
-    // rows are counted in 32 bits
-    if ((long long)a->batch * a->steps * a->num_heads > kMaxCtas) return HS_ERR_UNSUPPORTED;
+    // rows are counted in 32 bits, with those that a last tile lacks
+    if (a->batch > 0 && a->steps > (kMaxCtas - 4096) / a->num_heads / a->batch)
+        return HS_ERR_UNSUPPORTED;
     return HS_OK;
 }
 

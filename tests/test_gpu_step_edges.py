@@ -126,3 +126,36 @@ def test_bounds_of_the_longest_sequence():
     assert torch.equal(again, got)
     del flat, k, got, again, x
     torch.cuda.empty_cache()
+
+
+def test_prefix_of_the_longest_store():
+    """2^31 - 1 tokens of one head of 32, three tiles of rows: even rows give all their weight to the
+    last thousand tokens, odd ones none.  A row's sums over a CTA's tokens are up to 441506 tiles of 2
+    additions a thread, 2^-24 each, and of 4 products, 2^-23 each."""
+    L, T, D, n, last = 2 ** 31 - 1, 4096, 32, 520, 1000
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("the store is 137 GB")
+    fmt = pkg.make_kv_format(1, D, T)
+    rows = torch.zeros((1, L, 2 * D), dtype=torch.uint8, device="cuda")
+    rows[0, :, D:] = 0x38  # V: 1.0
+    rows[0, -last:, 0] = 0x38  # K
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(41)
+    v = torch.randn((last, D), device="cuda", generator=gen).to(torch.float8_e4m3fn)
+    rows[0, -last:, D:] = v.view(torch.uint8)
+    scales = torch.ones(fmt.scales_shape(1, L), device="cuda")
+    q = torch.zeros((n, 1, 1, D), dtype=torch.float16, device="cuda")
+    q[0::2, ..., 0], q[1::2, ..., 0] = 40.0, -40.0
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    ws = torch.empty(pkg.hs_prefix_workspace_bytes(fmt, n, 1, 1, 1), dtype=torch.uint8, device="cuda")
+    pkg.hs_attend_prefix(fmt, q, rows, scales, i32([0]), i32([L]), i32([0, n]), out, lse=lse,
+                         sm_scale=1.0, workspace=ws)
+    torch.cuda.synchronize()
+    # e^40 a token: the others' 2^31 together are under 2^-36 of it
+    assert (lse[0::2] - (40 + np.log(last))).abs().max() < 1e-4
+    assert (out[0::2].float() - v.float().mean(0)).abs().max() < 2e-3
+    tol = 441506 * 2.0 ** -23
+    assert (lse[1::2] - np.log(L - last)).abs().max() < tol + 1e-5
+    assert (out[1::2].float() - 1).abs().max() < 5 * tol
+    del rows, scales, q, out, lse, ws, v
+    torch.cuda.empty_cache()
