@@ -43,6 +43,12 @@ class SwapInCache:
         stream may still be in use there."""
         return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
+    def _workspace(self, o: Dict[str, torch.Tensor], name: str, need: int) -> None:
+        """A workspace among a call's outputs; one kept from a smaller call gives way to a larger."""
+        held = o.get(name)
+        if held is None or held.numel() * held.element_size() < need:
+            o[name] = torch.empty(need, dtype=torch.uint8, device=self.device)
+
     def swap_in(self, req_pool_indices: torch.Tensor, seq_lens: torch.Tensor,
                 topk: torch.Tensor, layer_id: int = 0, stats: bool = False, plan: bool = False,
                 out: Optional[Dict[str, torch.Tensor]] = None, stream=None):
@@ -111,8 +117,8 @@ class SwapInCache:
             if (weights or (acc is not None and S > 1)) and "weights" not in o:
                 o["weights"] = torch.empty((Bn, S, K), device=self.device)
             need = B.hs_attend_workspace_bytes(fmt, Bn, S, K, q.shape[2])
-            if need and "workspace" not in o:
-                o["workspace"] = torch.empty(need, dtype=torch.uint8, device=self.device)
+            if need:
+                self._workspace(o, "workspace", need)
         B.hs_attend(fmt, q, self.device_kv[layer_id], device_locs, topk, req_pool_indices, scales,
                     self.cfg.max_seq_len, o["out"], o.get("lse"), o.get("weights"), acc, sm_scale,
                     o.get("workspace"), stream)
@@ -150,10 +156,8 @@ class SwapInCache:
                                         device=self.device)
             if "scores" not in o:
                 o["scores"] = torch.empty((Bn, S, bounds.shape[1]), device=self.device)
-            if "select_workspace" not in o:
-                o["select_workspace"] = torch.empty(
-                    B.hs_select_workspace_bytes(Bn, S, self.cfg.max_seq_len, block_tokens),
-                    dtype=torch.uint8, device=self.device)
+            self._workspace(o, "select_workspace", B.hs_select_workspace_bytes(
+                Bn, S, self.cfg.max_seq_len, block_tokens))
         B.hs_select_blocks(q, bounds, req_pool_indices, seq_lens, block_tokens,
                            self.cfg.max_seq_len, first, last, o.get("blocks"), o["topk"],
                            o["scores"], o["select_workspace"], stream)
@@ -174,10 +178,8 @@ class SwapInCache:
                 o["out"] = torch.empty(q.shape, dtype=q.dtype, device=self.device)
             if "lse" not in o:
                 o["lse"] = torch.empty(q.shape[:3], device=self.device)
-            if "prefix_workspace" not in o:
-                o["prefix_workspace"] = torch.empty(
-                    B.hs_prefix_workspace_bytes(fmt, Bn, S, heads, prefix.shape[0]),
-                    dtype=torch.uint8, device=self.device)
+            self._workspace(o, "prefix_workspace", B.hs_prefix_workspace_bytes(
+                fmt, Bn, S, heads, prefix.shape[0]))
         B.hs_attend_prefix(fmt, q, rows, scales, prefix, lens, starts, o["out"], o["lse"],
                            None if join is None else join["out"],
                            None if join is None else join["lse"], sm_scale,
