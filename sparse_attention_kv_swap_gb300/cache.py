@@ -136,8 +136,7 @@ class SwapInCache:
                    req: torch.Tensor, start: torch.Tensor, count: torch.Tensor,
                    stream=None) -> None:
         """Brings new keys [batch, tokens, Hkv, D], those of append_kv, into their blocks' bounds.
-        (evict moves keys to other blocks: those of a sequence that it cut are brought anew, all of
-        them from token 0.)"""
+        (evict moves keys to other blocks, and makes the bounds that it is given anew.)"""
         B.hs_bound_keys(k, req, start, count, block_tokens, self.cfg.max_seq_len, bounds, stream)
 
     def select_blocks(self, bounds: torch.Tensor, block_tokens: int, q: torch.Tensor,
@@ -188,7 +187,8 @@ class SwapInCache:
 
     def evict(self, fmt: B.HsKvFormat, scales: List[torch.Tensor], acc: List[torch.Tensor],
               requests: List[int], seq_lens: List[int], budget: int, recent: int,
-              stream=None) -> List[int]:
+              stream=None, bounds: Optional[List[torch.Tensor]] = None,
+              block_tokens: Optional[int] = None) -> List[int]:
         """Cuts the given requests (lengths seq_lens) to `budget` tokens in every layer:
         the last `recent` and those of the largest accumulated weight acc[layer]
         [R, max_seq_len].  Kept rows move to the first positions of the host pools;
@@ -196,8 +196,11 @@ class SwapInCache:
         their new lengths are returned.  Bytes of a row past its keys and values move with it
         (the call then waits for the stream in every layer).  Needs budget rows of device
         memory per request.
+        Kept keys move to other blocks: bounds[layer] (key_bounds, in blocks of block_tokens) are
+        made anew for the requests, of the kept keys as attend reads them (code * scale, rounded to
+        the bounds' type).  Without `bounds`, bounds that were kept up for them are stale.
         Arguments that do not fit the cache raise ValueError before anything changes."""
-        self._check_evict(fmt, scales, acc, requests, seq_lens, budget, recent)
+        self._check_evict(fmt, scales, acc, requests, seq_lens, budget, recent, bounds, block_tokens)
         if not requests:
             return []
         kept = [min(n, budget) for n in seq_lens]
@@ -233,9 +236,24 @@ class SwapInCache:
                 scales[layer][req.long(), :nb] = new[:, :scales[layer].shape[1]]
                 acc[layer][req.long()] = 0
                 acc[layer][req.long(), :budget] = sums[:, :self.cfg.max_seq_len]
+                for i in range(len(requests) if bounds is not None else 0):
+                    k = self._keys(fmt, rows[i], new[i], bounds[layer].dtype)
+                    self.bound_keys(bounds[layer], block_tokens, k[None], req[i:i + 1],
+                                    torch.zeros_like(req[i:i + 1]), count[i:i + 1])
         return kept
 
-    def _check_evict(self, fmt, scales, acc, requests, seq_lens, budget, recent) -> None:
+    @staticmethod
+    def _keys(fmt, rows, scales, dtype) -> torch.Tensor:
+        """The keys [tokens, Hkv, D] that rows [tokens, W] hold, within the type's range."""
+        shape = (rows.shape[0], fmt.num_kv_heads, fmt.head_dim)
+        kind = torch.int8 if fmt.code == B.HS_KV_INT8 else torch.float8_e4m3fn
+        codes = rows[:, :shape[1] * shape[2]].contiguous().view(kind).view(shape).float()
+        each = scales[:, 0].repeat_interleave(fmt.block_tokens, 0)[:shape[0], :, None]
+        most = torch.finfo(dtype).max
+        return (codes * each).clamp_(-most, most).to(dtype)
+
+    def _check_evict(self, fmt, scales, acc, requests, seq_lens, budget, recent, bounds=None,
+                     block_tokens=None) -> None:
         """The arguments of evict, on the host: layers are cut one after the other, and indexing
         by a request knows no range, so nothing may be refused once the first kernel runs."""
         cfg = self.cfg
@@ -254,6 +272,19 @@ class SwapInCache:
                for p in self.host_pools):
             raise ValueError("the host pools must be uint8 [%d, %d, %d]"
                              % (R, L, cfg.item_size_bytes))
+        if (bounds is None) != (block_tokens is None):
+            raise ValueError("bounds and block_tokens must be given together")
+        if bounds is not None:
+            if not 1 <= block_tokens <= B.HS_MAX_KV_BLOCK:
+                raise ValueError("block_tokens must be from 1 to %d" % B.HS_MAX_KV_BLOCK)
+            shape = B.bounds_shape(R, L, block_tokens, fmt.num_kv_heads, fmt.head_dim)
+            if len(bounds) != cfg.num_layers or any(
+                    t.shape != shape or t.dtype not in (torch.bfloat16, torch.float16)
+                    or not t.is_contiguous() or t.device != self.device_kv[0].device
+                    for t in bounds):
+                raise ValueError("bounds must hold a contiguous bfloat16 or float16 tensor %s for "
+                                 "each of the %d layers, on the cache's device"
+                                 % (shape, cfg.num_layers))
         for name, given, shape in (("scales", scales, fmt.scales_shape(R, L)),
                                    ("acc", acc, (R, L))):
             if len(given) != cfg.num_layers or any(

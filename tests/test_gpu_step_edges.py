@@ -3,8 +3,11 @@ import numpy as np
 import pytest
 import torch
 
+import kv_reference as kvref
 import sparse_attention_kv_swap_gb300 as pkg
-from test_gpu_step import Prefix, dev, i32
+import step_reference as ref
+from sparse_attention_kv_swap_gb300 import binding as B
+from test_gpu_step import CODES, DTYPES, Prefix, dev, i32, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +162,57 @@ def test_prefix_of_the_longest_store():
     assert (out[1::2].float() - 1).abs().max() < 5 * tol
     del rows, scales, q, out, lse, ws, v
     torch.cuda.empty_cache()
+
+
+# ---- eviction and selection ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("code,dtype,T,each", [("e4m3", "bf16", 16, 16), ("int8", "fp16", 16, 8),
+                                               ("int8", "bf16", 24, 32), ("e4m3", "fp16", 16, 7)])
+def test_evict_makes_bounds_anew(code, dtype, T, each):
+    """Of what is kept, as the host pool holds it; other requests' stay, and tokens that are appended
+    later widen them.  Selection by them is that of the reference."""
+    from sparse_attention_kv_swap_gb300.cache import SwapInCache
+    rng = np.random.default_rng(each)
+    R, L, heads, D, layers, blocks = 3, 120, 2, 64, 2, 3
+    fmt = pkg.make_kv_format(heads, D, T, CODES[code])
+    cache = SwapInCache(pkg.make_config(R, L, fmt.item_size_bytes, 8 * each, blocks * each, 1,
+                                        num_layers=layers, extra_page_size=16))
+    req, none = i32([0, 1, 2]), i32([0, 0, 0])
+    lens = np.array([120, 75, 40])
+    scales = [cache.kv_scales(fmt) for _ in range(layers)]
+    bounds = [cache.key_bounds(fmt, DTYPES[dtype], each) for _ in range(layers)]
+    acc = [dev(rng.random((R, L)).astype(np.float32)) for _ in range(layers)]
+    for l in range(layers):
+        k = dev(randn(rng, (R, L, heads, D), dtype))
+        k[0, 5, 0, 3] = 60000.0  # fp16: the code's value is beyond the type
+        cache.append_kv(fmt, scales[l], k, k, req, none, i32(lens), layer_id=l)
+        cache.bound_keys(bounds[l], each, k, req, none, i32(lens))
+        acc[l][0, 5] = 2.0  # kept
+    want = [b.cpu() for b in bounds]
+    budget = 50
+    assert cache.evict(fmt, scales, acc, [0, 1], [120, 75], budget, 10, bounds=bounds,
+                       block_tokens=each) == [50, 50]
+    torch.cuda.synchronize()
+    most = torch.finfo(DTYPES[dtype]).max
+    for l in range(layers):
+        x = torch.from_numpy(kvref.unpack(cache.host_pools[l][:2, :budget].numpy(), heads, D,
+                                          code)[:, :, 0]).float()
+        s = scales[l].cpu()[:2, np.arange(budget) // T, 0, :, None]
+        keys = (x * s).clamp(-most, most).to(DTYPES[dtype])
+        full = want[l].double().numpy()
+        ref.bound(keys.double().numpy(), [0, 1], [0, 0], [budget, budget], each, L, full)
+        assert np.array_equal(bounds[l].cpu().double().numpy(), full)
+        # the next token, and a selection
+        k = dev(randn(rng, (R, 1, heads, D), dtype))
+        at = i32([50, 50, 40])
+        cache.append_kv(fmt, scales[l], k, k, req, at, i32([1, 1, 1]), layer_id=l)
+        cache.bound_keys(bounds[l], each, k, req, at, i32([1, 1, 1]))
+        ref.bound(k.cpu().double().numpy(), [0, 1, 2], [50, 50, 40], [1, 1, 1], each, L, full)
+        assert np.array_equal(bounds[l].cpu().double().numpy(), full)
+        q = randn(rng, (R, 1, 4, D), dtype)
+        got = cache.select_blocks(bounds[l], each, dev(q), req, i32([51, 51, 41]))["topk"]
+        score, _ = ref.scores(q.double().numpy(), full, [0, 1, 2], [51, 51, 41], each, L)
+        topk = ref.select(score, [51, 51, 41], [0, 1, 2], R, each, L, blocks, 1, 1)[1]
+        assert np.array_equal(got.cpu().numpy(), topk)
+    assert cache.status() == (B.HS_OK, 0)
+    cache.close()

@@ -87,3 +87,24 @@ def test_cache_workspaces_grow(lib, monkeypatch):
     o = attend(2, 32768, o)
     assert given[-1] is o["workspace"] and given[-1].numel() == sizes[1]
     assert "workspace" not in attend(1, 16, {})
+
+
+def test_cache_evict_refuses_bounds(lib):
+    """Bounds that do not fit the cache are refused before anything changes."""
+    from test_kv_edges import cpu_cache
+    cache = cpu_cache()  # 3 requests of 40 tokens in 2 layers
+    fmt = pkg.make_kv_format(2, 64, 16)
+    scales, acc = [torch.ones((3, 3, 2, 2))] * 2, [torch.ones((3, 40))] * 2
+
+    def bounds(*shape, dtype=torch.bfloat16, n=2):
+        return [torch.zeros(shape, dtype=dtype) for _ in range(n)]
+
+    for b, T in ((bounds(3, 5, 2, 2, 64), None), (None, 8), (bounds(3, 5, 2, 2, 64), 0),
+                 (bounds(3, 5, 2, 2, 64), -8), (bounds(3, 5, 2, 2, 64), 16),
+                 (bounds(3, 1, 2, 2, 64), 4097), (bounds(2, 5, 2, 2, 64), 8),
+                 (bounds(3, 5, 2, 2, 64, n=1), 8), (bounds(3, 5, 2, 2, 64, n=3), 8),
+                 (bounds(3, 5, 2, 2, 64, dtype=torch.float32), 8),
+                 ([x.transpose(0, 1) for x in bounds(5, 3, 2, 2, 64)], 8),
+                 (bounds(3, 5, 2, 2, 64, n=1) + bounds(3, 5, 1, 2, 64, n=1), 8)):
+        with pytest.raises(ValueError, match="bounds|block_tokens"):
+            cache.evict(fmt, scales, acc, [0], [40], 8, 2, bounds=b, block_tokens=T)
