@@ -111,19 +111,21 @@ __global__ void __launch_bounds__(32 * kWarps, 2) combine_kernel(const PrefixArg
         sum += (c == warp ? first_sum : ld(a.part_sum + slot(c) * tile_rows + row_of(c)).y) * f;
     }
     s_tmp[warp][lane] = sum;
-    // lse may be the given one itself, and a row's slices are CTAs of their own, which nothing orders:
-    // the slice that writes a row's lse must not be where the others read.  They read the parts' copy; a
-    // row without parts keeps the given lse.
+    // lse may be the given one itself, and a row's slices are CTAs of their own, which nothing orders: what
+    // one of them writes must not be where the others read.  They read the copy that lies with the
+    // parts then (copying always would cost 0.6 of 31.6 us for 21 requests of 3 steps), and a row without
+    // parts keeps the given lse.
+    const bool in_place = a.lse == a.join_lse;
     float other = -INFINITY;
     if (mine && a.join)
-        other = parts > 0 ? ld(a.part_join + slot(0) * tile_rows + row_of(0)) : ld(a.join_lse + out_row);
+        other = parts > 0 && in_place ? ld(a.part_join + slot(0) * tile_rows + row_of(0))
+                                      : ld(a.join_lse + out_row);
     __syncthreads();
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += s_tmp[w][lane];
     const Joined j(some ? top + log2f(sum) : -INFINITY, other);
-    if (mine && warp == 0 && slice == 0 && a.lse && (parts > 0 || a.lse != a.join_lse))
-        a.lse[out_row] = j.lse;
+    if (mine && warp == 0 && slice == 0 && a.lse && (parts > 0 || !in_place)) a.lse[out_row] = j.lse;
     const float by = some ? j.mine / sum : 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c0 = 0; sub + c0 * split < parts; c0 += kAhead) {

@@ -68,7 +68,7 @@ struct PrefixArgs {
     int32_t ctas;
     float* part;       // [ctas][2][D / 4][rows of a tile][4] outputs
     float2* part_sum;  // [ctas][2][rows of a tile] (r, l)
-    float* part_join;  // [ctas][2][rows of a tile] the row's given lse
+    float* part_join;  // [ctas][2][rows of a tile] the row's given lse, where lse is that itself
 };
 
 constexpr int prefix_pipes(int D) { return D <= 128 ? 2 : 1; }
@@ -726,7 +726,7 @@ __device__ __forceinline__ void finish(const PrefixArgs& a, const Plan& plan, ui
         if (!whole && on && half == 0) {
             const long long place = slot * X::kRows + tile_row;
             a.part_sum[place] = make_float2(done ? ref : -INFINITY, l);
-            if (a.join) a.part_join[place] = ld(a.join_lse + out_row);
+            if (a.join && a.lse == a.join_lse) a.part_join[place] = ld(a.join_lse + out_row);
         }
         if (!whole && !done) return;
         uint16_t* out = a.out + at.at(a.out_stride);
