@@ -647,7 +647,8 @@ typedef struct hs_norm_rope_args {
  *     (y0 cos a_j - y1 sin a_j, y0 sin a_j + y1 cos a_j)
  * in 32 bits, rounded once to the outputs' type.  The product turns * pos is
  * exact modulo whole turns, so that angles of far positions are as good as those of
- * near ones; pos may be negative.
+ * near ones; pos may be negative.  Where a weight is given, elements are under 2^59 (their squares
+ * are summed in 32 bits).
  * Returns HS_ERR_UNSUPPORTED for 2^31 heads or more in all.
  * Asynchronous on `stream`. */
 int hs_norm_rope(const hs_norm_rope_args* args, void* stream);
@@ -712,8 +713,9 @@ size_t hs_select_workspace_bytes(int32_t batch, int32_t steps, int32_t max_seq_l
  * With n = min(seq_lens[b], max_seq_len) tokens in ceil(n / T) blocks: all blocks if these
  * are no more than `select`; else the first `first`, the last `last` and, of those between, the
  * ones of the largest scores, ties to the lower block, a NaN below every number.
- * Scores are sums in 32 bits.  For finite bounds and queries the selection is that of scores of 46
- * bits: blocks that are closer than the sums tell apart are scored again.
+ * Scores are sums in 32 bits.  For finite bounds and queries, and sums of magnitudes between 2^-80 and
+ * 2^126, the selection is that of scores of 46 bits: blocks that are closer than the sums tell apart are
+ * scored again (by one SM for a query: time that grows with their number).
  * A request outside [0, num_requests) or a length of 0 or less selects nothing (-1, scores -inf).
  * Bounds of blocks past the sequence are not read.
  * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_SELECT_BLOCKS blocks of a sequence, HS_MAX_KV_HEADS query
@@ -770,13 +772,16 @@ size_t hs_prefix_workspace_bytes(const hs_kv_format* fmt, const hs_prefix_args* 
  * Products of codes and queries are exact (but for query elements under 2^-28 of their head's
  * largest, which are off by 2^-39 of that at most) and summed in 32 bits; the softmax statistics
  * are 32 bits; each weight times its V scale is rounded to 11 bits for the product with the V
- * codes (or by 2^-34 of the largest such term, if that is more; V scales up to about 2^100).
+ * codes (or by 2^-34 of the largest such term, if that is more).  V scales are up to about 2^100, and
+ * of 2^21 tokens in a row some have one above 2^-80; where a head has none above 2^-90, 2^-34 becomes
+ * 2^-18.
  * A NaN code in the prefix spoils the outputs of the heads that read it, an infinity or a NaN in a
  * query those of its head.  Outputs do not depend on timing.
  * The kernel holds the tensor memory of the SMs it runs on until it ends; it waits for nothing but
  * its own copies and products.
- * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_KV_HEADS query heads or HS_MAX_PREFIXES, for 2^31 tiles of
- * queries and tokens or more, or for a store of 2^40 bytes a request or more.
+ * Returns HS_ERR_UNSUPPORTED beyond HS_MAX_KV_HEADS query heads or HS_MAX_PREFIXES, for more than
+ * 2^31 - 4097 query heads in all, 2^31 tiles of queries and tokens or more, or a store of 2^40 bytes a
+ * request or more.
  * Should a wait inside the kernel ever give up, the outputs it would have written are NaN.
  * Asynchronous on `stream`. */
 int hs_attend_prefix(const hs_kv_format* fmt, const hs_prefix_args* args, void* stream);

@@ -7,7 +7,7 @@ import kv_reference as kvref
 import sparse_attention_kv_swap_gb300 as pkg
 import step_reference as ref
 from sparse_attention_kv_swap_gb300 import binding as B
-from test_gpu_step import CODES, DTYPES, Prefix, dev, i32, randn
+from test_gpu_step import CODES, DTYPES, Prefix, Rotate, Select, dev, i32, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +216,39 @@ def test_evict_makes_bounds_anew(code, dtype, T, each):
         assert np.array_equal(got.cpu().numpy(), topk)
     assert cache.status() == (B.HS_OK, 0)
     cache.close()
+
+
+# ---- selection ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("up", [-40, 55])
+def test_select_near_ties_of_small_and_large_scores(up):
+    """Queries and bounds of 2^-40 and of 2^55: scores that differ by less than the sums in 32 bits can
+    tell are told apart at the ends of the range too."""
+    rng = np.random.default_rng(50)
+    T, L = 4, 2400
+    s = Select(rng, 2, 2, 4, 4, 64, T, L, 100, 1, 1)
+    s.lens[:] = L
+    s.bounds[:] = s.bounds[:1, :1]
+    steps = torch.from_numpy(rng.integers(0, 128, (s.R, 600)) * 2.0 ** -7 + 1.0)
+    s.bounds[:, :, 2, 0, 5] = 0
+    s.bounds[:, :, 2, 1, 5] = (steps * 2.0 ** -14).to(torch.bfloat16)
+    s.q[:, :, 8:12, 5] = 1.0
+    plain = s.run()
+    s.check(plain)
+    s.q, s.bounds = s.q * 2.0 ** up, s.bounds * 2.0 ** up
+    got = s.run()
+    s.check(got)
+    assert torch.equal(got[0], plain[0]) and torch.equal(got[2], plain[2] * 2.0 ** (2 * up))
+
+
+# ---- norms and rotation ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rotate_largest_elements(dtype):
+    """Elements just under 2^59, the largest whose squares are promised to add up, beside small ones."""
+    rng = np.random.default_rng(51)
+    r = Rotate(rng, 1, 3, 4, 2, 256, 256, dtype)
+    r.q = torch.full(r.q.shape, 255 * 2.0 ** 51, dtype=r.q.dtype)
+    r.q[:, 1] = -r.q[:, 1]
+    r.q[:, 2] *= 2.0 ** -100
+    r.check(r.run())
