@@ -4,7 +4,7 @@
 // tokens, and least and greatest are joined in shared memory.  Minima and maxima of 16-bit
 // keys are keys: nothing is rounded, so that bounds kept up token by token are those of the whole
 // block.  Memory bound for prompts (each key is read once): 4 of 8192 tokens, 8 heads of 128, take
-// 14.8 us, 4.7 TB/s; latency for tokens (7.9 us for one of each of 64 requests, through Python).
+// 14.6 us, 4.7 TB/s; latency for tokens (8.0 us for one of each of 64 requests, through Python).
 #include "hs_step.cuh"
 
 namespace hs {

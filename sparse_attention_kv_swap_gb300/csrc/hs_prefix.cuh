@@ -30,13 +30,14 @@
 // of the largest z, so that l stays in range.
 //
 // What bounds it (e4m3, D = 128, 8 K/V heads, both kernels): 64 requests of 8 query heads a K/V head
-// over 32768 shared tokens take 83 us, 0.83 PFLOP/s; 2 requests of 4 over 131072 take 87 us, 3.1 TB/s.  With
-// 256 rows a tile costs 1.0 us, of which the matrix instructions alone need 0.96 (they read the queries
-// from shared memory anew for each 64 tokens: tensor memory is full of S and O) and the
-// softmax's chain alone 0.90; taking out the conversions saves 3%.  (A warp for all 64 tokens of its rows, with
-// half as many softmax warps, made the second call 4% slower, the first 1.5% faster.)  Launch, the first
-// tile's way through the roles, partial outputs and their joining cost some 25 us a call, whatever its
-// length.
+// over 32768 shared tokens take 83 us, 0.83 PFLOP/s, 1.0 us a tile of an SM; 2 requests of 4 over 131072
+// take 86 us, 3.1 TB/s, 0.6 us a tile.  That is mostly what it takes to hand a tile on from role to
+// role: with the work of all roles left out (a version of 86 and 89 us) 59 and 58 stayed, and without the
+// conversions, the softmax, the copies or nearly all matrix instructions alone 2 to 5 were saved.  (A
+// warp for all 64 tokens of its rows, with half as many softmax warps, made the second call 4% slower, the
+// first 1.5% faster.)  27 and 22 us of these calls do not grow with their length: launches, the first tile's
+// way through the roles, partial outputs of every SM and their joining.  The smallest call, a tile an SM
+// at most and few parts, takes 12.
 #pragma once
 
 #include <cuda.h>

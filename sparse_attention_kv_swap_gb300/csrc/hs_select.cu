@@ -25,6 +25,9 @@
 // 32-bit numbers and their largest magnitudes are kept), the selection 7, launches the rest.
 // 12 requests of up to 4096 blocks with 4 steps take 40: their lengths differ and a step's
 // products are latencies of few warps (the sums of 4 steps leave registers for 16 warps an SM).
+// More than kList blocks at the border are scored again a warp a block, by the query's one CTA: 390 us
+// where all blocks of the first call are alike, 9.5 ms for one query of 16384 such blocks (36 us
+// otherwise).
 #include "hs_step.cuh"
 
 namespace hs {
